@@ -609,6 +609,187 @@ tb_status tb_patch_group_norm_noalloc(const void* const* patches, void* const* o
                                       int64_t N, int64_t C, const int64_t* spatial, int32_t G, const void* gamma,
                                       const void* beta, float eps, int32_t silu, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Training: layer norm, gradient clipping, PatchGroupNorm's backward pass.
+ *
+ * These calls follow the conventions at the top of this file, with one
+ * exception: the row tensors of the layer norm may have any row stride.
+ * Device pointers must be aligned to their element type (TB_ERR_UNSUPPORTED
+ * otherwise); 16-byte aligned tensors whose rows are whole 16-byte chunks
+ * take the vector path.  Results are deterministic: no atomics, every sum in
+ * an order fixed by the sizes and the GPU.  Captured into a CUDA graph and
+ * replayed with new contents (tested): all of them.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * tb_layer_norm -- layer norm over the last axis, row by row:
+ *     h = residual ? rnd(x + residual) : x
+ *     mean = sum(h) / cols,  rstd = 1 / sqrt(sum((h - mean)^2) / cols + eps)
+ *     y = rnd((h - mean) * rstd * gamma + beta)
+ * in fp32, each output rounded once.
+ *
+ *   x, x_ld      [rows, cols] of dtype, row r at element r * x_ld (x_ld >=
+ *                cols; any value when rows <= 1); the same for the other rows
+ *   residual     NULL, or rows added to x first; then `total` (required)
+ *                receives h
+ *   gamma, beta  device [cols] of wdtype, or NULL for 1 / 0
+ *   wdtype       dtype or TB_F32
+ *   y            may equal x; total may equal x or residual; no other overlap
+ *   mean, rstd   device [rows] fp32, or NULL: kept for the backward pass
+ * A row with a NaN or an infinity comes out NaN; other rows are unaffected.
+ * rows == 0 launches nothing.
+ * Errors: TB_ERR_NULL (x or y, or total with a residual), TB_ERR_DTYPE,
+ * TB_ERR_SHAPE (negative rows, cols < 1, a stride below cols, eps < 0, NaN or
+ * infinite), TB_ERR_UNSUPPORTED (cols > 2^30, a misaligned pointer),
+ * TB_ERR_CUDA.
+ */
+tb_status tb_layer_norm(const void* x, int64_t x_ld, const void* residual, int64_t residual_ld, tb_dtype dtype,
+                        int64_t rows, int64_t cols, const void* gamma, const void* beta, tb_dtype wdtype, float eps,
+                        void* total, int64_t total_ld, void* y, int64_t y_ld, float* mean, float* rstd, void* stream);
+
+/* Most partial weight gradients (row groups) of one backward call. */
+#define TB_LN_PARTS 512
+
+/* Bytes of workspace tb_layer_norm_backward needs for these sizes:
+ * min(rows, TB_LN_PARTS) * cols * 8; -1 for sizes it does not take. */
+int64_t tb_layer_norm_workspace(int64_t rows, int64_t cols);
+
+/*
+ * tb_layer_norm_backward -- the gradients of tb_layer_norm.  With
+ * xhat = (x - mean) * rstd and g = dy * gamma:
+ *     dx = rnd(rstd * (g - sum(g) / cols - xhat * sum(g * xhat) / cols) + dtotal)
+ *     dgamma = sum over rows of dy * xhat,  dbeta = sum over rows of dy
+ * in fp32, each output rounded once.
+ *
+ *   dy           gradient of y
+ *   x            what was normalised: the forward call's x, or its total.  dx
+ *                is then the gradient of x and of the residual alike
+ *   mean, rstd   device [rows], as the forward call left them
+ *   gamma        as the forward call
+ *   dtotal       NULL, or a gradient that reaches h past the norm
+ *   dx           may equal dy, x or dtotal; NULL if only the weight gradients
+ *                are wanted
+ *   dgamma/dbeta device [cols] of wdtype; either may be NULL.  Written, not
+ *                added to; zero when rows == 0
+ *   workspace    device, 16-byte aligned, workspace_bytes >=
+ *                tb_layer_norm_workspace(rows, cols); may be NULL when
+ *                neither weight gradient is wanted or rows == 0.  Its contents
+ *                need no clearing and are not kept
+ * Errors: as tb_layer_norm, TB_ERR_SHAPE also for a workspace too small.
+ */
+tb_status tb_layer_norm_backward(const void* dy, int64_t dy_ld, const void* x, int64_t x_ld, tb_dtype dtype,
+                                 int64_t rows, int64_t cols, const float* mean, const float* rstd, const void* gamma,
+                                 tb_dtype wdtype, const void* dtotal, int64_t dtotal_ld, void* dx, int64_t dx_ld,
+                                 void* dgamma, void* dbeta, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Most gradient tensors of one call, tensors per record set, and records per
+ * set. */
+#define TB_MAX_GRADS 65536
+#define TB_GRAD_TABLE 1024
+#define TB_GRAD_PARTS 1024
+
+/* Records (doubles) tb_grad_stats writes for T tensors: TB_GRAD_PARTS for
+ * every TB_GRAD_TABLE tensors or part of them, at least one set; -1 for a
+ * count it does not take. */
+int64_t tb_grad_records(int32_t T);
+
+/*
+ * tb_grad_stats -- the sum of squares of many gradient tensors, as records:
+ * fp64 partial sums whose total is the square of the global norm.  Records of
+ * several calls (other tensors, other ranks) laid back to back describe all
+ * of their gradients together.
+ *
+ *   grads    host array of T device pointers
+ *   numel    host array of T element counts (>= 0)
+ *   dtypes   host array of T element types (they may differ)
+ *   records  device [tb_grad_records(T)], written fully
+ * Finite gradients of any size give their sum: values whose squares leave
+ * fp32's range are squared scaled.  An infinity or a NaN makes the sum
+ * infinite or NaN.
+ * Errors: TB_ERR_NULL, TB_ERR_DTYPE, TB_ERR_SHAPE (negative counts),
+ * TB_ERR_UNSUPPORTED (T > TB_MAX_GRADS, more than 2^42 elements in a tensor,
+ * a misaligned pointer), TB_ERR_CUDA.
+ */
+tb_status tb_grad_stats(const void* const* grads, const int64_t* numel, const tb_dtype* dtypes, int32_t T,
+                        double* records, void* stream);
+
+/* tb_grad_norm -- the norm the records describe, sqrt of their sum, rounded
+ * to fp32: one device float.  Errors: TB_ERR_NULL, TB_ERR_SHAPE,
+ * TB_ERR_UNSUPPORTED (a misaligned pointer), TB_ERR_CUDA. */
+tb_status tb_grad_norm(const double* records, int64_t n_records, float* norm, void* stream);
+
+/*
+ * tb_grad_clip -- every gradient times one factor:
+ *     norm = sqrt(sum of the records),  out = rnd(g * min(1, max_norm / (norm + 1e-6)))
+ * (norm, factor and product in fp32).  An infinite norm gives a factor of
+ * zero, a NaN norm NaN gradients.
+ *
+ *   grads, numel, dtypes, T  as tb_grad_stats
+ *   outs      host array of T device pointers; outs[t] may equal grads[t] (in
+ *             place: nothing is written when the factor is 1), other overlaps
+ *             are not allowed
+ *   records   device [n_records]: the records of these gradients, and of any
+ *             others the norm is to cover (other ranks')
+ *   max_norm  >= 0
+ *   norm      device float or NULL: receives the norm
+ * Errors: as tb_grad_stats, TB_ERR_SHAPE also for a negative or NaN max_norm.
+ */
+tb_status tb_grad_clip(const void* const* grads, void* const* outs, const int64_t* numel, const tb_dtype* dtypes,
+                       int32_t T, const double* records, int64_t n_records, float max_norm, float* norm,
+                       void* stream);
+
+/* Partial sums of one part of one (patch, sample, channel) of PatchGroupNorm's
+ * backward pass: of dz and of dz * xhat (see tb_patch_gn_grad_stats). */
+typedef struct {
+    float dz;
+    float dzx;
+} tb_gn_grad_partial;
+
+/*
+ * tb_patch_gn_grad_stats -- first half of the backward pass of PatchGroupNorm
+ * (+ SiLU).  With the pooled mean and rstd of the forward pass's records,
+ * xhat = (x - mean) * rstd, z = xhat * gamma + beta and s = 1 / (1 + exp(-z)):
+ *     dz = silu ? dy * s * (1 + z * (1 - s)) : dy
+ * The sums of dz and dz * xhat over every (patch, sample, channel) go to
+ *     grad_partials[((p * N + n) * C + c) * TB_GN_PARTS + k]
+ * in up to TB_GN_PARTS parts k (unused parts zero).
+ *
+ *   patches    host array of P device pointers: the forward call's inputs x
+ *   grads      host array of P device pointers: dy, shaped like the patches
+ *   P, dtype, N, C, spatial, G, gamma, beta, eps, silu   as the forward call
+ *   partials   the forward pass's records, R sets (R = P, or every rank's)
+ *   grad_partials  device [P][N][C][TB_GN_PARTS], written fully
+ * Errors as tb_patch_gn_apply_gathered; TB_ERR_UNSUPPORTED also for
+ * max(P, R) * N * C * TB_GN_PARTS above 2e9 and a misaligned pointer.
+ */
+tb_status tb_patch_gn_grad_stats(const void* const* patches, const void* const* grads, int32_t P, tb_dtype dtype,
+                                 int64_t N, int64_t C, const int64_t* spatial, int32_t G,
+                                 const tb_gn_partial* partials, int32_t R, const void* gamma, const void* beta,
+                                 float eps, int32_t silu, tb_gn_grad_partial* grad_partials, void* stream);
+
+/*
+ * tb_patch_gn_grad_apply -- second half: with A and B the sums of dz * xhat
+ * and dz over a channel's records of all R sets, and c1, c2 the sums over a
+ * group's channels of gamma * B and gamma * A, divided by the group's count,
+ *     dx = rnd(rstd * (gamma * dz - c1 - xhat * c2))
+ *     dgamma(c) = sum over samples of A,  dbeta(c) = sum over samples of B
+ * in fp32, each output rounded once.
+ *
+ *   outs           host array of P device pointers (dx); outs[p] may equal
+ *                  patches[p] or grads[p]
+ *   grad_partials  device, R sets of [N][C][TB_GN_PARTS] records back to back,
+ *                  describing the same patches as `partials`
+ *   dgamma, dbeta  device [C] of dtype, or NULL: the gradients over all R sets
+ *                  (every rank gets the whole sum)
+ *   the rest       as tb_patch_gn_grad_stats
+ * Errors as tb_patch_gn_grad_stats.
+ */
+tb_status tb_patch_gn_grad_apply(const void* const* patches, const void* const* grads, void* const* outs, int32_t P,
+                                 tb_dtype dtype, int64_t N, int64_t C, const int64_t* spatial, int32_t G,
+                                 const tb_gn_partial* partials, const tb_gn_grad_partial* grad_partials, int32_t R,
+                                 const void* gamma, const void* beta, float eps, int32_t silu, void* dgamma,
+                                 void* dbeta, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

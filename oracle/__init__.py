@@ -20,4 +20,6 @@ ramp       the normalised-ramp stitch of equally sized tiles, in float64.
 patchify   the ragged band split of one axis among ranks (whole bands of
            the VAE's scale factor, the first ranks one band more) and the
            gather that reassembles the patches, in plain numpy.
+training   layer norm, the global gradient norm with the clip, and the
+           backward passes of the layer norm and of PatchGroupNorm, in float64.
 """

@@ -30,8 +30,11 @@ UNITS = {
     "tb_patchify.cu": [],
     "tb_shard.cu": [],
     "tb_status.cu": [],
+    "tb_layernorm.cu": [],
+    "tb_gradclip.cu": [],
+    "tb_train.cpp": [],
 }
-HEADERS = ["tb_internal.h"]
+HEADERS = ["tb_internal.h", "tb_elem.cuh"]
 
 
 def _nvcc() -> str:

@@ -1,0 +1,183 @@
+// tb_elem.cuh -- element and chunk helpers of the training kernels (layer
+// norm, gradient clipping, PatchGroupNorm's backward pass).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "tb_internal.h"
+
+namespace tb {
+
+__host__ __device__ constexpr int elem_size(int dt) { return dt == F32 ? 4 : 2; }
+
+// A chunk: VEC neighbouring elements, loaded and stored as one word of
+// VEC * elem_size(DT) bytes (2, 4, 8 or 16).
+template <int BYTES>
+struct Word;
+template <>
+struct Word<16> {
+    using T = uint4;
+};
+template <>
+struct Word<8> {
+    using T = uint2;
+};
+template <>
+struct Word<4> {
+    using T = uint32_t;
+};
+template <>
+struct Word<2> {
+    using T = unsigned short;
+};
+
+template <int DT>
+__device__ __forceinline__ float elem_to_f(uint32_t bits) {
+    if constexpr (DT == F32) {
+        return __uint_as_float(bits);
+    } else if constexpr (DT == F16) {
+        return __half2float(__ushort_as_half((unsigned short)bits));
+    } else {
+        return __uint_as_float(bits << 16);
+    }
+}
+
+// Two 16-bit elements of a 32-bit word, low half first.
+template <int DT>
+__device__ __forceinline__ void pair_to_f(uint32_t v, float& lo, float& hi) {
+    if constexpr (DT == F16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+        lo = f.x;
+        hi = f.y;
+    } else {
+        lo = __uint_as_float(v << 16);
+        hi = __uint_as_float(v & 0xffff0000u);
+    }
+}
+
+// Round to nearest even, once, into the storage type.
+template <int DT>
+__device__ __forceinline__ uint32_t f_to_pair(float lo, float hi) {
+    if constexpr (DT == F16) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+
+template <int DT, int VEC>
+__device__ __forceinline__ void unpack(const typename Word<VEC * elem_size(DT)>::T& w, float (&f)[VEC]) {
+    if constexpr (VEC == 1) {
+        f[0] = elem_to_f<DT>((uint32_t)w);
+    } else {
+        uint32_t u[VEC * elem_size(DT) / 4];
+        *reinterpret_cast<typename Word<VEC * elem_size(DT)>::T*>(u) = w;
+#pragma unroll
+        for (int q = 0; q < VEC * elem_size(DT) / 4; ++q) {
+            if constexpr (DT == F32) {
+                f[q] = __uint_as_float(u[q]);
+            } else {
+                pair_to_f<DT>(u[q], f[2 * q], f[2 * q + 1]);
+            }
+        }
+    }
+}
+
+template <int DT, int VEC>
+__device__ __forceinline__ typename Word<VEC * elem_size(DT)>::T pack(const float (&f)[VEC]) {
+    if constexpr (VEC == 1) {
+        if constexpr (DT == F32) {
+            return __float_as_uint(f[0]);
+        } else {
+            return (unsigned short)(f_to_pair<DT>(f[0], 0.f) & 0xffffu);
+        }
+    } else {
+        uint32_t u[VEC * elem_size(DT) / 4];
+#pragma unroll
+        for (int q = 0; q < VEC * elem_size(DT) / 4; ++q) {
+            if constexpr (DT == F32) {
+                u[q] = __float_as_uint(f[q]);
+            } else {
+                u[q] = f_to_pair<DT>(f[2 * q], f[2 * q + 1]);
+            }
+        }
+        return *reinterpret_cast<const typename Word<VEC * elem_size(DT)>::T*>(u);
+    }
+}
+
+// Element i of a weight vector whose type is the rows' or f32, as f32.
+__device__ __forceinline__ float weight_at(const void* w, int dtype, int64_t i, float dflt) {
+    if (w == nullptr) return dflt;
+    if (dtype == F32) return reinterpret_cast<const float*>(w)[i];
+    const uint32_t v = reinterpret_cast<const unsigned short*>(w)[i];
+    return dtype == F16 ? elem_to_f<F16>(v) : elem_to_f<BF16>(v);
+}
+
+// VEC neighbouring weights starting at element i.  VECTOR: the address is
+// 16-byte aligned and whole chunks are in range.
+template <int VEC, bool VECTOR>
+__device__ __forceinline__ void weights_at(const void* w, int dtype, int64_t i, float dflt, float (&f)[VEC]) {
+    if (w == nullptr) {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) f[q] = dflt;
+    } else if constexpr (!VECTOR || VEC < 4) {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) f[q] = weight_at(w, dtype, i + q, dflt);
+    } else if (dtype == F32) {
+#pragma unroll
+        for (int q = 0; q < VEC; q += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(w) + i + q);
+            f[q] = v.x;
+            f[q + 1] = v.y;
+            f[q + 2] = v.z;
+            f[q + 3] = v.w;
+        }
+    } else {
+        if constexpr (VEC == 8) {
+            const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned short*>(w) + i);
+            if (dtype == F16) unpack<F16, 8>(v, f);
+            else unpack<BF16, 8>(v, f);
+        }
+    }
+}
+
+__device__ __forceinline__ void store_weight(void* w, int dtype, int64_t i, float v) {
+    if (dtype == F32) {
+        reinterpret_cast<float*>(w)[i] = v;
+    } else {
+        reinterpret_cast<unsigned short*>(w)[i] =
+            (unsigned short)((dtype == F16 ? f_to_pair<F16>(v, 0.f) : f_to_pair<BF16>(v, 0.f)) & 0xffffu);
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+
+// Waits until the grids before this one on the stream have completed and
+// their writes are visible (launches use programmatic stream serialisation).
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launches `fn` with programmatic stream serialisation, as every kernel of
+// the library is launched.
+template <typename P>
+inline cudaError_t launch_pdl(void (*fn)(const P), const P& p, dim3 grid, int block, size_t smem, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+}  // namespace tb

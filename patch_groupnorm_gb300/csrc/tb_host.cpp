@@ -886,6 +886,8 @@ tb_status patch_copy(bool to_patches, void* whole, void* const* patches, int32_t
 }  // namespace
 
 void tb::record_cuda_error(cudaError_t e) { g_last_cuda_error = (int)e; }
+tb_status tb::sm_count(int* sms) { return device_sms(sms); }
+uint32_t* tb::checked_build_status() { return debug_status(); }
 
 // ---------------------------------------------------------------------------
 // normalised-ramp stitch

@@ -422,4 +422,127 @@ void record_cuda_error(cudaError_t e);
 cudaError_t launch_gn_stats(const GnStatsParams& p, int dtype, int64_t units, cudaStream_t s);
 cudaError_t launch_gn_apply(const GnApplyParams& p, int dtype, int64_t items, cudaStream_t s);
 
+struct GnGradParams {
+    const void* patches[GN_MAXP];     // x
+    const void* grads[GN_MAXP];       // dy
+    void* outs[GN_MAXP];              // dx (apply only)
+    int64_t spatial[GN_MAXP];
+    int64_t item_start[GN_MAXP + 1];  // first work item of patch p (prefix sums; apply only)
+    int64_t nseg[GN_MAXP];            // segments per channel row of patch p (apply only)
+    const GnPartial* partials;        // the forward pass's records: [R][N][G][TB_GN_PARTS]
+    float2* grad_partials;            // (sum dz, sum dz * xhat): [P or R][N][C][TB_GN_PARTS]
+    const void* gamma;                // [C] or null
+    const void* beta;                 // [C] or null
+    void* dgamma;                     // [C] or null (apply only)
+    void* dbeta;                      // [C] or null (apply only)
+    int64_t N, C;
+    int32_t P, G;
+    int32_t parts;                    // CTAs per channel row (stats only): 1 .. TB_GN_PARTS
+    int32_t seg;                      // elements per segment (apply only)
+    int32_t R;                        // record sets
+    int32_t wblocks;                  // leading CTAs that reduce the weight gradients (apply only)
+    float eps;
+    int32_t silu;
+    int32_t aligned;                  // every channel row start is 16-byte aligned
+    uint32_t* status;                 // bounds-checked build: device status word (else null)
+};
+static_assert(sizeof(GnGradParams) <= 32000, "kernel parameter block too large");
+
+int gn_grad_segment(int dtype, bool aligned);
+cudaError_t launch_gn_grad_stats(const GnGradParams& p, int dtype, int64_t units, cudaStream_t s);
+cudaError_t launch_gn_grad_apply(const GnGradParams& p, int dtype, int64_t items, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// Layer norm
+// ---------------------------------------------------------------------------
+
+// Row strides (*_ld) are in elements.
+struct LnFwdParams {
+    const void* x;
+    const void* residual;   // or null
+    const void* gamma;      // [cols] of wdtype, or null
+    const void* beta;       // [cols] of wdtype, or null
+    void* total;            // x + residual, rounded (residual only)
+    void* y;
+    float* mean;            // [rows] or null
+    float* rstd;            // [rows] or null
+    int64_t rows, cols;
+    int64_t x_ld, r_ld, t_ld, y_ld;
+    uint32_t* status;       // bounds-checked build: device status word (else null)
+    int32_t wdtype;
+    float eps;
+};
+
+struct LnBwdParams {
+    const void* dy;
+    const void* x;          // the normalised input (the total, with a residual)
+    const float* mean;
+    const float* rstd;
+    const void* gamma;      // [cols] of wdtype, or null
+    const void* dtotal;     // or null
+    void* dx;               // or null
+    float* workspace;       // [parts][2][cols], or null: no weight gradients
+    int64_t rows, cols;
+    int64_t dy_ld, x_ld, dt_ld, dx_ld;
+    uint32_t* status;       // bounds-checked build: device status word (else null)
+    int32_t wdtype;
+};
+
+struct LnWgradParams {
+    const float* workspace;
+    void* dgamma;           // [cols] of wdtype, or null
+    void* dbeta;            // [cols] of wdtype, or null
+    int64_t cols;
+    int32_t parts, wdtype;
+};
+
+// vector: every row start is 16-byte aligned and rows are whole chunks.
+cudaError_t launch_ln_fwd(const LnFwdParams& p, int dtype, bool vector, int sms, cudaStream_t s);
+// *parts receives the number of workspace slices written.
+cudaError_t launch_ln_bwd(const LnBwdParams& p, int dtype, bool vector, int sms, int* parts, cudaStream_t s);
+cudaError_t launch_ln_wgrad(const LnWgradParams& p, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// Gradient norm and clip
+// ---------------------------------------------------------------------------
+
+constexpr int GRAD_MAXT = 1024;         // tensors per launch
+constexpr int GRAD_SMALL_MAXT = 64;     // tensors of the small parameter block
+constexpr int GRAD_PIECE_BYTES = 16384; // input bytes of one work piece
+static_assert(TB_GRAD_TABLE == GRAD_MAXT, "tensors per record set differ from the header");
+
+// The tensors of one launch.  Tensor t is `head[t]` elements up to its first
+// 16-byte boundary, whole 16-byte chunks, and a rest; its pieces are
+// start[t] .. start[t + 1] - 1, GRAD_PIECE_BYTES of its chunks each, the head
+// with the first and the rest with the last.
+template <int MAXT>
+struct GradParams {
+    const void* in[MAXT];
+    void* out[MAXT];              // clip only
+    int64_t numel[MAXT];
+    int32_t start[MAXT + 1];
+    uint8_t dtype[MAXT];
+    uint8_t head[MAXT];
+    double* records;              // this launch's TB_GRAD_PARTS records (stats), or all of them (clip)
+    int64_t n_records;            // clip only
+    float* norm;                  // clip only, or null
+    uint32_t* status;             // bounds-checked build: device status word (else null)
+    float max_norm;
+    int32_t T;
+    int32_t first;                // clip: the launch that writes the norm
+};
+using GradParamsSmall = GradParams<GRAD_SMALL_MAXT>;
+using GradParamsLarge = GradParams<GRAD_MAXT>;
+static_assert(sizeof(GradParamsLarge) <= 32000, "kernel parameter block too large");
+
+cudaError_t launch_grad_stats(const GradParamsSmall& p, int sms, cudaStream_t s);
+cudaError_t launch_grad_stats(const GradParamsLarge& p, int sms, cudaStream_t s);
+cudaError_t launch_grad_clip(const GradParamsSmall& p, int sms, cudaStream_t s);
+cudaError_t launch_grad_clip(const GradParamsLarge& p, int sms, cudaStream_t s);
+cudaError_t launch_grad_norm(const double* records, int64_t n, float* norm, cudaStream_t s);
+
+// Facts the host files share (tb_host.cpp).
+tb_status sm_count(int* sms);
+uint32_t* checked_build_status();
+
 }  // namespace tb

@@ -1,8 +1,10 @@
 """Python binding of libtileblend (include/tileblend.h).
 
-Argument marshalling only: every step of the stitch and of PatchGroupNorm
-runs in the library's CUDA kernels.  Tensors must be CUDA tensors on the
-current device, contiguous, of one dtype (float32, float16 or bfloat16).
+Argument marshalling only: every step of the stitch, of PatchGroupNorm and of
+the training calls (layer norm, gradient clipping, PatchGroupNorm's backward
+pass) runs in the library's CUDA kernels.  Tensors must be CUDA tensors on the
+current device, contiguous (the layer norm takes strided rows), of one dtype
+(float32, float16 or bfloat16).
 Calls are asynchronous on the current torch stream unless ``stream`` (a
 ``torch.cuda.Stream`` or a raw ``cudaStream_t`` integer) is given.
 
@@ -132,12 +134,40 @@ _lib.tb_gather_patches.restype = ctypes.c_int
 _lib.tb_gather_patches.argtypes = [_P_vp, _i32, _P_i64, ctypes.c_int, _i32, _P_i64, _i32, _i64, _vp, _vp]
 TB_MAX_PATCHES = 64
 
+
+_lib.tb_layer_norm.restype = ctypes.c_int
+_lib.tb_layer_norm.argtypes = [_vp, _i64, _vp, _i64, ctypes.c_int, _i64, _i64, _vp, _vp, ctypes.c_int, ctypes.c_float,
+                               _vp, _i64, _vp, _i64, _vp, _vp, _vp]
+_lib.tb_layer_norm_workspace.restype = _i64
+_lib.tb_layer_norm_workspace.argtypes = [_i64, _i64]
+_lib.tb_layer_norm_backward.restype = ctypes.c_int
+_lib.tb_layer_norm_backward.argtypes = [_vp, _i64, _vp, _i64, ctypes.c_int, _i64, _i64, _vp, _vp, _vp, ctypes.c_int,
+                                        _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp]
+_lib.tb_grad_records.restype = _i64
+_lib.tb_grad_records.argtypes = [_i32]
+_lib.tb_grad_stats.restype = ctypes.c_int
+_lib.tb_grad_stats.argtypes = [_P_vp, _P_i64, _P_i32, _i32, _vp, _vp]
+_lib.tb_grad_norm.restype = ctypes.c_int
+_lib.tb_grad_norm.argtypes = [_vp, _i64, _vp, _vp]
+_lib.tb_grad_clip.restype = ctypes.c_int
+_lib.tb_grad_clip.argtypes = [_P_vp, _P_vp, _P_i64, _P_i32, _i32, _vp, _i64, ctypes.c_float, _vp, _vp]
+_lib.tb_patch_gn_grad_stats.restype = ctypes.c_int
+_lib.tb_patch_gn_grad_stats.argtypes = [_P_vp, _P_vp, _i32, ctypes.c_int, _i64, _i64, _P_i64, _i32, _vp, _i32, _vp,
+                                        _vp, ctypes.c_float, _i32, _vp, _vp]
+_lib.tb_patch_gn_grad_apply.restype = ctypes.c_int
+_lib.tb_patch_gn_grad_apply.argtypes = [_P_vp, _P_vp, _P_vp, _i32, ctypes.c_int, _i64, _i64, _P_i64, _i32, _vp, _vp,
+                                        _i32, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp]
+TB_LN_PARTS = 512
+TB_MAX_GRADS, TB_GRAD_TABLE, TB_GRAD_PARTS = 65536, 1024, 1024
+
 EXPORTED = ("tb_version", "tb_status_string", "tb_last_cuda_error", "tb_axis_layout", "tb_stitch2d",
             "tb_stitch3d", "tb_stitch_shard_layout", "tb_stitch_halo_pack", "tb_stitch2d_shard",
             "tb_stitch3d_shard", "tb_stitch2d_ramp", "tb_patch_gn_stats", "tb_patch_gn_apply",
             "tb_patch_gn_apply_gathered", "tb_patch_group_norm_noalloc", "tb_patchify_layout", "tb_patchify",
             "tb_gather_patches", "tb_device_status", "tb_ramp_axis_spread", "tb_stitch_shard_frames_layout",
-            "tb_stitch_halo_pack_frames", "tb_stitch3d_shard_frames")
+            "tb_stitch_halo_pack_frames", "tb_stitch3d_shard_frames", "tb_layer_norm", "tb_layer_norm_workspace",
+            "tb_layer_norm_backward", "tb_grad_records", "tb_grad_stats", "tb_grad_norm", "tb_grad_clip",
+            "tb_patch_gn_grad_stats", "tb_patch_gn_grad_apply")
 
 
 class TileBlendError(RuntimeError):
@@ -741,3 +771,383 @@ def tb_gather_patches(patches: Sequence[torch.Tensor], sizes: Sequence[int], axi
                                   out.dim(), _shape_arr(shape), axis, slot, out.data_ptr(), _stream_handle(stream)),
            "tb_gather_patches")
     return out
+
+
+# ---------------------------------------------------------------------------
+# training: layer norm
+# ---------------------------------------------------------------------------
+
+def _on_stream(make, stream):
+    """Tensors made by ``make()`` for work on ``stream``: allocated with that
+    stream current, so that the allocator reuses their memory in its order."""
+    if stream is None:
+        return make()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _row_ld(t: torch.Tensor, shape, dtype, device: int, what: str) -> int:
+    """The row stride (elements) of a tensor seen as rows of its last axis."""
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError("%s has %s %s, expected %s %s" % (what, t.dtype, tuple(t.shape), dtype, tuple(shape)))
+    if t.get_device() != device:
+        raise ValueError("%s must be on the CUDA device of the other tensors" % what)
+    if t.is_contiguous():
+        return shape[-1]
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("%s: the elements of a row must be contiguous" % what)
+    ld, span = None, 1  # stride of the innermost row axis, and the rows inside the axis at hand
+    for size, st in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if ld is None:
+            ld = st
+        elif st != ld * span:
+            raise ValueError("%s: the rows must have one stride" % what)
+        span *= size
+    if ld is None:
+        return shape[-1]
+    if ld < shape[-1] and t.numel() > 0:
+        raise ValueError("%s: the rows overlap" % what)
+    return ld
+
+
+def _vec(t: Optional[torch.Tensor], n: int, dtype, device: int, what: str):
+    """Address of a contiguous 1D tensor of n elements, or None."""
+    if t is None:
+        return None
+    if t.numel() != n or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError("%s must be a contiguous [%d] %s tensor on the same device" % (what, n, dtype))
+    return t.data_ptr()
+
+
+def _ln_head(x: torch.Tensor, weights) -> Tuple[torch.Size, int, int, int, torch.dtype]:
+    if not x.is_cuda:
+        raise ValueError("the rows must be CUDA tensors")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("rows of at least one element")
+    shape = x.shape
+    cols = shape[-1]
+    wdtype = next((w.dtype for w in weights if w is not None), x.dtype)
+    if wdtype is not x.dtype and wdtype is not torch.float32:
+        raise ValueError("the weights must have the rows' dtype or float32, got %s" % wdtype)
+    return shape, x.numel() // cols, cols, x.get_device(), wdtype
+
+
+def tb_layer_norm(x: torch.Tensor, y: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor],
+                  eps: float, mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+                  residual: Optional[torch.Tensor] = None, total: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """Layer norm of x (or x + residual, which goes to ``total``) over the
+    last axis into ``y``.  ``x``, ``residual``, ``total`` and ``y`` are
+    [..., cols] with any row stride; ``gamma`` / ``beta`` [cols] of x's dtype
+    or float32; ``mean`` / ``rstd`` float32, one per row, for the backward
+    pass.  ``y`` may be ``x``; ``total`` may be ``x`` or ``residual``."""
+    shape, rows, cols, dev, wdt = _ln_head(x, (gamma, beta))
+    dt = x.dtype
+    x_ld, y_ld = _row_ld(x, shape, dt, dev, "x"), _row_ld(y, shape, dt, dev, "y")
+    rp = tp = None
+    r_ld = t_ld = 0
+    if residual is not None:
+        if total is None:
+            raise ValueError("a residual needs a total to write the sum to")
+        r_ld, t_ld = _row_ld(residual, shape, dt, dev, "residual"), _row_ld(total, shape, dt, dev, "total")
+        rp, tp = residual.data_ptr(), total.data_ptr()
+    elif total is not None:
+        raise ValueError("total without a residual")
+    _check(_lib.tb_layer_norm(x.data_ptr(), x_ld, rp, r_ld, _dtype_code(x), rows, cols,
+                              _vec(gamma, cols, wdt, dev, "gamma"), _vec(beta, cols, wdt, dev, "beta"),
+                              _DTYPES[wdt], eps, tp, t_ld, y.data_ptr(), y_ld,
+                              _vec(mean, rows, torch.float32, dev, "mean"),
+                              _vec(rstd, rows, torch.float32, dev, "rstd"), _stream_handle(stream)), "tb_layer_norm")
+    return y
+
+
+def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor], eps: float,
+               residual: Optional[torch.Tensor] = None, stream=None):
+    """``(y, mean, rstd)`` of tb_layer_norm in new tensors; with a residual
+    ``(y, mean, rstd, total)``."""
+    def make():
+        stats = torch.empty((2,) + tuple(x.shape[:-1]), dtype=torch.float32, device=x.device)
+        out = [torch.empty(x.shape, dtype=x.dtype, device=x.device), stats[0], stats[1]]
+        return out if residual is None else out + [torch.empty(x.shape, dtype=x.dtype, device=x.device)]
+    out = _on_stream(make, stream)
+    tb_layer_norm(x, out[0], gamma, beta, eps, out[1], out[2], residual, out[3] if residual is not None else None,
+                  stream)
+    return tuple(out)
+
+
+def ln_workspace(rows: int, cols: int, device=None) -> torch.Tensor:
+    """The device workspace of tb_layer_norm_backward for these sizes; it may
+    serve any number of calls in turn on one stream."""
+    n = int(_lib.tb_layer_norm_workspace(rows, cols))
+    if n < 0:
+        raise ValueError("no layer norm of %d rows of %d elements" % (rows, cols))
+    return torch.empty(n, dtype=torch.uint8, device=device or torch.device("cuda"))
+
+
+def tb_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                           gamma: Optional[torch.Tensor], dx: Optional[torch.Tensor], dgamma: Optional[torch.Tensor],
+                           dbeta: Optional[torch.Tensor], workspace: Optional[torch.Tensor],
+                           dtotal: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of tb_layer_norm: ``dx`` (rows like ``x``; ``x`` is what was
+    normalised, the total where there was a residual), ``dgamma`` / ``dbeta``
+    ([cols]; the sums over all rows).  ``dtotal`` is added to dx.  Any output
+    may be None; ``workspace`` comes from ``ln_workspace`` (None without
+    weight gradients)."""
+    shape, rows, cols, dev, wdt = _ln_head(x, (gamma, dgamma, dbeta))
+    dt = x.dtype
+    dy_ld, x_ld = _row_ld(dy, shape, dt, dev, "dy"), _row_ld(x, shape, dt, dev, "x")
+    dxp = dtp = None
+    dx_ld = dt_ld = 0
+    if dx is not None:
+        dx_ld, dxp = _row_ld(dx, shape, dt, dev, "dx"), dx.data_ptr()
+    if dtotal is not None:
+        dt_ld, dtp = _row_ld(dtotal, shape, dt, dev, "dtotal"), dtotal.data_ptr()
+    wp, wb = None, 0
+    if workspace is not None:
+        if not workspace.is_contiguous() or workspace.get_device() != dev:
+            raise ValueError("workspace must be contiguous, on the same device")
+        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(_lib.tb_layer_norm_backward(dy.data_ptr(), dy_ld, x.data_ptr(), x_ld, _dtype_code(x), rows, cols,
+                                       _vec(mean, rows, torch.float32, dev, "mean"),
+                                       _vec(rstd, rows, torch.float32, dev, "rstd"),
+                                       _vec(gamma, cols, wdt, dev, "gamma"), _DTYPES[wdt], dtp, dt_ld, dxp, dx_ld,
+                                       _vec(dgamma, cols, wdt, dev, "dgamma"), _vec(dbeta, cols, wdt, dev, "dbeta"),
+                                       wp, wb, _stream_handle(stream)), "tb_layer_norm_backward")
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                        gamma: Optional[torch.Tensor], dtotal: Optional[torch.Tensor] = None, wdtype=None,
+                        stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """``(dx, dgamma, dbeta)`` in new tensors (the weights' dtype is gamma's,
+    or ``wdtype``)."""
+    cols = x.shape[-1]
+    wdt = gamma.dtype if gamma is not None else wdtype or x.dtype
+
+    def make():
+        w = torch.empty((2, cols), dtype=wdt, device=x.device)
+        return (torch.empty(x.shape, dtype=x.dtype, device=x.device), torch.empty_like(w[0]), torch.empty_like(w[1]),
+                ln_workspace(x.numel() // max(1, cols), cols, x.device))
+    dx, dgamma, dbeta, ws = _on_stream(make, stream)
+    tb_layer_norm_backward(dy, x, mean, rstd, gamma, dx, dgamma, dbeta, ws, dtotal, stream)
+    return dx, dgamma, dbeta
+
+
+# ---------------------------------------------------------------------------
+# training: gradient norm and clip
+# ---------------------------------------------------------------------------
+
+class GradTable:
+    """The gradients of a program's parameters (``grads``), and where their
+    clipped values go (``outs``; None: in place), as the library takes them.
+    It holds the tensors and their addresses, none of their contents: make it
+    once, and again when a gradient tensor is replaced."""
+
+    def __init__(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None):
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        if len(self.outs) != len(self.grads):
+            raise ValueError("one output per gradient")
+        n = len(self.grads)
+        for q, (g, o) in enumerate(zip(self.grads, self.outs)):
+            _cuda_contig(g, "gradient %d" % q)
+            if o is not g:
+                _cuda_contig(o, "output %d" % q)
+                if o.shape != g.shape or o.dtype != g.dtype:
+                    raise ValueError("output %d must match gradient %d" % (q, q))
+            if g.device != self.grads[0].device or o.device != g.device:
+                raise ValueError("all gradients and outputs must be on one device")
+        self._in = _ptr_array([g.data_ptr() for g in self.grads])
+        self._out = _ptr_array([o.data_ptr() for o in self.outs])
+        self._numel = (ctypes.c_int64 * max(1, n))(*[g.numel() for g in self.grads])
+        self._dtypes = (ctypes.c_int32 * max(1, n))(*[_dtype_code(g) for g in self.grads])
+
+    def __len__(self) -> int:
+        return len(self.grads)
+
+
+def new_grad_records(T: int, device=None) -> torch.Tensor:
+    """Device buffer (float64) for the records tb_grad_stats writes for T
+    tensors."""
+    n = int(_lib.tb_grad_records(T))
+    if n < 0:
+        raise ValueError("at most %d gradients in one call" % TB_MAX_GRADS)
+    return torch.empty(n, dtype=torch.float64, device=device or torch.device("cuda"))
+
+
+def _records(records: torch.Tensor, least: int) -> int:
+    _cuda_contig(records, "records")
+    if records.dtype != torch.float64 or records.numel() < least:
+        raise ValueError("records must hold at least %d float64 values" % least)
+    return records.data_ptr()
+
+
+def tb_grad_stats(table: GradTable, records: torch.Tensor, stream=None) -> torch.Tensor:
+    """Sums of squares of the table's gradients into ``records`` (from
+    ``new_grad_records``)."""
+    need = int(_lib.tb_grad_records(len(table)))
+    if need >= 0 and records.numel() != need:
+        raise ValueError("records must hold exactly %d values for %d gradients" % (need, len(table)))
+    _check(_lib.tb_grad_stats(table._in, table._numel, table._dtypes, len(table), _records(records, 0),
+                              _stream_handle(stream)), "tb_grad_stats")
+    return records
+
+
+def _norm_ptr(norm: Optional[torch.Tensor]):
+    if norm is None:
+        return None
+    _cuda_contig(norm, "norm")
+    if norm.dtype != torch.float32 or norm.numel() != 1:
+        raise ValueError("norm must be one float32")
+    return norm.data_ptr()
+
+
+def tb_grad_norm(records: torch.Tensor, norm: torch.Tensor, stream=None) -> torch.Tensor:
+    """The global norm that ``records`` (one or more record sets) describe."""
+    _check(_lib.tb_grad_norm(_records(records, 0), records.numel(), _norm_ptr(norm), _stream_handle(stream)),
+           "tb_grad_norm")
+    return norm
+
+
+def tb_grad_clip(table: GradTable, records: torch.Tensor, max_norm: float, norm: Optional[torch.Tensor] = None,
+                 stream=None) -> None:
+    """Every gradient of the table times min(1, max_norm / (norm + 1e-6)), into
+    its output; the norm is that of all ``records``."""
+    _check(_lib.tb_grad_clip(table._in, table._out, table._numel, table._dtypes, len(table), _records(records, 0),
+                             records.numel(), max_norm, _norm_ptr(norm), _stream_handle(stream)), "tb_grad_clip")
+
+
+def clip_grad_norm(grads, max_norm: float, records: Optional[torch.Tensor] = None,
+                   norm: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Both steps: the global norm of ``grads`` (a GradTable, or tensors to be
+    clipped in place), then the clip.  Returns the norm before it (a [1]
+    float32 tensor)."""
+    table = grads if isinstance(grads, GradTable) else GradTable(grads)
+    device = table.grads[0].device if len(table) else None
+    if records is None:
+        records = _on_stream(lambda: new_grad_records(len(table), device), stream)
+    if norm is None:
+        norm = _on_stream(lambda: torch.empty(1, dtype=torch.float32, device=records.device), stream)
+    handle = _stream_handle(stream)
+    tb_grad_stats(table, records, handle)
+    tb_grad_clip(table, records, max_norm, norm, handle)
+    return norm
+
+
+# ---------------------------------------------------------------------------
+# training: PatchGroupNorm backward
+# ---------------------------------------------------------------------------
+
+def new_grad_partials(P: int, N: int, C: int, device=None) -> torch.Tensor:
+    """Device buffer for the P * N * C * TB_GN_PARTS tb_gn_grad_partial records
+    (8 bytes each) that tb_patch_gn_grad_stats writes."""
+    return torch.empty((P, N, C, TB_GN_PARTS, 2), dtype=torch.float32, device=device or torch.device("cuda"))
+
+
+def _gn_grad_args(grads, patches, G, partials, R, gamma, beta):
+    N, C, dt, spatial, ptrs = _gn_args(patches)
+    if len(grads) != len(patches):
+        raise ValueError("one gradient per patch")
+    gptrs = []
+    for q, (d, t) in enumerate(zip(grads, patches)):
+        _cuda_contig(d, "gradient %d" % q)
+        if d.shape != t.shape or d.dtype != t.dtype:
+            raise ValueError("gradient %d must match patch %d" % (q, q))
+        gptrs.append(d.data_ptr())
+    for name, v in (("gamma", gamma), ("beta", beta)):
+        if v is not None:
+            _cuda_contig(v, name)
+            if v.numel() != C or v.dtype != patches[0].dtype:
+                raise ValueError("%s must be [C] of the patches' dtype" % name)
+    _cuda_contig(partials, "partials")
+    if partials.numel() * partials.element_size() != R * N * G * TB_GN_PARTS * 16:
+        raise ValueError("partials must hold R*N*G*TB_GN_PARTS 16-byte records")
+    return N, C, dt, (ctypes.c_int64 * len(spatial))(*spatial), _ptr_array(ptrs), _ptr_array(gptrs)
+
+
+def _grad_partials(t: torch.Tensor, R: int, N: int, C: int) -> int:
+    _cuda_contig(t, "grad_partials")
+    if t.numel() * t.element_size() != R * N * C * TB_GN_PARTS * 8:
+        raise ValueError("grad_partials must hold R*N*C*TB_GN_PARTS 8-byte records")
+    return t.data_ptr()
+
+
+def tb_patch_gn_grad_stats(grads: Sequence[torch.Tensor], patches: Sequence[torch.Tensor], G: int,
+                           partials: torch.Tensor, R: int, gamma: Optional[torch.Tensor],
+                           beta: Optional[torch.Tensor], eps: float, grad_partials: torch.Tensor, silu: bool = True,
+                           stream=None) -> torch.Tensor:
+    """Sums of dz and dz * xhat of every part of every (patch, sample,
+    channel) into ``grad_partials`` (from ``new_grad_partials``).  ``grads``
+    are the gradients of the norm's outputs, ``patches`` its inputs,
+    ``partials`` the forward pass's ``R`` record sets."""
+    N, C, dt, sp, xs, ds = _gn_grad_args(grads, patches, G, partials, R, gamma, beta)
+    P = len(patches)
+    _check(_lib.tb_patch_gn_grad_stats(xs, ds, P, dt, N, C, sp, G, partials.data_ptr(), R,
+                                       gamma.data_ptr() if gamma is not None else None,
+                                       beta.data_ptr() if beta is not None else None, float(eps), 1 if silu else 0,
+                                       _grad_partials(grad_partials, P, N, C), _stream_handle(stream)),
+           "tb_patch_gn_grad_stats")
+    return grad_partials
+
+
+def tb_patch_gn_grad_apply(grads: Sequence[torch.Tensor], patches: Sequence[torch.Tensor],
+                           dxs: Sequence[torch.Tensor], G: int, partials: torch.Tensor, grad_partials: torch.Tensor,
+                           R: int, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor], eps: float,
+                           dgamma: Optional[torch.Tensor] = None, dbeta: Optional[torch.Tensor] = None,
+                           silu: bool = True, stream=None) -> Sequence[torch.Tensor]:
+    """The gradients of the patches into ``dxs`` (``dxs[p]`` may be
+    ``grads[p]`` or ``patches[p]``), and of the weights into ``dgamma`` /
+    ``dbeta`` ([C] of the patches' dtype), from the ``R`` record sets of both
+    passes."""
+    N, C, dt, sp, xs, ds = _gn_grad_args(grads, patches, G, partials, R, gamma, beta)
+    P = len(patches)
+    if len(dxs) != P:
+        raise ValueError("one output per patch")
+    for q, (o, t) in enumerate(zip(dxs, patches)):
+        _cuda_contig(o, "dx %d" % q)
+        if o.shape != t.shape or o.dtype != t.dtype:
+            raise ValueError("dx %d must match patch %d" % (q, q))
+    wp = []
+    for name, v in (("dgamma", dgamma), ("dbeta", dbeta)):
+        if v is not None:
+            _cuda_contig(v, name)
+            if v.numel() != C or v.dtype != patches[0].dtype:
+                raise ValueError("%s must be [C] of the patches' dtype" % name)
+        wp.append(v.data_ptr() if v is not None else None)
+    _check(_lib.tb_patch_gn_grad_apply(xs, ds, _ptr_array([o.data_ptr() for o in dxs]), P, dt, N, C, sp, G,
+                                       partials.data_ptr(), _grad_partials(grad_partials, R, N, C), R,
+                                       gamma.data_ptr() if gamma is not None else None,
+                                       beta.data_ptr() if beta is not None else None, float(eps), 1 if silu else 0,
+                                       wp[0], wp[1], _stream_handle(stream)), "tb_patch_gn_grad_apply")
+    return dxs
+
+
+def patch_group_norm_backward(grads: Sequence[torch.Tensor], patches: Sequence[torch.Tensor], G: int,
+                              partials: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor],
+                              eps: float, silu: bool = True, dxs: Optional[Sequence[torch.Tensor]] = None,
+                              dgamma: Optional[torch.Tensor] = None, dbeta: Optional[torch.Tensor] = None,
+                              grad_partials: Optional[torch.Tensor] = None, stream=None):
+    """Both steps of the backward pass of ``patch_group_norm``: ``(dxs, dgamma,
+    dbeta)``.  ``partials`` are the forward pass's records of these patches;
+    outputs that are not given are made."""
+    P = len(patches)
+    if P == 0:
+        raise ValueError("at least one patch")
+    _cuda_contig(patches[0], "patch 0")
+    N, C = patches[0].shape[:2]
+
+    def make():
+        w = torch.empty((2, C), dtype=patches[0].dtype, device=patches[0].device)
+        return ([torch.empty_like(p) for p in patches] if dxs is None else dxs,
+                torch.empty_like(w[0]) if dgamma is None else dgamma,
+                torch.empty_like(w[1]) if dbeta is None else dbeta,
+                new_grad_partials(P, N, C, patches[0].device) if grad_partials is None else grad_partials)
+    dxs, dgamma, dbeta, grad_partials = _on_stream(make, stream)
+    handle = _stream_handle(stream)
+    tb_patch_gn_grad_stats(grads, patches, G, partials, P, gamma, beta, eps, grad_partials, silu, handle)
+    tb_patch_gn_grad_apply(grads, patches, dxs, G, partials, grad_partials, P, gamma, beta, eps, dgamma, dbeta, silu,
+                           handle)
+    return dxs, dgamma, dbeta

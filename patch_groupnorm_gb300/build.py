@@ -31,10 +31,11 @@ UNITS = {
     "tb_shard.cu": [],
     "tb_status.cu": [],
     "tb_layernorm.cu": [],
+    "tb_layernorm_bwd.cu": [],
     "tb_gradclip.cu": [],
     "tb_train.cpp": [],
 }
-HEADERS = ["tb_internal.h", "tb_elem.cuh"]
+HEADERS = ["tb_internal.h", "tb_elem.cuh", "tb_layernorm.cuh"]
 
 
 def _nvcc() -> str:

@@ -108,6 +108,89 @@ __device__ __forceinline__ typename Word<VEC * elem_size(DT)>::T pack(const floa
     }
 }
 
+// fp32 arithmetic on pairs of lanes (one instruction for two elements, each
+// lane rounded as the scalar instruction rounds) and on single elements.
+using f32x2 = unsigned long long;
+
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void halves(f32x2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 vadd(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 vsub(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 vmul(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 vfma(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float vsum(f32x2 v) {
+    float lo, hi;
+    halves(v, lo, hi);
+    return lo + hi;
+}
+__device__ __forceinline__ float vadd(float a, float b) { return a + b; }
+__device__ __forceinline__ float vsub(float a, float b) { return a - b; }
+__device__ __forceinline__ float vmul(float a, float b) { return a * b; }
+__device__ __forceinline__ float vfma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float vsum(float v) { return v; }
+
+// The lanes of a chunk: VEC / 2 pairs, or one single element.
+template <int VEC>
+struct Lanes {
+    using T = f32x2;
+    static constexpr int N = VEC / 2;
+    __device__ __forceinline__ static T splat(float v) { return pair(v, v); }
+};
+template <>
+struct Lanes<1> {
+    using T = float;
+    static constexpr int N = 1;
+    __device__ __forceinline__ static T splat(float v) { return v; }
+};
+
+template <int DT, int VEC>
+__device__ __forceinline__ void to_lanes(const typename Word<VEC * elem_size(DT)>::T& w,
+                                         typename Lanes<VEC>::T (&f)[Lanes<VEC>::N]) {
+    float e[VEC];
+    unpack<DT, VEC>(w, e);
+    if constexpr (VEC == 1) {
+        f[0] = e[0];
+    } else {
+#pragma unroll
+        for (int q = 0; q < VEC / 2; ++q) f[q] = pair(e[2 * q], e[2 * q + 1]);
+    }
+}
+
+template <int DT, int VEC>
+__device__ __forceinline__ typename Word<VEC * elem_size(DT)>::T from_lanes(
+    const typename Lanes<VEC>::T (&f)[Lanes<VEC>::N]) {
+    float e[VEC];
+    if constexpr (VEC == 1) {
+        e[0] = f[0];
+    } else {
+#pragma unroll
+        for (int q = 0; q < VEC / 2; ++q) halves(f[q], e[2 * q], e[2 * q + 1]);
+    }
+    return pack<DT, VEC>(e);
+}
+
 // Element i of a weight vector whose type is the rows' or f32, as f32.
 __device__ __forceinline__ float weight_at(const void* w, int dtype, int64_t i, float dflt) {
     if (w == nullptr) return dflt;
@@ -143,6 +226,39 @@ __device__ __forceinline__ void weights_at(const void* w, int dtype, int64_t i, 
         }
     }
 }
+
+// One chunk's weights as a thread keeps them over its rows: fp32 lanes
+// (WIDE), or packed in the rows' type.
+template <int DT, int VEC, bool WIDE>
+struct Weights {
+    using L = Lanes<VEC>;
+    typename L::T f[L::N];
+    __device__ __forceinline__ void load(const void* w, int dtype, int64_t i, float dflt) {
+        float e[VEC];
+        weights_at<VEC, true>(w, dtype, i, dflt, e);
+        if constexpr (VEC == 1) {
+            f[0] = e[0];
+        } else {
+#pragma unroll
+            for (int q = 0; q < VEC / 2; ++q) f[q] = pair(e[2 * q], e[2 * q + 1]);
+        }
+    }
+    __device__ __forceinline__ void get(typename L::T (&o)[L::N]) const {
+#pragma unroll
+        for (int q = 0; q < L::N; ++q) o[q] = f[q];
+    }
+};
+template <int DT, int VEC>
+struct Weights<DT, VEC, false> {
+    using L = Lanes<VEC>;
+    typename Word<VEC * elem_size(DT)>::T v;
+    __device__ __forceinline__ void load(const void* w, int dtype, int64_t i, float dflt) {
+        float e[VEC];
+        weights_at<VEC, true>(w, dtype, i, dflt, e);
+        v = pack<DT, VEC>(e);
+    }
+    __device__ __forceinline__ void get(typename L::T (&o)[L::N]) const { to_lanes<DT, VEC>(v, o); }
+};
 
 __device__ __forceinline__ void store_weight(void* w, int dtype, int64_t i, float v) {
     if (dtype == F32) {

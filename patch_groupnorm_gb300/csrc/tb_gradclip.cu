@@ -10,10 +10,11 @@
 // same bits every time) and scale their pieces, walking them from the last
 // to the first: the pieces the first kernel read last are still in L2.
 //
-// Within a piece a thread adds the squares of its elements in fp32 and
-// carries the pieces' sums in fp64.  A thread whose fp32 sum could have
-// overflowed or lost squares to underflow takes them again scaled by a power
-// of two, so any finite gradients give their norm wherever fp32 can hold it.
+// Within a piece a thread adds the squares of its elements in fp32, and it
+// carries the pieces' sums with their rounding errors.  A thread whose fp32
+// sum could have overflowed or lost squares to underflow takes them again
+// scaled by a power of two, so any finite gradients give their norm wherever
+// fp32 can hold it.
 #include "tb_elem.cuh"
 
 namespace tb {
@@ -72,12 +73,20 @@ __device__ __forceinline__ float squares(const uint4& v, float scale) {
 }
 
 // fp32 sums of squares inside (LOW, HIGH) have lost nothing: a sum below LOW
-// may miss squares that underflowed, one above HIGH may be about to overflow.
-constexpr float SQ_LOW = 0x1p-90f, SQ_HIGH = 0x1p120f;
+// may miss squares that underflowed, one above HIGH may soon overflow.  Such
+// sums are taken again of the elements times or over 2^96, and kept apart.
+constexpr float SQ_LOW = 0x1p-90f, SQ_HIGH = 0x1p100f;
 constexpr float SQ_SCALE = 0x1p96f;
 
+// A thread's sums: the ordinary ones with their rounding errors (Knuth's
+// two-sum), those of squares times 2^192 and over 2^192.
+struct Squares {
+    float sum = 0.f, err = 0.f, small = 0.f, large = 0.f;
+};
+
 template <int DT>
-__device__ __forceinline__ double piece_squares(const void* base, int64_t numel, const Piece& c, uint32_t* status) {
+__device__ __forceinline__ void piece_squares(Squares& acc, const void* base, int64_t numel, const Piece& c,
+                                              uint32_t* status) {
     constexpr int VEC = 16 / elem_size(DT);
     const char* const b = reinterpret_cast<const char*>(base);
     const int64_t bytes = numel * elem_size(DT);
@@ -104,18 +113,25 @@ __device__ __forceinline__ double piece_squares(const void* base, int64_t numel,
         for (int k = 0; k < GC_CPT; ++k) a += squares<DT>(v[k], scale);
         return a;
     };
-    const float s = total(1.f);
-    if (s > SQ_LOW && s < SQ_HIGH) return (double)s;
-    if (s < 1.f) return (double)total(SQ_SCALE) * 0x1p-192;
-    return (double)total(1.f / SQ_SCALE) * 0x1p192;
+    const float v2 = total(1.f);
+    if (v2 > SQ_LOW && v2 < SQ_HIGH) {
+        const float t = acc.sum + v2, b2 = t - acc.sum;
+        acc.err += (acc.sum - (t - b2)) + (v2 - b2);
+        acc.sum = t;
+    } else if (v2 < 1.f) {
+        acc.small += total(SQ_SCALE);
+    } else {
+        acc.large += total(1.f / SQ_SCALE);
+    }
 }
 
-__device__ __forceinline__ double block_sum(double v, double* slots) {
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+// Sum over the CTA; every thread gets it.  `slots` must not be reused before
+// another barrier.
+__device__ __forceinline__ float block_sum(float v, float* slots) {
+    v = warp_sum(v);
     if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0.0;
+    v = 0.f;
 #pragma unroll
     for (int w = 0; w < GC_BLOCK / 32; ++w) v += slots[w];
     return v;
@@ -123,32 +139,84 @@ __device__ __forceinline__ double block_sum(double v, double* slots) {
 
 template <int MAXT>
 __global__ void __launch_bounds__(GC_BLOCK, GC_CTAS) grad_stats_kernel(const __grid_constant__ GradParams<MAXT> p) {
-    __shared__ double s_part[GC_BLOCK / 32];
+    __shared__ float s_part[3][GC_BLOCK / 32];
     const int64_t total = p.start[p.T];
     const int begin = (int)(total * blockIdx.x / gridDim.x), end = (int)(total * (blockIdx.x + 1) / gridDim.x);
     int t = begin < end ? tensor_of(p, begin) : 0;
     grid_wait();
-    double acc = 0.0;
+    Squares acc;
     for (int piece = begin; piece < end; ++piece) {
         while (p.start[t + 1] <= piece) ++t;
         const Piece c = piece_of(p, t, piece);
         const int dt = p.dtype[t];
-        if (dt == F32) acc += piece_squares<F32>(p.in[t], p.numel[t], c, p.status);
-        else if (dt == F16) acc += piece_squares<F16>(p.in[t], p.numel[t], c, p.status);
-        else acc += piece_squares<BF16>(p.in[t], p.numel[t], c, p.status);
+        if (dt == F32) piece_squares<F32>(acc, p.in[t], p.numel[t], c, p.status);
+        else if (dt == F16) piece_squares<F16>(acc, p.in[t], p.numel[t], c, p.status);
+        else piece_squares<BF16>(acc, p.in[t], p.numel[t], c, p.status);
     }
-    acc = block_sum(acc, s_part);
+    const float sum = block_sum(acc.sum + acc.err, s_part[0]);
+    const bool scaled = __syncthreads_or(acc.small != 0.f || acc.large != 0.f);
+    float small = 0.f, large = 0.f;
+    if (scaled) {
+        small = block_sum(acc.small, s_part[1]);
+        large = block_sum(acc.large, s_part[2]);
+    }
     if (threadIdx.x == 0) {
-        p.records[blockIdx.x] = acc;
+        double r = (double)sum;
+        if (scaled) r += (double)small * 0x1p-192 + (double)large * 0x1p192;
+        p.records[blockIdx.x] = r;
         for (int k = blockIdx.x + gridDim.x; k < TB_GRAD_PARTS; k += gridDim.x) p.records[k] = 0.0;
     }
 }
 
-// The norm from all records, the same in every CTA.
-__device__ __forceinline__ float norm_of(const double* records, int64_t n, double* slots) {
-    double v = 0.0;
-    for (int64_t k = threadIdx.x; k < n; k += GC_BLOCK) v += records[k];
-    return (float)sqrt(block_sum(v, slots));
+// The norm from all records, the same in every CTA: the records' fp64 values
+// are added in 64-bit fixed point relative to the largest one's exponent (exact
+// sums, in any order, on the integer units: fp64 additions took longer than
+// the rest of a small clip, 10 of 18 us for 3.5 M elements).  An infinite
+// record makes the norm infinite, a NaN one NaN.
+__device__ __forceinline__ float norm_of(const double* records, int64_t n) {
+    __shared__ uint32_t s_max[GC_BLOCK / 32];
+    __shared__ unsigned long long s_sum[GC_BLOCK / 32];
+    constexpr int KEEP = TB_GRAD_PARTS / GC_BLOCK;  // one record set stays in registers
+    const unsigned long long* const bits = reinterpret_cast<const unsigned long long*>(records);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned long long r[KEEP];
+    uint32_t top = 0u;
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k) {
+        const int64_t i = threadIdx.x + k * GC_BLOCK;
+        r[k] = i < n ? bits[i] : 0ull;
+        top = max(top, (uint32_t)(r[k] >> 32));
+    }
+    for (int64_t i = threadIdx.x + KEEP * GC_BLOCK; i < n; i += GC_BLOCK) top = max(top, (uint32_t)(bits[i] >> 32));
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) s_max[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < GC_BLOCK / 32; ++w) top = max(top, s_max[w]);
+    if (top >= 0x7ff00000u) return top == 0x7ff00000u ? INFINITY : NAN;
+    // 53-bit mantissas: 1024 of them fit 63 bits, more are shifted down
+    const int head = n <= 1024 ? 0 : 64 - __clzll(n - 1) - 10;
+    const int e_top = (int)(top >> 20);
+    unsigned long long sum = 0ull;
+    auto add = [&](unsigned long long v) {
+        const int e = (int)(v >> 52);
+        const int shift = e_top - e + head;
+        if (e > 0 && shift < 64) sum += ((v & 0xfffffffffffffull) | 0x10000000000000ull) >> shift;
+    };
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k) add(r[k]);
+    for (int64_t i = threadIdx.x + KEEP * GC_BLOCK; i < n; i += GC_BLOCK) add(bits[i]);
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    sum = 0ull;
+#pragma unroll
+    for (int w = 0; w < GC_BLOCK / 32; ++w) sum += s_sum[w];
+    // sqrt(sum * 2^e): fp32 roundings of the sum, the root and the result
+    const int e = e_top - 1075 + head;
+    const float odd = (e & 1) ? 2.f : 1.f;
+    return ldexpf(sqrtf((float)sum * odd), (e - (e & 1)) / 2);
 }
 
 template <int DT>
@@ -201,12 +269,11 @@ __device__ __forceinline__ void piece_scale(const void* in, void* out, int64_t n
 
 template <int MAXT>
 __global__ void __launch_bounds__(GC_BLOCK, GC_CTAS) grad_clip_kernel(const __grid_constant__ GradParams<MAXT> p) {
-    __shared__ double s_part[GC_BLOCK / 32];
     const int64_t total = p.start[p.T];
     const int begin = (int)(total * blockIdx.x / gridDim.x), end = (int)(total * (blockIdx.x + 1) / gridDim.x);
     int t = begin < end ? tensor_of(p, end - 1) : 0;
     grid_wait();
-    const float norm = norm_of(p.records, p.n_records, s_part);
+    const float norm = norm_of(p.records, p.n_records);
     if (p.first && p.norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = norm;
     const float q = p.max_norm / (norm + 1e-6f);
     const float coef = q >= 1.f ? 1.f : q;  // a NaN stays one
@@ -228,9 +295,8 @@ struct GradNormParams {
 };
 
 __global__ void __launch_bounds__(GC_BLOCK) grad_norm_kernel(const __grid_constant__ GradNormParams p) {
-    __shared__ double s_part[GC_BLOCK / 32];
     grid_wait();
-    const float norm = norm_of(p.records, p.n, s_part);
+    const float norm = norm_of(p.records, p.n);
     if (threadIdx.x == 0) *p.norm = norm;
 }
 

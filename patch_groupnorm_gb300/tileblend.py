@@ -246,7 +246,8 @@ def tb_axis_layout(axis: Axis) -> Layout:
 
 def _stream_handle(stream) -> Optional[int]:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without making a Stream object (2.9 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -788,6 +789,13 @@ def _on_stream(make, stream):
         return make()
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream_of(stream, device: int) -> int:
+    return _raw_stream(device) if stream is None else _stream_handle(stream)
+
+
 def _row_ld(t: torch.Tensor, shape, dtype, device: int, what: str) -> int:
     """The row stride (elements) of a tensor seen as rows of its last axis."""
     if t.shape != shape or t.dtype is not dtype:
@@ -815,25 +823,26 @@ def _row_ld(t: torch.Tensor, shape, dtype, device: int, what: str) -> int:
 
 
 def _vec(t: Optional[torch.Tensor], n: int, dtype, device: int, what: str):
-    """Address of a contiguous 1D tensor of n elements, or None."""
+    """Address of a contiguous tensor of n elements, or None."""
     if t is None:
         return None
-    if t.numel() != n or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != device:
+    if t.numel() != n or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous [%d] %s tensor on the same device" % (what, n, dtype))
     return t.data_ptr()
 
 
-def _ln_head(x: torch.Tensor, weights) -> Tuple[torch.Size, int, int, int, torch.dtype]:
-    if not x.is_cuda:
+def _ln_head(x: torch.Tensor, weight: Optional[torch.Tensor]) -> Tuple[torch.Size, int, int, int, torch.dtype]:
+    """(shape, rows, cols, device, weights' dtype) of a layer norm of x."""
+    shape, dev = x.shape, x.get_device()
+    if dev < 0:
         raise ValueError("the rows must be CUDA tensors")
-    if x.dim() < 1 or x.shape[-1] < 1:
+    if not shape or shape[-1] < 1:
         raise ValueError("rows of at least one element")
-    shape = x.shape
     cols = shape[-1]
-    wdtype = next((w.dtype for w in weights if w is not None), x.dtype)
+    wdtype = x.dtype if weight is None else weight.dtype
     if wdtype is not x.dtype and wdtype is not torch.float32:
         raise ValueError("the weights must have the rows' dtype or float32, got %s" % wdtype)
-    return shape, x.numel() // cols, cols, x.get_device(), wdtype
+    return shape, x.numel() // cols, cols, dev, wdtype
 
 
 def tb_layer_norm(x: torch.Tensor, y: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor],
@@ -845,9 +854,8 @@ def tb_layer_norm(x: torch.Tensor, y: torch.Tensor, gamma: Optional[torch.Tensor
     [..., cols] with any row stride; ``gamma`` / ``beta`` [cols] of x's dtype
     or float32; ``mean`` / ``rstd`` float32, one per row, for the backward
     pass.  ``y`` may be ``x``; ``total`` may be ``x`` or ``residual``."""
-    shape, rows, cols, dev, wdt = _ln_head(x, (gamma, beta))
+    shape, rows, cols, dev, wdt = _ln_head(x, beta if gamma is None else gamma)
     dt = x.dtype
-    x_ld, y_ld = _row_ld(x, shape, dt, dev, "x"), _row_ld(y, shape, dt, dev, "y")
     rp = tp = None
     r_ld = t_ld = 0
     if residual is not None:
@@ -857,11 +865,13 @@ def tb_layer_norm(x: torch.Tensor, y: torch.Tensor, gamma: Optional[torch.Tensor
         rp, tp = residual.data_ptr(), total.data_ptr()
     elif total is not None:
         raise ValueError("total without a residual")
-    _check(_lib.tb_layer_norm(x.data_ptr(), x_ld, rp, r_ld, _dtype_code(x), rows, cols,
-                              _vec(gamma, cols, wdt, dev, "gamma"), _vec(beta, cols, wdt, dev, "beta"),
-                              _DTYPES[wdt], eps, tp, t_ld, y.data_ptr(), y_ld,
-                              _vec(mean, rows, torch.float32, dev, "mean"),
-                              _vec(rstd, rows, torch.float32, dev, "rstd"), _stream_handle(stream)), "tb_layer_norm")
+    status = _lib.tb_layer_norm(x.data_ptr(), _row_ld(x, shape, dt, dev, "x"), rp, r_ld, _dtype_code(x), rows, cols,
+                                _vec(gamma, cols, wdt, dev, "gamma"), _vec(beta, cols, wdt, dev, "beta"),
+                                _DTYPES[wdt], eps, tp, t_ld, y.data_ptr(), _row_ld(y, shape, dt, dev, "y"),
+                                _vec(mean, rows, torch.float32, dev, "mean"),
+                                _vec(rstd, rows, torch.float32, dev, "rstd"), _stream_of(stream, dev))
+    if status:
+        raise TileBlendError(status, "tb_layer_norm")
     return y
 
 
@@ -897,7 +907,8 @@ def tb_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor
     ([cols]; the sums over all rows).  ``dtotal`` is added to dx.  Any output
     may be None; ``workspace`` comes from ``ln_workspace`` (None without
     weight gradients)."""
-    shape, rows, cols, dev, wdt = _ln_head(x, (gamma, dgamma, dbeta))
+    weight = gamma if gamma is not None else dgamma if dgamma is not None else dbeta
+    shape, rows, cols, dev, wdt = _ln_head(x, weight)
     dt = x.dtype
     dy_ld, x_ld = _row_ld(dy, shape, dt, dev, "dy"), _row_ld(x, shape, dt, dev, "x")
     dxp = dtp = None
@@ -916,7 +927,7 @@ def tb_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor
                                        _vec(rstd, rows, torch.float32, dev, "rstd"),
                                        _vec(gamma, cols, wdt, dev, "gamma"), _DTYPES[wdt], dtp, dt_ld, dxp, dx_ld,
                                        _vec(dgamma, cols, wdt, dev, "dgamma"), _vec(dbeta, cols, wdt, dev, "dbeta"),
-                                       wp, wb, _stream_handle(stream)), "tb_layer_norm_backward")
+                                       wp, wb, _stream_of(stream, dev)), "tb_layer_norm_backward")
 
 
 def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
@@ -960,10 +971,12 @@ class GradTable:
                     raise ValueError("output %d must match gradient %d" % (q, q))
             if g.device != self.grads[0].device or o.device != g.device:
                 raise ValueError("all gradients and outputs must be on one device")
+        self.device = self.grads[0].device if n else None
         self._in = _ptr_array([g.data_ptr() for g in self.grads])
         self._out = _ptr_array([o.data_ptr() for o in self.outs])
         self._numel = (ctypes.c_int64 * max(1, n))(*[g.numel() for g in self.grads])
         self._dtypes = (ctypes.c_int32 * max(1, n))(*[_dtype_code(g) for g in self.grads])
+        self._records = int(_lib.tb_grad_records(n))
 
     def __len__(self) -> int:
         return len(self.grads)
@@ -978,37 +991,35 @@ def new_grad_records(T: int, device=None) -> torch.Tensor:
     return torch.empty(n, dtype=torch.float64, device=device or torch.device("cuda"))
 
 
-def _records(records: torch.Tensor, least: int) -> int:
-    _cuda_contig(records, "records")
-    if records.dtype != torch.float64 or records.numel() < least:
-        raise ValueError("records must hold at least %d float64 values" % least)
+def _records(records: torch.Tensor) -> int:
+    if records.get_device() < 0 or records.dtype is not torch.float64 or not records.is_contiguous():
+        raise ValueError("records must be a contiguous float64 CUDA tensor")
     return records.data_ptr()
 
 
 def tb_grad_stats(table: GradTable, records: torch.Tensor, stream=None) -> torch.Tensor:
     """Sums of squares of the table's gradients into ``records`` (from
     ``new_grad_records``)."""
-    need = int(_lib.tb_grad_records(len(table)))
-    if need >= 0 and records.numel() != need:
-        raise ValueError("records must hold exactly %d values for %d gradients" % (need, len(table)))
-    _check(_lib.tb_grad_stats(table._in, table._numel, table._dtypes, len(table), _records(records, 0),
-                              _stream_handle(stream)), "tb_grad_stats")
+    at = _records(records)
+    if records.numel() != table._records and table._records >= 0:
+        raise ValueError("records must hold exactly %d values for %d gradients" % (table._records, len(table)))
+    _check(_lib.tb_grad_stats(table._in, table._numel, table._dtypes, len(table), at,
+                              _stream_of(stream, records.get_device())), "tb_grad_stats")
     return records
 
 
 def _norm_ptr(norm: Optional[torch.Tensor]):
     if norm is None:
         return None
-    _cuda_contig(norm, "norm")
-    if norm.dtype != torch.float32 or norm.numel() != 1:
-        raise ValueError("norm must be one float32")
+    if norm.get_device() < 0 or norm.dtype is not torch.float32 or norm.numel() != 1:
+        raise ValueError("norm must be one float32 on the GPU")
     return norm.data_ptr()
 
 
 def tb_grad_norm(records: torch.Tensor, norm: torch.Tensor, stream=None) -> torch.Tensor:
     """The global norm that ``records`` (one or more record sets) describe."""
-    _check(_lib.tb_grad_norm(_records(records, 0), records.numel(), _norm_ptr(norm), _stream_handle(stream)),
-           "tb_grad_norm")
+    _check(_lib.tb_grad_norm(_records(records), records.numel(), _norm_ptr(norm),
+                             _stream_of(stream, records.get_device())), "tb_grad_norm")
     return norm
 
 
@@ -1016,8 +1027,9 @@ def tb_grad_clip(table: GradTable, records: torch.Tensor, max_norm: float, norm:
                  stream=None) -> None:
     """Every gradient of the table times min(1, max_norm / (norm + 1e-6)), into
     its output; the norm is that of all ``records``."""
-    _check(_lib.tb_grad_clip(table._in, table._out, table._numel, table._dtypes, len(table), _records(records, 0),
-                             records.numel(), max_norm, _norm_ptr(norm), _stream_handle(stream)), "tb_grad_clip")
+    _check(_lib.tb_grad_clip(table._in, table._out, table._numel, table._dtypes, len(table), _records(records),
+                             records.numel(), max_norm, _norm_ptr(norm), _stream_of(stream, records.get_device())),
+           "tb_grad_clip")
 
 
 def clip_grad_norm(grads, max_norm: float, records: Optional[torch.Tensor] = None,
@@ -1026,14 +1038,12 @@ def clip_grad_norm(grads, max_norm: float, records: Optional[torch.Tensor] = Non
     clipped in place), then the clip.  Returns the norm before it (a [1]
     float32 tensor)."""
     table = grads if isinstance(grads, GradTable) else GradTable(grads)
-    device = table.grads[0].device if len(table) else None
     if records is None:
-        records = _on_stream(lambda: new_grad_records(len(table), device), stream)
+        records = _on_stream(lambda: new_grad_records(len(table), table.device), stream)
     if norm is None:
         norm = _on_stream(lambda: torch.empty(1, dtype=torch.float32, device=records.device), stream)
-    handle = _stream_handle(stream)
-    tb_grad_stats(table, records, handle)
-    tb_grad_clip(table, records, max_norm, norm, handle)
+    tb_grad_stats(table, records, stream)
+    tb_grad_clip(table, records, max_norm, norm, stream)
     return norm
 
 

@@ -227,38 +227,19 @@ __device__ __forceinline__ void weights_at(const void* w, int dtype, int64_t i, 
     }
 }
 
-// One chunk's weights as a thread keeps them over its rows: fp32 lanes
-// (WIDE), or packed in the rows' type.
-template <int DT, int VEC, bool WIDE>
-struct Weights {
-    using L = Lanes<VEC>;
-    typename L::T f[L::N];
-    __device__ __forceinline__ void load(const void* w, int dtype, int64_t i, float dflt) {
-        float e[VEC];
-        weights_at<VEC, true>(w, dtype, i, dflt, e);
-        if constexpr (VEC == 1) {
-            f[0] = e[0];
-        } else {
+// One chunk's weights as fp32 lanes (16-byte aligned where VEC > 1).
+template <int VEC>
+__device__ __forceinline__ void weight_lanes(const void* w, int dtype, int64_t i, float dflt,
+                                             typename Lanes<VEC>::T (&f)[Lanes<VEC>::N]) {
+    float e[VEC];
+    weights_at<VEC, true>(w, dtype, i, dflt, e);
+    if constexpr (VEC == 1) {
+        f[0] = e[0];
+    } else {
 #pragma unroll
-            for (int q = 0; q < VEC / 2; ++q) f[q] = pair(e[2 * q], e[2 * q + 1]);
-        }
+        for (int q = 0; q < VEC / 2; ++q) f[q] = pair(e[2 * q], e[2 * q + 1]);
     }
-    __device__ __forceinline__ void get(typename L::T (&o)[L::N]) const {
-#pragma unroll
-        for (int q = 0; q < L::N; ++q) o[q] = f[q];
-    }
-};
-template <int DT, int VEC>
-struct Weights<DT, VEC, false> {
-    using L = Lanes<VEC>;
-    typename Word<VEC * elem_size(DT)>::T v;
-    __device__ __forceinline__ void load(const void* w, int dtype, int64_t i, float dflt) {
-        float e[VEC];
-        weights_at<VEC, true>(w, dtype, i, dflt, e);
-        v = pack<DT, VEC>(e);
-    }
-    __device__ __forceinline__ void get(typename L::T (&o)[L::N]) const { to_lanes<DT, VEC>(v, o); }
-};
+}
 
 __device__ __forceinline__ void store_weight(void* w, int dtype, int64_t i, float v) {
     if (dtype == F32) {
@@ -272,6 +253,62 @@ __device__ __forceinline__ void store_weight(void* w, int dtype, int64_t i, floa
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+
+// --- copies of whole rows into shared memory, completing on an mbarrier -------
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_init_fence() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t phase) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(phase)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ uint64_t timer_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+// A wait for copies gives up after this long (nanoseconds).
+constexpr uint64_t BAR_WAIT_NS = 1000000000ull;
+// Waits for the phase of `bar`; false, with DEV_WAIT_TIMEOUT recorded, if it
+// does not complete in time.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t phase, uint32_t* status) {
+    if (bar_try(bar, phase)) return true;
+    const uint64_t t0 = timer_ns();
+    while (!bar_try(bar, phase)) {
+        if (timer_ns() - t0 > BAR_WAIT_NS) {
+            if (status != nullptr) atomicCAS(status, (uint32_t)DEV_OK, (uint32_t)DEV_WAIT_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+// `bytes` (a multiple of 16) from global memory, both addresses 16-byte
+// aligned; counts towards the phase of `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+template <typename W>
+__device__ __forceinline__ W smem_load(uint32_t at) {
+    static_assert(sizeof(W) == 16, "16-byte words");
+    W v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
     return v;
 }
 

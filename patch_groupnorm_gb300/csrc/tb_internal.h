@@ -484,8 +484,9 @@ struct LnBwdParams {
     float* workspace;       // [parts][2][cols], or null: no weight gradients
     int64_t rows, cols;
     int64_t dy_ld, x_ld, dt_ld, dx_ld;
-    uint32_t* status;       // bounds-checked build: device status word (else null)
+    uint32_t* status;       // device status word (a wait that runs out is recorded there)
     int32_t wdtype;
+    int32_t stages;         // rows in flight per row group (set at the launch)
 };
 
 struct LnWgradParams {

@@ -22,7 +22,7 @@ namespace {
 #endif
 __host__ __device__ constexpr int ln_fwd_ctas(int tpr) { return tpr >= 1024 ? 1 : TB_LN_FWD_THREADS / ln_block(tpr); }
 
-template <int DT, int VEC, int TPR, int CPT, bool RES, bool WIDE>
+template <int DT, int VEC, int TPR, int CPT, bool RES>
 __global__ void __launch_bounds__(ln_block(TPR), ln_fwd_ctas(TPR)) ln_fwd_kernel(const __grid_constant__ LnFwdParams p) {
     using W = typename Word<VEC * elem_size(DT)>::T;
     using L = Lanes<VEC>;
@@ -53,14 +53,14 @@ __global__ void __launch_bounds__(ln_block(TPR), ln_fwd_ctas(TPR)) ln_fwd_kernel
         fetch(p.x, row, p.x_ld, nx);
         if constexpr (RES) fetch(p.residual, row, p.r_ld, nr);
     }
-    Weights<DT, VEC, WIDE> g[KEEP ? CPT : 1], b[KEEP ? CPT : 1];
+    T g[KEEP ? CPT : 1][L::N], b[KEEP ? CPT : 1][L::N];
     if constexpr (KEEP) {
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
             const int c = t + k * TPR;
             if (c < nchunk) {
-                g[k].load(p.gamma, p.wdtype, (int64_t)c * VEC, 1.f);
-                b[k].load(p.beta, p.wdtype, (int64_t)c * VEC, 0.f);
+                weight_lanes<VEC>(p.gamma, p.wdtype, (int64_t)c * VEC, 1.f, g[k]);
+                weight_lanes<VEC>(p.beta, p.wdtype, (int64_t)c * VEC, 0.f, b[k]);
             }
         }
     }
@@ -119,20 +119,18 @@ __global__ void __launch_bounds__(ln_block(TPR), ln_fwd_ctas(TPR)) ln_fwd_kernel
         for (int k = 0; k < CPT; ++k) {
             const int c = t + k * TPR;
             if (c < nchunk) {
-                T f[L::N], gv[L::N], bv[L::N];
+                T f[L::N];
                 to_lanes<DT, VEC>(h[k], f);
                 if constexpr (KEEP) {
-                    g[k].get(gv);
-                    b[k].get(bv);
-                } else {
-                    Weights<DT, VEC, true> w;
-                    w.load(p.gamma, p.wdtype, (int64_t)c * VEC, 1.f);
-                    w.get(gv);
-                    w.load(p.beta, p.wdtype, (int64_t)c * VEC, 0.f);
-                    w.get(bv);
-                }
 #pragma unroll
-                for (int q = 0; q < L::N; ++q) f[q] = vfma(vmul(vsub(f[q], mean2), rstd2), gv[q], bv[q]);
+                    for (int q = 0; q < L::N; ++q) f[q] = vfma(vsub(f[q], mean2), vmul(rstd2, g[k][q]), b[k][q]);
+                } else {
+                    T gv[L::N], bv[L::N];
+                    weight_lanes<VEC>(p.gamma, p.wdtype, (int64_t)c * VEC, 1.f, gv);
+                    weight_lanes<VEC>(p.beta, p.wdtype, (int64_t)c * VEC, 0.f, bv);
+#pragma unroll
+                    for (int q = 0; q < L::N; ++q) f[q] = vfma(vsub(f[q], mean2), vmul(rstd2, gv[q]), bv[q]);
+                }
                 W* const dst = reinterpret_cast<W*>(at) + c;
                 if (in_bounds(dst, sizeof(W), at, row_bytes, p.status)) *dst = from_lanes<DT, VEC>(f);
             }
@@ -206,22 +204,12 @@ __global__ void __launch_bounds__(LONG_BLOCK) ln_fwd_long_kernel(const __grid_co
 // dispatch: a row's chunk count picks the threads and chunks per thread
 // ---------------------------------------------------------------------------
 
-// WIDE: fp32 weights beside 16-bit rows (kept as fp32; otherwise packed).
-template <int DT, int VEC, int TPR, int CPT, bool RES>
-void (*fwd_fn(bool wide))(const LnFwdParams) {
-    if constexpr (DT != F32 && VEC > 1) {
-        if (!wide) return ln_fwd_kernel<DT, VEC, TPR, CPT, RES, false>;
-    }
-    return ln_fwd_kernel<DT, VEC, TPR, CPT, RES, true>;
-}
-
 template <int DT, int VEC, int TPR, int CPT>
 cudaError_t fwd_launch(const LnFwdParams& p, int sms, cudaStream_t s) {
     constexpr int rpc = ln_block(TPR) / TPR;
     const int64_t want = (p.rows + rpc - 1) / rpc;
     const unsigned grid = (unsigned)(want < (int64_t)sms * ln_fwd_ctas(TPR) ? want : (int64_t)sms * ln_fwd_ctas(TPR));
-    const bool wide = p.wdtype == F32;
-    return launch_pdl(p.residual ? fwd_fn<DT, VEC, TPR, CPT, true>(wide) : fwd_fn<DT, VEC, TPR, CPT, false>(wide), p,
+    return launch_pdl(p.residual ? ln_fwd_kernel<DT, VEC, TPR, CPT, true> : ln_fwd_kernel<DT, VEC, TPR, CPT, false>, p,
                       dim3(grid), ln_block(TPR), 0, s);
 }
 

@@ -258,7 +258,7 @@ TB_API tb_status tb_layer_norm_backward(const void* dy, int64_t dy_ld, const voi
         p.x_ld = x_ld;
         p.dt_ld = dtotal_ld;
         p.dx_ld = dx_ld;
-        p.status = tb::checked_build_status();
+        p.status = tb::device_status_word();
         p.wdtype = (int32_t)wdtype;
         TB_TRY(launched(tb::launch_ln_bwd(p, (int)dtype, vector, sms, &parts, reinterpret_cast<cudaStream_t>(stream))));
     }

@@ -33,9 +33,10 @@ UNITS = {
     "tb_layernorm.cu": [],
     "tb_layernorm_bwd.cu": [],
     "tb_gradclip.cu": [],
+    "tb_gngrad.cu": [],
     "tb_train.cpp": [],
 }
-HEADERS = ["tb_internal.h", "tb_elem.cuh", "tb_layernorm.cuh"]
+HEADERS = ["tb_internal.h", "tb_elem.cuh", "tb_layernorm.cuh", "tb_groupnorm.cuh"]
 
 
 def _nvcc() -> str:

@@ -1,0 +1,703 @@
+// tb_gngrad.cu -- the backward pass of PatchGroupNorm (+ SiLU).
+//
+// With the pooled mean and rstd of the forward pass's records,
+// xhat = (x - mean) * rstd, z = xhat * gamma + beta and s = 1 / (1 + e^-z):
+//     dz = silu ? dy * s * (1 + z * (1 - s)) : dy
+//     B(n, c) = sum dz,  A(n, c) = sum dz * xhat     (over the channel's elements)
+//     dgamma(c) = sum_n A,  dbeta(c) = sum_n B
+//     c1 = sum over the group's channels of gamma * B / count,  c2 the same of A
+//     dx = rnd(rstd * (gamma * dz - c1 - xhat * c2))
+// Sums are fp32, in an order fixed by the sizes and the GPU.
+//
+// dx needs sums over the whole group, so x and dy are read twice: once for
+// the records (B, A) and once for dx.  gn_grad_kernel does either pass, or
+// both in one launch that reads them from memory once where a group and its
+// successors fit in L2: its tasks are taken in order from a counter -- the
+// records of the first `lag` units (sample, group), then alternately a task of
+// the records of unit i + lag and one of the dx of unit i -- so a unit's
+// second reading follows its first by about 15 MB and finds it in L2.  A dx
+// task waits for the arrival counter of its unit's records.  Tasks are handed
+// out in order and only to running CTAs, so a task that another waits for has
+// always been started, whatever else occupies the GPU.
+//
+// One CTA per SM: 16 warps compute, a 17th takes the tasks and copies their
+// rows into a ring of three stages in shared memory (64 KB each: x and dy),
+// with the unit's and the rows' constants.  Bulk copies move whole 16-byte
+// words; the elements before the first and after the last boundary are copied
+// one by one, so rows of any length and offset take this path.
+#include "tb_elem.cuh"
+#include "tb_groupnorm.cuh"
+
+namespace tb {
+namespace {
+
+constexpr int GG_WARPS = 16;
+constexpr int GG_THREADS = GG_WARPS * 32;
+constexpr int GG_BLOCK = GG_THREADS + 32;
+constexpr int GG_STAGES = 3;
+constexpr int GG_TENSOR = GRAD_STAGE_BYTES + 128;  // room for a first, partial word
+constexpr int GG_SMEM = GG_STAGES * 2 * GG_TENSOR;
+static_assert(GG_SMEM <= 216 * 1024, "ring too large");
+
+enum TaskKind : int32_t { TASK_STATS = 0, TASK_APPLY = 1, TASK_WEIGHTS = 2, TASK_END = 3 };
+
+// What the computing warps need of the stage's rows.
+struct Stage {
+    int32_t kind;
+    int32_t rows;        // channel rows in the stage
+    int32_t row_elems;   // elements of each (of the part of one) in the stage
+    int32_t shift;       // elements before the first in the first word
+    int32_t last;        // TASK_STATS: the part ends with this stage
+    int32_t slot;        // TASK_STATS: the part's record slot
+    int64_t record;      // TASK_STATS: row index p * N * C + n * C + c of the first row; TASK_WEIGHTS: channel
+    int64_t unit;        // TASK_STATS: the unit, whose arrival counter is raised
+    char* out;           // TASK_APPLY: address of the first element
+    float mean, rstd;
+    float u, v;          // TASK_APPLY: dx = dz * rstd * gamma + (x - mean) * u + v
+    float2 row[GRAD_MAX_ROWS + 1];  // (rstd * gamma, beta) of each row
+};
+
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Arrival counter of a unit, and the task counter (GRAD_BOTH).
+__device__ __forceinline__ uint32_t* unit_counter(const GnGradParams& p, int64_t unit) {
+    const int64_t n = unit / p.G, g = unit - n * p.G;
+    return reinterpret_cast<uint32_t*>(p.grad_partials + (n * p.C + g * (p.C / p.G)) * TB_GN_PARTS + TB_GN_PARTS - 1);
+}
+__device__ __forceinline__ uint32_t* task_counter(const GnGradParams& p) {
+    return reinterpret_cast<uint32_t*>(p.grad_partials + TB_GN_PARTS - 2);
+}
+
+// Zeroes the counters of a GRAD_BOTH launch.
+__global__ void __launch_bounds__(256) gn_grad_zero_kernel(const __grid_constant__ GnGradParams p) {
+    pdl_trigger_dependents();
+    grid_wait();
+    const int64_t unit = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (unit < p.N * p.G) *unit_counter(p, unit) = 0u;
+    if (unit == 0) *task_counter(p) = 0u;
+}
+
+// dz of one pair of elements (see the top of this file).  The two
+// reciprocals share one approximate rcp: 1/a = b * (1 / ab).  e^-z is held
+// below 2^60 to keep ab finite: there s is below 1e-18, and dz is too small
+// beside dy (at most 1e-16 of it) for any sum or rounding to see.
+template <bool SILU>
+__device__ __forceinline__ f32x2 dz_pair(f32x2 u, f32x2 dy, f32x2 za, f32x2 zb) {
+    if constexpr (SILU) {
+        const f32x2 one = pair(1.f, 1.f);
+        const f32x2 z = vfma(u, za, zb);
+        float tl, th, al, ah;
+        halves(vmul(z, pair(-1.4426950408889634f, -1.4426950408889634f)), tl, th);
+        halves(vadd(pair(ex2_ftz(fminf(tl, 60.f)), ex2_ftz(fminf(th, 60.f))), one), al, ah);
+        const float r = rcp_ftz(al * ah);
+        const f32x2 s = vmul(pair(ah, al), pair(r, r));
+        return vmul(dy, vmul(s, vfma(z, vsub(one, s), one)));
+    } else {
+        return dy;
+    }
+}
+
+// --- the 17th warp --------------------------------------------------------------
+
+struct Ring {
+    Stage* stage;
+    uint32_t full, empty, sums, data;  // shared addresses: mbarriers, first stage's rows
+    volatile int* dead;          // a wait ran out: everyone leaves
+    int s = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == GG_STAGES) {
+            s = 0;
+            parity ^= 1u;
+        }
+    }
+};
+
+// A unit's constants as the copying warp last computed them.
+struct UnitCache {
+    int64_t unit = -1;
+    float mean = 0.f, rstd = 0.f, u = 0.f, v = 0.f;
+};
+
+// Waits until the counter of `unit` reaches the unit's tasks.
+__device__ __forceinline__ bool wait_unit(const GnGradParams& p, int64_t unit) {
+    const uint32_t* const at = unit_counter(p, unit);
+    const uint32_t want = (uint32_t)p.unit_tasks;
+    if (ld_acquire(at) >= want) return true;
+    const uint64_t t0 = timer_ns();
+    while (ld_acquire(at) < want) {
+        if (timer_ns() - t0 > BAR_WAIT_NS) {
+            if (p.status != nullptr) atomicCAS(p.status, (uint32_t)DEV_OK, (uint32_t)DEV_WAIT_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+// c1 and c2 times the group's count, by one warp.
+__device__ __forceinline__ float2 group_sums(const GnGradParams& p, int dtype, int64_t n, int64_t g) {
+    const int K = (int)(p.C / p.G);
+    const int lane = threadIdx.x & 31;
+    const int sets = p.mode == GRAD_BOTH ? p.P : p.R;
+    float B = 0.f, A = 0.f;
+    for (int r = 0; r < sets; ++r) {
+        const int per = p.mode == GRAD_BOTH ? p.parts[r] : TB_GN_PARTS;
+        const float2* const at = p.grad_partials + ((r * p.N + n) * p.C + g * K) * TB_GN_PARTS;
+        for (int q = lane; q < K * per; q += 32) {
+            const int c = q / per;
+            const float2 v = __ldcg(at + (int64_t)c * TB_GN_PARTS + (q - c * per));
+            const float w = weight_at(p.gamma, dtype, g * K + c, 1.f);
+            B = fmaf(v.x, w, B);
+            A = fmaf(v.y, w, A);
+        }
+    }
+    return make_float2(warp_sum(B), warp_sum(A));
+}
+
+// The unit's constants in `c`; false if its records do not arrive.
+__device__ __forceinline__ bool unit_constants(const GnGradParams& p, int dtype, int kind, int64_t unit, UnitCache& c) {
+    if (c.unit == unit) return true;
+    const int64_t n = unit / p.G, g = unit - n * p.G;
+    float mean, rstd, count;
+    pooled_stats(p, n, g, mean, rstd, count);
+    c.mean = __shfl_sync(0xffffffffu, mean, 0);
+    c.rstd = __shfl_sync(0xffffffffu, rstd, 0);
+    count = __shfl_sync(0xffffffffu, count, 0);
+    if (kind == TASK_APPLY) {
+        if (p.mode == GRAD_BOTH) {
+            const bool ok = wait_unit(p, unit);
+            if (__any_sync(0xffffffffu, !ok)) return false;
+        }
+        const float2 sums = group_sums(p, dtype, n, g);
+        c.v = -sums.x / count * c.rstd;
+        c.u = -sums.y / count * c.rstd * c.rstd;
+    }
+    c.unit = unit;
+    return true;
+}
+
+// Copies elements [first, first + count) of `base` into the stage's buffer at
+// `dst`, keeping their offset from 16-byte boundaries; `bytes` is the size of
+// the bulk copy, and lanes 0 .. 15 copy the elements on either side of it.
+template <int DT>
+__device__ __forceinline__ void copy_rows(const void* base, int64_t first, int64_t count, uint32_t dst, uint32_t bar,
+                                          bool leader) {
+    constexpr int ES = elem_size(DT);
+    using E = typename Word<ES>::T;
+    const char* const from = reinterpret_cast<const char*>(base) + first * ES;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(from);
+    const int shift = (int)(a & 15u);
+    const uintptr_t lo = (a + 15u) & ~(uintptr_t)15u, hi = (a + count * ES) & ~(uintptr_t)15u;
+    if (leader && hi > lo)
+        bulk_load(dst + (uint32_t)(lo - (a - shift)), reinterpret_cast<const void*>(lo), (uint32_t)(hi - lo), bar);
+    // lane k < 8: element k of the first word; lane 8 + k: element k of the last
+    const int lane = threadIdx.x & 31, k = lane & 7;
+    const uintptr_t word = lane < 8 ? a - shift : hi;
+    const uintptr_t at = word + k * ES;
+    const bool mine = lane < 16 && k * ES < 16 && at >= a && at < a + count * ES &&
+                      (lane < 8 ? (shift != 0 && at < lo) : (hi >= lo));
+    if (mine) {
+        const E v = *reinterpret_cast<const E*>(at);
+        const uint32_t to = dst + (uint32_t)(at - (a - shift));
+        if constexpr (ES == 4) asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(v) : "memory");
+        else asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(v) : "memory");
+    }
+}
+// Bytes copy_rows moves in bulk.
+__device__ __forceinline__ uint32_t bulk_bytes(const void* base, int64_t first, int64_t count, int es) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(base) + first * es;
+    const uintptr_t lo = (a + 15u) & ~(uintptr_t)15u, hi = (a + count * es) & ~(uintptr_t)15u;
+    return hi > lo ? (uint32_t)(hi - lo) : 0u;
+}
+
+template <int DT>
+__device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
+    constexpr int ES = elem_size(DT);
+    constexpr int VEC = 16 / ES;
+    const int lane = threadIdx.x & 31;
+    const int64_t units = p.N * p.G;
+    const int64_t T = p.unit_tasks;
+    const int K = (int)(p.C / p.G);
+    const int64_t lag = p.lag;
+    const bool both = p.mode == GRAD_BOTH;
+    const int64_t body = (both ? 2 : 1) * units * T, total = body + p.wtasks;
+    UnitCache cache[2];  // of TASK_STATS and TASK_APPLY
+    bool ok = true;
+    // GRAD_BOTH: tasks in order from the counter, the next one asked for while
+    // this one is copied; otherwise no task waits for another
+    uint32_t next = blockIdx.x;
+    auto ask = [&]() {
+        if (!both) next += gridDim.x;
+        else if (lane == 0) next = atomicAdd(task_counter(p), 1u);
+    };
+    if (both) ask();
+    auto claim = [&]() -> bool {  // the ring's next stage, once the computing warps are done with it
+        ok = ok && bar_wait(ring.empty + ring.s * 8u, ring.parity ^ 1u, p.status);
+        if (__any_sync(0xffffffffu, !ok) || *ring.dead) ok = false;
+        return ok;
+    };
+    while (true) {
+        const int64_t task = __shfl_sync(0xffffffffu, next, 0);
+        if (task >= total) break;
+        ask();
+        int kind;
+        int64_t unit = 0, item = 0;
+        if (task >= body) {
+            kind = TASK_WEIGHTS;
+            const int64_t c0 = (task - body) * GRAD_CHANNELS;
+            const int64_t c1 = min(p.C, c0 + GRAD_CHANNELS);
+            if (both) {
+                for (int64_t n = 0; n < p.N; ++n)
+                    for (int64_t g = c0 / K; g <= (c1 - 1) / K; ++g) ok = ok && wait_unit(p, n * p.G + g);
+                if (__any_sync(0xffffffffu, !ok)) break;
+            }
+            if (!claim()) break;
+            Stage& d = ring.stage[ring.s];
+            if (lane == 0) {
+                d.kind = kind;
+                d.record = c0;
+                bar_arrive(ring.full + ring.s * 8u);
+                bar_arrive(ring.full + ring.s * 8u);
+            }
+            ring.next();
+            continue;
+        }
+        if (!both) {
+            kind = p.mode == GRAD_STATS ? TASK_STATS : TASK_APPLY;
+            unit = task / T;
+            item = task - unit * T;
+        } else if (task < lag * T) {
+            kind = TASK_STATS;
+            unit = task / T;
+            item = task - unit * T;
+        } else {
+            const int64_t q = task - lag * T, pairs = 2 * (units - lag) * T;
+            if (q < pairs) {
+                const int64_t block = q / (2 * T), r = q - block * 2 * T;
+                kind = (r & 1) ? TASK_APPLY : TASK_STATS;
+                unit = (r & 1) ? block : block + lag;
+                item = r >> 1;
+            } else {
+                kind = TASK_APPLY;
+                unit = units - lag + (q - pairs) / T;
+                item = (q - pairs) % T;
+            }
+        }
+        // a unit's dx runs backwards: what was read last is the likeliest to be in L2
+        if (kind == TASK_APPLY) item = T - 1 - item;
+        int pp = 0;
+        while (p.task_start[pp + 1] <= item) ++pp;
+        item -= p.task_start[pp];
+        const int64_t n = unit / p.G, g = unit - n * p.G;
+        const int64_t S = p.spatial[pp];
+        int rows, part = 0, c_first;  // c_first: first row, within the group
+        int64_t e0, e1;               // element range within the row
+        if (p.parts[pp] > 1) {
+            c_first = (int)item / p.parts[pp];
+            part = (int)item - c_first * p.parts[pp];
+            rows = 1;
+            const int64_t words = S / VEC;
+            e0 = words * part / p.parts[pp] * VEC;
+            e1 = part + 1 == p.parts[pp] ? S : words * (part + 1) / p.parts[pp] * VEC;
+        } else {
+            c_first = (int)item * p.rows[pp];
+            rows = min(p.rows[pp], K - c_first);
+            e0 = 0;
+            e1 = S;
+        }
+        const int64_t row = n * p.C + g * K + c_first;
+        constexpr int64_t MOST = GRAD_STAGE_BYTES / ES;
+        // (one stage for whole rows; the stages of a part in turn)
+        // (an empty patch's rows still get their records)
+        for (int64_t at = e0; (at < e1 || at == e0) && ok; at += MOST) {
+            const int64_t len = min(MOST, e1 - at);
+            if (!claim()) break;
+            Stage& d = ring.stage[ring.s];
+            const uint32_t bar = ring.full + ring.s * 8u, dst = ring.data + ring.s * 2 * GG_TENSOR;
+            const int64_t first = row * S + at, count = rows * len;
+            if (lane == 0)
+                bar_expect(bar, bulk_bytes(p.patches[pp], first, count, ES) + bulk_bytes(p.grads[pp], first, count, ES));
+            copy_rows<DT>(p.patches[pp], first, count, dst, bar, lane == 0);
+            copy_rows<DT>(p.grads[pp], first, count, dst + GG_TENSOR, bar, lane == 0);
+            UnitCache& c = cache[kind];
+            ok = unit_constants(p, DT, kind, unit, c);
+            if (lane < rows) {
+                const int64_t ch = g * K + c_first + lane;
+                d.row[lane] = make_float2(c.rstd * weight_at(p.gamma, DT, ch, 1.f), weight_at(p.beta, DT, ch, 0.f));
+            }
+            if (lane == 0) {
+                d.kind = kind;
+                d.rows = rows;
+                d.row_elems = (int32_t)len;
+                d.shift = (int32_t)((reinterpret_cast<uintptr_t>(p.patches[pp]) + first * ES) & 15u) / ES;
+                d.last = at + len >= e1;
+                d.slot = part;
+                d.record = pp * p.N * p.C + row;
+                d.unit = unit;
+                d.out = reinterpret_cast<char*>(p.outs[pp]) + first * ES;
+                d.mean = c.mean;
+                d.rstd = c.rstd;
+                d.u = c.u;
+                d.v = c.v;
+            }
+            if (!ok && lane == 0) *ring.dead = 1;
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar);
+            ring.next();
+        }
+        if (!ok) break;
+    }
+    if (!ok) {
+        // a wait ran out: everyone leaves, once the copies in flight have
+        // landed (or their own waits have run out)
+        if (lane == 0) *ring.dead = 1;
+        for (int k = 0; k < GG_STAGES; ++k)
+            bar_wait(ring.full + k * 8u, k < ring.s ? ring.parity : ring.parity ^ 1u, p.status);
+        return;
+    }
+    const bool idle = bar_wait(ring.empty + ring.s * 8u, ring.parity ^ 1u, p.status);
+    if (idle && lane == 0) {
+        ring.stage[ring.s].kind = TASK_END;
+        bar_arrive(ring.full + ring.s * 8u);
+        bar_arrive(ring.full + ring.s * 8u);
+    }
+}
+
+// --- the computing warps ----------------------------------------------------------
+
+template <int DT, bool SILU>
+__device__ __forceinline__ void compute_loop(const GnGradParams& p, Ring ring, float2 (*slots)[2 * GG_WARPS]) {
+    constexpr int ES = elem_size(DT);
+    constexpr int VEC = 16 / ES;
+    constexpr int NP = VEC / 2;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    f32x2 B = 0ull, A = 0ull;  // 0ull: a pair of zeros
+    uint32_t sums_parity = 0;
+    while (true) {
+        const bool here = bar_wait(ring.full + ring.s * 8u, ring.parity, p.status);
+        if (!here && lane == 0) *ring.dead = 1;
+        if (__any_sync(0xffffffffu, !here) || *ring.dead) return;
+        const Stage& d = ring.stage[ring.s];
+        const int kind = d.kind;
+        const uint32_t empty = ring.empty + ring.s * 8u;
+        if (kind == TASK_END) return;
+        if (kind == TASK_WEIGHTS) {
+            // a warp per channel adds up its records of all samples and sets
+            const int64_t c = d.record + warp;
+            if (c < p.C) {
+                const bool both = p.mode == GRAD_BOTH;
+                const int64_t most = (int64_t)(both ? p.P : p.R) * p.N * TB_GN_PARTS;
+                float b = 0.f, a = 0.f;
+                for (int64_t q = lane; q < most; q += 32) {
+                    const int64_t set = q / TB_GN_PARTS;  // set * N + n
+                    const int slot = (int)(q - set * TB_GN_PARTS);
+                    if (both && slot >= p.parts[set / p.N]) continue;
+                    const float2 v = __ldcg(p.grad_partials + (set * p.C + c) * TB_GN_PARTS + slot);
+                    b += v.x;
+                    a += v.y;
+                }
+                b = warp_sum(b);
+                a = warp_sum(a);
+                if (lane == 0) {
+                    if (p.dgamma != nullptr) store_weight(p.dgamma, DT, c, a);
+                    if (p.dbeta != nullptr) store_weight(p.dbeta, DT, c, b);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(empty);
+            ring.next();
+            continue;
+        }
+        const int rows = d.rows, len = d.row_elems, shift = d.shift;
+        // `groups` row groups of `wpr` warps each
+        const int groups = rows >= GG_WARPS ? GG_WARPS : 1 << (31 - __clz(rows));
+        const int wpr = GG_WARPS / groups;
+        const int wg = warp / wpr, wi = warp - wg * wpr;
+        const uint32_t xs = ring.data + ring.s * 2 * GG_TENSOR, ds = xs + GG_TENSOR;
+        const float mean = d.mean;
+        const f32x2 mean2 = pair(mean, mean);
+        const f32x2 u2 = pair(d.u, d.u), v2 = pair(d.v, d.v);
+        for (int r = wg; r < rows; r += groups) {
+            const float2 k = d.row[r];
+            const f32x2 za = pair(k.x, k.x), zb = pair(k.y, k.y);
+            const int lo = shift + r * len, hi = lo + len;  // the row's elements in the buffer
+            const int w1 = (hi + VEC - 1) / VEC;
+            // word w of the row: x and dy as lanes, (mean, 0) outside [lo, hi)
+            auto word = [&](int w, f32x2 (&x)[NP], f32x2 (&dy)[NP]) {
+                to_lanes<DT, VEC>(smem_load<uint4>(xs + w * 16u), x);
+                to_lanes<DT, VEC>(smem_load<uint4>(ds + w * 16u), dy);
+                if (w * VEC < lo || (w + 1) * VEC > hi) {
+#pragma unroll
+                    for (int q = 0; q < NP; ++q) {
+                        float a, b, c, e;
+                        halves(x[q], a, b);
+                        halves(dy[q], c, e);
+                        const int i = w * VEC + 2 * q;
+                        if (i < lo || i >= hi) a = mean, c = 0.f;
+                        if (i + 1 < lo || i + 1 >= hi) b = mean, e = 0.f;
+                        x[q] = pair(a, b);
+                        dy[q] = pair(c, e);
+                    }
+                }
+            };
+            if (kind == TASK_STATS) {
+                for (int w = lo / VEC + wi * 32 + lane; w < w1; w += wpr * 32) {
+                    f32x2 x[NP], dy[NP];
+                    word(w, x, dy);
+#pragma unroll
+                    for (int q = 0; q < NP; ++q) {
+                        const f32x2 u = vsub(x[q], mean2);
+                        const f32x2 dz = dz_pair<SILU>(u, dy[q], za, zb);
+                        B = vadd(B, dz);
+                        A = vfma(dz, u, A);
+                    }
+                }
+                if (d.last) {
+                    const float b = warp_sum(vsum(B)), a = warp_sum(vsum(A)) * d.rstd;
+                    if (lane == 0) slots[ring.s][r * wpr + wi] = make_float2(b, a);
+                    B = A = 0ull;
+                }
+            } else {
+                for (int w = lo / VEC + wi * 32 + lane; w < w1; w += wpr * 32) {
+                    f32x2 x[NP], dy[NP];
+                    word(w, x, dy);
+#pragma unroll
+                    for (int q = 0; q < NP; ++q) {
+                        const f32x2 u = vsub(x[q], mean2);
+                        x[q] = vfma(dz_pair<SILU>(u, dy[q], za, zb), za, vfma(u, u2, v2));
+                    }
+                    const uint4 o = from_lanes<DT, VEC>(x);
+                    char* const at = d.out + ((int64_t)w * VEC - shift) * ES;
+                    if (w * VEC >= lo && (w + 1) * VEC <= hi) {
+                        __stcs(reinterpret_cast<uint4*>(at), o);
+                    } else {
+                        using E = typename Word<ES>::T;
+                        const uint32_t bits[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                        for (int q = 0; q < VEC; ++q) {
+                            const int i = w * VEC + q;
+                            if (i < lo || i >= hi) continue;
+                            if constexpr (ES == 4) reinterpret_cast<E*>(at)[q] = bits[q];
+                            else reinterpret_cast<E*>(at)[q] = (E)(bits[q >> 1] >> (16 * (q & 1)));
+                        }
+                    }
+                }
+            }
+        }
+        if (kind == TASK_STATS && d.last) {
+            // the row groups' sums meet; warp 0 writes the records
+            __syncwarp();
+            if (lane == 0) bar_arrive(ring.sums);
+            if (warp == 0) {
+                const bool met = bar_wait(ring.sums, sums_parity, p.status);
+                sums_parity ^= 1u;
+                if (!met && lane == 0) *ring.dead = 1;
+                if (__any_sync(0xffffffffu, !met)) return;
+                for (int r = lane; r < rows; r += 32) {
+                    float2 t = slots[ring.s][r * wpr];
+                    for (int w = 1; w < wpr; ++w) {
+                        const float2 v = slots[ring.s][r * wpr + w];
+                        t.x += v.x;
+                        t.y += v.y;
+                    }
+                    float2* const rec = p.grad_partials + (d.record + r) * TB_GN_PARTS;
+                    rec[d.slot] = t;
+                    if (p.mode == GRAD_STATS && d.slot == 0) {
+                        // the slots of parts that do not exist
+                        const int parts = p.parts[d.record / (p.N * p.C)];
+                        for (int q = parts; q < TB_GN_PARTS; ++q) rec[q] = make_float2(0.f, 0.f);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0 && p.mode == GRAD_BOTH) {
+                    __threadfence();
+                    atomicAdd(unit_counter(p, d.unit), 1u);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(empty);
+        ring.next();
+    }
+}
+
+template <int DT, bool SILU>
+__global__ void __launch_bounds__(GG_BLOCK, 1) gn_grad_kernel(const __grid_constant__ GnGradParams p) {
+    extern __shared__ __align__(128) unsigned char s_data[];
+    __shared__ Stage s_stage[GG_STAGES];
+    __shared__ float2 s_slots[GG_STAGES][2 * GG_WARPS];
+    __shared__ __align__(8) unsigned long long s_bar[2 * GG_STAGES + 1];
+    __shared__ int s_dead;
+    Ring ring;
+    ring.stage = s_stage;
+    ring.full = smem_addr(s_bar);
+    ring.empty = ring.full + GG_STAGES * 8u;
+    ring.sums = ring.empty + GG_STAGES * 8u;
+    ring.data = smem_addr(s_data);
+    ring.dead = &s_dead;
+    if (threadIdx.x == 0) {
+        s_dead = 0;
+        for (int k = 0; k < GG_STAGES; ++k) {
+            bar_init(ring.full + k * 8u, 2);        // the copies' bytes, and the constants
+            bar_init(ring.empty + k * 8u, GG_WARPS);
+        }
+        bar_init(ring.sums, GG_WARPS);  // the warps' sums of one part
+        bar_init_fence();
+    }
+    __syncthreads();
+    grid_wait();
+    if (threadIdx.x >= GG_THREADS) copy_loop<DT>(p, ring);
+    else compute_loop<DT, SILU>(p, ring, s_slots);
+    __syncthreads();  // (no warp's memory goes before the copies have landed)
+}
+
+// --- element kernels: patches, gradients and outputs at different offsets from
+// 16-byte boundaries -------------------------------------------------------------
+
+constexpr int EL_BLOCK = 256;
+constexpr int EL_SEG = 4096;  // elements per CTA of the second pass
+
+template <int DT>
+__device__ __forceinline__ float elem_at(const void* base, int64_t i) {
+    return elem_to_f<DT>(reinterpret_cast<const typename Word<elem_size(DT)>::T*>(base)[i]);
+}
+
+template <bool SILU>
+__device__ __forceinline__ float dz_one(float u, float dy, float2 k) {
+    float lo, hi;
+    halves(dz_pair<SILU>(pair(u, u), pair(dy, dy), pair(k.x, k.x), pair(k.y, k.y)), lo, hi);
+    return lo;
+}
+
+// One CTA per (patch, sample, channel) row: record 0, the others zero.
+template <int DT, bool SILU>
+__global__ void __launch_bounds__(EL_BLOCK) gn_grad_stats_elem_kernel(const __grid_constant__ GnGradParams p) {
+    __shared__ float2 s_warp[EL_BLOCK / 32];
+    const int64_t row = blockIdx.x, NC = p.N * p.C;
+    const int pp = (int)(row / NC);
+    const int64_t nc = row - pp * NC, n = nc / p.C, c = nc - n * p.C, g = c / (p.C / p.G);
+    grid_wait();
+    float mean, rstd, count;
+    pooled_stats(p, n, g, mean, rstd, count);
+    mean = __shfl_sync(0xffffffffu, mean, 0);
+    rstd = __shfl_sync(0xffffffffu, rstd, 0);
+    const float2 k = make_float2(rstd * weight_at(p.gamma, DT, c, 1.f), weight_at(p.beta, DT, c, 0.f));
+    const int64_t S = p.spatial[pp], base = nc * S;
+    float B = 0.f, A = 0.f;
+    for (int64_t i = threadIdx.x; i < S; i += EL_BLOCK) {
+        const float u = elem_at<DT>(p.patches[pp], base + i) - mean;
+        const float dz = dz_one<SILU>(u, elem_at<DT>(p.grads[pp], base + i), k);
+        B += dz;
+        A = fmaf(dz, u, A);
+    }
+    B = warp_sum(B);
+    A = warp_sum(A) * rstd;
+    if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = make_float2(B, A);
+    __syncthreads();
+    if (threadIdx.x < TB_GN_PARTS) {
+        float2 t = make_float2(0.f, 0.f);
+        if (threadIdx.x == 0) {
+            for (int w = 0; w < EL_BLOCK / 32; ++w) {
+                t.x += s_warp[w].x;
+                t.y += s_warp[w].y;
+            }
+        }
+        p.grad_partials[row * TB_GN_PARTS + threadIdx.x] = t;
+    }
+}
+
+// grid (row segments of the longest patch, rows + weight-gradient CTAs).
+template <int DT, bool SILU>
+__global__ void __launch_bounds__(EL_BLOCK) gn_grad_apply_elem_kernel(const __grid_constant__ GnGradParams p) {
+    const int64_t NC = p.N * p.C, rows = (int64_t)p.P * NC;
+    grid_wait();
+    for (int64_t row = blockIdx.x; row < rows + p.wtasks; row += gridDim.x) {
+        if (row >= rows) {
+            const int64_t c0 = (row - rows) * GRAD_CHANNELS;
+            for (int64_t c = c0 + (threadIdx.x >> 5); c < min(p.C, c0 + GRAD_CHANNELS); c += EL_BLOCK / 32) {
+                if (blockIdx.y > 0) break;
+                float b = 0.f, a = 0.f;
+                for (int64_t q = threadIdx.x & 31; q < (int64_t)p.R * p.N * TB_GN_PARTS; q += 32) {
+                    const float2 v = p.grad_partials[(q / TB_GN_PARTS * p.C + c) * TB_GN_PARTS + q % TB_GN_PARTS];
+                    b += v.x;
+                    a += v.y;
+                }
+                b = warp_sum(b);
+                a = warp_sum(a);
+                if ((threadIdx.x & 31) == 0) {
+                    if (p.dgamma != nullptr) store_weight(p.dgamma, DT, c, a);
+                    if (p.dbeta != nullptr) store_weight(p.dbeta, DT, c, b);
+                }
+            }
+            continue;
+        }
+        const int pp = (int)(row / NC);
+        const int64_t nc = row - pp * NC, n = nc / p.C, c = nc - n * p.C, g = c / (p.C / p.G);
+        const int64_t S = p.spatial[pp];
+        if ((int64_t)blockIdx.y * EL_SEG >= S) continue;
+        float mean, rstd, count;
+        pooled_stats(p, n, g, mean, rstd, count);
+        mean = __shfl_sync(0xffffffffu, mean, 0);
+        rstd = __shfl_sync(0xffffffffu, rstd, 0);
+        count = __shfl_sync(0xffffffffu, count, 0);
+        const float2 k = make_float2(rstd * weight_at(p.gamma, DT, c, 1.f), weight_at(p.beta, DT, c, 0.f));
+        const float2 sums = group_sums(p, DT, n, g);
+        const float v = -sums.x / count * rstd, uu = -sums.y / count * rstd * rstd;
+        using E = typename Word<elem_size(DT)>::T;
+        for (int64_t e0 = (int64_t)blockIdx.y * EL_SEG; e0 < S; e0 += (int64_t)gridDim.y * EL_SEG) {
+            for (int64_t i = e0 + threadIdx.x; i < min(S, e0 + EL_SEG); i += EL_BLOCK) {
+                const float u = elem_at<DT>(p.patches[pp], nc * S + i) - mean;
+                const float dz = dz_one<SILU>(u, elem_at<DT>(p.grads[pp], nc * S + i), k);
+                const float o[1] = {fmaf(dz, k.x, fmaf(u, uu, v))};
+                reinterpret_cast<E*>(p.outs[pp])[nc * S + i] = pack<DT, 1>(o);
+            }
+        }
+    }
+}
+
+template <int DT, bool SILU>
+cudaError_t grad_launch(const GnGradParams& p, bool ring, int sms, cudaStream_t s) {
+    if (ring) {
+        const int64_t tasks = (p.mode == GRAD_BOTH ? 2 : 1) * p.N * p.G * (int64_t)p.unit_tasks + p.wtasks;
+        if (tasks == 0) return cudaSuccess;
+        if (p.mode == GRAD_BOTH) {
+            const cudaError_t e = launch_pdl(gn_grad_zero_kernel, p, dim3((unsigned)((p.N * p.G + 255) / 256)), 256, 0, s);
+            if (e != cudaSuccess) return e;
+        }
+        cudaError_t e = cudaFuncSetAttribute(gn_grad_kernel<DT, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize, GG_SMEM);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(gn_grad_kernel<DT, SILU>, p, dim3((unsigned)(tasks < sms ? tasks : sms)), GG_BLOCK, GG_SMEM, s);
+    }
+    const int64_t rows = (int64_t)p.P * p.N * p.C;
+    if (p.mode == GRAD_STATS) return launch_pdl(gn_grad_stats_elem_kernel<DT, SILU>, p, dim3((unsigned)rows), EL_BLOCK, 0, s);
+    int64_t longest = 0;
+    for (int q = 0; q < p.P; ++q) longest = longest < p.spatial[q] ? p.spatial[q] : longest;
+    int64_t segs = (longest + EL_SEG - 1) / EL_SEG;
+    segs = segs < 1 ? 1 : segs > 65535 ? 65535 : segs;
+    return launch_pdl(gn_grad_apply_elem_kernel<DT, SILU>, p, dim3((unsigned)(rows + p.wtasks), (unsigned)segs), EL_BLOCK, 0,
+                      s);
+}
+
+template <int DT>
+cudaError_t grad_dt(const GnGradParams& p, bool ring, int sms, cudaStream_t s) {
+    return p.silu ? grad_launch<DT, true>(p, ring, sms, s) : grad_launch<DT, false>(p, ring, sms, s);
+}
+
+}  // namespace
+
+cudaError_t launch_gn_grad(const GnGradParams& p, int dtype, bool ring, int sms, cudaStream_t s) {
+    switch (dtype) {
+        case F32: return grad_dt<F32>(p, ring, sms, s);
+        case F16: return grad_dt<F16>(p, ring, sms, s);
+        default: return grad_dt<BF16>(p, ring, sms, s);
+    }
+}
+
+}  // namespace tb

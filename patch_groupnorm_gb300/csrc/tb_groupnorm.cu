@@ -51,7 +51,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "tb_elem.cuh"
+#include "tb_groupnorm.cuh"
 #include "tb_internal.h"
 
 namespace tb {
@@ -411,90 +411,6 @@ __global__ void __launch_bounds__(STATS_BLOCK) gn_stats_kernel(const __grid_cons
     }
 }
 
-// Pooled (mean, rstd) of group g of sample n from the part records, computed
-// by one warp.  `partials` holds R record sets of [N][G][TB_GN_PARTS] (the
-// sets of one or more statistics calls, e.g. gathered from every rank), and
-// every record describes itself: records with count 0 hold no elements and
-// are skipped, whichever call wrote them and however it split its units.
-// Each record (count c, mean m, M2) adds c, c * (m - K) and
-// M2 + c * (m - K)^2 to three sums taken about K, the mean of the first
-// record with elements (so the sums do not cancel); then
-//     mean = K + S1 / n,   M2 = S2 - S1^2 / n   (Chan's combination, summed),
-// and the variance is M2 / n, biased.  Counts are summed exactly in 64 bits
-// and converted to fp32 once.  Lane 0 holds the result.
-// P: the parameters of the apply or of the backward pass.
-template <typename P>
-__device__ __forceinline__ void pooled_stats(const P& p, int64_t n, int64_t g, float& mean, float& rstd, float& count) {
-    const int lane = threadIdx.x & 31;
-    const int total = p.R * TB_GN_PARTS;
-    const int64_t set_stride = p.N * p.G * TB_GN_PARTS;  // records between consecutive sets
-    const GnPartial* const unit0 = p.partials + (n * p.G + g) * TB_GN_PARTS;
-    auto record = [&](int q, long long& c, float& m, float& m2) {
-        const int r = q / TB_GN_PARTS, k = q - r * TB_GN_PARTS;
-        const GnPartial* const at = unit0 + r * set_stride + k;
-        if (!in_bounds(at, sizeof(GnPartial), p.partials, (int64_t)p.R * set_stride * (int64_t)sizeof(GnPartial),
-                       p.status)) {
-            c = 0;
-            m = m2 = 0.f;
-            return;
-        }
-        const longlong2 raw = __ldg(reinterpret_cast<const longlong2*>(at));
-        c = raw.x;
-        m = __int_as_float((int)(raw.y & 0xffffffffLL));
-        m2 = __int_as_float((int)(raw.y >> 32));
-    };
-    // the first 32 records stay in registers (all of them when R <= 4)
-    long long c0 = 0;
-    float m0 = 0.f, v0 = 0.f;
-    if (lane < total) record(lane, c0, m0, v0);
-    float K = 0.f;
-    unsigned has = __ballot_sync(0xffffffffu, c0 > 0);
-    if (has != 0u) {
-        K = __shfl_sync(0xffffffffu, m0, __ffs(has) - 1);
-    } else {
-        for (int base = 32; base < total; base += 32) {
-            long long c = 0;
-            float m = 0.f, m2 = 0.f;
-            if (base + lane < total) record(base + lane, c, m, m2);
-            has = __ballot_sync(0xffffffffu, c > 0);
-            if (has != 0u) {
-                K = __shfl_sync(0xffffffffu, m, __ffs(has) - 1);
-                break;
-            }
-        }
-    }
-    long long sn = 0;
-    float s1 = 0.f, s2 = 0.f;
-    auto add = [&](long long c, float m, float m2) {
-        if (c > 0) {
-            const float cf = (float)c;
-            const float d = m - K;
-            sn += c;
-            s1 = fmaf(cf, d, s1);
-            s2 += fmaf(cf * d, d, m2);
-        }
-    };
-    add(c0, m0, v0);
-    for (int q = lane + 32; q < total; q += 32) {
-        long long c;
-        float m, m2;
-        record(q, c, m, m2);
-        add(c, m, m2);
-    }
-#pragma unroll
-    for (int delta = 16; delta >= 1; delta >>= 1) {  // fixed order: deterministic
-        sn += __shfl_down_sync(0xffffffffu, sn, delta);
-        s1 += __shfl_down_sync(0xffffffffu, s1, delta);
-        s2 += __shfl_down_sync(0xffffffffu, s2, delta);
-    }
-    const float nf = (float)sn;
-    const float q1 = sn > 0 ? s1 / nf : 0.f;
-    const float var = sn > 0 ? fmaxf(0.f, fmaf(-s1, q1, s2) / nf) : 0.f;  // biased: divide by the count
-    mean = K + q1;
-    rstd = 1.0f / sqrtf(var + p.eps);
-    count = nf;
-}
-
 // (a, b) with y = x * a + b for channel c.
 template <int DT>
 __device__ __forceinline__ float2 channel_affine(const GnApplyParams& p, int64_t n, int64_t g, int64_t c);
@@ -520,22 +436,6 @@ __device__ __forceinline__ float2 channel_affine(const GnApplyParams& p, int64_t
     const bool c_ok = index_ok(c >= 0 && c < p.C, p.status);
     const float a = rstd * (c_ok ? load_param<DT>(p.gamma, c, 1.f) : 1.f);
     return make_float2(a, (c_ok ? load_param<DT>(p.beta, c, 0.f) : 0.f) - mean * a);
-}
-
-// silu(z) = z / (1 + e^-z), with e^-z = 2^(-z log2 e) and the reciprocal
-// from the approximate special-function unit (relative errors ~2^-22, far
-// inside the output tolerances).  Flushing subnormals there is harmless:
-// e^-z is subnormal only for z > 87, where 1 + e^-z rounds to 1, and the
-// reciprocal only for z < -87, where silu(z) lies below 1e-35.
-__device__ __forceinline__ float ex2_ftz(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float rcp_ftz(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 template <int SILU>
@@ -719,282 +619,6 @@ cudaError_t apply_dt(const GnApplyParams& p, int64_t items, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
-// ---------------------------------------------------------------------------
-// backward pass
-//
-// With xhat = (x - mean) * rstd, z = xhat * gamma + beta and, for SiLU,
-// s = 1 / (1 + e^-z):
-//     dz = silu ? dy * s * (1 + z * (1 - s)) : dy
-//     B(n, c) = sum dz,  A(n, c) = sum dz * xhat     (over the channel's elements)
-//     dgamma(c) = sum_n A,  dbeta(c) = sum_n B
-//     c1 = sum over the group's channels of gamma * B / count,  c2 the same of A
-//     dx = rnd(rstd * (gamma * dz - c1 - xhat * c2))
-// Like the forward pass it runs in two launches that meet in records:
-// gn_grad_stats_kernel writes (B, A) of every (patch, sample, channel), in up
-// to TB_GN_PARTS parts (the unused ones zero), and gn_grad_apply_kernel adds
-// up the records of all R sets, which may come from other ranks.
-// ---------------------------------------------------------------------------
-
-constexpr int GRAD_BLOCK = 256;
-#ifndef TB_GN_GRAD_CPT
-#define TB_GN_GRAD_CPT 4
-#endif
-constexpr int GRAD_CPT = TB_GN_GRAD_CPT;  // 16-byte chunks of x and of dy per thread in flight
-
-// One channel's constants: z = x * za + zb, xhat = x * rstd + xb.
-struct Channel {
-    float za, zb, rstd, xb, gamma;
-};
-
-template <int DT>
-__device__ __forceinline__ Channel grad_channel(const GnGradParams& p, int64_t c, float mean, float rstd) {
-    const bool c_ok = index_ok(c >= 0 && c < p.C, p.status);
-    Channel k;
-    k.gamma = c_ok ? load_param<DT>(p.gamma, c, 1.f) : 1.f;
-    k.za = rstd * k.gamma;
-    k.zb = (c_ok ? load_param<DT>(p.beta, c, 0.f) : 0.f) - mean * k.za;
-    k.rstd = rstd;
-    k.xb = -mean * rstd;
-    return k;
-}
-
-template <int SILU>
-__device__ __forceinline__ float grad_act(float x, float dy, const Channel& k) {
-    if constexpr (SILU) {
-        const float z = fmaf(x, k.za, k.zb);
-        const float s = rcp_ftz(1.0f + ex2_ftz(z * -1.4426950408889634f));
-        return dy * s * fmaf(z, 1.0f - s, 1.0f);
-    } else {
-        return dy;
-    }
-}
-
-template <int DT, bool VECTOR, int SILU>
-__global__ void __launch_bounds__(GRAD_BLOCK) gn_grad_stats_kernel(const __grid_constant__ GnGradParams p) {
-    constexpr int VEC = VECTOR ? 16 / GElt<DT>::BYTES : 1;
-    __shared__ float2 s_warp[GRAD_BLOCK / 32];
-    const unsigned parts = (unsigned)p.parts;
-    const unsigned unit = blockIdx.x / parts;  // (patch, sample, channel)
-    const int part = (int)(blockIdx.x - unit * parts);
-    const unsigned NC = (unsigned)p.N * (unsigned)p.C;
-    const unsigned pp = unit / NC;
-    const unsigned row = unit - pp * NC;  // n * C + c
-    const unsigned n = row / (unsigned)p.C;
-    const unsigned c = row - n * (unsigned)p.C;
-    const unsigned g = c / (unsigned)(p.C / p.G);
-    const int64_t S = p.spatial[pp];
-    const int64_t pbytes = p.N * p.C * S * GElt<DT>::BYTES;
-    const int64_t v0 = S / VEC * part / parts, v1 = S / VEC * (part + 1) / parts;
-    grid_wait();
-
-    float mean, rstd, count;
-    pooled_stats(p, n, g, mean, rstd, count);
-    mean = __shfl_sync(0xffffffffu, mean, 0);
-    rstd = __shfl_sync(0xffffffffu, rstd, 0);
-    const Channel k = grad_channel<DT>(p, c, mean, rstd);
-    float B = 0.f, A = 0.f;
-    auto add = [&](float x, float dy) {
-        const float dz = grad_act<SILU>(x, dy, k);
-        B += dz;
-        A = fmaf(dz, fmaf(x, k.rstd, k.xb), A);
-    };
-    if constexpr (VECTOR) {
-        const uint4* const xs = reinterpret_cast<const uint4*>(p.patches[pp]) + row * (S / VEC);
-        const uint4* const ds = reinterpret_cast<const uint4*>(p.grads[pp]) + row * (S / VEC);
-        for (int64_t i0 = v0; i0 < v1; i0 += GRAD_BLOCK * GRAD_CPT) {
-            uint4 x[GRAD_CPT], d[GRAD_CPT];
-#pragma unroll
-            for (int q = 0; q < GRAD_CPT; ++q) {
-                const int64_t i = i0 + threadIdx.x + q * GRAD_BLOCK;
-                x[q] = d[q] = make_uint4(0u, 0u, 0u, 0u);
-                if (i < v1 && in_bounds(xs + i, 16, p.patches[pp], pbytes, p.status) &&
-                    in_bounds(ds + i, 16, p.grads[pp], pbytes, p.status)) {
-                    x[q] = xs[i];
-                    d[q] = ds[i];
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < GRAD_CPT; ++q) {
-                if (i0 + threadIdx.x + q * GRAD_BLOCK < v1) {
-                    float xf[VEC], df[VEC];
-                    chunk_to_floats<DT>(x[q], xf);
-                    chunk_to_floats<DT>(d[q], df);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) add(xf[e], df[e]);
-                }
-            }
-        }
-    } else {
-        const int64_t base = (int64_t)row * S;
-        for (int64_t i = v0 + threadIdx.x; i < v1; i += GRAD_BLOCK) {
-            if (!index_ok((base + i) * GElt<DT>::BYTES < pbytes, p.status)) continue;
-            add(load_scalar<DT>(p.patches[pp], base + i), load_scalar<DT>(p.grads[pp], base + i));
-        }
-    }
-    B = warp_sum(B);
-    A = warp_sum(A);
-    if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = make_float2(B, A);
-    __syncthreads();
-    if (threadIdx.x < TB_GN_PARTS && threadIdx.x % parts == part) {
-        // record `part`, and the zero records of the parts no CTA takes
-        float2 t = make_float2(0.f, 0.f);
-        if (threadIdx.x == part) {
-#pragma unroll
-            for (int w = 0; w < GRAD_BLOCK / 32; ++w) {
-                t.x += s_warp[w].x;
-                t.y += s_warp[w].y;
-            }
-        }
-        if (index_ok(unit < (unsigned)p.P * NC, p.status))
-            p.grad_partials[(int64_t)unit * TB_GN_PARTS + threadIdx.x] = t;
-    }
-}
-
-// (c1, c2) of group g of sample n, times the group's count: one warp adds up
-// the records of the group's channels in all R sets, weighted with gamma.
-template <int DT>
-__device__ __forceinline__ float2 group_sums(const GnGradParams& p, int64_t n, int64_t g) {
-    const int cg = (int)(p.C / p.G);
-    const int per = cg * TB_GN_PARTS;
-    const int64_t set = p.N * p.C * TB_GN_PARTS;
-    const float2* const at = p.grad_partials + (n * p.C + g * cg) * TB_GN_PARTS;
-    float B = 0.f, A = 0.f;
-    for (int r = 0; r < p.R; ++r) {
-        for (int q = threadIdx.x & 31; q < per; q += 32) {
-            const float2* const src = at + r * set + q;
-            if (!in_bounds(src, sizeof(float2), p.grad_partials, (int64_t)p.R * set * (int64_t)sizeof(float2), p.status))
-                continue;
-            const float2 v = *src;
-            const float w = load_param<DT>(p.gamma, g * cg + q / TB_GN_PARTS, 1.f);
-            B = fmaf(v.x, w, B);
-            A = fmaf(v.y, w, A);
-        }
-    }
-    return make_float2(warp_sum(B), warp_sum(A));
-}
-
-template <int DT, bool VECTOR, int SILU>
-__global__ void __launch_bounds__(GRAD_BLOCK) gn_grad_apply_kernel(const __grid_constant__ GnGradParams p) {
-    constexpr int VEC = VECTOR ? 16 / GElt<DT>::BYTES : 1;
-    if ((int)blockIdx.x < p.wblocks) {
-        // the weight gradients: a warp per channel adds up its records of
-        // all samples and sets
-        grid_wait();
-        const int64_t c = (int64_t)blockIdx.x * (GRAD_BLOCK / 32) + (threadIdx.x >> 5);
-        if (c >= p.C) return;
-        const int64_t rows = (int64_t)p.R * p.N * TB_GN_PARTS;
-        float B = 0.f, A = 0.f;
-        for (int64_t q = threadIdx.x & 31; q < rows; q += 32) {
-            const float2 v = p.grad_partials[(q / TB_GN_PARTS * p.C + c) * TB_GN_PARTS + q % TB_GN_PARTS];
-            B += v.x;
-            A += v.y;
-        }
-        B = warp_sum(B);
-        A = warp_sum(A);
-        if ((threadIdx.x & 31) == 0) {
-            if (p.dgamma != nullptr) store_weight(p.dgamma, DT, c, A);
-            if (p.dbeta != nullptr) store_weight(p.dbeta, DT, c, B);
-        }
-        return;
-    }
-    const int64_t item = (int64_t)blockIdx.x - p.wblocks;
-    int pp = 0;
-    while (pp + 1 < p.P && p.item_start[pp + 1] <= item) ++pp;
-    const unsigned local = (unsigned)(item - p.item_start[pp]);
-    const unsigned nseg = (unsigned)p.nseg[pp];
-    const unsigned row = local / nseg;  // n * C + c
-    const int64_t seg = local - row * nseg;
-    const int64_t S = p.spatial[pp];
-    const unsigned C32 = (unsigned)p.C;
-    const int64_t c = row % C32;
-    const int64_t n = row / C32;
-    const int64_t g = (unsigned)c / (C32 / (unsigned)p.G);
-    const int64_t e_begin = seg * p.seg;
-    const int64_t e_end = min(S, e_begin + p.seg);
-    const int64_t row_start = (int64_t)row * S;
-    const int64_t pbytes = p.N * p.C * S * GElt<DT>::BYTES;
-    grid_wait();
-
-    constexpr int CPT = VECTOR ? GRAD_CPT : 1;
-    const uint4* const xs = reinterpret_cast<const uint4*>(p.patches[pp]) + (row_start + e_begin) / VEC;
-    const uint4* const ds = reinterpret_cast<const uint4*>(p.grads[pp]) + (row_start + e_begin) / VEC;
-    uint4* const os = reinterpret_cast<uint4*>(p.outs[pp]) + (row_start + e_begin) / VEC;
-    const int nchunk = (int)((e_end - e_begin) / VEC);
-    uint4 x[CPT], d[CPT];
-    if constexpr (VECTOR) {  // the data loads first; they cover the records' latency
-#pragma unroll
-        for (int q = 0; q < CPT; ++q) {
-            const int i = threadIdx.x + q * GRAD_BLOCK;
-            x[q] = d[q] = make_uint4(0u, 0u, 0u, 0u);
-            if (i < nchunk && in_bounds(xs + i, 16, p.patches[pp], pbytes, p.status) &&
-                in_bounds(ds + i, 16, p.grads[pp], pbytes, p.status)) {
-                x[q] = __ldcs(xs + i);
-                d[q] = __ldcs(ds + i);
-            }
-        }
-    }
-    float mean, rstd, count;
-    pooled_stats(p, n, g, mean, rstd, count);
-    mean = __shfl_sync(0xffffffffu, mean, 0);
-    rstd = __shfl_sync(0xffffffffu, rstd, 0);
-    count = __shfl_sync(0xffffffffu, count, 0);
-    const Channel k = grad_channel<DT>(p, c, mean, rstd);
-    const float2 sums = group_sums<DT>(p, n, g);
-    // dx = dz * za - (c1 + xhat * c2) * rstd = dz * za + x * u + v
-    const float c1 = sums.x / count * rstd, c2 = sums.y / count * rstd;
-    const float u = -c2 * k.rstd, v = -fmaf(c2, k.xb, c1);
-    auto grad = [&](float xv, float dy) { return fmaf(grad_act<SILU>(xv, dy, k), k.za, fmaf(xv, u, v)); };
-    if constexpr (VECTOR) {
-#pragma unroll
-        for (int q = 0; q < CPT; ++q) {
-            const int i = threadIdx.x + q * GRAD_BLOCK;
-            if (i >= nchunk) continue;
-            float xf[VEC], df[VEC];
-            chunk_to_floats<DT>(x[q], xf);
-            chunk_to_floats<DT>(d[q], df);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) xf[e] = grad(xf[e], df[e]);
-            uint4 o;
-            if constexpr (GElt<DT>::BYTES == 4) {
-                o = make_uint4(__float_as_uint(xf[0]), __float_as_uint(xf[1]), __float_as_uint(xf[2]),
-                               __float_as_uint(xf[3]));
-            } else {
-                o = make_uint4(GElt<DT>::pack(xf[0], xf[1]), GElt<DT>::pack(xf[2], xf[3]),
-                               GElt<DT>::pack(xf[4], xf[5]), GElt<DT>::pack(xf[6], xf[7]));
-            }
-            if (in_bounds(os + i, 16, p.outs[pp], pbytes, p.status)) __stcs(os + i, o);
-        }
-    } else {
-        for (int64_t e = e_begin + threadIdx.x; e < e_end; e += GRAD_BLOCK) {
-            if (!index_ok((row_start + e) * GElt<DT>::BYTES < pbytes, p.status)) continue;
-            const float o = grad(load_scalar<DT>(p.patches[pp], row_start + e),
-                                 load_scalar<DT>(p.grads[pp], row_start + e));
-            if constexpr (GElt<DT>::BYTES == 4) {
-                __stcs(reinterpret_cast<float*>(p.outs[pp]) + row_start + e, o);
-            } else {
-                __stcs(reinterpret_cast<unsigned short*>(p.outs[pp]) + row_start + e,
-                       (unsigned short)(GElt<DT>::pack(o, 0.f) & 0xffffu));
-            }
-        }
-    }
-}
-
-template <int DT>
-cudaError_t grad_stats_dt(const GnGradParams& p, int64_t units, cudaStream_t s) {
-    void (*fn)(const GnGradParams);
-    if (p.aligned) fn = p.silu ? gn_grad_stats_kernel<DT, true, 1> : gn_grad_stats_kernel<DT, true, 0>;
-    else fn = p.silu ? gn_grad_stats_kernel<DT, false, 1> : gn_grad_stats_kernel<DT, false, 0>;
-    return launch_pdl(fn, p, dim3((unsigned)(units * p.parts)), GRAD_BLOCK, 0, s);
-}
-
-template <int DT>
-cudaError_t grad_apply_dt(const GnGradParams& p, int64_t items, cudaStream_t s) {
-    void (*fn)(const GnGradParams);
-    if (p.aligned) fn = p.silu ? gn_grad_apply_kernel<DT, true, 1> : gn_grad_apply_kernel<DT, true, 0>;
-    else fn = p.silu ? gn_grad_apply_kernel<DT, false, 1> : gn_grad_apply_kernel<DT, false, 0>;
-    return launch_pdl(fn, p, dim3((unsigned)(items + p.wblocks)), GRAD_BLOCK, 0, s);
-}
-
 }  // namespace
 
 int gn_apply_segment(int dtype, bool aligned) {
@@ -1015,27 +639,6 @@ cudaError_t launch_gn_apply(const GnApplyParams& p, int dtype, int64_t items, cu
         case F32: return apply_dt<F32>(p, items, s);
         case F16: return apply_dt<F16>(p, items, s);
         default: return apply_dt<BF16>(p, items, s);
-    }
-}
-
-int gn_grad_segment(int dtype, bool aligned) {
-    const int bytes = dtype == F32 ? 4 : 2;
-    return GRAD_BLOCK * (aligned ? GRAD_CPT * (16 / bytes) : 16);
-}
-
-cudaError_t launch_gn_grad_stats(const GnGradParams& p, int dtype, int64_t units, cudaStream_t s) {
-    switch (dtype) {
-        case F32: return grad_stats_dt<F32>(p, units, s);
-        case F16: return grad_stats_dt<F16>(p, units, s);
-        default: return grad_stats_dt<BF16>(p, units, s);
-    }
-}
-
-cudaError_t launch_gn_grad_apply(const GnGradParams& p, int dtype, int64_t items, cudaStream_t s) {
-    switch (dtype) {
-        case F32: return grad_apply_dt<F32>(p, items, s);
-        case F16: return grad_apply_dt<F16>(p, items, s);
-        default: return grad_apply_dt<BF16>(p, items, s);
     }
 }
 

@@ -422,35 +422,53 @@ void record_cuda_error(cudaError_t e);
 cudaError_t launch_gn_stats(const GnStatsParams& p, int dtype, int64_t units, cudaStream_t s);
 cudaError_t launch_gn_apply(const GnApplyParams& p, int dtype, int64_t items, cudaStream_t s);
 
+// What a launch of the backward pass does.
+enum GnGradMode : int32_t {
+    GRAD_STATS = 0,  // write the records
+    GRAD_APPLY = 1,  // dx and the weight gradients from the records of R sets
+    GRAD_BOTH = 2    // both, each group's dx following its records in one launch
+};
+
 struct GnGradParams {
-    const void* patches[GN_MAXP];     // x
-    const void* grads[GN_MAXP];       // dy
-    void* outs[GN_MAXP];              // dx (apply only)
+    const void* patches[GN_MAXP];  // x
+    const void* grads[GN_MAXP];    // dy
+    void* outs[GN_MAXP];           // dx
     int64_t spatial[GN_MAXP];
-    int64_t item_start[GN_MAXP + 1];  // first work item of patch p (prefix sums; apply only)
-    int64_t nseg[GN_MAXP];            // segments per channel row of patch p (apply only)
-    const GnPartial* partials;        // the forward pass's records: [R][N][G][TB_GN_PARTS]
-    float2* grad_partials;            // (sum dz, sum dz * xhat): [P or R][N][C][TB_GN_PARTS]
-    const void* gamma;                // [C] or null
-    const void* beta;                 // [C] or null
-    void* dgamma;                     // [C] or null (apply only)
-    void* dbeta;                      // [C] or null (apply only)
+    const GnPartial* partials;     // the forward pass's records: [R][N][G][TB_GN_PARTS]
+    float2* grad_partials;         // (sum dz, sum dz * xhat): [P or R][N][C][TB_GN_PARTS]
+    const void* gamma;             // [C] or null
+    const void* beta;              // [C] or null
+    void* dgamma;                  // [C] or null
+    void* dbeta;                   // [C] or null
     int64_t N, C;
     int32_t P, G;
-    int32_t parts;                    // CTAs per channel row (stats only): 1 .. TB_GN_PARTS
-    int32_t seg;                      // elements per segment (apply only)
-    int32_t R;                        // record sets
-    int32_t wblocks;                  // leading CTAs that reduce the weight gradients (apply only)
+    int32_t R;                     // record sets
+    int32_t mode;
     float eps;
     int32_t silu;
-    int32_t aligned;                  // every channel row start is 16-byte aligned
-    uint32_t* status;                 // bounds-checked build: device status word (else null)
+    uint32_t* status;              // device status word (a wait that runs out is recorded there)
+    // The ring kernel's work: every group of every sample (a unit) is cut into
+    // unit_tasks tasks, patch p's being task_start[p] .. task_start[p + 1] - 1:
+    // rows[p] whole channel rows each, or parts[p] to a row where rows[p] is 1.
+    int32_t rows[GN_MAXP];
+    int32_t parts[GN_MAXP];
+    int32_t task_start[GN_MAXP + 1];
+    int32_t unit_tasks;
+    int32_t lag;                   // GRAD_BOTH: units whose records run ahead of the first dx
+    int32_t wtasks;                // tasks of GRAD_CHANNELS weight gradients each
 };
 static_assert(sizeof(GnGradParams) <= 32000, "kernel parameter block too large");
 
-int gn_grad_segment(int dtype, bool aligned);
-cudaError_t launch_gn_grad_stats(const GnGradParams& p, int dtype, int64_t units, cudaStream_t s);
-cudaError_t launch_gn_grad_apply(const GnGradParams& p, int dtype, int64_t items, cudaStream_t s);
+constexpr int GRAD_STAGE_BYTES = 32768;  // of x, and of dy, in one ring stage
+constexpr int GRAD_MAX_ROWS = 31;        // channel rows of one task
+constexpr int GRAD_CHANNELS = 16;        // channels of one weight-gradient task
+// GRAD_BOTH keeps the units' arrival counters and the task counter in the
+// last two record slots of a row, so it cuts rows into fewer parts.
+constexpr int GRAD_BOTH_PARTS = TB_GN_PARTS - 2;
+
+// ring: patches, gradients and outputs share their offset from 16-byte
+// boundaries (the ring kernel); otherwise the element kernels run.
+cudaError_t launch_gn_grad(const GnGradParams& p, int dtype, bool ring, int sms, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // Layer norm

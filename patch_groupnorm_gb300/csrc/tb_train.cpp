@@ -11,6 +11,11 @@
 
 #define TB_API extern "C" __attribute__((visibility("default")))
 
+// GroupNorm backward in one launch: tasks per SM by which the records run ahead.
+#ifndef TB_GN_GRAD_LAG
+#define TB_GN_GRAD_LAG 2
+#endif
+
 namespace {
 
 tb_status launched(cudaError_t e) {
@@ -126,10 +131,13 @@ tb_status each_table(const void* const* grads, void* const* outs, const int64_t*
 // PatchGroupNorm backward
 // ---------------------------------------------------------------------------
 
-tb_status gn_grad_params(tb::GnGradParams& prm, const void* const* patches, const void* const* grads, int32_t P,
-                         tb_dtype dtype, int64_t N, int64_t C, const int64_t* spatial, int32_t G,
-                         const tb_gn_partial* partials, int32_t R, const void* gamma, const void* beta, float eps,
-                         int32_t silu, const void* grad_partials) {
+// Validates a call and fills everything but the work.  `outs` NULL: a
+// statistics call.  *ring: every tensor of a patch has the same offset from
+// 16-byte boundaries.
+tb_status gn_grad_params(tb::GnGradParams& prm, bool* ring, const void* const* patches, const void* const* grads,
+                         void* const* outs, int32_t P, tb_dtype dtype, int64_t N, int64_t C, const int64_t* spatial,
+                         int32_t G, const tb_gn_partial* partials, int32_t R, const void* gamma, const void* beta,
+                         float eps, int32_t silu, const void* grad_partials, void* dgamma, void* dbeta) {
     if (!known(dtype)) return TB_ERR_DTYPE;
     if (P < 1 || N < 0 || C < 0 || G < 1 || R < 1) return TB_ERR_SHAPE;
     if (C % G != 0) return TB_ERR_SHAPE;
@@ -139,24 +147,30 @@ tb_status gn_grad_params(tb::GnGradParams& prm, const void* const* patches, cons
     if ((double)std::max(P, R) * (double)N * (double)C * TB_GN_PARTS > 2.0e9) return TB_ERR_UNSUPPORTED;
     std::memset(&prm, 0, sizeof(prm));
     const int es = elem_bytes(dtype);
-    bool vector = true;
+    *ring = true;
     for (int p = 0; p < P; ++p) {
         if (spatial[p] < 0) return TB_ERR_SHAPE;
         prm.patches[p] = patches[p];
         prm.grads[p] = grads[p];
+        prm.outs[p] = outs ? outs[p] : nullptr;
         prm.spatial[p] = spatial[p];
         if (N == 0 || C == 0 || spatial[p] == 0) continue;
-        if (patches[p] == nullptr || grads[p] == nullptr) return TB_ERR_NULL;
+        if (patches[p] == nullptr || grads[p] == nullptr || (outs && outs[p] == nullptr)) return TB_ERR_NULL;
         if ((double)N * (double)C * (double)spatial[p] > 2.0e18) return TB_ERR_SHAPE;
-        if (!aligned(patches[p], es) || !aligned(grads[p], es)) return TB_ERR_UNSUPPORTED;
-        if (!aligned(patches[p], 16) || !aligned(grads[p], 16) || spatial[p] % (16 / es) != 0) vector = false;
+        if (!aligned(patches[p], es) || !aligned(grads[p], es) || !aligned(prm.outs[p], es)) return TB_ERR_UNSUPPORTED;
+        const uintptr_t off = (uintptr_t)patches[p] & 15u;
+        if (((uintptr_t)grads[p] & 15u) != off || (outs && ((uintptr_t)outs[p] & 15u) != off)) *ring = false;
     }
     if (N > 0 && C > 0 && (partials == nullptr || grad_partials == nullptr)) return TB_ERR_NULL;
-    if (!aligned(gamma, es) || !aligned(beta, es)) return TB_ERR_UNSUPPORTED;
+    if (!aligned(gamma, es) || !aligned(beta, es) || !aligned(dgamma, es) || !aligned(dbeta, es))
+        return TB_ERR_UNSUPPORTED;
+    if (!aligned(partials, 16) || !aligned(grad_partials, 8)) return TB_ERR_UNSUPPORTED;
     prm.partials = reinterpret_cast<const tb::GnPartial*>(partials);
     prm.grad_partials = reinterpret_cast<float2*>(const_cast<void*>(grad_partials));
     prm.gamma = gamma;
     prm.beta = beta;
+    prm.dgamma = dgamma;
+    prm.dbeta = dbeta;
     prm.N = N;
     prm.C = C;
     prm.P = P;
@@ -164,8 +178,60 @@ tb_status gn_grad_params(tb::GnGradParams& prm, const void* const* patches, cons
     prm.R = R;
     prm.eps = eps;
     prm.silu = silu ? 1 : 0;
-    prm.aligned = vector ? 1 : 0;
-    prm.status = tb::checked_build_status();
+    prm.wtasks = dgamma != nullptr || dbeta != nullptr ? (int32_t)((C + tb::GRAD_CHANNELS - 1) / tb::GRAD_CHANNELS) : 0;
+    prm.status = tb::device_status_word();
+    return TB_OK;
+}
+
+// Cuts the work of `mode` into tasks: whole rows, as many as one ring stage
+// holds, or parts of a row of a stage each; smaller ones where that gives less
+// than two tasks per SM.
+tb_status gn_grad_tasks(tb::GnGradParams& prm, int mode, tb_dtype dtype, int sms) {
+    const int es = elem_bytes(dtype), vec = 16 / es;
+    const int64_t K = prm.C / prm.G, units = prm.N * prm.G;
+    const int most_parts = mode == tb::GRAD_BOTH ? tb::GRAD_BOTH_PARTS : TB_GN_PARTS;
+    prm.mode = mode;
+    for (int p = 0; p < prm.P; ++p) {
+        const int64_t row = prm.spatial[p] * es;
+        prm.rows[p] = prm.parts[p] = 0;
+        if (row == 0 && mode != tb::GRAD_STATS) continue;  // no elements; a statistics call still writes its records
+        const int64_t fit = row > 0 ? tb::GRAD_STAGE_BYTES / row : tb::GRAD_MAX_ROWS;
+        prm.rows[p] = (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fit, tb::GRAD_MAX_ROWS), K));
+        const int64_t want = (row + tb::GRAD_STAGE_BYTES - 1) / tb::GRAD_STAGE_BYTES;
+        prm.parts[p] = (int32_t)std::max<int64_t>(1, std::min<int64_t>(want, most_parts));
+    }
+    auto tasks_of = [&](int p) {
+        if (prm.rows[p] == 0) return (int64_t)0;
+        return prm.parts[p] > 1 ? K * prm.parts[p] : (K + prm.rows[p] - 1) / prm.rows[p];
+    };
+    for (bool smaller = true; smaller;) {
+        int64_t total = 0;
+        for (int p = 0; p < prm.P; ++p) total += units * tasks_of(p);
+        if (total >= 2 * (int64_t)sms) break;
+        smaller = false;
+        for (int p = 0; p < prm.P; ++p) {
+            if (prm.rows[p] > 1) {
+                prm.rows[p] = (prm.rows[p] + 1) / 2;
+                smaller = true;
+            } else if (prm.rows[p] == 1 && prm.parts[p] < most_parts &&
+                       prm.spatial[p] / vec / (prm.parts[p] + 1) >= 256) {
+                ++prm.parts[p];
+                smaller = true;
+            }
+        }
+    }
+    int64_t at = 0;
+    for (int p = 0; p < prm.P; ++p) {
+        prm.task_start[p] = (int32_t)at;
+        at += tasks_of(p);
+        if (at > 1000000000LL) return TB_ERR_UNSUPPORTED;
+    }
+    prm.task_start[prm.P] = (int32_t)at;
+    prm.unit_tasks = (int32_t)at;
+    if (2.0 * (double)units * (double)at + prm.wtasks > 2.0e9) return TB_ERR_UNSUPPORTED;
+    // the records run two tasks per SM ahead: by then a CTA has done with what
+    // it holds, and no dx task waits
+    prm.lag = (int32_t)std::min<int64_t>(units, (TB_GN_GRAD_LAG * sms + at - 1) / std::max<int64_t>(at, 1));
     return TB_OK;
 }
 
@@ -331,21 +397,14 @@ TB_API tb_status tb_patch_gn_grad_stats(const void* const* patches, const void* 
                                         const tb_gn_partial* partials, int32_t R, const void* gamma, const void* beta,
                                         float eps, int32_t silu, tb_gn_grad_partial* grad_partials, void* stream) {
     tb::GnGradParams prm;
-    TB_TRY(gn_grad_params(prm, patches, grads, P, dtype, N, C, spatial, G, partials, R, gamma, beta, eps, silu,
-                          grad_partials));
+    bool ring = false;
+    TB_TRY(gn_grad_params(prm, &ring, patches, grads, nullptr, P, dtype, N, C, spatial, G, partials, R, gamma, beta,
+                          eps, silu, grad_partials, nullptr, nullptr));
     if (N == 0 || C == 0) return TB_OK;
     int sms = 0;
     TB_TRY(tb::sm_count(&sms));
-    // CTAs per channel row: enough for about eight per SM, each with 16 KB of
-    // x or more
-    int64_t longest = 0;
-    for (int p = 0; p < P; ++p) longest = std::max(longest, spatial[p]);
-    const int64_t units = (int64_t)P * N * C;
-    const int64_t want = std::min<int64_t>((8LL * sms + units - 1) / units, longest * elem_bytes(dtype) / 16384);
-    int parts = 1;
-    while (parts * 2 <= TB_GN_PARTS && parts * 2 <= want) parts *= 2;
-    prm.parts = parts;
-    return launched(tb::launch_gn_grad_stats(prm, (int)dtype, units, reinterpret_cast<cudaStream_t>(stream)));
+    TB_TRY(gn_grad_tasks(prm, tb::GRAD_STATS, dtype, sms));
+    return launched(tb::launch_gn_grad(prm, (int)dtype, ring, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 TB_API tb_status tb_patch_gn_grad_apply(const void* const* patches, const void* const* grads, void* const* outs,
@@ -355,32 +414,39 @@ TB_API tb_status tb_patch_gn_grad_apply(const void* const* patches, const void* 
                                         const void* beta, float eps, int32_t silu, void* dgamma, void* dbeta,
                                         void* stream) {
     tb::GnGradParams prm;
-    TB_TRY(gn_grad_params(prm, patches, grads, P, dtype, N, C, spatial, G, partials, R, gamma, beta, eps, silu,
-                          grad_partials));
+    bool ring = false;
     if (outs == nullptr) return TB_ERR_NULL;
-    const int es = elem_bytes(dtype);
-    if (!aligned(dgamma, es) || !aligned(dbeta, es)) return TB_ERR_UNSUPPORTED;
-    if (C == 0) return TB_OK;
-    for (int p = 0; p < P && N > 0; ++p) {
-        if (spatial[p] == 0) continue;
-        if (outs[p] == nullptr) return TB_ERR_NULL;
-        if (!aligned(outs[p], es)) return TB_ERR_UNSUPPORTED;
-        if (!aligned(outs[p], 16)) prm.aligned = 0;
+    TB_TRY(gn_grad_params(prm, &ring, patches, grads, outs, P, dtype, N, C, spatial, G, partials, R, gamma, beta, eps,
+                          silu, grad_partials, dgamma, dbeta));
+    if (C == 0 || (N == 0 && prm.wtasks == 0)) return TB_OK;
+    int sms = 0;
+    TB_TRY(tb::sm_count(&sms));
+    TB_TRY(gn_grad_tasks(prm, tb::GRAD_APPLY, dtype, sms));
+    return launched(tb::launch_gn_grad(prm, (int)dtype, ring, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+TB_API tb_status tb_patch_gn_backward(const void* const* patches, const void* const* grads, void* const* outs,
+                                      int32_t P, tb_dtype dtype, int64_t N, int64_t C, const int64_t* spatial,
+                                      int32_t G, const tb_gn_partial* partials, const void* gamma, const void* beta,
+                                      float eps, int32_t silu, void* dgamma, void* dbeta,
+                                      tb_gn_grad_partial* grad_partials, void* stream) {
+    tb::GnGradParams prm;
+    bool ring = false;
+    if (outs == nullptr) return TB_ERR_NULL;
+    TB_TRY(gn_grad_params(prm, &ring, patches, grads, outs, P, dtype, N, C, spatial, G, partials, P, gamma, beta, eps,
+                          silu, grad_partials, dgamma, dbeta));
+    if (C == 0 || (N == 0 && prm.wtasks == 0)) return TB_OK;
+    int sms = 0;
+    TB_TRY(tb::sm_count(&sms));
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (ring && N > 0) {
+        TB_TRY(gn_grad_tasks(prm, tb::GRAD_BOTH, dtype, sms));
+        return launched(tb::launch_gn_grad(prm, (int)dtype, true, sms, s));
     }
-    const int64_t seg = tb::gn_grad_segment((int)dtype, prm.aligned != 0);
-    int64_t items = 0;
-    for (int p = 0; p < P; ++p) {
-        prm.outs[p] = outs[p];
-        prm.item_start[p] = items;
-        prm.nseg[p] = spatial[p] > 0 ? (spatial[p] + seg - 1) / seg : 1;
-        if (spatial[p] > 0) items += N * C * prm.nseg[p];
+    if (N > 0) {
+        TB_TRY(gn_grad_tasks(prm, tb::GRAD_STATS, dtype, sms));
+        TB_TRY(launched(tb::launch_gn_grad(prm, (int)dtype, ring, sms, s)));
     }
-    prm.item_start[P] = items;
-    prm.seg = (int32_t)seg;
-    prm.dgamma = dgamma;
-    prm.dbeta = dbeta;
-    prm.wblocks = dgamma != nullptr || dbeta != nullptr ? (int32_t)((C + 7) / 8) : 0;
-    if (items + prm.wblocks == 0) return TB_OK;
-    if (items + prm.wblocks > 2147483647LL) return TB_ERR_UNSUPPORTED;
-    return launched(tb::launch_gn_grad_apply(prm, (int)dtype, items, reinterpret_cast<cudaStream_t>(stream)));
+    TB_TRY(gn_grad_tasks(prm, tb::GRAD_APPLY, dtype, sms));
+    return launched(tb::launch_gn_grad(prm, (int)dtype, ring, sms, s));
 }

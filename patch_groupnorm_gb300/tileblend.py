@@ -157,6 +157,9 @@ _lib.tb_patch_gn_grad_stats.argtypes = [_P_vp, _P_vp, _i32, ctypes.c_int, _i64, 
 _lib.tb_patch_gn_grad_apply.restype = ctypes.c_int
 _lib.tb_patch_gn_grad_apply.argtypes = [_P_vp, _P_vp, _P_vp, _i32, ctypes.c_int, _i64, _i64, _P_i64, _i32, _vp, _vp,
                                         _i32, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp]
+_lib.tb_patch_gn_backward.restype = ctypes.c_int
+_lib.tb_patch_gn_backward.argtypes = [_P_vp, _P_vp, _P_vp, _i32, ctypes.c_int, _i64, _i64, _P_i64, _i32, _vp, _vp, _vp,
+                                      ctypes.c_float, _i32, _vp, _vp, _vp, _vp]
 TB_LN_PARTS = 512
 TB_MAX_GRADS, TB_GRAD_TABLE, TB_GRAD_PARTS = 65536, 1024, 1024
 
@@ -167,7 +170,7 @@ EXPORTED = ("tb_version", "tb_status_string", "tb_last_cuda_error", "tb_axis_lay
             "tb_gather_patches", "tb_device_status", "tb_ramp_axis_spread", "tb_stitch_shard_frames_layout",
             "tb_stitch_halo_pack_frames", "tb_stitch3d_shard_frames", "tb_layer_norm", "tb_layer_norm_workspace",
             "tb_layer_norm_backward", "tb_grad_records", "tb_grad_stats", "tb_grad_norm", "tb_grad_clip",
-            "tb_patch_gn_grad_stats", "tb_patch_gn_grad_apply")
+            "tb_patch_gn_grad_stats", "tb_patch_gn_grad_apply", "tb_patch_gn_backward")
 
 
 class TileBlendError(RuntimeError):
@@ -1057,30 +1060,53 @@ def new_grad_partials(P: int, N: int, C: int, device=None) -> torch.Tensor:
     return torch.empty((P, N, C, TB_GN_PARTS, 2), dtype=torch.float32, device=device or torch.device("cuda"))
 
 
+_PTRS = {n: ctypes.c_void_p * n for n in range(1, 65)}
+_COUNTS = {n: ctypes.c_int64 * n for n in range(1, 65)}
+
+
+def _like_patches(ts, patches, what: str):
+    """Addresses of one tensor per patch, each like its patch."""
+    P = len(patches)
+    if len(ts) != P:
+        raise ValueError("one %s per patch" % what)
+    for q in range(P):
+        t, x = ts[q], patches[q]
+        if t.shape != x.shape or t.dtype is not x.dtype or t.get_device() != x.get_device() or not t.is_contiguous():
+            raise ValueError("%s %d must be contiguous and match patch %d" % (what, q, q))
+    return _PTRS[P](*[t.data_ptr() for t in ts])
+
+
 def _gn_grad_args(grads, patches, G, partials, R, gamma, beta):
-    N, C, dt, spatial, ptrs = _gn_args(patches)
-    if len(grads) != len(patches):
-        raise ValueError("one gradient per patch")
-    gptrs = []
-    for q, (d, t) in enumerate(zip(grads, patches)):
-        _cuda_contig(d, "gradient %d" % q)
-        if d.shape != t.shape or d.dtype != t.dtype:
-            raise ValueError("gradient %d must match patch %d" % (q, q))
-        gptrs.append(d.data_ptr())
-    for name, v in (("gamma", gamma), ("beta", beta)):
-        if v is not None:
-            _cuda_contig(v, name)
-            if v.numel() != C or v.dtype != patches[0].dtype:
-                raise ValueError("%s must be [C] of the patches' dtype" % name)
-    _cuda_contig(partials, "partials")
-    if partials.numel() * partials.element_size() != R * N * G * TB_GN_PARTS * 16:
+    P = len(patches)
+    if not 1 <= P <= 64:
+        raise ValueError("1 to 64 patches")
+    first = patches[0]
+    dt, dev = first.dtype, first.get_device()
+    N, C = first.shape[:2]
+    spatial = []
+    for q, x in enumerate(patches):
+        if x.get_device() != dev or dev < 0 or not x.is_contiguous():
+            raise ValueError("patch %d must be a contiguous CUDA tensor, on the device of patch 0" % q)
+        if x.dtype is not dt or x.shape[0] != N or x.shape[1] != C:
+            raise ValueError("patch %d: dtype/leading dims differ from patch 0" % q)
+        spatial.append(x.numel() // (N * C) if N * C else 0)
+    xs = _PTRS[P](*[x.data_ptr() for x in patches])
+    ds = _like_patches(grads, patches, "gradient")
+    _vec(gamma, C, dt, dev, "gamma")
+    _vec(beta, C, dt, dev, "beta")
+    if partials.get_device() != dev or not partials.is_contiguous() or \
+            partials.numel() * partials.element_size() != R * N * G * TB_GN_PARTS * 16:
         raise ValueError("partials must hold R*N*G*TB_GN_PARTS 16-byte records")
-    return N, C, dt, (ctypes.c_int64 * len(spatial))(*spatial), _ptr_array(ptrs), _ptr_array(gptrs)
+    return N, C, _dtype_code(first), _COUNTS[P](*spatial), xs, ds
+
+
+def _gn_grad_outs(dxs, patches, C, dgamma, dbeta):
+    dt, dev = patches[0].dtype, patches[0].get_device()
+    return _like_patches(dxs, patches, "dx"), _vec(dgamma, C, dt, dev, "dgamma"), _vec(dbeta, C, dt, dev, "dbeta")
 
 
 def _grad_partials(t: torch.Tensor, R: int, N: int, C: int) -> int:
-    _cuda_contig(t, "grad_partials")
-    if t.numel() * t.element_size() != R * N * C * TB_GN_PARTS * 8:
+    if t.get_device() < 0 or not t.is_contiguous() or t.numel() * t.element_size() != R * N * C * TB_GN_PARTS * 8:
         raise ValueError("grad_partials must hold R*N*C*TB_GN_PARTS 8-byte records")
     return t.data_ptr()
 
@@ -1098,8 +1124,8 @@ def tb_patch_gn_grad_stats(grads: Sequence[torch.Tensor], patches: Sequence[torc
     _check(_lib.tb_patch_gn_grad_stats(xs, ds, P, dt, N, C, sp, G, partials.data_ptr(), R,
                                        gamma.data_ptr() if gamma is not None else None,
                                        beta.data_ptr() if beta is not None else None, float(eps), 1 if silu else 0,
-                                       _grad_partials(grad_partials, P, N, C), _stream_handle(stream)),
-           "tb_patch_gn_grad_stats")
+                                       _grad_partials(grad_partials, P, N, C),
+                                       _stream_of(stream, patches[0].get_device())), "tb_patch_gn_grad_stats")
     return grad_partials
 
 
@@ -1114,24 +1140,30 @@ def tb_patch_gn_grad_apply(grads: Sequence[torch.Tensor], patches: Sequence[torc
     passes."""
     N, C, dt, sp, xs, ds = _gn_grad_args(grads, patches, G, partials, R, gamma, beta)
     P = len(patches)
-    if len(dxs) != P:
-        raise ValueError("one output per patch")
-    for q, (o, t) in enumerate(zip(dxs, patches)):
-        _cuda_contig(o, "dx %d" % q)
-        if o.shape != t.shape or o.dtype != t.dtype:
-            raise ValueError("dx %d must match patch %d" % (q, q))
-    wp = []
-    for name, v in (("dgamma", dgamma), ("dbeta", dbeta)):
-        if v is not None:
-            _cuda_contig(v, name)
-            if v.numel() != C or v.dtype != patches[0].dtype:
-                raise ValueError("%s must be [C] of the patches' dtype" % name)
-        wp.append(v.data_ptr() if v is not None else None)
-    _check(_lib.tb_patch_gn_grad_apply(xs, ds, _ptr_array([o.data_ptr() for o in dxs]), P, dt, N, C, sp, G,
+    os_, gp, bp = _gn_grad_outs(dxs, patches, C, dgamma, dbeta)
+    _check(_lib.tb_patch_gn_grad_apply(xs, ds, os_, P, dt, N, C, sp, G,
                                        partials.data_ptr(), _grad_partials(grad_partials, R, N, C), R,
                                        gamma.data_ptr() if gamma is not None else None,
                                        beta.data_ptr() if beta is not None else None, float(eps), 1 if silu else 0,
-                                       wp[0], wp[1], _stream_handle(stream)), "tb_patch_gn_grad_apply")
+                                       gp, bp, _stream_of(stream, patches[0].get_device())),
+           "tb_patch_gn_grad_apply")
+    return dxs
+
+
+def tb_patch_gn_backward(grads: Sequence[torch.Tensor], patches: Sequence[torch.Tensor], dxs: Sequence[torch.Tensor],
+                         G: int, partials: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor],
+                         eps: float, dgamma: Optional[torch.Tensor], dbeta: Optional[torch.Tensor],
+                         grad_partials: torch.Tensor, silu: bool = True, stream=None) -> Sequence[torch.Tensor]:
+    """Both steps in one pass for patches that are all here;
+    ``grad_partials`` (from ``new_grad_partials``) is its workspace."""
+    P = len(patches)
+    N, C, dt, sp, xs, ds = _gn_grad_args(grads, patches, G, partials, P, gamma, beta)
+    os_, gp, bp = _gn_grad_outs(dxs, patches, C, dgamma, dbeta)
+    _check(_lib.tb_patch_gn_backward(xs, ds, os_, P, dt, N, C, sp, G, partials.data_ptr(),
+                                     gamma.data_ptr() if gamma is not None else None,
+                                     beta.data_ptr() if beta is not None else None, eps, 1 if silu else 0, gp, bp,
+                                     _grad_partials(grad_partials, P, N, C),
+                                     _stream_of(stream, patches[0].get_device())), "tb_patch_gn_backward")
     return dxs
 
 
@@ -1155,9 +1187,7 @@ def patch_group_norm_backward(grads: Sequence[torch.Tensor], patches: Sequence[t
                 torch.empty_like(w[0]) if dgamma is None else dgamma,
                 torch.empty_like(w[1]) if dbeta is None else dbeta,
                 new_grad_partials(P, N, C, patches[0].device) if grad_partials is None else grad_partials)
-    dxs, dgamma, dbeta, grad_partials = _on_stream(make, stream)
-    handle = _stream_handle(stream)
-    tb_patch_gn_grad_stats(grads, patches, G, partials, P, gamma, beta, eps, grad_partials, silu, handle)
-    tb_patch_gn_grad_apply(grads, patches, dxs, G, partials, grad_partials, P, gamma, beta, eps, dgamma, dbeta, silu,
-                           handle)
+    if dxs is None or dgamma is None or dbeta is None or grad_partials is None:
+        dxs, dgamma, dbeta, grad_partials = _on_stream(make, stream)
+    tb_patch_gn_backward(grads, patches, dxs, G, partials, gamma, beta, eps, dgamma, dbeta, grad_partials, silu, stream)
     return dxs, dgamma, dbeta

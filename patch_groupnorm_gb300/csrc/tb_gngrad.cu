@@ -21,10 +21,13 @@
 // always been started, whatever else occupies the GPU.
 //
 // One CTA per SM: 16 warps compute, a 17th takes the tasks and copies their
-// rows into a ring of three stages in shared memory (64 KB each: x and dy),
-// with the unit's and the rows' constants.  Bulk copies move whole 16-byte
-// words; the elements before the first and after the last boundary are copied
-// one by one, so rows of any length and offset take this path.
+// rows into a ring of three stages in shared memory (64 KB each: x and dy), and
+// each stage has a warp that finds the unit's and the rows' constants (chains
+// of dependent loads of about three times a stage's computing time: one warp
+// for all stages held the whole kernel up, 126 us of 4D against 84 of two
+// plain launches).  Bulk copies move whole 16-byte words; the elements before
+// the first and after the last boundary are copied one by one, so rows of any
+// length and offset take this path.
 #include "tb_elem.cuh"
 #include "tb_groupnorm.cuh"
 
@@ -33,8 +36,8 @@ namespace {
 
 constexpr int GG_WARPS = 16;
 constexpr int GG_THREADS = GG_WARPS * 32;
-constexpr int GG_BLOCK = GG_THREADS + 32;
 constexpr int GG_STAGES = 3;
+constexpr int GG_BLOCK = GG_THREADS + 32 * (1 + GG_STAGES);  // + the copying warp, and a warp of constants per stage
 constexpr int GG_TENSOR = GRAD_STAGE_BYTES + 128;  // room for a first, partial word
 constexpr int GG_SMEM = GG_STAGES * 2 * GG_TENSOR;
 static_assert(GG_SMEM <= 216 * 1024, "ring too large");
@@ -50,7 +53,8 @@ struct Stage {
     int32_t last;        // TASK_STATS: the part ends with this stage
     int32_t slot;        // TASK_STATS: the part's record slot
     int64_t record;      // TASK_STATS: row index p * N * C + n * C + c of the first row; TASK_WEIGHTS: channel
-    int64_t unit;        // TASK_STATS: the unit, whose arrival counter is raised
+    int64_t unit;
+    int64_t channel;     // of the first row
     char* out;           // TASK_APPLY: address of the first element
     float mean, rstd;
     float u, v;          // TASK_APPLY: dx = dz * rstd * gamma + (x - mean) * u + v
@@ -66,28 +70,33 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Arrival counter of a unit, and the task counter (GRAD_BOTH).
-__device__ __forceinline__ uint32_t* unit_counter(const GnGradParams& p, int64_t unit) {
+// What a GRAD_BOTH launch keeps of a unit, in the last two record slots of the
+// unit's first row.
+struct Unit {
+    uint32_t arrived;  // record tasks done
+    uint32_t tasks;    // of unit 0: tasks handed out
+    float mean, rstd;
+};
+static_assert(sizeof(Unit) == 2 * sizeof(float2) && GRAD_BOTH_PARTS == TB_GN_PARTS - 2, "two record slots");
+__device__ __forceinline__ Unit* unit_at(const GnGradParams& p, int64_t unit) {
     const int64_t n = unit / p.G, g = unit - n * p.G;
-    return reinterpret_cast<uint32_t*>(p.grad_partials + (n * p.C + g * (p.C / p.G)) * TB_GN_PARTS + TB_GN_PARTS - 1);
-}
-__device__ __forceinline__ uint32_t* task_counter(const GnGradParams& p) {
-    return reinterpret_cast<uint32_t*>(p.grad_partials + TB_GN_PARTS - 2);
+    return reinterpret_cast<Unit*>(p.grad_partials + (n * p.C + g * (p.C / p.G)) * TB_GN_PARTS + GRAD_BOTH_PARTS);
 }
 
-// Zeroes the counters of a GRAD_BOTH launch.
-__global__ void __launch_bounds__(256) gn_grad_zero_kernel(const __grid_constant__ GnGradParams p) {
+// Before a GRAD_BOTH launch: counters zero, every unit's mean and rstd.
+__global__ void __launch_bounds__(128) gn_grad_units_kernel(const __grid_constant__ GnGradParams p) {
     pdl_trigger_dependents();
     grid_wait();
-    const int64_t unit = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (unit < p.N * p.G) *unit_counter(p, unit) = 0u;
-    if (unit == 0) *task_counter(p) = 0u;
+    const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (unit >= p.N * p.G) return;
+    float mean, rstd, count;
+    pooled_stats(p, unit / p.G, unit % p.G, mean, rstd, count);
+    if ((threadIdx.x & 31) == 0) *unit_at(p, unit) = Unit{0u, 0u, mean, rstd};
 }
 
-// dz of one pair of elements (see the top of this file).  The two
-// reciprocals share one approximate rcp: 1/a = b * (1 / ab).  e^-z is held
-// below 2^60 to keep ab finite: there s is below 1e-18, and dz is too small
-// beside dy (at most 1e-16 of it) for any sum or rounding to see.
+// dz of one pair of elements (see the top of this file).  e^-z and the
+// reciprocal are approximate (2^-22 each); e^-z overflows for z < -88, where
+// s = 0 and dz = 0 (its true size is below 1e-36 of dy).
 template <bool SILU>
 __device__ __forceinline__ f32x2 dz_pair(f32x2 u, f32x2 dy, f32x2 za, f32x2 zb) {
     if constexpr (SILU) {
@@ -95,20 +104,23 @@ __device__ __forceinline__ f32x2 dz_pair(f32x2 u, f32x2 dy, f32x2 za, f32x2 zb) 
         const f32x2 z = vfma(u, za, zb);
         float tl, th, al, ah;
         halves(vmul(z, pair(-1.4426950408889634f, -1.4426950408889634f)), tl, th);
-        halves(vadd(pair(ex2_ftz(fminf(tl, 60.f)), ex2_ftz(fminf(th, 60.f))), one), al, ah);
-        const float r = rcp_ftz(al * ah);
-        const f32x2 s = vmul(pair(ah, al), pair(r, r));
+        halves(vadd(pair(ex2_ftz(tl), ex2_ftz(th)), one), al, ah);
+        const f32x2 s = pair(rcp_ftz(al), rcp_ftz(ah));
         return vmul(dy, vmul(s, vfma(z, vsub(one, s), one)));
     } else {
         return dy;
     }
 }
 
-// --- the 17th warp --------------------------------------------------------------
+// --- the ring -------------------------------------------------------------------
 
 struct Ring {
     Stage* stage;
-    uint32_t full, empty, sums, data;  // shared addresses: mbarriers, first stage's rows
+    // shared addresses: mbarriers (a stage's task is set; its rows and
+    // constants are there; the computing warps are done with it; their sums of
+    // one part are there) and the first stage's rows.  All are per stage: a
+    // warp may be two stages ahead of another
+    uint32_t task, full, empty, sums, data;
     volatile int* dead;          // a wait ran out: everyone leaves
     int s = 0;
     uint32_t parity = 0;
@@ -120,15 +132,9 @@ struct Ring {
     }
 };
 
-// A unit's constants as the copying warp last computed them.
-struct UnitCache {
-    int64_t unit = -1;
-    float mean = 0.f, rstd = 0.f, u = 0.f, v = 0.f;
-};
-
 // Waits until the counter of `unit` reaches the unit's tasks.
 __device__ __forceinline__ bool wait_unit(const GnGradParams& p, int64_t unit) {
-    const uint32_t* const at = unit_counter(p, unit);
+    const uint32_t* const at = &unit_at(p, unit)->arrived;
     const uint32_t want = (uint32_t)p.unit_tasks;
     if (ld_acquire(at) >= want) return true;
     const uint64_t t0 = timer_ns();
@@ -161,26 +167,70 @@ __device__ __forceinline__ float2 group_sums(const GnGradParams& p, int dtype, i
     return make_float2(warp_sum(B), warp_sum(A));
 }
 
-// The unit's constants in `c`; false if its records do not arrive.
-__device__ __forceinline__ bool unit_constants(const GnGradParams& p, int dtype, int kind, int64_t unit, UnitCache& c) {
-    if (c.unit == unit) return true;
-    const int64_t n = unit / p.G, g = unit - n * p.G;
-    float mean, rstd, count;
-    pooled_stats(p, n, g, mean, rstd, count);
-    c.mean = __shfl_sync(0xffffffffu, mean, 0);
-    c.rstd = __shfl_sync(0xffffffffu, rstd, 0);
-    count = __shfl_sync(0xffffffffu, count, 0);
-    if (kind == TASK_APPLY) {
-        if (p.mode == GRAD_BOTH) {
-            const bool ok = wait_unit(p, unit);
-            if (__any_sync(0xffffffffu, !ok)) return false;
+// The warp of stage `s`: for every task that comes through the stage, the
+// unit's and the rows' constants.
+__device__ __forceinline__ void constants_loop(const GnGradParams& p, int dtype, Ring ring, int s) {
+    const int lane = threadIdx.x & 31;
+    const bool both = p.mode == GRAD_BOTH;
+    Stage& d = ring.stage[s];
+    const uint32_t full = ring.full + s * 8u;
+    const float count_here = both ? p.count : 0.f;
+    for (uint32_t parity = 0;; parity ^= 1u) {
+        bool ok = bar_wait(ring.task + s * 8u, parity, p.status);
+        if (__any_sync(0xffffffffu, !ok) || *ring.dead) {
+            if (lane == 0) *ring.dead = 1;
+            return;
         }
-        const float2 sums = group_sums(p, dtype, n, g);
-        c.v = -sums.x / count * c.rstd;
-        c.u = -sums.y / count * c.rstd * c.rstd;
+        const int kind = d.kind;
+        if (kind == TASK_END) {
+            if (lane == 0) bar_arrive(full);
+            return;
+        }
+        if (kind == TASK_WEIGHTS) {
+            if (both) {
+                const int K = (int)(p.C / p.G);
+                const int64_t c0 = d.channel, c1 = min(p.C, c0 + GRAD_CHANNELS);
+                for (int64_t n = 0; n < p.N; ++n)
+                    for (int64_t g = c0 / K; g <= (c1 - 1) / K; ++g) ok = ok && wait_unit(p, n * p.G + g);
+            }
+        } else {
+            const int64_t unit = d.unit, n = unit / p.G, g = unit - n * p.G;
+            const int rows = d.rows;
+            const int64_t ch = d.channel + lane;
+            const float gamma = lane < rows ? weight_at(p.gamma, dtype, ch, 1.f) : 0.f;
+            const float beta = lane < rows ? weight_at(p.beta, dtype, ch, 0.f) : 0.f;
+            float mean, rstd, count;
+            if (both) {
+                const Unit* const at = unit_at(p, unit);
+                mean = at->mean;
+                rstd = at->rstd;
+                count = count_here;
+                if (kind == TASK_APPLY) ok = wait_unit(p, unit);
+            } else {
+                pooled_stats(p, n, g, mean, rstd, count);
+                mean = __shfl_sync(0xffffffffu, mean, 0);
+                rstd = __shfl_sync(0xffffffffu, rstd, 0);
+                count = __shfl_sync(0xffffffffu, count, 0);
+            }
+            float2 sums = make_float2(0.f, 0.f);
+            if (kind == TASK_APPLY) {
+                __syncwarp();
+                sums = group_sums(p, dtype, n, g);
+            }
+            if (lane < rows) d.row[lane] = make_float2(rstd * gamma, beta);
+            if (lane == 0) {
+                d.mean = mean;
+                d.rstd = rstd;
+                d.v = -sums.x / count * rstd;
+                d.u = -sums.y / count * rstd * rstd;
+            }
+        }
+        if (__any_sync(0xffffffffu, !ok)) {
+            if (lane == 0) *ring.dead = 1;
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(full);
     }
-    c.unit = unit;
-    return true;
 }
 
 // Copies elements [first, first + count) of `base` into the stage's buffer at
@@ -228,14 +278,13 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
     const int64_t lag = p.lag;
     const bool both = p.mode == GRAD_BOTH;
     const int64_t body = (both ? 2 : 1) * units * T, total = body + p.wtasks;
-    UnitCache cache[2];  // of TASK_STATS and TASK_APPLY
     bool ok = true;
     // GRAD_BOTH: tasks in order from the counter, the next one asked for while
     // this one is copied; otherwise no task waits for another
     uint32_t next = blockIdx.x;
     auto ask = [&]() {
         if (!both) next += gridDim.x;
-        else if (lane == 0) next = atomicAdd(task_counter(p), 1u);
+        else if (lane == 0) next = atomicAdd(&unit_at(p, 0)->tasks, 1u);
     };
     if (both) ask();
     auto claim = [&]() -> bool {  // the ring's next stage, once the computing warps are done with it
@@ -252,19 +301,14 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
         if (task >= body) {
             kind = TASK_WEIGHTS;
             const int64_t c0 = (task - body) * GRAD_CHANNELS;
-            const int64_t c1 = min(p.C, c0 + GRAD_CHANNELS);
-            if (both) {
-                for (int64_t n = 0; n < p.N; ++n)
-                    for (int64_t g = c0 / K; g <= (c1 - 1) / K; ++g) ok = ok && wait_unit(p, n * p.G + g);
-                if (__any_sync(0xffffffffu, !ok)) break;
-            }
             if (!claim()) break;
             Stage& d = ring.stage[ring.s];
             if (lane == 0) {
                 d.kind = kind;
-                d.record = c0;
+                d.channel = c0;
+                bar_arrive(ring.full + ring.s * 8u);  // (no copies)
                 bar_arrive(ring.full + ring.s * 8u);
-                bar_arrive(ring.full + ring.s * 8u);
+                bar_arrive(ring.task + ring.s * 8u);
             }
             ring.next();
             continue;
@@ -324,14 +368,6 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
             const int64_t first = row * S + at, count = rows * len;
             if (lane == 0)
                 bar_expect(bar, bulk_bytes(p.patches[pp], first, count, ES) + bulk_bytes(p.grads[pp], first, count, ES));
-            copy_rows<DT>(p.patches[pp], first, count, dst, bar, lane == 0);
-            copy_rows<DT>(p.grads[pp], first, count, dst + GG_TENSOR, bar, lane == 0);
-            UnitCache& c = cache[kind];
-            ok = unit_constants(p, DT, kind, unit, c);
-            if (lane < rows) {
-                const int64_t ch = g * K + c_first + lane;
-                d.row[lane] = make_float2(c.rstd * weight_at(p.gamma, DT, ch, 1.f), weight_at(p.beta, DT, ch, 0.f));
-            }
             if (lane == 0) {
                 d.kind = kind;
                 d.rows = rows;
@@ -341,15 +377,14 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
                 d.slot = part;
                 d.record = pp * p.N * p.C + row;
                 d.unit = unit;
+                d.channel = g * K + c_first;
                 d.out = reinterpret_cast<char*>(p.outs[pp]) + first * ES;
-                d.mean = c.mean;
-                d.rstd = c.rstd;
-                d.u = c.u;
-                d.v = c.v;
+                bar_arrive(ring.task + ring.s * 8u);
             }
-            if (!ok && lane == 0) *ring.dead = 1;
+            copy_rows<DT>(p.patches[pp], first, count, dst, bar, lane == 0);
+            copy_rows<DT>(p.grads[pp], first, count, dst + GG_TENSOR, bar, lane == 0);
             __syncwarp();
-            if (lane == 0) bar_arrive(bar);
+            if (lane == 0) bar_arrive(bar);  // the elements copied one by one
             ring.next();
         }
         if (!ok) break;
@@ -362,12 +397,16 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
             bar_wait(ring.full + k * 8u, k < ring.s ? ring.parity : ring.parity ^ 1u, p.status);
         return;
     }
-    const bool idle = bar_wait(ring.empty + ring.s * 8u, ring.parity ^ 1u, p.status);
-    if (idle && lane == 0) {
-        ring.stage[ring.s].kind = TASK_END;
-        bar_arrive(ring.full + ring.s * 8u);
-        bar_arrive(ring.full + ring.s * 8u);
+    for (int k = 0; k < GG_STAGES && claim(); ++k) {  // each stage's warp must see it
+        if (lane == 0) {
+            ring.stage[ring.s].kind = TASK_END;
+            bar_arrive(ring.full + ring.s * 8u);
+            bar_arrive(ring.full + ring.s * 8u);
+            bar_arrive(ring.task + ring.s * 8u);
+        }
+        ring.next();
     }
+    if (!ok && lane == 0) *ring.dead = 1;
 }
 
 // --- the computing warps ----------------------------------------------------------
@@ -379,7 +418,7 @@ __device__ __forceinline__ void compute_loop(const GnGradParams& p, Ring ring, f
     constexpr int NP = VEC / 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     f32x2 B = 0ull, A = 0ull;  // 0ull: a pair of zeros
-    uint32_t sums_parity = 0;
+    uint32_t sums_parity = 0;  // a bit per stage
     while (true) {
         const bool here = bar_wait(ring.full + ring.s * 8u, ring.parity, p.status);
         if (!here && lane == 0) *ring.dead = 1;
@@ -390,7 +429,7 @@ __device__ __forceinline__ void compute_loop(const GnGradParams& p, Ring ring, f
         if (kind == TASK_END) return;
         if (kind == TASK_WEIGHTS) {
             // a warp per channel adds up its records of all samples and sets
-            const int64_t c = d.record + warp;
+            const int64_t c = d.channel + warp;
             if (c < p.C) {
                 const bool both = p.mode == GRAD_BOTH;
                 const int64_t most = (int64_t)(both ? p.P : p.R) * p.N * TB_GN_PARTS;
@@ -494,10 +533,10 @@ __device__ __forceinline__ void compute_loop(const GnGradParams& p, Ring ring, f
         if (kind == TASK_STATS && d.last) {
             // the row groups' sums meet; warp 0 writes the records
             __syncwarp();
-            if (lane == 0) bar_arrive(ring.sums);
+            if (lane == 0) bar_arrive(ring.sums + ring.s * 8u);
             if (warp == 0) {
-                const bool met = bar_wait(ring.sums, sums_parity, p.status);
-                sums_parity ^= 1u;
+                const bool met = bar_wait(ring.sums + ring.s * 8u, (sums_parity >> ring.s) & 1u, p.status);
+                sums_parity ^= 1u << ring.s;
                 if (!met && lane == 0) *ring.dead = 1;
                 if (__any_sync(0xffffffffu, !met)) return;
                 for (int r = lane; r < rows; r += 32) {
@@ -518,7 +557,7 @@ __device__ __forceinline__ void compute_loop(const GnGradParams& p, Ring ring, f
                 __syncwarp();
                 if (lane == 0 && p.mode == GRAD_BOTH) {
                     __threadfence();
-                    atomicAdd(unit_counter(p, d.unit), 1u);
+                    atomicAdd(&unit_at(p, d.unit)->arrived, 1u);
                 }
             }
         }
@@ -533,28 +572,31 @@ __global__ void __launch_bounds__(GG_BLOCK, 1) gn_grad_kernel(const __grid_const
     extern __shared__ __align__(128) unsigned char s_data[];
     __shared__ Stage s_stage[GG_STAGES];
     __shared__ float2 s_slots[GG_STAGES][2 * GG_WARPS];
-    __shared__ __align__(8) unsigned long long s_bar[2 * GG_STAGES + 1];
+    __shared__ __align__(8) unsigned long long s_bar[4 * GG_STAGES];
     __shared__ int s_dead;
     Ring ring;
     ring.stage = s_stage;
     ring.full = smem_addr(s_bar);
     ring.empty = ring.full + GG_STAGES * 8u;
-    ring.sums = ring.empty + GG_STAGES * 8u;
+    ring.task = ring.empty + GG_STAGES * 8u;
+    ring.sums = ring.task + GG_STAGES * 8u;
     ring.data = smem_addr(s_data);
     ring.dead = &s_dead;
     if (threadIdx.x == 0) {
         s_dead = 0;
         for (int k = 0; k < GG_STAGES; ++k) {
-            bar_init(ring.full + k * 8u, 2);        // the copies' bytes, and the constants
+            bar_init(ring.task + k * 8u, 1);
+            bar_init(ring.full + k * 8u, 3);  // the copies' bytes, the single elements, the constants
             bar_init(ring.empty + k * 8u, GG_WARPS);
+            bar_init(ring.sums + k * 8u, GG_WARPS);
         }
-        bar_init(ring.sums, GG_WARPS);  // the warps' sums of one part
         bar_init_fence();
     }
     __syncthreads();
     grid_wait();
-    if (threadIdx.x >= GG_THREADS) copy_loop<DT>(p, ring);
-    else compute_loop<DT, SILU>(p, ring, s_slots);
+    if (threadIdx.x < GG_THREADS) compute_loop<DT, SILU>(p, ring, s_slots);
+    else if (threadIdx.x < GG_THREADS + 32) copy_loop<DT>(p, ring);
+    else constants_loop(p, DT, ring, (int)(threadIdx.x - GG_THREADS) / 32 - 1);
     __syncthreads();  // (no warp's memory goes before the copies have landed)
 }
 
@@ -668,7 +710,7 @@ cudaError_t grad_launch(const GnGradParams& p, bool ring, int sms, cudaStream_t 
         const int64_t tasks = (p.mode == GRAD_BOTH ? 2 : 1) * p.N * p.G * (int64_t)p.unit_tasks + p.wtasks;
         if (tasks == 0) return cudaSuccess;
         if (p.mode == GRAD_BOTH) {
-            const cudaError_t e = launch_pdl(gn_grad_zero_kernel, p, dim3((unsigned)((p.N * p.G + 255) / 256)), 256, 0, s);
+            const cudaError_t e = launch_pdl(gn_grad_units_kernel, p, dim3((unsigned)((p.N * p.G + 3) / 4)), 128, 0, s);
             if (e != cudaSuccess) return e;
         }
         cudaError_t e = cudaFuncSetAttribute(gn_grad_kernel<DT, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize, GG_SMEM);

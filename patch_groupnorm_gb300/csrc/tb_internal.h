@@ -446,6 +446,7 @@ struct GnGradParams {
     int32_t mode;
     float eps;
     int32_t silu;
+    float count;                   // elements of a group in all patches (GRAD_BOTH)
     uint32_t* status;              // device status word (a wait that runs out is recorded there)
     // The ring kernel's work: every group of every sample (a unit) is cut into
     // unit_tasks tasks, patch p's being task_start[p] .. task_start[p + 1] - 1:
@@ -462,8 +463,8 @@ static_assert(sizeof(GnGradParams) <= 32000, "kernel parameter block too large")
 constexpr int GRAD_STAGE_BYTES = 32768;  // of x, and of dy, in one ring stage
 constexpr int GRAD_MAX_ROWS = 31;        // channel rows of one task
 constexpr int GRAD_CHANNELS = 16;        // channels of one weight-gradient task
-// GRAD_BOTH keeps the units' arrival counters and the task counter in the
-// last two record slots of a row, so it cuts rows into fewer parts.
+// GRAD_BOTH keeps the units' counters and statistics in the last two record
+// slots of their first rows, so it cuts rows into fewer parts.
 constexpr int GRAD_BOTH_PARTS = TB_GN_PARTS - 2;
 
 // ring: patches, gradients and outputs share their offset from 16-byte

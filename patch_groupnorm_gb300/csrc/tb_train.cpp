@@ -164,7 +164,7 @@ tb_status gn_grad_params(tb::GnGradParams& prm, bool* ring, const void* const* p
     if (N > 0 && C > 0 && (partials == nullptr || grad_partials == nullptr)) return TB_ERR_NULL;
     if (!aligned(gamma, es) || !aligned(beta, es) || !aligned(dgamma, es) || !aligned(dbeta, es))
         return TB_ERR_UNSUPPORTED;
-    if (!aligned(partials, 16) || !aligned(grad_partials, 8)) return TB_ERR_UNSUPPORTED;
+    if (!aligned(partials, 16) || !aligned(grad_partials, 16)) return TB_ERR_UNSUPPORTED;
     prm.partials = reinterpret_cast<const tb::GnPartial*>(partials);
     prm.grad_partials = reinterpret_cast<float2*>(const_cast<void*>(grad_partials));
     prm.gamma = gamma;
@@ -191,6 +191,9 @@ tb_status gn_grad_tasks(tb::GnGradParams& prm, int mode, tb_dtype dtype, int sms
     const int64_t K = prm.C / prm.G, units = prm.N * prm.G;
     const int most_parts = mode == tb::GRAD_BOTH ? tb::GRAD_BOTH_PARTS : TB_GN_PARTS;
     prm.mode = mode;
+    double count = 0.0;
+    for (int p = 0; p < prm.P; ++p) count += (double)K * (double)prm.spatial[p];
+    prm.count = (float)count;
     for (int p = 0; p < prm.P; ++p) {
         const int64_t row = prm.spatial[p] * es;
         prm.rows[p] = prm.parts[p] = 0;

@@ -673,6 +673,22 @@ def test_groupnorm_backward_is_deterministic(tbl):
     assert torch.equal(a[0][0], b[0][0]) and torch.equal(a[1], b[1]) and torch.equal(a[2], b[2])
 
 
+def test_groupnorm_backward_over_many_passes(tbl):
+    # warps of a CTA run apart by up to two stages of its ring: every pass must
+    # give the same bits, and no wait may run out
+    tbl.tb_device_status(clear=True)
+    x, dy = rows_of(1, (1, 48, 40, 1000), torch.bfloat16), rows_of(2, (1, 48, 40, 1000), torch.bfloat16)
+    gamma, beta = weights_of(3, 48, torch.bfloat16)
+    part = tbl.tb_patch_gn_stats([x], 16, tbl.new_partials(1, 1, 16))
+    first = None
+    for _ in range(600):
+        (dx,), dg, db = tbl.patch_group_norm_backward([dy], [x], 16, part, gamma, beta, 1e-6)
+        if first is None:
+            first = [t.clone() for t in (dx, dg, db)]
+        assert all(torch.equal(a, b) for a, b in zip(first, (dx, dg, db)))
+    assert tbl.tb_device_status() == tbl.TB_DEV_OK
+
+
 # --------------------------------------------------------------------------
 # streams and graphs
 # --------------------------------------------------------------------------

@@ -53,7 +53,8 @@ struct Stage {
     int32_t last;        // TASK_STATS: the part ends with this stage
     int32_t slot;        // TASK_STATS: the part's record slot
     int64_t record;      // TASK_STATS: row index p * N * C + n * C + c of the first row; TASK_WEIGHTS: channel
-    int64_t unit;
+    int32_t n, g;        // sample and group
+    int64_t unit;        // row index n * C + c of the group's first channel
     int64_t channel;     // of the first row
     char* out;           // TASK_APPLY: address of the first element
     float mean, rstd;
@@ -78,9 +79,9 @@ struct Unit {
     float mean, rstd;
 };
 static_assert(sizeof(Unit) == 2 * sizeof(float2) && GRAD_BOTH_PARTS == TB_GN_PARTS - 2, "two record slots");
-__device__ __forceinline__ Unit* unit_at(const GnGradParams& p, int64_t unit) {
-    const int64_t n = unit / p.G, g = unit - n * p.G;
-    return reinterpret_cast<Unit*>(p.grad_partials + (n * p.C + g * (p.C / p.G)) * TB_GN_PARTS + GRAD_BOTH_PARTS);
+// `row`: n * C + the group's first channel.
+__device__ __forceinline__ Unit* unit_at(const GnGradParams& p, int64_t row) {
+    return reinterpret_cast<Unit*>(p.grad_partials + row * TB_GN_PARTS + GRAD_BOTH_PARTS);
 }
 
 // Before a GRAD_BOTH launch: counters zero, every unit's mean and rstd.
@@ -91,7 +92,8 @@ __global__ void __launch_bounds__(128) gn_grad_units_kernel(const __grid_constan
     if (unit >= p.N * p.G) return;
     float mean, rstd, count;
     pooled_stats(p, unit / p.G, unit % p.G, mean, rstd, count);
-    if ((threadIdx.x & 31) == 0) *unit_at(p, unit) = Unit{0u, 0u, mean, rstd};
+    if ((threadIdx.x & 31) == 0)
+        *unit_at(p, unit / p.G * p.C + unit % p.G * (p.C / p.G)) = Unit{0u, 0u, mean, rstd};
 }
 
 // dz of one pair of elements (see the top of this file).  e^-z and the
@@ -132,9 +134,9 @@ struct Ring {
     }
 };
 
-// Waits until the counter of `unit` reaches the unit's tasks.
-__device__ __forceinline__ bool wait_unit(const GnGradParams& p, int64_t unit) {
-    const uint32_t* const at = &unit_at(p, unit)->arrived;
+// Waits until the counter of the unit with this first row reaches its tasks.
+__device__ __forceinline__ bool wait_unit(const GnGradParams& p, int64_t row) {
+    const uint32_t* const at = &unit_at(p, row)->arrived;
     const uint32_t want = (uint32_t)p.unit_tasks;
     if (ld_acquire(at) >= want) return true;
     const uint64_t t0 = timer_ns();
@@ -191,10 +193,10 @@ __device__ __forceinline__ void constants_loop(const GnGradParams& p, int dtype,
                 const int K = (int)(p.C / p.G);
                 const int64_t c0 = d.channel, c1 = min(p.C, c0 + GRAD_CHANNELS);
                 for (int64_t n = 0; n < p.N; ++n)
-                    for (int64_t g = c0 / K; g <= (c1 - 1) / K; ++g) ok = ok && wait_unit(p, n * p.G + g);
+                    for (int64_t g = c0 / K; g <= (c1 - 1) / K; ++g) ok = ok && wait_unit(p, n * p.C + g * K);
             }
         } else {
-            const int64_t unit = d.unit, n = unit / p.G, g = unit - n * p.G;
+            const int64_t unit = d.unit, n = d.n, g = d.g;
             const int rows = d.rows;
             const int64_t ch = d.channel + lane;
             const float gamma = lane < rows ? weight_at(p.gamma, dtype, ch, 1.f) : 0.f;
@@ -272,12 +274,12 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
     constexpr int ES = elem_size(DT);
     constexpr int VEC = 16 / ES;
     const int lane = threadIdx.x & 31;
-    const int64_t units = p.N * p.G;
-    const int64_t T = p.unit_tasks;
-    const int K = (int)(p.C / p.G);
-    const int64_t lag = p.lag;
+    // (the host keeps the tasks below 2^31: 32-bit divisions throughout, the
+    // 64-bit ones took longer than a task's copies)
+    const uint32_t G = (uint32_t)p.G, K = (uint32_t)(p.C / p.G), units = (uint32_t)p.N * G;
+    const uint32_t T = (uint32_t)p.unit_tasks, lag = (uint32_t)p.lag;
     const bool both = p.mode == GRAD_BOTH;
-    const int64_t body = (both ? 2 : 1) * units * T, total = body + p.wtasks;
+    const uint32_t body = (both ? 2u : 1u) * units * T, total = body + (uint32_t)p.wtasks;
     bool ok = true;
     // GRAD_BOTH: tasks in order from the counter, the next one asked for while
     // this one is copied; otherwise no task waits for another
@@ -293,14 +295,14 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
         return ok;
     };
     while (true) {
-        const int64_t task = __shfl_sync(0xffffffffu, next, 0);
+        const uint32_t task = __shfl_sync(0xffffffffu, next, 0);
         if (task >= total) break;
         ask();
         int kind;
-        int64_t unit = 0, item = 0;
+        uint32_t unit = 0, item = 0;
         if (task >= body) {
             kind = TASK_WEIGHTS;
-            const int64_t c0 = (task - body) * GRAD_CHANNELS;
+            const int64_t c0 = (int64_t)(task - body) * GRAD_CHANNELS;
             if (!claim()) break;
             Stage& d = ring.stage[ring.s];
             if (lane == 0) {
@@ -322,37 +324,39 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
             unit = task / T;
             item = task - unit * T;
         } else {
-            const int64_t q = task - lag * T, pairs = 2 * (units - lag) * T;
+            const uint32_t q = task - lag * T, pairs = 2u * (units - lag) * T;
             if (q < pairs) {
-                const int64_t block = q / (2 * T), r = q - block * 2 * T;
-                kind = (r & 1) ? TASK_APPLY : TASK_STATS;
-                unit = (r & 1) ? block : block + lag;
-                item = r >> 1;
+                const uint32_t block = (q >> 1) / T;
+                kind = (q & 1u) ? TASK_APPLY : TASK_STATS;
+                unit = (q & 1u) ? block : block + lag;
+                item = (q >> 1) - block * T;
             } else {
                 kind = TASK_APPLY;
-                unit = units - lag + (q - pairs) / T;
-                item = (q - pairs) % T;
+                const uint32_t block = (q - pairs) / T;
+                unit = units - lag + block;
+                item = q - pairs - block * T;
             }
         }
         // a unit's dx runs backwards: what was read last is the likeliest to be in L2
         if (kind == TASK_APPLY) item = T - 1 - item;
         int pp = 0;
-        while (p.task_start[pp + 1] <= item) ++pp;
-        item -= p.task_start[pp];
-        const int64_t n = unit / p.G, g = unit - n * p.G;
+        while ((uint32_t)p.task_start[pp + 1] <= item) ++pp;
+        item -= (uint32_t)p.task_start[pp];
+        const int64_t n = unit / G, g = unit - (uint32_t)n * G;
         const int64_t S = p.spatial[pp];
+        const uint32_t parts = (uint32_t)p.parts[pp];
         int rows, part = 0, c_first;  // c_first: first row, within the group
         int64_t e0, e1;               // element range within the row
-        if (p.parts[pp] > 1) {
-            c_first = (int)item / p.parts[pp];
-            part = (int)item - c_first * p.parts[pp];
+        if (parts > 1) {
+            c_first = (int)(item / parts);
+            part = (int)(item - (uint32_t)c_first * parts);
             rows = 1;
-            const int64_t words = S / VEC;
-            e0 = words * part / p.parts[pp] * VEC;
-            e1 = part + 1 == p.parts[pp] ? S : words * (part + 1) / p.parts[pp] * VEC;
+            const int64_t each = p.part_elems[pp];
+            e0 = part * each;
+            e1 = part + 1 == (int)parts ? S : e0 + each;
         } else {
             c_first = (int)item * p.rows[pp];
-            rows = min(p.rows[pp], K - c_first);
+            rows = min(p.rows[pp], (int)K - c_first);
             e0 = 0;
             e1 = S;
         }
@@ -376,7 +380,9 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
                 d.last = at + len >= e1;
                 d.slot = part;
                 d.record = pp * p.N * p.C + row;
-                d.unit = unit;
+                d.n = (int32_t)n;
+                d.g = (int32_t)g;
+                d.unit = n * p.C + g * K;
                 d.channel = g * K + c_first;
                 d.out = reinterpret_cast<char*>(p.outs[pp]) + first * ES;
                 bar_arrive(ring.task + ring.s * 8u);

@@ -453,6 +453,7 @@ struct GnGradParams {
     // rows[p] whole channel rows each, or parts[p] to a row where rows[p] is 1.
     int32_t rows[GN_MAXP];
     int32_t parts[GN_MAXP];
+    int64_t part_elems[GN_MAXP];   // elements of every part but the last
     int32_t task_start[GN_MAXP + 1];
     int32_t unit_tasks;
     int32_t lag;                   // GRAD_BOTH: units whose records run ahead of the first dx

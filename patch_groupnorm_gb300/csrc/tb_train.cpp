@@ -13,7 +13,7 @@
 
 // GroupNorm backward in one launch: tasks per SM by which the records run ahead.
 #ifndef TB_GN_GRAD_LAG
-#define TB_GN_GRAD_LAG 2
+#define TB_GN_GRAD_LAG 4
 #endif
 
 namespace {
@@ -225,6 +225,8 @@ tb_status gn_grad_tasks(tb::GnGradParams& prm, int mode, tb_dtype dtype, int sms
     }
     int64_t at = 0;
     for (int p = 0; p < prm.P; ++p) {
+        // whole words, evenly; the last part takes what is left
+        if (prm.parts[p] > 1) prm.part_elems[p] = prm.spatial[p] / vec / prm.parts[p] * vec;
         prm.task_start[p] = (int32_t)at;
         at += tasks_of(p);
         if (at > 1000000000LL) return TB_ERR_UNSUPPORTED;

@@ -116,8 +116,12 @@ __device__ __forceinline__ f32x2 dz_pair(f32x2 u, f32x2 dy, f32x2 za, f32x2 zb) 
 
 // --- the ring -------------------------------------------------------------------
 
+// The computing warps work in groups on a stage's rows, a row per group.
+__device__ __forceinline__ int row_groups(int rows) { return rows >= GG_WARPS ? GG_WARPS : 1 << (31 - __clz(rows)); }
+
 struct Ring {
     Stage* stage;
+    float2* slots;  // [stage][2 * GG_WARPS]: the warps' sums of every row
     // shared addresses: mbarriers (a stage's task is set; its rows and
     // constants are there; the computing warps are done with it; their sums of
     // one part are there) and the first stage's rows.  All are per stage: a
@@ -170,13 +174,16 @@ __device__ __forceinline__ float2 group_sums(const GnGradParams& p, int dtype, i
 }
 
 // The warp of stage `s`: for every task that comes through the stage, the
-// unit's and the rows' constants.
+// unit's and the rows' constants and, once the computing warps have left their
+// sums of a part, its records.  (Those warps would wait for the fence that
+// orders the records before the unit's counter.)
 __device__ __forceinline__ void constants_loop(const GnGradParams& p, int dtype, Ring ring, int s) {
     const int lane = threadIdx.x & 31;
     const bool both = p.mode == GRAD_BOTH;
     Stage& d = ring.stage[s];
     const uint32_t full = ring.full + s * 8u;
     const float count_here = both ? p.count : 0.f;
+    uint32_t sums_parity = 0;
     for (uint32_t parity = 0;; parity ^= 1u) {
         bool ok = bar_wait(ring.task + s * 8u, parity, p.status);
         if (__any_sync(0xffffffffu, !ok) || *ring.dead) {
@@ -184,6 +191,10 @@ __device__ __forceinline__ void constants_loop(const GnGradParams& p, int dtype,
             return;
         }
         const int kind = d.kind;
+        // (the stage is refilled while the records are written)
+        const int task_rows = d.rows, slot = d.slot;
+        const bool last = d.last;
+        const int64_t record = d.record, first_row = d.unit;
         if (kind == TASK_END) {
             if (lane == 0) bar_arrive(full);
             return;
@@ -196,8 +207,8 @@ __device__ __forceinline__ void constants_loop(const GnGradParams& p, int dtype,
                     for (int64_t g = c0 / K; g <= (c1 - 1) / K; ++g) ok = ok && wait_unit(p, n * p.C + g * K);
             }
         } else {
-            const int64_t unit = d.unit, n = d.n, g = d.g;
-            const int rows = d.rows;
+            const int64_t unit = first_row, n = d.n, g = d.g;
+            const int rows = task_rows;
             const int64_t ch = d.channel + lane;
             const float gamma = lane < rows ? weight_at(p.gamma, dtype, ch, 1.f) : 0.f;
             const float beta = lane < rows ? weight_at(p.beta, dtype, ch, 0.f) : 0.f;
@@ -232,6 +243,35 @@ __device__ __forceinline__ void constants_loop(const GnGradParams& p, int dtype,
         }
         __syncwarp();
         if (lane == 0) bar_arrive(full);
+        if (kind == TASK_STATS && last) {
+            ok = bar_wait(ring.sums + s * 8u, sums_parity, p.status);
+            sums_parity ^= 1u;
+            if (__any_sync(0xffffffffu, !ok)) {
+                if (lane == 0) *ring.dead = 1;
+                return;
+            }
+            const int wpr = GG_WARPS / row_groups(task_rows);
+            if (lane < task_rows) {
+                const float2* const at = ring.slots + s * 2 * GG_WARPS + lane * wpr;
+                float2 t = at[0];
+                for (int w = 1; w < wpr; ++w) {
+                    t.x += at[w].x;
+                    t.y += at[w].y;
+                }
+                float2* const rec = p.grad_partials + (record + lane) * TB_GN_PARTS;
+                rec[slot] = t;
+                if (p.mode == GRAD_STATS && slot == 0) {
+                    // the slots of parts that do not exist
+                    const int parts = p.parts[record / (p.N * p.C)];
+                    for (int q = parts; q < TB_GN_PARTS; ++q) rec[q] = make_float2(0.f, 0.f);
+                }
+            }
+            __syncwarp();
+            if (lane == 0 && both) {
+                __threadfence();
+                atomicAdd(&unit_at(p, first_row)->arrived, 1u);
+            }
+        }
     }
 }
 
@@ -418,13 +458,12 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
 // --- the computing warps ----------------------------------------------------------
 
 template <int DT, bool SILU>
-__device__ __forceinline__ void compute_loop(const GnGradParams& p, Ring ring, float2 (*slots)[2 * GG_WARPS]) {
+__device__ __forceinline__ void compute_loop(const GnGradParams& p, Ring ring) {
     constexpr int ES = elem_size(DT);
     constexpr int VEC = 16 / ES;
     constexpr int NP = VEC / 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     f32x2 B = 0ull, A = 0ull;  // 0ull: a pair of zeros
-    uint32_t sums_parity = 0;  // a bit per stage
     while (true) {
         const bool here = bar_wait(ring.full + ring.s * 8u, ring.parity, p.status);
         if (!here && lane == 0) *ring.dead = 1;
@@ -461,9 +500,7 @@ __device__ __forceinline__ void compute_loop(const GnGradParams& p, Ring ring, f
             continue;
         }
         const int rows = d.rows, len = d.row_elems, shift = d.shift;
-        // `groups` row groups of `wpr` warps each
-        const int groups = rows >= GG_WARPS ? GG_WARPS : 1 << (31 - __clz(rows));
-        const int wpr = GG_WARPS / groups;
+        const int groups = row_groups(rows), wpr = GG_WARPS / groups;
         const int wg = warp / wpr, wi = warp - wg * wpr;
         const uint32_t xs = ring.data + ring.s * 2 * GG_TENSOR, ds = xs + GG_TENSOR;
         const float mean = d.mean;
@@ -506,7 +543,7 @@ __device__ __forceinline__ void compute_loop(const GnGradParams& p, Ring ring, f
                 }
                 if (d.last) {
                     const float b = warp_sum(vsum(B)), a = warp_sum(vsum(A)) * d.rstd;
-                    if (lane == 0) slots[ring.s][r * wpr + wi] = make_float2(b, a);
+                    if (lane == 0) ring.slots[ring.s * 2 * GG_WARPS + r * wpr + wi] = make_float2(b, a);
                     B = A = 0ull;
                 }
             } else {
@@ -537,35 +574,9 @@ __device__ __forceinline__ void compute_loop(const GnGradParams& p, Ring ring, f
             }
         }
         if (kind == TASK_STATS && d.last) {
-            // the row groups' sums meet; warp 0 writes the records
+            // the stage's warp of constants takes the sums from here
             __syncwarp();
             if (lane == 0) bar_arrive(ring.sums + ring.s * 8u);
-            if (warp == 0) {
-                const bool met = bar_wait(ring.sums + ring.s * 8u, (sums_parity >> ring.s) & 1u, p.status);
-                sums_parity ^= 1u << ring.s;
-                if (!met && lane == 0) *ring.dead = 1;
-                if (__any_sync(0xffffffffu, !met)) return;
-                for (int r = lane; r < rows; r += 32) {
-                    float2 t = slots[ring.s][r * wpr];
-                    for (int w = 1; w < wpr; ++w) {
-                        const float2 v = slots[ring.s][r * wpr + w];
-                        t.x += v.x;
-                        t.y += v.y;
-                    }
-                    float2* const rec = p.grad_partials + (d.record + r) * TB_GN_PARTS;
-                    rec[d.slot] = t;
-                    if (p.mode == GRAD_STATS && d.slot == 0) {
-                        // the slots of parts that do not exist
-                        const int parts = p.parts[d.record / (p.N * p.C)];
-                        for (int q = parts; q < TB_GN_PARTS; ++q) rec[q] = make_float2(0.f, 0.f);
-                    }
-                }
-                __syncwarp();
-                if (lane == 0 && p.mode == GRAD_BOTH) {
-                    __threadfence();
-                    atomicAdd(&unit_at(p, d.unit)->arrived, 1u);
-                }
-            }
         }
         __syncwarp();
         if (lane == 0) bar_arrive(empty);
@@ -582,6 +593,7 @@ __global__ void __launch_bounds__(GG_BLOCK, 1) gn_grad_kernel(const __grid_const
     __shared__ int s_dead;
     Ring ring;
     ring.stage = s_stage;
+    ring.slots = &s_slots[0][0];
     ring.full = smem_addr(s_bar);
     ring.empty = ring.full + GG_STAGES * 8u;
     ring.task = ring.empty + GG_STAGES * 8u;
@@ -600,7 +612,7 @@ __global__ void __launch_bounds__(GG_BLOCK, 1) gn_grad_kernel(const __grid_const
     }
     __syncthreads();
     grid_wait();
-    if (threadIdx.x < GG_THREADS) compute_loop<DT, SILU>(p, ring, s_slots);
+    if (threadIdx.x < GG_THREADS) compute_loop<DT, SILU>(p, ring);
     else if (threadIdx.x < GG_THREADS + 32) copy_loop<DT>(p, ring);
     else constants_loop(p, DT, ring, (int)(threadIdx.x - GG_THREADS) / 32 - 1);
     __syncthreads();  // (no warp's memory goes before the copies have landed)

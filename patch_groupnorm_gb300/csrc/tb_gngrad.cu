@@ -40,7 +40,8 @@ constexpr int GG_STAGES = 3;
 constexpr int GG_BLOCK = GG_THREADS + 32 * (1 + GG_STAGES);  // + the copying warp, and a warp of constants per stage
 constexpr int GG_TENSOR = GRAD_STAGE_BYTES + 128;  // room for a first, partial word
 constexpr int GG_SMEM = GG_STAGES * 2 * GG_TENSOR;
-static_assert(GG_SMEM <= 216 * 1024, "ring too large");
+constexpr int GG_SLOTS = GG_THREADS;               // a lane's sums each, or a warp's of every row
+static_assert(GG_SMEM + GG_STAGES * (GG_SLOTS + 64) * 8 <= 224 * 1024, "ring too large");
 
 enum TaskKind : int32_t { TASK_STATS = 0, TASK_APPLY = 1, TASK_WEIGHTS = 2, TASK_END = 3 };
 
@@ -71,14 +72,15 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// What a GRAD_BOTH launch keeps of a unit, in the last two record slots of the
+// What a GRAD_BOTH launch keeps of a unit, in the last record slots of the
 // unit's first row.
 struct Unit {
-    uint32_t arrived;  // record tasks done
+    uint32_t arrived;  // record tasks done; one more once u and v are there
     uint32_t tasks;    // of unit 0: tasks handed out
     float mean, rstd;
+    float u, v;        // dx = dz * rstd * gamma + (x - mean) * u + v
 };
-static_assert(sizeof(Unit) == 2 * sizeof(float2) && GRAD_BOTH_PARTS == TB_GN_PARTS - 2, "two record slots");
+static_assert(sizeof(Unit) == (TB_GN_PARTS - GRAD_BOTH_PARTS) * sizeof(float2), "the unused record slots");
 // `row`: n * C + the group's first channel.
 __device__ __forceinline__ Unit* unit_at(const GnGradParams& p, int64_t row) {
     return reinterpret_cast<Unit*>(p.grad_partials + row * TB_GN_PARTS + GRAD_BOTH_PARTS);
@@ -93,7 +95,7 @@ __global__ void __launch_bounds__(128) gn_grad_units_kernel(const __grid_constan
     float mean, rstd, count;
     pooled_stats(p, unit / p.G, unit % p.G, mean, rstd, count);
     if ((threadIdx.x & 31) == 0)
-        *unit_at(p, unit / p.G * p.C + unit % p.G * (p.C / p.G)) = Unit{0u, 0u, mean, rstd};
+        *unit_at(p, unit / p.G * p.C + unit % p.G * (p.C / p.G)) = Unit{0u, 0u, mean, rstd, 0.f, 0.f};
 }
 
 // dz of one pair of elements (see the top of this file).  e^-z and the
@@ -121,7 +123,7 @@ __device__ __forceinline__ int row_groups(int rows) { return rows >= GG_WARPS ? 
 
 struct Ring {
     Stage* stage;
-    float2* slots;  // [stage][2 * GG_WARPS]: the warps' sums of every row
+    float2* slots;  // [stage][GG_SLOTS]: sums of dz and dz * (x - mean), see compute_loop
     // shared addresses: mbarriers (a stage's task is set; its rows and
     // constants are there; the computing warps are done with it; their sums of
     // one part are there) and the first stage's rows.  All are per stage: a
@@ -138,10 +140,11 @@ struct Ring {
     }
 };
 
-// Waits until the counter of the unit with this first row reaches its tasks.
+// Waits until all records of the unit with this first row, and its u and v, are
+// there.
 __device__ __forceinline__ bool wait_unit(const GnGradParams& p, int64_t row) {
     const uint32_t* const at = &unit_at(p, row)->arrived;
-    const uint32_t want = (uint32_t)p.unit_tasks;
+    const uint32_t want = (uint32_t)p.unit_tasks + 1u;
     if (ld_acquire(at) >= want) return true;
     const uint64_t t0 = timer_ns();
     while (ld_acquire(at) < want) {
@@ -153,24 +156,37 @@ __device__ __forceinline__ bool wait_unit(const GnGradParams& p, int64_t row) {
     return true;
 }
 
-// c1 and c2 times the group's count, by one warp.
-__device__ __forceinline__ float2 group_sums(const GnGradParams& p, int dtype, int64_t n, int64_t g) {
-    const int K = (int)(p.C / p.G);
-    const int lane = threadIdx.x & 31;
-    const int sets = p.mode == GRAD_BOTH ? p.P : p.R;
+// (u, v) of a unit from its records, by one warp: c1 and c2 are its channels'
+// sums weighted with gamma, over the count.
+__device__ __forceinline__ float2 unit_sums(const GnGradParams& p, int dtype, int64_t n, int64_t g, float rstd,
+                                            float count) {
+    const bool both = p.mode == GRAD_BOTH;
+    const uint32_t K = (uint32_t)(p.C / p.G), slots = both ? GRAD_BOTH_PARTS : TB_GN_PARTS;
+    const uint32_t total = (uint32_t)(both ? p.P : p.R) * K * slots;
+    const float2* const first = p.grad_partials + (n * p.C + g * K) * TB_GN_PARTS;
+    const int64_t set = p.N * p.C * TB_GN_PARTS;
     float B = 0.f, A = 0.f;
-    for (int r = 0; r < sets; ++r) {
-        const int per = p.mode == GRAD_BOTH ? p.parts[r] : TB_GN_PARTS;
-        const float2* const at = p.grad_partials + ((r * p.N + n) * p.C + g * K) * TB_GN_PARTS;
-        for (int q = lane; q < K * per; q += 32) {
-            const int c = q / per;
-            const float2 v = __ldcg(at + (int64_t)c * TB_GN_PARTS + (q - c * per));
-            const float w = weight_at(p.gamma, dtype, g * K + c, 1.f);
-            B = fmaf(v.x, w, B);
-            A = fmaf(v.y, w, A);
+    for (uint32_t q0 = threadIdx.x & 31; q0 < total; q0 += 4 * 32) {
+        float2 v[4];
+        float w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // all loads before the first sum
+            const uint32_t q = q0 + k * 32;
+            const uint32_t row = q / slots, slot = q - row * slots, r = row / K, c = row - r * K;
+            v[k] = make_float2(0.f, 0.f);
+            w[k] = 0.f;
+            if (q < total && (!both || slot < (uint32_t)p.parts[r])) {
+                v[k] = __ldcg(first + r * set + c * TB_GN_PARTS + slot);
+                w[k] = weight_at(p.gamma, dtype, g * K + c, 1.f);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            B = fmaf(v[k].x, w[k], B);
+            A = fmaf(v[k].y, w[k], A);
         }
     }
-    return make_float2(warp_sum(B), warp_sum(A));
+    return make_float2(-warp_sum(A) / count * rstd * rstd, -warp_sum(B) / count * rstd);
 }
 
 // The warp of stage `s`: for every task that comes through the stage, the
@@ -182,7 +198,6 @@ __device__ __forceinline__ void constants_loop(const GnGradParams& p, int dtype,
     const bool both = p.mode == GRAD_BOTH;
     Stage& d = ring.stage[s];
     const uint32_t full = ring.full + s * 8u;
-    const float count_here = both ? p.count : 0.f;
     uint32_t sums_parity = 0;
     for (uint32_t parity = 0;; parity ^= 1u) {
         bool ok = bar_wait(ring.task + s * 8u, parity, p.status);
@@ -195,6 +210,8 @@ __device__ __forceinline__ void constants_loop(const GnGradParams& p, int dtype,
         const int task_rows = d.rows, slot = d.slot;
         const bool last = d.last;
         const int64_t record = d.record, first_row = d.unit;
+        const int unit_n = d.n, unit_g = d.g;
+        float unit_rstd = 0.f;
         if (kind == TASK_END) {
             if (lane == 0) bar_arrive(full);
             return;
@@ -207,35 +224,36 @@ __device__ __forceinline__ void constants_loop(const GnGradParams& p, int dtype,
                     for (int64_t g = c0 / K; g <= (c1 - 1) / K; ++g) ok = ok && wait_unit(p, n * p.C + g * K);
             }
         } else {
-            const int64_t unit = first_row, n = d.n, g = d.g;
+            const int64_t unit = first_row, n = unit_n, g = unit_g;
             const int rows = task_rows;
             const int64_t ch = d.channel + lane;
             const float gamma = lane < rows ? weight_at(p.gamma, dtype, ch, 1.f) : 0.f;
             const float beta = lane < rows ? weight_at(p.beta, dtype, ch, 0.f) : 0.f;
             float mean, rstd, count;
+            float2 uv = make_float2(0.f, 0.f);
             if (both) {
-                const Unit* const at = unit_at(p, unit);
-                mean = at->mean;
-                rstd = at->rstd;
-                count = count_here;
-                if (kind == TASK_APPLY) ok = wait_unit(p, unit);
+                Unit* const at = unit_at(p, unit);
+                if (kind == TASK_APPLY) {
+                    ok = wait_unit(p, unit);
+                    uv = __ldcg(reinterpret_cast<const float2*>(&at->u));
+                }
+                const float2 mr = __ldcg(reinterpret_cast<const float2*>(&at->mean));
+                mean = mr.x;
+                rstd = mr.y;
             } else {
                 pooled_stats(p, n, g, mean, rstd, count);
                 mean = __shfl_sync(0xffffffffu, mean, 0);
                 rstd = __shfl_sync(0xffffffffu, rstd, 0);
                 count = __shfl_sync(0xffffffffu, count, 0);
+                if (kind == TASK_APPLY) uv = unit_sums(p, dtype, n, g, rstd, count);
             }
-            float2 sums = make_float2(0.f, 0.f);
-            if (kind == TASK_APPLY) {
-                __syncwarp();
-                sums = group_sums(p, dtype, n, g);
-            }
+            unit_rstd = rstd;
             if (lane < rows) d.row[lane] = make_float2(rstd * gamma, beta);
             if (lane == 0) {
                 d.mean = mean;
                 d.rstd = rstd;
-                d.v = -sums.x / count * rstd;
-                d.u = -sums.y / count * rstd * rstd;
+                d.u = uv.x;
+                d.v = uv.y;
             }
         }
         if (__any_sync(0xffffffffu, !ok)) {
@@ -250,14 +268,24 @@ __device__ __forceinline__ void constants_loop(const GnGradParams& p, int dtype,
                 if (lane == 0) *ring.dead = 1;
                 return;
             }
-            const int wpr = GG_WARPS / row_groups(task_rows);
-            if (lane < task_rows) {
-                const float2* const at = ring.slots + s * 2 * GG_WARPS + lane * wpr;
-                float2 t = at[0];
-                for (int w = 1; w < wpr; ++w) {
-                    t.x += at[w].x;
-                    t.y += at[w].y;
+            const float2* const sums = ring.slots + s * GG_SLOTS;
+            float2 t = make_float2(0.f, 0.f);
+            if (task_rows == 1) {
+#pragma unroll
+                for (int w = 0; w < GG_WARPS; ++w) {
+                    t.x += sums[w * 32 + lane].x;
+                    t.y += sums[w * 32 + lane].y;
                 }
+                t = make_float2(warp_sum(t.x), warp_sum(t.y));
+            } else if (lane < task_rows) {
+                const int wpr = GG_WARPS / row_groups(task_rows);
+                for (int w = 0; w < wpr; ++w) {
+                    t.x += sums[lane * wpr + w].x;
+                    t.y += sums[lane * wpr + w].y;
+                }
+            }
+            t.y *= unit_rstd;
+            if (lane < task_rows) {
                 float2* const rec = p.grad_partials + (record + lane) * TB_GN_PARTS;
                 rec[slot] = t;
                 if (p.mode == GRAD_STATS && slot == 0) {
@@ -267,9 +295,25 @@ __device__ __forceinline__ void constants_loop(const GnGradParams& p, int dtype,
                 }
             }
             __syncwarp();
-            if (lane == 0 && both) {
-                __threadfence();
-                atomicAdd(&unit_at(p, first_row)->arrived, 1u);
+            if (both) {
+                Unit* const at = unit_at(p, first_row);
+                uint32_t before = 0;
+                if (lane == 0) {
+                    __threadfence();
+                    before = atomicAdd(&at->arrived, 1u);
+                }
+                before = __shfl_sync(0xffffffffu, before, 0);
+                if (before + 1u == (uint32_t)p.unit_tasks) {
+                    // the unit's last records: its u and v, for all dx tasks
+                    __threadfence();
+                    const float2 uv = unit_sums(p, dtype, unit_n, unit_g, unit_rstd, p.count);
+                    if (lane == 0) {
+                        at->u = uv.x;
+                        at->v = uv.y;
+                        __threadfence();
+                        atomicAdd(&at->arrived, 1u);
+                    }
+                }
             }
         }
     }
@@ -280,15 +324,18 @@ __device__ __forceinline__ void constants_loop(const GnGradParams& p, int dtype,
 // the bulk copy, and lanes 0 .. 15 copy the elements on either side of it.
 template <int DT>
 __device__ __forceinline__ void copy_rows(const void* base, int64_t first, int64_t count, uint32_t dst, uint32_t bar,
-                                          bool leader) {
+                                          bool leader, bool last_use) {
     constexpr int ES = elem_size(DT);
     using E = typename Word<ES>::T;
     const char* const from = reinterpret_cast<const char*>(base) + first * ES;
     const uintptr_t a = reinterpret_cast<uintptr_t>(from);
     const int shift = (int)(a & 15u);
     const uintptr_t lo = (a + 15u) & ~(uintptr_t)15u, hi = (a + count * ES) & ~(uintptr_t)15u;
-    if (leader && hi > lo)
-        bulk_load(dst + (uint32_t)(lo - (a - shift)), reinterpret_cast<const void*>(lo), (uint32_t)(hi - lo), bar);
+    if (leader && hi > lo) {
+        const uint32_t to = dst + (uint32_t)(lo - (a - shift));
+        if (last_use) bulk_load_once(to, reinterpret_cast<const void*>(lo), (uint32_t)(hi - lo), bar);
+        else bulk_load(to, reinterpret_cast<const void*>(lo), (uint32_t)(hi - lo), bar);
+    }
     // lane k < 8: element k of the first word; lane 8 + k: element k of the last
     const int lane = threadIdx.x & 31, k = lane & 7;
     const uintptr_t word = lane < 8 ? a - shift : hi;
@@ -427,8 +474,8 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
                 d.out = reinterpret_cast<char*>(p.outs[pp]) + first * ES;
                 bar_arrive(ring.task + ring.s * 8u);
             }
-            copy_rows<DT>(p.patches[pp], first, count, dst, bar, lane == 0);
-            copy_rows<DT>(p.grads[pp], first, count, dst + GG_TENSOR, bar, lane == 0);
+            copy_rows<DT>(p.patches[pp], first, count, dst, bar, lane == 0, kind == TASK_APPLY);
+            copy_rows<DT>(p.grads[pp], first, count, dst + GG_TENSOR, bar, lane == 0, kind == TASK_APPLY);
             __syncwarp();
             if (lane == 0) bar_arrive(bar);  // the elements copied one by one
             ring.next();
@@ -542,8 +589,15 @@ __device__ __forceinline__ void compute_loop(const GnGradParams& p, Ring ring) {
                     }
                 }
                 if (d.last) {
-                    const float b = warp_sum(vsum(B)), a = warp_sum(vsum(A)) * d.rstd;
-                    if (lane == 0) ring.slots[ring.s * 2 * GG_WARPS + r * wpr + wi] = make_float2(b, a);
+                    float2* const slot = ring.slots + ring.s * GG_SLOTS;
+                    if (rows == 1) {
+                        // every lane leaves its own sums: ten dependent shuffles
+                        // less at the end of a task
+                        slot[threadIdx.x] = make_float2(vsum(B), vsum(A));
+                    } else {
+                        const float b = warp_sum(vsum(B)), a = warp_sum(vsum(A));
+                        if (lane == 0) slot[r * wpr + wi] = make_float2(b, a);
+                    }
                     B = A = 0ull;
                 }
             } else {
@@ -588,7 +642,7 @@ template <int DT, bool SILU>
 __global__ void __launch_bounds__(GG_BLOCK, 1) gn_grad_kernel(const __grid_constant__ GnGradParams p) {
     extern __shared__ __align__(128) unsigned char s_data[];
     __shared__ Stage s_stage[GG_STAGES];
-    __shared__ float2 s_slots[GG_STAGES][2 * GG_WARPS];
+    __shared__ float2 s_slots[GG_STAGES][GG_SLOTS];
     __shared__ __align__(8) unsigned long long s_bar[4 * GG_STAGES];
     __shared__ int s_dead;
     Ring ring;
@@ -708,14 +762,13 @@ __global__ void __launch_bounds__(EL_BLOCK) gn_grad_apply_elem_kernel(const __gr
         rstd = __shfl_sync(0xffffffffu, rstd, 0);
         count = __shfl_sync(0xffffffffu, count, 0);
         const float2 k = make_float2(rstd * weight_at(p.gamma, DT, c, 1.f), weight_at(p.beta, DT, c, 0.f));
-        const float2 sums = group_sums(p, DT, n, g);
-        const float v = -sums.x / count * rstd, uu = -sums.y / count * rstd * rstd;
+        const float2 uv = unit_sums(p, DT, n, g, rstd, count);
         using E = typename Word<elem_size(DT)>::T;
         for (int64_t e0 = (int64_t)blockIdx.y * EL_SEG; e0 < S; e0 += (int64_t)gridDim.y * EL_SEG) {
             for (int64_t i = e0 + threadIdx.x; i < min(S, e0 + EL_SEG); i += EL_BLOCK) {
                 const float u = elem_at<DT>(p.patches[pp], nc * S + i) - mean;
                 const float dz = dz_one<SILU>(u, elem_at<DT>(p.grads[pp], nc * S + i), k);
-                const float o[1] = {fmaf(dz, k.x, fmaf(u, uu, v))};
+                const float o[1] = {fmaf(dz, k.x, fmaf(u, uv.x, uv.y))};
                 reinterpret_cast<E*>(p.outs[pp])[nc * S + i] = pack<DT, 1>(o);
             }
         }

@@ -466,7 +466,7 @@ constexpr int GRAD_MAX_ROWS = 31;        // channel rows of one task
 constexpr int GRAD_CHANNELS = 16;        // channels of one weight-gradient task
 // GRAD_BOTH keeps the units' counters and statistics in the last two record
 // slots of their first rows, so it cuts rows into fewer parts.
-constexpr int GRAD_BOTH_PARTS = TB_GN_PARTS - 2;
+constexpr int GRAD_BOTH_PARTS = TB_GN_PARTS - 3;
 
 // ring: patches, gradients and outputs share their offset from 16-byte
 // boundaries (the ring kernel); otherwise the element kernels run.

@@ -13,7 +13,7 @@
 
 // GroupNorm backward in one launch: tasks per SM by which the records run ahead.
 #ifndef TB_GN_GRAD_LAG
-#define TB_GN_GRAD_LAG 4
+#define TB_GN_GRAD_LAG 12
 #endif
 
 namespace {
@@ -444,7 +444,9 @@ TB_API tb_status tb_patch_gn_backward(const void* const* patches, const void* co
     int sms = 0;
     TB_TRY(tb::sm_count(&sms));
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (ring && N > 0) {
+    bool any = false;
+    for (int p = 0; p < P; ++p) any = any || spatial[p] > 0;
+    if (ring && N > 0 && any) {
         TB_TRY(gn_grad_tasks(prm, tb::GRAD_BOTH, dtype, sms));
         return launched(tb::launch_gn_grad(prm, (int)dtype, true, sms, s));
     }

@@ -654,6 +654,10 @@ def test_groupnorm_backward_checks_and_empty_batch(tbl):
     e = torch.empty(0, 8, 4, 4, device="cuda")
     dxs, dg, db = tbl.patch_group_norm_backward([e], [e], 2, tbl.new_partials(1, 0, 2), None, None, 1e-6)
     assert dxs[0].shape == e.shape and (dg == 0).all() and (db == 0).all()
+    e = torch.empty(2, 8, 0, 4, device="cuda")            # no positions at all
+    part = tbl.tb_patch_gn_stats([e], 2, tbl.new_partials(1, 2, 2))
+    dxs, dg, db = tbl.patch_group_norm_backward([e], [e], 2, part, None, None, 1e-6)
+    assert dxs[0].shape == e.shape and (dg == 0).all() and (db == 0).all()
 
 
 def test_groupnorm_backward_extreme_activations(tbl):

@@ -319,41 +319,15 @@ __device__ __forceinline__ void constants_loop(const GnGradParams& p, int dtype,
     }
 }
 
-// Copies elements [first, first + count) of `base` into the stage's buffer at
-// `dst`, keeping their offset from 16-byte boundaries; `bytes` is the size of
-// the bulk copy, and lanes 0 .. 15 copy the elements on either side of it.
-template <int DT>
-__device__ __forceinline__ void copy_rows(const void* base, int64_t first, int64_t count, uint32_t dst, uint32_t bar,
-                                          bool leader, bool last_use) {
-    constexpr int ES = elem_size(DT);
-    using E = typename Word<ES>::T;
-    const char* const from = reinterpret_cast<const char*>(base) + first * ES;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(from);
-    const int shift = (int)(a & 15u);
-    const uintptr_t lo = (a + 15u) & ~(uintptr_t)15u, hi = (a + count * ES) & ~(uintptr_t)15u;
-    if (leader && hi > lo) {
-        const uint32_t to = dst + (uint32_t)(lo - (a - shift));
-        if (last_use) bulk_load_once(to, reinterpret_cast<const void*>(lo), (uint32_t)(hi - lo), bar);
-        else bulk_load(to, reinterpret_cast<const void*>(lo), (uint32_t)(hi - lo), bar);
+// One of the elements on either side of a bulk copy, into shared memory.
+template <int ES>
+__device__ __forceinline__ void copy_element(uint32_t to, const char* from) {
+    if constexpr (ES == 4) {
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(*reinterpret_cast<const uint32_t*>(from)) : "memory");
+    } else {
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(*reinterpret_cast<const unsigned short*>(from))
+                     : "memory");
     }
-    // lane k < 8: element k of the first word; lane 8 + k: element k of the last
-    const int lane = threadIdx.x & 31, k = lane & 7;
-    const uintptr_t word = lane < 8 ? a - shift : hi;
-    const uintptr_t at = word + k * ES;
-    const bool mine = lane < 16 && k * ES < 16 && at >= a && at < a + count * ES &&
-                      (lane < 8 ? (shift != 0 && at < lo) : (hi >= lo));
-    if (mine) {
-        const E v = *reinterpret_cast<const E*>(at);
-        const uint32_t to = dst + (uint32_t)(at - (a - shift));
-        if constexpr (ES == 4) asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(v) : "memory");
-        else asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(v) : "memory");
-    }
-}
-// Bytes copy_rows moves in bulk.
-__device__ __forceinline__ uint32_t bulk_bytes(const void* base, int64_t first, int64_t count, int es) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(base) + first * es;
-    const uintptr_t lo = (a + 15u) & ~(uintptr_t)15u, hi = (a + count * es) & ~(uintptr_t)15u;
-    return hi > lo ? (uint32_t)(hi - lo) : 0u;
 }
 
 template <int DT>
@@ -448,6 +422,8 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
             e1 = S;
         }
         const int64_t row = n * p.C + g * K + c_first;
+        const char* const xbase = reinterpret_cast<const char*>(p.patches[pp]);
+        const char* const dbase = reinterpret_cast<const char*>(p.grads[pp]);
         constexpr int64_t MOST = GRAD_STAGE_BYTES / ES;
         // (one stage for whole rows; the stages of a part in turn)
         // (an empty patch's rows still get their records)
@@ -455,15 +431,21 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
             const int64_t len = min(MOST, e1 - at);
             if (!claim()) break;
             Stage& d = ring.stage[ring.s];
-            const uint32_t bar = ring.full + ring.s * 8u, dst = ring.data + ring.s * 2 * GG_TENSOR;
-            const int64_t first = row * S + at, count = rows * len;
-            if (lane == 0)
-                bar_expect(bar, bulk_bytes(p.patches[pp], first, count, ES) + bulk_bytes(p.grads[pp], first, count, ES));
+            const uint32_t bar = ring.full + ring.s * 8u;
+            const int64_t first = row * S + at;
+            // x on the lower lanes, dy on the upper ones: `head` bytes before the
+            // first 16-byte boundary, the bulk copy's, and the rest
+            const char* const from = (lane < 16 ? xbase : dbase) + first * ES;
+            const uint32_t bytes = (uint32_t)(rows * (int)len) * ES;
+            const uint32_t shift = (uint32_t)reinterpret_cast<uintptr_t>(from) & 15u;
+            const uint32_t head = min((16u - shift) & 15u, bytes), bulk = (bytes - head) & ~15u;
+            const uint32_t to = ring.data + (ring.s * 2 + (lane < 16 ? 0 : 1)) * GG_TENSOR + shift;
             if (lane == 0) {
+                bar_expect(bar, 2 * bulk);
                 d.kind = kind;
                 d.rows = rows;
                 d.row_elems = (int32_t)len;
-                d.shift = (int32_t)((reinterpret_cast<uintptr_t>(p.patches[pp]) + first * ES) & 15u) / ES;
+                d.shift = (int32_t)shift / ES;
                 d.last = at + len >= e1;
                 d.slot = part;
                 d.record = pp * p.N * p.C + row;
@@ -474,9 +456,21 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
                 d.out = reinterpret_cast<char*>(p.outs[pp]) + first * ES;
                 bar_arrive(ring.task + ring.s * 8u);
             }
-            copy_rows<DT>(p.patches[pp], first, count, dst, bar, lane == 0, kind == TASK_APPLY);
-            copy_rows<DT>(p.grads[pp], first, count, dst + GG_TENSOR, bar, lane == 0, kind == TASK_APPLY);
             __syncwarp();
+            if ((lane & 15) == 0 && bulk > 0) {
+                if (kind == TASK_APPLY) bulk_load_once(to + head, from + head, bulk, bar);
+                else bulk_load(to + head, from + head, bulk, bar);
+            }
+            if (bytes != bulk) {
+                // lane k < 8 of either half: element k before the bulk copy, and k after it
+                const uint32_t k = (lane & 7) * ES, tail = head + bulk + k;
+                if ((lane & 8) == 0) {
+                    if (k < head) copy_element<ES>(to + k, from + k);
+                } else if (tail < bytes) {
+                    copy_element<ES>(to + tail, from + tail);
+                }
+                __syncwarp();
+            }
             if (lane == 0) bar_arrive(bar);  // the elements copied one by one
             ring.next();
         }

@@ -13,7 +13,7 @@
 
 // GroupNorm backward in one launch: tasks per SM by which the records run ahead.
 #ifndef TB_GN_GRAD_LAG
-#define TB_GN_GRAD_LAG 12
+#define TB_GN_GRAD_LAG 16
 #endif
 
 namespace {

@@ -34,7 +34,7 @@
 namespace tb {
 namespace {
 
-constexpr int GG_WARPS = 16;
+constexpr int GG_LOG2 = 4, GG_WARPS = 1 << GG_LOG2;  // computing warps
 constexpr int GG_THREADS = GG_WARPS * 32;
 constexpr int GG_STAGES = 3;
 constexpr int GG_BLOCK = GG_THREADS + 32 * (1 + GG_STAGES);  // + the copying warp, and a warp of constants per stage
@@ -118,8 +118,9 @@ __device__ __forceinline__ f32x2 dz_pair(f32x2 u, f32x2 dy, f32x2 za, f32x2 zb) 
 
 // --- the ring -------------------------------------------------------------------
 
-// The computing warps work in groups on a stage's rows, a row per group.
-__device__ __forceinline__ int row_groups(int rows) { return rows >= GG_WARPS ? GG_WARPS : 1 << (31 - __clz(rows)); }
+// The computing warps work in 2^row_groups_log2 groups on a stage's rows, a row
+// per group.
+__device__ __forceinline__ int row_groups_log2(int rows) { return min(GG_LOG2, 31 - __clz(rows)); }
 
 struct Ring {
     Stage* stage;
@@ -278,7 +279,7 @@ __device__ __forceinline__ void constants_loop(const GnGradParams& p, int dtype,
                 }
                 t = make_float2(warp_sum(t.x), warp_sum(t.y));
             } else if (lane < task_rows) {
-                const int wpr = GG_WARPS / row_groups(task_rows);
+                const int wpr = GG_WARPS >> row_groups_log2(task_rows);
                 for (int w = 0; w < wpr; ++w) {
                     t.x += sums[lane * wpr + w].x;
                     t.y += sums[lane * wpr + w].y;
@@ -541,39 +542,39 @@ __device__ __forceinline__ void compute_loop(const GnGradParams& p, Ring ring) {
             continue;
         }
         const int rows = d.rows, len = d.row_elems, shift = d.shift;
-        const int groups = row_groups(rows), wpr = GG_WARPS / groups;
-        const int wg = warp / wpr, wi = warp - wg * wpr;
-        const uint32_t xs = ring.data + ring.s * 2 * GG_TENSOR, ds = xs + GG_TENSOR;
+        // 2^lg row groups of `wpr` warps each (GG_WARPS is a power of two)
+        const int lg = row_groups_log2(rows), wpr = GG_WARPS >> lg, groups = 1 << lg;
+        const int wg = warp >> (GG_LOG2 - lg), wi = warp & (wpr - 1);
+        const uint32_t xs = ring.data + ring.s * 2 * GG_TENSOR;
         const float mean = d.mean;
         const f32x2 mean2 = pair(mean, mean);
         const f32x2 u2 = pair(d.u, d.u), v2 = pair(d.v, d.v);
         for (int r = wg; r < rows; r += groups) {
             const float2 k = d.row[r];
             const f32x2 za = pair(k.x, k.x), zb = pair(k.y, k.y);
-            const int lo = shift + r * len, hi = lo + len;  // the row's elements in the buffer
-            const int w1 = (hi + VEC - 1) / VEC;
-            // word w of the row: x and dy as lanes, (mean, 0) outside [lo, hi)
-            auto word = [&](int w, f32x2 (&x)[NP], f32x2 (&dy)[NP]) {
-                to_lanes<DT, VEC>(smem_load<uint4>(xs + w * 16u), x);
-                to_lanes<DT, VEC>(smem_load<uint4>(ds + w * 16u), dy);
-                if (w * VEC < lo || (w + 1) * VEC > hi) {
+            const int lo = shift + r * len, hi = lo + len;            // the row's elements in the buffer
+            const int w0 = (lo + VEC - 1) / VEC, w1 = hi / VEC;       // its whole words
+            const int first = w0 + wi * 32 + lane, step = wpr * 32;
+            // the words at its ends: x and dy as lanes, (mean, 0) outside [lo, hi)
+            const int edge = lane == 0 ? lo / VEC : hi / VEC;
+            const bool at_edge = wi == 0 && ((lane == 0 && lo < w0 * VEC) || (lane == 1 && hi > w1 * VEC && w1 >= w0));
+            auto edge_word = [&](f32x2 (&x)[NP], f32x2 (&dy)[NP]) {
+                to_lanes<DT, VEC>(smem_load<uint4>(xs + edge * 16u), x);
+                to_lanes<DT, VEC>(smem_load<uint4>(xs + GG_TENSOR + edge * 16u), dy);
 #pragma unroll
-                    for (int q = 0; q < NP; ++q) {
-                        float a, b, c, e;
-                        halves(x[q], a, b);
-                        halves(dy[q], c, e);
-                        const int i = w * VEC + 2 * q;
-                        if (i < lo || i >= hi) a = mean, c = 0.f;
-                        if (i + 1 < lo || i + 1 >= hi) b = mean, e = 0.f;
-                        x[q] = pair(a, b);
-                        dy[q] = pair(c, e);
-                    }
+                for (int q = 0; q < NP; ++q) {
+                    float a, b, c, e;
+                    halves(x[q], a, b);
+                    halves(dy[q], c, e);
+                    const int i = edge * VEC + 2 * q;
+                    if (i < lo || i >= hi) a = mean, c = 0.f;
+                    if (i + 1 < lo || i + 1 >= hi) b = mean, e = 0.f;
+                    x[q] = pair(a, b);
+                    dy[q] = pair(c, e);
                 }
             };
             if (kind == TASK_STATS) {
-                for (int w = lo / VEC + wi * 32 + lane; w < w1; w += wpr * 32) {
-                    f32x2 x[NP], dy[NP];
-                    word(w, x, dy);
+                auto add = [&](const f32x2 (&x)[NP], const f32x2 (&dy)[NP]) {
 #pragma unroll
                     for (int q = 0; q < NP; ++q) {
                         const f32x2 u = vsub(x[q], mean2);
@@ -581,6 +582,18 @@ __device__ __forceinline__ void compute_loop(const GnGradParams& p, Ring ring) {
                         B = vadd(B, dz);
                         A = vfma(dz, u, A);
                     }
+                };
+                uint32_t at = xs + first * 16u;
+                for (int w = first; w < w1; w += step, at += step * 16u) {
+                    f32x2 x[NP], dy[NP];
+                    to_lanes<DT, VEC>(smem_load<uint4>(at), x);
+                    to_lanes<DT, VEC>(smem_load<uint4>(at + GG_TENSOR), dy);
+                    add(x, dy);
+                }
+                if (at_edge) {
+                    f32x2 x[NP], dy[NP];
+                    edge_word(x, dy);
+                    add(x, dy);
                 }
                 if (d.last) {
                     float2* const slot = ring.slots + ring.s * GG_SLOTS;
@@ -589,34 +602,43 @@ __device__ __forceinline__ void compute_loop(const GnGradParams& p, Ring ring) {
                         // less at the end of a task
                         slot[threadIdx.x] = make_float2(vsum(B), vsum(A));
                     } else {
+                        __syncwarp();
                         const float b = warp_sum(vsum(B)), a = warp_sum(vsum(A));
                         if (lane == 0) slot[r * wpr + wi] = make_float2(b, a);
                     }
                     B = A = 0ull;
                 }
             } else {
-                for (int w = lo / VEC + wi * 32 + lane; w < w1; w += wpr * 32) {
-                    f32x2 x[NP], dy[NP];
-                    word(w, x, dy);
+                auto grad = [&](f32x2 (&x)[NP], const f32x2 (&dy)[NP]) {
 #pragma unroll
                     for (int q = 0; q < NP; ++q) {
                         const f32x2 u = vsub(x[q], mean2);
                         x[q] = vfma(dz_pair<SILU>(u, dy[q], za, zb), za, vfma(u, u2, v2));
                     }
+                };
+                uint32_t at = xs + first * 16u;
+                uint4* out = reinterpret_cast<uint4*>(d.out - shift * ES) + first;
+                for (int w = first; w < w1; w += step, at += step * 16u, out += step) {
+                    f32x2 x[NP], dy[NP];
+                    to_lanes<DT, VEC>(smem_load<uint4>(at), x);
+                    to_lanes<DT, VEC>(smem_load<uint4>(at + GG_TENSOR), dy);
+                    grad(x, dy);
+                    __stcs(out, from_lanes<DT, VEC>(x));
+                }
+                if (at_edge) {
+                    f32x2 x[NP], dy[NP];
+                    edge_word(x, dy);
+                    grad(x, dy);
+                    using E = typename Word<ES>::T;
                     const uint4 o = from_lanes<DT, VEC>(x);
-                    char* const at = d.out + ((int64_t)w * VEC - shift) * ES;
-                    if (w * VEC >= lo && (w + 1) * VEC <= hi) {
-                        __stcs(reinterpret_cast<uint4*>(at), o);
-                    } else {
-                        using E = typename Word<ES>::T;
-                        const uint32_t bits[4] = {o.x, o.y, o.z, o.w};
+                    const uint32_t bits[4] = {o.x, o.y, o.z, o.w};
+                    E* const to = reinterpret_cast<E*>(d.out) + (edge * VEC - shift);
 #pragma unroll
-                        for (int q = 0; q < VEC; ++q) {
-                            const int i = w * VEC + q;
-                            if (i < lo || i >= hi) continue;
-                            if constexpr (ES == 4) reinterpret_cast<E*>(at)[q] = bits[q];
-                            else reinterpret_cast<E*>(at)[q] = (E)(bits[q >> 1] >> (16 * (q & 1)));
-                        }
+                    for (int q = 0; q < VEC; ++q) {
+                        const int i = edge * VEC + q;
+                        if (i < lo || i >= hi) continue;
+                        if constexpr (ES == 4) to[q] = bits[q];
+                        else to[q] = (E)(bits[q >> 1] >> (16 * (q & 1)));
                     }
                 }
             }

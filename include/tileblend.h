@@ -784,33 +784,15 @@ tb_status tb_patch_gn_grad_stats(const void* const* patches, const void* const* 
  *   the rest       as tb_patch_gn_grad_stats
  * Errors as tb_patch_gn_grad_stats.
  *
- * Kernels of this pass wait for copies, and in tb_patch_gn_backward for each
- * other's records, at most about a second; a wait that runs out is reported as
- * TB_DEV_WAIT_TIMEOUT by tb_device_status and leaves the outputs unfinished.
+ * The kernels of this pass wait for their copies at most about a second; a wait
+ * that runs out is reported as TB_DEV_WAIT_TIMEOUT by tb_device_status and
+ * leaves the outputs unfinished.
  */
 tb_status tb_patch_gn_grad_apply(const void* const* patches, const void* const* grads, void* const* outs, int32_t P,
                                  tb_dtype dtype, int64_t N, int64_t C, const int64_t* spatial, int32_t G,
                                  const tb_gn_partial* partials, const tb_gn_grad_partial* grad_partials, int32_t R,
                                  const void* gamma, const void* beta, float eps, int32_t silu, void* dgamma,
                                  void* dbeta, void* stream);
-
-/*
- * tb_patch_gn_backward -- the backward pass of a PatchGroupNorm whose patches
- * are all here: tb_patch_gn_grad_stats and tb_patch_gn_grad_apply (R = P) in
- * one pass over memory where a few groups' patches fit in the L2 cache.
- *
- *   grad_partials  device [P][N][C][TB_GN_PARTS], a workspace: its contents
- *                  need no clearing and mean nothing afterwards
- *   the rest       as those calls
- * The weight gradients equal those calls' up to the order of their sums.
- * Errors as tb_patch_gn_grad_apply; TB_ERR_UNSUPPORTED also for more than
- * about 1e9 pieces of work (32 KB of x, or a channel row, each).
- */
-tb_status tb_patch_gn_backward(const void* const* patches, const void* const* grads, void* const* outs, int32_t P,
-                               tb_dtype dtype, int64_t N, int64_t C, const int64_t* spatial, int32_t G,
-                               const tb_gn_partial* partials, const void* gamma, const void* beta, float eps,
-                               int32_t silu, void* dgamma, void* dbeta, tb_gn_grad_partial* grad_partials,
-                               void* stream);
 
 #ifdef __cplusplus
 }

@@ -9,25 +9,27 @@
 //     dx = rnd(rstd * (gamma * dz - c1 - xhat * c2))
 // Sums are fp32, in an order fixed by the sizes and the GPU.
 //
-// dx needs sums over the whole group, so x and dy are read twice: once for
-// the records (B, A) and once for dx.  gn_grad_kernel does either pass, or
-// both in one launch that reads them from memory once where a group and its
-// successors fit in L2: its tasks are taken in order from a counter -- the
-// records of the first `lag` units (sample, group), then alternately a task of
-// the records of unit i + lag and one of the dx of unit i -- so a unit's
-// second reading follows its first by about 15 MB and finds it in L2.  A dx
-// task waits for the arrival counter of its unit's records.  Tasks are handed
-// out in order and only to running CTAs, so a task that another waits for has
-// always been started, whatever else occupies the GPU.
+// dx needs sums over the whole group, so x and dy are read twice, once by each
+// of two launches of gn_grad_kernel: GRAD_STATS leaves the records (B, A) of
+// every channel, GRAD_APPLY writes dx.  A CTA takes the same contiguous run of
+// tasks (some rows of a group, or a part of one) in both, the second time from
+// its end, where the first has left its rows in L2.  One launch with both
+// passes interleaved, a group's dx following its records by 15 to 60 MB, was
+// built and measured: it reads memory once, but its waits cost what that saves
+// (4D 61 us, 5D 185, as the two launches take), because computing, not memory,
+// is the longer half: the SiLU derivative takes about 11 instructions a pair of
+// elements in each pass, and the kernel issues an instruction in 55 % of all
+// cycles.
 //
-// One CTA per SM: 16 warps compute, a 17th takes the tasks and copies their
-// rows into a ring of three stages in shared memory (64 KB each: x and dy), and
-// each stage has a warp that finds the unit's and the rows' constants (chains
-// of dependent loads of about three times a stage's computing time: one warp
-// for all stages held the whole kernel up, 126 us of 4D against 84 of two
-// plain launches).  Bulk copies move whole 16-byte words; the elements before
-// the first and after the last boundary are copied one by one, so rows of any
-// length and offset take this path.
+// One CTA per SM: 16 warps compute, a 17th copies the tasks' rows into a ring
+// of three stages in shared memory (64 KB each: x and dy), and each stage has a
+// warp that finds the unit's and the rows' constants and writes the records
+// (chains of dependent loads of about three times a stage's computing time:
+// with one warp for everything 4D took 126 us).  Stages of 16 KB a tensor, six
+// of them, took 92 us: a stage costs its copying warp 1.2 us whatever its size.
+// Bulk copies move whole 16-byte words; the elements before the first and after
+// the last boundary are copied one by one, so rows of any length and offset
+// take this path.
 #include "tb_elem.cuh"
 #include "tb_groupnorm.cuh"
 
@@ -55,47 +57,15 @@ struct Stage {
     int32_t slot;        // TASK_STATS: the part's record slot
     int64_t record;      // TASK_STATS: row index p * N * C + n * C + c of the first row; TASK_WEIGHTS: channel
     int32_t n, g;        // sample and group
-    int64_t unit;        // row index n * C + c of the group's first channel
     int64_t channel;     // of the first row
     char* out;           // TASK_APPLY: address of the first element
-    float mean, rstd;
+    float mean;
     float u, v;          // TASK_APPLY: dx = dz * rstd * gamma + (x - mean) * u + v
     float2 row[GRAD_MAX_ROWS + 1];  // (rstd * gamma, beta) of each row
 };
 
-__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
-    uint32_t v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// What a GRAD_BOTH launch keeps of a unit, in the last record slots of the
-// unit's first row.
-struct Unit {
-    uint32_t arrived;  // record tasks done; one more once u and v are there
-    uint32_t tasks;    // of unit 0: tasks handed out
-    float mean, rstd;
-    float u, v;        // dx = dz * rstd * gamma + (x - mean) * u + v
-};
-static_assert(sizeof(Unit) == (TB_GN_PARTS - GRAD_BOTH_PARTS) * sizeof(float2), "the unused record slots");
-// `row`: n * C + the group's first channel.
-__device__ __forceinline__ Unit* unit_at(const GnGradParams& p, int64_t row) {
-    return reinterpret_cast<Unit*>(p.grad_partials + row * TB_GN_PARTS + GRAD_BOTH_PARTS);
-}
-
-// Before a GRAD_BOTH launch: counters zero, every unit's mean and rstd.
-__global__ void __launch_bounds__(128) gn_grad_units_kernel(const __grid_constant__ GnGradParams p) {
-    pdl_trigger_dependents();
-    grid_wait();
-    const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (unit >= p.N * p.G) return;
-    float mean, rstd, count;
-    pooled_stats(p, unit / p.G, unit % p.G, mean, rstd, count);
-    if ((threadIdx.x & 31) == 0)
-        *unit_at(p, unit / p.G * p.C + unit % p.G * (p.C / p.G)) = Unit{0u, 0u, mean, rstd, 0.f, 0.f};
 }
 
 // dz of one pair of elements (see the top of this file).  e^-z and the
@@ -141,29 +111,12 @@ struct Ring {
     }
 };
 
-// Waits until all records of the unit with this first row, and its u and v, are
-// there.
-__device__ __forceinline__ bool wait_unit(const GnGradParams& p, int64_t row) {
-    const uint32_t* const at = &unit_at(p, row)->arrived;
-    const uint32_t want = (uint32_t)p.unit_tasks + 1u;
-    if (ld_acquire(at) >= want) return true;
-    const uint64_t t0 = timer_ns();
-    while (ld_acquire(at) < want) {
-        if (timer_ns() - t0 > BAR_WAIT_NS) {
-            if (p.status != nullptr) atomicCAS(p.status, (uint32_t)DEV_OK, (uint32_t)DEV_WAIT_TIMEOUT);
-            return false;
-        }
-    }
-    return true;
-}
-
 // (u, v) of a unit from its records, by one warp: c1 and c2 are its channels'
 // sums weighted with gamma, over the count.
 __device__ __forceinline__ float2 unit_sums(const GnGradParams& p, int dtype, int64_t n, int64_t g, float rstd,
                                             float count) {
-    const bool both = p.mode == GRAD_BOTH;
-    const uint32_t K = (uint32_t)(p.C / p.G), slots = both ? GRAD_BOTH_PARTS : TB_GN_PARTS;
-    const uint32_t total = (uint32_t)(both ? p.P : p.R) * K * slots;
+    const uint32_t K = (uint32_t)(p.C / p.G);
+    const uint32_t total = (uint32_t)p.R * K * TB_GN_PARTS;
     const float2* const first = p.grad_partials + (n * p.C + g * K) * TB_GN_PARTS;
     const int64_t set = p.N * p.C * TB_GN_PARTS;
     float B = 0.f, A = 0.f;
@@ -173,11 +126,11 @@ __device__ __forceinline__ float2 unit_sums(const GnGradParams& p, int dtype, in
 #pragma unroll
         for (int k = 0; k < 4; ++k) {  // all loads before the first sum
             const uint32_t q = q0 + k * 32;
-            const uint32_t row = q / slots, slot = q - row * slots, r = row / K, c = row - r * K;
+            const uint32_t row = q / TB_GN_PARTS, r = row / K, c = row - r * K;
             v[k] = make_float2(0.f, 0.f);
             w[k] = 0.f;
-            if (q < total && (!both || slot < (uint32_t)p.parts[r])) {
-                v[k] = __ldcg(first + r * set + c * TB_GN_PARTS + slot);
+            if (q < total) {
+                v[k] = first[r * set + c * TB_GN_PARTS + q % TB_GN_PARTS];
                 w[k] = weight_at(p.gamma, dtype, g * K + c, 1.f);
             }
         }
@@ -192,14 +145,17 @@ __device__ __forceinline__ float2 unit_sums(const GnGradParams& p, int dtype, in
 
 // The warp of stage `s`: for every task that comes through the stage, the
 // unit's and the rows' constants and, once the computing warps have left their
-// sums of a part, its records.  (Those warps would wait for the fence that
-// orders the records before the unit's counter.)
+// sums of a part, its records.
 __device__ __forceinline__ void constants_loop(const GnGradParams& p, int dtype, Ring ring, int s) {
     const int lane = threadIdx.x & 31;
-    const bool both = p.mode == GRAD_BOTH;
     Stage& d = ring.stage[s];
     const uint32_t full = ring.full + s * 8u;
     uint32_t sums_parity = 0;
+    // the unit that the constants at hand are of: a CTA's tasks follow each
+    // other, so it seldom changes
+    int unit_n = -1, unit_g = -1;
+    float mean = 0.f, rstd = 0.f;
+    float2 uv = make_float2(0.f, 0.f);
     for (uint32_t parity = 0;; parity ^= 1u) {
         bool ok = bar_wait(ring.task + s * 8u, parity, p.status);
         if (__any_sync(0xffffffffu, !ok) || *ring.dead) {
@@ -208,57 +164,33 @@ __device__ __forceinline__ void constants_loop(const GnGradParams& p, int dtype,
         }
         const int kind = d.kind;
         // (the stage is refilled while the records are written)
-        const int task_rows = d.rows, slot = d.slot;
+        const int rows = d.rows, slot = d.slot;
         const bool last = d.last;
-        const int64_t record = d.record, first_row = d.unit;
-        const int unit_n = d.n, unit_g = d.g;
-        float unit_rstd = 0.f;
+        const int64_t record = d.record;
         if (kind == TASK_END) {
             if (lane == 0) bar_arrive(full);
             return;
         }
-        if (kind == TASK_WEIGHTS) {
-            if (both) {
-                const int K = (int)(p.C / p.G);
-                const int64_t c0 = d.channel, c1 = min(p.C, c0 + GRAD_CHANNELS);
-                for (int64_t n = 0; n < p.N; ++n)
-                    for (int64_t g = c0 / K; g <= (c1 - 1) / K; ++g) ok = ok && wait_unit(p, n * p.C + g * K);
-            }
-        } else {
-            const int64_t unit = first_row, n = unit_n, g = unit_g;
-            const int rows = task_rows;
+        if (kind != TASK_WEIGHTS) {
             const int64_t ch = d.channel + lane;
             const float gamma = lane < rows ? weight_at(p.gamma, dtype, ch, 1.f) : 0.f;
             const float beta = lane < rows ? weight_at(p.beta, dtype, ch, 0.f) : 0.f;
-            float mean, rstd, count;
-            float2 uv = make_float2(0.f, 0.f);
-            if (both) {
-                Unit* const at = unit_at(p, unit);
-                if (kind == TASK_APPLY) {
-                    ok = wait_unit(p, unit);
-                    uv = __ldcg(reinterpret_cast<const float2*>(&at->u));
-                }
-                const float2 mr = __ldcg(reinterpret_cast<const float2*>(&at->mean));
-                mean = mr.x;
-                rstd = mr.y;
-            } else {
-                pooled_stats(p, n, g, mean, rstd, count);
+            if (d.n != unit_n || d.g != unit_g) {
+                unit_n = d.n;
+                unit_g = d.g;
+                float count;
+                pooled_stats(p, unit_n, unit_g, mean, rstd, count);
                 mean = __shfl_sync(0xffffffffu, mean, 0);
                 rstd = __shfl_sync(0xffffffffu, rstd, 0);
                 count = __shfl_sync(0xffffffffu, count, 0);
-                if (kind == TASK_APPLY) uv = unit_sums(p, dtype, n, g, rstd, count);
+                if (kind == TASK_APPLY) uv = unit_sums(p, dtype, unit_n, unit_g, rstd, count);
             }
-            unit_rstd = rstd;
             if (lane < rows) d.row[lane] = make_float2(rstd * gamma, beta);
             if (lane == 0) {
                 d.mean = mean;
-                d.rstd = rstd;
                 d.u = uv.x;
                 d.v = uv.y;
             }
-        }
-        if (__any_sync(0xffffffffu, !ok)) {
-            if (lane == 0) *ring.dead = 1;
         }
         __syncwarp();
         if (lane == 0) bar_arrive(full);
@@ -271,49 +203,28 @@ __device__ __forceinline__ void constants_loop(const GnGradParams& p, int dtype,
             }
             const float2* const sums = ring.slots + s * GG_SLOTS;
             float2 t = make_float2(0.f, 0.f);
-            if (task_rows == 1) {
+            if (rows == 1) {
 #pragma unroll
                 for (int w = 0; w < GG_WARPS; ++w) {
                     t.x += sums[w * 32 + lane].x;
                     t.y += sums[w * 32 + lane].y;
                 }
                 t = make_float2(warp_sum(t.x), warp_sum(t.y));
-            } else if (lane < task_rows) {
-                const int wpr = GG_WARPS >> row_groups_log2(task_rows);
+            } else if (lane < rows) {
+                const int wpr = GG_WARPS >> row_groups_log2(rows);
                 for (int w = 0; w < wpr; ++w) {
                     t.x += sums[lane * wpr + w].x;
                     t.y += sums[lane * wpr + w].y;
                 }
             }
-            t.y *= unit_rstd;
-            if (lane < task_rows) {
+            t.y *= rstd;
+            if (lane < rows) {
                 float2* const rec = p.grad_partials + (record + lane) * TB_GN_PARTS;
                 rec[slot] = t;
-                if (p.mode == GRAD_STATS && slot == 0) {
+                if (slot == 0) {
                     // the slots of parts that do not exist
                     const int parts = p.parts[record / (p.N * p.C)];
                     for (int q = parts; q < TB_GN_PARTS; ++q) rec[q] = make_float2(0.f, 0.f);
-                }
-            }
-            __syncwarp();
-            if (both) {
-                Unit* const at = unit_at(p, first_row);
-                uint32_t before = 0;
-                if (lane == 0) {
-                    __threadfence();
-                    before = atomicAdd(&at->arrived, 1u);
-                }
-                before = __shfl_sync(0xffffffffu, before, 0);
-                if (before + 1u == (uint32_t)p.unit_tasks) {
-                    // the unit's last records: its u and v, for all dx tasks
-                    __threadfence();
-                    const float2 uv = unit_sums(p, dtype, unit_n, unit_g, unit_rstd, p.count);
-                    if (lane == 0) {
-                        at->u = uv.x;
-                        at->v = uv.y;
-                        __threadfence();
-                        atomicAdd(&at->arrived, 1u);
-                    }
                 }
             }
         }
@@ -338,69 +249,34 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
     const int lane = threadIdx.x & 31;
     // (the host keeps the tasks below 2^31: 32-bit divisions throughout, the
     // 64-bit ones took longer than a task's copies)
-    const uint32_t G = (uint32_t)p.G, K = (uint32_t)(p.C / p.G), units = (uint32_t)p.N * G;
-    const uint32_t T = (uint32_t)p.unit_tasks, lag = (uint32_t)p.lag;
-    const bool both = p.mode == GRAD_BOTH;
-    const uint32_t body = (both ? 2u : 1u) * units * T, total = body + (uint32_t)p.wtasks;
+    const uint32_t G = (uint32_t)p.G, K = (uint32_t)(p.C / p.G);
+    const uint32_t T = (uint32_t)p.unit_tasks;
+    const int64_t body = p.N * p.G * (int64_t)T;
+    const uint32_t begin = (uint32_t)(body * blockIdx.x / gridDim.x);
+    const uint32_t end = (uint32_t)(body * (blockIdx.x + 1) / gridDim.x);
+    const int kind = p.mode == GRAD_STATS ? TASK_STATS : TASK_APPLY;
     bool ok = true;
-    // GRAD_BOTH: tasks in order from the counter, the next one asked for while
-    // this one is copied; otherwise no task waits for another
-    uint32_t next = blockIdx.x;
-    auto ask = [&]() {
-        if (!both) next += gridDim.x;
-        else if (lane == 0) next = atomicAdd(&unit_at(p, 0)->tasks, 1u);
-    };
-    if (both) ask();
     auto claim = [&]() -> bool {  // the ring's next stage, once the computing warps are done with it
         ok = ok && bar_wait(ring.empty + ring.s * 8u, ring.parity ^ 1u, p.status);
         if (__any_sync(0xffffffffu, !ok) || *ring.dead) ok = false;
         return ok;
     };
-    while (true) {
-        const uint32_t task = __shfl_sync(0xffffffffu, next, 0);
-        if (task >= total) break;
-        ask();
-        int kind;
-        uint32_t unit = 0, item = 0;
-        if (task >= body) {
-            kind = TASK_WEIGHTS;
-            const int64_t c0 = (int64_t)(task - body) * GRAD_CHANNELS;
-            if (!claim()) break;
+    for (uint32_t w = blockIdx.x; w < (uint32_t)p.wtasks && claim(); w += gridDim.x) {
+        if (lane == 0) {
             Stage& d = ring.stage[ring.s];
-            if (lane == 0) {
-                d.kind = kind;
-                d.channel = c0;
-                bar_arrive(ring.full + ring.s * 8u);  // (no copies)
-                bar_arrive(ring.full + ring.s * 8u);
-                bar_arrive(ring.task + ring.s * 8u);
-            }
-            ring.next();
-            continue;
+            d.kind = TASK_WEIGHTS;
+            d.channel = (int64_t)w * GRAD_CHANNELS;
+            bar_arrive(ring.full + ring.s * 8u);  // (no copies)
+            bar_arrive(ring.full + ring.s * 8u);
+            bar_arrive(ring.task + ring.s * 8u);
         }
-        if (!both) {
-            kind = p.mode == GRAD_STATS ? TASK_STATS : TASK_APPLY;
-            unit = task / T;
-            item = task - unit * T;
-        } else if (task < lag * T) {
-            kind = TASK_STATS;
-            unit = task / T;
-            item = task - unit * T;
-        } else {
-            const uint32_t q = task - lag * T, pairs = 2u * (units - lag) * T;
-            if (q < pairs) {
-                const uint32_t block = (q >> 1) / T;
-                kind = (q & 1u) ? TASK_APPLY : TASK_STATS;
-                unit = (q & 1u) ? block : block + lag;
-                item = (q >> 1) - block * T;
-            } else {
-                kind = TASK_APPLY;
-                const uint32_t block = (q - pairs) / T;
-                unit = units - lag + block;
-                item = q - pairs - block * T;
-            }
-        }
-        // a unit's dx runs backwards: what was read last is the likeliest to be in L2
-        if (kind == TASK_APPLY) item = T - 1 - item;
+        ring.next();
+    }
+    for (uint32_t k = begin; k < end && ok; ++k) {
+        // the dx from the end of the run: what was read last is in L2
+        const uint32_t task = kind == TASK_APPLY ? end - 1 - (k - begin) : k;
+        const uint32_t unit = task / T;
+        uint32_t item = task - unit * T;
         int pp = 0;
         while ((uint32_t)p.task_start[pp + 1] <= item) ++pp;
         item -= (uint32_t)p.task_start[pp];
@@ -452,7 +328,6 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
                 d.record = pp * p.N * p.C + row;
                 d.n = (int32_t)n;
                 d.g = (int32_t)g;
-                d.unit = n * p.C + g * K;
                 d.channel = g * K + c_first;
                 d.out = reinterpret_cast<char*>(p.outs[pp]) + first * ES;
                 bar_arrive(ring.task + ring.s * 8u);
@@ -475,7 +350,6 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
             if (lane == 0) bar_arrive(bar);  // the elements copied one by one
             ring.next();
         }
-        if (!ok) break;
     }
     if (!ok) {
         // a wait ran out: everyone leaves, once the copies in flight have
@@ -518,14 +392,9 @@ __device__ __forceinline__ void compute_loop(const GnGradParams& p, Ring ring) {
             // a warp per channel adds up its records of all samples and sets
             const int64_t c = d.channel + warp;
             if (c < p.C) {
-                const bool both = p.mode == GRAD_BOTH;
-                const int64_t most = (int64_t)(both ? p.P : p.R) * p.N * TB_GN_PARTS;
                 float b = 0.f, a = 0.f;
-                for (int64_t q = lane; q < most; q += 32) {
-                    const int64_t set = q / TB_GN_PARTS;  // set * N + n
-                    const int slot = (int)(q - set * TB_GN_PARTS);
-                    if (both && slot >= p.parts[set / p.N]) continue;
-                    const float2 v = __ldcg(p.grad_partials + (set * p.C + c) * TB_GN_PARTS + slot);
+                for (int64_t q = lane; q < (int64_t)p.R * p.N * TB_GN_PARTS; q += 32) {
+                    const float2 v = p.grad_partials[(q / TB_GN_PARTS * p.C + c) * TB_GN_PARTS + q % TB_GN_PARTS];
                     b += v.x;
                     a += v.y;
                 }
@@ -681,6 +550,9 @@ __global__ void __launch_bounds__(GG_BLOCK, 1) gn_grad_kernel(const __grid_const
         bar_init_fence();
     }
     __syncthreads();
+    // the second pass may be placed as the first one's CTAs leave: a CTA fills
+    // its SM, so none of them takes a place that this grid still needs
+    if (p.mode == GRAD_STATS) pdl_trigger_dependents();
     grid_wait();
     if (threadIdx.x < GG_THREADS) compute_loop<DT, SILU>(p, ring);
     else if (threadIdx.x < GG_THREADS + 32) copy_loop<DT>(p, ring);
@@ -794,12 +666,8 @@ __global__ void __launch_bounds__(EL_BLOCK) gn_grad_apply_elem_kernel(const __gr
 template <int DT, bool SILU>
 cudaError_t grad_launch(const GnGradParams& p, bool ring, int sms, cudaStream_t s) {
     if (ring) {
-        const int64_t tasks = (p.mode == GRAD_BOTH ? 2 : 1) * p.N * p.G * (int64_t)p.unit_tasks + p.wtasks;
+        const int64_t body = p.N * p.G * (int64_t)p.unit_tasks, tasks = body > p.wtasks ? body : p.wtasks;
         if (tasks == 0) return cudaSuccess;
-        if (p.mode == GRAD_BOTH) {
-            const cudaError_t e = launch_pdl(gn_grad_units_kernel, p, dim3((unsigned)((p.N * p.G + 3) / 4)), 128, 0, s);
-            if (e != cudaSuccess) return e;
-        }
         cudaError_t e = cudaFuncSetAttribute(gn_grad_kernel<DT, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize, GG_SMEM);
         if (e != cudaSuccess) return e;
         return launch_pdl(gn_grad_kernel<DT, SILU>, p, dim3((unsigned)(tasks < sms ? tasks : sms)), GG_BLOCK, GG_SMEM, s);

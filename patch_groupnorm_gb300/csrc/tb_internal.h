@@ -425,8 +425,7 @@ cudaError_t launch_gn_apply(const GnApplyParams& p, int dtype, int64_t items, cu
 // What a launch of the backward pass does.
 enum GnGradMode : int32_t {
     GRAD_STATS = 0,  // write the records
-    GRAD_APPLY = 1,  // dx and the weight gradients from the records of R sets
-    GRAD_BOTH = 2    // both, each group's dx following its records in one launch
+    GRAD_APPLY = 1   // dx and the weight gradients from the records of R sets
 };
 
 struct GnGradParams {
@@ -446,7 +445,6 @@ struct GnGradParams {
     int32_t mode;
     float eps;
     int32_t silu;
-    float count;                   // elements of a group in all patches (GRAD_BOTH)
     uint32_t* status;              // device status word (a wait that runs out is recorded there)
     // The ring kernel's work: every group of every sample (a unit) is cut into
     // unit_tasks tasks, patch p's being task_start[p] .. task_start[p + 1] - 1:
@@ -456,7 +454,6 @@ struct GnGradParams {
     int64_t part_elems[GN_MAXP];   // elements of every part but the last
     int32_t task_start[GN_MAXP + 1];
     int32_t unit_tasks;
-    int32_t lag;                   // GRAD_BOTH: units whose records run ahead of the first dx
     int32_t wtasks;                // tasks of GRAD_CHANNELS weight gradients each
 };
 static_assert(sizeof(GnGradParams) <= 32000, "kernel parameter block too large");
@@ -464,10 +461,6 @@ static_assert(sizeof(GnGradParams) <= 32000, "kernel parameter block too large")
 constexpr int GRAD_STAGE_BYTES = 32768;  // of x, and of dy, in one ring stage
 constexpr int GRAD_MAX_ROWS = 31;        // channel rows of one task
 constexpr int GRAD_CHANNELS = 16;        // channels of one weight-gradient task
-// GRAD_BOTH keeps the units' counters and statistics in the last two record
-// slots of their first rows, so it cuts rows into fewer parts.
-constexpr int GRAD_BOTH_PARTS = TB_GN_PARTS - 3;
-
 // ring: patches, gradients and outputs share their offset from 16-byte
 // boundaries (the ring kernel); otherwise the element kernels run.
 cudaError_t launch_gn_grad(const GnGradParams& p, int dtype, bool ring, int sms, cudaStream_t s);

@@ -11,11 +11,6 @@
 
 #define TB_API extern "C" __attribute__((visibility("default")))
 
-// GroupNorm backward in one launch: tasks per SM by which the records run ahead.
-#ifndef TB_GN_GRAD_LAG
-#define TB_GN_GRAD_LAG 16
-#endif
-
 namespace {
 
 tb_status launched(cudaError_t e) {
@@ -189,11 +184,7 @@ tb_status gn_grad_params(tb::GnGradParams& prm, bool* ring, const void* const* p
 tb_status gn_grad_tasks(tb::GnGradParams& prm, int mode, tb_dtype dtype, int sms) {
     const int es = elem_bytes(dtype), vec = 16 / es;
     const int64_t K = prm.C / prm.G, units = prm.N * prm.G;
-    const int most_parts = mode == tb::GRAD_BOTH ? tb::GRAD_BOTH_PARTS : TB_GN_PARTS;
     prm.mode = mode;
-    double count = 0.0;
-    for (int p = 0; p < prm.P; ++p) count += (double)K * (double)prm.spatial[p];
-    prm.count = (float)count;
     for (int p = 0; p < prm.P; ++p) {
         const int64_t row = prm.spatial[p] * es;
         prm.rows[p] = prm.parts[p] = 0;
@@ -201,7 +192,7 @@ tb_status gn_grad_tasks(tb::GnGradParams& prm, int mode, tb_dtype dtype, int sms
         const int64_t fit = row > 0 ? tb::GRAD_STAGE_BYTES / row : tb::GRAD_MAX_ROWS;
         prm.rows[p] = (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fit, tb::GRAD_MAX_ROWS), K));
         const int64_t want = (row + tb::GRAD_STAGE_BYTES - 1) / tb::GRAD_STAGE_BYTES;
-        prm.parts[p] = (int32_t)std::max<int64_t>(1, std::min<int64_t>(want, most_parts));
+        prm.parts[p] = (int32_t)std::max<int64_t>(1, std::min<int64_t>(want, (int64_t)TB_GN_PARTS));
     }
     auto tasks_of = [&](int p) {
         if (prm.rows[p] == 0) return (int64_t)0;
@@ -216,7 +207,7 @@ tb_status gn_grad_tasks(tb::GnGradParams& prm, int mode, tb_dtype dtype, int sms
             if (prm.rows[p] > 1) {
                 prm.rows[p] = (prm.rows[p] + 1) / 2;
                 smaller = true;
-            } else if (prm.rows[p] == 1 && prm.parts[p] < most_parts &&
+            } else if (prm.rows[p] == 1 && prm.parts[p] < TB_GN_PARTS &&
                        prm.spatial[p] / vec / (prm.parts[p] + 1) >= 256) {
                 ++prm.parts[p];
                 smaller = true;
@@ -233,10 +224,7 @@ tb_status gn_grad_tasks(tb::GnGradParams& prm, int mode, tb_dtype dtype, int sms
     }
     prm.task_start[prm.P] = (int32_t)at;
     prm.unit_tasks = (int32_t)at;
-    if (2.0 * (double)units * (double)at + prm.wtasks > 2.0e9) return TB_ERR_UNSUPPORTED;
-    // the records run two tasks per SM ahead: by then a CTA has done with what
-    // it holds, and no dx task waits
-    prm.lag = (int32_t)std::min<int64_t>(units, (TB_GN_GRAD_LAG * sms + at - 1) / std::max<int64_t>(at, 1));
+    if ((double)units * (double)at > 2.0e9) return TB_ERR_UNSUPPORTED;
     return TB_OK;
 }
 
@@ -428,32 +416,4 @@ TB_API tb_status tb_patch_gn_grad_apply(const void* const* patches, const void* 
     TB_TRY(tb::sm_count(&sms));
     TB_TRY(gn_grad_tasks(prm, tb::GRAD_APPLY, dtype, sms));
     return launched(tb::launch_gn_grad(prm, (int)dtype, ring, sms, reinterpret_cast<cudaStream_t>(stream)));
-}
-
-TB_API tb_status tb_patch_gn_backward(const void* const* patches, const void* const* grads, void* const* outs,
-                                      int32_t P, tb_dtype dtype, int64_t N, int64_t C, const int64_t* spatial,
-                                      int32_t G, const tb_gn_partial* partials, const void* gamma, const void* beta,
-                                      float eps, int32_t silu, void* dgamma, void* dbeta,
-                                      tb_gn_grad_partial* grad_partials, void* stream) {
-    tb::GnGradParams prm;
-    bool ring = false;
-    if (outs == nullptr) return TB_ERR_NULL;
-    TB_TRY(gn_grad_params(prm, &ring, patches, grads, outs, P, dtype, N, C, spatial, G, partials, P, gamma, beta, eps,
-                          silu, grad_partials, dgamma, dbeta));
-    if (C == 0 || (N == 0 && prm.wtasks == 0)) return TB_OK;
-    int sms = 0;
-    TB_TRY(tb::sm_count(&sms));
-    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    bool any = false;
-    for (int p = 0; p < P; ++p) any = any || spatial[p] > 0;
-    if (ring && N > 0 && any) {
-        TB_TRY(gn_grad_tasks(prm, tb::GRAD_BOTH, dtype, sms));
-        return launched(tb::launch_gn_grad(prm, (int)dtype, true, sms, s));
-    }
-    if (N > 0) {
-        TB_TRY(gn_grad_tasks(prm, tb::GRAD_STATS, dtype, sms));
-        TB_TRY(launched(tb::launch_gn_grad(prm, (int)dtype, ring, sms, s)));
-    }
-    TB_TRY(gn_grad_tasks(prm, tb::GRAD_APPLY, dtype, sms));
-    return launched(tb::launch_gn_grad(prm, (int)dtype, ring, sms, s));
 }

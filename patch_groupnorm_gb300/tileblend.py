@@ -157,9 +157,6 @@ _lib.tb_patch_gn_grad_stats.argtypes = [_P_vp, _P_vp, _i32, ctypes.c_int, _i64, 
 _lib.tb_patch_gn_grad_apply.restype = ctypes.c_int
 _lib.tb_patch_gn_grad_apply.argtypes = [_P_vp, _P_vp, _P_vp, _i32, ctypes.c_int, _i64, _i64, _P_i64, _i32, _vp, _vp,
                                         _i32, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp]
-_lib.tb_patch_gn_backward.restype = ctypes.c_int
-_lib.tb_patch_gn_backward.argtypes = [_P_vp, _P_vp, _P_vp, _i32, ctypes.c_int, _i64, _i64, _P_i64, _i32, _vp, _vp, _vp,
-                                      ctypes.c_float, _i32, _vp, _vp, _vp, _vp]
 TB_LN_PARTS = 512
 TB_MAX_GRADS, TB_GRAD_TABLE, TB_GRAD_PARTS = 65536, 1024, 1024
 
@@ -170,7 +167,7 @@ EXPORTED = ("tb_version", "tb_status_string", "tb_last_cuda_error", "tb_axis_lay
             "tb_gather_patches", "tb_device_status", "tb_ramp_axis_spread", "tb_stitch_shard_frames_layout",
             "tb_stitch_halo_pack_frames", "tb_stitch3d_shard_frames", "tb_layer_norm", "tb_layer_norm_workspace",
             "tb_layer_norm_backward", "tb_grad_records", "tb_grad_stats", "tb_grad_norm", "tb_grad_clip",
-            "tb_patch_gn_grad_stats", "tb_patch_gn_grad_apply", "tb_patch_gn_backward")
+            "tb_patch_gn_grad_stats", "tb_patch_gn_grad_apply")
 
 
 class TileBlendError(RuntimeError):
@@ -1150,23 +1147,6 @@ def tb_patch_gn_grad_apply(grads: Sequence[torch.Tensor], patches: Sequence[torc
     return dxs
 
 
-def tb_patch_gn_backward(grads: Sequence[torch.Tensor], patches: Sequence[torch.Tensor], dxs: Sequence[torch.Tensor],
-                         G: int, partials: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor],
-                         eps: float, dgamma: Optional[torch.Tensor], dbeta: Optional[torch.Tensor],
-                         grad_partials: torch.Tensor, silu: bool = True, stream=None) -> Sequence[torch.Tensor]:
-    """Both steps in one pass for patches that are all here;
-    ``grad_partials`` (from ``new_grad_partials``) is its workspace."""
-    P = len(patches)
-    N, C, dt, sp, xs, ds = _gn_grad_args(grads, patches, G, partials, P, gamma, beta)
-    os_, gp, bp = _gn_grad_outs(dxs, patches, C, dgamma, dbeta)
-    _check(_lib.tb_patch_gn_backward(xs, ds, os_, P, dt, N, C, sp, G, partials.data_ptr(),
-                                     gamma.data_ptr() if gamma is not None else None,
-                                     beta.data_ptr() if beta is not None else None, eps, 1 if silu else 0, gp, bp,
-                                     _grad_partials(grad_partials, P, N, C),
-                                     _stream_of(stream, patches[0].get_device())), "tb_patch_gn_backward")
-    return dxs
-
-
 def patch_group_norm_backward(grads: Sequence[torch.Tensor], patches: Sequence[torch.Tensor], G: int,
                               partials: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor],
                               eps: float, silu: bool = True, dxs: Optional[Sequence[torch.Tensor]] = None,
@@ -1189,5 +1169,15 @@ def patch_group_norm_backward(grads: Sequence[torch.Tensor], patches: Sequence[t
                 new_grad_partials(P, N, C, patches[0].device) if grad_partials is None else grad_partials)
     if dxs is None or dgamma is None or dbeta is None or grad_partials is None:
         dxs, dgamma, dbeta, grad_partials = _on_stream(make, stream)
-    tb_patch_gn_backward(grads, patches, dxs, G, partials, gamma, beta, eps, dgamma, dbeta, grad_partials, silu, stream)
+    # one check and one set of argument arrays for both calls
+    N, C, dt, sp, xs, ds = _gn_grad_args(grads, patches, G, partials, P, gamma, beta)
+    os_, gp, bp = _gn_grad_outs(dxs, patches, C, dgamma, dbeta)
+    rec, grec = partials.data_ptr(), _grad_partials(grad_partials, P, N, C)
+    ga = gamma.data_ptr() if gamma is not None else None
+    be = beta.data_ptr() if beta is not None else None
+    handle, act = _stream_of(stream, patches[0].get_device()), 1 if silu else 0
+    _check(_lib.tb_patch_gn_grad_stats(xs, ds, P, dt, N, C, sp, G, rec, P, ga, be, eps, act, grec, handle),
+           "tb_patch_gn_grad_stats")
+    _check(_lib.tb_patch_gn_grad_apply(xs, ds, os_, P, dt, N, C, sp, G, rec, grec, P, ga, be, eps, act, gp, bp, handle),
+           "tb_patch_gn_grad_apply")
     return dxs, dgamma, dbeta

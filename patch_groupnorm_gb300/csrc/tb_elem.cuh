@@ -314,6 +314,31 @@ __device__ __forceinline__ void bulk_load_once(uint32_t dst, const void* src, ui
         "l"(src), "r"(bytes), "r"(bar), "l"(policy)
         : "memory");
 }
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// One of the elements on either side of a bulk copy, into shared memory.
+template <int ES>
+__device__ __forceinline__ void copy_element(uint32_t to, const char* from) {
+    if constexpr (ES == 4) {
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(*reinterpret_cast<const uint32_t*>(from)) : "memory");
+    } else {
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(*reinterpret_cast<const unsigned short*>(from))
+                     : "memory");
+    }
+}
+template <int ES>
+__device__ __forceinline__ uint32_t smem_element(uint32_t at) {
+    if constexpr (ES == 4) {
+        uint32_t v;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+        return v;
+    } else {
+        unsigned short v;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+        return v;
+    }
+}
 template <typename W>
 __device__ __forceinline__ W smem_load(uint32_t at) {
     static_assert(sizeof(W) == 16, "16-byte words");

@@ -64,10 +64,6 @@ struct Stage {
     float2 row[GRAD_MAX_ROWS + 1];  // (rstd * gamma, beta) of each row
 };
 
-__device__ __forceinline__ void bar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
 // dz of one pair of elements (see the top of this file).  e^-z and the
 // reciprocal are approximate (2^-22 each); e^-z overflows for z < -88, where
 // s = 0 and dz = 0 (its true size is below 1e-36 of dy).
@@ -228,17 +224,6 @@ __device__ __forceinline__ void constants_loop(const GnGradParams& p, int dtype,
                 }
             }
         }
-    }
-}
-
-// One of the elements on either side of a bulk copy, into shared memory.
-template <int ES>
-__device__ __forceinline__ void copy_element(uint32_t to, const char* from) {
-    if constexpr (ES == 4) {
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(*reinterpret_cast<const uint32_t*>(from)) : "memory");
-    } else {
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(*reinterpret_cast<const unsigned short*>(from))
-                     : "memory");
     }
 }
 

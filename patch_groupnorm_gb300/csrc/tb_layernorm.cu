@@ -11,12 +11,20 @@
 // second pass over registers, so an outlier or a large offset costs no
 // precision) and the output.  The next row's chunks are requested before the
 // current row is reduced.
+//
+// Bound by memory: 16384 x 4096 bf16 with residual moves 537 MB in 82.5 us (6.5
+// TB/s, 97 % of the measured copy rate), 65536 x 512 bf16 134 MB in 25.5 us (79
+// %, where ten shuffles a row per warp count).  Rows of single elements (no
+// 16-byte words) load 2 bytes a lane: 65536 x 515 bf16 takes 72 us.  One row of
+// 4096 takes 8 us, all of it the call.
 #include "tb_layernorm.cuh"
 
 namespace tb {
 namespace {
 
-// CTAs per SM the forward kernel is compiled for.
+// CTAs per SM the forward kernel is compiled for: 768 threads of 85 registers.
+// (16384 x 4096 bf16 with residual, f32 weights: 1024 / 768 / 512 threads take
+// 93.7 / 82.4 / 89.2 us; the first spill, the last have too few loads in flight.)
 #ifndef TB_LN_FWD_THREADS
 #define TB_LN_FWD_THREADS 768
 #endif
@@ -235,10 +243,15 @@ cudaError_t fwd_dt(const LnFwdParams& p, bool vector, int sms, cudaStream_t s) {
         if (n <= 4096) return fwd_launch<DT, V, 1024, 4>(p, sms, s);
         return fwd_long<DT, V>(p, sms, s);
     }
+    // (16 columns a thread from 2049 on: with 8, bf16 rows of 4095 / 5001 / 8191
+    // took 105 / 158 / 103 us instead of 76 / 108 / 78, and with 16 below, rows of
+    // 515 / 2047 took 77 / 79 us instead of 72 / 77; 67 M elements, at most 65536 rows)
     if (p.cols <= 256) return fwd_launch<DT, 1, 32, 8>(p, sms, s);
+    if (p.cols <= 512) return fwd_launch<DT, 1, 64, 8>(p, sms, s);
     if (p.cols <= 1024) return fwd_launch<DT, 1, 128, 8>(p, sms, s);
     if (p.cols <= 2048) return fwd_launch<DT, 1, 256, 8>(p, sms, s);
-    if (p.cols <= 4096) return fwd_launch<DT, 1, 512, 8>(p, sms, s);
+    if (p.cols <= 4096) return fwd_launch<DT, 1, 256, 16>(p, sms, s);
+    if (p.cols <= 8192) return fwd_launch<DT, 1, 512, 16>(p, sms, s);
     if (p.cols <= 16384) return fwd_launch<DT, 1, 1024, 16>(p, sms, s);
     return fwd_long<DT, 1>(p, sms, s);
 }

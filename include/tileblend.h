@@ -1,6 +1,7 @@
 /*
- * tileblend.h -- C ABI of libtileblend: tiled-VAE tile stitching and
- * patch-parallel GroupNorm on NVIDIA GB300 (sm_103a).
+ * tileblend.h -- C ABI of libtileblend: tiled-VAE tile stitching,
+ * patch-parallel GroupNorm, and the norms and gradient clipping of a training
+ * step on NVIDIA GB300 (sm_103a).
  *
  * Sources of the operations (web pages, cited by title and section):
  *   [VTB] "[Proposal] Vectorize tiled VAE blending while preserving rounding
@@ -618,7 +619,7 @@ tb_status tb_patch_group_norm_noalloc(const void* const* patches, void* const* o
  * otherwise); 16-byte aligned tensors whose rows are whole 16-byte chunks
  * take the vector path.  Results are deterministic: no atomics, every sum in
  * an order fixed by the sizes and the GPU.  Captured into a CUDA graph and
- * replayed with new contents (tested): all of them.
+ * replayed with new contents (tested): all but tb_grad_norm.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -675,6 +676,9 @@ int64_t tb_layer_norm_workspace(int64_t rows, int64_t cols);
  *                tb_layer_norm_workspace(rows, cols); may be NULL when
  *                neither weight gradient is wanted or rows == 0.  Its contents
  *                need no clearing and are not kept
+ * The kernel waits for its copies into shared memory at most about a second; a
+ * wait that runs out is reported as TB_DEV_WAIT_TIMEOUT by tb_device_status and
+ * leaves the outputs unfinished.
  * Errors: as tb_layer_norm, TB_ERR_SHAPE also for a workspace too small.
  */
 tb_status tb_layer_norm_backward(const void* dy, int64_t dy_ld, const void* x, int64_t x_ld, tb_dtype dtype,

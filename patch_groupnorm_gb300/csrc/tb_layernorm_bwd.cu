@@ -23,13 +23,11 @@ constexpr int LN_BWD_MAX_STAGES = 8;
 // 16384 x 4096 with dtotal and 112 / 216 KB 111 / 92 (two CTAs per SM).
 constexpr int64_t ln_bwd_room(int tpr) { return (tpr <= 32 ? 144 : 216) * 1024; }
 
-// Threads per CTA: a row's threads, at least 16 warps.  One CTA per SM: 512
-// threads of 128 registers, and one partial weight gradient each.
-#ifndef TB_LN_BWD_BLOCK
-#define TB_LN_BWD_BLOCK 512
-#endif
-__host__ __device__ constexpr int bwd_block(int tpr) { return tpr < TB_LN_BWD_BLOCK ? TB_LN_BWD_BLOCK : tpr; }
-__host__ __device__ constexpr int bwd_ctas(int tpr) { return 512 / bwd_block(tpr) > 1 ? 512 / bwd_block(tpr) : 1; }
+// Threads per CTA, one CTA per SM: 128 registers a thread, and one partial
+// weight gradient each.  Rows past 1024 words take four words a thread; 1024
+// threads of 64 registers with two words each took 138 us where they take 133
+// (4096 x 16384 bf16; 161 / 145 with dtotal, 185 / 131 at 12001 columns).
+constexpr int BWD_BLOCK = 512;
 
 // Each thread keeps the weight gradients of its own columns over all rows
 // its CTA takes; the CTA's sums go to workspace[part][2][cols] (dgamma, then
@@ -47,18 +45,18 @@ __host__ __device__ constexpr int bwd_ctas(int tpr) { return 512 / bwd_block(tpr
 // copied one by one, and thread t takes the columns t + j * TPR, whose
 // neighbours lie in neighbouring lanes.
 template <int DT, int TPR, int CPT, bool TOT, bool WHOLE>
-__global__ void __launch_bounds__(bwd_block(TPR), bwd_ctas(TPR))
+__global__ void __launch_bounds__(BWD_BLOCK, 1)
     ln_bwd_kernel(const __grid_constant__ LnBwdParams p) {
     constexpr int ES = elem_size(DT), VEC = 16 / ES;
     using E = typename Word<ES>::T;
     using L = Lanes<VEC>;
     using T = typename L::T;
-    constexpr int BLOCK = bwd_block(TPR);
+    constexpr int BLOCK = BWD_BLOCK;
     constexpr int RPC = BLOCK / TPR;
     constexpr int WPR = TPR / 32;
     constexpr int HOLD = TPR < 32 ? TPR : 32;  // lanes of a warp in one row group
     constexpr int NT = TOT ? 3 : 2;
-    constexpr bool LEAN = TPR >= 1024;  // 64 registers a thread: nothing but the weight gradients is kept
+    constexpr bool LEAN = CPT > 2;  // no registers left for anything but the weight gradients
     __shared__ float2 s_sum[2][BLOCK / 32];
     __shared__ __align__(8) unsigned long long s_bar[RPC * LN_BWD_MAX_STAGES];
     extern __shared__ __align__(16) unsigned char s_rows[];  // [RPC][stages][NT][pitch]; then the CTA's sums
@@ -379,13 +377,13 @@ __global__ void __launch_bounds__(bwd_block(TPR), bwd_ctas(TPR))
 constexpr int64_t ELEM_COLS = 4096;
 
 template <int DT, int TPR, int CPT, bool TOT>
-__global__ void __launch_bounds__(bwd_block(TPR), bwd_ctas(TPR))
+__global__ void __launch_bounds__(BWD_BLOCK, 1)
     ln_bwd_elem_kernel(const __grid_constant__ LnBwdParams p) {
     constexpr int VEC = 1;
     using W = typename Word<elem_size(DT)>::T;
     using L = Lanes<VEC>;
     using T = typename L::T;
-    constexpr int BLOCK = bwd_block(TPR);
+    constexpr int BLOCK = BWD_BLOCK;
     constexpr int RPC = BLOCK / TPR;
     constexpr int WPR = TPR / 32;
     __shared__ float2 s_sum[2][BLOCK / 32];
@@ -674,16 +672,15 @@ __global__ void __launch_bounds__(32 * WG_SLICES) ln_wgrad_kernel(const __grid_c
 
 template <int DT, int TPR, int CPT, bool WHOLE>
 cudaError_t bwd_launch(const LnBwdParams& p, int sms, int* parts, cudaStream_t s) {
-    constexpr int VEC = 16 / elem_size(DT), rpc = bwd_block(TPR) / TPR;
+    constexpr int VEC = 16 / elem_size(DT), rpc = BWD_BLOCK / TPR;
     const int64_t want = (p.rows + rpc - 1) / rpc;
-    int64_t grid = (int64_t)sms * bwd_ctas(TPR);
-    if (grid > TB_LN_PARTS) grid = TB_LN_PARTS;
+    int64_t grid = sms < TB_LN_PARTS ? sms : TB_LN_PARTS;
     if (grid > want) grid = want;
     *parts = (int)grid;
     LnBwdParams q = p;
     const int64_t bytes = p.cols * elem_size(DT), pitch = WHOLE ? bytes : (bytes + 31) / 16 * 16;
     const int64_t stage = (int64_t)rpc * (p.dtotal ? 3 : 2) * pitch;
-    const int64_t fit = ln_bwd_room(TPR) / bwd_ctas(TPR) / stage;
+    const int64_t fit = ln_bwd_room(TPR) / stage;
     q.stages = (int)(fit < 2 ? 2 : fit > LN_BWD_MAX_STAGES ? LN_BWD_MAX_STAGES : fit);
     int64_t smem = rpc > 1 ? (int64_t)rpc * 2 * CPT * VEC * (TPR + 4) * 4 : 0;
     if (smem < q.stages * stage) smem = q.stages * stage;
@@ -693,7 +690,7 @@ cudaError_t bwd_launch(const LnBwdParams& p, int sms, int* parts, cudaStream_t s
         const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(fn, q, dim3((unsigned)grid), bwd_block(TPR), (size_t)smem, s);
+    return launch_pdl(fn, q, dim3((unsigned)grid), BWD_BLOCK, (size_t)smem, s);
 }
 
 template <int DT, int VEC>
@@ -707,15 +704,14 @@ cudaError_t bwd_long(const LnBwdParams& p, int sms, int* parts, cudaStream_t s) 
 
 template <int DT, int TPR, int CPT>
 cudaError_t bwd_elem(const LnBwdParams& p, int sms, int* parts, cudaStream_t s) {
-    constexpr int rpc = bwd_block(TPR) / TPR;
+    constexpr int rpc = BWD_BLOCK / TPR;
     const int64_t want = (p.rows + rpc - 1) / rpc;
-    int64_t grid = (int64_t)sms * bwd_ctas(TPR);
-    if (grid > TB_LN_PARTS) grid = TB_LN_PARTS;
+    int64_t grid = sms < TB_LN_PARTS ? sms : TB_LN_PARTS;
     if (grid > want) grid = want;
     *parts = (int)grid;
     const size_t smem = rpc > 1 ? (size_t)rpc * 2 * CPT * (TPR + 4) * 4 : 0;  // at most 37 KB
     return launch_pdl(p.dtotal ? ln_bwd_elem_kernel<DT, TPR, CPT, true> : ln_bwd_elem_kernel<DT, TPR, CPT, false>, p,
-                      dim3((unsigned)grid), bwd_block(TPR), smem, s);
+                      dim3((unsigned)grid), BWD_BLOCK, smem, s);
 }
 
 // A row's 16-byte words, or columns, pick its threads.
@@ -732,7 +728,7 @@ cudaError_t bwd_dt(const LnBwdParams& p, bool vector, int sms, int* parts, cudaS
         if (n <= 256) return bwd_launch<DT, 128, 2, true>(p, sms, parts, s);
         if (n <= 512) return bwd_launch<DT, 256, 2, true>(p, sms, parts, s);
         if (n <= 1024) return bwd_launch<DT, 512, 2, true>(p, sms, parts, s);
-        if (n <= 2048) return bwd_launch<DT, 1024, 2, true>(p, sms, parts, s);
+        if (n <= 2048) return bwd_launch<DT, 512, 4, true>(p, sms, parts, s);
         return bwd_long<DT, V>(p, sms, parts, s);
     }
     if (p.cols <= 256) return bwd_elem<DT, 32, 8>(p, sms, parts, s);
@@ -741,7 +737,7 @@ cudaError_t bwd_dt(const LnBwdParams& p, bool vector, int sms, int* parts, cudaS
     if (p.cols <= 2048) return bwd_elem<DT, 256, 8>(p, sms, parts, s);
     if (p.cols <= ELEM_COLS) return bwd_elem<DT, 512, 8>(p, sms, parts, s);
     if (n <= 1024) return bwd_launch<DT, 512, 2, false>(p, sms, parts, s);
-    if (n <= 2048) return bwd_launch<DT, 1024, 2, false>(p, sms, parts, s);
+    if (n <= 2048) return bwd_launch<DT, 512, 4, false>(p, sms, parts, s);
     return bwd_long<DT, 1>(p, sms, parts, s);
 }
 

@@ -154,6 +154,20 @@ def test_layer_norm_row_counts(tbl, rows, cols, dtype):
 
 
 @pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("cols", [5001, 8192, 8191, 12008, 12001, 16384, 16383])
+def test_layer_norm_wide_rows_many_to_a_cta(tbl, cols, dtype):
+    # every row buffer of the backward kernel is filled and read several times
+    dt = DT[dtype]
+    if dtype == "f32":
+        cols = (cols + 1) // 2
+    rows = 1001
+    gamma, beta = weights_of(6, cols, dt)
+    x, dy = rows_of(1, (rows, cols), dt, 1.0, 0.1), rows_of(2, (rows, cols), dt, 0.1)
+    run_ln(tbl, x, gamma, beta, 1e-6, dy)
+    run_ln(tbl, x, gamma, beta, 1e-6, dy, dtotal=rows_of(3, (rows, cols), dt))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
 def test_layer_norm_more_long_rows_than_ctas(tbl, dtype):
     # the long-row kernels loop over rows, the weight gradients add up in each
     # CTA's own slice; more rows than workspace parts

@@ -10,9 +10,10 @@
 // same bits every time) and scale their pieces, walking them from the last
 // to the first: the pieces the first kernel read last are still in L2.
 //
-// Bound by memory: 368 M elements (1024-wide blocks, bf16) are read at 6.7 TB/s
-// by the first kernel (110 us) and read and written at 6.4 TB/s by the second (229
-// us).  3.5 M fp32 elements take 10 us, the time of the two launches.
+// Bound by memory: 368 M elements (1024-wide blocks, bf16) take 344 us, the read
+// by the first kernel (736 MB; 124 us timed alone) and the read and write by the
+// second (229 us alone, 6.4 TB/s).  3.5 M fp32 elements take 10 us, the time of
+// the two launches.
 //
 // Within a piece a thread adds the squares of its elements in fp32, and it
 // carries the pieces' sums with their rounding errors.  A thread whose fp32
@@ -25,7 +26,10 @@ namespace tb {
 namespace {
 
 constexpr int GC_BLOCK = 256;
-constexpr int GC_CTAS = 6;                                    // per SM
+constexpr int GC_CTAS = 5;                                    // per SM: 344 us where 6 take 347 and 4 346
+// The last pieces of each CTA's run are the ones that grad_clip_kernel takes first; those before them are
+// read evict-first, so that these stay in L2: 8 x 16 KB x 760 CTAs, 100 MB (344 us; all read alike 354).
+constexpr int GC_KEEP = 8;
 constexpr int GC_CPT = GRAD_PIECE_BYTES / (GC_BLOCK * 16);    // chunks per thread and piece
 
 // The tensor that piece `piece` belongs to.
@@ -90,7 +94,7 @@ struct Squares {
 
 template <int DT>
 __device__ __forceinline__ void piece_squares(Squares& acc, const void* base, int64_t numel, const Piece& c,
-                                              uint32_t* status) {
+                                              uint32_t* status, bool keep) {
     constexpr int VEC = 16 / elem_size(DT);
     const char* const b = reinterpret_cast<const char*>(base);
     const int64_t bytes = numel * elem_size(DT);
@@ -100,7 +104,7 @@ __device__ __forceinline__ void piece_squares(Squares& acc, const void* base, in
     for (int k = 0; k < GC_CPT; ++k) {
         const int i = threadIdx.x + k * GC_BLOCK;
         v[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (i < c.n && in_bounds(src + i, 16, b, bytes, status)) v[k] = src[i];
+        if (i < c.n && in_bounds(src + i, 16, b, bytes, status)) v[k] = keep ? src[i] : __ldcs(src + i);
     }
     // the head and the rest are fewer than VEC elements each
     uint32_t one = 0u;
@@ -153,9 +157,10 @@ __global__ void __launch_bounds__(GC_BLOCK, GC_CTAS) grad_stats_kernel(const __g
         while (p.start[t + 1] <= piece) ++t;
         const Piece c = piece_of(p, t, piece);
         const int dt = p.dtype[t];
-        if (dt == F32) piece_squares<F32>(acc, p.in[t], p.numel[t], c, p.status);
-        else if (dt == F16) piece_squares<F16>(acc, p.in[t], p.numel[t], c, p.status);
-        else piece_squares<BF16>(acc, p.in[t], p.numel[t], c, p.status);
+        const bool keep = end - piece <= GC_KEEP;
+        if (dt == F32) piece_squares<F32>(acc, p.in[t], p.numel[t], c, p.status, keep);
+        else if (dt == F16) piece_squares<F16>(acc, p.in[t], p.numel[t], c, p.status, keep);
+        else piece_squares<BF16>(acc, p.in[t], p.numel[t], c, p.status, keep);
     }
     const float sum = block_sum(acc.sum + acc.err, s_part[0]);
     const bool scaled = __syncthreads_or(acc.small != 0.f || acc.large != 0.f);

@@ -13,7 +13,7 @@
 // of two launches of gn_grad_kernel: GRAD_STATS leaves the records (B, A) of
 // every channel, GRAD_APPLY writes dx.  A CTA takes the same contiguous run of
 // tasks (some rows of a group, or a part of one) in both, the second time from
-// its end, where the first has left its rows in L2.  One launch with both
+// its end, where the first has left its rows in L2 (about 100 MB of them).  One launch with both
 // passes interleaved, a group's dx following its records by 15 to 60 MB, was
 // built and measured: it reads memory once, but its waits cost what that saves
 // (4D 61 us, 5D 185, as the two launches take), because computing, not memory,
@@ -40,6 +40,11 @@ constexpr int GG_LOG2 = 4, GG_WARPS = 1 << GG_LOG2;  // computing warps
 constexpr int GG_THREADS = GG_WARPS * 32;
 constexpr int GG_STAGES = 3;
 constexpr int GG_BLOCK = GG_THREADS + 32 * (1 + GG_STAGES);  // + the copying warp, and a warp of constants per stage
+// Bytes of x (and of dy) at the end of each CTA's run that L2 is to keep for the
+// second launch, 97 MB over 152 CTAs; GRAD_STATS reads what comes before
+// them evict-first.  (4D / 5D with 192, 256, 320, 384 KB and all alike:
+// 63.7 / 200, 62.9 / 199, 62.5 / 199, 62.8 / 200, 63.2 / 206 us.)
+constexpr int64_t GG_KEEP = 320 * 1024;
 constexpr int GG_TENSOR = GRAD_STAGE_BYTES + 128;  // room for a first, partial word
 constexpr int GG_SMEM = GG_STAGES * 2 * GG_TENSOR;
 constexpr int GG_SLOTS = GG_THREADS;               // a lane's sums each, or a warp's of every row
@@ -287,6 +292,7 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
         const char* const xbase = reinterpret_cast<const char*>(p.patches[pp]);
         const char* const dbase = reinterpret_cast<const char*>(p.grads[pp]);
         constexpr int64_t MOST = GRAD_STAGE_BYTES / ES;
+        const bool once = kind == TASK_APPLY || (int64_t)(end - k) * rows * (e1 - e0) * ES > GG_KEEP;
         // (one stage for whole rows; the stages of a part in turn)
         // (an empty patch's rows still get their records)
         for (int64_t at = e0; (at < e1 || at == e0) && ok; at += MOST) {
@@ -319,7 +325,7 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
             }
             __syncwarp();
             if ((lane & 15) == 0 && bulk > 0) {
-                if (kind == TASK_APPLY) bulk_load_once(to + head, from + head, bulk, bar);
+                if (once) bulk_load_once(to + head, from + head, bulk, bar);
                 else bulk_load(to + head, from + head, bulk, bar);
             }
             if (bytes != bulk) {

@@ -15,8 +15,8 @@
 // tasks (some rows of a group, or a part of one) in both, the second time from
 // its end, where the first has left its rows in L2 (about 100 MB of them).  One launch with both
 // passes interleaved, a group's dx following its records by 15 to 60 MB, was
-// built and measured: it reads memory once, but its waits cost what that saves
-// (4D 61 us, 5D 185, as the two launches take), because computing, not memory,
+// built and measured: it reads memory once, but its waits cost most of what that
+// saves (4D 61.8 us, 5D 184; the two launches 62.5 and 199), because computing, not memory,
 // is the longer half: the SiLU derivative takes about 11 instructions a pair of
 // elements in each pass, and the kernel issues an instruction in 55 % of all
 // cycles.

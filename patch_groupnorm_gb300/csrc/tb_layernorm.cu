@@ -6,7 +6,8 @@
 //     y = rnd((h - mean) * rstd * gamma + beta)
 // Sums and statistics are fp32; every output is rounded once.
 //
-// A row is held by TPR threads, CPT chunks each, in registers and in its
+// A row is held by TPR threads (fewer than a warp where rows are short), CPT
+// chunks each, in registers and in its
 // storage type: one read of the row serves the mean, the squares about it (a
 // second pass over registers, so an outlier or a large offset costs no
 // precision) and the output.  The next row's chunks are requested before the
@@ -14,9 +15,9 @@
 //
 // Bound by memory: 16384 x 4096 bf16 with residual moves 537 MB in 82.5 us (6.5
 // TB/s, 97 % of the measured copy rate), 65536 x 512 bf16 134 MB in 25.5 us (79
-// %, where ten shuffles a row per warp count).  Rows of single elements (no
-// 16-byte words) load 2 bytes a lane: 65536 x 515 bf16 takes 72 us.  One row of
-// 4096 takes 8 us, all of it the call.
+// %, where ten shuffles a row per warp count), 262144 x 64 bf16 67 MB in 14.3 us
+// (73 %).  Rows of single elements (no 16-byte words) load 2 bytes a lane:
+// 65536 x 515 bf16 takes 72 us.  One row of 4096 takes 8 us, all of it the call.
 #include "tb_layernorm.cuh"
 
 namespace tb {
@@ -25,10 +26,7 @@ namespace {
 // CTAs per SM the forward kernel is compiled for: 768 threads of 85 registers.
 // (16384 x 4096 bf16 with residual, f32 weights: 1024 / 768 / 512 threads take
 // 93.7 / 82.4 / 89.2 us; the first spill, the last have too few loads in flight.)
-#ifndef TB_LN_FWD_THREADS
-#define TB_LN_FWD_THREADS 768
-#endif
-__host__ __device__ constexpr int ln_fwd_ctas(int tpr) { return tpr >= 1024 ? 1 : TB_LN_FWD_THREADS / ln_block(tpr); }
+__host__ __device__ constexpr int ln_fwd_ctas(int tpr) { return tpr >= 1024 ? 1 : 768 / ln_block(tpr); }
 
 template <int DT, int VEC, int TPR, int CPT, bool RES>
 __global__ void __launch_bounds__(ln_block(TPR), ln_fwd_ctas(TPR)) ln_fwd_kernel(const __grid_constant__ LnFwdParams p) {
@@ -42,7 +40,9 @@ __global__ void __launch_bounds__(ln_block(TPR), ln_fwd_ctas(TPR)) ln_fwd_kernel
     const int t = threadIdx.x % TPR, rl = threadIdx.x / TPR;
     const int64_t step = (int64_t)gridDim.x * RPC;
     int64_t row = (int64_t)blockIdx.x * RPC + rl;
-    const int nchunk = (int)(p.cols / VEC);
+    // the rows of one warp stay together: its first row ends the loop for all
+    int64_t lead = TPR < 32 ? row - rl % (TPR < 32 ? 32 / TPR : 1) : row;
+    const int chunks = (int)(p.cols / VEC);
     const float n = (float)p.cols;
     const int64_t row_bytes = p.cols * elem_size(DT);
     grid_wait();
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(ln_block(TPR), ln_fwd_ctas(TPR)) ln_fwd_kernel
         for (int k = 0; k < CPT; ++k) {
             const int c = t + k * TPR;
             const W* const src = reinterpret_cast<const W*>(at) + c;
-            if (c < nchunk && in_bounds(src, sizeof(W), at, row_bytes, p.status)) v[k] = __ldcs(src);
+            if (c < chunks && in_bounds(src, sizeof(W), at, row_bytes, p.status)) v[k] = __ldcs(src);
         }
     };
     W nx[CPT], nr[RES ? CPT : 1];
@@ -66,13 +66,15 @@ __global__ void __launch_bounds__(ln_block(TPR), ln_fwd_ctas(TPR)) ln_fwd_kernel
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
             const int c = t + k * TPR;
-            if (c < nchunk) {
+            if (c < chunks) {
                 weight_lanes<VEC>(p.gamma, p.wdtype, (int64_t)c * VEC, 1.f, g[k]);
                 weight_lanes<VEC>(p.beta, p.wdtype, (int64_t)c * VEC, 0.f, b[k]);
             }
         }
     }
-    for (; row < p.rows; row += step) {
+    for (; lead < p.rows; lead += step, row += step) {
+        const bool here = TPR >= 32 || row < p.rows;
+        const int nchunk = here ? chunks : 0;
         W h[CPT];  // the row as stored
         T sum = L::splat(0.f);
 #pragma unroll
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(ln_block(TPR), ln_fwd_ctas(TPR)) ln_fwd_kernel
             }
         }
         const float rstd = 1.0f / sqrtf(row_sum<TPR, BLOCK>(vsum(m2), s_b, rl) / n + p.eps);
-        if (t == 0) {
+        if (t == 0 && here) {
             if (p.mean) p.mean[row] = mean;
             if (p.rstd) p.rstd[row] = rstd;
         }
@@ -233,7 +235,13 @@ cudaError_t fwd_dt(const LnFwdParams& p, bool vector, int sms, cudaStream_t s) {
     if (vector) {
         constexpr int V = 16 / elem_size(DT);
         const int64_t n = p.cols / V;
-        if (n <= 32) return fwd_launch<DT, V, 32, 1>(p, sms, s);
+        // (a warp takes several short rows, two words a thread: 262144 x 64 / 128 bf16
+        // 14.3 / 25.7 us, with a word a thread 15.5 / 29.3, a warp to a row 52.8 / 53.3;
+        // 131072 x 256 25.6 against 28.2)
+        if (n <= 4) return fwd_launch<DT, V, 4, 1>(p, sms, s);
+        if (n <= 8) return fwd_launch<DT, V, 4, 2>(p, sms, s);
+        if (n <= 16) return fwd_launch<DT, V, 8, 2>(p, sms, s);
+        if (n <= 32) return fwd_launch<DT, V, 16, 2>(p, sms, s);
         if (n <= 64) return fwd_launch<DT, V, 32, 2>(p, sms, s);
         if (n <= 128) return fwd_launch<DT, V, 64, 2>(p, sms, s);
         if (n <= 256) return fwd_launch<DT, V, 128, 2>(p, sms, s);
@@ -246,6 +254,9 @@ cudaError_t fwd_dt(const LnFwdParams& p, bool vector, int sms, cudaStream_t s) {
     // (16 columns a thread from 2049 on: with 8, bf16 rows of 4095 / 5001 / 8191
     // took 105 / 158 / 103 us instead of 76 / 108 / 78, and with 16 below, rows of
     // 515 / 2047 took 77 / 79 us instead of 72 / 77; 67 M elements, at most 65536 rows)
+    // (short rows: several to a warp; one to a warp took 64.6 us where 262144 x 63 bf16 takes 24.0)
+    if (p.cols <= 64) return fwd_launch<DT, 1, 8, 8>(p, sms, s);
+    if (p.cols <= 128) return fwd_launch<DT, 1, 16, 8>(p, sms, s);
     if (p.cols <= 256) return fwd_launch<DT, 1, 32, 8>(p, sms, s);
     if (p.cols <= 512) return fwd_launch<DT, 1, 64, 8>(p, sms, s);
     if (p.cols <= 1024) return fwd_launch<DT, 1, 128, 8>(p, sms, s);

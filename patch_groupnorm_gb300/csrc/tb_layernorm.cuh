@@ -25,7 +25,9 @@ __device__ __forceinline__ void row_barrier(int rl) {
 // (one float per warp of the CTA) must not be reused before another barrier.
 template <int TPR, int BLOCK>
 __device__ __forceinline__ float row_sum(float v, float* slots, int rl) {
-    v = warp_sum(v);
+    constexpr int HOLD = TPR < 32 ? TPR : 32;  // lanes of a warp in one row
+#pragma unroll
+    for (int d = HOLD / 2; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
     if constexpr (TPR > 32) {
         if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
         row_barrier<TPR, BLOCK>(rl);

@@ -154,6 +154,17 @@ def test_layer_norm_row_counts(tbl, rows, cols, dtype):
 
 
 @pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("rows", [1, 5, 33, 130, 30001])
+@pytest.mark.parametrize("cols", [4, 16, 33, 63, 65, 72, 127, 128, 200])
+def test_layer_norm_short_rows(tbl, cols, rows, dtype):
+    # several rows to a warp: warps whose last rows are missing, lanes without a column
+    dt = DT[dtype]
+    gamma, beta = weights_of(7, cols, dt)
+    x, dy = rows_of(1, (rows, cols), dt, 1.0, 0.2), rows_of(2, (rows, cols), dt, 0.3)
+    run_ln(tbl, x, gamma, beta, 1e-5, dy, residual=rows_of(3, (rows, cols), dt), dtotal=rows_of(4, (rows, cols), dt))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("cols", [5001, 8192, 8191, 12008, 12001, 16384, 16383])
 def test_layer_norm_wide_rows_many_to_a_cta(tbl, cols, dtype):
     # every row buffer of the backward kernel is filled and read several times

@@ -386,6 +386,7 @@ __global__ void __launch_bounds__(BWD_BLOCK, 1)
     constexpr int BLOCK = BWD_BLOCK;
     constexpr int RPC = BLOCK / TPR;
     constexpr int WPR = TPR / 32;
+    constexpr int HOLD = TPR < 32 ? TPR : 32;  // lanes of a warp in one row group
     __shared__ float2 s_sum[2][BLOCK / 32];
     extern __shared__ __align__(16) unsigned char s_rows[];  // RPC > 1: the CTA's sums
     const int t = threadIdx.x % TPR, rl = threadIdx.x / TPR;
@@ -408,12 +409,12 @@ __global__ void __launch_bounds__(BWD_BLOCK, 1)
         }
     };
     W nd[CPT], nx[CPT], nt[CPT];
-    // the statistics of the row group's next 32 rows, one row per lane, and of
-    // the 32 after them
+    // the statistics of the row group's next HOLD rows, one row per lane, and of
+    // the HOLD after them
     const int lane = threadIdx.x & 31;
     float mean_now, rstd_now, mean_next, rstd_next;
     auto stats = [&](int64_t r, float& m, float& rs) {
-        r += lane * step;
+        r += lane % HOLD * step;
         m = rs = 0.f;
         if (r < p.rows) {
             m = p.mean[r];
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(BWD_BLOCK, 1)
         if constexpr (TOT) fetch(p.dtotal, row, p.dt_ld, nt);
     }
     stats(row, mean_now, rstd_now);
-    stats(row + 32 * step, mean_next, rstd_next);
+    stats(row + HOLD * step, mean_next, rstd_next);
     T g[CPT][L::N], dg[CPT][L::N], db[CPT][L::N];
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
@@ -437,14 +438,18 @@ __global__ void __launch_bounds__(BWD_BLOCK, 1)
         for (int q = 0; q < L::N; ++q) dg[k][q] = db[k][q] = L::splat(0.f);
     }
     int phase = 0, turn = 0;
-    for (; row < p.rows; row += step) {
-        if (turn == 32) {
+    // (the row groups of one warp go round together, those without a row idle)
+    const int64_t warp_row = TPR < 32 ? (int64_t)blockIdx.x * RPC + rl / (32 / HOLD) * (32 / HOLD) : row;
+    for (int64_t any = warp_row; any < p.rows; any += step, row += step) {
+        const int mine = TPR >= 32 || row < p.rows ? nchunk : 0;
+        if (turn == HOLD) {
             turn = 0;
             mean_now = mean_next;
             rstd_now = rstd_next;
-            stats(row + 32 * step, mean_next, rstd_next);
+            stats(row + HOLD * step, mean_next, rstd_next);
         }
-        const float mean = __shfl_sync(0xffffffffu, mean_now, turn), rstd = __shfl_sync(0xffffffffu, rstd_now, turn);
+        const float mean = __shfl_sync(0xffffffffu, mean_now, (lane & ~(HOLD - 1)) + turn);
+        const float rstd = __shfl_sync(0xffffffffu, rstd_now, (lane & ~(HOLD - 1)) + turn);
         ++turn;
         const T mean2 = L::splat(mean), rstd2 = L::splat(rstd);
         W cd[CPT], cx[CPT], ct[CPT];
@@ -463,7 +468,7 @@ __global__ void __launch_bounds__(BWD_BLOCK, 1)
         T a1 = L::splat(0.f), a2 = L::splat(0.f);
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
-            if (t + k * TPR < nchunk) {
+            if (t + k * TPR < mine) {
                 to_lanes<DT, 1>(cd[k], d[k]);
                 to_lanes<DT, 1>(cx[k], x[k]);
 #pragma unroll
@@ -478,7 +483,12 @@ __global__ void __launch_bounds__(BWD_BLOCK, 1)
                 }
             }
         }
-        float s1 = warp_sum(vsum(a1)), s2 = warp_sum(vsum(a2));
+        float s1 = vsum(a1), s2 = vsum(a2);
+#pragma unroll
+        for (int o = HOLD / 2; o >= 1; o >>= 1) {
+            s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+            s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+        }
         if constexpr (TPR > 32) {
             if ((threadIdx.x & 31) == 0) s_sum[phase][threadIdx.x >> 5] = make_float2(s1, s2);
             row_barrier<TPR, BLOCK>(rl);
@@ -500,7 +510,7 @@ __global__ void __launch_bounds__(BWD_BLOCK, 1)
 #pragma unroll
             for (int k = 0; k < CPT; ++k) {
                 const int c = t + k * TPR;
-                if (c < nchunk) {
+                if (c < mine) {
                     T o[L::N];
                     if constexpr (TOT) {
                         to_lanes<DT, 1>(ct[k], o);
@@ -709,7 +719,7 @@ cudaError_t bwd_elem(const LnBwdParams& p, int sms, int* parts, cudaStream_t s) 
     int64_t grid = sms < TB_LN_PARTS ? sms : TB_LN_PARTS;
     if (grid > want) grid = want;
     *parts = (int)grid;
-    const size_t smem = rpc > 1 ? (size_t)rpc * 2 * CPT * (TPR + 4) * 4 : 0;  // at most 37 KB
+    const size_t smem = rpc > 1 ? (size_t)rpc * 2 * CPT * (TPR + 4) * 4 : 0;  // at most 40 KB
     return launch_pdl(p.dtotal ? ln_bwd_elem_kernel<DT, TPR, CPT, true> : ln_bwd_elem_kernel<DT, TPR, CPT, false>, p,
                       dim3((unsigned)grid), BWD_BLOCK, smem, s);
 }
@@ -731,6 +741,9 @@ cudaError_t bwd_dt(const LnBwdParams& p, bool vector, int sms, int* parts, cudaS
         if (n <= 2048) return bwd_launch<DT, 512, 4, true>(p, sms, parts, s);
         return bwd_long<DT, V>(p, sms, parts, s);
     }
+    // (short rows two to a warp: 262144 x 63 bf16 42.1 us, 131072 x 127 28.8; one to a warp 72.7 and 42.9)
+    if (p.cols <= 64) return bwd_elem<DT, 16, 4>(p, sms, parts, s);
+    if (p.cols <= 128) return bwd_elem<DT, 16, 8>(p, sms, parts, s);
     if (p.cols <= 256) return bwd_elem<DT, 32, 8>(p, sms, parts, s);
     if (p.cols <= 512) return bwd_elem<DT, 64, 8>(p, sms, parts, s);
     if (p.cols <= 1024) return bwd_elem<DT, 128, 8>(p, sms, parts, s);

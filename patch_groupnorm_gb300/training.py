@@ -2,7 +2,8 @@
 runs them together.
 
 ``layer_norm`` and ``patch_group_norm`` take tensors that require gradients;
-their backward passes run in the library's kernels.  ``Trainer`` keeps a
+their backward passes run in the library's kernels, and a second derivative
+through them raises an error.  ``Trainer`` keeps a
 parameter set's gradient table and clips it by its global norm before a plain
 gradient step.
 
@@ -31,6 +32,21 @@ def _rows(t: torch.Tensor) -> torch.Tensor:
         return t.contiguous()
 
 
+# The gradients are nodes of their own.  A graph made of them (create_graph)
+# then reaches back to the norm's inputs and ends in an error: the kernels have
+# no second derivatives, and gradients without a node would be taken for
+# constants whenever dy is one.
+
+class _LayerNormGrad(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, dy, h, mean, rstd, gamma, wdtype, dtotal):
+        return tb.layer_norm_backward(dy, h, mean, rstd, gamma, dtotal, wdtype=wdtype)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the layer norm has no second derivative")
+
+
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gamma, beta, eps, residual):
@@ -43,8 +59,8 @@ class _LayerNorm(torch.autograd.Function):
     def backward(ctx, dy, dtotal=None):
         h, mean, rstd, gamma, beta = ctx.saved_tensors
         dtotal = None if dtotal is None else _rows(dtotal)
-        dx, dgamma, dbeta = tb.layer_norm_backward(_rows(dy), h, mean, rstd, gamma, dtotal,
-                                                   wdtype=None if beta is None else beta.dtype)
+        dx, dgamma, dbeta = _LayerNormGrad.apply(_rows(dy), h, mean, rstd, gamma, None if beta is None else beta.dtype,
+                                                 dtotal)
         needs = ctx.needs_input_grad
         return (dx if needs[0] else None, dgamma if needs[1] else None, dbeta if needs[2] else None, None,
                 dx if needs[4] else None)
@@ -52,9 +68,23 @@ class _LayerNorm(torch.autograd.Function):
 
 def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor], eps: float = 1e-6,
                residual: Optional[torch.Tensor] = None):
-    """Layer norm over the last axis, differentiable.  With a residual:
-    ``(LN(x + residual), x + residual)``."""
+    """Layer norm over the last axis, differentiable once (a second derivative
+    raises).  With a residual: ``(LN(x + residual), x + residual)``."""
     return _LayerNorm.apply(x, gamma, beta, eps, residual)
+
+
+class _PatchGroupNormGrad(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, args, partials, gamma, beta, *dys_and_patches):
+        P = len(dys_and_patches) // 2
+        G, eps, silu = args
+        dxs, dgamma, dbeta = tb.patch_group_norm_backward(dys_and_patches[:P], dys_and_patches[P:], G, partials, gamma,
+                                                          beta, eps, silu)
+        return dgamma, dbeta, *dxs
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the patch group norm has no second derivative")
 
 
 class _PatchGroupNorm(torch.autograd.Function):
@@ -69,16 +99,16 @@ class _PatchGroupNorm(torch.autograd.Function):
     @staticmethod
     def backward(ctx, *dys):
         partials, gamma, beta, *patches = ctx.saved_tensors
-        G, eps, silu = ctx.args
-        dxs, dgamma, dbeta = tb.patch_group_norm_backward([d.contiguous() for d in dys], patches, G, partials, gamma,
-                                                          beta, eps, silu)
+        dgamma, dbeta, *dxs = _PatchGroupNormGrad.apply(ctx.args, partials, gamma, beta,
+                                                        *[d.contiguous() for d in dys], *patches)
         needs = ctx.needs_input_grad
         return (None, None, None, dgamma if needs[3] else None, dbeta if needs[4] else None, *dxs)
 
 
 def patch_group_norm(patches: Sequence[torch.Tensor], G: int, gamma: Optional[torch.Tensor],
                      beta: Optional[torch.Tensor], eps: float = 1e-6, silu: bool = True) -> Tuple[torch.Tensor, ...]:
-    """GroupNorm (+ SiLU) of the whole tensor over its patches, differentiable."""
+    """GroupNorm (+ SiLU) of the whole tensor over its patches, differentiable
+    once (a second derivative raises)."""
     return _PatchGroupNorm.apply(G, eps, silu, gamma, beta, *patches)
 
 

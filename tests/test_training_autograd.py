@@ -1,0 +1,97 @@
+"""CPU checks of the training module's autograd functions and step.  The
+library's kernels are replaced by the same formulas in torch, run without a
+graph as the kernels run: what is tested is what the module makes of them."""
+import pytest
+import torch
+import torch.nn.functional as F
+
+
+def _layer_norm(x, gamma, beta, eps, residual=None, stream=None):
+    with torch.no_grad():
+        h = x if residual is None else x + residual
+        mean = h.mean(-1)
+        rstd = 1.0 / torch.sqrt(h.var(-1, unbiased=False) + eps)
+        y = (h - mean[..., None]) * rstd[..., None]
+        y = y if gamma is None else y * gamma.reshape(-1)
+        y = y if beta is None else y + beta.reshape(-1)
+    return (y, mean, rstd) if residual is None else (y, mean, rstd, h)
+
+
+def _layer_norm_backward(dy, x, mean, rstd, gamma, dtotal=None, wdtype=None, stream=None):
+    with torch.no_grad():
+        n, r = x.shape[-1], rstd[..., None]
+        xhat = (x - mean[..., None]) * r
+        g = dy if gamma is None else dy * gamma.reshape(-1)
+        dx = r * (g - g.mean(-1, keepdim=True) - xhat * (g * xhat).mean(-1, keepdim=True))
+        dx = dx if dtotal is None else dx + dtotal
+        return dx, (dy * xhat).reshape(-1, n).sum(0), dy.reshape(-1, n).sum(0)
+
+
+def _patch_group_norm(patches, G, gamma, beta, eps, silu=True, outs=None, partials=None, stream=None):
+    with torch.no_grad():
+        y = F.group_norm(torch.cat(list(patches), 2), G, gamma.reshape(-1), beta.reshape(-1), eps)
+        return list((F.silu(y) if silu else y).split([p.shape[2] for p in patches], 2))
+
+
+def _patch_group_norm_backward(grads, patches, G, partials, gamma, beta, eps, silu=True):
+    with torch.enable_grad():
+        xs = [p.detach().requires_grad_() for p in patches]
+        w, b = (t.detach().reshape(-1).requires_grad_() for t in (gamma, beta))
+        y = F.group_norm(torch.cat(xs, 2), G, w, b, eps)
+        out = torch.autograd.grad(F.silu(y) if silu else y, [*xs, w, b], torch.cat(list(grads), 2))
+    return list(out[:-2]), out[-2], out[-1]
+
+
+@pytest.fixture
+def training(monkeypatch):
+    from patch_groupnorm_gb300 import build
+    build.build()
+    from patch_groupnorm_gb300 import training
+    for name, f in (("layer_norm", _layer_norm), ("layer_norm_backward", _layer_norm_backward),
+                    ("patch_group_norm", _patch_group_norm), ("patch_group_norm_backward", _patch_group_norm_backward),
+                    ("new_partials", lambda *a: torch.zeros(1)), ("_row_ld", lambda t, *a: t.stride(0))):
+        monkeypatch.setattr(training.tb, name, f)
+    return training
+
+
+def _randn(seed, *shape):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed), dtype=torch.float64)
+
+
+# --------------------------------------------------------------------------
+# second derivatives: the kernels compute none, so asking for one is an error
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("residual", [False, True])
+def test_layer_norm_second_derivative_is_refused(training, residual):
+    x, w, b = _randn(1, 3, 8).requires_grad_(), _randn(2, 8).requires_grad_(), _randn(3, 8).requires_grad_()
+    r = _randn(4, 3, 8).requires_grad_() if residual else None
+
+    def penalised(dy):
+        y = training.layer_norm(x, w, b, 1e-5, r)
+        y = y[0] if residual else y
+        g, = torch.autograd.grad(y, x, dy, create_graph=True)
+        return y.square().mean() + g.square().sum()   # the first term has a graph of its own
+    # the gradient of y may itself be a constant, or not
+    for dy in (_randn(5, 3, 8), _randn(5, 3, 8).requires_grad_()):
+        with pytest.raises(RuntimeError, match="second derivative"):
+            penalised(dy).backward()
+    # first derivatives with create_graph are what they are without it
+    y = training.layer_norm(x, w, b, 1e-5)
+    a = torch.autograd.grad(y, [x, w, b], _randn(6, 3, 8), create_graph=True)
+    y = training.layer_norm(x, w, b, 1e-5)
+    c = torch.autograd.grad(y, [x, w, b], _randn(6, 3, 8))
+    assert all(torch.equal(p, q) for p, q in zip(a, c))
+
+
+def test_group_norm_second_derivative_is_refused(training):
+    xs = [_randn(1, 2, 4, 3, 5).requires_grad_(), _randn(2, 2, 4, 2, 5).requires_grad_()]
+    w, b = _randn(3, 4).requires_grad_(), _randn(4, 4).requires_grad_()
+    for last in (False, True):
+        dys = [_randn(5 + k, *x.shape) for k, x in enumerate(xs)]
+        dys[1].requires_grad_(last)
+        outs = training.patch_group_norm(xs, 2, w, b)
+        gs = torch.autograd.grad(outs, xs, dys, create_graph=True)
+        loss = sum(o.square().mean() for o in outs) + sum(g.square().sum() for g in gs)
+        with pytest.raises(RuntimeError, match="second derivative"):
+            loss.backward()

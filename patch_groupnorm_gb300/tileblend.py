@@ -932,16 +932,19 @@ def tb_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor
 
 def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
                         gamma: Optional[torch.Tensor], dtotal: Optional[torch.Tensor] = None, wdtype=None,
-                        stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+                        stream=None, needs=(True, True, True)
+                        ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor], Optional[torch.Tensor]]:
     """``(dx, dgamma, dbeta)`` in new tensors (the weights' dtype is gamma's,
-    or ``wdtype``)."""
+    or ``wdtype``).  ``needs``: which of the three are wanted; the others are
+    None and not computed."""
     cols = x.shape[-1]
     wdt = gamma.dtype if gamma is not None else wdtype or x.dtype
 
     def make():
-        w = torch.empty((2, cols), dtype=wdt, device=x.device)
-        return (torch.empty(x.shape, dtype=x.dtype, device=x.device), torch.empty_like(w[0]), torch.empty_like(w[1]),
-                ln_workspace(x.numel() // max(1, cols), cols, x.device))
+        return (torch.empty(x.shape, dtype=x.dtype, device=x.device) if needs[0] else None,
+                torch.empty(cols, dtype=wdt, device=x.device) if needs[1] else None,
+                torch.empty(cols, dtype=wdt, device=x.device) if needs[2] else None,
+                ln_workspace(x.numel() // max(1, cols), cols, x.device) if needs[1] or needs[2] else None)
     dx, dgamma, dbeta, ws = _on_stream(make, stream)
     tb_layer_norm_backward(dy, x, mean, rstd, gamma, dx, dgamma, dbeta, ws, dtotal, stream)
     return dx, dgamma, dbeta

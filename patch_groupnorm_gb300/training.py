@@ -39,8 +39,8 @@ def _rows(t: torch.Tensor) -> torch.Tensor:
 
 class _LayerNormGrad(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, dy, h, mean, rstd, gamma, wdtype, dtotal):
-        return tb.layer_norm_backward(dy, h, mean, rstd, gamma, dtotal, wdtype=wdtype)
+    def forward(ctx, dy, h, mean, rstd, gamma, wdtype, dtotal, needs):
+        return tb.layer_norm_backward(dy, h, mean, rstd, gamma, dtotal, wdtype=wdtype, needs=needs)
 
     @staticmethod
     def backward(ctx, *grads):
@@ -53,17 +53,19 @@ class _LayerNorm(torch.autograd.Function):
         out = tb.layer_norm(x, gamma, beta, eps, residual)
         h = x if residual is None else out[3]
         ctx.save_for_backward(h, out[1], out[2], gamma, beta)
+        ctx.set_materialize_grads(False)
         return out[0] if residual is None else (out[0], out[3])
 
     @staticmethod
     def backward(ctx, dy, dtotal=None):
+        x_, gamma_, beta_, _, residual_ = ctx.needs_input_grad
+        if dy is None:  # only the sum was used
+            return dtotal if x_ else None, None, None, None, dtotal if residual_ else None
         h, mean, rstd, gamma, beta = ctx.saved_tensors
-        dtotal = None if dtotal is None else _rows(dtotal)
         dx, dgamma, dbeta = _LayerNormGrad.apply(_rows(dy), h, mean, rstd, gamma, None if beta is None else beta.dtype,
-                                                 dtotal)
-        needs = ctx.needs_input_grad
-        return (dx if needs[0] else None, dgamma if needs[1] else None, dbeta if needs[2] else None, None,
-                dx if needs[4] else None)
+                                                 None if dtotal is None else _rows(dtotal),
+                                                 (x_ or residual_, gamma_, beta_))
+        return dx if x_ else None, dgamma, dbeta, None, dx if residual_ else None
 
 
 def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor], eps: float = 1e-6,

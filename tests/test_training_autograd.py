@@ -17,14 +17,15 @@ def _layer_norm(x, gamma, beta, eps, residual=None, stream=None):
     return (y, mean, rstd) if residual is None else (y, mean, rstd, h)
 
 
-def _layer_norm_backward(dy, x, mean, rstd, gamma, dtotal=None, wdtype=None, stream=None):
+def _layer_norm_backward(dy, x, mean, rstd, gamma, dtotal=None, wdtype=None, stream=None, needs=(True, True, True)):
     with torch.no_grad():
         n, r = x.shape[-1], rstd[..., None]
         xhat = (x - mean[..., None]) * r
         g = dy if gamma is None else dy * gamma.reshape(-1)
         dx = r * (g - g.mean(-1, keepdim=True) - xhat * (g * xhat).mean(-1, keepdim=True))
         dx = dx if dtotal is None else dx + dtotal
-        return dx, (dy * xhat).reshape(-1, n).sum(0), dy.reshape(-1, n).sum(0)
+        out = dx, (dy * xhat).reshape(-1, n).sum(0), dy.reshape(-1, n).sum(0)
+        return tuple(t if want else None for t, want in zip(out, needs))
 
 
 def _patch_group_norm(patches, G, gamma, beta, eps, silu=True, outs=None, partials=None, stream=None):
@@ -95,3 +96,61 @@ def test_group_norm_second_derivative_is_refused(training):
         loss = sum(o.square().mean() for o in outs) + sum(g.square().sum() for g in gs)
         with pytest.raises(RuntimeError, match="second derivative"):
             loss.backward()
+
+
+# --------------------------------------------------------------------------
+# only what is asked for is computed
+# --------------------------------------------------------------------------
+
+@pytest.fixture
+def calls(training, monkeypatch):
+    """The arguments (dtotal, needs) of every backward call."""
+    seen = []
+
+    def backward(dy, x, mean, rstd, gamma, dtotal=None, wdtype=None, stream=None, needs=(True, True, True)):
+        seen.append((dtotal, tuple(needs)))
+        return _layer_norm_backward(dy, x, mean, rstd, gamma, dtotal, needs=needs)
+    monkeypatch.setattr(training.tb, "layer_norm_backward", backward)
+    return seen
+
+
+def _leaves():
+    return (_randn(1, 3, 8).requires_grad_(), _randn(2, 8).requires_grad_(), _randn(3, 8).requires_grad_(),
+            _randn(4, 3, 8).requires_grad_())
+
+
+def _plain(x, w, b, r):
+    total = x + r
+    return F.layer_norm(total, (8,), w, b, 1e-5), total
+
+
+@pytest.mark.parametrize("used", ["y", "total", "both"])
+def test_layer_norm_outputs_that_are_not_used_cost_nothing(training, calls, used):
+    def grads(f):
+        ts = _leaves()
+        y, total = f(*ts)
+        v, u = _randn(5, 3, 8), _randn(6, 3, 8)
+        sum(t for name, t in (("y", (y * v).sum()), ("total", (total * u).sum())) if used in (name, "both")).backward()
+        return [t.grad for t in ts]
+    got = grads(lambda x, w, b, r: training.layer_norm(x, w, b, 1e-5, r))
+    for a, c in zip(got, grads(_plain)):
+        assert a is None and c is None or torch.allclose(a, c, rtol=1e-10, atol=1e-12)
+    if used == "total":
+        assert calls == []
+    else:
+        (dtotal, needs), = calls
+        assert (dtotal is None) == (used == "y") and needs == (True, True, True)
+
+
+@pytest.mark.parametrize("frozen", [(1, 2), (0,), (0, 3), (1,), (2, 0, 3)])
+def test_layer_norm_gradients_that_are_not_wanted_are_not_computed(training, calls, frozen):
+    ts, plain = _leaves(), _leaves()
+    for k in frozen:
+        ts[k].requires_grad_(False)
+    v = _randn(5, 3, 8)
+    (training.layer_norm(*ts[:3], 1e-5, ts[3])[0] * v).sum().backward()
+    (_plain(*plain)[0] * v).sum().backward()
+    for k, (t, p) in enumerate(zip(ts, plain)):
+        assert t.grad is None if k in frozen else torch.allclose(t.grad, p.grad, rtol=1e-10, atol=1e-12)
+    (_, needs), = calls
+    assert needs == (not {0, 3} <= set(frozen), 1 not in frozen, 2 not in frozen)

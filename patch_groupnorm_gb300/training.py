@@ -129,13 +129,13 @@ class Trainer:
 
     def step(self, loss: torch.Tensor) -> torch.Tensor:
         """Backward pass, clip and update; returns the norm before the clip."""
-        for p in self.params:
-            p.grad.zero_()
+        for p, g in zip(self.params, self.table.grads):
+            p.grad = g.zero_()  # a program may have dropped or replaced it since
         loss.backward()
         norm = tb.clip_grad_norm(self.table, self.max_norm, records=self.records)
         with torch.no_grad():
-            for p in self.params:
-                p -= self.lr * p.grad
+            for p, g in zip(self.params, self.table.grads):
+                p -= self.lr * g
         return norm
 
 

@@ -154,3 +154,44 @@ def test_layer_norm_gradients_that_are_not_wanted_are_not_computed(training, cal
         assert t.grad is None if k in frozen else torch.allclose(t.grad, p.grad, rtol=1e-10, atol=1e-12)
     (_, needs), = calls
     assert needs == (not {0, 3} <= set(frozen), 1 not in frozen, 2 not in frozen)
+
+
+# --------------------------------------------------------------------------
+# the step
+# --------------------------------------------------------------------------
+
+class _Table:
+    def __init__(self, grads, outs=None):
+        self.grads = list(grads)
+
+
+def _clip_grad_norm(table, max_norm, records=None, norm=None, stream=None):
+    n = torch.sqrt(sum(g.square().sum() for g in table.grads))
+    for g in table.grads:
+        g.mul_(torch.clamp(max_norm / (n + 1e-6), max=1.0))
+    return n.reshape(1)
+
+
+@pytest.mark.parametrize("between", ["nothing", "dropped", "replaced", "scaled"])
+def test_step_clips_the_gradients_it_applies(training, monkeypatch, between):
+    # whatever a program did to the parameters' .grad since the last step
+    for name, f in (("GradTable", _Table), ("new_grad_records", lambda *a: None), ("clip_grad_norm", _clip_grad_norm)):
+        monkeypatch.setattr(training.tb, name, f)
+    w, b = _randn(1, 4, 4).requires_grad_(), _randn(2, 4).requires_grad_()
+    trainer = training.Trainer([w, b], lr=0.5, max_norm=0.25)
+    x = _randn(3, 5, 4)
+    for _ in range(2):
+        for p in (w, b):
+            if between == "dropped":
+                p.grad = None
+            elif between == "replaced":
+                p.grad = torch.full_like(p, 3.0)
+            elif between == "scaled":
+                p.grad *= 7.0
+        ps = [p.detach().clone().requires_grad_() for p in (w, b)]
+        (x @ ps[0] + ps[1]).square().mean().backward()
+        want = torch.nn.utils.clip_grad_norm_(ps, 0.25)
+        norm = trainer.step((x @ w + b).square().mean())
+        assert want > 0.25 and torch.allclose(norm, want)
+        for p, q in zip((w, b), ps):
+            assert torch.allclose(p.grad, q.grad) and torch.allclose(p.detach(), q.detach() - 0.5 * q.grad)

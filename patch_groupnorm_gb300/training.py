@@ -32,6 +32,11 @@ def _rows(t: torch.Tensor) -> torch.Tensor:
         return t.contiguous()
 
 
+def _like(grad: Optional[torch.Tensor], weight: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """A weight's gradient in the weight's shape (the kernels see vectors)."""
+    return None if grad is None or weight is None else grad.view(weight.shape)
+
+
 # The gradients are nodes of their own.  A graph made of them (create_graph)
 # then reaches back to the norm's inputs and ends in an error: the kernels have
 # no second derivatives, and gradients without a node would be taken for
@@ -65,7 +70,7 @@ class _LayerNorm(torch.autograd.Function):
         dx, dgamma, dbeta = _LayerNormGrad.apply(_rows(dy), h, mean, rstd, gamma, None if beta is None else beta.dtype,
                                                  None if dtotal is None else _rows(dtotal),
                                                  (x_ or residual_, gamma_, beta_))
-        return dx if x_ else None, dgamma, dbeta, None, dx if residual_ else None
+        return dx if x_ else None, _like(dgamma, gamma), _like(dbeta, beta), None, dx if residual_ else None
 
 
 def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor], eps: float = 1e-6,
@@ -103,8 +108,7 @@ class _PatchGroupNorm(torch.autograd.Function):
         partials, gamma, beta, *patches = ctx.saved_tensors
         dgamma, dbeta, *dxs = _PatchGroupNormGrad.apply(ctx.args, partials, gamma, beta,
                                                         *[d.contiguous() for d in dys], *patches)
-        needs = ctx.needs_input_grad
-        return (None, None, None, dgamma if needs[3] else None, dbeta if needs[4] else None, *dxs)
+        return (None, None, None, _like(dgamma, gamma), _like(dbeta, beta), *dxs)
 
 
 def patch_group_norm(patches: Sequence[torch.Tensor], G: int, gamma: Optional[torch.Tensor],

@@ -195,3 +195,25 @@ def test_step_clips_the_gradients_it_applies(training, monkeypatch, between):
         assert want > 0.25 and torch.allclose(norm, want)
         for p, q in zip((w, b), ps):
             assert torch.allclose(p.grad, q.grad) and torch.allclose(p.detach(), q.detach() - 0.5 * q.grad)
+
+
+# --------------------------------------------------------------------------
+# weights of any shape of the right size
+# --------------------------------------------------------------------------
+
+def test_weight_gradients_have_their_weights_shapes(training):
+    x, w, b = _randn(1, 3, 8).requires_grad_(), _randn(2, 1, 1, 8).requires_grad_(), _randn(3, 8, 1).requires_grad_()
+    v = _randn(4, 3, 8)
+    (training.layer_norm(x, w, b, 1e-5) * v).sum().backward()
+    ps = [t.detach().reshape(-1).requires_grad_() for t in (w, b)]
+    (F.layer_norm(x.detach(), (8,), *ps, 1e-5) * v).sum().backward()
+    for t, p in zip((w, b), ps):
+        assert t.grad.shape == t.shape and torch.allclose(t.grad.reshape(-1), p.grad)
+    xs = [_randn(5, 2, 4, 3, 5), _randn(6, 2, 4, 2, 5)]
+    w, b = _randn(7, 1, 4, 1, 1).requires_grad_(), _randn(8, 4, 1).requires_grad_()
+    v = _randn(9, 2, 4, 5, 5)
+    (torch.cat(training.patch_group_norm(xs, 2, w, b), 2) * v).sum().backward()
+    ps = [t.detach().reshape(-1).requires_grad_() for t in (w, b)]
+    (F.silu(F.group_norm(torch.cat(xs, 2), 2, *ps, 1e-6)) * v).sum().backward()
+    for t, p in zip((w, b), ps):
+        assert t.grad.shape == t.shape and torch.allclose(t.grad.reshape(-1), p.grad)

@@ -790,9 +790,14 @@ def _on_stream(make, stream):
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _stream_of(stream, device: int) -> int:
+    """The stream's handle, for a launch that takes tensors of ``device``: the
+    library launches on the current device."""
+    if device != _current_device():
+        raise ValueError("the tensors are on CUDA device %d, the current device is %d" % (device, _current_device()))
     return _raw_stream(device) if stream is None else _stream_handle(stream)
 
 
@@ -994,16 +999,18 @@ def new_grad_records(T: int, device=None) -> torch.Tensor:
     return torch.empty(n, dtype=torch.float64, device=device or torch.device("cuda"))
 
 
-def _records(records: torch.Tensor) -> int:
+def _records(records: torch.Tensor, table: Optional[GradTable] = None) -> int:
     if records.get_device() < 0 or records.dtype is not torch.float64 or not records.is_contiguous():
         raise ValueError("records must be a contiguous float64 CUDA tensor")
+    if table is not None and len(table) and records.get_device() != table.grads[0].get_device():
+        raise ValueError("records must be on the gradients' device")
     return records.data_ptr()
 
 
 def tb_grad_stats(table: GradTable, records: torch.Tensor, stream=None) -> torch.Tensor:
     """Sums of squares of the table's gradients into ``records`` (from
     ``new_grad_records``)."""
-    at = _records(records)
+    at = _records(records, table)
     if records.numel() != table._records and table._records >= 0:
         raise ValueError("records must hold exactly %d values for %d gradients" % (table._records, len(table)))
     _check(_lib.tb_grad_stats(table._in, table._numel, table._dtypes, len(table), at,
@@ -1011,18 +1018,18 @@ def tb_grad_stats(table: GradTable, records: torch.Tensor, stream=None) -> torch
     return records
 
 
-def _norm_ptr(norm: Optional[torch.Tensor]):
+def _norm_ptr(norm: Optional[torch.Tensor], device: int):
     if norm is None:
         return None
-    if norm.get_device() < 0 or norm.dtype is not torch.float32 or norm.numel() != 1:
-        raise ValueError("norm must be one float32 on the GPU")
+    if norm.get_device() != device or norm.dtype is not torch.float32 or norm.numel() != 1:
+        raise ValueError("norm must be one float32 on the records' device")
     return norm.data_ptr()
 
 
 def tb_grad_norm(records: torch.Tensor, norm: torch.Tensor, stream=None) -> torch.Tensor:
     """The global norm that ``records`` (one or more record sets) describe."""
-    _check(_lib.tb_grad_norm(_records(records), records.numel(), _norm_ptr(norm),
-                             _stream_of(stream, records.get_device())), "tb_grad_norm")
+    at, dev = _records(records), records.get_device()
+    _check(_lib.tb_grad_norm(at, records.numel(), _norm_ptr(norm, dev), _stream_of(stream, dev)), "tb_grad_norm")
     return norm
 
 
@@ -1030,9 +1037,9 @@ def tb_grad_clip(table: GradTable, records: torch.Tensor, max_norm: float, norm:
                  stream=None) -> None:
     """Every gradient of the table times min(1, max_norm / (norm + 1e-6)), into
     its output; the norm is that of all ``records``."""
-    _check(_lib.tb_grad_clip(table._in, table._out, table._numel, table._dtypes, len(table), _records(records),
-                             records.numel(), max_norm, _norm_ptr(norm), _stream_of(stream, records.get_device())),
-           "tb_grad_clip")
+    at, dev = _records(records, table), records.get_device()
+    _check(_lib.tb_grad_clip(table._in, table._out, table._numel, table._dtypes, len(table), at, records.numel(),
+                             max_norm, _norm_ptr(norm, dev), _stream_of(stream, dev)), "tb_grad_clip")
 
 
 def clip_grad_norm(grads, max_norm: float, records: Optional[torch.Tensor] = None,
@@ -1105,9 +1112,9 @@ def _gn_grad_outs(dxs, patches, C, dgamma, dbeta):
     return _like_patches(dxs, patches, "dx"), _vec(dgamma, C, dt, dev, "dgamma"), _vec(dbeta, C, dt, dev, "dbeta")
 
 
-def _grad_partials(t: torch.Tensor, R: int, N: int, C: int) -> int:
-    if t.get_device() < 0 or not t.is_contiguous() or t.numel() * t.element_size() != R * N * C * TB_GN_PARTS * 8:
-        raise ValueError("grad_partials must hold R*N*C*TB_GN_PARTS 8-byte records")
+def _grad_partials(t: torch.Tensor, R: int, N: int, C: int, device: int) -> int:
+    if t.get_device() != device or not t.is_contiguous() or t.numel() * t.element_size() != R * N * C * TB_GN_PARTS * 8:
+        raise ValueError("grad_partials must hold R*N*C*TB_GN_PARTS 8-byte records on the patches' device")
     return t.data_ptr()
 
 
@@ -1124,7 +1131,7 @@ def tb_patch_gn_grad_stats(grads: Sequence[torch.Tensor], patches: Sequence[torc
     _check(_lib.tb_patch_gn_grad_stats(xs, ds, P, dt, N, C, sp, G, partials.data_ptr(), R,
                                        gamma.data_ptr() if gamma is not None else None,
                                        beta.data_ptr() if beta is not None else None, float(eps), 1 if silu else 0,
-                                       _grad_partials(grad_partials, P, N, C),
+                                       _grad_partials(grad_partials, P, N, C, patches[0].get_device()),
                                        _stream_of(stream, patches[0].get_device())), "tb_patch_gn_grad_stats")
     return grad_partials
 
@@ -1139,13 +1146,13 @@ def tb_patch_gn_grad_apply(grads: Sequence[torch.Tensor], patches: Sequence[torc
     ``dbeta`` ([C] of the patches' dtype), from the ``R`` record sets of both
     passes."""
     N, C, dt, sp, xs, ds = _gn_grad_args(grads, patches, G, partials, R, gamma, beta)
-    P = len(patches)
+    P, dev = len(patches), patches[0].get_device()
     os_, gp, bp = _gn_grad_outs(dxs, patches, C, dgamma, dbeta)
     _check(_lib.tb_patch_gn_grad_apply(xs, ds, os_, P, dt, N, C, sp, G,
-                                       partials.data_ptr(), _grad_partials(grad_partials, R, N, C), R,
+                                       partials.data_ptr(), _grad_partials(grad_partials, R, N, C, dev), R,
                                        gamma.data_ptr() if gamma is not None else None,
                                        beta.data_ptr() if beta is not None else None, float(eps), 1 if silu else 0,
-                                       gp, bp, _stream_of(stream, patches[0].get_device())),
+                                       gp, bp, _stream_of(stream, dev)),
            "tb_patch_gn_grad_apply")
     return dxs
 
@@ -1175,10 +1182,11 @@ def patch_group_norm_backward(grads: Sequence[torch.Tensor], patches: Sequence[t
     # one check and one set of argument arrays for both calls
     N, C, dt, sp, xs, ds = _gn_grad_args(grads, patches, G, partials, P, gamma, beta)
     os_, gp, bp = _gn_grad_outs(dxs, patches, C, dgamma, dbeta)
-    rec, grec = partials.data_ptr(), _grad_partials(grad_partials, P, N, C)
+    dev = patches[0].get_device()
+    rec, grec = partials.data_ptr(), _grad_partials(grad_partials, P, N, C, dev)
     ga = gamma.data_ptr() if gamma is not None else None
     be = beta.data_ptr() if beta is not None else None
-    handle, act = _stream_of(stream, patches[0].get_device()), 1 if silu else 0
+    handle, act = _stream_of(stream, dev), 1 if silu else 0
     _check(_lib.tb_patch_gn_grad_stats(xs, ds, P, dt, N, C, sp, G, rec, P, ga, be, eps, act, grec, handle),
            "tb_patch_gn_grad_stats")
     _check(_lib.tb_patch_gn_grad_apply(xs, ds, os_, P, dt, N, C, sp, G, rec, grec, P, ga, be, eps, act, gp, bp, handle),

@@ -963,7 +963,8 @@ class GradTable:
     """The gradients of a program's parameters (``grads``), and where their
     clipped values go (``outs``; None: in place), as the library takes them.
     It holds the tensors and their addresses, none of their contents: make it
-    once, and again when a gradient tensor is replaced."""
+    once, and again when a gradient tensor is replaced.  Every output is
+    separate from the others and from the other gradients."""
 
     def __init__(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None):
         self.grads = list(grads)
@@ -980,6 +981,7 @@ class GradTable:
             if g.device != self.grads[0].device or o.device != g.device:
                 raise ValueError("all gradients and outputs must be on one device")
         self.device = self.grads[0].device if n else None
+        self._refuse_overlaps()
         self._in = _ptr_array([g.data_ptr() for g in self.grads])
         self._out = _ptr_array([o.data_ptr() for o in self.outs])
         self._numel = (ctypes.c_int64 * max(1, n))(*[g.numel() for g in self.grads])
@@ -988,6 +990,26 @@ class GradTable:
 
     def __len__(self) -> int:
         return len(self.grads)
+
+    def _refuse_overlaps(self) -> None:
+        """Outputs must not share elements with one another, nor with any
+        gradient but their own, in place (a shared parameter's gradient is
+        listed once)."""
+        ranges = []
+        for g, o in zip(self.grads, self.outs):
+            at, to, n = g.data_ptr(), o.data_ptr(), g.numel() * g.element_size()
+            if n:
+                ranges.append((to, to + n, True))
+                if at != to:
+                    ranges.append((at, at + n, False))
+        read_to = written_to = 0
+        for first, last, written in sorted(ranges):
+            if first < written_to or (written and first < read_to):
+                raise ValueError("outputs overlap one another, or gradients of other outputs")
+            if written:
+                written_to = max(written_to, last)
+            else:
+                read_to = max(read_to, last)
 
 
 def new_grad_records(T: int, device=None) -> torch.Tensor:

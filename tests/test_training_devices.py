@@ -96,3 +96,22 @@ def test_one_tensor_on_another_device_is_refused(tbl, name, other):
     with pytest.raises(ValueError):
         _calls(tbl, 0, **{other: 1})[name]()
     assert not [c for c in tbl._lib.calls if c != "tb_grad_stats" or other in ("recs", "grad")]
+
+
+def test_gradients_and_outputs_that_overlap_are_refused(tbl):
+    # elements that one CTA writes and another reads or writes would be scaled once or twice, by chance
+    buf, a, b, e = t(0, 64), t(0, 8), t(0, 9), t(0, 0)
+    for grads, outs in (([a, b, e, e], None),                                # in place; empty ones anywhere
+                        (list(buf.split([5, 3, 56])), None),                 # neighbours
+                        ([a, a], [buf[:8], buf[8:16]]),                      # one gradient to two places
+                        ([buf[:8], buf[8:16]], [buf[:8], buf[16:24]])):      # some in place
+        tbl.GradTable(grads, outs)
+    for grads, outs in (([a, b, a], None),                                   # a shared parameter's gradient, twice
+                        ([buf[:8], buf[7:16]], None),
+                        ([a, b[:8]], [buf[:8], buf[:8]]),
+                        ([a, b[:8]], [buf[:8], buf[4:12]]),
+                        ([buf[:8]], [buf[1:9]]),                             # shifted onto itself
+                        ([buf[:8], a], [b[:8], buf[:8]]),                    # onto another's gradient
+                        ([buf[:32], a], [buf[32:], buf[8:16]])):
+        with pytest.raises(ValueError, match="overlap"):
+            tbl.GradTable(grads, outs)

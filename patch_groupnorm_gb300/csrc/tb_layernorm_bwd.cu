@@ -690,14 +690,18 @@ cudaError_t bwd_launch(const LnBwdParams& p, int sms, int* parts, cudaStream_t s
     LnBwdParams q = p;
     const int64_t bytes = p.cols * elem_size(DT), pitch = WHOLE ? bytes : (bytes + 31) / 16 * 16;
     const int64_t stage = (int64_t)rpc * (p.dtotal ? 3 : 2) * pitch;
-    const int64_t fit = ln_bwd_room(TPR) / stage;
-    q.stages = (int)(fit < 2 ? 2 : fit > LN_BWD_MAX_STAGES ? LN_BWD_MAX_STAGES : fit);
-    int64_t smem = rpc > 1 ? (int64_t)rpc * 2 * CPT * VEC * (TPR + 4) * 4 : 0;
-    if (smem < q.stages * stage) smem = q.stages * stage;
+    constexpr int64_t room = ln_bwd_room(TPR), sums = rpc > 1 ? (int64_t)rpc * 2 * CPT * VEC * (TPR + 4) * 4 : 0;
+    static_assert(2 * rpc * 3 * (TPR * CPT * 16 + (WHOLE ? 0 : 16)) <= room && sums <= room,
+                  "two stages of the widest rows, or the row groups' sums, do not fit");
+    const int64_t fit = room / stage;
+    q.stages = (int)(fit > LN_BWD_MAX_STAGES ? LN_BWD_MAX_STAGES : fit);
+    const int64_t smem = q.stages * stage > sums ? q.stages * stage : sums;
     void (*fn)(const LnBwdParams) =
         p.dtotal ? ln_bwd_kernel<DT, TPR, CPT, true, WHOLE> : ln_bwd_kernel<DT, TPR, CPT, false, WHOLE>;
     if (smem > 40 * 1024) {  // with the static shared memory, past the 48 KB default
-        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // the limit belongs to the function, not to the launch: one value for
+        // rows of every width, since several host threads may be launching it
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)room);
         if (e != cudaSuccess) return e;
     }
     return launch_pdl(fn, q, dim3((unsigned)grid), BWD_BLOCK, (size_t)smem, s);

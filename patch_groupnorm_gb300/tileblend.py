@@ -981,6 +981,7 @@ class GradTable:
             if g.device != self.grads[0].device or o.device != g.device:
                 raise ValueError("all gradients and outputs must be on one device")
         self.device = self.grads[0].device if n else None
+        self._index = self.grads[0].get_device() if n else None
         self._refuse_overlaps()
         self._in = _ptr_array([g.data_ptr() for g in self.grads])
         self._out = _ptr_array([o.data_ptr() for o in self.outs])
@@ -1024,17 +1025,22 @@ def new_grad_records(T: int, device=None) -> torch.Tensor:
 def _records(records: torch.Tensor, table: Optional[GradTable] = None) -> int:
     if records.get_device() < 0 or records.dtype is not torch.float64 or not records.is_contiguous():
         raise ValueError("records must be a contiguous float64 CUDA tensor")
-    if table is not None and len(table) and records.get_device() != table.grads[0].get_device():
+    if table is not None and table._index not in (None, records.get_device()):
         raise ValueError("records must be on the gradients' device")
     return records.data_ptr()
+
+
+def _own_records(records: torch.Tensor, table: GradTable) -> int:
+    at = _records(records, table)
+    if records.numel() != table._records and table._records >= 0:
+        raise ValueError("records must hold exactly %d values for %d gradients" % (table._records, len(table)))
+    return at
 
 
 def tb_grad_stats(table: GradTable, records: torch.Tensor, stream=None) -> torch.Tensor:
     """Sums of squares of the table's gradients into ``records`` (from
     ``new_grad_records``)."""
-    at = _records(records, table)
-    if records.numel() != table._records and table._records >= 0:
-        raise ValueError("records must hold exactly %d values for %d gradients" % (table._records, len(table)))
+    at = _own_records(records, table)
     _check(_lib.tb_grad_stats(table._in, table._numel, table._dtypes, len(table), at,
                               _stream_of(stream, records.get_device())), "tb_grad_stats")
     return records
@@ -1074,8 +1080,12 @@ def clip_grad_norm(grads, max_norm: float, records: Optional[torch.Tensor] = Non
         records = _on_stream(lambda: new_grad_records(len(table), table.device), stream)
     if norm is None:
         norm = _on_stream(lambda: torch.empty(1, dtype=torch.float32, device=records.device), stream)
-    tb_grad_stats(table, records, stream)
-    tb_grad_clip(table, records, max_norm, norm, stream)
+    # one check of the arguments for both calls
+    at, dev = _own_records(records, table), records.get_device()
+    out, handle, T = _norm_ptr(norm, dev), _stream_of(stream, dev), len(table)
+    _check(_lib.tb_grad_stats(table._in, table._numel, table._dtypes, T, at, handle), "tb_grad_stats")
+    _check(_lib.tb_grad_clip(table._in, table._out, table._numel, table._dtypes, T, at, records.numel(), max_norm, out,
+                             handle), "tb_grad_clip")
     return norm
 
 

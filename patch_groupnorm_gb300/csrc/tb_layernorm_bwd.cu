@@ -177,7 +177,12 @@ __global__ void __launch_bounds__(BWD_BLOCK, 1)
         ++turn;
         const T mean2 = L::splat(mean), rstd2 = L::splat(rstd);
         const uint32_t at = ring + (uint32_t)(st * NT) * pitch;
-        if (here && !late && !bar_wait(bars + st * 8u, parity, p.status)) {
+        bool missing = here && !late && !bar_wait(bars + st * 8u, parity, p.status);
+        if constexpr (!WHOLE) {
+            // a row group's first warp copies together, so it stops together
+            missing = __any_sync(0xffffffffu, missing);
+        }
+        if (missing) {
             late = true;
             // no new copies from here on; those in flight must land (or run
             // out their own wait) before the CTA's memory is given up
@@ -186,9 +191,6 @@ __global__ void __launch_bounds__(BWD_BLOCK, 1)
                     bar_wait(bars + (uint32_t)s * 8u, s >= st ? parity : parity ^ 1u, p.status);
                     if (++s == stages) s = 0;
                 }
-        }
-        if constexpr (!WHOLE) {
-            late = __any_sync(0xffffffffu, late);  // a row group's first warp copies together
         }
         // the lanes of group k of one tensor's row (zero past the row's end)
         auto lanes_of = [&](uint32_t from, int k, T (&f)[L::N]) {

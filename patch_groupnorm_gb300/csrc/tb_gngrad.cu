@@ -343,15 +343,7 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
             ring.next();
         }
     }
-    if (!ok) {
-        // a wait ran out: everyone leaves, once the copies in flight have
-        // landed (or their own waits have run out)
-        if (lane == 0) *ring.dead = 1;
-        for (int k = 0; k < GG_STAGES; ++k)
-            bar_wait(ring.full + k * 8u, k < ring.s ? ring.parity : ring.parity ^ 1u, p.status);
-        return;
-    }
-    for (int k = 0; k < GG_STAGES && claim(); ++k) {  // each stage's warp must see it
+    for (int k = 0; k < GG_STAGES && ok && claim(); ++k) {  // each stage's warp must see it
         if (lane == 0) {
             ring.stage[ring.s].kind = TASK_END;
             bar_arrive(ring.full + ring.s * 8u);
@@ -360,7 +352,13 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
         }
         ring.next();
     }
-    if (!ok && lane == 0) *ring.dead = 1;
+    if (!ok) {
+        // a wait ran out, of this warp or of another: everyone leaves, once the
+        // copies in flight have landed (or their own waits have run out)
+        if (lane == 0) *ring.dead = 1;
+        for (int k = 0; k < GG_STAGES; ++k)
+            bar_wait(ring.full + k * 8u, k < ring.s ? ring.parity : ring.parity ^ 1u, p.status);
+    }
 }
 
 // --- the computing warps ----------------------------------------------------------

@@ -177,20 +177,10 @@ __global__ void __launch_bounds__(BWD_BLOCK, 1)
         ++turn;
         const T mean2 = L::splat(mean), rstd2 = L::splat(rstd);
         const uint32_t at = ring + (uint32_t)(st * NT) * pitch;
-        bool missing = here && !late && !bar_wait(bars + st * 8u, parity, p.status);
+        // (no new copies from there on)
+        if (here && !late && !bar_wait(bars + st * 8u, parity, p.status)) late = true;
         if constexpr (!WHOLE) {
-            // a row group's first warp copies together, so it stops together
-            missing = __any_sync(0xffffffffu, missing);
-        }
-        if (missing) {
-            late = true;
-            // no new copies from here on; those in flight must land (or run
-            // out their own wait) before the CTA's memory is given up
-            if (t == 0)
-                for (int64_t r = row, s = st; r < ahead; r += step) {
-                    bar_wait(bars + (uint32_t)s * 8u, s >= st ? parity : parity ^ 1u, p.status);
-                    if (++s == stages) s = 0;
-                }
+            late = __any_sync(0xffffffffu, late);  // a row group's first warp copies together
         }
         // the lanes of group k of one tensor's row (zero past the row's end)
         auto lanes_of = [&](uint32_t from, int k, T (&f)[L::N]) {
@@ -320,6 +310,13 @@ __global__ void __launch_bounds__(BWD_BLOCK, 1)
         }
     }
 
+    if (late && t == 0) {
+        // copies in flight must land (or run out their own wait) before the
+        // CTA's memory is given up: every stage's last one
+        const int copied = (int)((ahead - ((int64_t)blockIdx.x * RPC + rl)) / step);
+        for (int s = 0; s < stages && s < copied; ++s)
+            bar_wait(bars + s * 8u, (uint32_t)((copied - 1 - s) / stages) & 1u, p.status);
+    }
     if (p.workspace == nullptr || late) return;
     float* const out = p.workspace + (int64_t)blockIdx.x * 2 * p.cols;
     if constexpr (RPC > 1) {

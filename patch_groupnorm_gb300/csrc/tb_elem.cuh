@@ -317,6 +317,10 @@ __device__ __forceinline__ void bulk_load_once(uint32_t dst, const void* src, ui
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// For the bulk copies that come after this fence (and a barrier in between):
+// elements that were copied one by one, by this thread or before a barrier that it
+// has passed, are in place, and a bulk copy may overwrite them.
+__device__ __forceinline__ void bulk_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // One of the elements on either side of a bulk copy, into shared memory.
 template <int ES>
 __device__ __forceinline__ void copy_element(uint32_t to, const char* from) {

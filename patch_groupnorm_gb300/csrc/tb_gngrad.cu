@@ -337,6 +337,7 @@ __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
                 } else if (tail < bytes) {
                     copy_element<ES>(to + tail, from + tail);
                 }
+                bulk_fence();
                 __syncwarp();
             }
             if (lane == 0) bar_arrive(bar);  // the elements copied one by one

@@ -199,16 +199,14 @@ __device__ __forceinline__ float weight_at(const void* w, int dtype, int64_t i, 
     return dtype == F16 ? elem_to_f<F16>(v) : elem_to_f<BF16>(v);
 }
 
-// VEC neighbouring weights starting at element i.  VECTOR: the address is
-// 16-byte aligned and whole chunks are in range.
-template <int VEC, bool VECTOR>
+// VEC neighbouring weights starting at element i (16-byte aligned where VEC > 1).
+template <int VEC>
 __device__ __forceinline__ void weights_at(const void* w, int dtype, int64_t i, float dflt, float (&f)[VEC]) {
     if (w == nullptr) {
 #pragma unroll
         for (int q = 0; q < VEC; ++q) f[q] = dflt;
-    } else if constexpr (!VECTOR || VEC < 4) {
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) f[q] = weight_at(w, dtype, i + q, dflt);
+    } else if constexpr (VEC == 1) {
+        f[0] = weight_at(w, dtype, i, dflt);
     } else if (dtype == F32) {
 #pragma unroll
         for (int q = 0; q < VEC; q += 4) {
@@ -232,7 +230,7 @@ template <int VEC>
 __device__ __forceinline__ void weight_lanes(const void* w, int dtype, int64_t i, float dflt,
                                              typename Lanes<VEC>::T (&f)[Lanes<VEC>::N]) {
     float e[VEC];
-    weights_at<VEC, true>(w, dtype, i, dflt, e);
+    weights_at<VEC>(w, dtype, i, dflt, e);
     if constexpr (VEC == 1) {
         f[0] = e[0];
     } else {

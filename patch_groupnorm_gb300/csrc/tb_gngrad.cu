@@ -236,7 +236,6 @@ __device__ __forceinline__ void constants_loop(const GnGradParams& p, int dtype,
 template <int DT>
 __device__ __forceinline__ void copy_loop(const GnGradParams& p, Ring ring) {
     constexpr int ES = elem_size(DT);
-    constexpr int VEC = 16 / ES;
     const int lane = threadIdx.x & 31;
     // (the host keeps the tasks below 2^31: 32-bit divisions throughout, the
     // 64-bit ones took longer than a task's copies)

@@ -201,8 +201,8 @@ __global__ void __launch_bounds__(LONG_BLOCK) ln_fwd_long_kernel(const __grid_co
         for (int64_t c = threadIdx.x; c < nchunk; c += LONG_BLOCK) {
             float f[VEC], gv[VEC], bv[VEC];
             unpack<DT, VEC>(h[c], f);
-            weights_at<VEC, true>(p.gamma, p.wdtype, c * VEC, 1.f, gv);
-            weights_at<VEC, true>(p.beta, p.wdtype, c * VEC, 0.f, bv);
+            weights_at<VEC>(p.gamma, p.wdtype, c * VEC, 1.f, gv);
+            weights_at<VEC>(p.beta, p.wdtype, c * VEC, 0.f, bv);
 #pragma unroll
             for (int q = 0; q < VEC; ++q) f[q] = fmaf((f[q] - mean) * rstd, gv[q], bv[q]);
             y[c] = pack<DT, VEC>(f);

@@ -323,6 +323,7 @@ __global__ void __launch_bounds__(BWD_BLOCK, 1)
     if (p.workspace == nullptr || late) return;
     float* const out = p.workspace + (int64_t)blockIdx.x * 2 * p.cols;
     if constexpr (RPC > 1) {
+        static_assert(WHOLE, "wide odd rows have a CTA each");
         // the CTA's row groups' sums meet in the ring's memory, a thread's
         // value k * VEC + q at [group][which][k * VEC + q][t], the rows four
         // words longer than TPR so that neighbouring columns are in different
@@ -343,8 +344,7 @@ __global__ void __launch_bounds__(BWD_BLOCK, 1)
         for (int i = threadIdx.x; i < 2 * cols; i += BLOCK) {
             const int which = i >= cols ? 1 : 0;
             const int col = i - which * cols, c = col / VEC;
-            const int value = WHOLE ? c / TPR * VEC + col % VEC : col / TPR, thread = WHOLE ? c % TPR : col % TPR;
-            const float* const at = s_acc + (which * N + value) * PITCH + thread;
+            const float* const at = s_acc + (which * N + c / TPR * VEC + col % VEC) * PITCH + c % TPR;
             float v = at[0];
 #pragma unroll 8
             for (int w = 1; w < RPC; ++w) v += at[w * 2 * N * PITCH];
@@ -381,10 +381,7 @@ constexpr int64_t ELEM_COLS = 4096;
 template <int DT, int TPR, int CPT, bool TOT>
 __global__ void __launch_bounds__(BWD_BLOCK, 1)
     ln_bwd_elem_kernel(const __grid_constant__ LnBwdParams p) {
-    constexpr int VEC = 1;
     using W = typename Word<elem_size(DT)>::T;
-    using L = Lanes<VEC>;
-    using T = typename L::T;
     constexpr int BLOCK = BWD_BLOCK;
     constexpr int RPC = BLOCK / TPR;
     constexpr int WPR = TPR / 32;
@@ -393,7 +390,7 @@ __global__ void __launch_bounds__(BWD_BLOCK, 1)
     extern __shared__ __align__(16) unsigned char s_rows[];  // RPC > 1: the CTA's sums
     const int t = threadIdx.x % TPR, rl = threadIdx.x / TPR;
     const int64_t step = (int64_t)gridDim.x * RPC;
-    const int nchunk = (int)(p.cols / VEC);
+    const int cols = (int)p.cols;
     const float inv_n = 1.0f / (float)p.cols;
     const uint32_t row_bytes = (uint32_t)p.cols * elem_size(DT);
     grid_wait();
@@ -407,7 +404,7 @@ __global__ void __launch_bounds__(BWD_BLOCK, 1)
         for (int k = 0; k < CPT; ++k) {
             const int c = t + k * TPR;
             const W* const src = reinterpret_cast<const W*>(at) + c;
-            if (c < nchunk && in_bounds(src, sizeof(W), at, row_bytes, p.status)) v[k] = __ldcs(src);
+            if (c < cols && in_bounds(src, sizeof(W), at, row_bytes, p.status)) v[k] = __ldcs(src);
         }
     };
     W nd[CPT], nx[CPT], nt[CPT];
@@ -431,19 +428,18 @@ __global__ void __launch_bounds__(BWD_BLOCK, 1)
     }
     stats(row, mean_now, rstd_now);
     stats(row + HOLD * step, mean_next, rstd_next);
-    T g[CPT][L::N], dg[CPT][L::N], db[CPT][L::N];
+    float g[CPT], dg[CPT], db[CPT];
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
         const int c = t + k * TPR;
-        if (c < nchunk) weight_lanes<VEC>(p.gamma, p.wdtype, (int64_t)c * VEC, 1.f, g[k]);
-#pragma unroll
-        for (int q = 0; q < L::N; ++q) dg[k][q] = db[k][q] = L::splat(0.f);
+        if (c < cols) g[k] = weight_at(p.gamma, p.wdtype, c, 1.f);
+        dg[k] = db[k] = 0.f;
     }
     int phase = 0, turn = 0;
     // (the row groups of one warp go round together, those without a row idle)
     const int64_t warp_row = TPR < 32 ? (int64_t)blockIdx.x * RPC + rl / (32 / HOLD) * (32 / HOLD) : row;
     for (int64_t any = warp_row; any < p.rows; any += step, row += step) {
-        const int mine = TPR >= 32 || row < p.rows ? nchunk : 0;
+        const int mine = TPR >= 32 || row < p.rows ? cols : 0;
         if (turn == HOLD) {
             turn = 0;
             mean_now = mean_next;
@@ -453,7 +449,6 @@ __global__ void __launch_bounds__(BWD_BLOCK, 1)
         const float mean = __shfl_sync(0xffffffffu, mean_now, (lane & ~(HOLD - 1)) + turn);
         const float rstd = __shfl_sync(0xffffffffu, rstd_now, (lane & ~(HOLD - 1)) + turn);
         ++turn;
-        const T mean2 = L::splat(mean), rstd2 = L::splat(rstd);
         W cd[CPT], cx[CPT], ct[CPT];
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
@@ -466,26 +461,20 @@ __global__ void __launch_bounds__(BWD_BLOCK, 1)
             fetch(p.x, row + step, p.x_ld, nx);
             if constexpr (TOT) fetch(p.dtotal, row + step, p.dt_ld, nt);
         }
-        T d[CPT][L::N], x[CPT][L::N];
-        T a1 = L::splat(0.f), a2 = L::splat(0.f);
+        float d[CPT], x[CPT], s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
             if (t + k * TPR < mine) {
-                to_lanes<DT, 1>(cd[k], d[k]);
-                to_lanes<DT, 1>(cx[k], x[k]);
-#pragma unroll
-                for (int q = 0; q < L::N; ++q) {
-                    db[k][q] = vadd(db[k][q], d[k][q]);
-                    x[k][q] = vsub(x[k][q], mean2);
-                    d[k][q] = vmul(d[k][q], rstd2);
-                    const T gd = vmul(d[k][q], g[k][q]);
-                    a1 = vadd(a1, gd);
-                    a2 = vfma(gd, x[k][q], a2);
-                    dg[k][q] = vfma(d[k][q], x[k][q], dg[k][q]);
-                }
+                d[k] = elem_to_f<DT>(cd[k]);
+                x[k] = elem_to_f<DT>(cx[k]) - mean;
+                db[k] += d[k];
+                d[k] *= rstd;
+                const float gd = d[k] * g[k];
+                s1 += gd;
+                s2 = fmaf(gd, x[k], s2);
+                dg[k] = fmaf(d[k], x[k], dg[k]);
             }
         }
-        float s1 = vsum(a1), s2 = vsum(a2);
 #pragma unroll
         for (int o = HOLD / 2; o >= 1; o >>= 1) {
             s1 += __shfl_xor_sync(0xffffffffu, s1, o);
@@ -507,83 +496,53 @@ __global__ void __launch_bounds__(BWD_BLOCK, 1)
         if (p.dx != nullptr) {
             // s1 = rstd * sum(g), s2 = sum(g * xhat): with u = x - mean and
             // v = dy * rstd, dx = v * gamma - u * rstd^2 * s2 / n - s1 / n
-            const T ca = L::splat(-rstd * rstd * (s2 * inv_n)), cb = L::splat(-(s1 * inv_n));
+            const float ca = -rstd * rstd * (s2 * inv_n), cb = -(s1 * inv_n);
             char* const out = reinterpret_cast<char*>(p.dx) + row * p.dx_ld * elem_size(DT);
 #pragma unroll
             for (int k = 0; k < CPT; ++k) {
                 const int c = t + k * TPR;
                 if (c < mine) {
-                    T o[L::N];
-                    if constexpr (TOT) {
-                        to_lanes<DT, 1>(ct[k], o);
-#pragma unroll
-                        for (int q = 0; q < L::N; ++q) o[q] = vadd(o[q], cb);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < L::N; ++q) o[q] = cb;
-                    }
-#pragma unroll
-                    for (int q = 0; q < L::N; ++q)
-                        o[q] = vfma(d[k][q], g[k][q], vfma(x[k][q], ca, o[q]));
+                    const float t0 = TOT ? elem_to_f<DT>(ct[k]) + cb : cb;
+                    const float o[1] = {fmaf(d[k], g[k], fmaf(x[k], ca, t0))};
                     W* const dst = reinterpret_cast<W*>(out) + c;
-                    if (in_bounds(dst, sizeof(W), out, row_bytes, p.status)) *dst = from_lanes<DT, VEC>(o);
+                    if (in_bounds(dst, sizeof(W), out, row_bytes, p.status)) *dst = pack<DT, 1>(o);
                 }
             }
         }
     }
 
-    float fg[CPT][VEC], fb[CPT][VEC];
-#pragma unroll
-    for (int k = 0; k < CPT; ++k) {
-        if constexpr (VEC == 1) {
-            fg[k][0] = dg[k][0];
-            fb[k][0] = db[k][0];
-        } else {
-#pragma unroll
-            for (int q = 0; q < VEC / 2; ++q) {
-                halves(dg[k][q], fg[k][2 * q], fg[k][2 * q + 1]);
-                halves(db[k][q], fb[k][2 * q], fb[k][2 * q + 1]);
-            }
-        }
-    }
     if (p.workspace == nullptr) return;
     float* const out = p.workspace + (int64_t)blockIdx.x * 2 * p.cols;
     if constexpr (RPC > 1) {
-        // the CTA's row groups' sums meet in the ring's memory, each thread's
-        // column k * VEC + q at [group][which][k * VEC + q][t], the rows four
-        // words longer than TPR so that neighbouring columns are in different
-        // banks; then every column is added up over the groups in order
-        constexpr int PITCH = TPR + 4, N = CPT * VEC;
+        // the CTA's row groups' sums meet in shared memory, a thread's column k at
+        // [group][which][k][t], the rows four words longer than TPR so that
+        // neighbouring columns are in different banks; then every column is
+        // added up over the groups in order
+        constexpr int PITCH = TPR + 4;
         float* const s_acc = reinterpret_cast<float*>(s_rows);
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
-#pragma unroll
-            for (int q = 0; q < VEC; ++q) {
-                s_acc[((rl * 2 + 0) * N + k * VEC + q) * PITCH + t] = fg[k][q];
-                s_acc[((rl * 2 + 1) * N + k * VEC + q) * PITCH + t] = fb[k][q];
-            }
+            s_acc[((rl * 2 + 0) * CPT + k) * PITCH + t] = dg[k];
+            s_acc[((rl * 2 + 1) * CPT + k) * PITCH + t] = db[k];
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < 2 * (int)p.cols; i += BLOCK) {
-            const int which = i >= (int)p.cols ? 1 : 0;
-            const int col = i - which * (int)p.cols, c = col / VEC;
-            const float* const at = s_acc + (which * N + c / TPR * VEC + col % VEC) * PITCH + c % TPR;
+        for (int i = threadIdx.x; i < 2 * cols; i += BLOCK) {
+            const int which = i >= cols ? 1 : 0;
+            const int col = i - which * cols;
+            const float* const at = s_acc + (which * CPT + col / TPR) * PITCH + col % TPR;
             float v = at[0];
 #pragma unroll
-            for (int w = 1; w < RPC; ++w) v += at[w * 2 * N * PITCH];
+            for (int w = 1; w < RPC; ++w) v += at[w * 2 * CPT * PITCH];
             out[i] = v;
         }
     } else {
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
             const int c = t + k * TPR;
-            if (c < nchunk) {
-#pragma unroll
-                for (int q = 0; q < VEC; ++q) {
-                    out[c * VEC + q] = fg[k][q];
-                    out[p.cols + c * VEC + q] = fb[k][q];
-                }
+            if (c < cols) {
+                out[c] = dg[k];
+                out[p.cols + c] = db[k];
             }
         }
     }
@@ -610,7 +569,7 @@ __global__ void __launch_bounds__(LONG_BLOCK) ln_bwd_long_kernel(const __grid_co
             float d[VEC], xv[VEC], gv[VEC];
             unpack<DT, VEC>(dy[c], d);
             unpack<DT, VEC>(x[c], xv);
-            weights_at<VEC, true>(p.gamma, p.wdtype, c * VEC, 1.f, gv);
+            weights_at<VEC>(p.gamma, p.wdtype, c * VEC, 1.f, gv);
 #pragma unroll
             for (int q = 0; q < VEC; ++q) {
                 const float xh = (xv[q] - mean) * rstd, gd = d[q] * gv[q];
@@ -630,7 +589,7 @@ __global__ void __launch_bounds__(LONG_BLOCK) ln_bwd_long_kernel(const __grid_co
             float d[VEC], xv[VEC], gv[VEC], o[VEC];
             unpack<DT, VEC>(dy[c], d);
             unpack<DT, VEC>(x[c], xv);
-            weights_at<VEC, true>(p.gamma, p.wdtype, c * VEC, 1.f, gv);
+            weights_at<VEC>(p.gamma, p.wdtype, c * VEC, 1.f, gv);
 #pragma unroll
             for (int q = 0; q < VEC; ++q) {
                 const float xh = (xv[q] - mean) * rstd;

@@ -137,11 +137,11 @@ __device__ __forceinline__ bool index_ok(bool ok, uint32_t* status) {
 // SMs as the last wave drains (small stitches 12-18% faster back to back).  The
 // records of the GroupNorm's backward pass, for the dx that follow: one CTA
 // fills an SM, so the next grid's CTAs start as this one's leave, and set their
-// rings up while the others work.  The forward GroupNorm's statistics grid is one wave spread evenly over the SMs, and a
-// grid placed early, while its predecessor drains, lands unevenly (measured
-// up to 2x slower); so no kernel that may precede it in a sharded decode --
-// the Patchify copy, the forward GroupNorm itself -- triggers, and the
-// ramp stitch measured no gain from it.
+// rings up while the others work.  The forward GroupNorm's statistics grid is
+// one wave spread evenly over the SMs, and a grid placed early, while its
+// predecessor drains, lands unevenly (measured up to 2x slower); so no kernel
+// that may precede it in a sharded decode -- the Patchify copy, the forward
+// GroupNorm itself -- triggers, and the ramp stitch measured no gain from it.
 #ifndef TB_PDL_TRIGGER
 #define TB_PDL_TRIGGER 1
 #endif

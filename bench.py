@@ -114,7 +114,12 @@ def ramp_bytes(ay, ax, planes, esize):
 
 
 def source_digest(path):
-    return hashlib.sha256(open(path, "rb").read()).hexdigest()[:16]
+    """Digest of a kernel's source: one file, or several joined by "+" (a
+    kernel and the header it shares; relative ones from the repository's root)."""
+    h = hashlib.sha256()
+    for p in path.split("+"):
+        h.update(open(os.path.join(ROOT, p), "rb").read())
+    return h.hexdigest()[:16]
 
 
 def profiled_traffic(kernel_key, src_path):

@@ -17,10 +17,13 @@
 // 4D (1 x 512 x 256 x 256 bf16) takes 62.8 us, 5D (1 x 384 x 13 x 120 x 208) 200.
 // One launch with both passes interleaved, a group's dx following its records
 // by 15 to 60 MB, was built and measured: it reads memory once, but its waits
-// cost most of what that saves (61.8 and 184 us), because computing, not memory,
-// is the longer half: the SiLU derivative takes about 11 instructions a pair of
-// elements in each pass, and the kernel issues an instruction in 55 % of all
-// cycles.
+// cost most of what that saves (61.8 and 184 us).  What bounds 4D is latency,
+// neither memory (55 % busy in both passes) nor the issue slots (53 and 45 %): a
+// warp has one word of x and dy in work at a time, and a chain of an exponential
+// and a reciprocal for each pair of elements.  Without SiLU 4D takes 56.4 us.
+// In f32 both passes are near the copy rate (4D 105 us, read twice 100).
+// Tensors at different offsets from 16-byte boundaries take the element kernels
+// (4D with dy one element off: 253 us).
 //
 // One CTA per SM: 16 warps compute, a 17th copies the tasks' rows into a ring
 // of three stages in shared memory (64 KB each: x and dy), and each stage has a
@@ -42,9 +45,10 @@ constexpr int GG_THREADS = GG_WARPS * 32;
 constexpr int GG_STAGES = 3;
 constexpr int GG_BLOCK = GG_THREADS + 32 * (1 + GG_STAGES);  // + the copying warp, and a warp of constants per stage
 // Bytes of x (and of dy) at the end of each CTA's run that L2 is to keep for the
-// second launch, 97 MB over 152 CTAs; GRAD_STATS reads what comes before
-// them evict-first.  (4D / 5D with 192, 256, 320, 384 KB and all alike:
-// 63.7 / 200, 62.9 / 199, 62.5 / 199, 62.8 / 200, 63.2 / 206 us.)
+// second launch, 97 MB over 152 CTAs of this GPU's 129; GRAD_STATS reads what
+// comes before them evict-first.  (4D / 5D with 192, 256, 320, 384 KB and all
+// alike: 63.7 / 200, 62.9 / 199, 62.5 / 199, 62.8 / 200, 63.2 / 206 us: what counts
+// is that some are marked, the size within these does not.)
 constexpr int64_t GG_KEEP = 320 * 1024;
 constexpr int GG_TENSOR = GRAD_STAGE_BYTES + 128;  // room for a first, partial word
 constexpr int GG_SMEM = GG_STAGES * 2 * GG_TENSOR;

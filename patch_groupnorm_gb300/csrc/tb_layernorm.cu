@@ -16,8 +16,15 @@
 // Bound by memory: 16384 x 4096 bf16 with residual moves 537 MB in 82.5 us (6.5
 // TB/s, 97 % of the measured copy rate), 65536 x 512 bf16 134 MB in 25.5 us (79
 // %, where ten shuffles a row per warp count), 262144 x 64 bf16 67 MB in 14.3 us
-// (73 %).  Rows of single elements (no 16-byte words) load 2 bytes a lane:
-// 65536 x 515 bf16 takes 72 us.  One row of 4096 takes 8 us, all of it the call.
+// (73 %).  One row of 4096 takes 9 us, all of it the call.
+// Rows of single elements (no 16-byte words) are bound by this kernel, which
+// moves an element a lane and instruction, not by memory: 65536 x 515 bf16 takes
+// 71 us, 29 %, 13419 x 5001 107 us, 37 %, in f32 122 us, 66 %.
+// Registers run out, and spill, with 16 single elements a thread (256 threads
+// 112 to 936 bytes, 1024 threads 308 to 1068), with the 1024-thread forms of 16-bit
+// rows (40 to 256 bytes) and of f32 rows past 8192 columns (296, with residual
+// 656), and a little (16 to 72 bytes) with residual in 16-bit rows of up to 2048
+// columns: 4096 x 16384 f32 takes 105 us, 76 %, with residual 241, 67 %.
 #include "tb_layernorm.cuh"
 
 namespace tb {

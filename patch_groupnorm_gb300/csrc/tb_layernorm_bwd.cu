@@ -9,6 +9,12 @@
 // (and 10 MB of partial weight gradients) in 86.7 us, 93 % of the measured copy
 // rate; 65536 x 512 bf16 201 MB in 34.9 us (86 %, half of all issue slots busy).
 // One launch more adds up the CTAs' partial weight gradients.
+// Farther from it: rows of 1025 to 2048 words (4096 x 16384 bf16 131 us, 46 %: one
+// row a CTA at a time, read twice from shared memory, and 80 MB of partial
+// weight gradients), single elements (65536 x 515 bf16 87 us, 35 %: an element
+// a lane and instruction), and rows past 2048 words (4096 x 16384 f32 416 us, 29 %;
+// 2048 x 40000 bf16 778 us, 9 %: the weight gradients are read and written in
+// memory once a row, and nothing is copied ahead).
 #include "tb_layernorm.cuh"
 
 namespace tb {

@@ -798,6 +798,123 @@ tb_status tb_patch_gn_grad_apply(const void* const* patches, const void* const* 
                                  const void* gamma, const void* beta, float eps, int32_t silu, void* dgamma,
                                  void* dbeta, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Channels last: PatchGroupNorm of patches [N][spatial][C], forward and
+ * backward, and dropout.  What a training step runs whose projections read
+ * one position's channels side by side.
+ *
+ * The conventions are those of the training calls above.  The records are
+ * those of the channels-first calls (tb_gn_partial, tb_gn_grad_partial, in the
+ * same places), so either kind of statistics serves either kind of apply, and
+ * ranks gather them alike.  Captured into a CUDA graph and replayed with new
+ * contents (tested): all.
+ * ------------------------------------------------------------------------ */
+
+/* Most channels of the channels-last calls. */
+#define TB_GN_CL_MAX_CHANNELS 8192
+
+/*
+ * tb_patch_gn_stats_cl -- tb_patch_gn_stats for channels-last patches.
+ *   patches   host array of P device pointers; patch p is [N, spatial[p], C]
+ *   spatial   host array: positions of each patch (>= 0)
+ *   partials  device [P][N][G][TB_GN_PARTS], 16-byte aligned, written fully
+ * A patch may start at any multiple of its element's size; C may be any
+ * number of channels that G divides.
+ * Errors: TB_ERR_NULL, TB_ERR_DTYPE, TB_ERR_SHAPE (P < 1, N or C < 0, G < 1, C
+ * not a multiple of G, a negative size), TB_ERR_UNSUPPORTED (P > 64, C >
+ * TB_GN_CL_MAX_CHANNELS, P * N * C * TB_GN_PARTS above 2e9, a misaligned
+ * pointer), TB_ERR_CUDA.
+ */
+tb_status tb_patch_gn_stats_cl(const void* const* patches, int32_t P, tb_dtype dtype, int64_t N, int64_t C,
+                               const int64_t* spatial, int32_t G, tb_gn_partial* partials, void* stream);
+
+/*
+ * tb_patch_gn_apply_cl -- tb_patch_gn_apply_gathered for channels-last
+ * patches: with the mean and rstd pooled over the R record sets,
+ *     y = rnd(act((x - mean) * rstd * gamma + beta)),  act = silu or none
+ *   outs      host array of P device pointers; outs[p] may equal patches[p]
+ *   gamma, beta  device [C] of dtype, or NULL for 1 / 0
+ * A group with a NaN or an infinity comes out NaN; others are unaffected.
+ * Errors: as tb_patch_gn_stats_cl, with R (1 .. 65536) in the place of P where
+ * R is larger; TB_ERR_SHAPE also for an eps that is negative, NaN or infinite.
+ */
+tb_status tb_patch_gn_apply_cl(const void* const* patches, void* const* outs, int32_t P, tb_dtype dtype, int64_t N,
+                               int64_t C, const int64_t* spatial, int32_t G, const tb_gn_partial* partials, int32_t R,
+                               const void* gamma, const void* beta, float eps, int32_t silu, void* stream);
+
+/* tb_patch_group_norm_cl -- both steps in one call, on these patches' own
+ * records (R = P). */
+tb_status tb_patch_group_norm_cl(const void* const* patches, void* const* outs, int32_t P, tb_dtype dtype, int64_t N,
+                                 int64_t C, const int64_t* spatial, int32_t G, tb_gn_partial* partials,
+                                 const void* gamma, const void* beta, float eps, int32_t silu, void* stream);
+
+/* Bytes of workspace tb_patch_gn_grad_apply_cl needs: 16 * N * G; -1 for
+ * sizes it does not take. */
+int64_t tb_patch_gn_workspace_cl(int64_t N, int32_t G);
+
+/* tb_patch_gn_grad_stats_cl -- tb_patch_gn_grad_stats for channels-last
+ * patches and gradients.  Errors as tb_patch_gn_apply_cl. */
+tb_status tb_patch_gn_grad_stats_cl(const void* const* patches, const void* const* grads, int32_t P, tb_dtype dtype,
+                                    int64_t N, int64_t C, const int64_t* spatial, int32_t G,
+                                    const tb_gn_partial* partials, int32_t R, const void* gamma, const void* beta,
+                                    float eps, int32_t silu, tb_gn_grad_partial* grad_partials, void* stream);
+
+/*
+ * tb_patch_gn_grad_apply_cl -- tb_patch_gn_grad_apply for channels-last
+ * patches, gradients and outputs.
+ *   workspace  device, 16-byte aligned, workspace_bytes >=
+ *              tb_patch_gn_workspace_cl(N, G).  Its contents need no clearing
+ *              and are not kept; calls that may run at the same time need one
+ *              each
+ * Errors as tb_patch_gn_apply_cl, TB_ERR_SHAPE also for a workspace too small.
+ */
+tb_status tb_patch_gn_grad_apply_cl(const void* const* patches, const void* const* grads, void* const* outs, int32_t P,
+                                    tb_dtype dtype, int64_t N, int64_t C, const int64_t* spatial, int32_t G,
+                                    const tb_gn_partial* partials, const tb_gn_grad_partial* grad_partials, int32_t R,
+                                    const void* gamma, const void* beta, float eps, int32_t silu, void* dgamma,
+                                    void* dbeta, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* tb_patch_group_norm_backward_cl -- both steps of the backward pass in one
+ * call, on these patches' own records (R = P). */
+tb_status tb_patch_group_norm_backward_cl(const void* const* patches, const void* const* grads, void* const* outs,
+                                          int32_t P, tb_dtype dtype, int64_t N, int64_t C, const int64_t* spatial,
+                                          int32_t G, const tb_gn_partial* partials,
+                                          tb_gn_grad_partial* grad_partials, const void* gamma, const void* beta,
+                                          float eps, int32_t silu, void* dgamma, void* dbeta, void* workspace,
+                                          int64_t workspace_bytes, void* stream);
+
+/*
+ * tb_dropout -- dropout over rows, with a mask that is computed and never
+ * stored:
+ *     y = rnd((bits(i) >= t ? x * 65536 / (65536 - t) : 0) + residual)
+ * in fp32, rounded once, with t = floor(p * 65536 + 1/2), so that p is taken in
+ * steps of 2^-16 and the expectation is x exactly.  i = row * cols + column,
+ * whatever the strides.  bits(i) is 16 bits of Philox 4x32 (ten rounds) with the
+ * key `seed` and the counter (i / 8, offset), 64 bits each, the low word first;
+ * element e of a block of eight has the low (e even) or high half of word e / 2.
+ * The backward pass is the same call on the gradient: dx = tb_dropout(dy) with
+ * the same p, seed, offset and sizes, without a residual (whose gradient is dy).
+ *
+ *   x, x_ld   [rows, cols] of dtype, row r at element r * x_ld (x_ld >= cols;
+ *             any value when rows <= 1); the same for residual and y
+ *   residual  NULL, or rows to add
+ *   y         may equal x or residual (with the same stride); no other overlap
+ *   p         0 .. 1.  t = 0 keeps everything, t = 65536 nothing
+ *   seed, offset   one mask per (seed, offset); calls of one step take other
+ *             offsets, or other seeds, each
+ *   state     NULL, or device [2]: added to seed and offset (modulo 2^64) when
+ *             the kernel runs, so that a captured graph draws new masks as its
+ *             program changes them
+ * A dropped NaN or infinity is a zero.
+ * rows == 0 or cols == 0 launches nothing.
+ * Errors: TB_ERR_NULL (x or y), TB_ERR_DTYPE, TB_ERR_SHAPE (negative sizes, a
+ * stride below cols, p outside [0, 1] or NaN), TB_ERR_UNSUPPORTED (more than
+ * 2^40 elements, a misaligned pointer), TB_ERR_CUDA.
+ */
+tb_status tb_dropout(const void* x, int64_t x_ld, const void* residual, int64_t residual_ld, tb_dtype dtype,
+                     int64_t rows, int64_t cols, double p, uint64_t seed, uint64_t offset, const uint64_t* state,
+                     void* y, int64_t y_ld, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -35,8 +35,12 @@ UNITS = {
     "tb_gradclip.cu": [],
     "tb_gngrad.cu": [],
     "tb_train.cpp": [],
+    "tb_gncl.cu": [],
+    "tb_gncl_bwd.cu": [],
+    "tb_dropout.cu": [],
+    "tb_chlast.cpp": [],
 }
-HEADERS = ["tb_internal.h", "tb_elem.cuh", "tb_layernorm.cuh", "tb_groupnorm.cuh"]
+HEADERS = ["tb_internal.h", "tb_elem.cuh", "tb_layernorm.cuh", "tb_groupnorm.cuh", "tb_gncl.cuh", "tb_args.h"]
 
 
 def _nvcc() -> str:

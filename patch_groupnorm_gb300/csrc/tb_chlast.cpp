@@ -1,0 +1,352 @@
+// tb_chlast.cpp -- C ABI of the channels-last calls: PatchGroupNorm forward and
+// backward, and dropout.  Argument validation and launch configuration only.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <numeric>
+
+#include "tb_args.h"
+
+namespace {
+
+using tb::aligned;
+using tb::elem_bytes;
+using tb::known;
+using tb::launched;
+
+// What a call gives; outs, grads and the rest are NULL where it has none.
+struct ClCall {
+    const void* const* patches;
+    const void* const* grads;
+    void* const* outs;
+    int32_t P;
+    tb_dtype dtype;
+    int64_t N, C;
+    const int64_t* spatial;
+    int32_t G;
+    const tb_gn_partial* partials;
+    int32_t R;
+    const void* gamma;
+    const void* beta;
+    float eps;
+    int32_t silu;
+};
+
+tb_status cl_params(tb::GnClParams& prm, const ClCall& c, bool grads, bool outs) {
+    if (!known(c.dtype)) return TB_ERR_DTYPE;
+    if (c.P < 1 || c.N < 0 || c.C < 0 || c.G < 1 || c.R < 1) return TB_ERR_SHAPE;
+    if (c.C % c.G != 0) return TB_ERR_SHAPE;
+    if (!(c.eps >= 0.0f) || std::isinf(c.eps)) return TB_ERR_SHAPE;
+    if (c.P > tb::GN_MAXP || c.R > 65536 || c.C > tb::CL_MAXC) return TB_ERR_UNSUPPORTED;
+    if (c.spatial == nullptr || c.patches == nullptr || (grads && c.grads == nullptr) || (outs && c.outs == nullptr))
+        return TB_ERR_NULL;
+    if ((double)std::max(c.P, c.R) * (double)c.N * (double)std::max<int64_t>(c.C, c.G) * TB_GN_PARTS > 2.0e9)
+        return TB_ERR_UNSUPPORTED;
+    std::memset(&prm, 0, sizeof(prm));
+    const int es = elem_bytes(c.dtype);
+    for (int p = 0; p < c.P; ++p) {
+        if (c.spatial[p] < 0) return TB_ERR_SHAPE;
+        prm.spatial[p] = c.spatial[p];
+        if (c.N == 0 || c.C == 0 || c.spatial[p] == 0) continue;
+        if ((double)c.N * (double)c.C * (double)c.spatial[p] > 1.0e13) return TB_ERR_UNSUPPORTED;
+        prm.patches[p] = c.patches[p];
+        if (grads) prm.grads[p] = c.grads[p];
+        if (outs) prm.outs[p] = c.outs[p];
+        if (prm.patches[p] == nullptr || (grads && prm.grads[p] == nullptr) || (outs && prm.outs[p] == nullptr))
+            return TB_ERR_NULL;
+        if (!aligned(prm.patches[p], es) || !aligned(prm.grads[p], es) || !aligned(prm.outs[p], es))
+            return TB_ERR_UNSUPPORTED;
+    }
+    if (c.N > 0 && c.C > 0 && c.partials == nullptr) return TB_ERR_NULL;
+    if (!aligned(c.gamma, es) || !aligned(c.beta, es) || !aligned(c.partials, 16)) return TB_ERR_UNSUPPORTED;
+    prm.partials = reinterpret_cast<tb::GnPartial*>(const_cast<tb_gn_partial*>(c.partials));
+    prm.gamma = c.gamma;
+    prm.beta = c.beta;
+    prm.N = c.N;
+    prm.C = c.C;
+    prm.P = c.P;
+    prm.G = c.G;
+    prm.R = c.R;
+    prm.eps = c.eps;
+    prm.silu = c.silu ? 1 : 0;
+    prm.status = tb::checked_build_status();
+    return TB_OK;
+}
+
+// Chunks of 16 bytes, if the call's tensors of every patch share their offset
+// from 16-byte boundaries; then the period, and the columns a CTA takes at a time.
+bool cl_chunks(tb::GnClParams& prm, tb_dtype dtype, bool grads, bool outs) {
+    const int vec = 16 / elem_bytes(dtype);
+    bool vector = true;
+    for (int p = 0; p < prm.P; ++p) {
+        const uintptr_t off = (uintptr_t)prm.patches[p] & 15u;
+        if (grads && ((uintptr_t)prm.grads[p] & 15u) != off) vector = false;
+        if (outs && ((uintptr_t)prm.outs[p] & 15u) != off) vector = false;
+    }
+    prm.period = (int32_t)(vector ? prm.C / std::gcd<int64_t>(prm.C, vec) : prm.C);
+    const int turns = (prm.period + tb::CL_BLOCK - 1) / tb::CL_BLOCK;
+    prm.columns = (prm.period + turns - 1) / turns;
+    return vector;
+}
+
+int64_t cl_rows(const tb::GnClParams& prm, int p, int vec) {
+    const int64_t chunks = prm.spatial[p] * prm.C / vec;
+    return (chunks + prm.period - 1) / prm.period;
+}
+
+// Statistics: every (patch, sample) is a unit, cut into up to TB_GN_PARTS records
+// of a cluster of up to 8 CTAs each; where that leaves SMs idle, the channels are
+// split too, into runs of whole groups of at least 256 bytes a position.
+void cl_plan_stats(tb::GnClParams& prm, tb_dtype dtype, bool vector, int ctas_wanted, int64_t* ctas) {
+    const int es = elem_bytes(dtype), vec = vector ? 16 / es : 1;
+    bool whole = prm.C % vec == 0;
+    for (int p = 0; p < prm.P; ++p) whole = whole && (vec == 1 || aligned(prm.patches[p], 16));
+    const int64_t units = prm.N * prm.P;
+    int splits = 1;
+    while (units * splits * TB_GN_PARTS * 8 < ctas_wanted && whole && prm.G % (splits * 2) == 0 &&
+           (prm.C / (splits * 2)) % vec == 0 && prm.C / (splits * 2) * es >= 256)
+        splits *= 2;
+    prm.splits = splits;
+    const int width = prm.period / splits, turns = (width + tb::CL_BLOCK - 1) / tb::CL_BLOCK;
+    prm.columns = (width + turns - 1) / turns;
+    int64_t most = 1;
+    for (int p = 0; p < prm.P; ++p) most = std::max(most, cl_rows(prm, p, vec));
+    // at least four turns of a CTA's threads each
+    const int64_t side = std::max(1, tb::CL_BLOCK / prm.columns);
+    const int64_t useful = std::max<int64_t>(1, most / (side * 4));
+    const int64_t each = std::min(useful, std::max<int64_t>(1, ctas_wanted / (units * splits)));
+    const int64_t parts = std::min<int64_t>(TB_GN_PARTS, each);
+    prm.cluster = (int32_t)std::max<int64_t>(1, std::min<int64_t>(8, each / parts));
+    int64_t at = 0;
+    for (int p = 0; p < prm.P; ++p) {
+        const int64_t share = (cl_rows(prm, p, vec) * parts + most / 2) / most;
+        prm.parts[p] = (int32_t)std::min<int64_t>(TB_GN_PARTS, std::max<int64_t>(1, share));
+        prm.start[p] = (int32_t)at;
+        at += prm.N * prm.parts[p];
+    }
+    prm.start[prm.P] = (int32_t)at;
+    *ctas = at * prm.cluster;
+}
+
+// Element-wise passes: runs of rows of about the same length, as many as are
+// resident at once.
+void cl_plan_rows(tb::GnClParams& prm, tb_dtype dtype, bool vector, int ctas_wanted, int64_t* ctas) {
+    const int vec = vector ? 16 / elem_bytes(dtype) : 1;
+    const int64_t slabs = (prm.period + prm.columns - 1) / prm.columns;
+    const int64_t wanted = std::max<int64_t>(1, ctas_wanted / slabs);
+    const int64_t side = std::max(1, tb::CL_BLOCK / prm.columns);
+    int64_t rows[tb::GN_MAXP], total = 0;
+    for (int p = 0; p < prm.P; ++p) {
+        rows[p] = cl_rows(prm, p, vec);
+        total += prm.N * rows[p];
+    }
+    int64_t run = std::max<int64_t>(side, (total + wanted - 1) / wanted);
+    for (;;) {
+        int64_t at = 0;
+        bool single = true;
+        for (int p = 0; p < prm.P; ++p) {
+            prm.parts[p] = (int32_t)std::max<int64_t>(1, (rows[p] + run - 1) / run);
+            single = single && prm.parts[p] == 1;
+            prm.start[p] = (int32_t)at;
+            at += prm.N * prm.parts[p];
+        }
+        prm.start[prm.P] = (int32_t)at;
+        *ctas = at;
+        if (at <= wanted || single) return;
+        run += std::max<int64_t>(1, run / 64);
+    }
+}
+
+tb_status cl_stats(tb::GnClParams& prm, tb_dtype dtype, int sms, cudaStream_t s) {
+    const bool vector = cl_chunks(prm, dtype, false, false);
+    int64_t ctas = 0;
+    cl_plan_stats(prm, dtype, vector, 2 * sms, &ctas);
+    return launched(tb::launch_gncl_stats(prm, (int)dtype, vector, ctas, s));
+}
+
+tb_status cl_apply(tb::GnClParams& prm, tb_dtype dtype, int sms, cudaStream_t s) {
+    const bool vector = cl_chunks(prm, dtype, false, true);
+    int64_t ctas = 0;
+    cl_plan_rows(prm, dtype, vector, 3 * sms, &ctas);
+    return launched(tb::launch_gncl_apply(prm, (int)dtype, vector, ctas, s));
+}
+
+tb_status cl_grad_stats(tb::GnClParams& prm, tb_dtype dtype, int sms, cudaStream_t s) {
+    const bool vector = cl_chunks(prm, dtype, true, false);
+    int64_t ctas = 0;
+    cl_plan_stats(prm, dtype, vector, 2 * sms, &ctas);
+    return launched(tb::launch_gncl_grad_stats(prm, (int)dtype, vector, ctas, s));
+}
+
+tb_status cl_grad_apply(tb::GnClParams& prm, tb_dtype dtype, int sms, cudaStream_t s) {
+    TB_TRY(launched(tb::launch_gncl_coefs(prm, (int)dtype, s)));
+    if (prm.N == 0) return TB_OK;
+    const bool vector = cl_chunks(prm, dtype, true, true);
+    int64_t ctas = 0;
+    cl_plan_rows(prm, dtype, vector, 2 * sms, &ctas);
+    return launched(tb::launch_gncl_grad_apply(prm, (int)dtype, vector, ctas, s));
+}
+
+tb_status cl_records(tb::GnClParams& prm, const tb_gn_grad_partial* grad_partials) {
+    if (grad_partials == nullptr && prm.N > 0 && prm.C > 0) return TB_ERR_NULL;
+    if (!aligned(grad_partials, 16)) return TB_ERR_UNSUPPORTED;
+    prm.grad_partials = reinterpret_cast<float2*>(const_cast<tb_gn_grad_partial*>(grad_partials));
+    return TB_OK;
+}
+
+tb_status cl_weights(tb::GnClParams& prm, tb_dtype dtype, void* dgamma, void* dbeta, void* workspace,
+                     int64_t workspace_bytes) {
+    const int es = elem_bytes(dtype);
+    if (!aligned(dgamma, es) || !aligned(dbeta, es) || !aligned(workspace, 16)) return TB_ERR_UNSUPPORTED;
+    if (prm.N > 0 && prm.C > 0) {
+        if (workspace == nullptr) return TB_ERR_NULL;
+        if (workspace_bytes < tb_patch_gn_workspace_cl(prm.N, prm.G)) return TB_ERR_SHAPE;
+    }
+    prm.dgamma = dgamma;
+    prm.dbeta = dbeta;
+    prm.coefs = reinterpret_cast<float4*>(workspace);
+    return TB_OK;
+}
+
+cudaStream_t as_stream(void* stream) { return reinterpret_cast<cudaStream_t>(stream); }
+
+}  // namespace
+
+TB_API tb_status tb_patch_gn_stats_cl(const void* const* patches, int32_t P, tb_dtype dtype, int64_t N, int64_t C,
+                                      const int64_t* spatial, int32_t G, tb_gn_partial* partials, void* stream) {
+    tb::GnClParams prm;
+    TB_TRY(cl_params(prm, {patches, nullptr, nullptr, P, dtype, N, C, spatial, G, partials, 1, nullptr, nullptr, 0.f, 0},
+                     false, false));
+    if (N == 0 || C == 0) return TB_OK;
+    int sms = 0;
+    TB_TRY(tb::sm_count(&sms));
+    return cl_stats(prm, dtype, sms, as_stream(stream));
+}
+
+TB_API tb_status tb_patch_gn_apply_cl(const void* const* patches, void* const* outs, int32_t P, tb_dtype dtype,
+                                      int64_t N, int64_t C, const int64_t* spatial, int32_t G,
+                                      const tb_gn_partial* partials, int32_t R, const void* gamma, const void* beta,
+                                      float eps, int32_t silu, void* stream) {
+    tb::GnClParams prm;
+    TB_TRY(cl_params(prm, {patches, nullptr, outs, P, dtype, N, C, spatial, G, partials, R, gamma, beta, eps, silu},
+                     false, true));
+    if (N == 0 || C == 0) return TB_OK;
+    int sms = 0;
+    TB_TRY(tb::sm_count(&sms));
+    return cl_apply(prm, dtype, sms, as_stream(stream));
+}
+
+TB_API tb_status tb_patch_group_norm_cl(const void* const* patches, void* const* outs, int32_t P, tb_dtype dtype,
+                                        int64_t N, int64_t C, const int64_t* spatial, int32_t G,
+                                        tb_gn_partial* partials, const void* gamma, const void* beta, float eps,
+                                        int32_t silu, void* stream) {
+    tb::GnClParams prm;
+    TB_TRY(cl_params(prm, {patches, nullptr, outs, P, dtype, N, C, spatial, G, partials, P, gamma, beta, eps, silu},
+                     false, true));
+    if (N == 0 || C == 0) return TB_OK;
+    int sms = 0;
+    TB_TRY(tb::sm_count(&sms));
+    TB_TRY(cl_stats(prm, dtype, sms, as_stream(stream)));
+    return cl_apply(prm, dtype, sms, as_stream(stream));
+}
+
+TB_API int64_t tb_patch_gn_workspace_cl(int64_t N, int32_t G) {
+    if (N < 0 || G < 1 || G > tb::CL_MAXC || N > (int64_t)1 << 31) return -1;
+    return 16 * N * G;
+}
+
+TB_API tb_status tb_patch_gn_grad_stats_cl(const void* const* patches, const void* const* grads, int32_t P,
+                                           tb_dtype dtype, int64_t N, int64_t C, const int64_t* spatial, int32_t G,
+                                           const tb_gn_partial* partials, int32_t R, const void* gamma,
+                                           const void* beta, float eps, int32_t silu,
+                                           tb_gn_grad_partial* grad_partials, void* stream) {
+    tb::GnClParams prm;
+    TB_TRY(cl_params(prm, {patches, grads, nullptr, P, dtype, N, C, spatial, G, partials, R, gamma, beta, eps, silu},
+                     true, false));
+    TB_TRY(cl_records(prm, grad_partials));
+    if (N == 0 || C == 0) return TB_OK;
+    int sms = 0;
+    TB_TRY(tb::sm_count(&sms));
+    return cl_grad_stats(prm, dtype, sms, as_stream(stream));
+}
+
+TB_API tb_status tb_patch_gn_grad_apply_cl(const void* const* patches, const void* const* grads, void* const* outs,
+                                           int32_t P, tb_dtype dtype, int64_t N, int64_t C, const int64_t* spatial,
+                                           int32_t G, const tb_gn_partial* partials,
+                                           const tb_gn_grad_partial* grad_partials, int32_t R, const void* gamma,
+                                           const void* beta, float eps, int32_t silu, void* dgamma, void* dbeta,
+                                           void* workspace, int64_t workspace_bytes, void* stream) {
+    tb::GnClParams prm;
+    TB_TRY(cl_params(prm, {patches, grads, outs, P, dtype, N, C, spatial, G, partials, R, gamma, beta, eps, silu}, true,
+                     true));
+    TB_TRY(cl_records(prm, grad_partials));
+    TB_TRY(cl_weights(prm, dtype, dgamma, dbeta, workspace, workspace_bytes));
+    if (C == 0 || (N == 0 && dgamma == nullptr && dbeta == nullptr)) return TB_OK;
+    int sms = 0;
+    TB_TRY(tb::sm_count(&sms));
+    return cl_grad_apply(prm, dtype, sms, as_stream(stream));
+}
+
+TB_API tb_status tb_patch_group_norm_backward_cl(const void* const* patches, const void* const* grads,
+                                                 void* const* outs, int32_t P, tb_dtype dtype, int64_t N, int64_t C,
+                                                 const int64_t* spatial, int32_t G, const tb_gn_partial* partials,
+                                                 tb_gn_grad_partial* grad_partials, const void* gamma,
+                                                 const void* beta, float eps, int32_t silu, void* dgamma, void* dbeta,
+                                                 void* workspace, int64_t workspace_bytes, void* stream) {
+    tb::GnClParams prm;
+    TB_TRY(cl_params(prm, {patches, grads, outs, P, dtype, N, C, spatial, G, partials, P, gamma, beta, eps, silu}, true,
+                     true));
+    TB_TRY(cl_records(prm, grad_partials));
+    TB_TRY(cl_weights(prm, dtype, dgamma, dbeta, workspace, workspace_bytes));
+    if (C == 0 || (N == 0 && dgamma == nullptr && dbeta == nullptr)) return TB_OK;
+    int sms = 0;
+    TB_TRY(tb::sm_count(&sms));
+    if (N > 0) TB_TRY(cl_grad_stats(prm, dtype, sms, as_stream(stream)));
+    return cl_grad_apply(prm, dtype, sms, as_stream(stream));
+}
+
+TB_API tb_status tb_dropout(const void* x, int64_t x_ld, const void* residual, int64_t residual_ld, tb_dtype dtype,
+                            int64_t rows, int64_t cols, double p, uint64_t seed, uint64_t offset,
+                            const uint64_t* state, void* y, int64_t y_ld, void* stream) {
+    if (!known(dtype)) return TB_ERR_DTYPE;
+    if (rows < 0 || cols < 0 || !(p >= 0.0 && p <= 1.0)) return TB_ERR_SHAPE;
+    if (rows == 0 || cols == 0) return TB_OK;
+    if ((double)rows * (double)cols > 1099511627776.0) return TB_ERR_UNSUPPORTED;
+    const int es = elem_bytes(dtype);
+    bool vector = true, dense = true;
+    const struct {
+        const void* at;
+        int64_t ld;
+        bool needed;
+    } tensors[3] = {{x, x_ld, true}, {y, y_ld, true}, {residual, residual_ld, residual != nullptr}};
+    for (const auto& t : tensors) {
+        if (!t.needed) continue;
+        if (t.at == nullptr) return TB_ERR_NULL;
+        if (rows > 1 && (t.ld < cols || (double)rows * (double)t.ld > 2.0e18)) return TB_ERR_SHAPE;
+        if (!aligned(t.at, es)) return TB_ERR_UNSUPPORTED;
+        if (!aligned(t.at, 16) || (rows > 1 && t.ld % (16 / es) != 0)) vector = false;
+        if (rows > 1 && t.ld != cols) dense = false;
+    }
+    if (!aligned(state, 8)) return TB_ERR_UNSUPPORTED;
+    tb::DropoutParams prm;
+    prm.x = x;
+    prm.residual = residual;
+    prm.y = y;
+    prm.state = state;
+    prm.rows = dense ? 1 : rows;
+    prm.cols = dense ? rows * cols : cols;
+    prm.x_ld = x_ld;
+    prm.r_ld = residual_ld;
+    prm.y_ld = y_ld;
+    if (prm.rows == 1) prm.x_ld = prm.r_ld = prm.y_ld = prm.cols;
+    prm.seed = seed;
+    prm.offset = offset;
+    prm.status = tb::checked_build_status();
+    prm.threshold = (uint32_t)std::floor(p * 65536.0 + 0.5);
+    prm.scale = prm.threshold < 65536u ? (float)(65536.0 / (65536 - prm.threshold)) : 0.f;
+    // dense rows of any width are one row: its base decides
+    if (dense) vector = aligned(x, 16) && aligned(y, 16) && aligned(residual, 16);
+    else vector = vector && cols % 8 == 0;
+    return launched(tb::launch_dropout(prm, (int)dtype, vector, as_stream(stream)));
+}

@@ -1,0 +1,429 @@
+// tb_gncl_bwd.cu -- the backward pass of channels-last PatchGroupNorm (+ SiLU).
+//
+// With d = x - mean, xhat = d * rstd, z = xhat * gamma + beta, s = 1 / (1 + e^-z):
+//     dz = silu ? dy * s * (1 + z * (1 - s)) : dy
+//     B(n, c) = sum dz,  A(n, c) = sum dz * xhat     (over the channel's elements)
+//     dgamma(c) = sum_n A,  dbeta(c) = sum_n B
+//     c1 = sum over the group's channels of gamma * B / count,  c2 the same of A
+//     dx = rnd(rstd * (gamma * dz - c1 - xhat * c2)) = rnd(a * dz + u * d + v),
+//          a = rstd * gamma, u = -rstd^2 c2, v = -rstd c1
+//
+// Three launches: the records (B, A) of every channel; (mean, rstd, u, v) of every
+// group and the weight gradients from the records; dx.  A CTA of the last would
+// otherwise read every channel's records (131 KB for 512 channels in 32 parts).
+#include "tb_gncl.cuh"
+
+namespace tb {
+namespace {
+
+// dz (see the top of this file).  e^-z and the reciprocal are approximate (2^-22
+// each); e^-z overflows for z < -88, where s = 0 and dz = 0.
+template <bool SILU>
+__device__ __forceinline__ f32x2 dz_of(f32x2 dy, f32x2 z) {
+    if constexpr (SILU) {
+        const f32x2 one = pair(1.f, 1.f);
+        float tl, th, al, ah;
+        halves(vmul(z, pair(-1.4426950408889634f, -1.4426950408889634f)), tl, th);
+        halves(vadd(pair(ex2_ftz(tl), ex2_ftz(th)), one), al, ah);
+        const f32x2 s = pair(rcp_ftz(al), rcp_ftz(ah));
+        return vmul(dy, vmul(s, vfma(z, vsub(one, s), one)));
+    } else {
+        return dy;
+    }
+}
+template <bool SILU>
+__device__ __forceinline__ float dz_of(float dy, float z) {
+    if constexpr (SILU) {
+        const float s = rcp_ftz(1.f + ex2_ftz(z * -1.4426950408889634f));
+        return dy * (s * fmaf(z, 1.f - s, 1.f));
+    } else {
+        return dy;
+    }
+}
+
+// --- the records ------------------------------------------------------------------
+
+constexpr int FOLD = 64;  // chunks between two foldings of a thread's sums
+constexpr int GU = 2;     // chunks of x and of dy a thread loads together
+
+template <int DT, int VEC, bool SILU>
+__global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_stats_kernel(const __grid_constant__ GnClParams p) {
+    using L = Lanes<VEC>;
+    using W = ClWord<DT, VEC>;
+    constexpr int ES = elem_size(DT), NL = L::N;
+    extern __shared__ uint4 shared4[];
+    const int C = (int)p.C, K = C / p.G;
+    const int cs = C / p.splits, c0 = (int)blockIdx.y * cs;  // this CTA's channels
+    float2* const stage = reinterpret_cast<float2*>(shared4);  // [CL_BLOCK * VEC]: (sum dz, sum dz * d)
+    float2* const table = stage + CL_BLOCK * VEC;              // [cs]: (sum dz, sum dz * xhat)
+    float2* const stats = table + cs;                          // groups of those channels: (mean, rstd)
+    const int g0 = c0 / K, g1 = (c0 + cs + K - 1) / K;
+    for (int c = threadIdx.x; c < cs; c += CL_BLOCK) table[c] = make_float2(0.f, 0.f);
+    const ClUnit u = cl_unit(p);
+    const int parts = p.parts[u.p], piece = u.part * p.cluster + u.rank, pieces = parts * p.cluster;
+    const ClRun run = cl_run<ES, VEC>(p.patches[u.p], p.spatial[u.p], p.C, u.n);
+    const char* const patch = static_cast<const char*>(p.patches[u.p]);
+    const char* const grad = static_cast<const char*>(p.grads[u.p]);
+    const int64_t bytes = p.N * run.elems * ES, from = (run.first + run.head) * ES;
+    int64_t a, b;
+    cl_piece((run.chunks + p.period - 1) / p.period, piece, pieces, a, b);
+    grid_wait();
+    cl_group_stats(p, u.n, g0, g1, stats);
+    __syncthreads();
+
+    const int split_width = p.period / p.splits, split0 = (int)blockIdx.y * split_width;
+    for (int j0 = split0; j0 < split0 + split_width; j0 += p.columns) {
+        const int j1 = min(j0 + p.columns, split0 + split_width);
+        const ClPlace q = cl_place(j0, j1);
+        const ClWalk w = cl_walk(q, a, b, p.period, run.chunks);
+        typename L::T mean[NL], ga[NL], be[NL], sb[NL], sa[NL], tb_[NL], ta[NL];
+        float f0[VEC], f1[VEC], f2[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int c = cl_channel(run.head, q.col * VEC + i, C);
+            const float2 s = q.row >= 0 ? stats[c / K - g0] : make_float2(0.f, 0.f);
+            f0[i] = s.x;
+            f1[i] = SILU && q.row >= 0 ? s.y * weight_at(p.gamma, DT, c, 1.f) : 0.f;
+            f2[i] = SILU && q.row >= 0 ? weight_at(p.beta, DT, c, 0.f) : 0.f;
+        }
+        cl_lanes<VEC>(f0, mean);
+        cl_lanes<VEC>(f1, ga);
+        cl_lanes<VEC>(f2, be);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) tb_[i] = ta[i] = L::splat(0.f);
+        const W* ax = reinterpret_cast<const W*>(patch + from) + w.at;
+        const W* ad = reinterpret_cast<const W*>(grad + from) + w.at;
+        for (int done = 0; done < w.count; done += FOLD) {
+            const int now = min(FOLD, w.count - done);
+#pragma unroll
+            for (int i = 0; i < NL; ++i) sb[i] = sa[i] = L::splat(0.f);
+            for (int s = 0; s < now; s += GU) {
+                W x[GU], y[GU];
+#pragma unroll
+                for (int r = 0; r < GU; ++r) {
+                    if (s + r < now && in_bounds(ax + r * w.stride, sizeof(W), patch, bytes, p.status) &&
+                        in_bounds(ad + r * w.stride, sizeof(W), grad, bytes, p.status)) {
+                        x[r] = __ldg(ax + r * w.stride);
+                        y[r] = __ldg(ad + r * w.stride);
+                    }
+                }
+                ax += GU * w.stride;
+                ad += GU * w.stride;
+#pragma unroll
+                for (int r = 0; r < GU; ++r) {
+                    if (s + r < now) {
+                        typename L::T f[NL], dy[NL];
+                        to_lanes<DT, VEC>(x[r], f);
+                        to_lanes<DT, VEC>(y[r], dy);
+#pragma unroll
+                        for (int i = 0; i < NL; ++i) {
+                            const typename L::T d = vsub(f[i], mean[i]);
+                            const typename L::T dz = dz_of<SILU>(dy[i], vfma(d, ga[i], be[i]));
+                            sb[i] = vadd(sb[i], dz);
+                            sa[i] = vfma(dz, d, sa[i]);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                tb_[i] = vadd(tb_[i], sb[i]);
+                ta[i] = vadd(ta[i], sa[i]);
+            }
+        }
+        cl_values<VEC>(tb_, f0);
+        cl_values<VEC>(ta, f1);
+        __syncthreads();  // the columns before these are merged
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) stage[threadIdx.x * VEC + i] = make_float2(f0[i], f1[i]);
+        __syncthreads();
+        const int lo = run.head + j0 * VEC, hi = run.head + j1 * VEC, pitch = q.width * VEC;
+        for (int i = threadIdx.x; i < cs; i += CL_BLOCK) {
+            const int c = c0 + i;
+            float2 t = table[i];
+            const float rstd = stats[c / K - g0].y;
+            for (int at = c + (lo > c ? (lo - c + C - 1) / C * C : 0); at < hi; at += C) {
+                for (int r = 0; r < q.rows; ++r) {
+                    const float2 v = stage[r * pitch + at - lo];
+                    t.x += v.x;
+                    t.y = fmaf(v.y, rstd, t.y);
+                }
+            }
+            table[i] = t;
+        }
+    }
+    // elements outside the whole chunks: the first piece's before, the last one's after; a lane each
+    __syncthreads();
+    if (VEC > 1 && threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        const int h = piece == 0 ? run.head : 0, t = piece == pieces - 1 ? run.tail : 0;
+        float dz = 0.f, xhat = 0.f;
+        int c = -1;
+        if (lane < h + t) {
+            const int64_t e = lane < h ? lane : run.elems - run.tail + (lane - h);
+            if (in_bounds(patch + (run.first + e) * ES, ES, patch, bytes, p.status)) {
+                c = (int)(e % C);
+                if (c >= c0 && c < c0 + cs) {
+                    const float2 s = stats[c / K - g0];
+                    xhat = (cl_elem<DT>(patch, run.first + e) - s.x) * s.y;
+                    dz = dz_of<SILU>(cl_elem<DT>(grad, run.first + e),
+                                     fmaf(xhat, weight_at(p.gamma, DT, c, 1.f), weight_at(p.beta, DT, c, 0.f)));
+                } else {
+                    c = -1;
+                }
+            }
+        }
+        for (unsigned left = __ballot_sync(0xffffffffu, c >= 0); left; left &= left - 1) {
+            const int k = __ffs(left) - 1;
+            const int ck = __shfl_sync(0xffffffffu, c, k);
+            const float zk = __shfl_sync(0xffffffffu, dz, k), hk = __shfl_sync(0xffffffffu, xhat, k);
+            if (lane == 0) {
+                table[ck - c0].x += zk;
+                table[ck - c0].y = fmaf(zk, hk, table[ck - c0].y);
+            }
+        }
+        __syncwarp();
+    }
+    if (p.cluster > 1) cluster_sync();
+    else __syncthreads();
+    float2* const out = p.grad_partials + ((int64_t)u.p * p.N + u.n) * C * TB_GN_PARTS;
+    for (int i = u.rank * CL_BLOCK + (int)threadIdx.x; i < cs; i += p.cluster * CL_BLOCK) {
+        float2 t = make_float2(0.f, 0.f);
+        for (int r = 0; r < p.cluster; ++r) {
+            if (r == u.rank) {
+                t.x += table[i].x;
+                t.y += table[i].y;
+            } else {
+                const uint2 v = cluster_load8(smem_addr(table + i), (uint32_t)r);
+                t.x += __uint_as_float(v.x);
+                t.y += __uint_as_float(v.y);
+            }
+        }
+        float2* const at = out + (int64_t)(c0 + i) * TB_GN_PARTS;
+        if (!in_bounds(at, TB_GN_PARTS * sizeof(float2), p.grad_partials,
+                       (int64_t)p.P * p.N * C * TB_GN_PARTS * (int64_t)sizeof(float2), p.status))
+            continue;
+        at[u.part] = t;
+        if (u.part == 0)
+            for (int r = parts; r < TB_GN_PARTS; ++r) at[r] = make_float2(0.f, 0.f);
+    }
+    if (p.cluster > 1) cluster_sync();  // nobody leaves while its table may be read
+}
+
+size_t grad_stats_smem(int vec, int64_t C, int G, int splits) {
+    const int64_t cs = C / splits, K = C / G;
+    return (size_t)(CL_BLOCK * vec + cs + (cs + K - 1) / K + 1) * sizeof(float2);
+}
+
+// --- the groups' constants and the weight gradients -----------------------------------
+
+// CTAs 0 .. N * G - 1: one group of one sample; the rest: COEF_CHANNELS channels'
+// weight gradients each.
+constexpr int COEF_CHANNELS = CL_BLOCK / TB_GN_PARTS;
+
+template <int DT>
+__global__ void __launch_bounds__(CL_BLOCK) gncl_coefs_kernel(const __grid_constant__ GnClParams p) {
+    __shared__ float2 sums[CL_BLOCK / 32];
+    __shared__ float2 stats[1];
+    const int C = (int)p.C, K = C / p.G;
+    const int64_t units = p.N * p.G, set = p.N * C * TB_GN_PARTS;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t size = (int64_t)p.R * set * (int64_t)sizeof(float2);
+    grid_wait();
+    if ((int64_t)blockIdx.x < units) {
+        const int64_t n = blockIdx.x / p.G;
+        const int g = (int)(blockIdx.x - n * p.G);
+        const int per_set = K * TB_GN_PARTS;
+        float B = 0.f, A = 0.f;
+        for (int r = 0; r < p.R; ++r) {
+            const float2* const first = p.grad_partials + r * set + (n * C + (int64_t)g * K) * TB_GN_PARTS;
+#pragma unroll 4
+            for (int i = threadIdx.x; i < per_set; i += CL_BLOCK) {
+                if (!in_bounds(first + i, sizeof(float2), p.grad_partials, size, p.status)) continue;
+                const float2 v = __ldg(first + i);
+                const float w = weight_at(p.gamma, DT, g * K + i / TB_GN_PARTS, 1.f);
+                B = fmaf(w, v.x, B);
+                A = fmaf(w, v.y, A);
+            }
+        }
+        B = warp_sum(B);
+        A = warp_sum(A);
+        if (lane == 0) sums[warp] = make_float2(B, A);
+        // the count: of the forward pass's records
+        long long count = 0;
+        if (warp == 0) {
+            for (int q = lane; q < p.R * TB_GN_PARTS; q += 32)
+                count += p.partials[(((int64_t)(q / TB_GN_PARTS) * p.N + n) * p.G + g) * TB_GN_PARTS + q % TB_GN_PARTS].n;
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) count += __shfl_xor_sync(0xffffffffu, count, d);
+        }
+        cl_group_stats(p, n, g, g + 1, stats);
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            B = A = 0.f;
+            for (int k = 0; k < CL_BLOCK / 32; ++k) {
+                B += sums[k].x;
+                A += sums[k].y;
+            }
+            const float inv = count > 0 ? 1.f / (float)count : 0.f, rstd = stats[0].y;
+            p.coefs[blockIdx.x] = make_float4(stats[0].x, rstd, -(rstd * rstd) * (A * inv), -rstd * (B * inv));
+        }
+        return;
+    }
+    // a channel per eight lanes, a lane per part
+    const int64_t c = ((int64_t)blockIdx.x - units) * COEF_CHANNELS + threadIdx.x / TB_GN_PARTS;
+    float B = 0.f, A = 0.f;
+    if (c < C) {
+        for (int64_t r = 0; r < p.R * p.N; ++r) {
+            const float2* const at = p.grad_partials + (r * C + c) * TB_GN_PARTS + threadIdx.x % TB_GN_PARTS;
+            if (!in_bounds(at, sizeof(float2), p.grad_partials, size, p.status)) continue;
+            const float2 v = __ldg(at);
+            B += v.x;
+            A += v.y;
+        }
+    }
+#pragma unroll
+    for (int d = TB_GN_PARTS / 2; d >= 1; d >>= 1) {
+        B += __shfl_xor_sync(0xffffffffu, B, d);
+        A += __shfl_xor_sync(0xffffffffu, A, d);
+    }
+    if (c < C && threadIdx.x % TB_GN_PARTS == 0) {
+        if (p.dgamma != nullptr) store_weight(p.dgamma, DT, c, A);
+        if (p.dbeta != nullptr) store_weight(p.dbeta, DT, c, B);
+    }
+}
+
+// --- dx -----------------------------------------------------------------------------
+
+template <int DT, int VEC, bool SILU>
+__global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_apply_kernel(const __grid_constant__ GnClParams p) {
+    using L = Lanes<VEC>;
+    using W = ClWord<DT, VEC>;
+    constexpr int ES = elem_size(DT), NL = L::N;
+    const int C = (int)p.C, K = C / p.G;
+    int pt = 0;
+    while (pt + 1 < p.P && (int)blockIdx.x >= p.start[pt + 1]) ++pt;
+    const int local = (int)blockIdx.x - p.start[pt], n = local / p.parts[pt], piece = local - n * p.parts[pt];
+    const ClRun run = cl_run<ES, VEC>(p.patches[pt], p.spatial[pt], p.C, n);
+    const char* const patch = static_cast<const char*>(p.patches[pt]);
+    const char* const grad = static_cast<const char*>(p.grads[pt]);
+    char* const out = static_cast<char*>(p.outs[pt]);
+    const int64_t bytes = p.N * run.elems * ES, from = (run.first + run.head) * ES;
+    const int j0 = (int)blockIdx.y * p.columns, j1 = min(j0 + p.columns, p.period);
+    const ClPlace q = cl_place(j0, j1);
+    int64_t a, b;
+    cl_piece((run.chunks + p.period - 1) / p.period, piece, p.parts[pt], a, b);
+    const ClWalk w = cl_walk(q, a, b, p.period, run.chunks);
+    const float4* const coefs = p.coefs + (int64_t)n * p.G;
+    grid_wait();
+    typename L::T mean[NL], ga[NL], be[NL], cu[NL], cv[NL];
+    {
+        float f0[VEC], f1[VEC], f2[VEC], f3[VEC], f4[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int c = cl_channel(run.head, q.col * VEC + i, C);
+            const float4 k = __ldg(coefs + c / K);
+            f0[i] = k.x;
+            f1[i] = k.y * weight_at(p.gamma, DT, c, 1.f);
+            f2[i] = weight_at(p.beta, DT, c, 0.f);
+            f3[i] = k.z;
+            f4[i] = k.w;
+        }
+        cl_lanes<VEC>(f0, mean);
+        cl_lanes<VEC>(f1, ga);
+        cl_lanes<VEC>(f2, be);
+        cl_lanes<VEC>(f3, cu);
+        cl_lanes<VEC>(f4, cv);
+    }
+    // from the end of the run: the records' pass left that in L2
+    const W* const bx = reinterpret_cast<const W*>(patch + from) + w.at;
+    const W* const bd = reinterpret_cast<const W*>(grad + from) + w.at;
+    W* const to = reinterpret_cast<W*>(out + from) + w.at;
+    for (int s = w.count - 1; s >= 0; s -= GU) {
+        W x[GU], y[GU];
+#pragma unroll
+        for (int r = 0; r < GU; ++r) {
+            if (s - r >= 0 && in_bounds(bx + (s - r) * w.stride, sizeof(W), patch, bytes, p.status) &&
+                in_bounds(bd + (s - r) * w.stride, sizeof(W), grad, bytes, p.status)) {
+                x[r] = __ldcs(bx + (s - r) * w.stride);
+                y[r] = __ldcs(bd + (s - r) * w.stride);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < GU; ++r) {
+            if (s - r >= 0) {
+                typename L::T f[NL], dy[NL];
+                to_lanes<DT, VEC>(x[r], f);
+                to_lanes<DT, VEC>(y[r], dy);
+#pragma unroll
+                for (int i = 0; i < NL; ++i) {
+                    const typename L::T d = vsub(f[i], mean[i]);
+                    const typename L::T dz = dz_of<SILU>(dy[i], vfma(d, ga[i], be[i]));
+                    f[i] = vfma(dz, ga[i], vfma(d, cu[i], cv[i]));
+                }
+                if (in_bounds(to + (s - r) * w.stride, sizeof(W), out, bytes, p.status))
+                    __stcs(to + (s - r) * w.stride, from_lanes<DT, VEC>(f));
+            }
+        }
+    }
+    if (VEC > 1 && blockIdx.y == 0) {
+        const int h = piece == 0 ? run.head : 0, t = piece == p.parts[pt] - 1 ? run.tail : 0;
+        if ((int)threadIdx.x < h + t) {
+            const int64_t e = (int)threadIdx.x < h ? threadIdx.x : run.elems - run.tail + (threadIdx.x - h);
+            const int c = (int)(e % C);
+            const float4 k = __ldg(coefs + c / K);
+            const float gam = k.y * weight_at(p.gamma, DT, c, 1.f);
+            if (in_bounds(patch + (run.first + e) * ES, ES, patch, bytes, p.status)) {
+                const float d = cl_elem<DT>(patch, run.first + e) - k.x;
+                const float dz = dz_of<SILU>(cl_elem<DT>(grad, run.first + e),
+                                             fmaf(d, gam, weight_at(p.beta, DT, c, 0.f)));
+                cl_store_elem<DT>(out, run.first + e, fmaf(dz, gam, fmaf(d, k.z, k.w)));
+            }
+        }
+    }
+}
+
+template <int DT>
+cudaError_t stats_launch(const GnClParams& p, bool vector, int64_t ctas, cudaStream_t s) {
+    constexpr int V = 16 / elem_size(DT);
+    void (*const fn)(const GnClParams) =
+        vector ? (p.silu ? gncl_grad_stats_kernel<DT, V, true> : gncl_grad_stats_kernel<DT, V, false>)
+               : (p.silu ? gncl_grad_stats_kernel<DT, 1, true> : gncl_grad_stats_kernel<DT, 1, false>);
+    return launch_cluster(fn, p, dim3((unsigned)ctas, (unsigned)p.splits, 1), p.cluster,
+                          grad_stats_smem(vector ? V : 1, p.C, p.G, p.splits), s);
+}
+
+template <int DT>
+cudaError_t apply_launch(const GnClParams& p, bool vector, int64_t ctas, cudaStream_t s) {
+    constexpr int V = 16 / elem_size(DT);
+    void (*const fn)(const GnClParams) =
+        vector ? (p.silu ? gncl_grad_apply_kernel<DT, V, true> : gncl_grad_apply_kernel<DT, V, false>)
+               : (p.silu ? gncl_grad_apply_kernel<DT, 1, true> : gncl_grad_apply_kernel<DT, 1, false>);
+    const unsigned slabs = (unsigned)((p.period + p.columns - 1) / p.columns);
+    return launch_cluster(fn, p, dim3((unsigned)ctas, slabs, 1), 1, 0, s);
+}
+
+}  // namespace
+
+cudaError_t launch_gncl_grad_stats(const GnClParams& p, int dtype, bool vector, int64_t ctas, cudaStream_t s) {
+    if (dtype == F32) return stats_launch<F32>(p, vector, ctas, s);
+    if (dtype == F16) return stats_launch<F16>(p, vector, ctas, s);
+    return stats_launch<BF16>(p, vector, ctas, s);
+}
+
+cudaError_t launch_gncl_coefs(const GnClParams& p, int dtype, cudaStream_t s) {
+    const int64_t weights = p.dgamma != nullptr || p.dbeta != nullptr ? (p.C + COEF_CHANNELS - 1) / COEF_CHANNELS : 0;
+    const dim3 grid((unsigned)(p.N * p.G + weights), 1, 1);
+    void (*const fn)(const GnClParams) = dtype == F32 ? gncl_coefs_kernel<F32>
+                                         : dtype == F16 ? gncl_coefs_kernel<F16>
+                                                        : gncl_coefs_kernel<BF16>;
+    return launch_cluster(fn, p, grid, 1, 0, s);
+}
+
+cudaError_t launch_gncl_grad_apply(const GnClParams& p, int dtype, bool vector, int64_t ctas, cudaStream_t s) {
+    if (dtype == F32) return apply_launch<F32>(p, vector, ctas, s);
+    if (dtype == F16) return apply_launch<F16>(p, vector, ctas, s);
+    return apply_launch<BF16>(p, vector, ctas, s);
+}
+
+}  // namespace tb

@@ -468,6 +468,71 @@ constexpr int GRAD_CHANNELS = 16;        // channels of one weight-gradient task
 cudaError_t launch_gn_grad(const GnGradParams& p, int dtype, bool ring, int sms, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
+// PatchGroupNorm, channels last
+// ---------------------------------------------------------------------------
+
+constexpr int CL_BLOCK = 256;          // threads per CTA
+constexpr int CL_MAXC = TB_GN_CL_MAX_CHANNELS;
+
+// Chunks, columns, rows and periods: see tb_gncl.cuh.
+struct GnClParams {
+    const void* patches[GN_MAXP];  // x
+    const void* grads[GN_MAXP];    // dy (backward)
+    void* outs[GN_MAXP];           // y, or dx
+    int64_t spatial[GN_MAXP];
+    GnPartial* partials;           // [P or R][N][G][TB_GN_PARTS]
+    float2* grad_partials;         // (sum dz, sum dz * xhat): [P or R][N][C][TB_GN_PARTS]
+    float4* coefs;                 // (mean, rstd, u, v): [N][G], see GnClGradApply
+    const void* gamma;             // [C] or null
+    const void* beta;              // [C] or null
+    void* dgamma;                  // [C] or null
+    void* dbeta;                   // [C] or null
+    int64_t N, C;
+    int32_t P, G;
+    int32_t R;                     // record sets
+    float eps;
+    int32_t silu;
+    int32_t period;                // chunks after which the channels repeat
+    int32_t columns;               // of the period, one CTA takes at a time
+    int32_t splits;                // statistics: grid.y; whole groups of whole chunks each
+    int32_t cluster;               // statistics: CTAs whose sums make one record
+    int32_t parts[GN_MAXP];        // statistics: records of each unit of patch p; else CTAs of each sample
+    int32_t start[GN_MAXP + 1];    // first cluster (statistics) or CTA of patch p
+    uint32_t* status;              // bounds-checked build: device status word (else null)
+};
+static_assert(sizeof(GnClParams) <= 32000, "kernel parameter block too large");
+
+// vector: 16-byte chunks (every tensor of a patch has the same offset from
+// 16-byte boundaries); otherwise single elements.  ctas: along grid.x.
+cudaError_t launch_gncl_stats(const GnClParams& p, int dtype, bool vector, int64_t ctas, cudaStream_t s);
+cudaError_t launch_gncl_apply(const GnClParams& p, int dtype, bool vector, int64_t ctas, cudaStream_t s);
+cudaError_t launch_gncl_grad_stats(const GnClParams& p, int dtype, bool vector, int64_t ctas, cudaStream_t s);
+cudaError_t launch_gncl_coefs(const GnClParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_gncl_grad_apply(const GnClParams& p, int dtype, bool vector, int64_t ctas, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// Dropout
+// ---------------------------------------------------------------------------
+
+// Row strides (*_ld) are in elements; rows that follow each other densely in all
+// tensors are passed as one row.
+struct DropoutParams {
+    const void* x;
+    const void* residual;     // or null
+    void* y;
+    const uint64_t* state;    // device (seed, offset) added to the ones below, or null
+    int64_t rows, cols;
+    int64_t x_ld, r_ld, y_ld;
+    uint64_t seed, offset;
+    uint32_t* status;         // bounds-checked build: device status word (else null)
+    uint32_t threshold;       // dropped: 16 random bits below it; 0 .. 65536
+    float scale;              // of what is kept
+};
+
+// vector: whole 16-byte chunks, all rows on 16-byte boundaries.
+cudaError_t launch_dropout(const DropoutParams& p, int dtype, bool vector, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
 // Layer norm
 // ---------------------------------------------------------------------------
 

@@ -6,22 +6,14 @@
 #include <cstdint>
 #include <cstring>
 
-#include "tb_internal.h"
-#include "tileblend.h"
-
-#define TB_API extern "C" __attribute__((visibility("default")))
+#include "tb_args.h"
 
 namespace {
 
-tb_status launched(cudaError_t e) {
-    if (e == cudaSuccess) return TB_OK;
-    tb::record_cuda_error(e);
-    return TB_ERR_CUDA;
-}
-
-bool known(tb_dtype d) { return d == TB_F32 || d == TB_F16 || d == TB_BF16; }
-int elem_bytes(tb_dtype d) { return d == TB_F32 ? 4 : 2; }
-bool aligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
+using tb::aligned;
+using tb::elem_bytes;
+using tb::known;
+using tb::launched;
 
 // ---------------------------------------------------------------------------
 // layer norm
@@ -52,12 +44,6 @@ tb_status ln_weight(const void* p, tb_dtype wdtype, bool* vector) {
     if (!aligned(p, 16)) *vector = false;
     return TB_OK;
 }
-
-#define TB_TRY(call)                          \
-    do {                                      \
-        const tb_status try_status = (call);  \
-        if (try_status != TB_OK) return try_status; \
-    } while (0)
 
 // ---------------------------------------------------------------------------
 // gradients

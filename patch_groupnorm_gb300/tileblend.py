@@ -157,6 +157,26 @@ _lib.tb_patch_gn_grad_stats.argtypes = [_P_vp, _P_vp, _i32, ctypes.c_int, _i64, 
 _lib.tb_patch_gn_grad_apply.restype = ctypes.c_int
 _lib.tb_patch_gn_grad_apply.argtypes = [_P_vp, _P_vp, _P_vp, _i32, ctypes.c_int, _i64, _i64, _P_i64, _i32, _vp, _vp,
                                         _i32, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp]
+_lib.tb_patch_gn_stats_cl.restype = ctypes.c_int
+_lib.tb_patch_gn_stats_cl.argtypes = _lib.tb_patch_gn_stats.argtypes
+_lib.tb_patch_gn_apply_cl.restype = ctypes.c_int
+_lib.tb_patch_gn_apply_cl.argtypes = _lib.tb_patch_gn_apply_gathered.argtypes
+_lib.tb_patch_group_norm_cl.restype = ctypes.c_int
+_lib.tb_patch_group_norm_cl.argtypes = _lib.tb_patch_gn_apply.argtypes
+_lib.tb_patch_gn_workspace_cl.restype = _i64
+_lib.tb_patch_gn_workspace_cl.argtypes = [_i64, _i32]
+_lib.tb_patch_gn_grad_stats_cl.restype = ctypes.c_int
+_lib.tb_patch_gn_grad_stats_cl.argtypes = _lib.tb_patch_gn_grad_stats.argtypes
+_lib.tb_patch_gn_grad_apply_cl.restype = ctypes.c_int
+_lib.tb_patch_gn_grad_apply_cl.argtypes = [_P_vp, _P_vp, _P_vp, _i32, ctypes.c_int, _i64, _i64, _P_i64, _i32, _vp, _vp,
+                                           _i32, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp, _i64, _vp]
+_lib.tb_patch_group_norm_backward_cl.restype = ctypes.c_int
+_lib.tb_patch_group_norm_backward_cl.argtypes = [_P_vp, _P_vp, _P_vp, _i32, ctypes.c_int, _i64, _i64, _P_i64, _i32,
+                                                 _vp, _vp, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp, _i64, _vp]
+_lib.tb_dropout.restype = ctypes.c_int
+_lib.tb_dropout.argtypes = [_vp, _i64, _vp, _i64, ctypes.c_int, _i64, _i64, ctypes.c_double, ctypes.c_uint64,
+                            ctypes.c_uint64, _vp, _vp, _i64, _vp]
+TB_GN_CL_MAX_CHANNELS = 8192
 TB_LN_PARTS = 512
 TB_MAX_GRADS, TB_GRAD_TABLE, TB_GRAD_PARTS = 65536, 1024, 1024
 
@@ -167,7 +187,9 @@ EXPORTED = ("tb_version", "tb_status_string", "tb_last_cuda_error", "tb_axis_lay
             "tb_gather_patches", "tb_device_status", "tb_ramp_axis_spread", "tb_stitch_shard_frames_layout",
             "tb_stitch_halo_pack_frames", "tb_stitch3d_shard_frames", "tb_layer_norm", "tb_layer_norm_workspace",
             "tb_layer_norm_backward", "tb_grad_records", "tb_grad_stats", "tb_grad_norm", "tb_grad_clip",
-            "tb_patch_gn_grad_stats", "tb_patch_gn_grad_apply")
+            "tb_patch_gn_grad_stats", "tb_patch_gn_grad_apply", "tb_patch_gn_stats_cl", "tb_patch_gn_apply_cl",
+            "tb_patch_group_norm_cl", "tb_patch_gn_workspace_cl", "tb_patch_gn_grad_stats_cl",
+            "tb_patch_gn_grad_apply_cl", "tb_patch_group_norm_backward_cl", "tb_dropout")
 
 
 class TileBlendError(RuntimeError):
@@ -1224,3 +1246,202 @@ def patch_group_norm_backward(grads: Sequence[torch.Tensor], patches: Sequence[t
     _check(_lib.tb_patch_gn_grad_apply(xs, ds, os_, P, dt, N, C, sp, G, rec, grec, P, ga, be, eps, act, gp, bp, handle),
            "tb_patch_gn_grad_apply")
     return dxs, dgamma, dbeta
+
+
+# ---------------------------------------------------------------------------
+# channels last: PatchGroupNorm forward and backward
+# ---------------------------------------------------------------------------
+
+def _cl_args(patches, G, gamma, beta):
+    """(N, C, dtype, device, positions, addresses) of channels-last patches [N, *spatial_p, C]."""
+    P = len(patches)
+    if not 1 <= P <= 64:
+        raise ValueError("1 to 64 patches")
+    first = patches[0]
+    dt, dev = first.dtype, first.get_device()
+    if first.dim() < 2:
+        raise ValueError("patches are [N, *spatial, C]")
+    N, C = first.shape[0], first.shape[-1]
+    spatial = []
+    for q, x in enumerate(patches):
+        if x.get_device() != dev or dev < 0 or not x.is_contiguous():
+            raise ValueError("patch %d must be a contiguous CUDA tensor, on the device of patch 0" % q)
+        if x.dtype is not dt or x.dim() < 2 or x.shape[0] != N or x.shape[-1] != C:
+            raise ValueError("patch %d: dtype, samples or channels differ from patch 0" % q)
+        spatial.append(x.numel() // (N * C) if N * C else 0)
+    return (N, C, _dtype_code(first), dev, _COUNTS[P](*spatial), _PTRS[P](*[x.data_ptr() for x in patches]),
+            _vec(gamma, C, dt, dev, "gamma"), _vec(beta, C, dt, dev, "beta"))
+
+
+def _cl_records(partials: torch.Tensor, R: int, N: int, G: int, device: int) -> int:
+    if partials.get_device() != device or not partials.is_contiguous() or \
+            partials.numel() * partials.element_size() != R * N * G * TB_GN_PARTS * 16:
+        raise ValueError("partials must hold R*N*G*TB_GN_PARTS 16-byte records on the patches' device")
+    return partials.data_ptr()
+
+
+def _cl_workspace(workspace: torch.Tensor, device: int) -> Tuple[int, int]:
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous, on the patches' device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def gn_workspace_cl(N: int, G: int, device=None) -> torch.Tensor:
+    """The device workspace of tb_patch_gn_grad_apply_cl for these sizes; it
+    may serve any number of calls in turn on one stream."""
+    n = int(_lib.tb_patch_gn_workspace_cl(N, G))
+    if n < 0:
+        raise ValueError("no group norm of %d samples in %d groups" % (N, G))
+    return torch.empty(n, dtype=torch.uint8, device=device or torch.device("cuda"))
+
+
+def tb_patch_gn_stats_cl(patches: Sequence[torch.Tensor], G: int, partials: torch.Tensor, stream=None) -> torch.Tensor:
+    """``tb_patch_gn_stats`` of channels-last patches [N, *spatial_p, C]: the
+    same records, in the same places."""
+    N, C, dt, dev, sp, xs, _, _ = _cl_args(patches, G, None, None)
+    P = len(patches)
+    _check(_lib.tb_patch_gn_stats_cl(xs, P, dt, N, C, sp, G, _cl_records(partials, P, N, G, dev),
+                                     _stream_of(stream, dev)), "tb_patch_gn_stats_cl")
+    return partials
+
+
+def tb_patch_gn_apply_cl(patches: Sequence[torch.Tensor], outs: Sequence[torch.Tensor], G: int, partials: torch.Tensor,
+                         R: int, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor], eps: float,
+                         silu: bool = True, stream=None) -> Sequence[torch.Tensor]:
+    """Normalise (+ SiLU) channels-last patches [N, *spatial_p, C] into
+    ``outs`` (``outs[p]`` may be ``patches[p]``) with the statistics pooled
+    over the ``R`` record sets in ``partials``."""
+    N, C, dt, dev, sp, xs, ga, be = _cl_args(patches, G, gamma, beta)
+    P = len(patches)
+    _check(_lib.tb_patch_gn_apply_cl(xs, _like_patches(outs, patches, "output"), P, dt, N, C, sp, G,
+                                     _cl_records(partials, R, N, G, dev), R, ga, be, eps, 1 if silu else 0,
+                                     _stream_of(stream, dev)), "tb_patch_gn_apply_cl")
+    return outs
+
+
+def patch_group_norm_cl(patches: Sequence[torch.Tensor], G: int, gamma: Optional[torch.Tensor],
+                        beta: Optional[torch.Tensor], eps: float, silu: bool = True,
+                        outs: Optional[Sequence[torch.Tensor]] = None, partials: Optional[torch.Tensor] = None,
+                        stream=None) -> Sequence[torch.Tensor]:
+    """Both steps for channels-last patches [N, *spatial_p, C]: GroupNorm (+
+    SiLU) of the whole tensor over its patches.  Outputs that are not given
+    are made."""
+    if outs is None or partials is None:
+        if len(patches) == 0:
+            raise ValueError("at least one patch")
+        outs, partials = _on_stream(lambda: (
+            [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in patches] if outs is None else outs,
+            new_partials(len(patches), patches[0].shape[0], G, patches[0].device) if partials is None else partials),
+            stream)
+    N, C, dt, dev, sp, xs, ga, be = _cl_args(patches, G, gamma, beta)
+    P = len(patches)
+    _check(_lib.tb_patch_group_norm_cl(xs, _like_patches(outs, patches, "output"), P, dt, N, C, sp, G,
+                                       _cl_records(partials, P, N, G, dev), ga, be, eps, 1 if silu else 0,
+                                       _stream_of(stream, dev)), "tb_patch_group_norm_cl")
+    return outs
+
+
+def tb_patch_gn_grad_stats_cl(grads: Sequence[torch.Tensor], patches: Sequence[torch.Tensor], G: int,
+                              partials: torch.Tensor, R: int, gamma: Optional[torch.Tensor],
+                              beta: Optional[torch.Tensor], eps: float, grad_partials: torch.Tensor,
+                              silu: bool = True, stream=None) -> torch.Tensor:
+    """``tb_patch_gn_grad_stats`` of channels-last patches and gradients: the
+    same records, in the same places."""
+    N, C, dt, dev, sp, xs, ga, be = _cl_args(patches, G, gamma, beta)
+    P = len(patches)
+    _check(_lib.tb_patch_gn_grad_stats_cl(xs, _like_patches(grads, patches, "gradient"), P, dt, N, C, sp, G,
+                                          _cl_records(partials, R, N, G, dev), R, ga, be, eps, 1 if silu else 0,
+                                          _grad_partials(grad_partials, P, N, C, dev), _stream_of(stream, dev)),
+           "tb_patch_gn_grad_stats_cl")
+    return grad_partials
+
+
+def tb_patch_gn_grad_apply_cl(grads: Sequence[torch.Tensor], patches: Sequence[torch.Tensor],
+                              dxs: Sequence[torch.Tensor], G: int, partials: torch.Tensor,
+                              grad_partials: torch.Tensor, R: int, gamma: Optional[torch.Tensor],
+                              beta: Optional[torch.Tensor], eps: float, workspace: torch.Tensor,
+                              dgamma: Optional[torch.Tensor] = None, dbeta: Optional[torch.Tensor] = None,
+                              silu: bool = True, stream=None) -> Sequence[torch.Tensor]:
+    """The gradients of channels-last patches into ``dxs`` (``dxs[p]`` may be
+    ``grads[p]`` or ``patches[p]``), and of the weights into ``dgamma`` /
+    ``dbeta``, from the ``R`` record sets of both passes.  ``workspace`` comes
+    from ``gn_workspace_cl``."""
+    N, C, dt, dev, sp, xs, ga, be = _cl_args(patches, G, gamma, beta)
+    P = len(patches)
+    os_, gp, bp = _gn_grad_outs(dxs, patches, C, dgamma, dbeta)
+    _check(_lib.tb_patch_gn_grad_apply_cl(xs, _like_patches(grads, patches, "gradient"), os_, P, dt, N, C, sp, G,
+                                          _cl_records(partials, R, N, G, dev),
+                                          _grad_partials(grad_partials, R, N, C, dev), R, ga, be, eps,
+                                          1 if silu else 0, gp, bp, *_cl_workspace(workspace, dev),
+                                          _stream_of(stream, dev)), "tb_patch_gn_grad_apply_cl")
+    return dxs
+
+
+def patch_group_norm_backward_cl(grads: Sequence[torch.Tensor], patches: Sequence[torch.Tensor], G: int,
+                                 partials: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor],
+                                 eps: float, silu: bool = True, dxs: Optional[Sequence[torch.Tensor]] = None,
+                                 dgamma: Optional[torch.Tensor] = None, dbeta: Optional[torch.Tensor] = None,
+                                 grad_partials: Optional[torch.Tensor] = None,
+                                 workspace: Optional[torch.Tensor] = None, stream=None):
+    """Both steps of the backward pass of ``patch_group_norm_cl``: ``(dxs,
+    dgamma, dbeta)``.  ``partials`` are the forward pass's records of these
+    patches; outputs and workspaces that are not given are made."""
+    P = len(patches)
+    if dxs is None or dgamma is None or dbeta is None or grad_partials is None or workspace is None:
+        if P == 0 or patches[0].dim() < 2:
+            raise ValueError("at least one patch, [N, *spatial, C]")
+        N, C, dt, dev = patches[0].shape[0], patches[0].shape[-1], patches[0].dtype, patches[0].device
+
+        def make():
+            return ([torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in patches] if dxs is None else dxs,
+                    torch.empty(C, dtype=dt, device=dev) if dgamma is None else dgamma,
+                    torch.empty(C, dtype=dt, device=dev) if dbeta is None else dbeta,
+                    new_grad_partials(P, N, C, dev) if grad_partials is None else grad_partials,
+                    gn_workspace_cl(N, G, dev) if workspace is None else workspace)
+        dxs, dgamma, dbeta, grad_partials, workspace = _on_stream(make, stream)
+    N, C, dt, dev, sp, xs, ga, be = _cl_args(patches, G, gamma, beta)
+    os_, gp, bp = _gn_grad_outs(dxs, patches, C, dgamma, dbeta)
+    _check(_lib.tb_patch_group_norm_backward_cl(xs, _like_patches(grads, patches, "gradient"), os_, P, dt, N, C, sp, G,
+                                                _cl_records(partials, P, N, G, dev),
+                                                _grad_partials(grad_partials, P, N, C, dev), ga, be, eps,
+                                                1 if silu else 0, gp, bp, *_cl_workspace(workspace, dev),
+                                                _stream_of(stream, dev)), "tb_patch_group_norm_backward_cl")
+    return dxs, dgamma, dbeta
+
+
+# ---------------------------------------------------------------------------
+# dropout
+# ---------------------------------------------------------------------------
+
+def tb_dropout(x: torch.Tensor, y: torch.Tensor, p: float, seed: int, offset: int = 0,
+               residual: Optional[torch.Tensor] = None, state: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """Dropout of x, plus ``residual``, into ``y``; ``y`` may be ``x`` or
+    ``residual``.  All are [..., cols] with any row stride.  The mask belongs
+    to (seed, offset) and the element's number, so the same call on the
+    gradient, without a residual, is the backward pass.  ``seed`` and
+    ``offset`` are taken modulo 2^64; ``state``, a contiguous int64 tensor of
+    two, is added to them when the kernel runs."""
+    shape, dev = x.shape, x.get_device()
+    if dev < 0:
+        raise ValueError("the rows must be CUDA tensors")
+    if not shape:
+        raise ValueError("rows of elements")
+    dt, cols = x.dtype, shape[-1]
+    rp, r_ld = None, 0
+    if residual is not None:
+        rp, r_ld = residual.data_ptr(), _row_ld(residual, shape, dt, dev, "residual")
+    status = _lib.tb_dropout(x.data_ptr(), _row_ld(x, shape, dt, dev, "x"), rp, r_ld, _dtype_code(x),
+                             x.numel() // cols if cols else 0, cols, p, seed & 0xFFFFFFFFFFFFFFFF,
+                             offset & 0xFFFFFFFFFFFFFFFF, _vec(state, 2, torch.int64, dev, "state"), y.data_ptr(),
+                             _row_ld(y, shape, dt, dev, "y"), _stream_of(stream, dev))
+    if status:
+        raise TileBlendError(status, "tb_dropout")
+    return y
+
+
+def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, residual: Optional[torch.Tensor] = None,
+            state: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """tb_dropout into a new tensor."""
+    y = _on_stream(lambda: torch.empty(x.shape, dtype=x.dtype, device=x.device), stream)
+    return tb_dropout(x, y, p, seed, offset, residual, state, stream)

@@ -1,0 +1,376 @@
+"""GPU parity of channels-last PatchGroupNorm against the float64 oracle, which
+sees the same tensors with the channels moved forward.
+
+Forward tolerances as for the channels-first calls (``tests/tolerance.py``) where
+inputs are of order one, else derived at the test; backward tolerances as derived
+at the head of ``test_gpu_training.py`` (rounding of the output and K u times the
+magnitudes that make it)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import groupnorm as GN
+from tests.test_gpu_training import DT, HALF, TINY, U, check, check_gn, f64, rows_of, weights_of
+from tests.tolerance import gn_violation
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tbl():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from patch_groupnorm_gb300 import build
+    build.build()
+    from patch_groupnorm_gb300 import tileblend
+    return tileblend
+
+
+def cf(ts):
+    return [t.movedim(-1, 1) for t in ts]
+
+
+def check_forward(xs, G, gamma, beta, eps, silu, outs):
+    name = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}[xs[0].dtype]
+    assert gn_violation(cf(outs), cf(xs), gamma, beta, G, eps, silu, name) <= 1.0
+
+
+def check_backward(dys, xs, G, gamma, beta, eps, silu, dxs, dgamma, dbeta):
+    check_gn(cf(dys), cf(xs), G, gamma, beta, eps, silu, cf(dxs), dgamma, dbeta, 2e-5)
+
+
+def run(tbl, xs, dys, G, gamma, beta, eps, silu):
+    part = tbl.new_partials(len(xs), xs[0].shape[0], G)
+    part.fill_(-1)
+    outs = tbl.patch_group_norm_cl(xs, G, gamma, beta, eps, silu, partials=part)
+    check_forward(xs, G, gamma, beta, eps, silu, outs)
+    dxs, dg, db = tbl.patch_group_norm_backward_cl(dys, xs, G, part, gamma, beta, eps, silu)
+    check_backward(dys, xs, G, gamma, beta, eps, silu, dxs, dg, db)
+    return part, outs, dxs, dg, db
+
+
+# shape [N, *spatial, C], split axis, sizes, groups
+CASES = [
+    ((1, 24, 40, 32), 1, [6, 6, 6, 6], 4),
+    ((2, 10, 33, 16), 2, [9, 8, 8, 8], 4),
+    ((1, 5, 12, 16, 24), 3, [4, 4, 4, 4], 4),
+    ((1, 3, 7, 9, 12), 2, [4, 3], 2),             # a position is not a whole number of chunks
+    ((3, 64, 8), 1, [64], 4),
+    ((2, 1, 6), 1, [1], 3),                        # one position
+    ((1, 8, 16, 4), 1, [3, 0, 5], 1),              # an empty patch in the middle
+    ((3, 17, 3, 5), 1, [10, 7], 5),                # samples at odd addresses; one channel a group
+    ((1, 1, 1, 1), 1, [1], 1),                     # a single element
+    ((2, 2, 3), 1, [1, 1], 1),                     # fewer elements than a chunk
+    ((1, 900, 67), 1, [450, 450], 67),
+    ((1, 50, 515), 1, [20, 30], 5),                # a period wider than a CTA
+    ((2, 9, 1300), 1, [9], 26),                    # more columns than threads in 32 bits
+    ((1, 3, 2051), 1, [3], 7),
+    ((1, 7000, 40), 1, [3501, 3499], 5),           # many turns of a CTA
+    ((1, 33000, 8), 1, [33000], 2),
+    ((1, 4001, 64), 1, [1, 4000], 8),              # patches of very different size
+    ((70, 5, 24), 1, [2, 3], 3),                   # many samples
+]
+
+
+@pytest.mark.parametrize("silu", [True, False])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "x".join(map(str, c[0])))
+def test_forward_and_backward(tbl, case, dtype, silu):
+    shape, dim, sizes, G = case
+    dt = DT[dtype]
+    x = rows_of(sum(shape), shape, torch.float64, 1.5)
+    xs = [(p + m).to(dt).contiguous() for p, m in zip(x.split(sizes, dim), [-3.0, 3.0, -1.0, 1.0])]
+    dys = [p.contiguous() for p in rows_of(7, shape, dt, 0.5).split(sizes, dim)]
+    gamma, beta = weights_of(8, shape[-1], dt)
+    run(tbl, xs, dys, G, gamma, beta, 1e-6, silu)
+    run(tbl, xs, dys, G, None, None, 1e-6, silu)
+    run(tbl, xs, dys, G, gamma, None, 1e-6, silu)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("C,G", [(48, 4), (50, 5), (515, 103)])
+def test_in_place_misaligned_and_guard_bands(tbl, C, G, dtype):
+    dt = DT[dtype]
+    shape = (2, 30, C)
+    x, dy = rows_of(1, shape, dt, 1.0, 0.5), rows_of(2, shape, dt)
+    gamma, beta = weights_of(3, C, dt)
+    part, (y,), (dx,), dg, db = run(tbl, [x], [dy], G, gamma, beta, 1e-6, True)
+    t = x.clone()
+    assert torch.equal(tbl.patch_group_norm_cl([t], G, gamma, beta, 1e-6, outs=[t])[0], y)
+    for which in (0, 1):
+        t = [dy.clone(), x.clone()]
+        (o,), g2, b2 = tbl.patch_group_norm_backward_cl([t[0]], [t[1]], G, part, gamma, beta, 1e-6, dxs=[t[which]])
+        assert torch.equal(o, dx) and torch.equal(g2, dg) and torch.equal(b2, db)
+    # all tensors at one offset, then at several; what lies around them stays
+    n = x.numel()
+    for at in ((1, 1, 1), (3, 3, 3), (0, 1, 2), (1, 0, 0)):
+        buf = torch.full((3, (n + 24) // 8 * 8), 7.0, dtype=dt, device="cuda")
+        mx, md, mo = (b[a:a + n].view(shape) for a, b in zip(at, buf))
+        mx.copy_(x)
+        md.copy_(dy)
+        tbl.patch_group_norm_cl([mx], G, gamma, beta, 1e-6, outs=[mo])
+        check_forward([x], G, gamma, beta, 1e-6, True, [mo])
+        _, g2, b2 = tbl.patch_group_norm_backward_cl([md], [mx], G, part, gamma, beta, 1e-6, dxs=[mo])
+        check_backward([dy], [x], G, gamma, beta, 1e-6, True, [mo], g2, b2)
+        assert torch.equal(mx, x) and torch.equal(md, dy)
+        for a, b in zip(at, buf):
+            assert (b[:a] == 7.0).all() and (b[a + n:] == 7.0).all()
+
+
+def test_records_are_those_of_the_channels_first_calls(tbl):
+    # either statistics serve either apply; the pooled sums agree
+    dt, G = torch.float32, 4
+    xs = [p.contiguous() for p in rows_of(1, (2, 12, 8, 16), dt, 1.0, 2.0).split([5, 7], 1)]
+    fs = [x.movedim(-1, 1).contiguous() for x in xs]
+    gamma, beta = weights_of(2, 16, dt)
+    a = tbl.tb_patch_gn_stats_cl(xs, G, tbl.new_partials(2, 2, G))
+    b = tbl.tb_patch_gn_stats(fs, G, tbl.new_partials(2, 2, G))
+    assert torch.equal(a[..., 0].sum(-1), b[..., 0].sum(-1))
+    ya = tbl.tb_patch_gn_apply_cl(xs, [torch.empty_like(x) for x in xs], G, b, 2, gamma, beta, 1e-6)
+    check_forward(xs, G, gamma, beta, 1e-6, True, ya)
+    yb = tbl.tb_patch_gn_apply(fs, [torch.empty_like(f) for f in fs], G, a, gamma, beta, 1e-6)
+    check_forward(xs, G, gamma, beta, 1e-6, True, [y.movedim(1, -1) for y in yb])
+    dys = [rows_of(5 + k, x.shape, dt) for k, x in enumerate(xs)]
+    ga = tbl.tb_patch_gn_grad_stats_cl(dys, xs, G, b, 2, gamma, beta, 1e-6, tbl.new_grad_partials(2, 2, 16))
+    dfs = [torch.empty_like(f) for f in fs]
+    dg, db = torch.empty_like(gamma), torch.empty_like(gamma)
+    tbl.tb_patch_gn_grad_apply([d.movedim(-1, 1).contiguous() for d in dys], fs, dfs, G, b, ga, 2, gamma, beta, 1e-6, dg,
+                               db)
+    check_gn(cf(dys), cf(xs), G, gamma, beta, 1e-6, True, dfs, dg, db, 2e-5)
+
+
+@pytest.mark.parametrize("R", [2, 6])
+def test_gathered_records(tbl, R):
+    # ranks with one patch each: records of both passes gathered, each rank's results equal the unsharded ones
+    dt, G = torch.bfloat16, 4
+    x, dy = rows_of(1, (2, 4 * R, 8, 16), dt, 1.0, 0.5), rows_of(2, (2, 4 * R, 8, 16), dt)
+    sizes = [3, 5] + [4] * (R - 2)
+    xs, dys = ([p.contiguous() for p in t.split(sizes, 1)] for t in (x, dy))
+    gamma, beta = weights_of(3, 16, dt)
+    part = torch.cat([tbl.tb_patch_gn_stats_cl([p], G, tbl.new_partials(1, 2, G)) for p in xs])
+    ys = [tbl.tb_patch_gn_apply_cl([p], [torch.empty_like(p)], G, part, R, gamma, beta, 1e-6)[0] for p in xs]
+    check_forward(xs, G, gamma, beta, 1e-6, True, ys)
+    grad = torch.cat([tbl.tb_patch_gn_grad_stats_cl([d], [p], G, part, R, gamma, beta, 1e-6,
+                                                    tbl.new_grad_partials(1, 2, 16)) for d, p in zip(dys, xs)])
+    ws = tbl.gn_workspace_cl(2, G)
+    dxs, dgs, dbs = [], [], []
+    for d, p in zip(dys, xs):
+        o, dg, db = torch.empty_like(p), torch.empty_like(gamma), torch.empty_like(gamma)
+        tbl.tb_patch_gn_grad_apply_cl([d], [p], [o], G, part, grad, R, gamma, beta, 1e-6, ws, dg, db)
+        dxs.append(o)
+        dgs.append(dg)
+        dbs.append(db)
+    check_backward(dys, xs, G, gamma, beta, 1e-6, True, dxs, dgs[0], dbs[0])
+    assert all(torch.equal(dgs[0], t) for t in dgs) and all(torch.equal(dbs[0], t) for t in dbs)
+    # a rank whose patch is empty still gets the weight gradients
+    empty = torch.empty(2, 0, 8, 16, dtype=dt, device="cuda")
+    dg, db = torch.full_like(gamma, 9.0), torch.full_like(gamma, 9.0)
+    tbl.tb_patch_gn_grad_apply_cl([empty], [empty], [empty], G, part, grad, R, gamma, beta, 1e-6, ws, dg, db)
+    assert torch.equal(dg, dgs[0]) and torch.equal(db, dbs[0])
+
+
+def test_empty_sets_of_records_come_first(tbl):
+    # five ranks without elements before the one that has them all
+    x = rows_of(1, (1, 40, 16), torch.float32, 1.0, 100.0)
+    none = x[:, :0].contiguous()
+    part = torch.cat([tbl.tb_patch_gn_stats_cl([t], 2, tbl.new_partials(1, 1, 2)) for t in [none] * 5 + [x]])
+    y, = tbl.tb_patch_gn_apply_cl([x], [torch.empty_like(x)], 2, part, 6, None, None, 1e-6)
+    want, = tbl.patch_group_norm_cl([x], 2, None, None, 1e-6)
+    assert torch.equal(y, want)
+
+
+def test_checks_and_empty_batches(tbl):
+    x = rows_of(1, (1, 4, 8), torch.float32)
+    part = tbl.tb_patch_gn_stats_cl([x], 2, tbl.new_partials(1, 1, 2))
+    with pytest.raises(ValueError):
+        tbl.tb_patch_gn_stats_cl([x], 4, part)                                       # records of another size
+    with pytest.raises(ValueError):
+        tbl.tb_patch_gn_stats_cl([x.transpose(1, 2)], 2, part)                       # not contiguous
+    with pytest.raises(ValueError):
+        tbl.patch_group_norm_cl([x, x.half()], 2, None, None, 1e-6)
+    with pytest.raises(ValueError):
+        tbl.patch_group_norm_cl([x], 2, torch.ones(4, device="cuda"), None, 1e-6)
+    with pytest.raises(ValueError):
+        tbl.patch_group_norm_cl([x], 2, None, None, 1e-6, outs=[x[:, :2]])
+    with pytest.raises(ValueError):
+        tbl.patch_group_norm_backward_cl([x.half()], [x], 2, part, None, None, 1e-6)
+    with pytest.raises(ValueError):
+        tbl.patch_group_norm_backward_cl([x], [x], 2, part, None, None, 1e-6, grad_partials=torch.empty(4, device="cuda"))
+    with pytest.raises(tbl.TileBlendError):
+        tbl.patch_group_norm_backward_cl([x], [x], 2, part, None, None, 1e-6, workspace=torch.empty(4, device="cuda"))
+    with pytest.raises(tbl.TileBlendError):
+        tbl.patch_group_norm_cl([x], 3, None, None, 1e-6)                            # 8 channels in 3 groups
+    e = torch.empty(0, 4, 8, device="cuda")
+    part = tbl.new_partials(1, 0, 2)
+    assert tbl.patch_group_norm_cl([e], 2, None, None, 1e-6, partials=part)[0].shape == e.shape
+    dxs, dg, db = tbl.patch_group_norm_backward_cl([e], [e], 2, part, None, None, 1e-6)
+    assert dxs[0].shape == e.shape and (dg == 0).all() and (db == 0).all()
+    e = torch.empty(2, 0, 8, device="cuda")                                          # no positions at all
+    part = tbl.tb_patch_gn_stats_cl([e], 2, tbl.new_partials(1, 2, 2).fill_(-1))
+    assert (part[..., 0] == 0).all()
+    dxs, dg, db = tbl.patch_group_norm_backward_cl([e], [e], 2, part, None, None, 1e-6)
+    assert dxs[0].shape == e.shape and (dg == 0).all() and (db == 0).all()
+
+
+def test_far_means_and_an_outlier(tbl):
+    # statistics about a shift: a mean a thousand deviations away, a first
+    # element far from all others, a constant group.  The result's own bound: 4 u
+    # of the mean move xhat by 4 u * |mean| * rstd, the sum of what is left of the
+    # elements past their shift is off by 64 u of its magnitudes, the mean of
+    # |x - mean|, and the variance's error is that of 64 sums, relative to itself
+    x = rows_of(1, (1, 5000, 32), torch.float64)
+    x[..., 8:16] += 1000.0
+    x[0, 0, 16] = 1e4
+    x[..., 24:] = 3.25
+    x = x.float()
+    part = tbl.new_partials(1, 1, 4)
+    y, = tbl.patch_group_norm_cl([x], 4, None, None, 1e-6, silu=False, partials=part)
+    h = f64(x).reshape(5000, 4, 8)
+    mu = h.mean((0, 2), keepdims=True)
+    r = 1 / np.sqrt(((h - mu) ** 2).mean((0, 2), keepdims=True) + 1e-6)
+    want = ((h - mu) * r).reshape(1, 5000, 32)
+    away = np.abs(h - mu).mean((0, 2), keepdims=True)
+    scale = ((np.abs(mu) / 16 + away) * r + np.abs((h - mu) * r)).reshape(1, 5000, 32)
+    scale[..., 24:] = 0
+    check(y, want, scale)
+    assert (y[..., 24:] == 0).all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_bad_values_stay_in_their_group(tbl, bad):
+    x = rows_of(1, (2, 300, 16), torch.float32)
+    clean, = tbl.patch_group_norm_cl([x], 4, None, None, 1e-6)
+    t = x.clone()
+    t[1, 123, 5] = bad
+    y, = tbl.patch_group_norm_cl([t], 4, None, None, 1e-6)
+    assert torch.isnan(y[1, :, 4:8]).all()
+    y[1, :, 4:8] = clean[1, :, 4:8]
+    assert torch.equal(y, clean)
+
+
+def test_extreme_activations(tbl):
+    # z far on either side of zero: silu' goes to 1 and to 0, and never to NaN
+    x = rows_of(1, (1, 256, 4), torch.float32)
+    gamma = torch.tensor([1.0, 500.0, -500.0, 1e-3], device="cuda")
+    beta = torch.tensor([0.0, 200.0, -200.0, -90.0], device="cuda")
+    part = tbl.tb_patch_gn_stats_cl([x], 1, tbl.new_partials(1, 1, 1))
+    dy = rows_of(2, (1, 256, 4), torch.float32)
+    dxs, dg, db = tbl.patch_group_norm_backward_cl([dy], [x], 1, part, gamma, beta, 1e-6)
+    check_backward([dy], [x], 1, gamma, beta, 1e-6, True, dxs, dg, db)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("shape,G", [((1, 3000, 64), 8), ((2, 700, 515), 5), ((1, 40, 1300), 10)])
+def test_every_element_is_counted_once(tbl, shape, G, dtype):
+    # small integers: sums are exact, so one element left out or taken twice fails
+    dt = DT[dtype]
+    g = torch.Generator().manual_seed(1)
+    x = torch.randint(-2, 3, shape, generator=g).to(dt).cuda()
+    dy = torch.randint(-2, 3, shape, generator=g).to(dt).cuda()
+    N, S, C = shape
+    # a forward pass whose records say mean 0 and variance 1: xhat = x
+    part = torch.zeros(1, N, G, 8, 2, dtype=torch.int64, device="cuda")
+    part[..., 0, 0] = S * C // G
+    part.view(torch.float32)[..., 0, 3] = float(S * C // G)
+    grec = tbl.new_grad_partials(1, N, C).fill_(float("nan"))
+    tbl.tb_patch_gn_grad_stats_cl([dy], [x], G, part, 1, None, None, 0.0, grec, silu=False)
+    assert torch.equal(grec[0, ..., 0].sum(-1), dy.float().sum(1))
+    assert torch.equal(grec[0, ..., 1].sum(-1), (dy.float() * x.float()).sum(1))
+    rec = tbl.tb_patch_gn_stats_cl([x], G, tbl.new_partials(1, N, G).fill_(-1))
+    assert (rec[..., 0].sum(-1) == S * C // G).all()
+
+
+def test_deterministic_and_in_any_order_of_calls(tbl):
+    x, dy = rows_of(1, (1, 96 * 96, 64), torch.bfloat16), rows_of(2, (1, 96 * 96, 64), torch.bfloat16)
+    gamma, beta = weights_of(3, 64, torch.bfloat16)
+    first = None
+    for _ in range(50):
+        part = tbl.new_partials(1, 1, 32)
+        y, = tbl.patch_group_norm_cl([x], 32, gamma, beta, 1e-6, partials=part)
+        (dx,), dg, db = tbl.patch_group_norm_backward_cl([dy], [x], 32, part, gamma, beta, 1e-6)
+        got = [part, y, dx, dg, db]
+        if first is None:
+            first = [t.clone() for t in got]
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradient_matches_differences(tbl, dtype):
+    # the formula's gradient against differences of the oracle's forward pass
+    x, v, dy = rows_of(1, (1, 60, 24), torch.float64), rows_of(2, (1, 60, 24), torch.float64), rows_of(3, (1, 60, 24),
+                                                                                                       torch.float64)
+    dt = DT[dtype]
+    x, dy = x.to(dt), dy.to(dt)
+    gamma, beta = weights_of(4, 24, dt)
+    part = tbl.tb_patch_gn_stats_cl([x], 3, tbl.new_partials(1, 1, 3))
+    (dx,), _, _ = tbl.patch_group_norm_backward_cl([dy], [x], 3, part, gamma, beta, 1e-6)
+    h = 1e-5
+
+    def f(s):
+        return float((GN.patch_group_norm([(f64(x) + s * f64(v)).transpose(0, 2, 1)], 3, f64(gamma), f64(beta), 1e-6)[0]
+                      .transpose(0, 2, 1) * f64(dy)).sum())
+    want = (f(h) - f(-h)) / (2 * h)
+    got = float((f64(dx) * f64(v)).sum())
+    # each gradient is off by half a step of its type and 64 u; differences of h by h^2
+    bound = (np.abs(f64(dx) * f64(v)) * (HALF[dt] + 64 * U)).sum() + 1e-5 + TINY[dt]
+    assert abs(got - want) <= bound
+
+
+def test_offsets_past_32_bits(tbl):
+    # a patch of more than 2^31 elements: constant but for a few positions near its end
+    S, C, G = (1 << 31) // 64 + 4096, 64, 2
+    x = torch.zeros(1, S, C, dtype=torch.bfloat16, device="cuda")
+    x[0, ::2] = 1.0
+    x[0, 1::2] = -1.0
+    x[0, -1, 5] = 40.0
+    y, = tbl.patch_group_norm_cl([x], G, None, None, 0.0, silu=False)
+    # mean and variance move by less than 1e-6: the step of bf16 is far wider
+    assert torch.equal(y, x)
+    del y
+    part = tbl.tb_patch_gn_stats_cl([x], G, tbl.new_partials(1, 1, G))
+    dy = torch.zeros_like(x)
+    dy[0, -1, 7] = 1.0
+    dy[0, 0, 40] = 2.0
+    (dx,), dg, db = tbl.patch_group_norm_backward_cl([dy], [x], G, part, None, None, 0.0, silu=False)
+    assert db.tolist() == [1.0 if c == 7 else 2.0 if c == 40 else 0.0 for c in range(C)]
+    assert dx[0, -1, 7] == 1.0 and dx[0, 0, 40] == 2.0
+
+
+def _pass(tbl, x, dy, gamma, beta, stream=None):
+    part = tbl._on_stream(lambda: tbl.new_partials(1, 1, 4), stream)
+    y = tbl.patch_group_norm_cl([x], 4, gamma, beta, 1e-6, partials=part, stream=stream)
+    dxs, dg, db = tbl.patch_group_norm_backward_cl([dy], [x], 4, part, gamma, beta, 1e-6, stream=stream)
+    return [*y, *dxs, dg, db]
+
+
+def _inputs(seed=0):
+    bf = torch.bfloat16
+    return [rows_of(seed + 1, (1, 500, 16), bf), rows_of(seed + 2, (1, 500, 16), bf), *weights_of(seed + 3, 16, bf)]
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_on_another_stream(tbl, raw):
+    ins = _inputs()
+    want = _pass(tbl, *ins)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(20):
+        got = _pass(tbl, *ins, stream=s.cuda_stream if raw else s)
+        s.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_replay_from_a_graph(tbl):
+    ins = _inputs()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        _pass(tbl, *ins)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        outs = _pass(tbl, *ins)
+    for seed in (100, 200):
+        for t, u in zip(ins, _inputs(seed)):
+            t.copy_(u)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, _pass(tbl, *ins)))

@@ -104,7 +104,7 @@ void cl_plan_stats(tb::GnClParams& prm, tb_dtype dtype, bool vector, int ctas_wa
     for (int p = 0; p < prm.P; ++p) whole = whole && (vec == 1 || aligned(prm.patches[p], 16));
     const int64_t units = prm.N * prm.P;
     int splits = 1;
-    while (units * splits * TB_GN_PARTS * 8 < ctas_wanted && whole && prm.G % (splits * 2) == 0 &&
+    while (units * splits * TB_GN_PARTS * tb::CL_MAX_CLUSTER < ctas_wanted && whole && prm.G % (splits * 2) == 0 &&
            (prm.C / (splits * 2)) % vec == 0 && prm.C / (splits * 2) * es >= 256)
         splits *= 2;
     prm.splits = splits;
@@ -117,7 +117,7 @@ void cl_plan_stats(tb::GnClParams& prm, tb_dtype dtype, bool vector, int ctas_wa
     const int64_t useful = std::max<int64_t>(1, most / (side * 4));
     const int64_t each = std::min(useful, std::max<int64_t>(1, ctas_wanted / (units * splits)));
     const int64_t parts = std::min<int64_t>(TB_GN_PARTS, each);
-    prm.cluster = (int32_t)std::max<int64_t>(1, std::min<int64_t>(8, each / parts));
+    prm.cluster = (int32_t)std::max<int64_t>(1, std::min<int64_t>(tb::CL_MAX_CLUSTER, each / parts));
     int64_t at = 0;
     for (int p = 0; p < prm.P; ++p) {
         const int64_t share = (cl_rows(prm, p, vec) * parts + most / 2) / most;

@@ -14,32 +14,23 @@ namespace {
 
 // --- statistics -------------------------------------------------------------------
 
-// Groups of one CTA: count, mean and sum of squared deviations of what it read.
-struct ClTable {
-    int2* moments;   // (mean, M2) as bits
-    long long* n;
-};
-
-__device__ __forceinline__ void chan(long long& n, float& mean, float& m2, long long bn, float bmean, float bm2) {
-    if (bn == 0) return;
-    if (n == 0) {
-        n = bn;
-        mean = bmean;
-        m2 = bm2;
-        return;
-    }
-    const float na = (float)n, nb = (float)bn, total = (float)(n + bn);
-    const float d = bmean - mean, f = nb / total;
-    mean = fmaf(d, f, mean);
-    m2 += fmaf(d * d, na * f, bm2);
-    n += bn;
+// (n, mean, M2) joined with (bn, bmean, bm2), Chan's way.  Counts are floats, exact up
+// to 2^24 elements: they weigh means and squares here; a record's own count comes
+// from the sizes.
+__device__ __forceinline__ void chan(float& n, float& mean, float& m2, float bn, float bmean, float bm2) {
+    const float total = n + bn;
+    const float f = bn > 0.f ? __fdividef(bn, total) : 0.f;  // 1, exactly, where n is 0
+    const float d = n > 0.f && bn > 0.f ? bmean - mean : 0.f;
+    mean = n > 0.f ? fmaf(d, f, mean) : bmean;
+    m2 += fmaf(d * d, n * f, bn > 0.f ? bm2 : 0.f);
+    n = total;
 }
 
 constexpr int FOLD = 64;  // chunks between two foldings of a thread's sums
-constexpr int SU = 4;     // chunks a thread loads together
+constexpr int DEPTH = 8;  // chunks of a thread on their way or in work
 
 // Each thread sums x - K and (x - K)^2 of its VEC channels on packed pairs, K its
-// own first value, then its mean so far; after SU, SU, 2 SU, 4 SU, ... and then every
+// own first value, then its mean so far; after DEPTH, DEPTH, 2 DEPTH, 4 DEPTH, ... and then every
 // FOLD chunks the sums are merged into (mean, M2) (Chan), so that neither a far mean
 // nor a long run loses digits, nor a first value far from all others: n chunks
 // about a mean that it has moved by 1 / n of its distance add 1 / n of its square.
@@ -51,25 +42,22 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
     using W = ClWord<DT, VEC>;
     constexpr int ES = elem_size(DT), NL = L::N;
     extern __shared__ uint4 shared4[];
-    float* const stage_mean = reinterpret_cast<float*>(shared4);      // [CL_BLOCK * VEC]
+    using Stream = ClStream<DT, VEC, 1, DEPTH>;
+    float* const stage_mean = reinterpret_cast<float*>(shared4 + Stream::SMEM / 16);  // [CL_BLOCK * VEC]
     float* const stage_m2 = stage_mean + CL_BLOCK * VEC;              // [CL_BLOCK * VEC]
     int* const stage_n = reinterpret_cast<int*>(stage_m2 + CL_BLOCK * VEC);  // [CL_BLOCK]
     const int C = (int)p.C, G = p.G, K = C / G;
     const int gs = G / p.splits, g0 = (int)blockIdx.y * gs, g1 = g0 + gs;  // this CTA's groups
-    ClTable table;
-    table.n = reinterpret_cast<long long*>(stage_n + CL_BLOCK);       // [gs]
-    table.moments = reinterpret_cast<int2*>(table.n + gs);            // [gs]
+    float4* const table = reinterpret_cast<float4*>(stage_n + CL_BLOCK);     // [gs]: (count, mean, M2)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int g = threadIdx.x; g < gs; g += CL_BLOCK) {
-        table.n[g] = 0;
-        table.moments[g] = make_int2(0, 0);
-    }
+    int team = 32;  // threads that join a group's positions
+    while (team > 1 && gs * team > CL_BLOCK) team /= 2;
+    for (int i = threadIdx.x; i < gs; i += CL_BLOCK) table[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     const ClUnit u = cl_unit(p);
     const int parts = p.parts[u.p], piece = u.part * p.cluster + u.rank, pieces = parts * p.cluster;
     const ClRun run = cl_run<ES, VEC>(p.patches[u.p], p.spatial[u.p], p.C, u.n);
     const char* const patch = static_cast<const char*>(p.patches[u.p]);
     const int64_t bytes = p.N * run.elems * ES;
-    const W* const base = reinterpret_cast<const W*>(patch + (run.first + run.head) * ES);
     grid_wait();
 
     // elements outside the whole chunks: the first piece's before, the last one's after; a lane each
@@ -96,24 +84,29 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
         typename L::T k[NL], s1[NL], s2[NL], mean[NL], m2[NL];
 #pragma unroll
         for (int i = 0; i < NL; ++i) k[i] = mean[i] = m2[i] = L::splat(0.f);
-        const W* at = base + w.at;
+        Stream in;
+        in.base[0] = patch;
+        in.at[0] = patch + (run.first + run.head) * ES + w.at * (int64_t)sizeof(W);
+        in.stride = w.stride * (int64_t)sizeof(W);
+        in.bytes = bytes;
+        in.status = p.status;
+        in.start(w.count, shared4);
         for (int done = 0, now; done < w.count; done += now) {
-            now = min(min(FOLD, max(SU, done)), w.count - done);
+            now = min(min(FOLD, max(DEPTH, done)), w.count - done);
 #pragma unroll
             for (int i = 0; i < NL; ++i) s1[i] = s2[i] = L::splat(0.f);
-            for (int s = 0; s < now; s += SU) {
-                W v[SU];
+            for (int s = 0; s < now; s += DEPTH) {
 #pragma unroll
-                for (int r = 0; r < SU; ++r)
-                    if (s + r < now && in_bounds(at + r * w.stride, sizeof(W), patch, bytes, p.status))
-                        v[r] = __ldg(at + r * w.stride);
-                at += SU * w.stride;
-                if (done == 0 && s == 0) to_lanes<DT, VEC>(v[0], k);
-#pragma unroll
-                for (int r = 0; r < SU; ++r) {
+                for (int r = 0; r < DEPTH; ++r) {
                     if (s + r < now) {
+                        W v[1];
+                        in.step(r, v);
                         typename L::T f[NL];
-                        to_lanes<DT, VEC>(v[r], f);
+                        to_lanes<DT, VEC>(v[0], f);
+                        if (r == 0 && done + s == 0) {
+#pragma unroll
+                            for (int i = 0; i < NL; ++i) k[i] = mean[i] = f[i];
+                        }
 #pragma unroll
                         for (int i = 0; i < NL; ++i) {
                             const typename L::T d = vsub(f[i], k[i]);
@@ -148,47 +141,41 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
         }
         stage_n[threadIdx.x] = w.count;
         __syncthreads();
-        // phases [head + j0 * VEC, head + j1 * VEC) hold this group's channels in runs of at most K
+        // the rows side by side: a thread per position of the row
         const int lo = run.head + j0 * VEC, hi = run.head + j1 * VEC, pitch = q.width * VEC;
-        for (int g = g0 + warp; g < g1; g += CL_BLOCK / 32) {
-            const int c0 = g * K;
-            const int m_first = lo >= c0 + K ? (lo - c0 - K) / C + 1 : 0;  // the first run that ends past lo
-            long long n = 0;
-            float gm = 0.f, k0 = 0.f, s = 0.f;
-            for (int pass = 0; pass < 2; ++pass) {
-                long long sn = 0;
-                s = 0.f;
-                for (int m = m_first; c0 + m * C < hi; ++m) {
-                    const int from = max(c0 + m * C, lo) - lo, len = min(c0 + m * C + K, hi) - lo - from;
-                    if (pass == 0 && m == m_first) k0 = stage_mean[from];
-                    for (int e = lane; e < q.rows * len; e += 32) {
-                        const int row = e / len, idx = row * pitch + from + (e - row * len);
-                        const int ni = stage_n[idx / VEC];
-                        if (ni == 0) continue;
-                        if (pass == 0) {
-                            sn += ni;
-                            s = fmaf((float)ni, stage_mean[idx] - k0, s);
-                        } else {
-                            const float d = stage_mean[idx] - gm;
-                            s += fmaf((float)ni * d, d, stage_m2[idx]);
-                        }
+        for (int i = threadIdx.x; i < pitch; i += CL_BLOCK) {
+            float n = 0.f, mean_i = 0.f, m2_i = 0.f;
+            for (int r = 0; r < q.rows; ++r)
+                chan(n, mean_i, m2_i, (float)stage_n[r * q.width + i / VEC], stage_mean[r * pitch + i],
+                     stage_m2[r * pitch + i]);
+            stage_mean[i] = mean_i;
+            stage_m2[i] = m2_i;
+        }
+        __syncthreads();
+        // then the positions of each group, `team` threads to a group: its channels
+        // lie in phases [head + j0 * VEC, head + j1 * VEC), in runs of at most K
+        for (int first = 0; first < gs; first += CL_BLOCK / team) {
+            const int i = first + (int)threadIdx.x / team, c0 = (g0 + i) * K;
+            float n = 0.f, mean_g = 0.f, m2_g = 0.f;
+            if (i < gs) {
+                for (int m = lo >= c0 + K ? (lo - c0 - K) / C + 1 : 0; c0 + m * C < hi; ++m) {
+                    const int to = min(c0 + m * C + K, hi) - lo;
+                    for (int e = max(c0 + m * C, lo) - lo + (int)threadIdx.x % team; e < to; e += team) {
+                        int ne = 0;
+                        for (int r = 0; r < q.rows; ++r) ne += stage_n[r * q.width + e / VEC];
+                        chan(n, mean_g, m2_g, (float)ne, stage_mean[e], stage_m2[e]);
                     }
                 }
-                s = warp_sum(s);
-                if (pass == 0) {
-#pragma unroll
-                    for (int d = 16; d >= 1; d >>= 1) sn += __shfl_xor_sync(0xffffffffu, sn, d);
-                    n = sn;
-                    gm = n > 0 ? k0 + s / (float)n : 0.f;
-                }
             }
-            if (lane == 0 && n > 0) {
-                const int i = g - g0;
-                long long tn = table.n[i];
-                float tm = __int_as_float(table.moments[i].x), t2 = __int_as_float(table.moments[i].y);
-                chan(tn, tm, t2, n, gm, s);
-                table.n[i] = tn;
-                table.moments[i] = make_int2(__float_as_int(tm), __float_as_int(t2));
+            for (int d = team / 2; d >= 1; d >>= 1) {
+                const float nb = __shfl_down_sync(0xffffffffu, n, d), mb = __shfl_down_sync(0xffffffffu, mean_g, d);
+                chan(n, mean_g, m2_g, nb, mb, __shfl_down_sync(0xffffffffu, m2_g, d));
+            }
+            if (i < gs && threadIdx.x % team == 0) {
+                // table entries belong to this thread throughout
+                float4 t = table[i];
+                chan(t.x, t.y, t.z, n, mean_g, m2_g);
+                table[i] = t;
             }
         }
     }
@@ -198,51 +185,64 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
             const int from = __ffs(left) - 1, i = __shfl_sync(0xffffffffu, edge_group, from) - g0;
             const float v = __shfl_sync(0xffffffffu, edge, from);
             if (lane == 0) {
-                long long tn = table.n[i];
-                float tm = __int_as_float(table.moments[i].x), t2 = __int_as_float(table.moments[i].y);
-                chan(tn, tm, t2, 1, v, 0.f);
-                table.n[i] = tn;
-                table.moments[i] = make_int2(__float_as_int(tm), __float_as_int(t2));
+                float4 t = table[i];
+                chan(t.x, t.y, t.z, 1.f, v, 0.f);
+                table[i] = t;
             }
         }
         __syncwarp();
     }
     if (p.cluster > 1) cluster_sync();
     else __syncthreads();
+    // the cluster's tables: eight threads to a group, one for each CTA
+    static_assert(CL_MAX_CLUSTER == 8 && TB_GN_PARTS == 8, "eight threads read the CTAs' sums and write the parts");
+    int64_t row0, row1, none;
+    cl_piece(total_rows, u.part * p.cluster, pieces, row0, none);
+    cl_piece(total_rows, (u.part + 1) * p.cluster - 1, pieces, none, row1);
+    const int64_t wide = (int64_t)p.period * VEC;
+    const int64_t e0 = u.part == 0 ? 0 : run.head + row0 * wide;
+    const int64_t e1 = u.part == parts - 1 ? run.elems : run.head + row1 * wide;
+    // elements of channels c0 .. c0 + K - 1 among the first e
+    auto among = [&](int64_t e, int c0) { return e / C * K + min(max((int)(e % C) - c0, 0), K); };
     GnPartial* const out = p.partials + ((int64_t)u.p * p.N + u.n) * G * TB_GN_PARTS;
-    for (int i = u.rank * CL_BLOCK + (int)threadIdx.x; i < gs; i += p.cluster * CL_BLOCK) {
-        long long n = 0;
-        float mean = 0.f, m2 = 0.f;
-        for (int r = 0; r < p.cluster; ++r) {
-            long long bn;
-            int2 bm;
-            if (r == u.rank) {
-                bn = table.n[i];
-                bm = table.moments[i];
+    for (int first = 0; first < gs; first += p.cluster * (CL_BLOCK / 8)) {
+        const int i = first + u.rank * (CL_BLOCK / 8) + (int)threadIdx.x / 8, r = threadIdx.x & 7;
+        float n = 0.f, mean = 0.f, m2 = 0.f;
+        if (i < gs && r < p.cluster) {
+            if (p.cluster > 1) {
+                const uint2 lo = cluster_load8(smem_addr(table + i), (uint32_t)r);
+                n = __uint_as_float(lo.x);
+                mean = __uint_as_float(lo.y);
+                m2 = __uint_as_float(cluster_load8(smem_addr(table + i) + 8, (uint32_t)r).x);
             } else {
-                const uint2 c = cluster_load8(smem_addr(table.n + i), (uint32_t)r);
-                const uint2 m = cluster_load8(smem_addr(table.moments + i), (uint32_t)r);
-                bn = (long long)(((unsigned long long)c.y << 32) | c.x);
-                bm = make_int2((int)m.x, (int)m.y);
+                n = table[i].x;
+                mean = table[i].y;
+                m2 = table[i].z;
             }
-            chan(n, mean, m2, bn, __int_as_float(bm.x), __int_as_float(bm.y));
         }
+#pragma unroll
+        for (int d = 4; d >= 1; d >>= 1) {
+            const float nb = __shfl_down_sync(0xffffffffu, n, d), mb = __shfl_down_sync(0xffffffffu, mean, d);
+            chan(n, mean, m2, nb, mb, __shfl_down_sync(0xffffffffu, m2, d));
+        }
+        if (i >= gs) continue;
         GnPartial* const at = out + (int64_t)(g0 + i) * TB_GN_PARTS;
         if (!in_bounds(at, TB_GN_PARTS * sizeof(GnPartial), p.partials,
                        (int64_t)p.P * p.N * G * TB_GN_PARTS * (int64_t)sizeof(GnPartial), p.status))
             continue;
-        at[u.part] = GnPartial{n, mean, m2};
-        if (u.part == 0)
-            for (int r = parts; r < TB_GN_PARTS; ++r) at[r] = GnPartial{0, 0.f, 0.f};
+        const int c0 = (g0 + i) * K;
+        if (r == 0) at[u.part] = GnPartial{among(e1, c0) - among(e0, c0), mean, m2};
+        if (u.part == 0 && r >= parts) at[r] = GnPartial{0, 0.f, 0.f};
     }
     if (p.cluster > 1) cluster_sync();  // nobody leaves while its table may be read
 }
 
-size_t stats_smem(int vec, int groups) { return (size_t)CL_BLOCK * vec * 8 + CL_BLOCK * 4 + (size_t)groups * 16; }
+template <int DT, int VEC>
+size_t stats_smem(int groups) {
+    return ClStream<DT, VEC, 1, DEPTH>::SMEM + CL_BLOCK * VEC * 8 + CL_BLOCK * 4 + (size_t)groups * 16;
+}
 
 // --- normalisation ------------------------------------------------------------------
-
-constexpr int AU = 4;  // chunks a thread loads together
 
 template <bool SILU>
 __device__ __forceinline__ f32x2 act(f32x2 z) {
@@ -268,7 +268,8 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_apply_kernel(const __grid_co
     using W = ClWord<DT, VEC>;
     constexpr int ES = elem_size(DT), NL = L::N;
     extern __shared__ uint4 shared4[];
-    float2* const stats = reinterpret_cast<float2*>(shared4);  // [G]
+    using Stream = ClStream<DT, VEC, 1, DEPTH>;
+    float2* const stats = reinterpret_cast<float2*>(shared4 + Stream::SMEM / 16);  // [G]
     const int C = (int)p.C, K = C / p.G;
     int pt = 0;
     while (pt + 1 < p.P && (int)blockIdx.x >= p.start[pt + 1]) ++pt;
@@ -282,7 +283,16 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_apply_kernel(const __grid_co
     int64_t a, b;
     cl_piece((run.chunks + p.period - 1) / p.period, piece, p.parts[pt], a, b);
     const ClWalk w = cl_walk(q, a, b, p.period, run.chunks);
+    // from the end of the run: the statistics left that in L2
+    const int64_t last = from + (w.at + (w.count - 1) * w.stride) * (int64_t)sizeof(W);
+    Stream in;
+    in.base[0] = patch;
+    in.at[0] = patch + last;
+    in.stride = -w.stride * (int64_t)sizeof(W);
+    in.bytes = bytes;
+    in.status = p.status;
     grid_wait();
+    in.start(w.count, shared4);
     // this thread's channels
     float fm[VEC], fa[VEC], fb[VEC];
 #pragma unroll
@@ -303,24 +313,20 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_apply_kernel(const __grid_co
     cl_lanes<VEC>(fm, mean);
     cl_lanes<VEC>(fa, ga);
     cl_lanes<VEC>(fb, be);
-    // from the end of the run: the statistics left that in L2
-    const W* const base = reinterpret_cast<const W*>(patch + from) + w.at;
-    W* const to = reinterpret_cast<W*>(out + from) + w.at;
-    for (int s = w.count - 1; s >= 0; s -= AU) {
-        W v[AU];
+    char* to = out + last;
+    for (int s = 0; s < w.count; s += DEPTH) {
 #pragma unroll
-        for (int r = 0; r < AU; ++r)
-            if (s - r >= 0 && in_bounds(base + (s - r) * w.stride, sizeof(W), patch, bytes, p.status))
-                v[r] = __ldcs(base + (s - r) * w.stride);
-#pragma unroll
-        for (int r = 0; r < AU; ++r) {
-            if (s - r >= 0) {
+        for (int r = 0; r < DEPTH; ++r) {
+            if (s + r < w.count) {
+                W v[1];
+                in.step(r, v);
                 typename L::T f[NL];
-                to_lanes<DT, VEC>(v[r], f);
+                to_lanes<DT, VEC>(v[0], f);
 #pragma unroll
                 for (int i = 0; i < NL; ++i) f[i] = act<SILU>(vfma(vsub(f[i], mean[i]), ga[i], be[i]));
-                if (in_bounds(to + (s - r) * w.stride, sizeof(W), out, bytes, p.status))
-                    __stcs(to + (s - r) * w.stride, from_lanes<DT, VEC>(f));
+                if (in_bounds(to, sizeof(W), out, bytes, p.status))
+                    __stcs(reinterpret_cast<W*>(to), from_lanes<DT, VEC>(f));
+                to += in.stride;
             }
         }
     }
@@ -344,7 +350,7 @@ cudaError_t stats_launch(const GnClParams& p, bool vector, int64_t ctas, cudaStr
     constexpr int V = 16 / elem_size(DT);
     void (*const fn)(const GnClParams) = vector ? gncl_stats_kernel<DT, V> : gncl_stats_kernel<DT, 1>;
     return launch_cluster(fn, p, dim3((unsigned)ctas, (unsigned)p.splits, 1), p.cluster,
-                          stats_smem(vector ? V : 1, p.G / p.splits), s);
+                          vector ? stats_smem<DT, V>(p.G / p.splits) : stats_smem<DT, 1>(p.G / p.splits), s);
 }
 
 template <int DT>
@@ -354,7 +360,7 @@ cudaError_t apply_launch(const GnClParams& p, bool vector, int64_t ctas, cudaStr
         vector ? (p.silu ? gncl_apply_kernel<DT, V, true> : gncl_apply_kernel<DT, V, false>)
                : (p.silu ? gncl_apply_kernel<DT, 1, true> : gncl_apply_kernel<DT, 1, false>);
     const unsigned slabs = (unsigned)((p.period + p.columns - 1) / p.columns);
-    return launch_cluster(fn, p, dim3((unsigned)ctas, slabs, 1), 1, (size_t)p.G * sizeof(float2), s);
+    return launch_cluster(fn, p, dim3((unsigned)ctas, slabs, 1), 1, (vector ? ClStream<DT, V, 1, DEPTH>::SMEM : 0) + (size_t)p.G * sizeof(float2), s);
 }
 
 }  // namespace

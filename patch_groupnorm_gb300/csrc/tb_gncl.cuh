@@ -19,6 +19,10 @@
 
 namespace tb {
 
+// A chunk as it is loaded.
+template <int DT, int VEC>
+using ClWord = typename Word<VEC * elem_size(DT)>::T;
+
 // One sample of one patch.
 struct ClRun {
     int64_t first;   // its first element, counted in the patch
@@ -88,6 +92,66 @@ __device__ __forceinline__ void cl_piece(int64_t rows, int i, int pieces, int64_
 }
 
 __device__ __forceinline__ int cl_channel(int head, int phase, int C) { return (head + phase) % C; }
+
+// --- a thread's chunks, in flight ahead of their use --------------------------------
+
+// NS tensors' chunks of one walk: DEPTH - 1 of each are on their way while one is in
+// work.  16-byte chunks go through the thread's own slots in shared memory
+// (cp.async: no registers are held, no barrier is needed), single elements through
+// registers.  A slot is filled again only one step after its chunk was read, when
+// that chunk's values are in use.  step() is called with r = the step modulo DEPTH,
+// a constant once the caller's loop is unrolled.
+template <int DT, int VEC, int NS, int DEPTH>
+struct ClStream {
+    using W = ClWord<DT, VEC>;
+    static constexpr size_t SMEM = VEC > 1 ? (size_t)DEPTH * NS * CL_BLOCK * 16 : 0;
+    const char* at[NS];
+    const char* base[NS];
+    int64_t stride, bytes;  // from chunk to chunk; of a tensor (bounds-checked build)
+    int32_t left;           // chunks still to fetch
+    uint32_t slot;          // shared address of this thread's first slot
+    uint32_t* status;
+    W reg[VEC > 1 ? 1 : DEPTH][NS];
+
+    __device__ __forceinline__ void fetch(int r) {
+        if (left > 0) {
+#pragma unroll
+            for (int k = 0; k < NS; ++k) {
+                if (in_bounds(at[k], sizeof(W), base[k], bytes, status)) {
+                    if constexpr (VEC > 1) {
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                         slot + (uint32_t)((r * NS + k) * CL_BLOCK * 16)),
+                                     "l"(at[k])
+                                     : "memory");
+                    } else {
+                        reg[r][k] = __ldg(reinterpret_cast<const W*>(at[k]));
+                    }
+                }
+                at[k] += stride;
+            }
+        }
+        --left;
+        if constexpr (VEC > 1) asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    __device__ __forceinline__ void start(int count, void* ring) {
+        left = count;
+        slot = smem_addr(ring) + threadIdx.x * 16;
+#pragma unroll
+        for (int r = 0; r < DEPTH - 1; ++r) fetch(r);
+    }
+    __device__ __forceinline__ void step(int r, W (&v)[NS]) {
+        if constexpr (VEC > 1) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 2) : "memory");
+            fetch((r + DEPTH - 1) % DEPTH);
+#pragma unroll
+            for (int k = 0; k < NS; ++k) v[k] = smem_load<W>(slot + (uint32_t)((r * NS + k) * CL_BLOCK * 16));
+        } else {
+#pragma unroll
+            for (int k = 0; k < NS; ++k) v[k] = reg[r][k];
+            fetch((r + DEPTH - 1) % DEPTH);
+        }
+    }
+};
 
 // --- thread-block clusters ------------------------------------------------------
 
@@ -198,10 +262,6 @@ __device__ __forceinline__ void cl_group_stats(const GnClParams& p, int64_t n, i
     }
 }
 
-// A chunk as it is loaded.
-template <int DT, int VEC>
-using ClWord = typename Word<VEC * elem_size(DT)>::T;
-
 // VEC values of a thread's channels as lanes.
 template <int VEC>
 __device__ __forceinline__ void cl_lanes(const float (&f)[VEC], typename Lanes<VEC>::T (&l)[Lanes<VEC>::N]) {
@@ -237,7 +297,7 @@ __device__ __forceinline__ void cl_store_elem(void* base, int64_t i, float v) {
 // Shared memory of the largest call (CL_MAXC channels in as many groups).  A kernel
 // that needs more than the default is given this limit whatever the call's size:
 // calls of other threads may set it between this one's two steps.
-constexpr int CL_MAX_SMEM = 160 * 1024;
+constexpr int CL_MAX_SMEM = 216 * 1024;
 
 // Launches `fn` with programmatic stream serialisation in clusters of `cluster` CTAs.
 inline cudaError_t launch_cluster(void (*fn)(const GnClParams), const GnClParams& p, dim3 grid, int cluster, size_t smem,

@@ -43,8 +43,8 @@ __device__ __forceinline__ float dz_of(float dy, float z) {
 
 // --- the records ------------------------------------------------------------------
 
-constexpr int FOLD = 64;  // chunks between two foldings of a thread's sums
-constexpr int GU = 2;     // chunks of x and of dy a thread loads together
+constexpr int FOLD = 60;  // chunks between two foldings of a thread's sums: whole turns of DEPTH
+constexpr int DEPTH = 6;  // chunks of x and of dy of a thread on their way or in work
 
 template <int DT, int VEC, bool SILU>
 __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_stats_kernel(const __grid_constant__ GnClParams p) {
@@ -54,7 +54,8 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_stats_kernel(const __gr
     extern __shared__ uint4 shared4[];
     const int C = (int)p.C, K = C / p.G;
     const int cs = C / p.splits, c0 = (int)blockIdx.y * cs;  // this CTA's channels
-    float2* const stage = reinterpret_cast<float2*>(shared4);  // [CL_BLOCK * VEC]: (sum dz, sum dz * d)
+    using Stream = ClStream<DT, VEC, 2, DEPTH>;
+    float2* const stage = reinterpret_cast<float2*>(shared4 + Stream::SMEM / 16);  // [CL_BLOCK * VEC]: (sum dz, sum dz * d)
     float2* const table = stage + CL_BLOCK * VEC;              // [cs]: (sum dz, sum dz * xhat)
     float2* const stats = table + cs;                          // groups of those channels: (mean, rstd)
     const int g0 = c0 / K, g1 = (c0 + cs + K - 1) / K;
@@ -67,11 +68,25 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_stats_kernel(const __gr
     const int64_t bytes = p.N * run.elems * ES, from = (run.first + run.head) * ES;
     int64_t a, b;
     cl_piece((run.chunks + p.period - 1) / p.period, piece, pieces, a, b);
+    const int split_width = p.period / p.splits, split0 = (int)blockIdx.y * split_width;
+    Stream in;
+    in.base[0] = patch;
+    in.base[1] = grad;
+    in.bytes = bytes;
+    in.status = p.status;
+    auto begin = [&](const ClWalk& w) {
+        const int64_t at = from + w.at * (int64_t)sizeof(W);
+        in.at[0] = patch + at;
+        in.at[1] = grad + at;
+        in.stride = w.stride * (int64_t)sizeof(W);
+        in.start(w.count, shared4);
+    };
     grid_wait();
+    // the first columns' chunks are on their way while the groups' statistics are found
+    begin(cl_walk(cl_place(split0, min(split0 + p.columns, split0 + split_width)), a, b, p.period, run.chunks));
     cl_group_stats(p, u.n, g0, g1, stats);
     __syncthreads();
 
-    const int split_width = p.period / p.splits, split0 = (int)blockIdx.y * split_width;
     for (int j0 = split0; j0 < split0 + split_width; j0 += p.columns) {
         const int j1 = min(j0 + p.columns, split0 + split_width);
         const ClPlace q = cl_place(j0, j1);
@@ -91,30 +106,20 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_stats_kernel(const __gr
         cl_lanes<VEC>(f2, be);
 #pragma unroll
         for (int i = 0; i < NL; ++i) tb_[i] = ta[i] = L::splat(0.f);
-        const W* ax = reinterpret_cast<const W*>(patch + from) + w.at;
-        const W* ad = reinterpret_cast<const W*>(grad + from) + w.at;
+        if (j0 != split0) begin(w);
         for (int done = 0; done < w.count; done += FOLD) {
             const int now = min(FOLD, w.count - done);
 #pragma unroll
             for (int i = 0; i < NL; ++i) sb[i] = sa[i] = L::splat(0.f);
-            for (int s = 0; s < now; s += GU) {
-                W x[GU], y[GU];
+            for (int s = 0; s < now; s += DEPTH) {
 #pragma unroll
-                for (int r = 0; r < GU; ++r) {
-                    if (s + r < now && in_bounds(ax + r * w.stride, sizeof(W), patch, bytes, p.status) &&
-                        in_bounds(ad + r * w.stride, sizeof(W), grad, bytes, p.status)) {
-                        x[r] = __ldg(ax + r * w.stride);
-                        y[r] = __ldg(ad + r * w.stride);
-                    }
-                }
-                ax += GU * w.stride;
-                ad += GU * w.stride;
-#pragma unroll
-                for (int r = 0; r < GU; ++r) {
+                for (int r = 0; r < DEPTH; ++r) {
                     if (s + r < now) {
+                        W v[2];
+                        in.step(r, v);
                         typename L::T f[NL], dy[NL];
-                        to_lanes<DT, VEC>(x[r], f);
-                        to_lanes<DT, VEC>(y[r], dy);
+                        to_lanes<DT, VEC>(v[0], f);
+                        to_lanes<DT, VEC>(v[1], dy);
 #pragma unroll
                         for (int i = 0; i < NL; ++i) {
                             const typename L::T d = vsub(f[i], mean[i]);
@@ -188,15 +193,17 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_stats_kernel(const __gr
     else __syncthreads();
     float2* const out = p.grad_partials + ((int64_t)u.p * p.N + u.n) * C * TB_GN_PARTS;
     for (int i = u.rank * CL_BLOCK + (int)threadIdx.x; i < cs; i += p.cluster * CL_BLOCK) {
-        float2 t = make_float2(0.f, 0.f);
-        for (int r = 0; r < p.cluster; ++r) {
-            if (r == u.rank) {
-                t.x += table[i].x;
-                t.y += table[i].y;
-            } else {
-                const uint2 v = cluster_load8(smem_addr(table + i), (uint32_t)r);
-                t.x += __uint_as_float(v.x);
-                t.y += __uint_as_float(v.y);
+        float2 t = table[i];
+        if (p.cluster > 1) {
+            t = make_float2(0.f, 0.f);
+            uint2 v[CL_MAX_CLUSTER];
+#pragma unroll
+            for (int r = 0; r < CL_MAX_CLUSTER; ++r)  // all on their way before the first sum
+                v[r] = r < p.cluster ? cluster_load8(smem_addr(table + i), (uint32_t)r) : make_uint2(0u, 0u);
+#pragma unroll
+            for (int r = 0; r < CL_MAX_CLUSTER; ++r) {
+                t.x += __uint_as_float(v[r].x);
+                t.y += __uint_as_float(v[r].y);
             }
         }
         float2* const at = out + (int64_t)(c0 + i) * TB_GN_PARTS;
@@ -210,9 +217,12 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_stats_kernel(const __gr
     if (p.cluster > 1) cluster_sync();  // nobody leaves while its table may be read
 }
 
-size_t grad_stats_smem(int vec, int64_t C, int G, int splits) {
+static_assert(FOLD % DEPTH == 0, "a fold ends a turn");
+
+template <int DT, int VEC>
+size_t grad_stats_smem(int64_t C, int G, int splits) {
     const int64_t cs = C / splits, K = C / G;
-    return (size_t)(CL_BLOCK * vec + cs + (cs + K - 1) / K + 1) * sizeof(float2);
+    return ClStream<DT, VEC, 2, DEPTH>::SMEM + (size_t)(CL_BLOCK * VEC + cs + (cs + K - 1) / K + 1) * sizeof(float2);
 }
 
 // --- the groups' constants and the weight gradients -----------------------------------
@@ -315,7 +325,19 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_apply_kernel(const __gr
     cl_piece((run.chunks + p.period - 1) / p.period, piece, p.parts[pt], a, b);
     const ClWalk w = cl_walk(q, a, b, p.period, run.chunks);
     const float4* const coefs = p.coefs + (int64_t)n * p.G;
+    // from the end of the run: the records' pass left that in L2
+    const int64_t last = from + (w.at + (w.count - 1) * w.stride) * (int64_t)sizeof(W);
+    extern __shared__ uint4 shared4[];
+    ClStream<DT, VEC, 2, DEPTH> in;
+    in.base[0] = patch;
+    in.base[1] = grad;
+    in.at[0] = patch + last;
+    in.at[1] = grad + last;
+    in.stride = -w.stride * (int64_t)sizeof(W);
+    in.bytes = bytes;
+    in.status = p.status;
     grid_wait();
+    in.start(w.count, shared4);
     typename L::T mean[NL], ga[NL], be[NL], cu[NL], cv[NL];
     {
         float f0[VEC], f1[VEC], f2[VEC], f3[VEC], f4[VEC];
@@ -335,34 +357,25 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_apply_kernel(const __gr
         cl_lanes<VEC>(f3, cu);
         cl_lanes<VEC>(f4, cv);
     }
-    // from the end of the run: the records' pass left that in L2
-    const W* const bx = reinterpret_cast<const W*>(patch + from) + w.at;
-    const W* const bd = reinterpret_cast<const W*>(grad + from) + w.at;
-    W* const to = reinterpret_cast<W*>(out + from) + w.at;
-    for (int s = w.count - 1; s >= 0; s -= GU) {
-        W x[GU], y[GU];
+    char* to = out + last;
+    for (int s = 0; s < w.count; s += DEPTH) {
 #pragma unroll
-        for (int r = 0; r < GU; ++r) {
-            if (s - r >= 0 && in_bounds(bx + (s - r) * w.stride, sizeof(W), patch, bytes, p.status) &&
-                in_bounds(bd + (s - r) * w.stride, sizeof(W), grad, bytes, p.status)) {
-                x[r] = __ldcs(bx + (s - r) * w.stride);
-                y[r] = __ldcs(bd + (s - r) * w.stride);
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < GU; ++r) {
-            if (s - r >= 0) {
+        for (int r = 0; r < DEPTH; ++r) {
+            if (s + r < w.count) {
+                W v[2];
+                in.step(r, v);
                 typename L::T f[NL], dy[NL];
-                to_lanes<DT, VEC>(x[r], f);
-                to_lanes<DT, VEC>(y[r], dy);
+                to_lanes<DT, VEC>(v[0], f);
+                to_lanes<DT, VEC>(v[1], dy);
 #pragma unroll
                 for (int i = 0; i < NL; ++i) {
                     const typename L::T d = vsub(f[i], mean[i]);
                     const typename L::T dz = dz_of<SILU>(dy[i], vfma(d, ga[i], be[i]));
                     f[i] = vfma(dz, ga[i], vfma(d, cu[i], cv[i]));
                 }
-                if (in_bounds(to + (s - r) * w.stride, sizeof(W), out, bytes, p.status))
-                    __stcs(to + (s - r) * w.stride, from_lanes<DT, VEC>(f));
+                if (in_bounds(to, sizeof(W), out, bytes, p.status))
+                    __stcs(reinterpret_cast<W*>(to), from_lanes<DT, VEC>(f));
+                to += in.stride;
             }
         }
     }
@@ -390,7 +403,7 @@ cudaError_t stats_launch(const GnClParams& p, bool vector, int64_t ctas, cudaStr
         vector ? (p.silu ? gncl_grad_stats_kernel<DT, V, true> : gncl_grad_stats_kernel<DT, V, false>)
                : (p.silu ? gncl_grad_stats_kernel<DT, 1, true> : gncl_grad_stats_kernel<DT, 1, false>);
     return launch_cluster(fn, p, dim3((unsigned)ctas, (unsigned)p.splits, 1), p.cluster,
-                          grad_stats_smem(vector ? V : 1, p.C, p.G, p.splits), s);
+                          vector ? grad_stats_smem<DT, V>(p.C, p.G, p.splits) : grad_stats_smem<DT, 1>(p.C, p.G, p.splits), s);
 }
 
 template <int DT>
@@ -400,7 +413,7 @@ cudaError_t apply_launch(const GnClParams& p, bool vector, int64_t ctas, cudaStr
         vector ? (p.silu ? gncl_grad_apply_kernel<DT, V, true> : gncl_grad_apply_kernel<DT, V, false>)
                : (p.silu ? gncl_grad_apply_kernel<DT, 1, true> : gncl_grad_apply_kernel<DT, 1, false>);
     const unsigned slabs = (unsigned)((p.period + p.columns - 1) / p.columns);
-    return launch_cluster(fn, p, dim3((unsigned)ctas, slabs, 1), 1, 0, s);
+    return launch_cluster(fn, p, dim3((unsigned)ctas, slabs, 1), 1, vector ? ClStream<DT, V, 2, DEPTH>::SMEM : 0, s);
 }
 
 }  // namespace

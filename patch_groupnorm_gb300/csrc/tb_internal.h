@@ -472,6 +472,7 @@ cudaError_t launch_gn_grad(const GnGradParams& p, int dtype, bool ring, int sms,
 // ---------------------------------------------------------------------------
 
 constexpr int CL_BLOCK = 256;          // threads per CTA
+constexpr int CL_MAX_CLUSTER = 8;     // CTAs of a statistics cluster
 constexpr int CL_MAXC = TB_GN_CL_MAX_CHANNELS;
 
 // Chunks, columns, rows and periods: see tb_gncl.cuh.

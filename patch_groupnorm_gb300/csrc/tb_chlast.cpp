@@ -96,37 +96,55 @@ int64_t cl_rows(const tb::GnClParams& prm, int p, int vec) {
 }
 
 // Statistics: every (patch, sample) is a unit, cut into up to TB_GN_PARTS records
-// of a cluster of up to 8 CTAs each; where that leaves SMs idle, the channels are
-// split too, into runs of whole groups of at least 256 bytes a position.
+// of a cluster each; the channels may be split too, into runs of whole groups of at
+// least 256 bytes a position.  Of the ways to cut, the one that comes nearest to the
+// CTAs wanted (those resident at once), and of equals the one with the fewest splits,
+// then the smallest clusters.  A cluster's CTAs have to find their places in one
+// group of SMs: of 304 places (two on each SM) clusters of 1 and 2 take all, of 3 to 5
+// 290 to 296, of 6 to 8 266 to 288 (the runtime's own count).
 void cl_plan_stats(tb::GnClParams& prm, tb_dtype dtype, bool vector, int ctas_wanted, int64_t* ctas) {
     const int es = elem_bytes(dtype), vec = vector ? 16 / es : 1;
     bool whole = prm.C % vec == 0;
     for (int p = 0; p < prm.P; ++p) whole = whole && (vec == 1 || aligned(prm.patches[p], 16));
-    const int64_t units = prm.N * prm.P;
-    int splits = 1;
-    while (units * splits * TB_GN_PARTS * tb::CL_MAX_CLUSTER < ctas_wanted && whole && prm.G % (splits * 2) == 0 &&
-           (prm.C / (splits * 2)) % vec == 0 && prm.C / (splits * 2) * es >= 256)
-        splits *= 2;
+    int64_t rows[tb::GN_MAXP], most = 1;
+    for (int p = 0; p < prm.P; ++p) {
+        rows[p] = cl_rows(prm, p, vec);
+        most = std::max(most, rows[p]);
+    }
+    int64_t best = 0;
+    int32_t splits = 1, cluster = 1, parts = 1;
+    for (int s = 1; s <= 16; s *= 2) {
+        if (s > 1 && !(whole && prm.G % s == 0 && (prm.C / s) % vec == 0 && prm.C / s * es >= 256)) break;
+        const int64_t columns = std::min<int64_t>(prm.period / s, tb::CL_BLOCK);
+        // at least four turns of a CTA's threads each
+        const int64_t useful = std::max<int64_t>(1, most / (tb::CL_BLOCK / columns * 4));
+        for (int c = 1; c <= tb::CL_MAX_CLUSTER; ++c) {
+            const double places = (c <= 2 ? 1.0 : c <= 5 ? 0.95 : 0.87) * ctas_wanted;
+            for (int k = 1; k <= TB_GN_PARTS; ++k) {
+                if (c * k > useful && c * k > 1) continue;
+                int64_t total = 0;
+                for (int p = 0; p < prm.P; ++p) total += std::max<int64_t>(1, (rows[p] * k + most / 2) / most);
+                total *= prm.N * c * s;
+                if (total <= best || ((double)total > places && best > 0)) continue;
+                best = total;
+                splits = s;
+                cluster = c;
+                parts = k;
+            }
+        }
+    }
     prm.splits = splits;
+    prm.cluster = cluster;
     const int width = prm.period / splits, turns = (width + tb::CL_BLOCK - 1) / tb::CL_BLOCK;
     prm.columns = (width + turns - 1) / turns;
-    int64_t most = 1;
-    for (int p = 0; p < prm.P; ++p) most = std::max(most, cl_rows(prm, p, vec));
-    // at least four turns of a CTA's threads each
-    const int64_t side = std::max(1, tb::CL_BLOCK / prm.columns);
-    const int64_t useful = std::max<int64_t>(1, most / (side * 4));
-    const int64_t each = std::min(useful, std::max<int64_t>(1, ctas_wanted / (units * splits)));
-    const int64_t parts = std::min<int64_t>(TB_GN_PARTS, each);
-    prm.cluster = (int32_t)std::max<int64_t>(1, std::min<int64_t>(tb::CL_MAX_CLUSTER, each / parts));
     int64_t at = 0;
     for (int p = 0; p < prm.P; ++p) {
-        const int64_t share = (cl_rows(prm, p, vec) * parts + most / 2) / most;
-        prm.parts[p] = (int32_t)std::min<int64_t>(TB_GN_PARTS, std::max<int64_t>(1, share));
+        prm.parts[p] = (int32_t)std::max<int64_t>(1, (rows[p] * parts + most / 2) / most);
         prm.start[p] = (int32_t)at;
         at += prm.N * prm.parts[p];
     }
     prm.start[prm.P] = (int32_t)at;
-    *ctas = at * prm.cluster;
+    *ctas = at * cluster;
 }
 
 // Element-wise passes: runs of rows of about the same length, as many as are

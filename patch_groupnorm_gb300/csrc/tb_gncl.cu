@@ -14,18 +14,6 @@ namespace {
 
 // --- statistics -------------------------------------------------------------------
 
-// (n, mean, M2) joined with (bn, bmean, bm2), Chan's way.  Counts are floats, exact up
-// to 2^24 elements: they weigh means and squares here; a record's own count comes
-// from the sizes.
-__device__ __forceinline__ void chan(float& n, float& mean, float& m2, float bn, float bmean, float bm2) {
-    const float total = n + bn;
-    const float f = bn > 0.f ? __fdividef(bn, total) : 0.f;  // 1, exactly, where n is 0
-    const float d = n > 0.f && bn > 0.f ? bmean - mean : 0.f;
-    mean = n > 0.f ? fmaf(d, f, mean) : bmean;
-    m2 += fmaf(d * d, n * f, bn > 0.f ? bm2 : 0.f);
-    n = total;
-}
-
 constexpr int FOLD = 64;  // chunks between two foldings of a thread's sums
 constexpr int DEPTH = 8;  // chunks of a thread on their way or in work
 
@@ -295,19 +283,16 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_apply_kernel(const __grid_co
     in.start(w.count, shared4);
     // this thread's channels
     float fm[VEC], fa[VEC], fb[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        const int c = cl_channel(run.head, q.col * VEC + i, C);
-        fa[i] = weight_at(p.gamma, DT, c, 1.f);
-        fb[i] = weight_at(p.beta, DT, c, 0.f);
-    }
+    cl_weights<DT, VEC>(p, run.head, q.col * VEC, fa, fb);
     cl_group_stats(p, n, 0, p.G, stats);
     __syncthreads();
+    ClChannel ch(run.head, q.col * VEC, C, K);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-        const float2 s = stats[cl_channel(run.head, q.col * VEC + i, C) / K];
+        const float2 s = stats[ch.g];
         fm[i] = s.x;
         fa[i] *= s.y;
+        ch.next();
     }
     typename L::T mean[NL], ga[NL], be[NL];
     cl_lanes<VEC>(fm, mean);

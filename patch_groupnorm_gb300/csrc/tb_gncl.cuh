@@ -91,8 +91,6 @@ __device__ __forceinline__ void cl_piece(int64_t rows, int i, int pieces, int64_
     b = rows * (i + 1) / pieces;
 }
 
-__device__ __forceinline__ int cl_channel(int head, int phase, int C) { return (head + phase) % C; }
-
 // --- a thread's chunks, in flight ahead of their use --------------------------------
 
 // NS tensors' chunks of one walk: DEPTH - 1 of each are on their way while one is in
@@ -186,78 +184,91 @@ __device__ __forceinline__ ClUnit cl_unit(const GnClParams& prm) {
     return u;
 }
 
-// (mean, rstd) of groups [g0, g1) of sample n into out[0 .. g1 - g0), a group per
-// warp at a time: each record (count c, mean m, M2) adds c, c * (m - K) and
-// M2 + c * (m - K)^2 to sums about K, the mean of the first record with elements,
-// as the channels-first kernels pool them; unlike there, a NaN stays one.  Four
-// groups' records (32 of them: a load per lane) are on their way together, since a
-// wait for one group after the other would hold the CTA up for microseconds.
+// (n, mean, M2) joined with (bn, bmean, bm2), Chan's way.  Counts are floats, exact up
+// to 2^24 elements: they weigh means and squares here; a record's own count comes
+// from the sizes.
+__device__ __forceinline__ void chan(float& n, float& mean, float& m2, float bn, float bmean, float bm2) {
+    const float total = n + bn;
+    const float f = bn > 0.f ? __fdividef(bn, total) : 0.f;  // 1, exactly, where n is 0
+    const float d = n > 0.f && bn > 0.f ? bmean - mean : 0.f;
+    mean = n > 0.f ? fmaf(d, f, mean) : bmean;
+    m2 += fmaf(d * d, n * f, bn > 0.f ? bm2 : 0.f);
+    n = total;
+}
+
+// (mean, rstd, count) of groups [g0, g1) of sample n into out[0 .. g1 - g0): eight
+// threads to a group, four of whose record sets are on their way at once (a wait for
+// one after the other would hold the CTA up for microseconds).  A NaN stays one.
 __device__ __forceinline__ void cl_group_stats(const GnClParams& p, int64_t n, int g0, int g1, float2* out) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = (int)blockDim.x >> 5;
-    const int total = p.R * TB_GN_PARTS;
+    static_assert(TB_GN_PARTS == 8, "a thread takes one part of every set");
     constexpr int B = 4;
-    auto record = [&](int g, int q, long long& c, float& m, float& m2) {
-        c = 0;
-        m = m2 = 0.f;
-        if (g >= g1 || q >= total) return;
-        const GnPartial* const at = p.partials + (((int64_t)(q / TB_GN_PARTS) * p.N + n) * p.G + g) * TB_GN_PARTS +
-                                    q % TB_GN_PARTS;
-        if (!in_bounds(at, sizeof(GnPartial), p.partials,
-                       (int64_t)p.R * p.N * p.G * TB_GN_PARTS * (int64_t)sizeof(GnPartial), p.status))
-            return;
-        const longlong2 raw = __ldg(reinterpret_cast<const longlong2*>(at));
-        c = raw.x;
-        m = __int_as_float((int)(raw.y & 0xffffffffLL));
-        m2 = __int_as_float((int)(raw.y >> 32));
-    };
-    for (int first = g0 + warp; first < g1; first += warps * B) {
-        long long c[B];
-        float m[B], m2[B];
+    const int part = threadIdx.x & 7, teams = (int)blockDim.x >> 3;
+    const int64_t set = p.N * p.G * TB_GN_PARTS;
+    for (int first = g0; first < g1; first += teams) {
+        const int g = first + ((int)threadIdx.x >> 3);
+        const GnPartial* const unit = p.partials + (n * p.G + g) * TB_GN_PARTS + part;
+        float c = 0.f, m = 0.f, m2 = 0.f;
+        for (int r0 = 0; r0 < p.R; r0 += B) {
+            longlong2 raw[B];
 #pragma unroll
-        for (int k = 0; k < B; ++k) record(first + k * warps, lane, c[k], m[k], m2[k]);
-#pragma unroll
-        for (int k = 0; k < B; ++k) {
-            const int g = first + k * warps;
-            if (g >= g1) break;
-            unsigned has = __ballot_sync(0xffffffffu, c[k] > 0);
-            float K = has ? __shfl_sync(0xffffffffu, m[k], __ffs(has) - 1) : 0.f;
-            for (int base = 32; has == 0u && base < total; base += 32) {
-                long long oc;
-                float om, o2;
-                record(g, base + lane, oc, om, o2);
-                has = __ballot_sync(0xffffffffu, oc > 0);
-                if (has) K = __shfl_sync(0xffffffffu, om, __ffs(has) - 1);
-            }
-            long long sn = 0;
-            float s1 = 0.f, s2 = 0.f;
-            auto add = [&](long long rc, float rm, float r2) {
-                if (rc > 0) {
-                    const float cf = (float)rc, d = rm - K;
-                    sn += rc;
-                    s1 = fmaf(cf, d, s1);
-                    s2 += fmaf(cf * d, d, r2);
-                }
-            };
-            add(c[k], m[k], m2[k]);
-            for (int q = 32 + lane; q < total; q += 32) {
-                long long oc;
-                float om, o2;
-                record(g, q, oc, om, o2);
-                add(oc, om, o2);
+            for (int k = 0; k < B; ++k) {
+                const GnPartial* const at = unit + (r0 + k) * set;
+                raw[k] = make_longlong2(0, 0);
+                if (g < g1 && r0 + k < p.R &&
+                    in_bounds(at, sizeof(GnPartial), p.partials, p.R * set * (int64_t)sizeof(GnPartial), p.status))
+                    raw[k] = __ldg(reinterpret_cast<const longlong2*>(at));
             }
 #pragma unroll
-            for (int delta = 16; delta >= 1; delta >>= 1) {  // fixed order: deterministic
-                sn += __shfl_down_sync(0xffffffffu, sn, delta);
-                s1 += __shfl_down_sync(0xffffffffu, s1, delta);
-                s2 += __shfl_down_sync(0xffffffffu, s2, delta);
-            }
-            if (lane == 0) {
-                const float nf = (float)sn;
-                const float q1 = sn > 0 ? s1 / nf : 0.f;
-                float var = sn > 0 ? fmaf(-s1, q1, s2) / nf : 0.f;  // biased: divided by the count
-                if (var < 0.f) var = 0.f;
-                out[g - g0] = make_float2(K + q1, 1.0f / sqrtf(var + p.eps));
-            }
+            for (int k = 0; k < B; ++k)
+                chan(c, m, m2, (float)raw[k].x, __int_as_float((int)(raw[k].y & 0xffffffffLL)),
+                     __int_as_float((int)(raw[k].y >> 32)));
+        }
+#pragma unroll
+        for (int d = 4; d >= 1; d >>= 1) {
+            const float bc = __shfl_down_sync(0xffffffffu, c, d), bm = __shfl_down_sync(0xffffffffu, m, d);
+            chan(c, m, m2, bc, bm, __shfl_down_sync(0xffffffffu, m2, d));
+        }
+        if (g < g1 && part == 0) {
+            const float var = c > 0.f ? m2 / c : 0.f;  // biased: divided by the count
+            out[g - g0] = make_float2(m, 1.0f / sqrtf(var + p.eps));
+        }
+    }
+}
+
+// A thread's channels, one after the other: the channel and its group.
+struct ClChannel {
+    int c, g, k;  // channel, group, place in the group
+    int C, K;
+    __device__ __forceinline__ ClChannel(int head, int phase, int C_, int K_) : C(C_), K(K_) {
+        c = (head + phase) % C;
+        g = c / K;
+        k = c - g * K;
+    }
+    __device__ __forceinline__ void next() {
+        ++c;
+        if (++k == K) {
+            k = 0;
+            ++g;
+        }
+        if (c == C) c = g = 0;
+    }
+};
+
+// gamma and beta of a thread's VEC channels: one load each where they lie together.
+template <int DT, int VEC>
+__device__ __forceinline__ void cl_weights(const GnClParams& p, int head, int phase, float (&ga)[VEC], float (&be)[VEC]) {
+    const int c0 = (head + phase) % (int)p.C;
+    if (VEC > 1 && c0 % VEC == 0 && c0 + VEC <= p.C &&
+        ((reinterpret_cast<uintptr_t>(p.gamma) | reinterpret_cast<uintptr_t>(p.beta)) & 15u) == 0) {
+        weights_at<VEC>(p.gamma, DT, c0, 1.f, ga);
+        weights_at<VEC>(p.beta, DT, c0, 0.f, be);
+    } else {
+        ClChannel ch(head, phase, (int)p.C, 1);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            ga[i] = weight_at(p.gamma, DT, ch.c, 1.f);
+            be[i] = weight_at(p.beta, DT, ch.c, 0.f);
+            ch.next();
         }
     }
 }

@@ -93,13 +93,16 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_stats_kernel(const __gr
         const ClWalk w = cl_walk(q, a, b, p.period, run.chunks);
         typename L::T mean[NL], ga[NL], be[NL], sb[NL], sa[NL], tb_[NL], ta[NL];
         float f0[VEC], f1[VEC], f2[VEC];
+        if constexpr (SILU) cl_weights<DT, VEC>(p, run.head, q.col * VEC, f1, f2);
+        ClChannel ch(run.head, q.col * VEC, C, K);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            const int c = cl_channel(run.head, q.col * VEC + i, C);
-            const float2 s = q.row >= 0 ? stats[c / K - g0] : make_float2(0.f, 0.f);
+            // threads without a place may point past this CTA's groups
+            const float2 s = q.row >= 0 ? stats[ch.g - g0] : make_float2(0.f, 0.f);
             f0[i] = s.x;
-            f1[i] = SILU && q.row >= 0 ? s.y * weight_at(p.gamma, DT, c, 1.f) : 0.f;
-            f2[i] = SILU && q.row >= 0 ? weight_at(p.beta, DT, c, 0.f) : 0.f;
+            f1[i] = SILU ? s.y * f1[i] : 0.f;
+            f2[i] = SILU ? f2[i] : 0.f;
+            ch.next();
         }
         cl_lanes<VEC>(f0, mean);
         cl_lanes<VEC>(f1, ga);
@@ -341,15 +344,16 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_apply_kernel(const __gr
     typename L::T mean[NL], ga[NL], be[NL], cu[NL], cv[NL];
     {
         float f0[VEC], f1[VEC], f2[VEC], f3[VEC], f4[VEC];
+        cl_weights<DT, VEC>(p, run.head, q.col * VEC, f1, f2);
+        ClChannel ch(run.head, q.col * VEC, C, K);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            const int c = cl_channel(run.head, q.col * VEC + i, C);
-            const float4 k = __ldg(coefs + c / K);
+            const float4 k = __ldg(coefs + ch.g);
             f0[i] = k.x;
-            f1[i] = k.y * weight_at(p.gamma, DT, c, 1.f);
-            f2[i] = weight_at(p.beta, DT, c, 0.f);
+            f1[i] *= k.y;
             f3[i] = k.z;
             f4[i] = k.w;
+            ch.next();
         }
         cl_lanes<VEC>(f0, mean);
         cl_lanes<VEC>(f1, ga);

@@ -102,7 +102,7 @@ int64_t cl_rows(const tb::GnClParams& prm, int p, int vec) {
 // then the smallest clusters.  A cluster's CTAs have to find their places in one
 // group of SMs: of 304 places (two on each SM) clusters of 1 and 2 take all, of 3 to 5
 // 290 to 296, of 6 to 8 266 to 288 (the runtime's own count).
-void cl_plan_stats(tb::GnClParams& prm, tb_dtype dtype, bool vector, int ctas_wanted, int64_t* ctas) {
+tb_status cl_plan_stats(tb::GnClParams& prm, tb_dtype dtype, bool vector, int ctas_wanted, int64_t* ctas) {
     const int es = elem_bytes(dtype), vec = vector ? 16 / es : 1;
     bool whole = prm.C % vec == 0;
     for (int p = 0; p < prm.P; ++p) whole = whole && (vec == 1 || aligned(prm.patches[p], 16));
@@ -142,9 +142,14 @@ void cl_plan_stats(tb::GnClParams& prm, tb_dtype dtype, bool vector, int ctas_wa
         prm.parts[p] = (int32_t)std::max<int64_t>(1, (rows[p] * parts + most / 2) / most);
         prm.start[p] = (int32_t)at;
         at += prm.N * prm.parts[p];
+        const int64_t pieces = (int64_t)prm.parts[p] * cluster;
+        if (rows[p] / pieces > 2000000000LL) return TB_ERR_UNSUPPORTED;  // past any memory
+        prm.share[p] = (int32_t)(rows[p] / pieces);
+        prm.extra[p] = (int32_t)(rows[p] % pieces);
     }
     prm.start[prm.P] = (int32_t)at;
     *ctas = at * cluster;
+    return TB_OK;
 }
 
 // Element-wise passes: runs of rows of about the same length, as many as are
@@ -179,21 +184,21 @@ void cl_plan_rows(tb::GnClParams& prm, tb_dtype dtype, bool vector, int ctas_wan
 tb_status cl_stats(tb::GnClParams& prm, tb_dtype dtype, int sms, cudaStream_t s) {
     const bool vector = cl_chunks(prm, dtype, false, false);
     int64_t ctas = 0;
-    cl_plan_stats(prm, dtype, vector, 2 * sms, &ctas);
+    TB_TRY(cl_plan_stats(prm, dtype, vector, 2 * sms, &ctas));
     return launched(tb::launch_gncl_stats(prm, (int)dtype, vector, ctas, s));
 }
 
 tb_status cl_apply(tb::GnClParams& prm, tb_dtype dtype, int sms, cudaStream_t s) {
     const bool vector = cl_chunks(prm, dtype, false, true);
     int64_t ctas = 0;
-    cl_plan_rows(prm, dtype, vector, 3 * sms, &ctas);
+    cl_plan_rows(prm, dtype, vector, 2 * sms, &ctas);
     return launched(tb::launch_gncl_apply(prm, (int)dtype, vector, ctas, s));
 }
 
 tb_status cl_grad_stats(tb::GnClParams& prm, tb_dtype dtype, int sms, cudaStream_t s) {
     const bool vector = cl_chunks(prm, dtype, true, false);
     int64_t ctas = 0;
-    cl_plan_stats(prm, dtype, vector, 2 * sms, &ctas);
+    TB_TRY(cl_plan_stats(prm, dtype, vector, 2 * sms, &ctas));
     return launched(tb::launch_gncl_grad_stats(prm, (int)dtype, vector, ctas, s));
 }
 

@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
     const int gs = G / p.splits, g0 = (int)blockIdx.y * gs, g1 = g0 + gs;  // this CTA's groups
     float4* const table = reinterpret_cast<float4*>(stage_n + CL_BLOCK);     // [gs]: (count, mean, M2)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int team = 32;  // threads that join a group's positions
+    int team = 32;  // threads that join a group's sums
     while (team > 1 && gs * team > CL_BLOCK) team /= 2;
     for (int i = threadIdx.x; i < gs; i += CL_BLOCK) table[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     const ClUnit u = cl_unit(p);
@@ -46,6 +46,8 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
     const ClRun run = cl_run<ES, VEC>(p.patches[u.p], p.spatial[u.p], p.C, u.n);
     const char* const patch = static_cast<const char*>(p.patches[u.p]);
     const int64_t bytes = p.N * run.elems * ES;
+    // channels that every chunk has side by side in one group: a power of two
+    const int unit = min(VEC, (K | run.head) & -(K | run.head));
     grid_wait();
 
     // elements outside the whole chunks: the first piece's before, the last one's after; a lane each
@@ -61,9 +63,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
         }
     }
 
-    const int64_t total_rows = (run.chunks + p.period - 1) / p.period;
-    int64_t a, b;
-    cl_piece(total_rows, piece, pieces, a, b);
+    const int64_t a = cl_first_row(p, u.p, piece), b = cl_first_row(p, u.p, piece + 1);
     const int split_width = p.period / p.splits, split0 = (int)blockIdx.y * split_width;
     for (int j0 = split0; j0 < split0 + split_width; j0 += p.columns) {
         const int j1 = min(j0 + p.columns, split0 + split_width);
@@ -83,27 +83,20 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
             now = min(min(FOLD, max(DEPTH, done)), w.count - done);
 #pragma unroll
             for (int i = 0; i < NL; ++i) s1[i] = s2[i] = L::splat(0.f);
-            for (int s = 0; s < now; s += DEPTH) {
+            cl_each(in, now, [&](const W (&v)[1], int j) {
+                typename L::T f[NL];
+                to_lanes<DT, VEC>(v[0], f);
+                if (done + j == 0) {
 #pragma unroll
-                for (int r = 0; r < DEPTH; ++r) {
-                    if (s + r < now) {
-                        W v[1];
-                        in.step(r, v);
-                        typename L::T f[NL];
-                        to_lanes<DT, VEC>(v[0], f);
-                        if (r == 0 && done + s == 0) {
-#pragma unroll
-                            for (int i = 0; i < NL; ++i) k[i] = mean[i] = f[i];
-                        }
-#pragma unroll
-                        for (int i = 0; i < NL; ++i) {
-                            const typename L::T d = vsub(f[i], k[i]);
-                            s1[i] = vadd(s1[i], d);
-                            s2[i] = vfma(d, d, s2[i]);
-                        }
-                    }
+                    for (int i = 0; i < NL; ++i) k[i] = mean[i] = f[i];
                 }
-            }
+#pragma unroll
+                for (int i = 0; i < NL; ++i) {
+                    const typename L::T d = vsub(f[i], k[i]);
+                    s1[i] = vadd(s1[i], d);
+                    s2[i] = vfma(d, d, s2[i]);
+                }
+            });
             // the sums of `now` chunks about k join those of `done` before
             const float nb = (float)now, total = (float)(done + now);
             const auto inv = L::splat(1.f / nb), f = L::splat(nb / total), g = L::splat((float)done * (nb / total));
@@ -117,41 +110,49 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
                 k[i] = mean[i];
             }
         }
-        // rounding may leave a tiny negative sum of squares: it is a zero one
         float fm[VEC], f2[VEC];
         cl_values<VEC>(mean, fm);
         cl_values<VEC>(m2, f2);
+        // rounding may leave a tiny negative sum of squares: it is a zero one
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) f2[i] = f2[i] < 0.f ? 0.f : f2[i];
+        // neighbours of one group are joined at once; their counts are equal
+#pragma unroll
+        for (int d = 1; d < VEC; d *= 2) {
+            if (d < unit) {
+                const float half = 0.5f * (float)(w.count * d);
+#pragma unroll
+                for (int i = 0; i < VEC; i += 2 * d) {
+                    const float away = fm[i + d] - fm[i];
+                    fm[i] = fmaf(0.5f, away, fm[i]);
+                    f2[i] = f2[i] + f2[i + d] + half * away * away;
+                }
+            }
+        }
         __syncthreads();  // the table is set, or the columns before these are merged
+        const int each = VEC / unit;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            stage_mean[threadIdx.x * VEC + i] = fm[i];
-            stage_m2[threadIdx.x * VEC + i] = f2[i] < 0.f ? 0.f : f2[i];
+            if (i % unit == 0) {
+                stage_mean[threadIdx.x * each + i / unit] = fm[i];
+                stage_m2[threadIdx.x * each + i / unit] = f2[i];
+            }
         }
-        stage_n[threadIdx.x] = w.count;
+        stage_n[threadIdx.x] = w.count * unit;
         __syncthreads();
-        // the rows side by side: a thread per position of the row
-        const int lo = run.head + j0 * VEC, hi = run.head + j1 * VEC, pitch = q.width * VEC;
-        for (int i = threadIdx.x; i < pitch; i += CL_BLOCK) {
-            float n = 0.f, mean_i = 0.f, m2_i = 0.f;
-            for (int r = 0; r < q.rows; ++r)
-                chan(n, mean_i, m2_i, (float)stage_n[r * q.width + i / VEC], stage_mean[r * pitch + i],
-                     stage_m2[r * pitch + i]);
-            stage_mean[i] = mean_i;
-            stage_m2[i] = m2_i;
-        }
-        __syncthreads();
-        // then the positions of each group, `team` threads to a group: its channels
-        // lie in phases [head + j0 * VEC, head + j1 * VEC), in runs of at most K
+        // The units of a row that are one group's lie in phases [head + j0 * VEC, head +
+        // j1 * VEC), in runs of at most K / unit.  `team` threads join those of all rows
+        const int lo = (run.head + j0 * VEC) / unit, hi = (run.head + j1 * VEC) / unit, pitch = q.width * each;
+        const int Ku = K / unit, Cu = C / unit;
         for (int first = 0; first < gs; first += CL_BLOCK / team) {
-            const int i = first + (int)threadIdx.x / team, c0 = (g0 + i) * K;
+            const int i = first + (int)threadIdx.x / team, c0 = (g0 + i) * Ku;
             float n = 0.f, mean_g = 0.f, m2_g = 0.f;
             if (i < gs) {
-                for (int m = lo >= c0 + K ? (lo - c0 - K) / C + 1 : 0; c0 + m * C < hi; ++m) {
-                    const int to = min(c0 + m * C + K, hi) - lo;
-                    for (int e = max(c0 + m * C, lo) - lo + (int)threadIdx.x % team; e < to; e += team) {
-                        int ne = 0;
-                        for (int r = 0; r < q.rows; ++r) ne += stage_n[r * q.width + e / VEC];
-                        chan(n, mean_g, m2_g, (float)ne, stage_mean[e], stage_m2[e]);
+                for (int m = lo >= c0 + Ku ? (lo - c0 - Ku) / Cu + 1 : 0; c0 + m * Cu < hi; ++m) {
+                    const int from = max(c0 + m * Cu, lo) - lo, len = min(c0 + m * Cu + Ku, hi) - lo - from;
+                    for (int e = (int)threadIdx.x % team; e < q.rows * len; e += team) {
+                        const int row = (int)((unsigned)e / (unsigned)len), at = row * pitch + from + (e - row * len);
+                        chan(n, mean_g, m2_g, (float)stage_n[(unsigned)at / (unsigned)each], stage_mean[at], stage_m2[at]);
                     }
                 }
             }
@@ -184,14 +185,10 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
     else __syncthreads();
     // the cluster's tables: eight threads to a group, one for each CTA
     static_assert(CL_MAX_CLUSTER == 8 && TB_GN_PARTS == 8, "eight threads read the CTAs' sums and write the parts");
-    int64_t row0, row1, none;
-    cl_piece(total_rows, u.part * p.cluster, pieces, row0, none);
-    cl_piece(total_rows, (u.part + 1) * p.cluster - 1, pieces, none, row1);
-    const int64_t wide = (int64_t)p.period * VEC;
-    const int64_t e0 = u.part == 0 ? 0 : run.head + row0 * wide;
-    const int64_t e1 = u.part == parts - 1 ? run.elems : run.head + row1 * wide;
-    // elements of channels c0 .. c0 + K - 1 among the first e
-    auto among = [&](int64_t e, int c0) { return e / C * K + min(max((int)(e % C) - c0, 0), K); };
+    // whole rows have reps * K elements of every group; the first part has the head's
+    // too, and the last one whatever the others leave
+    const int reps = (int)((unsigned)(p.period * VEC) / (unsigned)C);
+    const int64_t row0 = cl_first_row(p, u.p, u.part * p.cluster), row1 = cl_first_row(p, u.p, (u.part + 1) * p.cluster);
     GnPartial* const out = p.partials + ((int64_t)u.p * p.N + u.n) * G * TB_GN_PARTS;
     for (int first = 0; first < gs; first += p.cluster * (CL_BLOCK / 8)) {
         const int i = first + u.rank * (CL_BLOCK / 8) + (int)threadIdx.x / 8, r = threadIdx.x & 7;
@@ -219,7 +216,10 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
                        (int64_t)p.P * p.N * G * TB_GN_PARTS * (int64_t)sizeof(GnPartial), p.status))
             continue;
         const int c0 = (g0 + i) * K;
-        if (r == 0) at[u.part] = GnPartial{among(e1, c0) - among(e0, c0), mean, m2};
+        const int64_t ahead = min(max((run.head % C) - c0, 0), K) + (int64_t)(run.head / C) * K;
+        const int64_t e0 = u.part == 0 ? 0 : ahead + row0 * reps * K;
+        const int64_t e1 = u.part == parts - 1 ? p.spatial[u.p] * K : ahead + row1 * reps * K;
+        if (r == 0) at[u.part] = GnPartial{max(e1 - e0, (int64_t)0), mean, m2};
         if (u.part == 0 && r >= parts) at[r] = GnPartial{0, 0.f, 0.f};
     }
     if (p.cluster > 1) cluster_sync();  // nobody leaves while its table may be read
@@ -231,6 +231,8 @@ size_t stats_smem(int groups) {
 }
 
 // --- normalisation ------------------------------------------------------------------
+
+constexpr int APPLY_DEPTH = 6;  // as DEPTH
 
 template <bool SILU>
 __device__ __forceinline__ f32x2 act(f32x2 z) {
@@ -256,7 +258,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_apply_kernel(const __grid_co
     using W = ClWord<DT, VEC>;
     constexpr int ES = elem_size(DT), NL = L::N;
     extern __shared__ uint4 shared4[];
-    using Stream = ClStream<DT, VEC, 1, DEPTH>;
+    using Stream = ClStream<DT, VEC, 1, APPLY_DEPTH>;
     float2* const stats = reinterpret_cast<float2*>(shared4 + Stream::SMEM / 16);  // [G]
     const int C = (int)p.C, K = C / p.G;
     int pt = 0;
@@ -268,10 +270,8 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_apply_kernel(const __grid_co
     const int64_t bytes = p.N * run.elems * ES, from = (run.first + run.head) * ES;
     const int j0 = (int)blockIdx.y * p.columns, j1 = min(j0 + p.columns, p.period);
     const ClPlace q = cl_place(j0, j1);
-    int64_t a, b;
-    cl_piece((run.chunks + p.period - 1) / p.period, piece, p.parts[pt], a, b);
-    const ClWalk w = cl_walk(q, a, b, p.period, run.chunks);
-    // from the end of the run: the statistics left that in L2
+    const ClWalk w = cl_walk_dealt(q, piece, p.parts[pt], p.period, run.chunks);
+    // from the end: the statistics left that in L2
     const int64_t last = from + (w.at + (w.count - 1) * w.stride) * (int64_t)sizeof(W);
     Stream in;
     in.base[0] = patch;
@@ -299,22 +299,14 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_apply_kernel(const __grid_co
     cl_lanes<VEC>(fa, ga);
     cl_lanes<VEC>(fb, be);
     char* to = out + last;
-    for (int s = 0; s < w.count; s += DEPTH) {
+    cl_each(in, w.count, [&](const W (&v)[1], int) {
+        typename L::T f[NL];
+        to_lanes<DT, VEC>(v[0], f);
 #pragma unroll
-        for (int r = 0; r < DEPTH; ++r) {
-            if (s + r < w.count) {
-                W v[1];
-                in.step(r, v);
-                typename L::T f[NL];
-                to_lanes<DT, VEC>(v[0], f);
-#pragma unroll
-                for (int i = 0; i < NL; ++i) f[i] = act<SILU>(vfma(vsub(f[i], mean[i]), ga[i], be[i]));
-                if (in_bounds(to, sizeof(W), out, bytes, p.status))
-                    __stcs(reinterpret_cast<W*>(to), from_lanes<DT, VEC>(f));
-                to += in.stride;
-            }
-        }
-    }
+        for (int i = 0; i < NL; ++i) f[i] = act<SILU>(vfma(vsub(f[i], mean[i]), ga[i], be[i]));
+        if (in_bounds(to, sizeof(W), out, bytes, p.status)) __stcs(reinterpret_cast<W*>(to), from_lanes<DT, VEC>(f));
+        to += in.stride;
+    });
     if (VEC > 1 && blockIdx.y == 0) {
         const int h = piece == 0 ? run.head : 0, t = piece == p.parts[pt] - 1 ? run.tail : 0;
         if ((int)threadIdx.x < h + t) {
@@ -345,7 +337,7 @@ cudaError_t apply_launch(const GnClParams& p, bool vector, int64_t ctas, cudaStr
         vector ? (p.silu ? gncl_apply_kernel<DT, V, true> : gncl_apply_kernel<DT, V, false>)
                : (p.silu ? gncl_apply_kernel<DT, 1, true> : gncl_apply_kernel<DT, 1, false>);
     const unsigned slabs = (unsigned)((p.period + p.columns - 1) / p.columns);
-    return launch_cluster(fn, p, dim3((unsigned)ctas, slabs, 1), 1, (vector ? ClStream<DT, V, 1, DEPTH>::SMEM : 0) + (size_t)p.G * sizeof(float2), s);
+    return launch_cluster(fn, p, dim3((unsigned)ctas, slabs, 1), 1, (vector ? ClStream<DT, V, 1, APPLY_DEPTH>::SMEM : 0) + (size_t)p.G * sizeof(float2), s);
 }
 
 }  // namespace

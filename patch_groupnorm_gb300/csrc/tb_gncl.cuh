@@ -65,30 +65,48 @@ __device__ __forceinline__ ClPlace cl_place(int j0, int j1) {
     return q;
 }
 
-// The chunks of this thread in rows [a, b): `count` of them, `stride` chunks
-// apart, the first at chunk `at`.
+// The chunks of this thread: `count` of them, `stride` chunks apart, the first at
+// chunk `at`.
 struct ClWalk {
     int64_t at, stride;
     int32_t count;
 };
 
+// In rows [a, b).
 __device__ __forceinline__ ClWalk cl_walk(const ClPlace& q, int64_t a, int64_t b, int period, int64_t chunks) {
     ClWalk w;
     w.at = (a + q.row) * period + q.col;
     w.stride = (int64_t)q.rows * period;
     w.count = 0;
-    if (q.row >= 0 && a + q.row < b) {
-        w.count = (int32_t)((b - a - q.row + q.rows - 1) / q.rows);
-        // only the sample's last row may be cut short
-        if (w.at + (w.count - 1) * w.stride >= chunks) --w.count;
+    const int rows = (int)(b - a) - q.row;
+    if (q.row >= 0 && rows > 0) {
+        w.count = (int)((unsigned)(rows + q.rows - 1) / (unsigned)q.rows);
+        // the sample's last row may be cut short, and a sample may have a row less than the share
+        while (w.count > 0 && w.at + (w.count - 1) * w.stride >= chunks) --w.count;
     }
     return w;
 }
 
-// Rows [a, b) of piece i of `pieces` (rows < 2^47, pieces < 2^16).
-__device__ __forceinline__ void cl_piece(int64_t rows, int i, int pieces, int64_t& a, int64_t& b) {
-    a = rows * i / pieces;
-    b = rows * (i + 1) / pieces;
+// Rows dealt out in turn: piece i of `pieces` takes `rows` of them, then the pieces
+// after it, so that neighbouring CTAs read neighbouring addresses.
+__device__ __forceinline__ ClWalk cl_walk_dealt(const ClPlace& q, int i, int pieces, int period, int64_t chunks) {
+    ClWalk w;
+    w.at = ((int64_t)i * q.rows + q.row) * period + q.col;
+    w.stride = (int64_t)pieces * q.rows * period;
+    w.count = 0;
+    if (q.row >= 0 && w.at < chunks) {
+        const uint64_t left = (uint64_t)(chunks - w.at - 1);
+        // a 64-bit division is a hundred instructions
+        w.count = (int32_t)(left >> 32 || w.stride >> 32 ? left / (uint64_t)w.stride
+                                                         : (uint32_t)left / (uint32_t)w.stride) + 1;
+    }
+    return w;
+}
+
+// The first row of piece i of patch p (statistics).  The pieces that have a row more
+// than the others are the last ones, so the sample's last row is the last piece's.
+__device__ __forceinline__ int64_t cl_first_row(const GnClParams& prm, int p, int i) {
+    return (int64_t)prm.share[p] * i + max(0, i - (prm.parts[p] * prm.cluster - prm.extra[p]));
 }
 
 // --- a thread's chunks, in flight ahead of their use --------------------------------
@@ -102,6 +120,7 @@ __device__ __forceinline__ void cl_piece(int64_t rows, int i, int pieces, int64_
 template <int DT, int VEC, int NS, int DEPTH>
 struct ClStream {
     using W = ClWord<DT, VEC>;
+    static constexpr int D = DEPTH, N = NS;
     static constexpr size_t SMEM = VEC > 1 ? (size_t)DEPTH * NS * CL_BLOCK * 16 : 0;
     const char* at[NS];
     const char* base[NS];
@@ -111,8 +130,10 @@ struct ClStream {
     uint32_t* status;
     W reg[VEC > 1 ? 1 : DEPTH][NS];
 
+    // SURE: the caller knows that there is one more
+    template <bool SURE = false>
     __device__ __forceinline__ void fetch(int r) {
-        if (left > 0) {
+        if (SURE || left > 0) {
 #pragma unroll
             for (int k = 0; k < NS; ++k) {
                 if (in_bounds(at[k], sizeof(W), base[k], bytes, status)) {
@@ -137,19 +158,47 @@ struct ClStream {
 #pragma unroll
         for (int r = 0; r < DEPTH - 1; ++r) fetch(r);
     }
+    // whether the next DEPTH steps each fetch another chunk
+    __device__ __forceinline__ bool full() const { return left >= DEPTH; }
+    template <bool SURE = false>
     __device__ __forceinline__ void step(int r, W (&v)[NS]) {
         if constexpr (VEC > 1) {
             asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 2) : "memory");
-            fetch((r + DEPTH - 1) % DEPTH);
+            fetch<SURE>((r + DEPTH - 1) % DEPTH);
 #pragma unroll
             for (int k = 0; k < NS; ++k) v[k] = smem_load<W>(slot + (uint32_t)((r * NS + k) * CL_BLOCK * 16));
         } else {
 #pragma unroll
             for (int k = 0; k < NS; ++k) v[k] = reg[r][k];
-            fetch((r + DEPTH - 1) % DEPTH);
+            fetch<SURE>((r + DEPTH - 1) % DEPTH);
         }
     }
 };
+
+// The next `count` chunks (at most the whole turns of DEPTH that precede another
+// call, or the rest): body(v, k) for chunk k of them.
+template <typename Stream, typename Body>
+__device__ __forceinline__ void cl_each(Stream& in, int count, Body&& body) {
+    constexpr int D = Stream::D, NS = Stream::N;
+    typename Stream::W v[NS];
+    int k = 0;
+    for (; k + D <= count && in.full(); k += D) {
+#pragma unroll
+        for (int r = 0; r < D; ++r) {
+            in.template step<true>(r, v);
+            body(v, k + r);
+        }
+    }
+    for (; k < count; k += D) {
+#pragma unroll
+        for (int r = 0; r < D; ++r) {
+            if (k + r < count) {
+                in.step(r, v);
+                body(v, k + r);
+            }
+        }
+    }
+}
 
 // --- thread-block clusters ------------------------------------------------------
 

@@ -66,8 +66,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_stats_kernel(const __gr
     const char* const patch = static_cast<const char*>(p.patches[u.p]);
     const char* const grad = static_cast<const char*>(p.grads[u.p]);
     const int64_t bytes = p.N * run.elems * ES, from = (run.first + run.head) * ES;
-    int64_t a, b;
-    cl_piece((run.chunks + p.period - 1) / p.period, piece, pieces, a, b);
+    const int64_t a = cl_first_row(p, u.p, piece), b = cl_first_row(p, u.p, piece + 1);
     const int split_width = p.period / p.splits, split0 = (int)blockIdx.y * split_width;
     Stream in;
     in.base[0] = patch;
@@ -114,25 +113,18 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_stats_kernel(const __gr
             const int now = min(FOLD, w.count - done);
 #pragma unroll
             for (int i = 0; i < NL; ++i) sb[i] = sa[i] = L::splat(0.f);
-            for (int s = 0; s < now; s += DEPTH) {
+            cl_each(in, now, [&](const W (&v)[2], int) {
+                typename L::T f[NL], dy[NL];
+                to_lanes<DT, VEC>(v[0], f);
+                to_lanes<DT, VEC>(v[1], dy);
 #pragma unroll
-                for (int r = 0; r < DEPTH; ++r) {
-                    if (s + r < now) {
-                        W v[2];
-                        in.step(r, v);
-                        typename L::T f[NL], dy[NL];
-                        to_lanes<DT, VEC>(v[0], f);
-                        to_lanes<DT, VEC>(v[1], dy);
-#pragma unroll
-                        for (int i = 0; i < NL; ++i) {
-                            const typename L::T d = vsub(f[i], mean[i]);
-                            const typename L::T dz = dz_of<SILU>(dy[i], vfma(d, ga[i], be[i]));
-                            sb[i] = vadd(sb[i], dz);
-                            sa[i] = vfma(dz, d, sa[i]);
-                        }
-                    }
+                for (int i = 0; i < NL; ++i) {
+                    const typename L::T d = vsub(f[i], mean[i]);
+                    const typename L::T dz = dz_of<SILU>(dy[i], vfma(d, ga[i], be[i]));
+                    sb[i] = vadd(sb[i], dz);
+                    sa[i] = vfma(dz, d, sa[i]);
                 }
-            }
+            });
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
                 tb_[i] = vadd(tb_[i], sb[i]);
@@ -308,6 +300,8 @@ __global__ void __launch_bounds__(CL_BLOCK) gncl_coefs_kernel(const __grid_const
 
 // --- dx -----------------------------------------------------------------------------
 
+constexpr int APPLY_DEPTH = 4;  // as DEPTH
+
 template <int DT, int VEC, bool SILU>
 __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_apply_kernel(const __grid_constant__ GnClParams p) {
     using L = Lanes<VEC>;
@@ -324,14 +318,12 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_apply_kernel(const __gr
     const int64_t bytes = p.N * run.elems * ES, from = (run.first + run.head) * ES;
     const int j0 = (int)blockIdx.y * p.columns, j1 = min(j0 + p.columns, p.period);
     const ClPlace q = cl_place(j0, j1);
-    int64_t a, b;
-    cl_piece((run.chunks + p.period - 1) / p.period, piece, p.parts[pt], a, b);
-    const ClWalk w = cl_walk(q, a, b, p.period, run.chunks);
+    const ClWalk w = cl_walk_dealt(q, piece, p.parts[pt], p.period, run.chunks);
     const float4* const coefs = p.coefs + (int64_t)n * p.G;
-    // from the end of the run: the records' pass left that in L2
+    // from the end: the records' pass left that in L2
     const int64_t last = from + (w.at + (w.count - 1) * w.stride) * (int64_t)sizeof(W);
     extern __shared__ uint4 shared4[];
-    ClStream<DT, VEC, 2, DEPTH> in;
+    ClStream<DT, VEC, 2, APPLY_DEPTH> in;
     in.base[0] = patch;
     in.base[1] = grad;
     in.at[0] = patch + last;
@@ -362,27 +354,19 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_apply_kernel(const __gr
         cl_lanes<VEC>(f4, cv);
     }
     char* to = out + last;
-    for (int s = 0; s < w.count; s += DEPTH) {
+    cl_each(in, w.count, [&](const W (&v)[2], int) {
+        typename L::T f[NL], dy[NL];
+        to_lanes<DT, VEC>(v[0], f);
+        to_lanes<DT, VEC>(v[1], dy);
 #pragma unroll
-        for (int r = 0; r < DEPTH; ++r) {
-            if (s + r < w.count) {
-                W v[2];
-                in.step(r, v);
-                typename L::T f[NL], dy[NL];
-                to_lanes<DT, VEC>(v[0], f);
-                to_lanes<DT, VEC>(v[1], dy);
-#pragma unroll
-                for (int i = 0; i < NL; ++i) {
-                    const typename L::T d = vsub(f[i], mean[i]);
-                    const typename L::T dz = dz_of<SILU>(dy[i], vfma(d, ga[i], be[i]));
-                    f[i] = vfma(dz, ga[i], vfma(d, cu[i], cv[i]));
-                }
-                if (in_bounds(to, sizeof(W), out, bytes, p.status))
-                    __stcs(reinterpret_cast<W*>(to), from_lanes<DT, VEC>(f));
-                to += in.stride;
-            }
+        for (int i = 0; i < NL; ++i) {
+            const typename L::T d = vsub(f[i], mean[i]);
+            const typename L::T dz = dz_of<SILU>(dy[i], vfma(d, ga[i], be[i]));
+            f[i] = vfma(dz, ga[i], vfma(d, cu[i], cv[i]));
         }
-    }
+        if (in_bounds(to, sizeof(W), out, bytes, p.status)) __stcs(reinterpret_cast<W*>(to), from_lanes<DT, VEC>(f));
+        to += in.stride;
+    });
     if (VEC > 1 && blockIdx.y == 0) {
         const int h = piece == 0 ? run.head : 0, t = piece == p.parts[pt] - 1 ? run.tail : 0;
         if ((int)threadIdx.x < h + t) {
@@ -417,7 +401,7 @@ cudaError_t apply_launch(const GnClParams& p, bool vector, int64_t ctas, cudaStr
         vector ? (p.silu ? gncl_grad_apply_kernel<DT, V, true> : gncl_grad_apply_kernel<DT, V, false>)
                : (p.silu ? gncl_grad_apply_kernel<DT, 1, true> : gncl_grad_apply_kernel<DT, 1, false>);
     const unsigned slabs = (unsigned)((p.period + p.columns - 1) / p.columns);
-    return launch_cluster(fn, p, dim3((unsigned)ctas, slabs, 1), 1, vector ? ClStream<DT, V, 2, DEPTH>::SMEM : 0, s);
+    return launch_cluster(fn, p, dim3((unsigned)ctas, slabs, 1), 1, vector ? ClStream<DT, V, 2, APPLY_DEPTH>::SMEM : 0, s);
 }
 
 }  // namespace

@@ -499,6 +499,8 @@ struct GnClParams {
     int32_t cluster;               // statistics: CTAs whose sums make one record
     int32_t parts[GN_MAXP];        // statistics: records of each unit of patch p; else CTAs of each sample
     int32_t start[GN_MAXP + 1];    // first cluster (statistics) or CTA of patch p
+    int32_t share[GN_MAXP];        // statistics: rows of a CTA (each of the last `extra` ones has another)
+    int32_t extra[GN_MAXP];
     uint32_t* status;              // bounds-checked build: device status word (else null)
 };
 static_assert(sizeof(GnClParams) <= 32000, "kernel parameter block too large");

@@ -95,6 +95,11 @@ int64_t cl_rows(const tb::GnClParams& prm, int p, int vec) {
     return (chunks + prm.period - 1) / prm.period;
 }
 
+int cl_slabs(int width) {
+    const int turns = (width + tb::CL_BLOCK - 1) / tb::CL_BLOCK;
+    return turns <= tb::CL_MAX_CLUSTER ? turns : 1;
+}
+
 // Statistics: every (patch, sample) is a unit, cut into up to TB_GN_PARTS records
 // of a cluster each; the channels may be split too, into runs of whole groups of at
 // least 256 bytes a position.  Of the ways to cut, the one that comes nearest to the
@@ -112,16 +117,18 @@ tb_status cl_plan_stats(tb::GnClParams& prm, tb_dtype dtype, bool vector, int ct
         most = std::max(most, rows[p]);
     }
     int64_t best = 0;
-    int32_t splits = 1, cluster = 1, parts = 1;
+    int32_t splits = 1, cluster = cl_slabs(prm.period), parts = 1;
     for (int s = 1; s <= 16; s *= 2) {
         if (s > 1 && !(whole && prm.G % s == 0 && (prm.C / s) % vec == 0 && prm.C / s * es >= 256)) break;
         const int64_t columns = std::min<int64_t>(prm.period / s, tb::CL_BLOCK);
+        // columns that do not fit a CTA's threads go to CTAs of a cluster, up to eight
+        const int slabs = cl_slabs(prm.period / s);
         // at least four turns of a CTA's threads each
-        const int64_t useful = std::max<int64_t>(1, most / (tb::CL_BLOCK / columns * 4));
-        for (int c = 1; c <= tb::CL_MAX_CLUSTER; ++c) {
+        const int64_t useful = std::max<int64_t>(1, most / (tb::CL_BLOCK / columns * 4)) * slabs;
+        for (int c = slabs; c <= tb::CL_MAX_CLUSTER; c += slabs) {
             const double places = (c <= 2 ? 1.0 : c <= 5 ? 0.95 : 0.87) * ctas_wanted;
             for (int k = 1; k <= TB_GN_PARTS; ++k) {
-                if (c * k > useful && c * k > 1) continue;
+                if (c * k > useful && c * k > slabs) continue;
                 int64_t total = 0;
                 for (int p = 0; p < prm.P; ++p) total += std::max<int64_t>(1, (rows[p] * k + most / 2) / most);
                 total *= prm.N * c * s;
@@ -137,12 +144,13 @@ tb_status cl_plan_stats(tb::GnClParams& prm, tb_dtype dtype, bool vector, int ct
     prm.cluster = cluster;
     const int width = prm.period / splits, turns = (width + tb::CL_BLOCK - 1) / tb::CL_BLOCK;
     prm.columns = (width + turns - 1) / turns;
+    prm.slabs = cl_slabs(width);
     int64_t at = 0;
     for (int p = 0; p < prm.P; ++p) {
         prm.parts[p] = (int32_t)std::max<int64_t>(1, (rows[p] * parts + most / 2) / most);
         prm.start[p] = (int32_t)at;
         at += prm.N * prm.parts[p];
-        const int64_t pieces = (int64_t)prm.parts[p] * cluster;
+        const int64_t pieces = (int64_t)prm.parts[p] * (cluster / prm.slabs);
         if (rows[p] / pieces > 2000000000LL) return TB_ERR_UNSUPPORTED;  // past any memory
         prm.share[p] = (int32_t)(rows[p] / pieces);
         prm.extra[p] = (int32_t)(rows[p] % pieces);

@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
     while (team > 1 && gs * team > CL_BLOCK) team /= 2;
     for (int i = threadIdx.x; i < gs; i += CL_BLOCK) table[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     const ClUnit u = cl_unit(p);
-    const int parts = p.parts[u.p], piece = u.part * p.cluster + u.rank, pieces = parts * p.cluster;
+    const int parts = p.parts[u.p], piece = u.piece, pieces = u.pieces;
     const ClRun run = cl_run<ES, VEC>(p.patches[u.p], p.spatial[u.p], p.C, u.n);
     const char* const patch = static_cast<const char*>(p.patches[u.p]);
     const int64_t bytes = p.N * run.elems * ES;
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
     float edge = 0.f;
     int edge_group = -1;
     if (VEC > 1 && warp == 0) {
-        const int h = piece == 0 ? run.head : 0, t = piece == pieces - 1 ? run.tail : 0;
+        const int h = piece == 0 && u.slab == 0 ? run.head : 0, t = piece == pieces - 1 && u.slab == 0 ? run.tail : 0;
         if (lane < h + t) {
             const int64_t e = lane < h ? lane : run.elems - run.tail + (lane - h);
             if (in_bounds(patch + (run.first + e) * ES, ES, patch, bytes, p.status))
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
 
     const int64_t a = cl_first_row(p, u.p, piece), b = cl_first_row(p, u.p, piece + 1);
     const int split_width = p.period / p.splits, split0 = (int)blockIdx.y * split_width;
-    for (int j0 = split0; j0 < split0 + split_width; j0 += p.columns) {
+    for (int j0 = split0 + u.slab * p.columns; j0 < split0 + split_width; j0 += p.slabs * p.columns) {
         const int j1 = min(j0 + p.columns, split0 + split_width);
         const ClPlace q = cl_place(j0, j1);
         const ClWalk w = cl_walk(q, a, b, p.period, run.chunks);
@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
     // whole rows have reps * K elements of every group; the first part has the head's
     // too, and the last one whatever the others leave
     const int reps = (int)((unsigned)(p.period * VEC) / (unsigned)C);
-    const int64_t row0 = cl_first_row(p, u.p, u.part * p.cluster), row1 = cl_first_row(p, u.p, (u.part + 1) * p.cluster);
+    const int slices = p.cluster / p.slabs;
+    const int64_t row0 = cl_first_row(p, u.p, u.part * slices), row1 = cl_first_row(p, u.p, (u.part + 1) * slices);
     GnPartial* const out = p.partials + ((int64_t)u.p * p.N + u.n) * G * TB_GN_PARTS;
     for (int first = 0; first < gs; first += p.cluster * (CL_BLOCK / 8)) {
         const int i = first + u.rank * (CL_BLOCK / 8) + (int)threadIdx.x / 8, r = threadIdx.x & 7;

@@ -106,7 +106,7 @@ __device__ __forceinline__ ClWalk cl_walk_dealt(const ClPlace& q, int i, int pie
 // The first row of piece i of patch p (statistics).  The pieces that have a row more
 // than the others are the last ones, so the sample's last row is the last piece's.
 __device__ __forceinline__ int64_t cl_first_row(const GnClParams& prm, int p, int i) {
-    return (int64_t)prm.share[p] * i + max(0, i - (prm.parts[p] * prm.cluster - prm.extra[p]));
+    return (int64_t)prm.share[p] * i + max(0, i - (prm.parts[p] * (prm.cluster / prm.slabs) - prm.extra[p]));
 }
 
 // --- a thread's chunks, in flight ahead of their use --------------------------------
@@ -214,10 +214,13 @@ __device__ __forceinline__ uint2 cluster_load8(uint32_t at, uint32_t rank) {
     return v;
 }
 
-// The (patch, sample, part) and place of a statistics CTA.  Clusters are
-// numbered patch by patch, then sample, then part.
+// The (patch, sample, part) of a statistics CTA, its rank in the part's cluster, its
+// piece of the sample's rows, and its slab of the columns.  Clusters are numbered
+// patch by patch, then sample, then part; in a cluster the slabs run fastest.
 struct ClUnit {
     int p, part, rank;
+    int piece, pieces;  // of the sample's rows
+    int slab;
     int64_t n;
 };
 
@@ -230,6 +233,10 @@ __device__ __forceinline__ ClUnit cl_unit(const GnClParams& prm) {
     const int local = cluster - prm.start[u.p];
     u.n = local / prm.parts[u.p];
     u.part = local - (int)u.n * prm.parts[u.p];
+    const int each = prm.cluster / prm.slabs;
+    u.piece = u.part * each + u.rank / prm.slabs;
+    u.pieces = prm.parts[u.p] * each;
+    u.slab = u.rank % prm.slabs;
     return u;
 }
 

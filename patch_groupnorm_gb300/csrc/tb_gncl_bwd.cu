@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_stats_kernel(const __gr
     const int g0 = c0 / K, g1 = (c0 + cs + K - 1) / K;
     for (int c = threadIdx.x; c < cs; c += CL_BLOCK) table[c] = make_float2(0.f, 0.f);
     const ClUnit u = cl_unit(p);
-    const int parts = p.parts[u.p], piece = u.part * p.cluster + u.rank, pieces = parts * p.cluster;
+    const int parts = p.parts[u.p], piece = u.piece, pieces = u.pieces;
     const ClRun run = cl_run<ES, VEC>(p.patches[u.p], p.spatial[u.p], p.C, u.n);
     const char* const patch = static_cast<const char*>(p.patches[u.p]);
     const char* const grad = static_cast<const char*>(p.grads[u.p]);
@@ -82,11 +82,12 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_stats_kernel(const __gr
     };
     grid_wait();
     // the first columns' chunks are on their way while the groups' statistics are found
-    begin(cl_walk(cl_place(split0, min(split0 + p.columns, split0 + split_width)), a, b, p.period, run.chunks));
+    const int mine = split0 + u.slab * p.columns;
+    begin(cl_walk(cl_place(mine, min(mine + p.columns, split0 + split_width)), a, b, p.period, run.chunks));
     cl_group_stats(p, u.n, g0, g1, stats);
     __syncthreads();
 
-    for (int j0 = split0; j0 < split0 + split_width; j0 += p.columns) {
+    for (int j0 = mine; j0 < split0 + split_width; j0 += p.slabs * p.columns) {
         const int j1 = min(j0 + p.columns, split0 + split_width);
         const ClPlace q = cl_place(j0, j1);
         const ClWalk w = cl_walk(q, a, b, p.period, run.chunks);
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_stats_kernel(const __gr
         cl_lanes<VEC>(f2, be);
 #pragma unroll
         for (int i = 0; i < NL; ++i) tb_[i] = ta[i] = L::splat(0.f);
-        if (j0 != split0) begin(w);
+        if (j0 != mine) begin(w);
         for (int done = 0; done < w.count; done += FOLD) {
             const int now = min(FOLD, w.count - done);
 #pragma unroll
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_stats_kernel(const __gr
     __syncthreads();
     if (VEC > 1 && threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        const int h = piece == 0 ? run.head : 0, t = piece == pieces - 1 ? run.tail : 0;
+        const int h = piece == 0 && u.slab == 0 ? run.head : 0, t = piece == pieces - 1 && u.slab == 0 ? run.tail : 0;
         float dz = 0.f, xhat = 0.f;
         int c = -1;
         if (lane < h + t) {
@@ -235,6 +236,9 @@ __global__ void __launch_bounds__(CL_BLOCK) gncl_coefs_kernel(const __grid_const
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t size = (int64_t)p.R * set * (int64_t)sizeof(float2);
     grid_wait();
+    // what came before is done, so dx's launch may fetch its first chunks of x and dy
+    // while this one works; it waits before it reads a constant or writes a chunk
+    pdl_trigger_dependents();
     if ((int64_t)blockIdx.x < units) {
         const int64_t n = blockIdx.x / p.G;
         const int g = (int)(blockIdx.x - n * p.G);
@@ -331,8 +335,10 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_apply_kernel(const __gr
     in.stride = -w.stride * (int64_t)sizeof(W);
     in.bytes = bytes;
     in.status = p.status;
-    grid_wait();
+    // the launch before this one is always the constants', which starts it once
+    // everything before that is done: x and dy are in place, the constants are not
     in.start(w.count, shared4);
+    grid_wait();
     typename L::T mean[NL], ga[NL], be[NL], cu[NL], cv[NL];
     {
         float f0[VEC], f1[VEC], f2[VEC], f3[VEC], f4[VEC];

@@ -132,7 +132,7 @@ __device__ __forceinline__ bool index_ok(bool ok, uint32_t* status) {
 // the start of each CTA lets the next kernel in the stream launch as soon as
 // every CTA of this grid has started (so it never takes a slot this grid
 // still needs); its CTAs run their parameter-only prologue and then wait for
-// this grid to complete and its writes to become visible.  Two kernels
+// this grid to complete and its writes to become visible.  Three kernels
 // trigger.  The stitch: its grids run many waves, and the next grid fills the
 // SMs as the last wave drains (small stitches 12-18% faster back to back).  The
 // records of the GroupNorm's backward pass, for the dx that follow: one CTA
@@ -497,6 +497,7 @@ struct GnClParams {
     int32_t columns;               // of the period, one CTA takes at a time
     int32_t splits;                // statistics: grid.y; whole groups of whole chunks each
     int32_t cluster;               // statistics: CTAs whose sums make one record
+    int32_t slabs;                 // statistics: of these, CTAs with columns of their own (1: each takes all)
     int32_t parts[GN_MAXP];        // statistics: records of each unit of patch p; else CTAs of each sample
     int32_t start[GN_MAXP + 1];    // first cluster (statistics) or CTA of patch p
     int32_t share[GN_MAXP];        // statistics: rows of a CTA (each of the last `extra` ones has another)

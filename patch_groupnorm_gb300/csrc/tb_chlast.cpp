@@ -151,9 +151,11 @@ tb_status cl_plan_stats(tb::GnClParams& prm, tb_dtype dtype, bool vector, int ct
         prm.start[p] = (int32_t)at;
         at += prm.N * prm.parts[p];
         const int64_t pieces = (int64_t)prm.parts[p] * (cluster / prm.slabs);
-        if (rows[p] / pieces > 2000000000LL) return TB_ERR_UNSUPPORTED;  // past any memory
-        prm.share[p] = (int32_t)(rows[p] / pieces);
-        prm.extra[p] = (int32_t)(rows[p] % pieces);
+        const int64_t side = tb::CL_BLOCK / prm.columns, blocks = (rows[p] + side - 1) / side;
+        if (blocks / pieces > 2000000000LL) return TB_ERR_UNSUPPORTED;  // past any memory
+        prm.rows[p] = rows[p];
+        prm.share[p] = (int32_t)(blocks / pieces);
+        prm.extra[p] = (int32_t)(blocks % pieces);
     }
     prm.start[prm.P] = (int32_t)at;
     *ctas = at * cluster;

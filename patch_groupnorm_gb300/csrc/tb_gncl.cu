@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
     while (team > 1 && gs * team > CL_BLOCK) team /= 2;
     for (int i = threadIdx.x; i < gs; i += CL_BLOCK) table[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     const ClUnit u = cl_unit(p);
-    const int parts = p.parts[u.p], piece = u.piece, pieces = u.pieces;
+    const int parts = p.parts[u.p], piece = u.piece, pieces = u.pieces, last = cl_last_piece(p, u.p, pieces);
     const ClRun run = cl_run<ES, VEC>(p.patches[u.p], p.spatial[u.p], p.C, u.n);
     const char* const patch = static_cast<const char*>(p.patches[u.p]);
     const int64_t bytes = p.N * run.elems * ES;
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
     float edge = 0.f;
     int edge_group = -1;
     if (VEC > 1 && warp == 0) {
-        const int h = piece == 0 && u.slab == 0 ? run.head : 0, t = piece == pieces - 1 && u.slab == 0 ? run.tail : 0;
+        const int h = piece == 0 && u.slab == 0 ? run.head : 0, t = piece == last && u.slab == 0 ? run.tail : 0;
         if (lane < h + t) {
             const int64_t e = lane < h ? lane : run.elems - run.tail + (lane - h);
             if (in_bounds(patch + (run.first + e) * ES, ES, patch, bytes, p.status))
@@ -63,12 +63,11 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
         }
     }
 
-    const int64_t a = cl_first_row(p, u.p, piece), b = cl_first_row(p, u.p, piece + 1);
     const int split_width = p.period / p.splits, split0 = (int)blockIdx.y * split_width;
     for (int j0 = split0 + u.slab * p.columns; j0 < split0 + split_width; j0 += p.slabs * p.columns) {
         const int j1 = min(j0 + p.columns, split0 + split_width);
-        const ClPlace q = cl_place(j0, j1);
-        const ClWalk w = cl_walk(q, a, b, p.period, run.chunks);
+        const ClPlace q = cl_place(p, j0, j1);
+        const ClWalk w = cl_walk_share(p, q, u.p, piece, pieces, run.chunks);
         typename L::T k[NL], s1[NL], s2[NL], mean[NL], m2[NL];
 #pragma unroll
         for (int i = 0; i < NL; ++i) k[i] = mean[i] = m2[i] = L::splat(0.f);
@@ -185,11 +184,16 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
     else __syncthreads();
     // the cluster's tables: eight threads to a group, one for each CTA
     static_assert(CL_MAX_CLUSTER == 8 && TB_GN_PARTS == 8, "eight threads read the CTAs' sums and write the parts");
-    // whole rows have reps * K elements of every group; the first part has the head's
-    // too, and the last one whatever the others leave
-    const int reps = (int)((unsigned)(p.period * VEC) / (unsigned)C);
-    const int slices = p.cluster / p.slabs;
-    const int64_t row0 = cl_first_row(p, u.p, u.part * slices), row1 = cl_first_row(p, u.p, (u.part + 1) * slices);
+    // whole rows have reps * K elements of every group; whoever has the last row has
+    // whatever the others leave, and the first piece the head's too
+    const int reps = (int)((unsigned)(p.period * VEC) / (unsigned)C), slices = p.cluster / p.slabs;
+    const int first_piece = u.part * slices, side = CL_BLOCK / p.columns;
+    const bool ends = p.rows[u.p] > 0 && last >= first_piece && last < first_piece + slices;
+    int64_t whole = ((int64_t)p.share[u.p] * slices + min(max(p.extra[u.p] - first_piece, 0), slices)) * side;
+    if (ends) {  // its last block may be short; its last row is counted apart
+        const int64_t blocks = (int64_t)p.share[u.p] * pieces + p.extra[u.p];
+        whole -= blocks * side - p.rows[u.p] + 1;
+    }
     GnPartial* const out = p.partials + ((int64_t)u.p * p.N + u.n) * G * TB_GN_PARTS;
     for (int first = 0; first < gs; first += p.cluster * (CL_BLOCK / 8)) {
         const int i = first + u.rank * (CL_BLOCK / 8) + (int)threadIdx.x / 8, r = threadIdx.x & 7;
@@ -218,9 +222,11 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
             continue;
         const int c0 = (g0 + i) * K;
         const int64_t ahead = min(max((run.head % C) - c0, 0), K) + (int64_t)(run.head / C) * K;
-        const int64_t e0 = u.part == 0 ? 0 : ahead + row0 * reps * K;
-        const int64_t e1 = u.part == parts - 1 ? p.spatial[u.p] * K : ahead + row1 * reps * K;
-        if (r == 0) at[u.part] = GnPartial{max(e1 - e0, (int64_t)0), mean, m2};
+        int64_t count = whole * reps * K + (u.part == 0 ? ahead : 0);
+        if (ends) count += p.spatial[u.p] * K - ahead - (p.rows[u.p] - 1) * reps * K;
+        // a sample of less than a chunk has no rows
+        if (p.rows[u.p] == 0) count = u.part == 0 ? p.spatial[u.p] * K : 0;
+        if (r == 0) at[u.part] = GnPartial{count, mean, m2};
         if (u.part == 0 && r >= parts) at[r] = GnPartial{0, 0.f, 0.f};
     }
     if (p.cluster > 1) cluster_sync();  // nobody leaves while its table may be read
@@ -270,7 +276,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_apply_kernel(const __grid_co
     char* const out = static_cast<char*>(p.outs[pt]);
     const int64_t bytes = p.N * run.elems * ES, from = (run.first + run.head) * ES;
     const int j0 = (int)blockIdx.y * p.columns, j1 = min(j0 + p.columns, p.period);
-    const ClPlace q = cl_place(j0, j1);
+    const ClPlace q = cl_place(p, j0, j1);
     const ClWalk w = cl_walk_dealt(q, piece, p.parts[pt], p.period, run.chunks);
     // from the end: the statistics left that in L2
     const int64_t last = from + (w.at + (w.count - 1) * w.stride) * (int64_t)sizeof(W);

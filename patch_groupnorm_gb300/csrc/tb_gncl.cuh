@@ -55,10 +55,10 @@ struct ClPlace {
     int32_t row, col;     // this thread's (row < 0: none)
 };
 
-__device__ __forceinline__ ClPlace cl_place(int j0, int j1) {
+__device__ __forceinline__ ClPlace cl_place(const GnClParams& p, int j0, int j1) {
     ClPlace q;
     q.width = j1 - j0;
-    q.rows = CL_BLOCK / q.width;
+    q.rows = CL_BLOCK / p.columns;  // of every slab, the last and narrower one too
     q.row = (int)threadIdx.x / q.width;
     q.col = j0 + (int)threadIdx.x - q.row * q.width;
     if (q.row >= q.rows) q.row = -1;
@@ -71,21 +71,6 @@ struct ClWalk {
     int64_t at, stride;
     int32_t count;
 };
-
-// In rows [a, b).
-__device__ __forceinline__ ClWalk cl_walk(const ClPlace& q, int64_t a, int64_t b, int period, int64_t chunks) {
-    ClWalk w;
-    w.at = (a + q.row) * period + q.col;
-    w.stride = (int64_t)q.rows * period;
-    w.count = 0;
-    const int rows = (int)(b - a) - q.row;
-    if (q.row >= 0 && rows > 0) {
-        w.count = (int)((unsigned)(rows + q.rows - 1) / (unsigned)q.rows);
-        // the sample's last row may be cut short, and a sample may have a row less than the share
-        while (w.count > 0 && w.at + (w.count - 1) * w.stride >= chunks) --w.count;
-    }
-    return w;
-}
 
 // Rows dealt out in turn: piece i of `pieces` takes `rows` of them, then the pieces
 // after it, so that neighbouring CTAs read neighbouring addresses.
@@ -103,10 +88,22 @@ __device__ __forceinline__ ClWalk cl_walk_dealt(const ClPlace& q, int i, int pie
     return w;
 }
 
-// The first row of piece i of patch p (statistics).  The pieces that have a row more
-// than the others are the last ones, so the sample's last row is the last piece's.
-__device__ __forceinline__ int64_t cl_first_row(const GnClParams& prm, int p, int i) {
-    return (int64_t)prm.share[p] * i + max(0, i - (prm.parts[p] * (prm.cluster / prm.slabs) - prm.extra[p]));
+// The same for piece i of `pieces` of a statistics pass, whose share of blocks (rows
+// side by side) the host has counted from a sample that starts on a boundary; another
+// may have a chunk less, in its last row.
+__device__ __forceinline__ ClWalk cl_walk_share(const GnClParams& prm, const ClPlace& q, int p, int i, int pieces,
+                                                int64_t chunks) {
+    ClWalk w;
+    w.at = ((int64_t)i * q.rows + q.row) * prm.period + q.col;
+    w.stride = (int64_t)pieces * q.rows * prm.period;
+    w.count = q.row >= 0 ? prm.share[p] + (i < prm.extra[p] ? 1 : 0) : 0;
+    if (w.count > 0 && w.at + (w.count - 1) * w.stride >= chunks) --w.count;
+    return w;
+}
+
+// The piece that has the sample's last block, and with it its tail.
+__device__ __forceinline__ int cl_last_piece(const GnClParams& prm, int p, int pieces) {
+    return (prm.extra[p] > 0 ? prm.extra[p] : pieces) - 1;
 }
 
 // --- a thread's chunks, in flight ahead of their use --------------------------------

@@ -61,12 +61,11 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_stats_kernel(const __gr
     const int g0 = c0 / K, g1 = (c0 + cs + K - 1) / K;
     for (int c = threadIdx.x; c < cs; c += CL_BLOCK) table[c] = make_float2(0.f, 0.f);
     const ClUnit u = cl_unit(p);
-    const int parts = p.parts[u.p], piece = u.piece, pieces = u.pieces;
+    const int parts = p.parts[u.p], piece = u.piece, pieces = u.pieces, last = cl_last_piece(p, u.p, pieces);
     const ClRun run = cl_run<ES, VEC>(p.patches[u.p], p.spatial[u.p], p.C, u.n);
     const char* const patch = static_cast<const char*>(p.patches[u.p]);
     const char* const grad = static_cast<const char*>(p.grads[u.p]);
     const int64_t bytes = p.N * run.elems * ES, from = (run.first + run.head) * ES;
-    const int64_t a = cl_first_row(p, u.p, piece), b = cl_first_row(p, u.p, piece + 1);
     const int split_width = p.period / p.splits, split0 = (int)blockIdx.y * split_width;
     Stream in;
     in.base[0] = patch;
@@ -83,14 +82,14 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_stats_kernel(const __gr
     grid_wait();
     // the first columns' chunks are on their way while the groups' statistics are found
     const int mine = split0 + u.slab * p.columns;
-    begin(cl_walk(cl_place(mine, min(mine + p.columns, split0 + split_width)), a, b, p.period, run.chunks));
+    begin(cl_walk_share(p, cl_place(p, mine, min(mine + p.columns, split0 + split_width)), u.p, piece, pieces, run.chunks));
     cl_group_stats(p, u.n, g0, g1, stats);
     __syncthreads();
 
     for (int j0 = mine; j0 < split0 + split_width; j0 += p.slabs * p.columns) {
         const int j1 = min(j0 + p.columns, split0 + split_width);
-        const ClPlace q = cl_place(j0, j1);
-        const ClWalk w = cl_walk(q, a, b, p.period, run.chunks);
+        const ClPlace q = cl_place(p, j0, j1);
+        const ClWalk w = cl_walk_share(p, q, u.p, piece, pieces, run.chunks);
         typename L::T mean[NL], ga[NL], be[NL], sb[NL], sa[NL], tb_[NL], ta[NL];
         float f0[VEC], f1[VEC], f2[VEC];
         if constexpr (SILU) cl_weights<DT, VEC>(p, run.head, q.col * VEC, f1, f2);
@@ -157,7 +156,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_stats_kernel(const __gr
     __syncthreads();
     if (VEC > 1 && threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        const int h = piece == 0 && u.slab == 0 ? run.head : 0, t = piece == pieces - 1 && u.slab == 0 ? run.tail : 0;
+        const int h = piece == 0 && u.slab == 0 ? run.head : 0, t = piece == last && u.slab == 0 ? run.tail : 0;
         float dz = 0.f, xhat = 0.f;
         int c = -1;
         if (lane < h + t) {
@@ -321,7 +320,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_apply_kernel(const __gr
     char* const out = static_cast<char*>(p.outs[pt]);
     const int64_t bytes = p.N * run.elems * ES, from = (run.first + run.head) * ES;
     const int j0 = (int)blockIdx.y * p.columns, j1 = min(j0 + p.columns, p.period);
-    const ClPlace q = cl_place(j0, j1);
+    const ClPlace q = cl_place(p, j0, j1);
     const ClWalk w = cl_walk_dealt(q, piece, p.parts[pt], p.period, run.chunks);
     const float4* const coefs = p.coefs + (int64_t)n * p.G;
     // from the end: the records' pass left that in L2

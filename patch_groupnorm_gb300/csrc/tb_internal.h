@@ -500,7 +500,8 @@ struct GnClParams {
     int32_t slabs;                 // statistics: of these, CTAs with columns of their own (1: each takes all)
     int32_t parts[GN_MAXP];        // statistics: records of each unit of patch p; else CTAs of each sample
     int32_t start[GN_MAXP + 1];    // first cluster (statistics) or CTA of patch p
-    int32_t share[GN_MAXP];        // statistics: rows of a CTA (each of the last `extra` ones has another)
+    int64_t rows[GN_MAXP];         // statistics: rows of a sample of patch p, and their blocks for
+    int32_t share[GN_MAXP];        // each piece (each of the first `extra` pieces has another)
     int32_t extra[GN_MAXP];
     uint32_t* status;              // bounds-checked build: device status word (else null)
 };

@@ -37,6 +37,7 @@ UNITS = {
     "tb_train.cpp": [],
     "tb_gncl.cu": [],
     "tb_gncl_bwd.cu": [],
+    "tb_gncl_fused.cu": [],
     "tb_dropout.cu": [],
     "tb_chlast.cpp": [],
 }

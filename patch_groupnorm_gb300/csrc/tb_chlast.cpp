@@ -95,6 +95,16 @@ int64_t cl_rows(const tb::GnClParams& prm, int p, int vec) {
     return (chunks + prm.period - 1) / prm.period;
 }
 
+// The share of the SMs' places that clusters of this size find: theirs have to be in
+// one group of SMs.  Of 304 places (two on each SM) clusters of 1 and 2 take all, of 3
+// to 5 290 to 296, of 6 to 8 266 to 288; of 152, 138 to 144 and 105 to 138 (the
+// runtime's own count).
+double cl_places(int cluster, int per_sm) {
+    if (cluster <= 2) return 1.0;
+    if (cluster <= 5) return per_sm > 1 ? 0.95 : 0.9;
+    return per_sm > 1 ? 0.87 : 0.69;
+}
+
 int cl_slabs(int width) {
     const int turns = (width + tb::CL_BLOCK - 1) / tb::CL_BLOCK;
     return turns <= tb::CL_MAX_CLUSTER ? turns : 1;
@@ -104,9 +114,7 @@ int cl_slabs(int width) {
 // of a cluster each; the channels may be split too, into runs of whole groups of at
 // least 256 bytes a position.  Of the ways to cut, the one that comes nearest to the
 // CTAs wanted (those resident at once), and of equals the one with the fewest splits,
-// then the smallest clusters.  A cluster's CTAs have to find their places in one
-// group of SMs: of 304 places (two on each SM) clusters of 1 and 2 take all, of 3 to 5
-// 290 to 296, of 6 to 8 266 to 288 (the runtime's own count).
+// then the smallest clusters.
 tb_status cl_plan_stats(tb::GnClParams& prm, tb_dtype dtype, bool vector, int ctas_wanted, int64_t* ctas) {
     const int es = elem_bytes(dtype), vec = vector ? 16 / es : 1;
     bool whole = prm.C % vec == 0;
@@ -126,7 +134,7 @@ tb_status cl_plan_stats(tb::GnClParams& prm, tb_dtype dtype, bool vector, int ct
         // at least four turns of a CTA's threads each
         const int64_t useful = std::max<int64_t>(1, most / (tb::CL_BLOCK / columns * 4)) * slabs;
         for (int c = slabs; c <= tb::CL_MAX_CLUSTER; c += slabs) {
-            const double places = (c <= 2 ? 1.0 : c <= 5 ? 0.95 : 0.87) * ctas_wanted;
+            const double places = cl_places(c, 2) * ctas_wanted;
             for (int k = 1; k <= TB_GN_PARTS; ++k) {
                 if (c * k > useful && c * k > slabs) continue;
                 int64_t total = 0;
@@ -160,6 +168,62 @@ tb_status cl_plan_stats(tb::GnClParams& prm, tb_dtype dtype, bool vector, int ct
     prm.start[prm.P] = (int32_t)at;
     *ctas = at * cluster;
     return TB_OK;
+}
+
+// Whether a call fits into shared memory in one launch, and how it is cut (see
+// tb_gncl_fused.cu): of the ways for which all clusters have room at once, the one
+// that a simple account of its time favours: an SM's bytes at its share of the
+// memory's rate, and a thread's chunks one after the other.
+bool cl_plan_fused(tb::GnClParams& prm, tb_dtype dtype, bool grad, int sms, int* block) {
+    const int es = elem_bytes(dtype), vec = 16 / es, tensors = grad ? 2 : 1;
+    double bytes = 0;
+    for (int p = 0; p < prm.P; ++p) {
+        if (!aligned(prm.patches[p], 16) || !aligned(prm.outs[p], 16) || !aligned(prm.grads[p], 16)) return false;
+        if (prm.spatial[p] * prm.C % vec != 0) return false;  // no single elements
+        bytes += (double)prm.N * (double)prm.spatial[p] * (double)prm.C * es * tensors;
+    }
+    if (bytes > (double)sms * tb::CL_MAX_SMEM || prm.N > 65535) return false;
+    prm.period = (int32_t)(prm.C / std::gcd<int64_t>(prm.C, vec));
+    uint32_t rows[tb::GN_MAXP];  // below 2^31: they fit into shared memory
+    for (int p = 0; p < prm.P; ++p)
+        rows[p] = (uint32_t)((prm.spatial[p] * prm.C / vec + prm.period - 1) / prm.period);
+    double best = 1e30;
+    int32_t splits = 0, slabs = 0, columns = 0, cluster = 0, most = 0;
+    for (int s = 1; s <= prm.G && (s == 1 || prm.C / s * es >= 64); s *= 2) {
+        if (s > 1 && (prm.G % s != 0 || prm.C % vec != 0 || (prm.C / s) % vec != 0)) break;
+        prm.splits = s;
+        const int width = prm.period / s;
+        for (int b = 256; b <= 512; b *= 2) {
+            const int turns = (width + b - 1) / b, wide = (width + turns - 1) / turns;
+            for (int c = turns; c <= tb::CL_MAX_CLUSTER; c *= 2) {
+                const uint32_t side = (uint32_t)(b / wide) * (uint32_t)(c / turns);
+                uint32_t held = 0;
+                for (int p = 0; p < prm.P; ++p) held += (rows[p] + side - 1) / side;
+                if ((double)held * b * 16 > tb::CL_MAX_SMEM) continue;
+                const size_t smem = tb::gncl_fused_smem(prm, (int)dtype, grad, b, (int)held);
+                if (smem > (size_t)tb::CL_MAX_SMEM) continue;
+                const int per_sm = (int)std::min<size_t>((size_t)(227 * 1024) / (smem + 1024), (size_t)(512 / b));
+                const int64_t ctas = prm.N * s * c;
+                if ((double)ctas > cl_places(c, per_sm) * per_sm * sms) continue;
+                const double on_sm = (double)std::min<int64_t>(per_sm, (ctas + sms - 1) / sms);
+                const double us = on_sm * held * b * 16 * tensors / 25000.0 + 0.12 * held + (c > 1 ? 0.5 : 0.0);
+                if (us >= best * 0.999) continue;
+                best = us;
+                splits = s;
+                slabs = turns;
+                columns = wide;
+                cluster = c;
+                most = (int32_t)held;
+                *block = b;
+            }
+        }
+    }
+    prm.splits = splits;
+    prm.slabs = slabs;
+    prm.columns = columns;
+    prm.cluster = cluster;
+    prm.held = most;
+    return splits > 0;
 }
 
 // Element-wise passes: runs of rows of about the same length, as many as are
@@ -213,7 +277,7 @@ tb_status cl_grad_stats(tb::GnClParams& prm, tb_dtype dtype, int sms, cudaStream
 }
 
 tb_status cl_grad_apply(tb::GnClParams& prm, tb_dtype dtype, int sms, cudaStream_t s) {
-    TB_TRY(launched(tb::launch_gncl_coefs(prm, (int)dtype, s)));
+    TB_TRY(launched(tb::launch_gncl_coefs(prm, (int)dtype, false, s)));
     if (prm.N == 0) return TB_OK;
     const bool vector = cl_chunks(prm, dtype, true, true);
     int64_t ctas = 0;
@@ -280,6 +344,9 @@ TB_API tb_status tb_patch_group_norm_cl(const void* const* patches, void* const*
     if (N == 0 || C == 0) return TB_OK;
     int sms = 0;
     TB_TRY(tb::sm_count(&sms));
+    int block = 0;
+    if (cl_plan_fused(prm, dtype, false, sms, &block))
+        return launched(tb::launch_gncl_fused(prm, (int)dtype, false, block, as_stream(stream)));
     TB_TRY(cl_stats(prm, dtype, sms, as_stream(stream)));
     return cl_apply(prm, dtype, sms, as_stream(stream));
 }
@@ -335,6 +402,13 @@ TB_API tb_status tb_patch_group_norm_backward_cl(const void* const* patches, con
     if (C == 0 || (N == 0 && dgamma == nullptr && dbeta == nullptr)) return TB_OK;
     int sms = 0;
     TB_TRY(tb::sm_count(&sms));
+    int block = 0;
+    if (N > 0 && cl_plan_fused(prm, dtype, true, sms, &block)) {
+        TB_TRY(launched(tb::launch_gncl_fused(prm, (int)dtype, true, block, as_stream(stream))));
+        if (N == 1 || (dgamma == nullptr && dbeta == nullptr)) return TB_OK;
+        prm.coefs = nullptr;
+        return launched(tb::launch_gncl_coefs(prm, (int)dtype, true, as_stream(stream)));
+    }
     if (N > 0) TB_TRY(cl_grad_stats(prm, dtype, sms, as_stream(stream)));
     return cl_grad_apply(prm, dtype, sms, as_stream(stream));
 }

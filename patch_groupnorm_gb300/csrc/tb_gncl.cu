@@ -26,9 +26,8 @@ constexpr int DEPTH = 8;  // chunks of a thread on their way or in work
 // cluster read each other's tables, in a fixed order: one record per cluster.
 template <int DT, int VEC>
 __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_constant__ GnClParams p) {
-    using L = Lanes<VEC>;
     using W = ClWord<DT, VEC>;
-    constexpr int ES = elem_size(DT), NL = L::N;
+    constexpr int ES = elem_size(DT);
     extern __shared__ uint4 shared4[];
     using Stream = ClStream<DT, VEC, 1, DEPTH>;
     float* const stage_mean = reinterpret_cast<float*>(shared4 + Stream::SMEM / 16);  // [CL_BLOCK * VEC]
@@ -38,16 +37,13 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
     const int gs = G / p.splits, g0 = (int)blockIdx.y * gs, g1 = g0 + gs;  // this CTA's groups
     float4* const table = reinterpret_cast<float4*>(stage_n + CL_BLOCK);     // [gs]: (count, mean, M2)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int team = 32;  // threads that join a group's sums
-    while (team > 1 && gs * team > CL_BLOCK) team /= 2;
     for (int i = threadIdx.x; i < gs; i += CL_BLOCK) table[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     const ClUnit u = cl_unit(p);
     const int parts = p.parts[u.p], piece = u.piece, pieces = u.pieces, last = cl_last_piece(p, u.p, pieces);
     const ClRun run = cl_run<ES, VEC>(p.patches[u.p], p.spatial[u.p], p.C, u.n);
     const char* const patch = static_cast<const char*>(p.patches[u.p]);
     const int64_t bytes = p.N * run.elems * ES;
-    // channels that every chunk has side by side in one group: a power of two
-    const int unit = min(VEC, (K | run.head) & -(K | run.head));
+    const int unit = cl_unit_channels(VEC, K, run.head);
     grid_wait();
 
     // elements outside the whole chunks: the first piece's before, the last one's after; a lane each
@@ -68,9 +64,8 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
         const int j1 = min(j0 + p.columns, split0 + split_width);
         const ClPlace q = cl_place(p, j0, j1);
         const ClWalk w = cl_walk_share(p, q, u.p, piece, pieces, run.chunks);
-        typename L::T k[NL], s1[NL], s2[NL], mean[NL], m2[NL];
-#pragma unroll
-        for (int i = 0; i < NL; ++i) k[i] = mean[i] = m2[i] = L::splat(0.f);
+        ClMoments<DT, VEC> sums;
+        sums.clear();
         Stream in;
         in.base[0] = patch;
         in.at[0] = patch + (run.first + run.head) * ES + w.at * (int64_t)sizeof(W);
@@ -80,92 +75,14 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
         in.start(w.count, shared4);
         for (int done = 0, now; done < w.count; done += now) {
             now = min(min(FOLD, max(DEPTH, done)), w.count - done);
-#pragma unroll
-            for (int i = 0; i < NL; ++i) s1[i] = s2[i] = L::splat(0.f);
-            cl_each(in, now, [&](const W (&v)[1], int j) {
-                typename L::T f[NL];
-                to_lanes<DT, VEC>(v[0], f);
-                if (done + j == 0) {
-#pragma unroll
-                    for (int i = 0; i < NL; ++i) k[i] = mean[i] = f[i];
-                }
-#pragma unroll
-                for (int i = 0; i < NL; ++i) {
-                    const typename L::T d = vsub(f[i], k[i]);
-                    s1[i] = vadd(s1[i], d);
-                    s2[i] = vfma(d, d, s2[i]);
-                }
-            });
-            // the sums of `now` chunks about k join those of `done` before
-            const float nb = (float)now, total = (float)(done + now);
-            const auto inv = L::splat(1.f / nb), f = L::splat(nb / total), g = L::splat((float)done * (nb / total));
-#pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                const typename L::T d1 = vmul(s1[i], inv);                       // mean - k
-                const typename L::T bm2 = vsub(s2[i], vmul(s1[i], d1));
-                const typename L::T bmean = vadd(k[i], d1), d = vsub(bmean, mean[i]);
-                mean[i] = vfma(d, f, mean[i]);
-                m2[i] = vadd(m2[i], vfma(vmul(d, d), g, bm2));
-                k[i] = mean[i];
-            }
-        }
-        float fm[VEC], f2[VEC];
-        cl_values<VEC>(mean, fm);
-        cl_values<VEC>(m2, f2);
-        // rounding may leave a tiny negative sum of squares: it is a zero one
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) f2[i] = f2[i] < 0.f ? 0.f : f2[i];
-        // neighbours of one group are joined at once; their counts are equal
-#pragma unroll
-        for (int d = 1; d < VEC; d *= 2) {
-            if (d < unit) {
-                const float half = 0.5f * (float)(w.count * d);
-#pragma unroll
-                for (int i = 0; i < VEC; i += 2 * d) {
-                    const float away = fm[i + d] - fm[i];
-                    fm[i] = fmaf(0.5f, away, fm[i]);
-                    f2[i] = f2[i] + f2[i + d] + half * away * away;
-                }
-            }
+            cl_each(in, now, [&](const W (&v)[1], int j) { sums.add(v[0], done + j == 0); });
+            sums.fold(done, now);
         }
         __syncthreads();  // the table is set, or the columns before these are merged
-        const int each = VEC / unit;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            if (i % unit == 0) {
-                stage_mean[threadIdx.x * each + i / unit] = fm[i];
-                stage_m2[threadIdx.x * each + i / unit] = f2[i];
-            }
-        }
+        sums.store(w.count, unit, stage_mean, stage_m2);
         stage_n[threadIdx.x] = w.count * unit;
         __syncthreads();
-        // The units of a row that are one group's lie in phases [head + j0 * VEC, head +
-        // j1 * VEC), in runs of at most K / unit.  `team` threads join those of all rows
-        const int lo = (run.head + j0 * VEC) / unit, hi = (run.head + j1 * VEC) / unit, pitch = q.width * each;
-        const int Ku = K / unit, Cu = C / unit;
-        for (int first = 0; first < gs; first += CL_BLOCK / team) {
-            const int i = first + (int)threadIdx.x / team, c0 = (g0 + i) * Ku;
-            float n = 0.f, mean_g = 0.f, m2_g = 0.f;
-            if (i < gs) {
-                for (int m = lo >= c0 + Ku ? (lo - c0 - Ku) / Cu + 1 : 0; c0 + m * Cu < hi; ++m) {
-                    const int from = max(c0 + m * Cu, lo) - lo, len = min(c0 + m * Cu + Ku, hi) - lo - from;
-                    for (int e = (int)threadIdx.x % team; e < q.rows * len; e += team) {
-                        const int row = (int)((unsigned)e / (unsigned)len), at = row * pitch + from + (e - row * len);
-                        chan(n, mean_g, m2_g, (float)stage_n[(unsigned)at / (unsigned)each], stage_mean[at], stage_m2[at]);
-                    }
-                }
-            }
-            for (int d = team / 2; d >= 1; d >>= 1) {
-                const float nb = __shfl_down_sync(0xffffffffu, n, d), mb = __shfl_down_sync(0xffffffffu, mean_g, d);
-                chan(n, mean_g, m2_g, nb, mb, __shfl_down_sync(0xffffffffu, m2_g, d));
-            }
-            if (i < gs && threadIdx.x % team == 0) {
-                // table entries belong to this thread throughout
-                float4 t = table[i];
-                chan(t.x, t.y, t.z, n, mean_g, m2_g);
-                table[i] = t;
-            }
-        }
+        cl_join_groups<VEC>(q, run.head, j0, j1, unit, C, K, g0, gs, stage_mean, stage_m2, stage_n, table);
     }
     __syncthreads();
     if (VEC > 1 && warp == 0) {
@@ -183,7 +100,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
     if (p.cluster > 1) cluster_sync();
     else __syncthreads();
     // the cluster's tables: eight threads to a group, one for each CTA
-    static_assert(CL_MAX_CLUSTER == 8 && TB_GN_PARTS == 8, "eight threads read the CTAs' sums and write the parts");
+    static_assert(TB_GN_PARTS == 8, "the eight threads of a group write its parts");
     // whole rows have reps * K elements of every group; whoever has the last row has
     // whatever the others leave, and the first piece the head's too
     const int reps = (int)((unsigned)(p.period * VEC) / (unsigned)C), slices = p.cluster / p.slabs;
@@ -197,24 +114,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
     GnPartial* const out = p.partials + ((int64_t)u.p * p.N + u.n) * G * TB_GN_PARTS;
     for (int first = 0; first < gs; first += p.cluster * (CL_BLOCK / 8)) {
         const int i = first + u.rank * (CL_BLOCK / 8) + (int)threadIdx.x / 8, r = threadIdx.x & 7;
-        float n = 0.f, mean = 0.f, m2 = 0.f;
-        if (i < gs && r < p.cluster) {
-            if (p.cluster > 1) {
-                const uint2 lo = cluster_load8(smem_addr(table + i), (uint32_t)r);
-                n = __uint_as_float(lo.x);
-                mean = __uint_as_float(lo.y);
-                m2 = __uint_as_float(cluster_load8(smem_addr(table + i) + 8, (uint32_t)r).x);
-            } else {
-                n = table[i].x;
-                mean = table[i].y;
-                m2 = table[i].z;
-            }
-        }
-#pragma unroll
-        for (int d = 4; d >= 1; d >>= 1) {
-            const float nb = __shfl_down_sync(0xffffffffu, n, d), mb = __shfl_down_sync(0xffffffffu, mean, d);
-            chan(n, mean, m2, nb, mb, __shfl_down_sync(0xffffffffu, m2, d));
-        }
+        const float4 t = cl_join_cluster(table, i, gs, p.cluster);
         if (i >= gs) continue;
         GnPartial* const at = out + (int64_t)(g0 + i) * TB_GN_PARTS;
         if (!in_bounds(at, TB_GN_PARTS * sizeof(GnPartial), p.partials,
@@ -226,7 +126,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
         if (ends) count += p.spatial[u.p] * K - ahead - (p.rows[u.p] - 1) * reps * K;
         // a sample of less than a chunk has no rows
         if (p.rows[u.p] == 0) count = u.part == 0 ? p.spatial[u.p] * K : 0;
-        if (r == 0) at[u.part] = GnPartial{count, mean, m2};
+        if (r == 0) at[u.part] = GnPartial{count, t.y, t.z};
         if (u.part == 0 && r >= parts) at[r] = GnPartial{0, 0.f, 0.f};
     }
     if (p.cluster > 1) cluster_sync();  // nobody leaves while its table may be read
@@ -240,24 +140,6 @@ size_t stats_smem(int groups) {
 // --- normalisation ------------------------------------------------------------------
 
 constexpr int APPLY_DEPTH = 6;  // as DEPTH
-
-template <bool SILU>
-__device__ __forceinline__ f32x2 act(f32x2 z) {
-    if constexpr (SILU) {
-        float zl, zh, tl, th;
-        halves(z, zl, zh);
-        halves(vmul(z, pair(-1.4426950408889634f, -1.4426950408889634f)), tl, th);
-        float al, ah;
-        halves(vadd(pair(ex2_ftz(tl), ex2_ftz(th)), pair(1.f, 1.f)), al, ah);
-        return vmul(z, pair(rcp_ftz(al), rcp_ftz(ah)));
-    } else {
-        return z;
-    }
-}
-template <bool SILU>
-__device__ __forceinline__ float act(float z) {
-    return SILU ? z * rcp_ftz(1.f + ex2_ftz(z * -1.4426950408889634f)) : z;
-}
 
 template <int DT, int VEC, bool SILU>
 __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_apply_kernel(const __grid_constant__ GnClParams p) {

@@ -58,7 +58,7 @@ struct ClPlace {
 __device__ __forceinline__ ClPlace cl_place(const GnClParams& p, int j0, int j1) {
     ClPlace q;
     q.width = j1 - j0;
-    q.rows = CL_BLOCK / p.columns;  // of every slab, the last and narrower one too
+    q.rows = (int)blockDim.x / p.columns;  // of every slab, the last and narrower one too
     q.row = (int)threadIdx.x / q.width;
     q.col = j0 + (int)threadIdx.x - q.row * q.width;
     if (q.row >= q.rows) q.row = -1;
@@ -197,6 +197,152 @@ __device__ __forceinline__ void cl_each(Stream& in, int count, Body&& body) {
     }
 }
 
+// VEC values of a thread's channels as lanes.
+template <int VEC>
+__device__ __forceinline__ void cl_lanes(const float (&f)[VEC], typename Lanes<VEC>::T (&l)[Lanes<VEC>::N]) {
+    if constexpr (VEC == 1) {
+        l[0] = f[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) l[i] = pair(f[2 * i], f[2 * i + 1]);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void cl_values(const typename Lanes<VEC>::T (&l)[Lanes<VEC>::N], float (&f)[VEC]) {
+    if constexpr (VEC == 1) {
+        f[0] = l[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) halves(l[i], f[2 * i], f[2 * i + 1]);
+    }
+}
+
+// (n, mean, M2) joined with (bn, bmean, bm2), Chan's way.  Counts are floats, exact up
+// to 2^24 elements: they weigh means and squares here; a record's own count comes
+// from the sizes.
+__device__ __forceinline__ void chan(float& n, float& mean, float& m2, float bn, float bmean, float bm2) {
+    const float total = n + bn;
+    const float f = bn > 0.f ? __fdividef(bn, total) : 0.f;  // 1, exactly, where n is 0
+    const float d = n > 0.f && bn > 0.f ? bmean - mean : 0.f;
+    mean = n > 0.f ? fmaf(d, f, mean) : bmean;
+    m2 += fmaf(d * d, n * f, bn > 0.f ? bm2 : 0.f);
+    n = total;
+}
+
+// --- a thread's statistics --------------------------------------------------------
+
+// (mean, M2) of each of a thread's VEC channels, with the sums of what came since:
+// x - k and (x - k)^2, k the channel's first value, then its mean so far.
+template <int DT, int VEC>
+struct ClMoments {
+    using L = Lanes<VEC>;
+    using T = typename L::T;
+    static constexpr int NL = L::N;
+    T k[NL], s1[NL], s2[NL], mean[NL], m2[NL];
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) k[i] = mean[i] = m2[i] = s1[i] = s2[i] = L::splat(0.f);
+    }
+    __device__ __forceinline__ void add(const ClWord<DT, VEC>& v, bool first) {
+        T f[NL];
+        to_lanes<DT, VEC>(v, f);
+        if (first) {
+#pragma unroll
+            for (int i = 0; i < NL; ++i) k[i] = mean[i] = f[i];
+        }
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const T d = vsub(f[i], k[i]);
+            s1[i] = vadd(s1[i], d);
+            s2[i] = vfma(d, d, s2[i]);
+        }
+    }
+    // The sums of the last `now` chunks join those of `done` before (Chan).
+    __device__ __forceinline__ void fold(int done, int now) {
+        const float nb = (float)now, total = (float)(done + now);
+        const T inv = L::splat(1.f / nb), f = L::splat(nb / total), g = L::splat((float)done * (nb / total));
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const T d1 = vmul(s1[i], inv);  // mean - k
+            const T bm2 = vsub(s2[i], vmul(s1[i], d1));
+            const T bmean = vadd(k[i], d1), d = vsub(bmean, mean[i]);
+            mean[i] = vfma(d, f, mean[i]);
+            m2[i] = vadd(m2[i], vfma(vmul(d, d), g, bm2));
+            k[i] = mean[i];
+            s1[i] = s2[i] = L::splat(0.f);
+        }
+    }
+    // Into shared memory: `unit` neighbouring channels, which are one group's, as one.
+    __device__ __forceinline__ void store(int count, int unit, float* stage_mean, float* stage_m2) const {
+        float fm[VEC], f2[VEC];
+        cl_values<VEC>(mean, fm);
+        cl_values<VEC>(m2, f2);
+        // rounding may leave a tiny negative sum of squares: it is a zero one
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) f2[i] = f2[i] < 0.f ? 0.f : f2[i];
+#pragma unroll
+        for (int d = 1; d < VEC; d *= 2) {
+            if (d < unit) {  // their counts are equal
+                const float half = 0.5f * (float)(count * d);
+#pragma unroll
+                for (int i = 0; i < VEC; i += 2 * d) {
+                    const float away = fm[i + d] - fm[i];
+                    fm[i] = fmaf(0.5f, away, fm[i]);
+                    f2[i] = f2[i] + f2[i + d] + half * away * away;
+                }
+            }
+        }
+        const int each = VEC / unit;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            if (i % unit == 0) {
+                stage_mean[threadIdx.x * each + i / unit] = fm[i];
+                stage_m2[threadIdx.x * each + i / unit] = f2[i];
+            }
+        }
+    }
+};
+
+// Channels that every chunk has side by side in one group: a power of two.
+__device__ __forceinline__ int cl_unit_channels(int VEC, int K, int head) { return min(VEC, (K | head) & -(K | head)); }
+
+// The staged sums of groups g0 .. g0 + gs - 1 join those groups' entries of `table`
+// (count, mean, M2).  The units of a row that are one group's lie in phases [head + j0 *
+// VEC, head + j1 * VEC), in runs of at most K / unit; `team` threads join those of all
+// rows.  An entry belongs to one thread throughout.
+template <int VEC>
+__device__ __forceinline__ void cl_join_groups(const ClPlace& q, int head, int j0, int j1, int unit, int C, int K, int g0,
+                                               int gs, const float* stage_mean, const float* stage_m2,
+                                               const int* stage_n, float4* table) {
+    int team = 32;
+    while (team > 1 && gs * team > (int)blockDim.x) team /= 2;
+    const int each = VEC / unit, lo = (head + j0 * VEC) / unit, hi = (head + j1 * VEC) / unit, pitch = q.width * each;
+    const int Ku = K / unit, Cu = C / unit;
+    for (int first = 0; first < gs; first += (int)blockDim.x / team) {
+        const int i = first + (int)threadIdx.x / team, c0 = (g0 + i) * Ku;
+        float n = 0.f, mean = 0.f, m2 = 0.f;
+        if (i < gs) {
+            for (int m = lo >= c0 + Ku ? (lo - c0 - Ku) / Cu + 1 : 0; c0 + m * Cu < hi; ++m) {
+                const int from = max(c0 + m * Cu, lo) - lo, len = min(c0 + m * Cu + Ku, hi) - lo - from;
+                for (int e = (int)threadIdx.x % team; e < q.rows * len; e += team) {
+                    const int row = (int)((unsigned)e / (unsigned)len), at = row * pitch + from + (e - row * len);
+                    chan(n, mean, m2, (float)stage_n[(unsigned)at / (unsigned)each], stage_mean[at], stage_m2[at]);
+                }
+            }
+        }
+        for (int d = team / 2; d >= 1; d >>= 1) {
+            const float nb = __shfl_down_sync(0xffffffffu, n, d), mb = __shfl_down_sync(0xffffffffu, mean, d);
+            chan(n, mean, m2, nb, mb, __shfl_down_sync(0xffffffffu, m2, d));
+        }
+        if (i < gs && threadIdx.x % team == 0) {
+            float4 t = table[i];
+            chan(t.x, t.y, t.z, n, mean, m2);
+            table[i] = t;
+        }
+    }
+}
+
 // --- thread-block clusters ------------------------------------------------------
 
 __device__ __forceinline__ void cluster_sync() {
@@ -209,6 +355,32 @@ __device__ __forceinline__ uint2 cluster_load8(uint32_t at, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(at), "r"(rank));
     asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(far) : "memory");
     return v;
+}
+
+// (count, mean, M2) of entry `i` of the cluster's tables: eight threads to an entry,
+// one for each CTA; the first of them holds the result.
+__device__ __forceinline__ float4 cl_join_cluster(const float4* table, int i, int gs, int cluster) {
+    static_assert(CL_MAX_CLUSTER == 8, "eight threads read the CTAs' sums");
+    const int r = threadIdx.x & 7;
+    float n = 0.f, mean = 0.f, m2 = 0.f;
+    if (i < gs && r < cluster) {
+        if (cluster > 1) {
+            const uint2 lo = cluster_load8(smem_addr(table + i), (uint32_t)r);
+            n = __uint_as_float(lo.x);
+            mean = __uint_as_float(lo.y);
+            m2 = __uint_as_float(cluster_load8(smem_addr(table + i) + 8, (uint32_t)r).x);
+        } else {
+            n = table[i].x;
+            mean = table[i].y;
+            m2 = table[i].z;
+        }
+    }
+#pragma unroll
+    for (int d = 4; d >= 1; d >>= 1) {
+        const float nb = __shfl_down_sync(0xffffffffu, n, d), mb = __shfl_down_sync(0xffffffffu, mean, d);
+        chan(n, mean, m2, nb, mb, __shfl_down_sync(0xffffffffu, m2, d));
+    }
+    return make_float4(n, mean, m2, 0.f);
 }
 
 // The (patch, sample, part) of a statistics CTA, its rank in the part's cluster, its
@@ -237,19 +409,7 @@ __device__ __forceinline__ ClUnit cl_unit(const GnClParams& prm) {
     return u;
 }
 
-// (n, mean, M2) joined with (bn, bmean, bm2), Chan's way.  Counts are floats, exact up
-// to 2^24 elements: they weigh means and squares here; a record's own count comes
-// from the sizes.
-__device__ __forceinline__ void chan(float& n, float& mean, float& m2, float bn, float bmean, float bm2) {
-    const float total = n + bn;
-    const float f = bn > 0.f ? __fdividef(bn, total) : 0.f;  // 1, exactly, where n is 0
-    const float d = n > 0.f && bn > 0.f ? bmean - mean : 0.f;
-    mean = n > 0.f ? fmaf(d, f, mean) : bmean;
-    m2 += fmaf(d * d, n * f, bn > 0.f ? bm2 : 0.f);
-    n = total;
-}
-
-// (mean, rstd, count) of groups [g0, g1) of sample n into out[0 .. g1 - g0): eight
+// (mean, rstd) of groups [g0, g1) of sample n into out[0 .. g1 - g0): eight
 // threads to a group, four of whose record sets are on their way at once (a wait for
 // one after the other would hold the CTA up for microseconds).  A NaN stays one.
 __device__ __forceinline__ void cl_group_stats(const GnClParams& p, int64_t n, int g0, int g1, float2* out) {
@@ -326,23 +486,49 @@ __device__ __forceinline__ void cl_weights(const GnClParams& p, int head, int ph
     }
 }
 
-// VEC values of a thread's channels as lanes.
-template <int VEC>
-__device__ __forceinline__ void cl_lanes(const float (&f)[VEC], typename Lanes<VEC>::T (&l)[Lanes<VEC>::N]) {
-    if constexpr (VEC == 1) {
-        l[0] = f[0];
+// --- the activation -------------------------------------------------------------------
+
+// silu(z), or z.
+template <bool SILU>
+__device__ __forceinline__ f32x2 act(f32x2 z) {
+    if constexpr (SILU) {
+        float zl, zh, tl, th;
+        halves(z, zl, zh);
+        halves(vmul(z, pair(-1.4426950408889634f, -1.4426950408889634f)), tl, th);
+        float al, ah;
+        halves(vadd(pair(ex2_ftz(tl), ex2_ftz(th)), pair(1.f, 1.f)), al, ah);
+        return vmul(z, pair(rcp_ftz(al), rcp_ftz(ah)));
     } else {
-#pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) l[i] = pair(f[2 * i], f[2 * i + 1]);
+        return z;
     }
 }
-template <int VEC>
-__device__ __forceinline__ void cl_values(const typename Lanes<VEC>::T (&l)[Lanes<VEC>::N], float (&f)[VEC]) {
-    if constexpr (VEC == 1) {
-        f[0] = l[0];
+template <bool SILU>
+__device__ __forceinline__ float act(float z) {
+    return SILU ? z * rcp_ftz(1.f + ex2_ftz(z * -1.4426950408889634f)) : z;
+}
+
+// dz = dy * silu'(z), or dy.  e^-z and the reciprocal are approximate (2^-22 each);
+// e^-z overflows for z < -88, where s = 0 and dz = 0.
+template <bool SILU>
+__device__ __forceinline__ f32x2 dz_of(f32x2 dy, f32x2 z) {
+    if constexpr (SILU) {
+        const f32x2 one = pair(1.f, 1.f);
+        float tl, th, al, ah;
+        halves(vmul(z, pair(-1.4426950408889634f, -1.4426950408889634f)), tl, th);
+        halves(vadd(pair(ex2_ftz(tl), ex2_ftz(th)), one), al, ah);
+        const f32x2 s = pair(rcp_ftz(al), rcp_ftz(ah));
+        return vmul(dy, vmul(s, vfma(z, vsub(one, s), one)));
     } else {
-#pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) halves(l[i], f[2 * i], f[2 * i + 1]);
+        return dy;
+    }
+}
+template <bool SILU>
+__device__ __forceinline__ float dz_of(float dy, float z) {
+    if constexpr (SILU) {
+        const float s = rcp_ftz(1.f + ex2_ftz(z * -1.4426950408889634f));
+        return dy * (s * fmaf(z, 1.f - s, 1.f));
+    } else {
+        return dy;
     }
 }
 
@@ -358,21 +544,18 @@ __device__ __forceinline__ void cl_store_elem(void* base, int64_t i, float v) {
     reinterpret_cast<ClWord<DT, 1>*>(base)[i] = pack<DT, 1>(f);
 }
 
-// Shared memory of the largest call (CL_MAXC channels in as many groups).  A kernel
-// that needs more than the default is given this limit whatever the call's size:
-// calls of other threads may set it between this one's two steps.
-constexpr int CL_MAX_SMEM = 216 * 1024;
-
 // Launches `fn` with programmatic stream serialisation in clusters of `cluster` CTAs.
+// A kernel that needs more shared memory than the default is given the limit of the
+// largest call: calls of other threads may set it between this one's two steps.
 inline cudaError_t launch_cluster(void (*fn)(const GnClParams), const GnClParams& p, dim3 grid, int cluster, size_t smem,
-                                  cudaStream_t s) {
+                                  cudaStream_t s, int block = CL_BLOCK) {
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, CL_MAX_SMEM);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(CL_BLOCK, 1, 1);
+    cfg.blockDim = dim3((unsigned)block, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];

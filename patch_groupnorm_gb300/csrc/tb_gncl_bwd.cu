@@ -16,31 +16,6 @@
 namespace tb {
 namespace {
 
-// dz (see the top of this file).  e^-z and the reciprocal are approximate (2^-22
-// each); e^-z overflows for z < -88, where s = 0 and dz = 0.
-template <bool SILU>
-__device__ __forceinline__ f32x2 dz_of(f32x2 dy, f32x2 z) {
-    if constexpr (SILU) {
-        const f32x2 one = pair(1.f, 1.f);
-        float tl, th, al, ah;
-        halves(vmul(z, pair(-1.4426950408889634f, -1.4426950408889634f)), tl, th);
-        halves(vadd(pair(ex2_ftz(tl), ex2_ftz(th)), one), al, ah);
-        const f32x2 s = pair(rcp_ftz(al), rcp_ftz(ah));
-        return vmul(dy, vmul(s, vfma(z, vsub(one, s), one)));
-    } else {
-        return dy;
-    }
-}
-template <bool SILU>
-__device__ __forceinline__ float dz_of(float dy, float z) {
-    if constexpr (SILU) {
-        const float s = rcp_ftz(1.f + ex2_ftz(z * -1.4426950408889634f));
-        return dy * (s * fmaf(z, 1.f - s, 1.f));
-    } else {
-        return dy;
-    }
-}
-
 // --- the records ------------------------------------------------------------------
 
 constexpr int FOLD = 60;  // chunks between two foldings of a thread's sums: whole turns of DEPTH
@@ -231,13 +206,13 @@ __global__ void __launch_bounds__(CL_BLOCK) gncl_coefs_kernel(const __grid_const
     __shared__ float2 sums[CL_BLOCK / 32];
     __shared__ float2 stats[1];
     const int C = (int)p.C, K = C / p.G;
-    const int64_t units = p.N * p.G, set = p.N * C * TB_GN_PARTS;
+    const int64_t units = p.coefs != nullptr ? p.N * p.G : 0, set = p.N * C * TB_GN_PARTS;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t size = (int64_t)p.R * set * (int64_t)sizeof(float2);
     grid_wait();
     // what came before is done, so dx's launch may fetch its first chunks of x and dy
     // while this one works; it waits before it reads a constant or writes a chunk
-    pdl_trigger_dependents();
+    if (units > 0) pdl_trigger_dependents();
     if ((int64_t)blockIdx.x < units) {
         const int64_t n = blockIdx.x / p.G;
         const int g = (int)(blockIdx.x - n * p.G);
@@ -417,9 +392,9 @@ cudaError_t launch_gncl_grad_stats(const GnClParams& p, int dtype, bool vector, 
     return stats_launch<BF16>(p, vector, ctas, s);
 }
 
-cudaError_t launch_gncl_coefs(const GnClParams& p, int dtype, cudaStream_t s) {
+cudaError_t launch_gncl_coefs(const GnClParams& p, int dtype, bool weights_only, cudaStream_t s) {
     const int64_t weights = p.dgamma != nullptr || p.dbeta != nullptr ? (p.C + COEF_CHANNELS - 1) / COEF_CHANNELS : 0;
-    const dim3 grid((unsigned)(p.N * p.G + weights), 1, 1);
+    const dim3 grid((unsigned)((weights_only ? 0 : p.N * p.G) + weights), 1, 1);
     void (*const fn)(const GnClParams) = dtype == F32 ? gncl_coefs_kernel<F32>
                                          : dtype == F16 ? gncl_coefs_kernel<F16>
                                                         : gncl_coefs_kernel<BF16>;

@@ -1,0 +1,400 @@
+// tb_gncl_fused.cu -- channels-last PatchGroupNorm in one launch, forward and
+// backward, where the tensors fit into shared memory.
+//
+// A cluster of up to eight CTAs takes one sample's groups, or as many of them as
+// whole chunks allow (a split), of all patches.  Its CTAs copy their chunks of x (and
+// of dy) into shared memory once, sum them as they arrive, read each other's sums
+// (one barrier of the cluster), and go over the same chunks again from shared
+// memory: every tensor is read once, and what two or three launches of the general
+// path spend on starting and on waiting for each other is spent once.  Chunks are a
+// thread's own from its copy to its result, so the copies need no barrier.
+//
+// Taken where every patch starts on 16 bytes, samples and splits are whole chunks, and
+// all clusters find room at once (cl_plan_fused).
+#include "tb_gncl.cuh"
+
+namespace tb {
+namespace {
+
+// A thread's chunks of all patches, in the order in which they are copied: chunk k of
+// NS tensors in slots k * NS .. of its column of the ring.
+template <int NS>
+struct ClHeld {
+    const GnClParams& p;
+    ClPlace q;
+    int64_t sample;          // n
+    int slice, slices, vec;  // this CTA's blocks of rows: slice, slice + slices, ...
+    uint32_t slot;
+    int count;               // chunks
+    int sure;                // of these, known to have arrived
+
+    __device__ __forceinline__ int chunks_of(int pt) const { return (int)(p.spatial[pt] * p.C / vec); }
+    // Calls body(patch, chunk of the sample, k) for every chunk.
+    template <typename Body>
+    __device__ __forceinline__ void each(Body&& body) {
+        int k = 0;
+        if (q.row >= 0) {
+            for (int pt = 0; pt < p.P; ++pt) {
+                const int chunks = chunks_of(pt), stride = slices * q.rows * p.period;
+                for (int at = (slice * q.rows + q.row) * p.period + q.col; at < chunks; at += stride, ++k) body(pt, at, k);
+            }
+        }
+        count = k;
+    }
+    // Chunk k has arrived: waits in steps, as the number of copies that may still be
+    // on their way is part of the instruction.
+    __device__ __forceinline__ void arrived(int k) {
+        if (k < sure) return;
+        const int after = count - k - 1;
+        if (after >= 16) {
+            asm volatile("cp.async.wait_group 16;" ::: "memory");
+            sure = count - 16;
+        } else if (after >= 8) {
+            asm volatile("cp.async.wait_group 8;" ::: "memory");
+            sure = count - 8;
+        } else if (after >= 4) {
+            asm volatile("cp.async.wait_group 4;" ::: "memory");
+            sure = count - 4;
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            sure = count;
+        }
+    }
+    __device__ __forceinline__ uint32_t at(int k, int tensor) const {
+        return slot + (uint32_t)((k * NS + tensor) * (int)blockDim.x * 16);
+    }
+};
+
+__device__ __forceinline__ void copy16(uint32_t to, const char* from, const char* base, int64_t bytes, uint32_t* status) {
+    if (in_bounds(from, 16, base, bytes, status))
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// Where a CTA stands: cluster = (sample, split), splits fastest; in a cluster the slabs
+// of the split's columns, then the slices of the rows.
+struct ClSeat {
+    int64_t n;
+    int split, rank, g0, gs, j0, j1;
+    template <int NS>
+    __device__ __forceinline__ static ClSeat take(const GnClParams& p, int vec, void* ring, ClHeld<NS>& held) {
+        ClSeat s;
+        const int unit = (int)blockIdx.x / p.cluster;
+        s.rank = (int)blockIdx.x - unit * p.cluster;
+        s.n = unit / p.splits;
+        s.split = unit - (int)s.n * p.splits;
+        s.gs = p.G / p.splits;
+        s.g0 = s.split * s.gs;
+        const int width = p.period / p.splits, first = s.split * width;
+        s.j0 = first + s.rank % p.slabs * p.columns;
+        s.j1 = min(s.j0 + p.columns, first + width);
+        held.q = cl_place(p, s.j0, s.j1);
+        held.sample = s.n;
+        held.slice = s.rank / p.slabs;
+        held.slices = p.cluster / p.slabs;
+        held.vec = vec;
+        held.slot = smem_addr(ring) + threadIdx.x * 16;
+        held.sure = 0;
+        return s;
+    }
+};
+
+// --- forward ------------------------------------------------------------------------
+
+template <int DT, bool SILU, int BLOCK>
+__global__ void __launch_bounds__(BLOCK, 512 / BLOCK) gncl_fused_kernel(const __grid_constant__ GnClParams p) {
+    constexpr int ES = elem_size(DT), VEC = 16 / ES;
+    using L = Lanes<VEC>;
+    using W = ClWord<DT, VEC>;
+    constexpr int NL = L::N;
+    extern __shared__ uint4 shared4[];
+    float* const stage_mean = reinterpret_cast<float*>(shared4 + p.held * BLOCK);  // [BLOCK * VEC]
+    float* const stage_m2 = stage_mean + BLOCK * VEC;                              // [BLOCK * VEC]
+    int* const stage_n = reinterpret_cast<int*>(stage_m2 + BLOCK * VEC);           // [BLOCK]
+    float4* const table = reinterpret_cast<float4*>(stage_n + BLOCK);              // [gs]: (count, mean, M2)
+    const int C = (int)p.C, K = C / p.G;
+    ClHeld<1> held{p};
+    const ClSeat seat = ClSeat::take(p, VEC, shared4, held);
+    float2* const stats = reinterpret_cast<float2*>(table + seat.gs);              // [gs]: (mean, rstd)
+    for (int i = threadIdx.x; i < seat.gs; i += BLOCK) table[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    grid_wait();
+    held.each([&](int pt, int at, int k) {
+        const char* const patch = static_cast<const char*>(p.patches[pt]);
+        const int64_t bytes = p.spatial[pt] * C * ES;
+        copy16(held.at(k, 0), patch + seat.n * bytes + (int64_t)at * 16, patch, p.N * bytes, p.status);
+        copies_end();
+    });
+    float fm[VEC], fa[VEC], fb[VEC];
+    cl_weights<DT, VEC>(p, 0, held.q.col * VEC, fa, fb);
+    ClMoments<DT, VEC> sums;
+    sums.clear();
+    for (int done = 0, now; done < held.count; done += now) {
+        now = min(max(8, done), held.count - done);
+        for (int k = done; k < done + now; ++k) {
+            held.arrived(k);
+            sums.add(smem_load<W>(held.at(k, 0)), k == 0);
+        }
+        sums.fold(done, now);
+    }
+    const int unit = cl_unit_channels(VEC, K, 0);
+    sums.store(held.count, unit, stage_mean, stage_m2);
+    stage_n[threadIdx.x] = held.count * unit;
+    __syncthreads();
+    cl_join_groups<VEC>(held.q, 0, seat.j0, seat.j1, unit, C, K, seat.g0, seat.gs, stage_mean, stage_m2, stage_n, table);
+    if (p.cluster > 1) cluster_sync();
+    else __syncthreads();
+    // every CTA joins all of its split's groups for itself
+    for (int first = 0; first < seat.gs; first += BLOCK / 8) {
+        const int i = first + (int)threadIdx.x / 8, r = threadIdx.x & 7;
+        const float4 t = cl_join_cluster(table, i, seat.gs, p.cluster);
+        // the team's first thread has the result
+        const float mean = __shfl_sync(0xffffffffu, t.y, threadIdx.x & 24), m2 = __shfl_sync(0xffffffffu, t.z, threadIdx.x & 24);
+        if (i >= seat.gs) continue;
+        if (r == 0) {
+            const float var = t.x > 0.f ? t.z / t.x : 0.f;  // biased: divided by the count
+            stats[i] = make_float2(t.y, 1.0f / sqrtf(var + p.eps));
+        }
+        if (seat.rank != 0) continue;
+        // the records of all patches together are one, the others are empty
+        int64_t count = 0;
+        for (int pt = 0; pt < p.P; ++pt) count += p.spatial[pt] * K;
+        for (int pt = 0; pt < p.P; ++pt) {
+            GnPartial* const at = p.partials + (((int64_t)pt * p.N + seat.n) * p.G + seat.g0 + i) * TB_GN_PARTS + r;
+            if (in_bounds(at, sizeof(GnPartial), p.partials,
+                          (int64_t)p.P * p.N * p.G * TB_GN_PARTS * (int64_t)sizeof(GnPartial), p.status))
+                *at = pt == 0 && r == 0 ? GnPartial{count, mean, m2} : GnPartial{0, 0.f, 0.f};
+        }
+    }
+    __syncthreads();
+    ClChannel ch(0, held.q.col * VEC, C, K);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        const float2 s = held.q.row >= 0 ? stats[ch.g - seat.g0] : make_float2(0.f, 0.f);
+        fm[i] = s.x;
+        fa[i] *= s.y;
+        ch.next();
+    }
+    typename L::T mean[NL], ga[NL], be[NL];
+    cl_lanes<VEC>(fm, mean);
+    cl_lanes<VEC>(fa, ga);
+    cl_lanes<VEC>(fb, be);
+    held.each([&](int pt, int at, int k) {
+        typename L::T f[NL];
+        to_lanes<DT, VEC>(smem_load<W>(held.at(k, 0)), f);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) f[i] = act<SILU>(vfma(vsub(f[i], mean[i]), ga[i], be[i]));
+        char* const out = static_cast<char*>(p.outs[pt]);
+        const int64_t bytes = p.spatial[pt] * C * ES;
+        char* const to = out + seat.n * bytes + (int64_t)at * 16;
+        if (in_bounds(to, 16, out, p.N * bytes, p.status)) *reinterpret_cast<W*>(to) = from_lanes<DT, VEC>(f);
+    });
+    if (p.cluster > 1) cluster_sync();  // nobody leaves while its table may be read
+}
+
+// --- backward -----------------------------------------------------------------------
+
+template <int DT, bool SILU, int BLOCK>
+__global__ void __launch_bounds__(BLOCK, 512 / BLOCK) gncl_fused_grad_kernel(const __grid_constant__ GnClParams p) {
+    constexpr int ES = elem_size(DT), VEC = 16 / ES;
+    using L = Lanes<VEC>;
+    using W = ClWord<DT, VEC>;
+    constexpr int NL = L::N;
+    extern __shared__ uint4 shared4[];
+    float2* const stage = reinterpret_cast<float2*>(shared4 + p.held * 2 * BLOCK);  // [BLOCK * VEC]: (sum dz, sum dz * d)
+    float2* const table = stage + BLOCK * VEC;                                      // [cs]: (sum dz, sum dz * xhat)
+    const int C = (int)p.C, K = C / p.G;
+    ClHeld<2> held{p};
+    const ClSeat seat = ClSeat::take(p, VEC, shared4, held);
+    const int cs = seat.gs * K, c0 = seat.g0 * K;                // the split's channels
+    float2* const whole = table + cs;                            // [cs]: the cluster's sums
+    float4* const coefs = reinterpret_cast<float4*>(whole + cs); // [gs]: (mean, rstd, u, v)
+    float2* const stats = reinterpret_cast<float2*>(coefs + seat.gs);  // [gs]: (mean, rstd)
+    for (int i = threadIdx.x; i < cs; i += BLOCK) table[i] = make_float2(0.f, 0.f);
+    grid_wait();
+    held.each([&](int pt, int at, int k) {
+        const char* const patch = static_cast<const char*>(p.patches[pt]);
+        const char* const grad = static_cast<const char*>(p.grads[pt]);
+        const int64_t bytes = p.spatial[pt] * C * ES, from = seat.n * bytes + (int64_t)at * 16;
+        copy16(held.at(k, 0), patch + from, patch, p.N * bytes, p.status);
+        copy16(held.at(k, 1), grad + from, grad, p.N * bytes, p.status);
+        copies_end();
+    });
+    float f0[VEC], f1[VEC], f2[VEC];
+    cl_weights<DT, VEC>(p, 0, held.q.col * VEC, f1, f2);
+    cl_group_stats(p, seat.n, seat.g0, seat.g0 + seat.gs, stats);
+    __syncthreads();
+    {
+        ClChannel ch(0, held.q.col * VEC, C, K);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const float2 s = held.q.row >= 0 ? stats[ch.g - seat.g0] : make_float2(0.f, 0.f);
+            f0[i] = s.x;
+            f1[i] *= s.y;
+            ch.next();
+        }
+    }
+    typename L::T mean[NL], ga[NL], be[NL], sb[NL], sa[NL];
+    cl_lanes<VEC>(f0, mean);
+    cl_lanes<VEC>(f1, ga);
+    cl_lanes<VEC>(f2, be);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) sb[i] = sa[i] = L::splat(0.f);
+    for (int k = 0; k < held.count; ++k) {
+        held.arrived(k);
+        typename L::T f[NL], dy[NL];
+        to_lanes<DT, VEC>(smem_load<W>(held.at(k, 0)), f);
+        to_lanes<DT, VEC>(smem_load<W>(held.at(k, 1)), dy);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const typename L::T d = vsub(f[i], mean[i]);
+            const typename L::T dz = dz_of<SILU>(dy[i], vfma(d, ga[i], be[i]));
+            sb[i] = vadd(sb[i], dz);
+            sa[i] = vfma(dz, d, sa[i]);
+        }
+    }
+    {
+        float b[VEC], a[VEC];
+        cl_values<VEC>(sb, b);
+        cl_values<VEC>(sa, a);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) stage[threadIdx.x * VEC + i] = make_float2(b[i], a[i]);
+    }
+    __syncthreads();
+    const int lo = seat.j0 * VEC, hi = seat.j1 * VEC, pitch = held.q.width * VEC;
+    for (int i = threadIdx.x; i < cs; i += BLOCK) {
+        const int c = c0 + i;
+        float2 t = make_float2(0.f, 0.f);
+        for (int at = c + (lo > c ? (lo - c + C - 1) / C * C : 0); at < hi; at += C) {
+            for (int r = 0; r < held.q.rows; ++r) {
+                const float2 v = stage[r * pitch + at - lo];
+                t.x += v.x;
+                t.y += v.y;
+            }
+        }
+        t.y *= stats[i / K].y;
+        table[i] = t;
+    }
+    if (p.cluster > 1) cluster_sync();
+    else __syncthreads();
+    // every CTA joins all of its split's channels for itself
+    for (int i = threadIdx.x; i < cs; i += BLOCK) {
+        float2 t = table[i];
+        if (p.cluster > 1) {
+            t = make_float2(0.f, 0.f);
+            uint2 v[CL_MAX_CLUSTER];
+#pragma unroll
+            for (int r = 0; r < CL_MAX_CLUSTER; ++r)  // all on their way before the first sum
+                v[r] = r < p.cluster ? cluster_load8(smem_addr(table + i), (uint32_t)r) : make_uint2(0u, 0u);
+#pragma unroll
+            for (int r = 0; r < CL_MAX_CLUSTER; ++r) {
+                t.x += __uint_as_float(v[r].x);
+                t.y += __uint_as_float(v[r].y);
+            }
+        }
+        whole[i] = t;
+        if (seat.rank != 0) continue;
+        if (p.N == 1) {
+            if (p.dgamma != nullptr) store_weight(p.dgamma, DT, c0 + i, t.y);
+            if (p.dbeta != nullptr) store_weight(p.dbeta, DT, c0 + i, t.x);
+        } else if (p.dgamma != nullptr || p.dbeta != nullptr) {
+            // one record a sample, for the launch that adds the samples up
+            for (int pt = 0; pt < p.P; ++pt) {
+                float2* const at = p.grad_partials + (((int64_t)pt * p.N + seat.n) * C + c0 + i) * TB_GN_PARTS;
+                if (!in_bounds(at, TB_GN_PARTS * sizeof(float2), p.grad_partials,
+                               (int64_t)p.P * p.N * C * TB_GN_PARTS * (int64_t)sizeof(float2), p.status))
+                    continue;
+#pragma unroll
+                for (int r = 0; r < TB_GN_PARTS; ++r) at[r] = pt == 0 && r == 0 ? t : make_float2(0.f, 0.f);
+            }
+        }
+    }
+    __syncthreads();
+    // (mean, rstd, u, v) of the groups: eight threads to a group
+    int64_t count = 0;
+    for (int pt = 0; pt < p.P; ++pt) count += p.spatial[pt] * K;
+    const float inv = count > 0 ? 1.f / (float)count : 0.f;
+    for (int first = 0; first < seat.gs; first += BLOCK / 8) {
+        const int i = first + (int)threadIdx.x / 8;
+        float B = 0.f, A = 0.f;
+        if (i < seat.gs) {
+            for (int j = threadIdx.x & 7; j < K; j += 8) {
+                const float w = weight_at(p.gamma, DT, c0 + i * K + j, 1.f);
+                const float2 t = whole[i * K + j];
+                B = fmaf(w, t.x, B);
+                A = fmaf(w, t.y, A);
+            }
+        }
+#pragma unroll
+        for (int d = 4; d >= 1; d >>= 1) {
+            B += __shfl_xor_sync(0xffffffffu, B, d);
+            A += __shfl_xor_sync(0xffffffffu, A, d);
+        }
+        if (i < seat.gs && (threadIdx.x & 7) == 0) {
+            const float2 s = stats[i];
+            coefs[i] = make_float4(s.x, s.y, -(s.y * s.y) * (A * inv), -s.y * (B * inv));
+        }
+    }
+    __syncthreads();
+    typename L::T cu[NL], cv[NL];
+    {
+        float u[VEC], v[VEC];
+        ClChannel ch(0, held.q.col * VEC, C, K);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const float4 k = held.q.row >= 0 ? coefs[ch.g - seat.g0] : make_float4(0.f, 0.f, 0.f, 0.f);
+            u[i] = k.z;
+            v[i] = k.w;
+            ch.next();
+        }
+        cl_lanes<VEC>(u, cu);
+        cl_lanes<VEC>(v, cv);
+    }
+    held.each([&](int pt, int at, int k) {
+        typename L::T f[NL], dy[NL];
+        to_lanes<DT, VEC>(smem_load<W>(held.at(k, 0)), f);
+        to_lanes<DT, VEC>(smem_load<W>(held.at(k, 1)), dy);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const typename L::T d = vsub(f[i], mean[i]);
+            const typename L::T dz = dz_of<SILU>(dy[i], vfma(d, ga[i], be[i]));
+            f[i] = vfma(dz, ga[i], vfma(d, cu[i], cv[i]));
+        }
+        char* const out = static_cast<char*>(p.outs[pt]);
+        const int64_t bytes = p.spatial[pt] * C * ES;
+        char* const to = out + seat.n * bytes + (int64_t)at * 16;
+        if (in_bounds(to, 16, out, p.N * bytes, p.status)) *reinterpret_cast<W*>(to) = from_lanes<DT, VEC>(f);
+    });
+    if (p.cluster > 1) cluster_sync();  // nobody leaves while its table may be read
+}
+
+template <int DT, int BLOCK>
+cudaError_t fused_launch(const GnClParams& p, bool grad, cudaStream_t s) {
+    const dim3 grid((unsigned)(p.N * p.splits * p.cluster), 1, 1);
+    void (*const fn)(const GnClParams) =
+        grad ? (p.silu ? gncl_fused_grad_kernel<DT, true, BLOCK> : gncl_fused_grad_kernel<DT, false, BLOCK>)
+             : (p.silu ? gncl_fused_kernel<DT, true, BLOCK> : gncl_fused_kernel<DT, false, BLOCK>);
+    return launch_cluster(fn, p, grid, p.cluster, gncl_fused_smem(p, DT, grad, BLOCK, p.held), s, BLOCK);
+}
+
+template <int DT>
+cudaError_t fused_launch(const GnClParams& p, bool grad, int block, cudaStream_t s) {
+    return block == 512 ? fused_launch<DT, 512>(p, grad, s) : fused_launch<DT, 256>(p, grad, s);
+}
+
+}  // namespace
+
+size_t gncl_fused_smem(const GnClParams& p, int dtype, bool grad, int block, int held) {
+    const int vec = 16 / elem_size(dtype);
+    const size_t gs = (size_t)(p.G / p.splits), cs = (size_t)(p.C / p.splits);
+    const size_t stage = (size_t)block * vec * 8;
+    return grad ? (size_t)held * 2 * block * 16 + stage + cs * 16 + gs * 24
+                : (size_t)held * block * 16 + stage + (size_t)block * 4 + gs * 24;
+}
+
+cudaError_t launch_gncl_fused(const GnClParams& p, int dtype, bool grad, int block, cudaStream_t s) {
+    if (dtype == F32) return fused_launch<F32>(p, grad, block, s);
+    if (dtype == F16) return fused_launch<F16>(p, grad, block, s);
+    return fused_launch<BF16>(p, grad, block, s);
+}
+
+}  // namespace tb

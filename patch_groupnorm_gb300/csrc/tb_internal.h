@@ -472,7 +472,8 @@ cudaError_t launch_gn_grad(const GnGradParams& p, int dtype, bool ring, int sms,
 // ---------------------------------------------------------------------------
 
 constexpr int CL_BLOCK = 256;          // threads per CTA
-constexpr int CL_MAX_CLUSTER = 8;     // CTAs of a statistics cluster
+constexpr int CL_MAX_CLUSTER = 8;     // CTAs of a cluster
+constexpr int CL_MAX_SMEM = 224 * 1024;  // shared memory of a CTA at most
 constexpr int CL_MAXC = TB_GN_CL_MAX_CHANNELS;
 
 // Chunks, columns, rows and periods: see tb_gncl.cuh.
@@ -503,6 +504,7 @@ struct GnClParams {
     int64_t rows[GN_MAXP];         // statistics: rows of a sample of patch p, and their blocks for
     int32_t share[GN_MAXP];        // each piece (each of the first `extra` pieces has another)
     int32_t extra[GN_MAXP];
+    int32_t held;                  // one launch: chunks of each tensor that a thread holds at most
     uint32_t* status;              // bounds-checked build: device status word (else null)
 };
 static_assert(sizeof(GnClParams) <= 32000, "kernel parameter block too large");
@@ -512,7 +514,11 @@ static_assert(sizeof(GnClParams) <= 32000, "kernel parameter block too large");
 cudaError_t launch_gncl_stats(const GnClParams& p, int dtype, bool vector, int64_t ctas, cudaStream_t s);
 cudaError_t launch_gncl_apply(const GnClParams& p, int dtype, bool vector, int64_t ctas, cudaStream_t s);
 cudaError_t launch_gncl_grad_stats(const GnClParams& p, int dtype, bool vector, int64_t ctas, cudaStream_t s);
-cudaError_t launch_gncl_coefs(const GnClParams& p, int dtype, cudaStream_t s);
+// The groups' constants (unless weights_only) and the weight gradients.
+cudaError_t launch_gncl_coefs(const GnClParams& p, int dtype, bool weights_only, cudaStream_t s);
+// One launch for the whole forward or backward pass (grad).
+size_t gncl_fused_smem(const GnClParams& p, int dtype, bool grad, int block, int held);
+cudaError_t launch_gncl_fused(const GnClParams& p, int dtype, bool grad, int block, cudaStream_t s);
 cudaError_t launch_gncl_grad_apply(const GnClParams& p, int dtype, bool vector, int64_t ctas, cudaStream_t s);
 
 // ---------------------------------------------------------------------------

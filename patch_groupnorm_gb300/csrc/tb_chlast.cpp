@@ -67,6 +67,7 @@ tb_status cl_params(tb::GnClParams& prm, const ClCall& c, bool grads, bool outs)
     prm.C = c.C;
     prm.P = c.P;
     prm.G = c.G;
+    prm.K = (int32_t)(c.C / c.G);
     prm.R = c.R;
     prm.eps = c.eps;
     prm.silu = c.silu ? 1 : 0;
@@ -171,9 +172,15 @@ tb_status cl_plan_stats(tb::GnClParams& prm, tb_dtype dtype, bool vector, int ct
 }
 
 // Whether a call fits into shared memory in one launch, and how it is cut (see
-// tb_gncl_fused.cu): of the ways for which all clusters have room at once, the one
-// that a simple account of its time favours: an SM's bytes at its share of the
-// memory's rate, and a thread's chunks one after the other.
+// tb_gncl_fused.cu): of the ways for which all clusters have room at once, the fastest
+// by an account fitted to measurements (us): 4.5 for the launch and the joining of
+// sums, 0.4 for each chunk that a thread takes after the other, 0.6 with twice the
+// threads on an SM, and more where few channels of a chunk share a group.  The general
+// path takes at least 10.5 us (backward 12.5): where the account says more, it is
+// taken.  Both, by graph: 1 x 64 x 64 x 512 bf16 8.9 and 11.3 us (backward 11.4 and
+// 14.1), 1 x 32 x 32 x 512 6.4 and 9.8 (7.6 and 12.5), 2 patches of 15 x 16 x 64 5.5
+// and 8.1 (6.5 and 10.8); where the groups cannot be split among clusters, 2 x 25 x 60
+// x 200 in 4 groups, 15.9 and 10.6 (13.2 and 13.3).
 bool cl_plan_fused(tb::GnClParams& prm, tb_dtype dtype, bool grad, int sms, int* block) {
     const int es = elem_bytes(dtype), vec = 16 / es, tensors = grad ? 2 : 1;
     double bytes = 0;
@@ -187,7 +194,8 @@ bool cl_plan_fused(tb::GnClParams& prm, tb_dtype dtype, bool grad, int sms, int*
     uint32_t rows[tb::GN_MAXP];  // below 2^31: they fit into shared memory
     for (int p = 0; p < prm.P; ++p)
         rows[p] = (uint32_t)((prm.spatial[p] * prm.C / vec + prm.period - 1) / prm.period);
-    double best = 1e30;
+    const int unit = std::min(vec, prm.K & -prm.K);
+    double best = grad ? 12.5 : 10.5;
     int32_t splits = 0, slabs = 0, columns = 0, cluster = 0, most = 0;
     for (int s = 1; s <= prm.G && (s == 1 || prm.C / s * es >= 64); s *= 2) {
         if (s > 1 && (prm.G % s != 0 || prm.C % vec != 0 || (prm.C / s) % vec != 0)) break;
@@ -205,9 +213,9 @@ bool cl_plan_fused(tb::GnClParams& prm, tb_dtype dtype, bool grad, int sms, int*
                 const int per_sm = (int)std::min<size_t>((size_t)(227 * 1024) / (smem + 1024), (size_t)(512 / b));
                 const int64_t ctas = prm.N * s * c;
                 if ((double)ctas > cl_places(c, per_sm) * per_sm * sms) continue;
-                const double on_sm = (double)std::min<int64_t>(per_sm, (ctas + sms - 1) / sms);
-                const double us = on_sm * held * b * 16 * tensors / 25000.0 + 0.12 * held + (c > 1 ? 0.5 : 0.0);
-                if (us >= best * 0.999) continue;
+                const int64_t threads = std::min<int64_t>(per_sm, (ctas + sms - 1) / sms) * b;
+                const double us = 4.5 + held * (0.2 + threads / 1280.0) + 0.3 * (vec / unit);
+                if (us >= best) continue;
                 best = us;
                 splits = s;
                 slabs = turns;
@@ -223,7 +231,12 @@ bool cl_plan_fused(tb::GnClParams& prm, tb_dtype dtype, bool grad, int sms, int*
     prm.columns = columns;
     prm.cluster = cluster;
     prm.held = most;
-    return splits > 0;
+    if (splits == 0) return false;
+    prm.parts[0] = prm.G / splits;
+    prm.parts[1] = prm.period / splits;
+    prm.share[0] = cluster / slabs;
+    for (int p = 0; p < prm.P; ++p) prm.start[p] = (int32_t)(prm.spatial[p] * prm.C / vec);
+    return true;
 }
 
 // Element-wise passes: runs of rows of about the same length, as many as are

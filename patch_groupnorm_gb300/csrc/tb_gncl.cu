@@ -33,9 +33,10 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
     float* const stage_mean = reinterpret_cast<float*>(shared4 + Stream::SMEM / 16);  // [CL_BLOCK * VEC]
     float* const stage_m2 = stage_mean + CL_BLOCK * VEC;              // [CL_BLOCK * VEC]
     int* const stage_n = reinterpret_cast<int*>(stage_m2 + CL_BLOCK * VEC);  // [CL_BLOCK]
-    const int C = (int)p.C, G = p.G, K = C / G;
+    const int C = (int)p.C, G = p.G, K = p.K;
     const int gs = G / p.splits, g0 = (int)blockIdx.y * gs, g1 = g0 + gs;  // this CTA's groups
-    float4* const table = reinterpret_cast<float4*>(stage_n + CL_BLOCK);     // [gs]: (count, mean, M2)
+    float2* const warps = reinterpret_cast<float2*>(stage_n + CL_BLOCK);     // [CL_BLOCK / 32]
+    float4* const table = reinterpret_cast<float4*>(warps + CL_BLOCK / 32);  // [gs]: (count, mean, M2)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < gs; i += CL_BLOCK) table[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     const ClUnit u = cl_unit(p);
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
         sums.store(w.count, unit, stage_mean, stage_m2);
         stage_n[threadIdx.x] = w.count * unit;
         __syncthreads();
-        cl_join_groups<VEC>(q, run.head, j0, j1, unit, C, K, g0, gs, stage_mean, stage_m2, stage_n, table);
+        cl_join_groups<VEC>(q, run.head, j0, j1, unit, C, K, g0, gs, stage_mean, stage_m2, stage_n, warps, table);
     }
     __syncthreads();
     if (VEC > 1 && warp == 0) {
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
 
 template <int DT, int VEC>
 size_t stats_smem(int groups) {
-    return ClStream<DT, VEC, 1, DEPTH>::SMEM + CL_BLOCK * VEC * 8 + CL_BLOCK * 4 + (size_t)groups * 16;
+    return ClStream<DT, VEC, 1, DEPTH>::SMEM + CL_BLOCK * VEC * 8 + CL_BLOCK * 4 + CL_BLOCK / 4 + (size_t)groups * 16;
 }
 
 // --- normalisation ------------------------------------------------------------------
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_apply_kernel(const __grid_co
     extern __shared__ uint4 shared4[];
     using Stream = ClStream<DT, VEC, 1, APPLY_DEPTH>;
     float2* const stats = reinterpret_cast<float2*>(shared4 + Stream::SMEM / 16);  // [G]
-    const int C = (int)p.C, K = C / p.G;
+    const int C = (int)p.C, K = p.K;
     int pt = 0;
     while (pt + 1 < p.P && (int)blockIdx.x >= p.start[pt + 1]) ++pt;
     const int local = (int)blockIdx.x - p.start[pt], n = local / p.parts[pt], piece = local - n * p.parts[pt];

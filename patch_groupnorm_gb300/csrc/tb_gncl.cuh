@@ -307,37 +307,81 @@ struct ClMoments {
 // Channels that every chunk has side by side in one group: a power of two.
 __device__ __forceinline__ int cl_unit_channels(int VEC, int K, int head) { return min(VEC, (K | head) & -(K | head)); }
 
+// Sums of a pair over `team` neighbouring threads (a power of two, the same for all
+// threads of the CTA), for every one of them; teams of several warps meet in `warps`
+// [blockDim / 32].
+__device__ __forceinline__ float2 cl_team_sum(float a, float b, int team, float2* warps) {
+    for (int d = min(team, 32) / 2; d >= 1; d >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, d);
+        b += __shfl_xor_sync(0xffffffffu, b, d);
+    }
+    if (team > 32) {
+        __syncthreads();  // whoever read them before is done
+        if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = make_float2(a, b);
+        __syncthreads();
+        const int first = (int)(threadIdx.x & ~(unsigned)(team - 1)) >> 5;
+        a = b = 0.f;
+        for (int w = 0; w < team >> 5; ++w) {
+            a += warps[first + w].x;
+            b += warps[first + w].y;
+        }
+    }
+    return make_float2(a, b);
+}
+
 // The staged sums of groups g0 .. g0 + gs - 1 join those groups' entries of `table`
 // (count, mean, M2).  The units of a row that are one group's lie in phases [head + j0 *
-// VEC, head + j1 * VEC), in runs of at most K / unit; `team` threads join those of all
-// rows.  An entry belongs to one thread throughout.
+// VEC, head + j1 * VEC), in runs of at most K / unit.  A team of threads joins a group:
+// the mean about one of its means, then squares about that mean, corrected by what it
+// was off (it may come from a value far from all others).
 template <int VEC>
 __device__ __forceinline__ void cl_join_groups(const ClPlace& q, int head, int j0, int j1, int unit, int C, int K, int g0,
                                                int gs, const float* stage_mean, const float* stage_m2,
-                                               const int* stage_n, float4* table) {
+                                               const int* stage_n, float2* warps, float4* table) {
+    const int log2_unit = 31 - __clz(unit), log2_each = (VEC == 8 ? 3 : VEC == 4 ? 2 : 0) - log2_unit;
+    const int lo = (head + j0 * VEC) >> log2_unit, hi = (head + j1 * VEC) >> log2_unit, pitch = q.width << log2_each;
+    const int Ku = K >> log2_unit, Cu = C >> log2_unit;
+    // a warp to a group; more where that leaves threads idle and has much to add up
     int team = 32;
-    while (team > 1 && gs * team > (int)blockDim.x) team /= 2;
-    const int each = VEC / unit, lo = (head + j0 * VEC) / unit, hi = (head + j1 * VEC) / unit, pitch = q.width * each;
-    const int Ku = K / unit, Cu = C / unit;
+    while (team > 1 && gs * team > (int)blockDim.x) team >>= 1;
+    while (gs * team * 2 <= (int)blockDim.x && q.rows * pitch > gs * team * 8) team <<= 1;
+    const int lane = threadIdx.x & (team - 1);
     for (int first = 0; first < gs; first += (int)blockDim.x / team) {
         const int i = first + (int)threadIdx.x / team, c0 = (g0 + i) * Ku;
-        float n = 0.f, mean = 0.f, m2 = 0.f;
-        if (i < gs) {
-            for (int m = lo >= c0 + Ku ? (lo - c0 - Ku) / Cu + 1 : 0; c0 + m * Cu < hi; ++m) {
+        const int m_first = lo >= c0 + Ku ? (lo - c0 - Ku) / Cu + 1 : 0;
+        auto each = [&](auto&& body) {
+            if (i >= gs) return;
+            for (int m = m_first; c0 + m * Cu < hi; ++m) {
                 const int from = max(c0 + m * Cu, lo) - lo, len = min(c0 + m * Cu + Ku, hi) - lo - from;
-                for (int e = (int)threadIdx.x % team; e < q.rows * len; e += team) {
-                    const int row = (int)((unsigned)e / (unsigned)len), at = row * pitch + from + (e - row * len);
-                    chan(n, mean, m2, (float)stage_n[(unsigned)at / (unsigned)each], stage_mean[at], stage_m2[at]);
+                const float per = __fdividef(1.f, (float)len);
+                for (int e = lane; e < q.rows * len; e += team) {
+                    // e / len: both below 2^13, so half a step keeps the product from the borders
+                    const int row = (int)(((float)e + 0.5f) * per);
+                    body(row * pitch + from + (e - row * len));
                 }
             }
-        }
-        for (int d = team / 2; d >= 1; d >>= 1) {
-            const float nb = __shfl_down_sync(0xffffffffu, n, d), mb = __shfl_down_sync(0xffffffffu, mean, d);
-            chan(n, mean, m2, nb, mb, __shfl_down_sync(0xffffffffu, m2, d));
-        }
-        if (i < gs && threadIdx.x % team == 0) {
+        };
+        const int at0 = i < gs && c0 + m_first * Cu < hi ? max(c0 + m_first * Cu, lo) - lo : 0;
+        const float k0 = stage_mean[at0];
+        float n = 0.f, s = 0.f;
+        each([&](int at) {
+            const float ni = (float)stage_n[at >> log2_each];
+            n += ni;
+            s = fmaf(ni, stage_mean[at] - k0, s);
+        });
+        const float2 ns = cl_team_sum(n, s, team, warps);
+        const float inv = ns.x > 0.f ? 1.f / ns.x : 0.f, mean = fmaf(ns.y, inv, k0);
+        float off = 0.f, m2 = 0.f;
+        each([&](int at) {
+            const float ni = (float)stage_n[at >> log2_each], d = stage_mean[at] - mean;
+            off = fmaf(ni, d, off);
+            m2 += fmaf(ni * d, d, ni > 0.f ? stage_m2[at] : 0.f);
+        });
+        const float2 om = cl_team_sum(off, m2, team, warps);
+        if (i < gs && lane == 0 && ns.x > 0.f) {
+            const float by = om.x * inv, left = fmaf(-om.x, by, om.y);
             float4 t = table[i];
-            chan(t.x, t.y, t.z, n, mean, m2);
+            chan(t.x, t.y, t.z, ns.x, mean + by, left < 0.f ? 0.f : left);
             table[i] = t;
         }
     }
@@ -345,8 +389,11 @@ __device__ __forceinline__ void cl_join_groups(const ClPlace& q, int head, int j
 
 // --- thread-block clusters ------------------------------------------------------
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 // 8 bytes of shared memory of CTA `rank` of this cluster, at this CTA's address `at`.
 __device__ __forceinline__ uint2 cluster_load8(uint32_t at, uint32_t rank) {
@@ -357,30 +404,41 @@ __device__ __forceinline__ uint2 cluster_load8(uint32_t at, uint32_t rank) {
     return v;
 }
 
-// (count, mean, M2) of entry `i` of the cluster's tables: eight threads to an entry,
-// one for each CTA; the first of them holds the result.
+// 16 bytes.
+__device__ __forceinline__ float4 cluster_load16(uint32_t at, uint32_t rank) {
+    uint32_t far;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(at), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(far)
+                 : "memory");
+    return v;
+}
+
+// (count, mean, M2) of entry `i` of the cluster's tables, for each of its team of eight
+// threads, one for each CTA.
 __device__ __forceinline__ float4 cl_join_cluster(const float4* table, int i, int gs, int cluster) {
     static_assert(CL_MAX_CLUSTER == 8, "eight threads read the CTAs' sums");
     const int r = threadIdx.x & 7;
-    float n = 0.f, mean = 0.f, m2 = 0.f;
-    if (i < gs && r < cluster) {
-        if (cluster > 1) {
-            const uint2 lo = cluster_load8(smem_addr(table + i), (uint32_t)r);
-            n = __uint_as_float(lo.x);
-            mean = __uint_as_float(lo.y);
-            m2 = __uint_as_float(cluster_load8(smem_addr(table + i) + 8, (uint32_t)r).x);
-        } else {
-            n = table[i].x;
-            mean = table[i].y;
-            m2 = table[i].z;
-        }
-    }
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < gs && r < cluster) t = cluster > 1 ? cluster_load16(smem_addr(table + i), (uint32_t)r) : table[i];
+    const float k0 = __shfl_sync(0xffffffffu, t.y, threadIdx.x & 24);
+    float n = t.x, s = t.x > 0.f ? t.x * (t.y - k0) : 0.f;
 #pragma unroll
     for (int d = 4; d >= 1; d >>= 1) {
-        const float nb = __shfl_down_sync(0xffffffffu, n, d), mb = __shfl_down_sync(0xffffffffu, mean, d);
-        chan(n, mean, m2, nb, mb, __shfl_down_sync(0xffffffffu, m2, d));
+        n += __shfl_xor_sync(0xffffffffu, n, d);
+        s += __shfl_xor_sync(0xffffffffu, s, d);
     }
-    return make_float4(n, mean, m2, 0.f);
+    const float inv = n > 0.f ? 1.f / n : 0.f, mean = fmaf(s, inv, k0), d = t.y - mean;
+    float off = t.x > 0.f ? t.x * d : 0.f, m2 = t.x > 0.f ? fmaf(t.x * d, d, t.z) : 0.f;
+#pragma unroll
+    for (int k = 4; k >= 1; k >>= 1) {
+        off += __shfl_xor_sync(0xffffffffu, off, k);
+        m2 += __shfl_xor_sync(0xffffffffu, m2, k);
+    }
+    const float by = off * inv, left = fmaf(-off, by, m2);
+    return make_float4(n, mean + by, left < 0.f ? 0.f : left, 0.f);
 }
 
 // The (patch, sample, part) of a statistics CTA, its rank in the part's cluster, its
@@ -453,7 +511,8 @@ struct ClChannel {
     int c, g, k;  // channel, group, place in the group
     int C, K;
     __device__ __forceinline__ ClChannel(int head, int phase, int C_, int K_) : C(C_), K(K_) {
-        c = (head + phase) % C;
+        c = head + phase;
+        if (c >= C) c %= C;
         g = c / K;
         k = c - g * K;
     }
@@ -470,7 +529,8 @@ struct ClChannel {
 // gamma and beta of a thread's VEC channels: one load each where they lie together.
 template <int DT, int VEC>
 __device__ __forceinline__ void cl_weights(const GnClParams& p, int head, int phase, float (&ga)[VEC], float (&be)[VEC]) {
-    const int c0 = (head + phase) % (int)p.C;
+    int c0 = head + phase;
+    if (c0 >= p.C) c0 %= (int)p.C;
     if (VEC > 1 && c0 % VEC == 0 && c0 + VEC <= p.C &&
         ((reinterpret_cast<uintptr_t>(p.gamma) | reinterpret_cast<uintptr_t>(p.beta)) & 15u) == 0) {
         weights_at<VEC>(p.gamma, DT, c0, 1.f, ga);

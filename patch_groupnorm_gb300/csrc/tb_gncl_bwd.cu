@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_stats_kernel(const __gr
     using W = ClWord<DT, VEC>;
     constexpr int ES = elem_size(DT), NL = L::N;
     extern __shared__ uint4 shared4[];
-    const int C = (int)p.C, K = C / p.G;
+    const int C = (int)p.C, K = p.K;
     const int cs = C / p.splits, c0 = (int)blockIdx.y * cs;  // this CTA's channels
     using Stream = ClStream<DT, VEC, 2, DEPTH>;
     float2* const stage = reinterpret_cast<float2*>(shared4 + Stream::SMEM / 16);  // [CL_BLOCK * VEC]: (sum dz, sum dz * d)
@@ -205,7 +205,7 @@ template <int DT>
 __global__ void __launch_bounds__(CL_BLOCK) gncl_coefs_kernel(const __grid_constant__ GnClParams p) {
     __shared__ float2 sums[CL_BLOCK / 32];
     __shared__ float2 stats[1];
-    const int C = (int)p.C, K = C / p.G;
+    const int C = (int)p.C, K = p.K;
     const int64_t units = p.coefs != nullptr ? p.N * p.G : 0, set = p.N * C * TB_GN_PARTS;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t size = (int64_t)p.R * set * (int64_t)sizeof(float2);
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_apply_kernel(const __gr
     using L = Lanes<VEC>;
     using W = ClWord<DT, VEC>;
     constexpr int ES = elem_size(DT), NL = L::N;
-    const int C = (int)p.C, K = C / p.G;
+    const int C = (int)p.C, K = p.K;
     int pt = 0;
     while (pt + 1 < p.P && (int)blockIdx.x >= p.start[pt + 1]) ++pt;
     const int local = (int)blockIdx.x - p.start[pt], n = local / p.parts[pt], piece = local - n * p.parts[pt];

@@ -16,6 +16,11 @@
 namespace tb {
 namespace {
 
+template <int N>
+struct Count {
+    static constexpr int value = N;
+};
+
 // A thread's chunks of all patches, in the order in which they are copied: chunk k of
 // NS tensors in slots k * NS .. of its column of the ring.
 template <int NS>
@@ -23,20 +28,24 @@ struct ClHeld {
     const GnClParams& p;
     ClPlace q;
     int64_t sample;          // n
-    int slice, slices, vec;  // this CTA's blocks of rows: slice, slice + slices, ...
+    int slice;               // this CTA's blocks of rows: slice, slice + slices, ...
+    int stride;              // chunks from one of them to the next
     uint32_t slot;
     int count;               // chunks
     int sure;                // of these, known to have arrived
 
-    __device__ __forceinline__ int chunks_of(int pt) const { return (int)(p.spatial[pt] * p.C / vec); }
-    // Calls body(patch, chunk of the sample, k) for every chunk.
+    // Calls body(patch, chunk of the sample, k, count) for every chunk, or pair of
+    // chunks `stride` apart: count is a constant of 1 or 2.
     template <typename Body>
     __device__ __forceinline__ void each(Body&& body) {
+        const int first = (slice * q.rows + q.row) * p.period + q.col;
         int k = 0;
         if (q.row >= 0) {
             for (int pt = 0; pt < p.P; ++pt) {
-                const int chunks = chunks_of(pt), stride = slices * q.rows * p.period;
-                for (int at = (slice * q.rows + q.row) * p.period + q.col; at < chunks; at += stride, ++k) body(pt, at, k);
+                const int chunks = p.start[pt];
+                int at = first;
+                for (; at + stride < chunks; at += 2 * stride, k += 2) body(pt, at, k, Count<2>());
+                if (at < chunks) body(pt, at, k++, Count<1>());
             }
         }
         count = k;
@@ -71,28 +80,27 @@ __device__ __forceinline__ void copy16(uint32_t to, const char* from, const char
 }
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// Where a CTA stands: cluster = (sample, split), splits fastest; in a cluster the slabs
-// of the split's columns, then the slices of the rows.
+// Where a CTA stands: grid.x is the rank in the cluster (the slabs of the split's
+// columns, then the slices of the rows), grid.y the split, grid.z the sample.
 struct ClSeat {
     int64_t n;
     int split, rank, g0, gs, j0, j1;
     template <int NS>
-    __device__ __forceinline__ static ClSeat take(const GnClParams& p, int vec, void* ring, ClHeld<NS>& held) {
+    __device__ __forceinline__ static ClSeat take(const GnClParams& p, void* ring, ClHeld<NS>& held) {
         ClSeat s;
-        const int unit = (int)blockIdx.x / p.cluster;
-        s.rank = (int)blockIdx.x - unit * p.cluster;
-        s.n = unit / p.splits;
-        s.split = unit - (int)s.n * p.splits;
-        s.gs = p.G / p.splits;
+        s.rank = (int)blockIdx.x;
+        s.n = blockIdx.z;
+        s.split = (int)blockIdx.y;
+        s.gs = p.parts[0];
         s.g0 = s.split * s.gs;
-        const int width = p.period / p.splits, first = s.split * width;
-        s.j0 = first + s.rank % p.slabs * p.columns;
+        const int width = p.parts[1], first = s.split * width;
+        const int slice = p.slabs == 1 ? s.rank : s.rank / p.slabs;
+        s.j0 = first + (s.rank - slice * p.slabs) * p.columns;
         s.j1 = min(s.j0 + p.columns, first + width);
         held.q = cl_place(p, s.j0, s.j1);
         held.sample = s.n;
-        held.slice = s.rank / p.slabs;
-        held.slices = p.cluster / p.slabs;
-        held.vec = vec;
+        held.slice = slice;
+        held.stride = p.share[0] * held.q.rows * p.period;
         held.slot = smem_addr(ring) + threadIdx.x * 16;
         held.sure = 0;
         return s;
@@ -111,18 +119,23 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) gncl_fused_kernel(const __
     float* const stage_mean = reinterpret_cast<float*>(shared4 + p.held * BLOCK);  // [BLOCK * VEC]
     float* const stage_m2 = stage_mean + BLOCK * VEC;                              // [BLOCK * VEC]
     int* const stage_n = reinterpret_cast<int*>(stage_m2 + BLOCK * VEC);           // [BLOCK]
-    float4* const table = reinterpret_cast<float4*>(stage_n + BLOCK);              // [gs]: (count, mean, M2)
-    const int C = (int)p.C, K = C / p.G;
+    float2* const warps = reinterpret_cast<float2*>(stage_n + BLOCK);              // [BLOCK / 32]
+    float4* const table = reinterpret_cast<float4*>(warps + BLOCK / 32);           // [gs]: (count, mean, M2)
+    const int C = (int)p.C, K = p.K;
     ClHeld<1> held{p};
-    const ClSeat seat = ClSeat::take(p, VEC, shared4, held);
-    float2* const stats = reinterpret_cast<float2*>(table + seat.gs);              // [gs]: (mean, rstd)
+    const ClSeat seat = ClSeat::take(p, shared4, held);
+    float4* const stats = table + seat.gs;                                         // [gs]: (mean, rstd, M2)
     for (int i = threadIdx.x; i < seat.gs; i += BLOCK) table[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     grid_wait();
-    held.each([&](int pt, int at, int k) {
+    held.each([&](int pt, int at, int k, auto count) {
         const char* const patch = static_cast<const char*>(p.patches[pt]);
         const int64_t bytes = p.spatial[pt] * C * ES;
-        copy16(held.at(k, 0), patch + seat.n * bytes + (int64_t)at * 16, patch, p.N * bytes, p.status);
-        copies_end();
+        const char* const from = patch + seat.n * bytes + (int64_t)at * 16;
+#pragma unroll
+        for (int j = 0; j < decltype(count)::value; ++j) {
+            copy16(held.at(k + j, 0), from + (int64_t)j * held.stride * 16, patch, p.N * bytes, p.status);
+            copies_end();
+        }
     });
     float fm[VEC], fa[VEC], fb[VEC];
     cl_weights<DT, VEC>(p, 0, held.q.col * VEC, fa, fb);
@@ -140,36 +153,24 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) gncl_fused_kernel(const __
     sums.store(held.count, unit, stage_mean, stage_m2);
     stage_n[threadIdx.x] = held.count * unit;
     __syncthreads();
-    cl_join_groups<VEC>(held.q, 0, seat.j0, seat.j1, unit, C, K, seat.g0, seat.gs, stage_mean, stage_m2, stage_n, table);
+    cl_join_groups<VEC>(held.q, 0, seat.j0, seat.j1, unit, C, K, seat.g0, seat.gs, stage_mean, stage_m2, stage_n, warps, table);
     if (p.cluster > 1) cluster_sync();
     else __syncthreads();
     // every CTA joins all of its split's groups for itself
     for (int first = 0; first < seat.gs; first += BLOCK / 8) {
-        const int i = first + (int)threadIdx.x / 8, r = threadIdx.x & 7;
+        const int i = first + (int)threadIdx.x / 8;
         const float4 t = cl_join_cluster(table, i, seat.gs, p.cluster);
-        // the team's first thread has the result
-        const float mean = __shfl_sync(0xffffffffu, t.y, threadIdx.x & 24), m2 = __shfl_sync(0xffffffffu, t.z, threadIdx.x & 24);
-        if (i >= seat.gs) continue;
-        if (r == 0) {
+        if (i < seat.gs && (threadIdx.x & 7) == 0) {
             const float var = t.x > 0.f ? t.z / t.x : 0.f;  // biased: divided by the count
-            stats[i] = make_float2(t.y, 1.0f / sqrtf(var + p.eps));
-        }
-        if (seat.rank != 0) continue;
-        // the records of all patches together are one, the others are empty
-        int64_t count = 0;
-        for (int pt = 0; pt < p.P; ++pt) count += p.spatial[pt] * K;
-        for (int pt = 0; pt < p.P; ++pt) {
-            GnPartial* const at = p.partials + (((int64_t)pt * p.N + seat.n) * p.G + seat.g0 + i) * TB_GN_PARTS + r;
-            if (in_bounds(at, sizeof(GnPartial), p.partials,
-                          (int64_t)p.P * p.N * p.G * TB_GN_PARTS * (int64_t)sizeof(GnPartial), p.status))
-                *at = pt == 0 && r == 0 ? GnPartial{count, mean, m2} : GnPartial{0, 0.f, 0.f};
+            stats[i] = make_float4(t.y, rsqrtf(var + p.eps), t.z, 0.f);
         }
     }
+    if (p.cluster > 1) cluster_arrive();  // this CTA has read the others' tables
     __syncthreads();
     ClChannel ch(0, held.q.col * VEC, C, K);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-        const float2 s = held.q.row >= 0 ? stats[ch.g - seat.g0] : make_float2(0.f, 0.f);
+        const float4 s = held.q.row >= 0 ? stats[ch.g - seat.g0] : make_float4(0.f, 0.f, 0.f, 0.f);
         fm[i] = s.x;
         fa[i] *= s.y;
         ch.next();
@@ -178,17 +179,39 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) gncl_fused_kernel(const __
     cl_lanes<VEC>(fm, mean);
     cl_lanes<VEC>(fa, ga);
     cl_lanes<VEC>(fb, be);
-    held.each([&](int pt, int at, int k) {
-        typename L::T f[NL];
-        to_lanes<DT, VEC>(smem_load<W>(held.at(k, 0)), f);
+    held.each([&](int pt, int at, int k, auto count) {
+        constexpr int N = decltype(count)::value;
+        typename L::T f[N][NL];
 #pragma unroll
-        for (int i = 0; i < NL; ++i) f[i] = act<SILU>(vfma(vsub(f[i], mean[i]), ga[i], be[i]));
+        for (int j = 0; j < N; ++j) to_lanes<DT, VEC>(smem_load<W>(held.at(k + j, 0)), f[j]);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+#pragma unroll
+            for (int i = 0; i < NL; ++i) f[j][i] = act<SILU>(vfma(vsub(f[j][i], mean[i]), ga[i], be[i]));
+        }
         char* const out = static_cast<char*>(p.outs[pt]);
         const int64_t bytes = p.spatial[pt] * C * ES;
         char* const to = out + seat.n * bytes + (int64_t)at * 16;
-        if (in_bounds(to, 16, out, p.N * bytes, p.status)) *reinterpret_cast<W*>(to) = from_lanes<DT, VEC>(f);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            char* const here = to + (int64_t)j * held.stride * 16;
+            if (in_bounds(here, 16, out, p.N * bytes, p.status)) *reinterpret_cast<W*>(here) = from_lanes<DT, VEC>(f[j]);
+        }
     });
-    if (p.cluster > 1) cluster_sync();  // nobody leaves while its table may be read
+    if (seat.rank == 0) {  // the records of all patches together are one, the others are empty
+        int64_t count = 0;
+        for (int pt = 0; pt < p.P; ++pt) count += p.spatial[pt] * K;
+        for (int j = threadIdx.x; j < seat.gs * TB_GN_PARTS; j += BLOCK) {
+            const float4 t = stats[j / TB_GN_PARTS];
+            for (int pt = 0; pt < p.P; ++pt) {
+                GnPartial* const at = p.partials + (((int64_t)pt * p.N + seat.n) * p.G + seat.g0) * TB_GN_PARTS + j;
+                if (in_bounds(at, sizeof(GnPartial), p.partials,
+                              (int64_t)p.P * p.N * p.G * TB_GN_PARTS * (int64_t)sizeof(GnPartial), p.status))
+                    *at = pt == 0 && j % TB_GN_PARTS == 0 ? GnPartial{count, t.x, t.z} : GnPartial{0, 0.f, 0.f};
+            }
+        }
+    }
+    if (p.cluster > 1) cluster_wait();  // nobody leaves while its table may be read
 }
 
 // --- backward -----------------------------------------------------------------------
@@ -202,22 +225,26 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) gncl_fused_grad_kernel(con
     extern __shared__ uint4 shared4[];
     float2* const stage = reinterpret_cast<float2*>(shared4 + p.held * 2 * BLOCK);  // [BLOCK * VEC]: (sum dz, sum dz * d)
     float2* const table = stage + BLOCK * VEC;                                      // [cs]: (sum dz, sum dz * xhat)
-    const int C = (int)p.C, K = C / p.G;
+    const int C = (int)p.C, K = p.K;
     ClHeld<2> held{p};
-    const ClSeat seat = ClSeat::take(p, VEC, shared4, held);
+    const ClSeat seat = ClSeat::take(p, shared4, held);
     const int cs = seat.gs * K, c0 = seat.g0 * K;                // the split's channels
     float2* const whole = table + cs;                            // [cs]: the cluster's sums
     float4* const coefs = reinterpret_cast<float4*>(whole + cs); // [gs]: (mean, rstd, u, v)
     float2* const stats = reinterpret_cast<float2*>(coefs + seat.gs);  // [gs]: (mean, rstd)
     for (int i = threadIdx.x; i < cs; i += BLOCK) table[i] = make_float2(0.f, 0.f);
     grid_wait();
-    held.each([&](int pt, int at, int k) {
+    held.each([&](int pt, int at, int k, auto count) {
         const char* const patch = static_cast<const char*>(p.patches[pt]);
         const char* const grad = static_cast<const char*>(p.grads[pt]);
-        const int64_t bytes = p.spatial[pt] * C * ES, from = seat.n * bytes + (int64_t)at * 16;
-        copy16(held.at(k, 0), patch + from, patch, p.N * bytes, p.status);
-        copy16(held.at(k, 1), grad + from, grad, p.N * bytes, p.status);
-        copies_end();
+        const int64_t bytes = p.spatial[pt] * C * ES;
+#pragma unroll
+        for (int j = 0; j < decltype(count)::value; ++j) {
+            const int64_t from = seat.n * bytes + (at + (int64_t)j * held.stride) * 16;
+            copy16(held.at(k + j, 0), patch + from, patch, p.N * bytes, p.status);
+            copy16(held.at(k + j, 1), grad + from, grad, p.N * bytes, p.status);
+            copies_end();
+        }
     });
     float f0[VEC], f1[VEC], f2[VEC];
     cl_weights<DT, VEC>(p, 0, held.q.col * VEC, f1, f2);
@@ -292,22 +319,8 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) gncl_fused_grad_kernel(con
             }
         }
         whole[i] = t;
-        if (seat.rank != 0) continue;
-        if (p.N == 1) {
-            if (p.dgamma != nullptr) store_weight(p.dgamma, DT, c0 + i, t.y);
-            if (p.dbeta != nullptr) store_weight(p.dbeta, DT, c0 + i, t.x);
-        } else if (p.dgamma != nullptr || p.dbeta != nullptr) {
-            // one record a sample, for the launch that adds the samples up
-            for (int pt = 0; pt < p.P; ++pt) {
-                float2* const at = p.grad_partials + (((int64_t)pt * p.N + seat.n) * C + c0 + i) * TB_GN_PARTS;
-                if (!in_bounds(at, TB_GN_PARTS * sizeof(float2), p.grad_partials,
-                               (int64_t)p.P * p.N * C * TB_GN_PARTS * (int64_t)sizeof(float2), p.status))
-                    continue;
-#pragma unroll
-                for (int r = 0; r < TB_GN_PARTS; ++r) at[r] = pt == 0 && r == 0 ? t : make_float2(0.f, 0.f);
-            }
-        }
     }
+    if (p.cluster > 1) cluster_arrive();  // this CTA has read the others' tables
     __syncthreads();
     // (mean, rstd, u, v) of the groups: eight threads to a group
     int64_t count = 0;
@@ -349,27 +362,57 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) gncl_fused_grad_kernel(con
         cl_lanes<VEC>(u, cu);
         cl_lanes<VEC>(v, cv);
     }
-    held.each([&](int pt, int at, int k) {
-        typename L::T f[NL], dy[NL];
-        to_lanes<DT, VEC>(smem_load<W>(held.at(k, 0)), f);
-        to_lanes<DT, VEC>(smem_load<W>(held.at(k, 1)), dy);
+    held.each([&](int pt, int at, int k, auto count) {
+        constexpr int N = decltype(count)::value;
+        typename L::T f[N][NL], dy[N][NL];
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const typename L::T d = vsub(f[i], mean[i]);
-            const typename L::T dz = dz_of<SILU>(dy[i], vfma(d, ga[i], be[i]));
-            f[i] = vfma(dz, ga[i], vfma(d, cu[i], cv[i]));
+        for (int j = 0; j < N; ++j) {
+            to_lanes<DT, VEC>(smem_load<W>(held.at(k + j, 0)), f[j]);
+            to_lanes<DT, VEC>(smem_load<W>(held.at(k + j, 1)), dy[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const typename L::T d = vsub(f[j][i], mean[i]);
+                const typename L::T dz = dz_of<SILU>(dy[j][i], vfma(d, ga[i], be[i]));
+                f[j][i] = vfma(dz, ga[i], vfma(d, cu[i], cv[i]));
+            }
         }
         char* const out = static_cast<char*>(p.outs[pt]);
         const int64_t bytes = p.spatial[pt] * C * ES;
         char* const to = out + seat.n * bytes + (int64_t)at * 16;
-        if (in_bounds(to, 16, out, p.N * bytes, p.status)) *reinterpret_cast<W*>(to) = from_lanes<DT, VEC>(f);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            char* const here = to + (int64_t)j * held.stride * 16;
+            if (in_bounds(here, 16, out, p.N * bytes, p.status)) *reinterpret_cast<W*>(here) = from_lanes<DT, VEC>(f[j]);
+        }
     });
-    if (p.cluster > 1) cluster_sync();  // nobody leaves while its table may be read
+    if (seat.rank == 0 && (p.dgamma != nullptr || p.dbeta != nullptr)) {
+        for (int i = threadIdx.x; i < cs; i += BLOCK) {
+            const float2 t = whole[i];
+            if (p.N == 1) {
+                if (p.dgamma != nullptr) store_weight(p.dgamma, DT, c0 + i, t.y);
+                if (p.dbeta != nullptr) store_weight(p.dbeta, DT, c0 + i, t.x);
+                continue;
+            }
+            // one record a sample, for the launch that adds the samples up
+            for (int pt = 0; pt < p.P; ++pt) {
+                float2* const at = p.grad_partials + (((int64_t)pt * p.N + seat.n) * C + c0 + i) * TB_GN_PARTS;
+                if (!in_bounds(at, TB_GN_PARTS * sizeof(float2), p.grad_partials,
+                               (int64_t)p.P * p.N * C * TB_GN_PARTS * (int64_t)sizeof(float2), p.status))
+                    continue;
+#pragma unroll
+                for (int r = 0; r < TB_GN_PARTS; ++r) at[r] = pt == 0 && r == 0 ? t : make_float2(0.f, 0.f);
+            }
+        }
+    }
+    if (p.cluster > 1) cluster_wait();  // nobody leaves while its table may be read
 }
 
 template <int DT, int BLOCK>
 cudaError_t fused_launch(const GnClParams& p, bool grad, cudaStream_t s) {
-    const dim3 grid((unsigned)(p.N * p.splits * p.cluster), 1, 1);
+    const dim3 grid((unsigned)p.cluster, (unsigned)p.splits, (unsigned)p.N);
     void (*const fn)(const GnClParams) =
         grad ? (p.silu ? gncl_fused_grad_kernel<DT, true, BLOCK> : gncl_fused_grad_kernel<DT, false, BLOCK>)
              : (p.silu ? gncl_fused_kernel<DT, true, BLOCK> : gncl_fused_kernel<DT, false, BLOCK>);
@@ -388,7 +431,7 @@ size_t gncl_fused_smem(const GnClParams& p, int dtype, bool grad, int block, int
     const size_t gs = (size_t)(p.G / p.splits), cs = (size_t)(p.C / p.splits);
     const size_t stage = (size_t)block * vec * 8;
     return grad ? (size_t)held * 2 * block * 16 + stage + cs * 16 + gs * 24
-                : (size_t)held * block * 16 + stage + (size_t)block * 4 + gs * 24;
+                : (size_t)held * block * 16 + stage + (size_t)block * 4 + (size_t)block / 4 + gs * 32;
 }
 
 cudaError_t launch_gncl_fused(const GnClParams& p, int dtype, bool grad, int block, cudaStream_t s) {

@@ -491,6 +491,7 @@ struct GnClParams {
     void* dbeta;                   // [C] or null
     int64_t N, C;
     int32_t P, G;
+    int32_t K;                     // channels of a group
     int32_t R;                     // record sets
     float eps;
     int32_t silu;
@@ -504,7 +505,9 @@ struct GnClParams {
     int64_t rows[GN_MAXP];         // statistics: rows of a sample of patch p, and their blocks for
     int32_t share[GN_MAXP];        // each piece (each of the first `extra` pieces has another)
     int32_t extra[GN_MAXP];
-    int32_t held;                  // one launch: chunks of each tensor that a thread holds at most
+    // one launch: parts[0] and [1] are a split's groups and columns, share[0] the slices
+    // of a cluster, start[p] the chunks of a sample of patch p
+    int32_t held;                  // chunks of each tensor that a thread holds at most
     uint32_t* status;              // bounds-checked build: device status word (else null)
 };
 static_assert(sizeof(GnClParams) <= 32000, "kernel parameter block too large");

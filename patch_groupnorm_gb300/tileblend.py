@@ -1252,25 +1252,40 @@ def patch_group_norm_backward(grads: Sequence[torch.Tensor], patches: Sequence[t
 # channels last: PatchGroupNorm forward and backward
 # ---------------------------------------------------------------------------
 
-def _cl_args(patches, G, gamma, beta):
-    """(N, C, dtype, device, positions, addresses) of channels-last patches [N, *spatial_p, C]."""
+def _cl_args(patches, gamma, beta, **likes):
+    """(N, C, dtype, device, P, positions, gamma's and beta's address, the patches'
+    addresses, and those of each list of tensors like them) of channels-last patches
+    [N, *spatial_p, C]."""
     P = len(patches)
     if not 1 <= P <= 64:
         raise ValueError("1 to 64 patches")
     first = patches[0]
-    dt, dev = first.dtype, first.get_device()
-    if first.dim() < 2:
-        raise ValueError("patches are [N, *spatial, C]")
-    N, C = first.shape[0], first.shape[-1]
-    spatial = []
+    dt, dev, shape = first.dtype, first.get_device(), first.shape
+    if len(shape) < 2 or dev < 0:
+        raise ValueError("patches are CUDA tensors [N, *spatial, C]")
+    N, C = shape[0], shape[-1]
+    for what, ts in likes.items():
+        if len(ts) != P:
+            raise ValueError("one %s per patch" % what)
+    spatial, ptrs, NC = [], [[] for _ in range(1 + len(likes))], N * C
+    lists = list(zip(ptrs[1:], likes.values(), likes))
     for q, x in enumerate(patches):
-        if x.get_device() != dev or dev < 0 or not x.is_contiguous():
-            raise ValueError("patch %d must be a contiguous CUDA tensor, on the device of patch 0" % q)
-        if x.dtype is not dt or x.dim() < 2 or x.shape[0] != N or x.shape[-1] != C:
-            raise ValueError("patch %d: dtype, samples or channels differ from patch 0" % q)
-        spatial.append(x.numel() // (N * C) if N * C else 0)
-    return (N, C, _dtype_code(first), dev, _COUNTS[P](*spatial), _PTRS[P](*[x.data_ptr() for x in patches]),
-            _vec(gamma, C, dt, dev, "gamma"), _vec(beta, C, dt, dev, "beta"))
+        if q:
+            shape = x.shape
+            if x.dtype is not dt or x.get_device() != dev or len(shape) < 2 or shape[0] != N or shape[-1] != C:
+                raise ValueError("patch %d: dtype, device, samples or channels differ from patch 0" % q)
+        if not x.is_contiguous():
+            raise ValueError("patch %d must be contiguous" % q)
+        spatial.append(x.numel() // NC if NC else 0)
+        ptrs[0].append(x.data_ptr())
+        for at, ts, what in lists:
+            t = ts[q]
+            if t.shape != shape or t.dtype is not dt or t.get_device() != dev or not t.is_contiguous():
+                raise ValueError("%s %d must be contiguous and match patch %d" % (what, q, q))
+            at.append(t.data_ptr())
+    array = _PTRS[P]
+    return (N, C, _DTYPES[dt] if dt in _DTYPES else _dtype_code(first), dev, P, _COUNTS[P](*spatial),
+            _vec(gamma, C, dt, dev, "gamma"), _vec(beta, C, dt, dev, "beta"), *[array(*at) for at in ptrs])
 
 
 def _cl_records(partials: torch.Tensor, R: int, N: int, G: int, device: int) -> int:
@@ -1298,8 +1313,7 @@ def gn_workspace_cl(N: int, G: int, device=None) -> torch.Tensor:
 def tb_patch_gn_stats_cl(patches: Sequence[torch.Tensor], G: int, partials: torch.Tensor, stream=None) -> torch.Tensor:
     """``tb_patch_gn_stats`` of channels-last patches [N, *spatial_p, C]: the
     same records, in the same places."""
-    N, C, dt, dev, sp, xs, _, _ = _cl_args(patches, G, None, None)
-    P = len(patches)
+    N, C, dt, dev, P, sp, _, _, xs = _cl_args(patches, None, None)
     _check(_lib.tb_patch_gn_stats_cl(xs, P, dt, N, C, sp, G, _cl_records(partials, P, N, G, dev),
                                      _stream_of(stream, dev)), "tb_patch_gn_stats_cl")
     return partials
@@ -1311,9 +1325,8 @@ def tb_patch_gn_apply_cl(patches: Sequence[torch.Tensor], outs: Sequence[torch.T
     """Normalise (+ SiLU) channels-last patches [N, *spatial_p, C] into
     ``outs`` (``outs[p]`` may be ``patches[p]``) with the statistics pooled
     over the ``R`` record sets in ``partials``."""
-    N, C, dt, dev, sp, xs, ga, be = _cl_args(patches, G, gamma, beta)
-    P = len(patches)
-    _check(_lib.tb_patch_gn_apply_cl(xs, _like_patches(outs, patches, "output"), P, dt, N, C, sp, G,
+    N, C, dt, dev, P, sp, ga, be, xs, os_ = _cl_args(patches, gamma, beta, output=outs)
+    _check(_lib.tb_patch_gn_apply_cl(xs, os_, P, dt, N, C, sp, G,
                                      _cl_records(partials, R, N, G, dev), R, ga, be, eps, 1 if silu else 0,
                                      _stream_of(stream, dev)), "tb_patch_gn_apply_cl")
     return outs
@@ -1333,11 +1346,11 @@ def patch_group_norm_cl(patches: Sequence[torch.Tensor], G: int, gamma: Optional
             [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in patches] if outs is None else outs,
             new_partials(len(patches), patches[0].shape[0], G, patches[0].device) if partials is None else partials),
             stream)
-    N, C, dt, dev, sp, xs, ga, be = _cl_args(patches, G, gamma, beta)
-    P = len(patches)
-    _check(_lib.tb_patch_group_norm_cl(xs, _like_patches(outs, patches, "output"), P, dt, N, C, sp, G,
-                                       _cl_records(partials, P, N, G, dev), ga, be, eps, 1 if silu else 0,
-                                       _stream_of(stream, dev)), "tb_patch_group_norm_cl")
+    N, C, dt, dev, P, sp, ga, be, xs, os_ = _cl_args(patches, gamma, beta, output=outs)
+    status = _lib.tb_patch_group_norm_cl(xs, os_, P, dt, N, C, sp, G, _cl_records(partials, P, N, G, dev), ga, be, eps,
+                                         1 if silu else 0, _stream_of(stream, dev))
+    if status:
+        raise TileBlendError(status, "tb_patch_group_norm_cl")
     return outs
 
 
@@ -1347,9 +1360,8 @@ def tb_patch_gn_grad_stats_cl(grads: Sequence[torch.Tensor], patches: Sequence[t
                               silu: bool = True, stream=None) -> torch.Tensor:
     """``tb_patch_gn_grad_stats`` of channels-last patches and gradients: the
     same records, in the same places."""
-    N, C, dt, dev, sp, xs, ga, be = _cl_args(patches, G, gamma, beta)
-    P = len(patches)
-    _check(_lib.tb_patch_gn_grad_stats_cl(xs, _like_patches(grads, patches, "gradient"), P, dt, N, C, sp, G,
+    N, C, dt, dev, P, sp, ga, be, xs, ds = _cl_args(patches, gamma, beta, gradient=grads)
+    _check(_lib.tb_patch_gn_grad_stats_cl(xs, ds, P, dt, N, C, sp, G,
                                           _cl_records(partials, R, N, G, dev), R, ga, be, eps, 1 if silu else 0,
                                           _grad_partials(grad_partials, P, N, C, dev), _stream_of(stream, dev)),
            "tb_patch_gn_grad_stats_cl")
@@ -1366,10 +1378,9 @@ def tb_patch_gn_grad_apply_cl(grads: Sequence[torch.Tensor], patches: Sequence[t
     ``grads[p]`` or ``patches[p]``), and of the weights into ``dgamma`` /
     ``dbeta``, from the ``R`` record sets of both passes.  ``workspace`` comes
     from ``gn_workspace_cl``."""
-    N, C, dt, dev, sp, xs, ga, be = _cl_args(patches, G, gamma, beta)
-    P = len(patches)
-    os_, gp, bp = _gn_grad_outs(dxs, patches, C, dgamma, dbeta)
-    _check(_lib.tb_patch_gn_grad_apply_cl(xs, _like_patches(grads, patches, "gradient"), os_, P, dt, N, C, sp, G,
+    N, C, dt, dev, P, sp, ga, be, xs, ds, os_ = _cl_args(patches, gamma, beta, gradient=grads, dx=dxs)
+    gp, bp = _vec(dgamma, C, patches[0].dtype, dev, "dgamma"), _vec(dbeta, C, patches[0].dtype, dev, "dbeta")
+    _check(_lib.tb_patch_gn_grad_apply_cl(xs, ds, os_, P, dt, N, C, sp, G,
                                           _cl_records(partials, R, N, G, dev),
                                           _grad_partials(grad_partials, R, N, C, dev), R, ga, be, eps,
                                           1 if silu else 0, gp, bp, *_cl_workspace(workspace, dev),
@@ -1399,13 +1410,15 @@ def patch_group_norm_backward_cl(grads: Sequence[torch.Tensor], patches: Sequenc
                     new_grad_partials(P, N, C, dev) if grad_partials is None else grad_partials,
                     gn_workspace_cl(N, G, dev) if workspace is None else workspace)
         dxs, dgamma, dbeta, grad_partials, workspace = _on_stream(make, stream)
-    N, C, dt, dev, sp, xs, ga, be = _cl_args(patches, G, gamma, beta)
-    os_, gp, bp = _gn_grad_outs(dxs, patches, C, dgamma, dbeta)
-    _check(_lib.tb_patch_group_norm_backward_cl(xs, _like_patches(grads, patches, "gradient"), os_, P, dt, N, C, sp, G,
-                                                _cl_records(partials, P, N, G, dev),
-                                                _grad_partials(grad_partials, P, N, C, dev), ga, be, eps,
-                                                1 if silu else 0, gp, bp, *_cl_workspace(workspace, dev),
-                                                _stream_of(stream, dev)), "tb_patch_group_norm_backward_cl")
+    N, C, dt, dev, P, sp, ga, be, xs, ds, os_ = _cl_args(patches, gamma, beta, gradient=grads, dx=dxs)
+    wdt = patches[0].dtype
+    status = _lib.tb_patch_group_norm_backward_cl(xs, ds, os_, P, dt, N, C, sp, G, _cl_records(partials, P, N, G, dev),
+                                                  _grad_partials(grad_partials, P, N, C, dev), ga, be, eps,
+                                                  1 if silu else 0, _vec(dgamma, C, wdt, dev, "dgamma"),
+                                                  _vec(dbeta, C, wdt, dev, "dbeta"), *_cl_workspace(workspace, dev),
+                                                  _stream_of(stream, dev))
+    if status:
+        raise TileBlendError(status, "tb_patch_group_norm_backward_cl")
     return dxs, dgamma, dbeta
 
 

@@ -174,8 +174,9 @@ def test_empty_sets_of_records_come_first(tbl):
     none = x[:, :0].contiguous()
     part = torch.cat([tbl.tb_patch_gn_stats_cl([t], 2, tbl.new_partials(1, 1, 2)) for t in [none] * 5 + [x]])
     y, = tbl.tb_patch_gn_apply_cl([x], [torch.empty_like(x)], 2, part, 6, None, None, 1e-6)
-    want, = tbl.patch_group_norm_cl([x], 2, None, None, 1e-6)
+    want, = tbl.tb_patch_gn_apply_cl([x], [torch.empty_like(x)], 2, part[5:], 1, None, None, 1e-6)
     assert torch.equal(y, want)
+    check_forward([x], 2, None, None, 1e-6, True, [y])
 
 
 def test_checks_and_empty_batches(tbl):

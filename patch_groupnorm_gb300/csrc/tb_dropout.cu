@@ -20,7 +20,12 @@ namespace {
 
 constexpr int DROP_BLOCK = 256;
 constexpr int RB = 8;  // elements of one block of random numbers
-constexpr int DU = 2;  // blocks a thread loads together
+
+// Blocks a thread loads together: two where a block is two or more 16-byte words (f32,
+// or with a residual), four where it is one.  16384 x 4096 bf16: 51.5, 46.3 and 44.6 us
+// with one, two and four; onto a residual 65536 x 512 31.0, 29.4 and 30.8.
+template <int DT, bool RES>
+constexpr int DROP_TURNS = DT == F32 || RES ? 2 : 4;
 
 struct Keys {
     uint32_t k0[10], k1[10];
@@ -79,12 +84,13 @@ __device__ __forceinline__ void generator(const DropoutParams& p, uint64_t& offs
     key_schedule(seed, keys);
 }
 
-// Whole chunks: a block's elements per thread and turn, DU turns side by side.
+// Whole chunks: a block's elements per thread and turn, DROP_TURNS turns side by side.
+// Nothing is read twice: loads and stores are marked so (44.6 us against 47.2).
 // Rows of whole blocks; one row may end inside a block (its last thread takes the
 // rest one by one).
 template <int DT, bool RES, bool RANDOM, bool STATE>
 __global__ void __launch_bounds__(DROP_BLOCK) dropout_kernel(const __grid_constant__ DropoutParams p) {
-    constexpr int ES = elem_size(DT), VEC = 16 / ES, NW = RB / VEC;
+    constexpr int ES = elem_size(DT), VEC = 16 / ES, NW = RB / VEC, DU = DROP_TURNS<DT, RES>;
     const int64_t per_row = p.cols / RB, blocks = per_row * p.rows;
     const int64_t first = (int64_t)blockIdx.x * (DROP_BLOCK * DU) + threadIdx.x;
     const char* const x = static_cast<const char*>(p.x);
@@ -116,8 +122,8 @@ __global__ void __launch_bounds__(DROP_BLOCK) dropout_kernel(const __grid_consta
             } else {
 #pragma unroll
                 for (int w = 0; w < NW; ++w) {
-                    vx[u][w] = reinterpret_cast<const uint4*>(ax)[w];
-                    if (RES) vr[u][w] = reinterpret_cast<const uint4*>(ar)[w];
+                    vx[u][w] = __ldcs(reinterpret_cast<const uint4*>(ax) + w);
+                    if (RES) vr[u][w] = __ldcs(reinterpret_cast<const uint4*>(ar) + w);
                 }
             }
         }
@@ -147,7 +153,7 @@ __global__ void __launch_bounds__(DROP_BLOCK) dropout_kernel(const __grid_consta
                 const bool k = keep[w * VEC + e];
                 f[e] = RES ? (k ? fmaf(f[e], p.scale, r[e]) : r[e]) : (k ? f[e] * p.scale : 0.f);
             }
-            *reinterpret_cast<uint4*>(y + at_y[u] + w * 16) = pack<DT, VEC>(f);
+            __stcs(reinterpret_cast<uint4*>(y + at_y[u] + w * 16), pack<DT, VEC>(f));
         }
     }
     const int rest = (int)(p.cols - per_row * RB);  // one row only
@@ -170,10 +176,25 @@ __global__ void __launch_bounds__(DROP_BLOCK) dropout_kernel(const __grid_consta
     }
 }
 
+// One element.
+template <int DT, bool RES>
+__device__ __forceinline__ typename Word<elem_size(DT)>::T drop_one(typename Word<elem_size(DT)>::T x,
+                                                                    typename Word<elem_size(DT)>::T res, bool keep,
+                                                                    float scale) {
+    float f[1], r[1] = {0.f};
+    unpack<DT, 1>(x, f);
+    if (RES) unpack<DT, 1>(res, r);
+    f[0] = RES ? (keep ? fmaf(f[0], scale, r[0]) : r[0]) : (keep ? f[0] * scale : 0.f);
+    return pack<DT, 1>(f);
+}
+
 // Any strides and addresses: a warp takes 32 blocks (256 neighbouring elements),
 // each lane a block's mask, and the elements in turns of 32, whose bits come from
-// the lane that has their block.
-template <int DT, bool RES, bool RANDOM, bool STATE>
+// the lane that has their block.  Where a row has at least as many elements (not
+// NARROW) they lie in one row or two, and an element's address is one of two bases
+// and a constant; in narrower rows the row and the column are stepped from turn to
+// turn.  (16387 x 2047 bf16 out of wider rows: 78 us with an index for every element.)
+template <int DT, bool RES, bool RANDOM, bool STATE, bool NARROW>
 __global__ void __launch_bounds__(DROP_BLOCK) dropout_elem_kernel(const __grid_constant__ DropoutParams p) {
     constexpr int ES = elem_size(DT), SPAN = 32 * RB;
     using W = typename Word<ES>::T;
@@ -181,70 +202,102 @@ __global__ void __launch_bounds__(DROP_BLOCK) dropout_elem_kernel(const __grid_c
     const int64_t warp = ((int64_t)blockIdx.x * DROP_BLOCK + threadIdx.x) >> 5, total = p.rows * p.cols;
     const int64_t first = warp * SPAN;
     if (first >= total) return;
-    const W* const x = static_cast<const W*>(p.x);
-    const W* const res = static_cast<const W*>(p.residual);
-    W* const y = static_cast<W*>(p.y);
-    const int64_t row0 = first / p.cols, col0 = first - row0 * p.cols;
+    // a 64-bit division is a hundred instructions
+    const int64_t row0 = total >> 32 ? first / p.cols : (uint32_t)first / (uint32_t)p.cols, col0 = first - row0 * p.cols;
+    const int left = (int)min((int64_t)SPAN, total - first);           // elements of this warp
+    const int cut = (int)min((int64_t)SPAN, p.cols - col0);            // of these, in the first row
+    const int cols = NARROW ? (int)p.cols : 0, row_step = NARROW ? 32 / cols : 0, col_step = 32 - row_step * cols;
+    const int64_t last = p.rows - 1;
+    const W* const x = static_cast<const W*>(p.x) + row0 * p.x_ld + col0;
+    const W* const res = RES ? static_cast<const W*>(p.residual) + row0 * p.r_ld + col0 : nullptr;
+    W* const y = static_cast<W*>(p.y) + row0 * p.y_ld + col0;
+    // Calls body(turn, element of x, of the residual, of y) for each of the lane's eight
+    // elements; those past the end are the last one again, so that all loads are on
+    // their way before the first is waited for (with a branch each: 68 us).
+    auto each = [&](auto&& body) {
+        [[maybe_unused]] int row = 0, at = (int)col0 + lane;
+        if constexpr (NARROW) {
+            row = at / cols;
+            at -= row * cols;
+        }
+        [[maybe_unused]] const int end = (int)col0 + left - 1, end_row = NARROW ? end / cols : 0, end_at = end - end_row * cols;
+#pragma unroll
+        for (int j = 0; j < RB; ++j) {
+            if constexpr (NARROW) {
+                const bool past = j * 32 + lane >= left;
+                const int r = past ? end_row : row, c = (past ? end_at : at) - (int)col0;
+                body(j, x + r * p.x_ld + c, RES ? res + r * p.r_ld + c : nullptr, y + r * p.y_ld + c);
+                row += row_step;
+                at += col_step;
+                if (at >= cols) {
+                    at -= cols;
+                    ++row;
+                }
+            } else {
+                const int e = min(j * 32 + lane, left - 1);
+                const bool second = e >= cut;  // the next row's first element is number `cut`
+                body(j, x + (second ? p.x_ld - p.cols : 0) + e, RES ? res + (second ? p.r_ld - p.cols : 0) + e : nullptr,
+                     y + (second ? p.y_ld - p.cols : 0) + e);
+            }
+        }
+    };
+    // The lane's elements, masked and scaled.
+    auto drop = [&](const W (&vx)[RB], const W (&vr)[RB], W (&out)[RB], const Keys& keys, uint64_t offset) {
+        bool keep[RB];
+        kept<RANDOM>((uint64_t)(warp * 32 + lane), offset, keys, p.threshold, keep);
+        uint32_t mask = 0;
+#pragma unroll
+        for (int e = 0; e < RB; ++e) mask |= (uint32_t)keep[e] << e;
+#pragma unroll
+        for (int j = 0; j < RB; ++j) {
+            const uint32_t m = __shfl_sync(0xffffffffu, mask, j * 4 + (lane >> 3));
+            out[j] = drop_one<DT, RES>(vx[j], vr[j], (m >> (lane & 7)) & 1u, p.scale);
+        }
+    };
     grid_wait();
     Keys keys;
     uint64_t offset;
     generator<STATE>(p, offset, keys);
-    W vx[RB], vr[RB];
-    int64_t at_y[RB];
+    W vx[RB], vr[RB], out[RB];
+    if (!NARROW && cut == SPAN) {  // one row
 #pragma unroll
-    for (int j = 0; j < RB; ++j) {
-        int64_t row = row0, col = col0 + j * 32 + lane;
-        at_y[j] = -1;
-        if (first + j * 32 + lane < total) {
-            if (p.cols >= SPAN) {
-                if (col >= p.cols) {
-                    col -= p.cols;
-                    ++row;
-                }
-            } else {
-                const uint32_t k = (uint32_t)col / (uint32_t)p.cols;
-                row += k;
-                col -= (int64_t)k * p.cols;
-            }
-            at_y[j] = row * p.y_ld + col;
-            const int64_t ax = row * p.x_ld + col, ar = row * p.r_ld + col;
-            if (!in_bounds(x + ax, ES, x, ((p.rows - 1) * p.x_ld + p.cols) * ES, p.status) ||
-                (RES && !in_bounds(res + ar, ES, res, ((p.rows - 1) * p.r_ld + p.cols) * ES, p.status)) ||
-                !in_bounds(y + at_y[j], ES, y, ((p.rows - 1) * p.y_ld + p.cols) * ES, p.status)) {
-                at_y[j] = -1;
-            } else {
-                vx[j] = x[ax];
-                if (RES) vr[j] = res[ar];
-            }
+        for (int j = 0; j < RB; ++j) {
+            vx[j] = vr[j] = W{};
+            if (in_bounds(x + j * 32 + lane, ES, p.x, (last * p.x_ld + p.cols) * ES, p.status)) vx[j] = x[j * 32 + lane];
+            if (RES && in_bounds(res + j * 32 + lane, ES, p.residual, (last * p.r_ld + p.cols) * ES, p.status))
+                vr[j] = res[j * 32 + lane];
         }
-    }
-    bool keep[RB];
-    kept<RANDOM>((uint64_t)(warp * 32 + lane), offset, keys, p.threshold, keep);
-    uint32_t mask = 0;
+        drop(vx, vr, out, keys, offset);
 #pragma unroll
-    for (int e = 0; e < RB; ++e) mask |= (uint32_t)keep[e] << e;
-#pragma unroll
-    for (int j = 0; j < RB; ++j) {
-        const uint32_t m = __shfl_sync(0xffffffffu, mask, j * 4 + (lane >> 3));
-        if (at_y[j] < 0) continue;
-        const bool k = (m >> (lane & 7)) & 1u;
-        float f[1], r[1] = {0.f};
-        unpack<DT, 1>(vx[j], f);
-        if (RES) unpack<DT, 1>(vr[j], r);
-        f[0] = RES ? (k ? fmaf(f[0], p.scale, r[0]) : r[0]) : (k ? f[0] * p.scale : 0.f);
-        y[at_y[j]] = pack<DT, 1>(f);
+        for (int j = 0; j < RB; ++j)
+            if (in_bounds(y + j * 32 + lane, ES, p.y, (last * p.y_ld + p.cols) * ES, p.status)) y[j * 32 + lane] = out[j];
+        return;
     }
+    each([&](int j, const W* ax, const W* ar, W*) {
+        vx[j] = vr[j] = W{};
+        if (in_bounds(ax, ES, p.x, (last * p.x_ld + p.cols) * ES, p.status)) vx[j] = *ax;
+        if (RES && in_bounds(ar, ES, p.residual, (last * p.r_ld + p.cols) * ES, p.status)) vr[j] = *ar;
+    });
+    drop(vx, vr, out, keys, offset);
+    each([&](int j, const W*, const W*, W* ay) {
+        if (j * 32 + lane < left && in_bounds(ay, ES, p.y, (last * p.y_ld + p.cols) * ES, p.status)) *ay = out[j];
+    });
 }
 
 template <int DT, bool RES, bool RANDOM>
 cudaError_t drop_launch(const DropoutParams& p, bool vector, cudaStream_t s) {
-    const int64_t span = (int64_t)DROP_BLOCK * RB * (vector ? DU : 1), total = p.rows * p.cols;
+    const int64_t span = (int64_t)DROP_BLOCK * RB * (vector ? DROP_TURNS<DT, RES> : 1), total = p.rows * p.cols;
     const int64_t ctas = (total + span - 1) / span;
     if (ctas > 2147483647LL) return cudaErrorInvalidValue;
-    void (*const fn)(const DropoutParams) =
-        vector ? (RANDOM && p.state ? dropout_kernel<DT, RES, RANDOM, RANDOM> : dropout_kernel<DT, RES, RANDOM, false>)
-               : (RANDOM && p.state ? dropout_elem_kernel<DT, RES, RANDOM, RANDOM>
-                                    : dropout_elem_kernel<DT, RES, RANDOM, false>);
+    constexpr bool R = RANDOM;
+    void (*fn)(const DropoutParams);
+    if (vector) {
+        fn = R && p.state ? dropout_kernel<DT, RES, R, R> : dropout_kernel<DT, RES, R, false>;
+    } else if (p.cols < 32 * RB) {
+        fn = R && p.state ? dropout_elem_kernel<DT, RES, R, R, true> : dropout_elem_kernel<DT, RES, R, false, true>;
+    } else {
+        fn = R && p.state ? dropout_elem_kernel<DT, RES, R, R, false> : dropout_elem_kernel<DT, RES, R, false, false>;
+    }
     return launch_pdl(fn, p, dim3((unsigned)ctas, 1, 1), DROP_BLOCK, 0, s);
 }
 

@@ -14,6 +14,7 @@ module raises.
 import ctypes
 import functools
 import os
+from array import array
 from dataclasses import dataclass
 from typing import List, Optional, Sequence, Tuple
 
@@ -157,22 +158,22 @@ _lib.tb_patch_gn_grad_stats.argtypes = [_P_vp, _P_vp, _i32, ctypes.c_int, _i64, 
 _lib.tb_patch_gn_grad_apply.restype = ctypes.c_int
 _lib.tb_patch_gn_grad_apply.argtypes = [_P_vp, _P_vp, _P_vp, _i32, ctypes.c_int, _i64, _i64, _P_i64, _i32, _vp, _vp,
                                         _i32, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp]
-_lib.tb_patch_gn_stats_cl.restype = ctypes.c_int
-_lib.tb_patch_gn_stats_cl.argtypes = _lib.tb_patch_gn_stats.argtypes
-_lib.tb_patch_gn_apply_cl.restype = ctypes.c_int
-_lib.tb_patch_gn_apply_cl.argtypes = _lib.tb_patch_gn_apply_gathered.argtypes
-_lib.tb_patch_group_norm_cl.restype = ctypes.c_int
-_lib.tb_patch_group_norm_cl.argtypes = _lib.tb_patch_gn_apply.argtypes
+# the channels-last calls take the addresses of their tables (parts of one array)
+_int, _f32 = ctypes.c_int, ctypes.c_float
+for _name, _args in {
+        "tb_patch_gn_stats_cl": [_vp, _i32, _int, _i64, _i64, _vp, _i32, _vp, _vp],
+        "tb_patch_gn_apply_cl": [_vp, _vp, _i32, _int, _i64, _i64, _vp, _i32, _vp, _i32, _vp, _vp, _f32, _i32, _vp],
+        "tb_patch_group_norm_cl": [_vp, _vp, _i32, _int, _i64, _i64, _vp, _i32, _vp, _vp, _vp, _f32, _i32, _vp],
+        "tb_patch_gn_grad_stats_cl": [_vp, _vp, _i32, _int, _i64, _i64, _vp, _i32, _vp, _i32, _vp, _vp, _f32, _i32, _vp,
+                                      _vp],
+        "tb_patch_gn_grad_apply_cl": [_vp, _vp, _vp, _i32, _int, _i64, _i64, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _f32,
+                                      _i32, _vp, _vp, _vp, _i64, _vp],
+        "tb_patch_group_norm_backward_cl": [_vp, _vp, _vp, _i32, _int, _i64, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _f32,
+                                            _i32, _vp, _vp, _vp, _i64, _vp]}.items():
+    getattr(_lib, _name).restype = _int
+    getattr(_lib, _name).argtypes = _args
 _lib.tb_patch_gn_workspace_cl.restype = _i64
 _lib.tb_patch_gn_workspace_cl.argtypes = [_i64, _i32]
-_lib.tb_patch_gn_grad_stats_cl.restype = ctypes.c_int
-_lib.tb_patch_gn_grad_stats_cl.argtypes = _lib.tb_patch_gn_grad_stats.argtypes
-_lib.tb_patch_gn_grad_apply_cl.restype = ctypes.c_int
-_lib.tb_patch_gn_grad_apply_cl.argtypes = [_P_vp, _P_vp, _P_vp, _i32, ctypes.c_int, _i64, _i64, _P_i64, _i32, _vp, _vp,
-                                           _i32, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp, _i64, _vp]
-_lib.tb_patch_group_norm_backward_cl.restype = ctypes.c_int
-_lib.tb_patch_group_norm_backward_cl.argtypes = [_P_vp, _P_vp, _P_vp, _i32, ctypes.c_int, _i64, _i64, _P_i64, _i32,
-                                                 _vp, _vp, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp, _i64, _vp]
 _lib.tb_dropout.restype = ctypes.c_int
 _lib.tb_dropout.argtypes = [_vp, _i64, _vp, _i64, ctypes.c_int, _i64, _i64, ctypes.c_double, ctypes.c_uint64,
                             ctypes.c_uint64, _vp, _vp, _i64, _vp]
@@ -1252,40 +1253,43 @@ def patch_group_norm_backward(grads: Sequence[torch.Tensor], patches: Sequence[t
 # channels last: PatchGroupNorm forward and backward
 # ---------------------------------------------------------------------------
 
-def _cl_args(patches, gamma, beta, **likes):
-    """(N, C, dtype, device, P, positions, gamma's and beta's address, the patches'
-    addresses, and those of each list of tensors like them) of channels-last patches
-    [N, *spatial_p, C]."""
+def _cl_args(patches, gamma, beta, *likes):
+    """(N, C, dtype, device, P, table, addresses of its parts, gamma's and beta's
+    address) of channels-last patches [N, *spatial_p, C] and lists of tensors like
+    them.  The table is one array: each patch's positions, the patches' addresses,
+    then those of each list."""
     P = len(patches)
     if not 1 <= P <= 64:
         raise ValueError("1 to 64 patches")
-    first = patches[0]
-    dt, dev, shape = first.dtype, first.get_device(), first.shape
+    x = patches[0]
+    dt, dev, shape = x.dtype, x.get_device(), x.shape
     if len(shape) < 2 or dev < 0:
         raise ValueError("patches are CUDA tensors [N, *spatial, C]")
     N, C = shape[0], shape[-1]
-    for what, ts in likes.items():
+    NC = N * C or 1
+    for ts in likes:
         if len(ts) != P:
-            raise ValueError("one %s per patch" % what)
-    spatial, ptrs, NC = [], [[] for _ in range(1 + len(likes))], N * C
-    lists = list(zip(ptrs[1:], likes.values(), likes))
-    for q, x in enumerate(patches):
-        if q:
-            shape = x.shape
-            if x.dtype is not dt or x.get_device() != dev or len(shape) < 2 or shape[0] != N or shape[-1] != C:
-                raise ValueError("patch %d: dtype, device, samples or channels differ from patch 0" % q)
+            raise ValueError("one output, and one gradient, per patch")
+    spatial, ptrs, shapes = [], [], []
+    for x in patches:
+        s = x.shape
+        if x.dtype is not dt or x.get_device() != dev or len(s) < 2 or s[0] != N or s[-1] != C:
+            raise ValueError("the patches' dtypes, devices, samples or channels differ")
         if not x.is_contiguous():
-            raise ValueError("patch %d must be contiguous" % q)
-        spatial.append(x.numel() // NC if NC else 0)
-        ptrs[0].append(x.data_ptr())
-        for at, ts, what in lists:
-            t = ts[q]
-            if t.shape != shape or t.dtype is not dt or t.get_device() != dev or not t.is_contiguous():
-                raise ValueError("%s %d must be contiguous and match patch %d" % (what, q, q))
-            at.append(t.data_ptr())
-    array = _PTRS[P]
-    return (N, C, _DTYPES[dt] if dt in _DTYPES else _dtype_code(first), dev, P, _COUNTS[P](*spatial),
-            _vec(gamma, C, dt, dev, "gamma"), _vec(beta, C, dt, dev, "beta"), *[array(*at) for at in ptrs])
+            raise ValueError("the patches must be contiguous")
+        spatial.append(x.numel() // NC)
+        ptrs.append(x.data_ptr())
+        shapes.append(s)
+    for ts in likes:
+        for t, s in zip(ts, shapes):
+            if t.shape != s or t.dtype is not dt or t.get_device() != dev or not t.is_contiguous():
+                raise ValueError("outputs and gradients must be contiguous and match their patches")
+            ptrs.append(t.data_ptr())
+    table = array("q", spatial + ptrs)
+    at = table.buffer_info()[0]
+    return (N, C, _DTYPES[dt] if dt in _DTYPES else _dtype_code(x), dev, P, table,
+            range(at, at + 8 * len(table), 8 * P), None if gamma is None else _vec(gamma, C, dt, dev, "gamma"),
+            None if beta is None else _vec(beta, C, dt, dev, "beta"))
 
 
 def _cl_records(partials: torch.Tensor, R: int, N: int, G: int, device: int) -> int:
@@ -1313,7 +1317,7 @@ def gn_workspace_cl(N: int, G: int, device=None) -> torch.Tensor:
 def tb_patch_gn_stats_cl(patches: Sequence[torch.Tensor], G: int, partials: torch.Tensor, stream=None) -> torch.Tensor:
     """``tb_patch_gn_stats`` of channels-last patches [N, *spatial_p, C]: the
     same records, in the same places."""
-    N, C, dt, dev, P, sp, _, _, xs = _cl_args(patches, None, None)
+    N, C, dt, dev, P, table, (sp, xs), _, _ = _cl_args(patches, None, None)
     _check(_lib.tb_patch_gn_stats_cl(xs, P, dt, N, C, sp, G, _cl_records(partials, P, N, G, dev),
                                      _stream_of(stream, dev)), "tb_patch_gn_stats_cl")
     return partials
@@ -1325,7 +1329,7 @@ def tb_patch_gn_apply_cl(patches: Sequence[torch.Tensor], outs: Sequence[torch.T
     """Normalise (+ SiLU) channels-last patches [N, *spatial_p, C] into
     ``outs`` (``outs[p]`` may be ``patches[p]``) with the statistics pooled
     over the ``R`` record sets in ``partials``."""
-    N, C, dt, dev, P, sp, ga, be, xs, os_ = _cl_args(patches, gamma, beta, output=outs)
+    N, C, dt, dev, P, table, (sp, xs, os_), ga, be = _cl_args(patches, gamma, beta, outs)
     _check(_lib.tb_patch_gn_apply_cl(xs, os_, P, dt, N, C, sp, G,
                                      _cl_records(partials, R, N, G, dev), R, ga, be, eps, 1 if silu else 0,
                                      _stream_of(stream, dev)), "tb_patch_gn_apply_cl")
@@ -1346,7 +1350,7 @@ def patch_group_norm_cl(patches: Sequence[torch.Tensor], G: int, gamma: Optional
             [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in patches] if outs is None else outs,
             new_partials(len(patches), patches[0].shape[0], G, patches[0].device) if partials is None else partials),
             stream)
-    N, C, dt, dev, P, sp, ga, be, xs, os_ = _cl_args(patches, gamma, beta, output=outs)
+    N, C, dt, dev, P, table, (sp, xs, os_), ga, be = _cl_args(patches, gamma, beta, outs)
     status = _lib.tb_patch_group_norm_cl(xs, os_, P, dt, N, C, sp, G, _cl_records(partials, P, N, G, dev), ga, be, eps,
                                          1 if silu else 0, _stream_of(stream, dev))
     if status:
@@ -1360,7 +1364,7 @@ def tb_patch_gn_grad_stats_cl(grads: Sequence[torch.Tensor], patches: Sequence[t
                               silu: bool = True, stream=None) -> torch.Tensor:
     """``tb_patch_gn_grad_stats`` of channels-last patches and gradients: the
     same records, in the same places."""
-    N, C, dt, dev, P, sp, ga, be, xs, ds = _cl_args(patches, gamma, beta, gradient=grads)
+    N, C, dt, dev, P, table, (sp, xs, ds), ga, be = _cl_args(patches, gamma, beta, grads)
     _check(_lib.tb_patch_gn_grad_stats_cl(xs, ds, P, dt, N, C, sp, G,
                                           _cl_records(partials, R, N, G, dev), R, ga, be, eps, 1 if silu else 0,
                                           _grad_partials(grad_partials, P, N, C, dev), _stream_of(stream, dev)),
@@ -1378,7 +1382,7 @@ def tb_patch_gn_grad_apply_cl(grads: Sequence[torch.Tensor], patches: Sequence[t
     ``grads[p]`` or ``patches[p]``), and of the weights into ``dgamma`` /
     ``dbeta``, from the ``R`` record sets of both passes.  ``workspace`` comes
     from ``gn_workspace_cl``."""
-    N, C, dt, dev, P, sp, ga, be, xs, ds, os_ = _cl_args(patches, gamma, beta, gradient=grads, dx=dxs)
+    N, C, dt, dev, P, table, (sp, xs, ds, os_), ga, be = _cl_args(patches, gamma, beta, grads, dxs)
     gp, bp = _vec(dgamma, C, patches[0].dtype, dev, "dgamma"), _vec(dbeta, C, patches[0].dtype, dev, "dbeta")
     _check(_lib.tb_patch_gn_grad_apply_cl(xs, ds, os_, P, dt, N, C, sp, G,
                                           _cl_records(partials, R, N, G, dev),
@@ -1410,7 +1414,7 @@ def patch_group_norm_backward_cl(grads: Sequence[torch.Tensor], patches: Sequenc
                     new_grad_partials(P, N, C, dev) if grad_partials is None else grad_partials,
                     gn_workspace_cl(N, G, dev) if workspace is None else workspace)
         dxs, dgamma, dbeta, grad_partials, workspace = _on_stream(make, stream)
-    N, C, dt, dev, P, sp, ga, be, xs, ds, os_ = _cl_args(patches, gamma, beta, gradient=grads, dx=dxs)
+    N, C, dt, dev, P, table, (sp, xs, ds, os_), ga, be = _cl_args(patches, gamma, beta, grads, dxs)
     wdt = patches[0].dtype
     status = _lib.tb_patch_group_norm_backward_cl(xs, ds, os_, P, dt, N, C, sp, G, _cl_records(partials, P, N, G, dev),
                                                   _grad_partials(grad_partials, P, N, C, dev), ga, be, eps,

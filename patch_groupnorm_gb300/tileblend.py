@@ -1449,8 +1449,8 @@ def tb_dropout(x: torch.Tensor, y: torch.Tensor, p: float, seed: int, offset: in
     if residual is not None:
         rp, r_ld = residual.data_ptr(), _row_ld(residual, shape, dt, dev, "residual")
     status = _lib.tb_dropout(x.data_ptr(), _row_ld(x, shape, dt, dev, "x"), rp, r_ld, _dtype_code(x),
-                             x.numel() // cols if cols else 0, cols, p, seed & 0xFFFFFFFFFFFFFFFF,
-                             offset & 0xFFFFFFFFFFFFFFFF, _vec(state, 2, torch.int64, dev, "state"), y.data_ptr(),
+                             x.numel() // cols if cols else 0, cols, p, int(seed) & 0xFFFFFFFFFFFFFFFF,
+                             int(offset) & 0xFFFFFFFFFFFFFFFF, _vec(state, 2, torch.int64, dev, "state"), y.data_ptr(),
                              _row_ld(y, shape, dt, dev, "y"), _stream_of(stream, dev))
     if status:
         raise TileBlendError(status, "tb_dropout")

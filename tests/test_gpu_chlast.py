@@ -336,6 +336,77 @@ def test_offsets_past_32_bits(tbl):
     assert dx[0, -1, 7] == 1.0 and dx[0, 0, 40] == 2.0
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("G", [1, 8192])
+def test_the_most_channels(tbl, G, dtype):
+    # one group of all of them, and a group each; the records of two patches
+    dt = DT[dtype]
+    xs = [rows_of(k, (1, 40 + k, 8192), dt, 1.0, 0.5) for k in (1, 2)]
+    dys = [rows_of(5 + k, x.shape, dt) for k, x in enumerate(xs)]
+    gamma, beta = weights_of(3, 8192, dt)
+    x = torch.cat(xs, 1).double().reshape(1, -1, G, 8192 // G)
+    mu = x.mean((1, 3), keepdim=True)
+    rstd = 1 / (((x - mu) ** 2).mean((1, 3), keepdim=True) + 1e-6).sqrt()
+    xhat = (x - mu) * rstd
+    z = xhat * gamma.double().reshape(G, -1) + beta.double().reshape(G, -1)
+    part = tbl.new_partials(2, 1, G)
+    ys = tbl.patch_group_norm_cl(xs, G, gamma, beta, 1e-6, partials=part)
+    got = torch.cat(ys, 1).double().reshape(x.shape)
+    want = z * torch.sigmoid(z)
+    # half a step of the output, and 64 u of z (at most 40 and of slope 1.1) and of the statistics
+    assert ((got - want).abs() <= want.abs() * HALF[dt] + 64 * U * (z.abs() + 8) * 1.1).all()
+    dxs, dg, db = tbl.patch_group_norm_backward_cl(dys, xs, G, part, gamma, beta, 1e-6)
+    s = torch.sigmoid(z)
+    dz = torch.cat(dys, 1).double().reshape(x.shape) * s * (1 + z * (1 - s))
+    gam = gamma.double().reshape(G, -1)
+    v = dz * gam
+    dx = (v - v.mean((1, 3), keepdim=True) - xhat * (v * xhat).mean((1, 3), keepdim=True)) * rstd
+    scale = rstd.max() * (v.abs() + 1 + xhat.abs()) * 8
+    assert ((torch.cat(dxs, 1).double().reshape(x.shape) - dx).abs() <= dx.abs() * HALF[dt] + 64 * U * scale).all()
+    for t, w, m in ((dg, (dz * xhat).sum(1), (dz * xhat).abs().sum(1)), (db, dz.sum(1), dz.abs().sum(1))):
+        assert ((t.double() - w.reshape(-1)).abs() <= w.reshape(-1).abs() * HALF[dt] + 128 * U * (m.reshape(-1) + 1)).all()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_more_columns_than_a_cluster_takes(tbl, dtype):
+    # tensors at different offsets (single elements), each CTA with all columns in turn
+    dt = DT[dtype]
+    shape, C, G = (1, 5, 2601), 2601, 9
+    x, dy = rows_of(1, shape, dt, 1.0, 0.5), rows_of(2, shape, dt)
+    gamma, beta = weights_of(3, C, dt)
+    buf = torch.full((3, (x.numel() + 24) // 8 * 8), 7.0, dtype=dt, device="cuda")
+    mx, md, mo = (b[a:a + x.numel()].view(shape) for a, b in zip((1, 2, 3), buf))
+    mx.copy_(x)
+    md.copy_(dy)
+    part = tbl.new_partials(1, 1, G)
+    tbl.patch_group_norm_cl([mx], G, gamma, beta, 1e-6, outs=[mo], partials=part)
+    check_forward([x], G, gamma, beta, 1e-6, True, [mo])
+    _, dg, db = tbl.patch_group_norm_backward_cl([md], [mx], G, part, gamma, beta, 1e-6, dxs=[mo])
+    check_backward([dy], [x], G, gamma, beta, 1e-6, True, [mo], dg, db)
+
+
+def test_the_two_ways_agree(tbl):
+    # in one launch, and in the launches of the general path
+    for shape, G in (((1, 1024, 512), 32), ((2, 500, 64), 8), ((1, 700, 37), 1)):
+        for dt in (torch.float32, torch.bfloat16):
+            x, dy = rows_of(1, shape, dt, 1.0, 3.0), rows_of(2, shape, dt)
+            gamma, beta = weights_of(3, shape[-1], dt)
+            part = tbl.new_partials(1, shape[0], G)
+            y, = tbl.patch_group_norm_cl([x], G, gamma, beta, 1e-6, partials=part)
+            rec = tbl.tb_patch_gn_stats_cl([x], G, tbl.new_partials(1, shape[0], G))
+            w, = tbl.tb_patch_gn_apply_cl([x], [torch.empty_like(x)], G, rec, 1, gamma, beta, 1e-6)
+            (dx,), dg, db = tbl.patch_group_norm_backward_cl([dy], [x], G, part, gamma, beta, 1e-6)
+            grec = tbl.tb_patch_gn_grad_stats_cl([dy], [x], G, rec, 1, gamma, beta, 1e-6,
+                                                 tbl.new_grad_partials(1, shape[0], shape[-1]))
+            vg, vb, vx = torch.empty_like(dg), torch.empty_like(db), torch.empty_like(x)
+            tbl.tb_patch_gn_grad_apply_cl([dy], [x], [vx], G, rec, grec, 1, gamma, beta, 1e-6,
+                                          tbl.gn_workspace_cl(shape[0], G), vg, vb)
+            # both round once what differs by fp32 arithmetic: a step apart at most, or 64 u of the values' size
+            for a, b in ((y, w), (dx, vx), (dg, vg), (db, vb)):
+                a, b = a.double(), b.double()
+                assert ((a - b).abs() <= 2 * HALF[dt] * b.abs() + 64 * U * b.abs().max()).all()
+
+
 def _pass(tbl, x, dy, gamma, beta, stream=None):
     part = tbl._on_stream(lambda: tbl.new_partials(1, 1, 4), stream)
     y = tbl.patch_group_norm_cl([x], 4, gamma, beta, 1e-6, partials=part, stream=stream)
@@ -343,14 +414,19 @@ def _pass(tbl, x, dy, gamma, beta, stream=None):
     return [*y, *dxs, dg, db]
 
 
-def _inputs(seed=0):
+# one that fits into shared memory, one that does not
+LENGTHS = [500, 600000]
+
+
+def _inputs(length, seed=0):
     bf = torch.bfloat16
-    return [rows_of(seed + 1, (1, 500, 16), bf), rows_of(seed + 2, (1, 500, 16), bf), *weights_of(seed + 3, 16, bf)]
+    return [rows_of(seed + 1, (1, length, 16), bf), rows_of(seed + 2, (1, length, 16), bf), *weights_of(seed + 3, 16, bf)]
 
 
+@pytest.mark.parametrize("length", LENGTHS)
 @pytest.mark.parametrize("raw", [False, True])
-def test_on_another_stream(tbl, raw):
-    ins = _inputs()
+def test_on_another_stream(tbl, raw, length):
+    ins = _inputs(length)
     want = _pass(tbl, *ins)
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
@@ -360,8 +436,9 @@ def test_on_another_stream(tbl, raw):
         assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
-def test_replay_from_a_graph(tbl):
-    ins = _inputs()
+@pytest.mark.parametrize("length", LENGTHS)
+def test_replay_from_a_graph(tbl, length):
+    ins = _inputs(length)
     s = torch.cuda.Stream()
     with torch.cuda.stream(s):
         _pass(tbl, *ins)
@@ -370,7 +447,7 @@ def test_replay_from_a_graph(tbl):
     with torch.cuda.graph(g, stream=s):
         outs = _pass(tbl, *ins)
     for seed in (100, 200):
-        for t, u in zip(ins, _inputs(seed)):
+        for t, u in zip(ins, _inputs(length, seed)):
             t.copy_(u)
         g.replay()
         torch.cuda.synchronize()

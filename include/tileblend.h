@@ -1,7 +1,7 @@
 /*
  * tileblend.h -- C ABI of libtileblend: tiled-VAE tile stitching,
- * patch-parallel GroupNorm, and the norms and gradient clipping of a training
- * step on NVIDIA GB300 (sm_103a).
+ * patch-parallel GroupNorm, and the norms, dropout and gradient clipping of a
+ * training step on NVIDIA GB300 (sm_103a).
  *
  * Sources of the operations (web pages, cited by title and section):
  *   [VTB] "[Proposal] Vectorize tiled VAE blending while preserving rounding
@@ -842,8 +842,14 @@ tb_status tb_patch_gn_apply_cl(const void* const* patches, void* const* outs, in
                                int64_t C, const int64_t* spatial, int32_t G, const tb_gn_partial* partials, int32_t R,
                                const void* gamma, const void* beta, float eps, int32_t silu, void* stream);
 
-/* tb_patch_group_norm_cl -- both steps in one call, on these patches' own
- * records (R = P). */
+/*
+ * tb_patch_group_norm_cl -- both steps in one call.
+ *   partials  device [P][N][G][TB_GN_PARTS], 16-byte aligned, written fully:
+ *             records that describe the P patches together (R = P record sets
+ *             for the backward pass, or for ranks that gather them).  Which of
+ *             them holds what is not specified; tb_patch_gn_stats_cl writes
+ *             each patch's own
+ * Where the patches fit into shared memory this is one launch. */
 tb_status tb_patch_group_norm_cl(const void* const* patches, void* const* outs, int32_t P, tb_dtype dtype, int64_t N,
                                  int64_t C, const int64_t* spatial, int32_t G, tb_gn_partial* partials,
                                  const void* gamma, const void* beta, float eps, int32_t silu, void* stream);
@@ -874,8 +880,12 @@ tb_status tb_patch_gn_grad_apply_cl(const void* const* patches, const void* cons
                                     const void* gamma, const void* beta, float eps, int32_t silu, void* dgamma,
                                     void* dbeta, void* workspace, int64_t workspace_bytes, void* stream);
 
-/* tb_patch_group_norm_backward_cl -- both steps of the backward pass in one
- * call, on these patches' own records (R = P). */
+/*
+ * tb_patch_group_norm_backward_cl -- both steps of the backward pass in one
+ * call, from R = P record sets of these patches.
+ *   grad_partials  device [P][N][C][TB_GN_PARTS], 16-byte aligned: a workspace
+ *                  here; its contents afterwards are not specified
+ * Where patches and gradients fit into shared memory this is one launch. */
 tb_status tb_patch_group_norm_backward_cl(const void* const* patches, const void* const* grads, void* const* outs,
                                           int32_t P, tb_dtype dtype, int64_t N, int64_t C, const int64_t* spatial,
                                           int32_t G, const tb_gn_partial* partials,

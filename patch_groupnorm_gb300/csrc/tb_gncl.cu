@@ -6,7 +6,17 @@
 // single x * a + b would lose where the mean is far from zero.
 //
 // Statistics need all of a group before the first output, so x is read twice, by
-// two launches; what is bound by memory is bound there.
+// two launches (where it fits into shared memory, once: tb_gncl_fused.cu).  1 x 256 x
+// 256 x 512 bf16 in four patches takes 37.7 us, 16.3 of them the statistics; 67 MB
+// read twice and written once are 31 us at the copy rate.  What is left is the start
+// and the end of each launch: sums joined over rows, groups and clusters, a latency
+// after the other (3 us), and the groups' pooled statistics before the first output
+// (2 us).  13 x 120 x 208 x 384: 126 us, of 115 at that rate.
+//
+// Statistics grids: 288 CTAs in clusters of 3 for four patches on 152 SMs; 256 in
+// clusters of 8 took 18.8 us for the first and 50.8 for the second (16.3, 43), 304
+// that find no room at once 23 and 65.  Splits of the channels down to 64 bytes a
+// position cost nothing (16.1 us), of 32 bytes 20.4.
 #include "tb_gncl.cuh"
 
 namespace tb {
@@ -18,8 +28,8 @@ constexpr int FOLD = 64;  // chunks between two foldings of a thread's sums
 constexpr int DEPTH = 8;  // chunks of a thread on their way or in work
 
 // Each thread sums x - K and (x - K)^2 of its VEC channels on packed pairs, K its
-// own first value, then its mean so far; after DEPTH, DEPTH, 2 DEPTH, 4 DEPTH, ... and then every
-// FOLD chunks the sums are merged into (mean, M2) (Chan), so that neither a far mean
+// own first value, then its mean so far; after DEPTH, DEPTH, 2 DEPTH, 4 DEPTH, ... and
+// then every FOLD chunks the sums are merged into (mean, M2) (Chan), so that neither a far mean
 // nor a long run loses digits, nor a first value far from all others: n chunks
 // about a mean that it has moved by 1 / n of its distance add 1 / n of its square.
 // A CTA's threads meet in shared memory, group by group, and the CTAs of a
@@ -140,7 +150,9 @@ size_t stats_smem(int groups) {
 
 // --- normalisation ------------------------------------------------------------------
 
-constexpr int APPLY_DEPTH = 6;  // as DEPTH
+// As DEPTH.  Two CTAs per SM; 8 chunks and two, or 6 and three, take 88 us for 13 x 120 x
+// 208 x 384 bf16 alone, 6 and two 79: reads and writes together want fewer on their way.
+constexpr int APPLY_DEPTH = 6;
 
 template <int DT, int VEC, bool SILU>
 __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_apply_kernel(const __grid_constant__ GnClParams p) {

@@ -137,7 +137,9 @@ __device__ __forceinline__ bool index_ok(bool ok, uint32_t* status) {
 // SMs as the last wave drains (small stitches 12-18% faster back to back).  The
 // records of the GroupNorm's backward pass, for the dx that follow: one CTA
 // fills an SM, so the next grid's CTAs start as this one's leave, and set their
-// rings up while the others work.  The forward GroupNorm's statistics grid is
+// rings up while the others work.  The constants of the channels-last GroupNorm's
+// backward pass, a small grid, for the dx that follow in the same call (and fetch x
+// and dy before they wait).  The forward GroupNorm's statistics grid is
 // one wave spread evenly over the SMs, and a grid placed early, while its
 // predecessor drains, lands unevenly (measured up to 2x slower); so no kernel
 // that may precede it in a sharded decode -- the Patchify copy, the forward
@@ -484,7 +486,7 @@ struct GnClParams {
     int64_t spatial[GN_MAXP];
     GnPartial* partials;           // [P or R][N][G][TB_GN_PARTS]
     float2* grad_partials;         // (sum dz, sum dz * xhat): [P or R][N][C][TB_GN_PARTS]
-    float4* coefs;                 // (mean, rstd, u, v): [N][G], see GnClGradApply
+    float4* coefs;                 // (mean, rstd, u, v): [N][G] (dx = a dz + u d + v, tb_gncl_bwd.cu)
     const void* gamma;             // [C] or null
     const void* beta;              // [C] or null
     void* dgamma;                  // [C] or null

@@ -1,9 +1,9 @@
 """Python binding of libtileblend (include/tileblend.h).
 
-Argument marshalling only: every step of the stitch, of PatchGroupNorm and of
-the training calls (layer norm, gradient clipping, PatchGroupNorm's backward
-pass) runs in the library's CUDA kernels.  Tensors must be CUDA tensors on the
-current device, contiguous (the layer norm takes strided rows), of one dtype
+Argument marshalling only: every step of the stitch, of PatchGroupNorm (channels
+first and last) and of the training calls (layer norm, gradient clipping,
+PatchGroupNorm's backward pass, dropout) runs in the library's CUDA kernels.  Tensors must be CUDA tensors on the
+current device, contiguous (the layer norm and dropout take strided rows), of one dtype
 (float32, float16 or bfloat16).
 Calls are asynchronous on the current torch stream unless ``stream`` (a
 ``torch.cuda.Stream`` or a raw ``cudaStream_t`` integer) is given.
@@ -1341,8 +1341,8 @@ def patch_group_norm_cl(patches: Sequence[torch.Tensor], G: int, gamma: Optional
                         outs: Optional[Sequence[torch.Tensor]] = None, partials: Optional[torch.Tensor] = None,
                         stream=None) -> Sequence[torch.Tensor]:
     """Both steps for channels-last patches [N, *spatial_p, C]: GroupNorm (+
-    SiLU) of the whole tensor over its patches.  Outputs that are not given
-    are made."""
+    SiLU) of the whole tensor over its patches.  ``partials`` receives records
+    that describe the patches together.  Outputs that are not given are made."""
     if outs is None or partials is None:
         if len(patches) == 0:
             raise ValueError("at least one patch")

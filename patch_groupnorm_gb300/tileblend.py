@@ -1439,18 +1439,18 @@ def tb_dropout(x: torch.Tensor, y: torch.Tensor, p: float, seed: int, offset: in
     gradient, without a residual, is the backward pass.  ``seed`` and
     ``offset`` are taken modulo 2^64; ``state``, a contiguous int64 tensor of
     two, is added to them when the kernel runs."""
-    shape, dev = x.shape, x.get_device()
+    shape, dev, dt = x.shape, x.get_device(), x.dtype
     if dev < 0:
         raise ValueError("the rows must be CUDA tensors")
     if not shape:
         raise ValueError("rows of elements")
-    dt, cols = x.dtype, shape[-1]
-    rp, r_ld = None, 0
+    cols, rp, r_ld = shape[-1], None, 0
     if residual is not None:
         rp, r_ld = residual.data_ptr(), _row_ld(residual, shape, dt, dev, "residual")
-    status = _lib.tb_dropout(x.data_ptr(), _row_ld(x, shape, dt, dev, "x"), rp, r_ld, _dtype_code(x),
-                             x.numel() // cols if cols else 0, cols, p, int(seed) & 0xFFFFFFFFFFFFFFFF,
-                             int(offset) & 0xFFFFFFFFFFFFFFFF, _vec(state, 2, torch.int64, dev, "state"), y.data_ptr(),
+    status = _lib.tb_dropout(x.data_ptr(), cols if x.is_contiguous() else _row_ld(x, shape, dt, dev, "x"), rp, r_ld,
+                             _DTYPES[dt] if dt in _DTYPES else _dtype_code(x), x.numel() // cols if cols else 0, cols, p,
+                             int(seed) & 0xFFFFFFFFFFFFFFFF, int(offset) & 0xFFFFFFFFFFFFFFFF,
+                             None if state is None else _vec(state, 2, torch.int64, dev, "state"), y.data_ptr(),
                              _row_ld(y, shape, dt, dev, "y"), _stream_of(stream, dev))
     if status:
         raise TileBlendError(status, "tb_dropout")

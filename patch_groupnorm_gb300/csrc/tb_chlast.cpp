@@ -175,8 +175,8 @@ tb_status cl_plan_stats(tb::GnClParams& prm, tb_dtype dtype, bool vector, int ct
 // tb_gncl_fused.cu): of the ways for which all clusters have room at once, the fastest
 // by an account fitted to measurements (us): 5.5 (backward 6.4) for the launch and the
 // joining of sums, 0.43 (0.62) for each chunk that a thread takes after the other, half
-// as much again with twice the threads on an SM, and forward more where few channels
-// of a chunk share a group.  The general path takes 9.8 and 0.36 a MB (12 and 0.26):
+// as much again with twice the threads on an SM, and forward 0.25 for every further sum
+// that a chunk leaves.  The general path takes 9.8 and 0.36 a MB (12 and 0.26):
 // where that is less, it is taken.  Both, by graph: 2 patches of 15 x 16 x 64 bf16 5.5
 // and 7.9 us (6.6 and 10.7), 64 x 64 x 512 8.9 and 11.3 (11.4 and 14.1), 80 x 80 x 512
 // 11.3 and 12.1, 96 x 96 x 512 13.8 and 13.5; where the groups cannot be split among
@@ -194,7 +194,7 @@ bool cl_plan_fused(tb::GnClParams& prm, tb_dtype dtype, bool grad, int sms, int*
     uint32_t rows[tb::GN_MAXP];  // below 2^31: they fit into shared memory
     for (int p = 0; p < prm.P; ++p)
         rows[p] = (uint32_t)((prm.spatial[p] * prm.C / vec + prm.period - 1) / prm.period);
-    const int unit = std::min(vec, prm.K & -prm.K);
+    const int unit = std::min(vec, prm.K & -prm.K), sums = prm.K >= vec && unit * 2 < vec ? 2 : vec / unit;
     double best = (grad ? 12.0 : 9.8) + (grad ? 0.26e-6 : 0.36e-6) * bytes;
     int32_t splits = 0, slabs = 0, columns = 0, cluster = 0, most = 0;
     for (int s = 1; s <= prm.G && (s == 1 || prm.C / s * es >= 64); s *= 2) {
@@ -215,7 +215,7 @@ bool cl_plan_fused(tb::GnClParams& prm, tb_dtype dtype, bool grad, int sms, int*
                 if ((double)ctas > cl_places(c, per_sm) * per_sm * sms) continue;
                 const int64_t threads = std::min<int64_t>(per_sm, (ctas + sms - 1) / sms) * b;
                 const double us = grad ? 6.4 + held * (0.24 + threads / 670.0)
-                                       : 5.5 + held * (0.2 + threads / 1100.0) + 0.25 * (vec / unit - 1);
+                                       : 5.5 + held * (0.2 + threads / 1100.0) + 0.25 * (sums - 1);
                 if (us >= best) continue;
                 best = us;
                 splits = s;

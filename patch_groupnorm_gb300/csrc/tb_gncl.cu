@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
     extern __shared__ uint4 shared4[];
     using Stream = ClStream<DT, VEC, 1, DEPTH>;
     float* const stage_mean = reinterpret_cast<float*>(shared4 + Stream::SMEM / 16);  // [CL_BLOCK * VEC]
-    float* const stage_m2 = stage_mean + CL_BLOCK * VEC;              // [CL_BLOCK * VEC]
+    float* const stage_m2 = stage_mean + CL_BLOCK * VEC;
     int* const stage_n = reinterpret_cast<int*>(stage_m2 + CL_BLOCK * VEC);  // [CL_BLOCK]
     const int C = (int)p.C, G = p.G, K = p.K;
     const int gs = G / p.splits, g0 = (int)blockIdx.y * gs, g1 = g0 + gs;  // this CTA's groups
@@ -54,7 +54,6 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
     const ClRun run = cl_run<ES, VEC>(p.patches[u.p], p.spatial[u.p], p.C, u.n);
     const char* const patch = static_cast<const char*>(p.patches[u.p]);
     const int64_t bytes = p.N * run.elems * ES;
-    const int unit = cl_unit_channels(VEC, K, run.head);
     grid_wait();
 
     // elements outside the whole chunks: the first piece's before, the last one's after; a lane each
@@ -90,10 +89,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
             sums.fold(done, now);
         }
         __syncthreads();  // the table is set, or the columns before these are merged
-        sums.store(w.count, unit, stage_mean, stage_m2);
-        stage_n[threadIdx.x] = w.count * unit;
-        __syncthreads();
-        cl_join_groups<VEC>(q, run.head, j0, j1, unit, C, K, g0, gs, stage_mean, stage_m2, stage_n, warps, table);
+        cl_join(sums, w.count, q, run.head, j0, j1, C, K, g0, gs, stage_mean, stage_m2, stage_n, warps, table);
     }
     __syncthreads();
     if (VEC > 1 && warp == 0) {

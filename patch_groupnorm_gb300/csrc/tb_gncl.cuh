@@ -275,7 +275,7 @@ struct ClMoments {
         }
     }
     // Into shared memory: `unit` neighbouring channels, which are one group's, as one.
-    __device__ __forceinline__ void store(int count, int unit, float* stage_mean, float* stage_m2) const {
+    __device__ __forceinline__ void store_units(int count, int unit, float* stage_mean, float* stage_m2) const {
         float fm[VEC], f2[VEC];
         cl_values<VEC>(mean, fm);
         cl_values<VEC>(m2, f2);
@@ -303,10 +303,48 @@ struct ClMoments {
             }
         }
     }
+    // Into shared memory, two sums: of the first `in_first` lanes, which are one group's, and
+    // of the others, which are the next one's (their counts are equal).
+    __device__ __forceinline__ void store_pairs(int count, int in_first, float* stage_mean, float* stage_m2) const {
+        float fm[VEC], f2[VEC];
+        cl_values<VEC>(mean, fm);
+        cl_values<VEC>(m2, f2);
+        float s0 = 0.f, s1_ = 0.f, q0 = 0.f, q1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            s0 += i < in_first ? fm[i] - fm[0] : 0.f;
+            s1_ += i < in_first ? 0.f : fm[i] - fm[VEC - 1];
+        }
+        const float m0 = fm[0] + __fdividef(s0, (float)in_first);
+        const float m1 = in_first < VEC ? fm[VEC - 1] + __fdividef(s1_, (float)(VEC - in_first)) : 0.f;
+        const float n = (float)count;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            // rounding may have left a tiny negative sum of squares: it is a zero one
+            const float d = fm[i] - (i < in_first ? m0 : m1), q = fmaf(n * d, d, f2[i] < 0.f ? 0.f : f2[i]);
+            q0 += i < in_first ? q : 0.f;
+            q1 += i < in_first ? 0.f : q;
+        }
+        stage_mean[threadIdx.x * 2] = m0;
+        stage_mean[threadIdx.x * 2 + 1] = m1;
+        stage_m2[threadIdx.x * 2] = q0;
+        stage_m2[threadIdx.x * 2 + 1] = q1;
+    }
 };
 
-// Channels that every chunk has side by side in one group: a power of two.
+// What a thread leaves of a chunk: one sum for every `unit` lanes, the largest power of
+// two that divides a group's channels and the elements before the first chunk; where
+// that is less than half a chunk and a group has at least a chunk's channels, two sums,
+// of the lanes of either group (each lane's alone took 2.3 us to join, 1.2 with two).
 __device__ __forceinline__ int cl_unit_channels(int VEC, int K, int head) { return min(VEC, (K | head) & -(K | head)); }
+__device__ __forceinline__ bool cl_in_pairs(int VEC, int K, int unit) { return VEC > 2 && unit * 2 < VEC && K >= VEC; }
+
+// Lanes of a chunk at column `col` that belong to its first channel's group.
+__device__ __forceinline__ int cl_in_first(int VEC, int head, int col, int C, int K) {
+    int c = head + col * VEC;
+    if (c >= C) c %= C;
+    return min(VEC, K - c % K);
+}
 
 // Sums of a pair over `team` neighbouring threads (a power of two, the same for all
 // threads of the CTA), for every one of them; teams of several warps meet in `warps`
@@ -331,50 +369,62 @@ __device__ __forceinline__ float2 cl_team_sum(float a, float b, int team, float2
 }
 
 // The staged sums of groups g0 .. g0 + gs - 1 join those groups' entries of `table`
-// (count, mean, M2).  The units of a row that are one group's lie in phases [head + j0 *
-// VEC, head + j1 * VEC), in runs of at most K / unit.  A team of threads joins a group:
-// the mean about one of its means, then squares about that mean, corrected by what it
-// was off (it may come from a value far from all others).
-template <int VEC>
+// (count, mean, M2).  The lanes of a row that are one group's lie in phases [head + j0 *
+// VEC, head + j1 * VEC), in runs of at most K.  A team of threads joins a group: the
+// mean about one of its means, then squares about that mean, corrected by what it was
+// off (it may come from a value far from all others).  PAIRS: two sums a chunk.
+template <int VEC, bool PAIRS>
 __device__ __forceinline__ void cl_join_groups(const ClPlace& q, int head, int j0, int j1, int unit, int C, int K, int g0,
                                                int gs, const float* stage_mean, const float* stage_m2,
                                                const int* stage_n, float2* warps, float4* table) {
-    const int log2_unit = 31 - __clz(unit), log2_each = (VEC == 8 ? 3 : VEC == 4 ? 2 : 0) - log2_unit;
+    // in units of lanes (PAIRS: in lanes)
+    const int log2_unit = PAIRS ? 0 : 31 - __clz(unit), log2_each = (VEC == 8 ? 3 : VEC == 4 ? 2 : 0) - log2_unit;
     const int lo = (head + j0 * VEC) >> log2_unit, hi = (head + j1 * VEC) >> log2_unit, pitch = q.width << log2_each;
     const int Ku = K >> log2_unit, Cu = C >> log2_unit;
     // a warp to a group; more where that leaves threads idle and has much to add up
     int team = 32;
     while (team > 1 && gs * team > (int)blockDim.x) team >>= 1;
-    while (gs * team * 2 <= (int)blockDim.x && q.rows * pitch > gs * team * 8) team <<= 1;
+    while (gs * team * 2 <= (int)blockDim.x && q.rows * (PAIRS ? q.width : pitch) > gs * team * 8) team <<= 1;
     const int lane = threadIdx.x & (team - 1);
     for (int first = 0; first < gs; first += (int)blockDim.x / team) {
         const int i = first + (int)threadIdx.x / team, c0 = (g0 + i) * Ku;
         const int m_first = lo >= c0 + Ku ? (lo - c0 - Ku) / Cu + 1 : 0;
+        // body(entry, its elements), for each of this thread's
         auto each = [&](auto&& body) {
             if (i >= gs) return;
             for (int m = m_first; c0 + m * Cu < hi; ++m) {
-                const int from = max(c0 + m * Cu, lo) - lo, len = min(c0 + m * Cu + Ku, hi) - lo - from;
+                const int start = c0 + m * Cu - lo, from = max(start, 0), to = min(start + Ku, hi - lo);
+                // PAIRS: the run's chunks; its first one begins with another group's lanes if the
+                // run starts inside it
+                const int at0 = PAIRS ? from / VEC : from, len = (PAIRS ? (to + VEC - 1) / VEC : to) - at0;
                 const float per = __fdividef(1.f, (float)len);
                 for (int e = lane; e < q.rows * len; e += team) {
                     // e / len: both below 2^13, so half a step keeps the product from the borders
-                    const int row = (int)(((float)e + 0.5f) * per);
-                    body(row * pitch + from + (e - row * len));
+                    const int row = (int)(((float)e + 0.5f) * per), at = at0 + e - row * len;
+                    if constexpr (PAIRS) {
+                        const int t = row * q.width + at, lanes = min(to, at * VEC + VEC) - max(from, at * VEC);
+                        body(t * 2 + (start > at * VEC ? 1 : 0), (float)(stage_n[t] * lanes));
+                    } else {
+                        body(row * pitch + at, (float)stage_n[(row * pitch + at) >> log2_each]);
+                    }
                 }
             }
         };
-        const int at0 = i < gs && c0 + m_first * Cu < hi ? max(c0 + m_first * Cu, lo) - lo : 0;
-        const float k0 = stage_mean[at0];
+        float k0 = 0.f;
+        if (i < gs && c0 + m_first * Cu < hi) {
+            const int start = c0 + m_first * Cu - lo, from = max(start, 0);
+            k0 = stage_mean[PAIRS ? from / VEC * 2 + (start > from / VEC * VEC ? 1 : 0) : from];
+        }
         float n = 0.f, s = 0.f;
-        each([&](int at) {
-            const float ni = (float)stage_n[at >> log2_each];
+        each([&](int at, float ni) {
             n += ni;
             s = fmaf(ni, stage_mean[at] - k0, s);
         });
         const float2 ns = cl_team_sum(n, s, team, warps);
         const float inv = ns.x > 0.f ? 1.f / ns.x : 0.f, mean = fmaf(ns.y, inv, k0);
         float off = 0.f, m2 = 0.f;
-        each([&](int at) {
-            const float ni = (float)stage_n[at >> log2_each], d = stage_mean[at] - mean;
+        each([&](int at, float ni) {
+            const float d = stage_mean[at] - mean;
             off = fmaf(ni, d, off);
             m2 += fmaf(ni * d, d, ni > 0.f ? stage_m2[at] : 0.f);
         });
@@ -385,6 +435,25 @@ __device__ __forceinline__ void cl_join_groups(const ClPlace& q, int head, int j
             chan(t.x, t.y, t.z, ns.x, mean + by, left < 0.f ? 0.f : left);
             table[i] = t;
         }
+    }
+}
+
+// A thread's sums into shared memory, and from there into the table.
+template <int DT, int VEC>
+__device__ __forceinline__ void cl_join(const ClMoments<DT, VEC>& sums, int count, const ClPlace& q, int head, int j0, int j1,
+                                        int C, int K, int g0, int gs, float* stage_mean, float* stage_m2, int* stage_n,
+                                        float2* warps, float4* table) {
+    const int unit = cl_unit_channels(VEC, K, head);
+    if (cl_in_pairs(VEC, K, unit)) {
+        sums.store_pairs(count, cl_in_first(VEC, head, q.col, C, K), stage_mean, stage_m2);
+        stage_n[threadIdx.x] = count;
+        __syncthreads();
+        cl_join_groups<VEC, true>(q, head, j0, j1, unit, C, K, g0, gs, stage_mean, stage_m2, stage_n, warps, table);
+    } else {
+        sums.store_units(count, unit, stage_mean, stage_m2);
+        stage_n[threadIdx.x] = count * unit;
+        __syncthreads();
+        cl_join_groups<VEC, false>(q, head, j0, j1, unit, C, K, g0, gs, stage_mean, stage_m2, stage_n, warps, table);
     }
 }
 

@@ -154,11 +154,8 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) gncl_fused_kernel(const __
         }
         sums.fold(done, now);
     }
-    const int unit = cl_unit_channels(VEC, K, 0);
-    sums.store(held.count, unit, stage_mean, stage_m2);
-    stage_n[threadIdx.x] = held.count * unit;
-    __syncthreads();
-    cl_join_groups<VEC>(held.q, 0, seat.j0, seat.j1, unit, C, K, seat.g0, seat.gs, stage_mean, stage_m2, stage_n, warps, table);
+    cl_join(sums, held.count, held.q, 0, seat.j0, seat.j1, C, K, seat.g0, seat.gs, stage_mean, stage_m2, stage_n, warps,
+            table);
     if (p.cluster > 1) cluster_sync();
     else __syncthreads();
     // every CTA joins all of its split's groups for itself

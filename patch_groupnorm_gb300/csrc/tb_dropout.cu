@@ -221,7 +221,8 @@ __global__ void __launch_bounds__(DROP_BLOCK) dropout_elem_kernel(const __grid_c
             row = at / cols;
             at -= row * cols;
         }
-        [[maybe_unused]] const int end = (int)col0 + left - 1, end_row = NARROW ? end / cols : 0, end_at = end - end_row * cols;
+        [[maybe_unused]] const int end = (int)col0 + left - 1, end_row = NARROW ? end / cols : 0;
+        [[maybe_unused]] const int end_at = end - end_row * cols;
 #pragma unroll
         for (int j = 0; j < RB; ++j) {
             if constexpr (NARROW) {

@@ -235,7 +235,8 @@ cudaError_t apply_launch(const GnClParams& p, bool vector, int64_t ctas, cudaStr
         vector ? (p.silu ? gncl_apply_kernel<DT, V, true> : gncl_apply_kernel<DT, V, false>)
                : (p.silu ? gncl_apply_kernel<DT, 1, true> : gncl_apply_kernel<DT, 1, false>);
     const unsigned slabs = (unsigned)((p.period + p.columns - 1) / p.columns);
-    return launch_cluster(fn, p, dim3((unsigned)ctas, slabs, 1), 1, (vector ? ClStream<DT, V, 1, APPLY_DEPTH>::SMEM : 0) + (size_t)p.G * sizeof(float2), s);
+    const size_t ring = vector ? ClStream<DT, V, 1, APPLY_DEPTH>::SMEM : 0;
+    return launch_cluster(fn, p, dim3((unsigned)ctas, slabs, 1), 1, ring + (size_t)p.G * sizeof(float2), s);
 }
 
 }  // namespace

@@ -112,9 +112,9 @@ __device__ __forceinline__ int cl_last_piece(const GnClParams& prm, int p, int p
 // work.  16-byte chunks go through the thread's own slots in shared memory
 // (cp.async: no registers are held, no barrier is needed; with 4 or 8 chunks loaded
 // into registers at a time the forward pass of 256 x 256 x 512 bf16 took 49 us, not
-// 38), single elements through registers.  A slot is filled again only one step after its chunk was read, when
-// that chunk's values are in use.  step() is called with r = the step modulo DEPTH,
-// a constant once the caller's loop is unrolled.
+// 38), single elements through registers.  A slot is filled again only one step after
+// its chunk was read, when that chunk's values are in use.  step() is called with r =
+// the step modulo DEPTH, a constant once the caller's loop is unrolled.
 template <int DT, int VEC, int NS, int DEPTH>
 struct ClStream {
     using W = ClWord<DT, VEC>;
@@ -440,9 +440,9 @@ __device__ __forceinline__ void cl_join_groups(const ClPlace& q, int head, int j
 
 // A thread's sums into shared memory, and from there into the table.
 template <int DT, int VEC>
-__device__ __forceinline__ void cl_join(const ClMoments<DT, VEC>& sums, int count, const ClPlace& q, int head, int j0, int j1,
-                                        int C, int K, int g0, int gs, float* stage_mean, float* stage_m2, int* stage_n,
-                                        float2* warps, float4* table) {
+__device__ __forceinline__ void cl_join(const ClMoments<DT, VEC>& sums, int count, const ClPlace& q, int head, int j0,
+                                        int j1, int C, int K, int g0, int gs, float* stage_mean, float* stage_m2,
+                                        int* stage_n, float2* warps, float4* table) {
     const int unit = cl_unit_channels(VEC, K, head);
     if (cl_in_pairs(VEC, K, unit)) {
         sums.store_pairs(count, cl_in_first(VEC, head, q.col, C, K), stage_mean, stage_m2);

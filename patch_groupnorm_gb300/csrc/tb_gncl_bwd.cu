@@ -380,8 +380,8 @@ cudaError_t stats_launch(const GnClParams& p, bool vector, int64_t ctas, cudaStr
     void (*const fn)(const GnClParams) =
         vector ? (p.silu ? gncl_grad_stats_kernel<DT, V, true> : gncl_grad_stats_kernel<DT, V, false>)
                : (p.silu ? gncl_grad_stats_kernel<DT, 1, true> : gncl_grad_stats_kernel<DT, 1, false>);
-    return launch_cluster(fn, p, dim3((unsigned)ctas, (unsigned)p.splits, 1), p.cluster,
-                          vector ? grad_stats_smem<DT, V>(p.C, p.G, p.splits) : grad_stats_smem<DT, 1>(p.C, p.G, p.splits), s);
+    const size_t smem = vector ? grad_stats_smem<DT, V>(p.C, p.G, p.splits) : grad_stats_smem<DT, 1>(p.C, p.G, p.splits);
+    return launch_cluster(fn, p, dim3((unsigned)ctas, (unsigned)p.splits, 1), p.cluster, smem, s);
 }
 
 template <int DT>

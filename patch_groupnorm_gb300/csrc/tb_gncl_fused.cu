@@ -32,7 +32,6 @@ template <int NS>
 struct ClHeld {
     const GnClParams& p;
     ClPlace q;
-    int64_t sample;          // n
     int slice;               // this CTA's blocks of rows: slice, slice + slices, ...
     int stride;              // chunks from one of them to the next
     uint32_t slot;
@@ -103,7 +102,6 @@ struct ClSeat {
         s.j0 = first + (s.rank - slice * p.slabs) * p.columns;
         s.j1 = min(s.j0 + p.columns, first + width);
         held.q = cl_place(p, s.j0, s.j1);
-        held.sample = s.n;
         held.slice = slice;
         held.stride = p.share[0] * held.q.rows * p.period;
         held.slot = smem_addr(ring) + threadIdx.x * 16;

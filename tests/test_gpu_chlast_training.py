@@ -110,6 +110,30 @@ def test_a_captured_step_draws_new_masks(training):
     assert int(state[1]) == 3
 
 
+def test_gradients_of_any_layout_and_frozen_inputs(training):
+    # gradients that are expanded, or not contiguous; inputs that want none
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(5, 7, 24, generator=g).cuda().requires_grad_()
+    r = torch.randn(5, 7, 24, generator=g).cuda().requires_grad_()
+    keep = torch.from_numpy(D.bits(0, x.numel(), 3, 5) >= D.threshold(0.25)).view(x.shape).cuda()
+    gx, gr = torch.autograd.grad(training.dropout(x, 0.25, 3, 5, r).sum(), (x, r))
+    scale = torch.tensor(65536 / (65536 - D.threshold(0.25)), device="cuda")
+    assert torch.equal(gx, torch.where(keep, scale, torch.zeros_like(scale))) and (gr == 1).all()
+    dy = torch.randn(24, 7, 5, generator=g).cuda().permute(2, 1, 0)
+    gx, gr = torch.autograd.grad(training.dropout(x, 0.25, 3, 5, r), (x, r), dy)
+    assert torch.equal(gx, torch.where(keep, dy * scale, torch.zeros_like(scale))) and torch.equal(gr, dy)
+    w, b = torch.ones(24, device="cuda", requires_grad=True), torch.zeros(24, device="cuda")
+    y, = training.patch_group_norm_cl([x], 4, w, b)
+    want = torch.autograd.grad(y, (x, w), dy.contiguous())
+    y, = training.patch_group_norm_cl([x], 4, w, b)
+    got = torch.autograd.grad(y, (x, w), dy)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    y, = training.patch_group_norm_cl([x.detach()], 4, w, b)
+    assert torch.equal(torch.autograd.grad(y, w, dy)[0], want[1])
+    y, = training.patch_group_norm_cl([x], 4, None, None)
+    assert torch.isfinite(torch.autograd.grad(y.sum(), x)[0]).all()
+
+
 def test_the_command_runs(training):
     r = subprocess.run([sys.executable, "-m", "patch_groupnorm_gb300.training", "--steps", "3", "--channels-last",
                         "--dropout", "0.1"], capture_output=True, text=True, timeout=300)

@@ -12,8 +12,8 @@
 //
 // 16 bits an element, not 32: the generator's products and sums are what bounds
 // the kernel otherwise (a trial of 16384 x 4096 bf16: 53.4 us with a word an element,
-// 43.1 with half a word, 42.4 for a copy).  That size takes 44.5 us, the pipe of the
-// products busiest (issue slots 68 %); 65536 x 512 onto a residual 29.5, 6830 GB/s.
+// 43.1 with half a word, 42.4 for a copy).  That size takes 42.1 us; 65536 x 512 onto a
+// residual 29.4, 6850 GB/s.
 #include "tb_elem.cuh"
 
 namespace tb {
@@ -87,9 +87,10 @@ __device__ __forceinline__ void generator(const DropoutParams& p, uint64_t& offs
 
 // Whole chunks: a block's elements per thread and turn, DROP_TURNS turns side by side.
 // Nothing is read twice: loads and stores are marked so (44.6 us against 47.2).
-// Rows of whole blocks; one row may end inside a block (its last thread takes the
-// rest one by one).
-template <int DT, bool RES, bool RANDOM, bool STATE>
+// ROWS: rows of whole blocks, with strides.  Else one row, which may end inside a block
+// (its last thread takes the rest one by one): an instance for both took 44.6 us for
+// 16384 x 4096 bf16, this one 42.1.
+template <int DT, bool RES, bool RANDOM, bool STATE, bool ROWS>
 __global__ void __launch_bounds__(DROP_BLOCK) dropout_kernel(const __grid_constant__ DropoutParams p) {
     constexpr int ES = elem_size(DT), VEC = 16 / ES, NW = RB / VEC, DU = DROP_TURNS<DT, RES>;
     const int64_t per_row = p.cols / RB, blocks = per_row * p.rows;
@@ -97,11 +98,15 @@ __global__ void __launch_bounds__(DROP_BLOCK) dropout_kernel(const __grid_consta
     const char* const x = static_cast<const char*>(p.x);
     const char* const res = static_cast<const char*>(p.residual);
     char* const y = static_cast<char*>(p.y);
-    // row and block of the row, stepped from turn to turn
+    // row and block of the row, stepped from turn to turn (a 64-bit division is a hundred
+    // instructions; 2 000 000 x 8 bf16 out of wider rows takes 15.3 us, 116 row by row)
     int64_t row = 0, col = first;
-    if (p.rows > 1) {
-        row = first / per_row;
+    [[maybe_unused]] int row_step = 0, col_step = DROP_BLOCK;
+    if constexpr (ROWS) {
+        row = blocks >> 32 ? first / per_row : (uint32_t)first / (uint32_t)per_row;
         col = first - row * per_row;
+        row_step = per_row > DROP_BLOCK ? 0 : DROP_BLOCK / (int)per_row;
+        col_step -= row_step * (int)per_row;
     }
     grid_wait();
     Keys keys;
@@ -128,9 +133,10 @@ __global__ void __launch_bounds__(DROP_BLOCK) dropout_kernel(const __grid_consta
                 }
             }
         }
-        if (p.rows > 1) {
-            col += DROP_BLOCK;
-            while (col >= per_row) {
+        if constexpr (ROWS) {
+            row += row_step;
+            col += col_step;
+            if (col >= per_row) {
                 col -= per_row;
                 ++row;
             }
@@ -157,7 +163,7 @@ __global__ void __launch_bounds__(DROP_BLOCK) dropout_kernel(const __grid_consta
             __stcs(reinterpret_cast<uint4*>(y + at_y[u] + w * 16), pack<DT, VEC>(f));
         }
     }
-    const int rest = (int)(p.cols - per_row * RB);  // one row only
+    const int rest = ROWS ? 0 : (int)(p.cols - per_row * RB);  // one row only
     if (rest > 0 && blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) {
         bool keep[RB];
         kept<RANDOM>((uint64_t)per_row, offset, keys, p.threshold, keep);
@@ -294,7 +300,8 @@ cudaError_t drop_launch(const DropoutParams& p, bool vector, cudaStream_t s) {
     constexpr bool R = RANDOM;
     void (*fn)(const DropoutParams);
     if (vector) {
-        fn = R && p.state ? dropout_kernel<DT, RES, R, R> : dropout_kernel<DT, RES, R, false>;
+        fn = p.rows > 1 ? (R && p.state ? dropout_kernel<DT, RES, R, R, true> : dropout_kernel<DT, RES, R, false, true>)
+                        : (R && p.state ? dropout_kernel<DT, RES, R, R, false> : dropout_kernel<DT, RES, R, false, false>);
     } else if (p.cols < 32 * RB) {
         fn = R && p.state ? dropout_elem_kernel<DT, RES, R, R, true> : dropout_elem_kernel<DT, RES, R, false, true>;
     } else {

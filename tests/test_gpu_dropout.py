@@ -96,6 +96,17 @@ def test_strides_offsets_and_guard_bands(tbl, cols, dtype):
         flat.fill_(7.0)
 
 
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("rows, cols", [(4099, 8), (2053, 16), (1031, 40), (130, 2040), (130, 2048), (130, 2056)])
+def test_rows_that_a_thread_steps_over(tbl, rows, cols, residual):
+    # whole blocks out of wider rows: a thread's blocks lie 256 apart, many rows or less
+    # than one
+    buf = rows_of(1, (2, rows, cols + 8), torch.bfloat16)
+    x, r = buf[0, :, 8:], buf[1, :, :cols] if residual else None
+    check(tbl.dropout(x, 0.3, SEED, 3, r), x, 0.3, SEED, 3, r)
+
+
+
 def test_dropped_bad_values_are_gone(tbl):
     for bad in (float("nan"), float("inf")):
         x = torch.full((64, 40), bad, device="cuda")

@@ -12,8 +12,8 @@
 //
 // 16 bits an element, not 32: the generator's products and sums are what bounds
 // the kernel otherwise (a trial of 16384 x 4096 bf16: 53.4 us with a word an element,
-// 43.1 with half a word, 42.4 for a copy).  That size takes 42.1 us; 65536 x 512 onto a
-// residual 29.4, 6850 GB/s.
+// 43.1 with half a word, 42.4 for a copy).  That size takes 40.2 us, 6680 GB/s; 65536 x 512
+// onto a residual 29.2, 6900 GB/s.
 #include "tb_elem.cuh"
 
 namespace tb {
@@ -22,11 +22,19 @@ namespace {
 constexpr int DROP_BLOCK = 256;
 constexpr int RB = 8;  // elements of one block of random numbers
 
-// Blocks a thread loads together: two where a block is two or more 16-byte words (f32,
-// or with a residual), four where it is one.  16384 x 4096 bf16: 51.5, 46.3 and 44.6 us
-// with one, two and four; onto a residual 65536 x 512 31.0, 29.4 and 30.8.
-template <int DT, bool RES>
-constexpr int DROP_TURNS = DT == F32 || RES ? 2 : 4;
+// Blocks a thread loads together.  16384 x 4096 bf16 with 1, 2, 4, 6 and 8: 48.9, 41.9,
+// 42.1, 40.1 and 41.0 us; 16384 x 2048 out of wider rows 31.1, 27.9, 25.2, 28.4 (6); f32 and
+// with a residual, where a block is two 16-byte words or more, 65536 x 512 bf16 onto a
+// residual 29.2, 29.4 (2), 29.9 (4).
+template <int DT, bool RES, bool ROWS>
+constexpr int DROP_TURNS = DT == F32 || RES ? 1 : ROWS ? 4 : 6;
+
+// Rows of 16-bit elements that are not whole vectors, from WORD_COLS on: turns of a warp, and
+// threads of a CTA (16387 x 2047 bf16 out of wider rows with 2, 3, 4, 6 and 8 turns 39.8,
+// 34.0, 36.0, 37.1 and 51.5 us; 4099 x 1111 f16 onto a residual 8.7, 8.5, 11.1, 9.8 and 14.4,
+// 7.9 with CTAs half as large).  Element by element: rows of 257, 23.3 and 20.6 us onto a
+// residual, of 300 20.0 and 19.6, of 511 15.1 and 17.7; f32 gains nothing (1111, 17.9 and 17.5).
+constexpr int WORD_TURNS = 3, WORD_BLOCK = 128, WORD_COLS = 320;
 
 struct Keys {
     uint32_t k0[10], k1[10];
@@ -92,7 +100,7 @@ __device__ __forceinline__ void generator(const DropoutParams& p, uint64_t& offs
 // 16384 x 4096 bf16, this one 42.1.
 template <int DT, bool RES, bool RANDOM, bool STATE, bool ROWS>
 __global__ void __launch_bounds__(DROP_BLOCK) dropout_kernel(const __grid_constant__ DropoutParams p) {
-    constexpr int ES = elem_size(DT), VEC = 16 / ES, NW = RB / VEC, DU = DROP_TURNS<DT, RES>;
+    constexpr int ES = elem_size(DT), VEC = 16 / ES, NW = RB / VEC, DU = DROP_TURNS<DT, RES, ROWS>;
     const int64_t per_row = p.cols / RB, blocks = per_row * p.rows;
     const int64_t first = (int64_t)blockIdx.x * (DROP_BLOCK * DU) + threadIdx.x;
     const char* const x = static_cast<const char*>(p.x);
@@ -195,7 +203,7 @@ __device__ __forceinline__ typename Word<elem_size(DT)>::T drop_one(typename Wor
     return pack<DT, 1>(f);
 }
 
-// Any strides and addresses: a warp takes 32 blocks (256 neighbouring elements),
+// Single elements, any strides and addresses: a warp takes 32 blocks (256 neighbouring elements),
 // each lane a block's mask, and the elements in turns of 32, whose bits come from
 // the lane that has their block.  Where a row has at least as many elements (not
 // NARROW) they lie in one row or two, and an element's address is one of two bases
@@ -292,22 +300,219 @@ __global__ void __launch_bounds__(DROP_BLOCK) dropout_elem_kernel(const __grid_c
     });
 }
 
+template <int N>
+struct Words {
+    static constexpr int value = N;
+};
+
+// The words that hold a unit's elements, the first at `at`, `off` bytes past a 16-byte
+// boundary.  WHOLE: 16 bytes from that boundary on, and 16 more if off > 0, lie in the
+// tensor; else elements [lo, hi) one by one, from the first word's start.
+template <bool WHOLE>
+__device__ __forceinline__ void load_unit(const char* at, int off, int lo, int hi, uint4 (&w)[2]) {
+    w[1] = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (WHOLE) {
+        const uint4* const from = reinterpret_cast<const uint4*>(at - off);
+        w[0] = from[0];
+        if (off > 0) w[1] = from[1];
+    } else {
+        uint32_t u[4] = {};
+#pragma unroll
+        for (int e = 0; e < RB; ++e)
+            if (e >= lo && e < hi)
+                u[e / 2] |= (uint32_t)*(reinterpret_cast<const unsigned short*>(at) + e) << (e % 2 * 16);
+        w[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+}
+
+// The 16 bytes that start `off` bytes into w.  A branch on the whole words of the offset,
+// which is the warp's: choosing them is ten operations more on the busiest pipe.
+__device__ __forceinline__ void shift_unit(const uint4 (&w)[2], int off, uint32_t (&u)[4]) {
+    const uint32_t v[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+    const int by = (off & 2) * 8;
+    auto from = [&](auto first) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            constexpr int F = decltype(first)::value;
+            u[k] = __funnelshift_r(v[k + F], v[k + F + 1], by);
+        }
+    };
+    if (off < 8) {
+        if (off < 4) from(Words<0>());
+        else from(Words<1>());
+    } else {
+        if (off < 12) from(Words<2>());
+        else from(Words<3>());
+    }
+}
+
+// A word's two elements: all ones where bit 2 * word, and the one after, of m are set.
+__device__ __forceinline__ uint32_t spread(uint32_t m, int word) {
+    uint32_t r;  // a byte's sign, twice, and another's
+    asm("prmt.b32 %0, %1, %2, 0xCC88;" : "=r"(r) : "r"(m << (7 - 2 * word)), "r"(m << (6 - 2 * word)));
+    return r;
+}
+
+// A block's mask, element e in bit e.  The bits are summed as powers of two in a float's
+// last places: that pipe is the least busy.
+template <bool RANDOM>
+__device__ __forceinline__ uint32_t mask_bits(uint64_t block, uint64_t offset, const Keys& k, uint32_t threshold) {
+    if constexpr (RANDOM) {
+        uint32_t c[4];
+        philox(block, offset, k, c);
+        const uint32_t t = threshold << 16;
+        float lo = 8388608.f, hi = 8388608.f;  // 2^23
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            asm("{\n\t.reg .pred p;\n\tsetp.ge.u32 p, %1, %2;\n\t@p add.f32 %0, %0, %3;\n\t}"
+                : "+f"(lo)
+                : "r"(c[w] << 16), "r"(t), "f"((float)(1 << (2 * w))));
+            asm("{\n\t.reg .pred p;\n\tsetp.ge.u32 p, %1, %2;\n\t@p add.f32 %0, %0, %3;\n\t}"
+                : "+f"(hi)
+                : "r"(c[w]), "r"(t), "f"((float)(2 << (2 * w))));
+        }
+        return (__float_as_uint(lo) | __float_as_uint(hi)) & 0xffu;
+    } else {
+        return threshold == 0u ? 0xffu : 0u;
+    }
+}
+
+// Rows of 16-bit elements of any width from WORD_COLS on, any strides and addresses.  A
+// unit is 16 bytes, eight elements, of a row of y from a 16-byte boundary on (the first of a
+// row may begin before it, the last end behind it: those are stored one by one).  A warp
+// takes 32 * T units of one row, so that everything about the row is its own, not a
+// lane's.  What a unit needs of x and of the residual is loaded in aligned words and
+// shifted into place; its elements lie in two blocks of random numbers, of which a lane
+// computes the first and has the second from the next lane, except at the end of a row and
+// of the warp's units.  Words that reach into what lies between two rows are read
+// whole; where they would reach out of the tensor, the warp's elements are read one by one.
+//
+// What bounds it is integer and logic instructions, 71 % of that pipe while resident.
+// 16387 x 2047 bf16 out of wider rows: 33.8 us, element by element 44.1.
+template <int DT, bool RES, bool RANDOM, bool STATE>
+__global__ void __launch_bounds__(WORD_BLOCK) dropout_word_kernel(const __grid_constant__ DropoutParams p) {
+    static_assert(elem_size(DT) == 2, "a unit is 16 bytes");
+    constexpr int T = WORD_TURNS, SPAN = 32 * T * RB;
+    const int lane = threadIdx.x & 31;
+    const int64_t runs = (p.cols + RB - 1 + SPAN - 1) / SPAN, total = runs * p.rows;
+    const int64_t warp = (int64_t)blockIdx.x * (WORD_BLOCK / 32) + __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
+    if (warp >= total) return;
+    const int64_t row = total >> 32 ? warp / runs : (uint32_t)warp / (uint32_t)runs;
+    const char* const x = static_cast<const char*>(p.x);
+    const char* const res = static_cast<const char*>(p.residual);
+    // the warp's first element; a row's first `before` belong to the row before, or to nobody
+    char* const y_row = static_cast<char*>(p.y) + row * p.y_ld * 2;
+    const int before = (int)(reinterpret_cast<uintptr_t>(y_row) & 15u) / 2;
+    const int64_t col = (warp - row * runs) * SPAN - before, left = p.cols - col;
+    if (left <= 0) return;
+    const int64_t at = row * p.cols + col;
+    char* const to = y_row + col * 2;
+    const char* const from_x = x + (row * p.x_ld + col) * 2;
+    const char* const from_r = RES ? res + (row * p.r_ld + col) * 2 : nullptr;
+    const int off_x = (int)(reinterpret_cast<uintptr_t>(from_x) & 15u);
+    const int off_r = RES ? (int)(reinterpret_cast<uintptr_t>(from_r) & 15u) : 0;
+    const int first = col < 0 ? before : 0, end = (int)min(left, (int64_t)SPAN), units = (end + RB - 1) / RB;
+    // all units' words lie in the tensor
+    auto inside = [&](const char* from, int off, const char* base, int64_t ld) {
+        return from - off >= base && from - off + (units + (off > 0)) * 16 <= base + ((p.rows - 1) * ld + p.cols) * 2;
+    };
+    const bool whole = inside(from_x, off_x, x, p.x_ld) && (!RES || inside(from_r, off_r, res, p.r_ld));
+    uint4 vx[T][2], vr[T][2];
+    grid_wait();
+    Keys keys;
+    uint64_t offset;
+    generator<STATE>(p, offset, keys);
+    if (whole) {
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            const int u = t * 32 + lane;
+            if (u < units) {
+                load_unit<true>(from_x + u * 16, off_x, 0, RB, vx[t]);
+                if (RES) load_unit<true>(from_r + u * 16, off_r, 0, RB, vr[t]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            const int u = t * 32 + lane, lo = max(first - u * RB, 0), hi = end - u * RB;
+            load_unit<false>(from_x + u * 16, 0, lo, hi, vx[t]);
+            if (RES) load_unit<false>(from_r + u * 16, 0, lo, hi, vr[t]);
+        }
+    }
+    const int by_x = whole ? off_x : 0, by_r = whole ? off_r : 0, into = (int)(at & 7);
+    auto bits = [&](int u) { return mask_bits<RANDOM>((uint64_t)((at >> 3) + u), offset, keys, p.threshold); };
+    const int64_t size = ((p.rows - 1) * p.y_ld + p.cols) * 2;
+    uint32_t mask = bits(lane);
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        if (t * 32 >= units) break;
+        const int u = t * 32 + lane;
+        const uint32_t later = t + 1 < T && t * 32 + 32 < units ? bits(u + 32) : 0u;
+        const uint32_t turn = __shfl_sync(0xffffffffu, later, 0);
+        uint32_t next = __shfl_down_sync(0xffffffffu, mask, 1);
+        if (lane == 31) next = turn;
+        // the last unit, if it reaches into the next block
+        if (RANDOM && u + 1 == units && RB - into < end - u * RB) next = bits(u + 1);
+        const uint32_t m = (mask | next << RB) >> into;
+        mask = later;
+        uint32_t word[4], r_word[4];
+        shift_unit(vx[t], by_x, word);
+        if (RES) shift_unit(vr[t], by_r, r_word);
+        float f[RB], r[RB];
+        unpack<DT, RB>(make_uint4(word[0], word[1], word[2], word[3]), f);
+        if (RES) unpack<DT, RB>(make_uint4(r_word[0], r_word[1], r_word[2], r_word[3]), r);
+#pragma unroll
+        for (int e = 0; e < RB; ++e) f[e] = RES ? fmaf(f[e], p.scale, r[e]) : f[e] * p.scale;
+        const uint4 out = pack<DT, RB>(f);
+        const uint32_t kept_word[4] = {out.x, out.y, out.z, out.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            // chosen, not multiplied: a dropped infinity or NaN is gone
+            const uint32_t on = spread(m, k);
+            word[k] = RES ? (kept_word[k] & on) | (r_word[k] & ~on) : kept_word[k] & on;
+        }
+        char* const here = to + u * 16;
+        const int lo = max(first - u * RB, 0), hi = end - u * RB;
+        if (lo == 0 && hi >= RB) {
+            if (in_bounds(here, 16, p.y, size, p.status))
+                *reinterpret_cast<uint4*>(here) = make_uint4(word[0], word[1], word[2], word[3]);
+        } else if (hi > 0) {
+#pragma unroll
+            for (int e = 0; e < RB; ++e) {
+                if (e >= lo && e < hi && in_bounds(here + e * 2, 2, p.y, size, p.status))
+                    *(reinterpret_cast<unsigned short*>(here) + e) = (unsigned short)(word[e / 2] >> (e % 2 * 16));
+            }
+        }
+    }
+}
+
 template <int DT, bool RES, bool RANDOM>
 cudaError_t drop_launch(const DropoutParams& p, bool vector, cudaStream_t s) {
-    const int64_t span = (int64_t)DROP_BLOCK * RB * (vector ? DROP_TURNS<DT, RES> : 1), total = p.rows * p.cols;
-    const int64_t ctas = (total + span - 1) / span;
-    if (ctas > 2147483647LL) return cudaErrorInvalidValue;
-    constexpr bool R = RANDOM;
+    constexpr bool R = RANDOM, HALVES = elem_size(DT) == 2;
+    constexpr int H = HALVES ? DT : F16;
+    int64_t work = (p.rows * p.cols + RB - 1) / RB;  // blocks, or warps
+    int per_cta = DROP_BLOCK, block = DROP_BLOCK;
     void (*fn)(const DropoutParams);
-    if (vector) {
-        fn = p.rows > 1 ? (R && p.state ? dropout_kernel<DT, RES, R, R, true> : dropout_kernel<DT, RES, R, false, true>)
-                        : (R && p.state ? dropout_kernel<DT, RES, R, R, false> : dropout_kernel<DT, RES, R, false, false>);
+    if (vector && p.rows > 1) {
+        per_cta = DROP_BLOCK * DROP_TURNS<DT, RES, true>;
+        fn = R && p.state ? dropout_kernel<DT, RES, R, R, true> : dropout_kernel<DT, RES, R, false, true>;
+    } else if (vector) {
+        per_cta = DROP_BLOCK * DROP_TURNS<DT, RES, false>;
+        fn = R && p.state ? dropout_kernel<DT, RES, R, R, false> : dropout_kernel<DT, RES, R, false, false>;
+    } else if (HALVES && p.cols >= WORD_COLS) {
+        constexpr int span = 32 * WORD_TURNS * RB;
+        work = p.rows * ((p.cols + RB - 1 + span - 1) / span);
+        per_cta = WORD_BLOCK / 32;
+        block = WORD_BLOCK;
+        fn = R && p.state ? dropout_word_kernel<H, RES, R, R> : dropout_word_kernel<H, RES, R, false>;
     } else if (p.cols < 32 * RB) {
         fn = R && p.state ? dropout_elem_kernel<DT, RES, R, R, true> : dropout_elem_kernel<DT, RES, R, false, true>;
     } else {
         fn = R && p.state ? dropout_elem_kernel<DT, RES, R, R, false> : dropout_elem_kernel<DT, RES, R, false, false>;
     }
-    return launch_pdl(fn, p, dim3((unsigned)ctas, 1, 1), DROP_BLOCK, 0, s);
+    const int64_t ctas = (work + per_cta - 1) / per_cta;
+    if (ctas > 2147483647LL) return cudaErrorInvalidValue;
+    return launch_pdl(fn, p, dim3((unsigned)ctas, 1, 1), block, 0, s);
 }
 
 template <int DT>

@@ -97,6 +97,46 @@ def test_strides_offsets_and_guard_bands(tbl, cols, dtype):
 
 
 @pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows, cols", [(6, 319), (6, 320), (1, 761), (5, 767), (5, 769), (40, 1537), (3, 2311)])
+def test_odd_rows_of_halves(tbl, rows, cols, dtype, residual):
+    # every alignment of x, of the residual and of y against 16 bytes, rows of one and of
+    # several warps, and in place
+    dt = DT[dtype]
+    x, r = rows_of(1, (rows, cols), dt), rows_of(2, (rows, cols), dt) if residual else None
+    want = tbl.dropout(x, 0.3, SEED, 9, r)
+    check(want, x, 0.3, SEED, 9, r)
+    for at in range(8):
+        buf = torch.full((3, rows * (cols + 11) + 8), 7.0, dtype=dt, device="cuda")
+        vx, vr, vy = (b[k:k + rows * ld].view(rows, ld)[:, :cols]
+                      for b, k, ld in zip(buf, (at, 3 * at % 8, 5 * at % 8), (cols + 3, cols + at, cols + 11)))
+        vx.copy_(x)
+        if residual:
+            vr.copy_(r)
+        tbl.tb_dropout(vx, vy, 0.3, SEED, 9, residual=vr if residual else None)
+        assert torch.equal(vy, want) and torch.equal(vx, x)
+        vy.fill_(7.0)
+        assert (buf[2] == 7.0).all()
+        into = vr if residual and at % 2 else vx
+        tbl.tb_dropout(vx, into, 0.3, SEED, 9, residual=vr if residual else None)
+        assert torch.equal(into, want)
+        into.fill_(7.0)
+        assert (buf[1 if into is vr else 0] == 7.0).all()
+
+
+def test_odd_rows_of_halves_by_state_and_special_values(tbl):
+    x, r = rows_of(1, (33, 1001), torch.bfloat16), rows_of(2, (33, 1001), torch.bfloat16)
+    state = torch.tensor([5, 3], dtype=torch.int64, device="cuda")
+    assert torch.equal(tbl.dropout(x[:, 1:], 0.3, 11, 2, r[:, 1:], state), tbl.dropout(x[:, 1:], 0.3, 16, 5, r[:, 1:]))
+    odd = torch.full((33, 1003), float("nan"), dtype=torch.bfloat16, device="cuda")[:, 1:-1]
+    assert torch.equal(tbl.dropout(odd, 1.0, 1, 2, r), r) and (tbl.dropout(odd, 1.0, 1, 2) == 0).all()
+    assert torch.equal(tbl.dropout(x[:, 1:], 0.0, 1), x[:, 1:])
+    keep = tbl.dropout(torch.ones_like(x), 0.5, 3, 4) != 0
+    y = tbl.dropout(odd, 0.5, 3, 4, r)
+    assert torch.equal(y.isnan(), keep) and torch.equal(y[~keep], r[~keep])
+
+
+@pytest.mark.parametrize("residual", [False, True])
 @pytest.mark.parametrize("rows, cols", [(4099, 8), (2053, 16), (1031, 40), (130, 2040), (130, 2048), (130, 2056)])
 def test_rows_that_a_thread_steps_over(tbl, rows, cols, residual):
     # whole blocks out of wider rows: a thread's blocks lie 256 apart, many rows or less

@@ -387,8 +387,8 @@ __device__ __forceinline__ uint32_t mask_bits(uint64_t block, uint64_t offset, c
 // of the warp's units.  Words that reach into what lies between two rows are read
 // whole; where they would reach out of the tensor, the warp's elements are read one by one.
 //
-// What bounds it is integer and logic instructions, 71 % of that pipe while resident.
-// 16387 x 2047 bf16 out of wider rows: 33.8 us, element by element 44.1.
+// What bounds it is issue slots (72 % of all cycles) and the pipe of integer and logic
+// operations.  16387 x 2047 bf16 out of wider rows: 33.6 us, element by element 44.1.
 template <int DT, bool RES, bool RANDOM, bool STATE>
 __global__ void __launch_bounds__(WORD_BLOCK) dropout_word_kernel(const __grid_constant__ DropoutParams p) {
     static_assert(elem_size(DT) == 2, "a unit is 16 bytes");

@@ -212,6 +212,23 @@ def test_offsets_past_32_bits(tbl):
     assert (x[: (n // 9) * 9].view(-1, 9)[:, 7:] == 1).all()
 
 
+@pytest.mark.parametrize("rows, cols, pad", [(3870000, 1111, 1), (3, (1 << 31) + 5, 2), (4200000, 1024, 8), (1, (1 << 32) + 21, 0)])
+def test_odd_rows_past_32_bits(tbl, rows, cols, pad):
+    # more than 2^32 elements out of wider rows, and from an odd address: the first and the
+    # last ones of some rows
+    buf = torch.ones(rows * (cols + pad) + 8, dtype=torch.bfloat16, device="cuda")
+    v = buf[8 if pad == 8 else 3:][:rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+    assert v.numel() > 1 << 32
+    tbl.tb_dropout(v, v, 0.5, SEED, OFFSET)
+    for row in sorted({0, rows // 2, rows - 1}):
+        for at in (0, cols - 600):
+            got = v[row, at:at + 600]
+            check(got, torch.ones(600, dtype=torch.bfloat16), 0.5, SEED, OFFSET, first=row * cols + at)
+    if pad:
+        gaps = buf[8 if pad == 8 else 3:][:rows * (cols + pad)].view(rows, cols + pad)[:, cols:]
+        assert (gaps == 1).all()
+
+
 @pytest.mark.parametrize("raw", [False, True])
 def test_on_another_stream(tbl, raw):
     x, r = rows_of(1, (300, 256), torch.bfloat16), rows_of(2, (300, 256), torch.bfloat16)

@@ -439,7 +439,8 @@ __global__ void __launch_bounds__(WORD_BLOCK) dropout_word_kernel(const __grid_c
             if (RES) load_unit<false>(from_r + u * 16, 0, lo, hi, vr[t]);
         }
     }
-    const int by_x = whole ? off_x : 0, by_r = whole ? off_r : 0, into = (int)(at & 7);
+    const int by_x = whole ? off_x : 0, by_r = whole ? off_r : 0;
+    [[maybe_unused]] const int into = (int)(at & 7);
     auto bits = [&](int u) { return mask_bits<RANDOM>((uint64_t)((at >> 3) + u), offset, keys, p.threshold); };
     const int64_t size = ((p.rows - 1) * p.y_ld + p.cols) * 2;
     uint32_t mask = bits(lane);
@@ -447,14 +448,17 @@ __global__ void __launch_bounds__(WORD_BLOCK) dropout_word_kernel(const __grid_c
     for (int t = 0; t < T; ++t) {
         if (t * 32 >= units) break;
         const int u = t * 32 + lane;
-        const uint32_t later = t + 1 < T && t * 32 + 32 < units ? bits(u + 32) : 0u;
-        const uint32_t turn = __shfl_sync(0xffffffffu, later, 0);
-        uint32_t next = __shfl_down_sync(0xffffffffu, mask, 1);
-        if (lane == 31) next = turn;
-        // the last unit, if it reaches into the next block
-        if (RANDOM && u + 1 == units && RB - into < end - u * RB) next = bits(u + 1);
-        const uint32_t m = (mask | next << RB) >> into;
-        mask = later;
+        uint32_t m = mask;  // where nothing is random every block's is the same
+        if constexpr (RANDOM) {
+            const uint32_t later = t + 1 < T && t * 32 + 32 < units ? bits(u + 32) : 0u;
+            const uint32_t turn = __shfl_sync(0xffffffffu, later, 0);
+            uint32_t next = __shfl_down_sync(0xffffffffu, mask, 1);
+            if (lane == 31) next = turn;
+            // the last unit, if it reaches into the next block
+            if (u + 1 == units && RB - into < end - u * RB) next = bits(u + 1);
+            m = (mask | next << RB) >> into;
+            mask = later;
+        }
         uint32_t word[4], r_word[4];
         shift_unit(vx[t], by_x, word);
         if (RES) shift_unit(vr[t], by_r, r_word);

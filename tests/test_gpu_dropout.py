@@ -137,6 +137,35 @@ def test_odd_rows_of_halves_by_state_and_special_values(tbl):
 
 
 @pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+# the last ones: a row's last run is 32, 64 or 96 units at some alignments, or at all of them
+@pytest.mark.parametrize("rows, cols", [(6, 319), (6, 320), (1, 761), (5, 767), (5, 769), (40, 1537), (3, 2311),
+                                        (4, 505), (9, 511), (3, 512), (8, 1021), (4, 1111), (2, 1279), (5, 1535),
+                                        (5, 2000)])
+def test_odd_rows_of_halves_all_kept_or_all_dropped(tbl, rows, cols, dtype, residual):
+    # at every alignment what is not random is exact: x (and the residual, one rounding), or
+    # the residual alone (or zero)
+    dt = DT[dtype]
+    x, r = rows_of(1, (rows, cols), dt), rows_of(2, (rows, cols), dt) if residual else None
+    kept = (x.float() + r.float()).to(dt) if residual else x
+    gone = r if residual else torch.zeros_like(x)
+    for at in range(8):
+        buf = torch.full((3, rows * (cols + 11) + 8), 7.0, dtype=dt, device="cuda")
+        vx, vr, vy = (b[k:k + rows * ld].view(rows, ld)[:, :cols]
+                      for b, k, ld in zip(buf, (at, 3 * at % 8, 5 * at % 8), (cols + 3, cols + at, cols + 11)))
+        for p, want in ((0.0, kept), (2.0 ** -18, kept), (1 - 2.0 ** -18, gone), (1.0, gone)):
+            for into in (vy, vx, vr) if residual else (vy, vx):
+                buf.fill_(7.0)
+                vx.copy_(x)
+                if residual:
+                    vr.copy_(r)
+                tbl.tb_dropout(vx, into, p, SEED, 9, residual=vr if residual else None)
+                assert torch.equal(into, want)
+                into.fill_(7.0)
+                assert (buf[2 if into is vy else 0 if into is vx else 1] == 7.0).all()
+
+
+@pytest.mark.parametrize("residual", [False, True])
 @pytest.mark.parametrize("rows, cols", [(4099, 8), (2053, 16), (1031, 40), (130, 2040), (130, 2048), (130, 2056)])
 def test_rows_that_a_thread_steps_over(tbl, rows, cols, residual):
     # whole blocks out of wider rows: a thread's blocks lie 256 apart, many rows or less

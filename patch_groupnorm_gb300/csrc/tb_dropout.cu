@@ -87,8 +87,8 @@ __device__ __forceinline__ void generator(const DropoutParams& p, uint64_t& offs
     uint64_t seed = p.seed;
     offset = p.offset;
     if constexpr (STATE) {
-        seed += __ldg(p.state);
-        offset += __ldg(p.state + 1);
+        seed += p.state[0];
+        offset += p.state[1];
     }
     key_schedule(seed, keys);
 }

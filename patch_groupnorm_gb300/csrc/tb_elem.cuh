@@ -351,6 +351,9 @@ __device__ __forceinline__ W smem_load(uint32_t at) {
 
 // Waits until the grids before this one on the stream have completed and
 // their writes are visible (launches use programmatic stream serialisation).
+// What they may have written is read behind the wait with coherent loads: the read-only
+// path (__ldg) is for what nothing writes while a kernel is resident, and its loads need
+// not stay behind the wait.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Launches `fn` with programmatic stream serialisation, as every kernel of

@@ -141,7 +141,7 @@ struct ClStream {
                                      "l"(at[k])
                                      : "memory");
                     } else {
-                        reg[r][k] = __ldg(reinterpret_cast<const W*>(at[k]));
+                        reg[r][k] = *reinterpret_cast<const W*>(at[k]);
                     }
                 }
                 at[k] += stride;
@@ -557,7 +557,7 @@ __device__ __forceinline__ void cl_group_stats(const GnClParams& p, int64_t n, i
                 raw[k] = make_longlong2(0, 0);
                 if (g < g1 && r0 + k < p.R &&
                     in_bounds(at, sizeof(GnPartial), p.partials, p.R * set * (int64_t)sizeof(GnPartial), p.status))
-                    raw[k] = __ldg(reinterpret_cast<const longlong2*>(at));
+                    raw[k] = *reinterpret_cast<const longlong2*>(at);
             }
 #pragma unroll
             for (int k = 0; k < B; ++k)

@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(CL_BLOCK) gncl_coefs_kernel(const __grid_const
 #pragma unroll 4
             for (int i = threadIdx.x; i < per_set; i += CL_BLOCK) {
                 if (!in_bounds(first + i, sizeof(float2), p.grad_partials, size, p.status)) continue;
-                const float2 v = __ldg(first + i);
+                const float2 v = first[i];
                 const float w = weight_at(p.gamma, DT, g * K + i / TB_GN_PARTS, 1.f);
                 B = fmaf(w, v.x, B);
                 A = fmaf(w, v.y, A);
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(CL_BLOCK) gncl_coefs_kernel(const __grid_const
         for (int64_t r = 0; r < p.R * p.N; ++r) {
             const float2* const at = p.grad_partials + (r * C + c) * TB_GN_PARTS + threadIdx.x % TB_GN_PARTS;
             if (!in_bounds(at, sizeof(float2), p.grad_partials, size, p.status)) continue;
-            const float2 v = __ldg(at);
+            const float2 v = *at;
             B += v.x;
             A += v.y;
         }
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_apply_kernel(const __gr
         ClChannel ch(run.head, q.col * VEC, C, K);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            const float4 k = __ldg(coefs + ch.g);
+            const float4 k = coefs[ch.g];
             f0[i] = k.x;
             f1[i] *= k.y;
             f3[i] = k.z;
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_apply_kernel(const __gr
         if ((int)threadIdx.x < h + t) {
             const int64_t e = (int)threadIdx.x < h ? threadIdx.x : run.elems - run.tail + (threadIdx.x - h);
             const int c = (int)(e % C);
-            const float4 k = __ldg(coefs + c / K);
+            const float4 k = coefs[c / K];
             const float gam = k.y * weight_at(p.gamma, DT, c, 1.f);
             if (in_bounds(patch + (run.first + e) * ES, ES, patch, bytes, p.status)) {
                 const float d = cl_elem<DT>(patch, run.first + e) - k.x;

@@ -1,9 +1,13 @@
 """CPU-only checks of the channels-last calls: sizes, and refusals on the host
 before a GPU is touched."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "patch_groupnorm_gb300", "csrc")
 
 
 @pytest.fixture(scope="module")
@@ -132,3 +136,11 @@ def test_bindings_refuse_cpu_tensors(tbl):
                  lambda: tbl.tb_patch_gn_stats_cl([x], 2, part)):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("name", ["tb_gncl.cuh", "tb_gncl.cu", "tb_gncl_bwd.cu", "tb_gncl_fused.cu", "tb_dropout.cu"])
+def test_kernels_launched_early_read_coherently(name):
+    # records, constants, states and tensors may be written while these kernels are resident
+    # already, so none is read through the read-only path
+    source = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
+    assert not re.findall(r"__ldg\s*\(|\.nc\b|__restrict__", source)

@@ -452,3 +452,26 @@ def test_replay_from_a_graph(tbl, length):
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, _pass(tbl, *ins)))
+
+
+def test_calls_in_turn_share_a_workspace(tbl):
+    # dx is launched before the constants are written: each call's are its own, not the last call's
+    sets = [(rows_of(k, (1, 70000, 64), torch.bfloat16, 1.0 + k, 2.0 * k), rows_of(20 + k, (1, 70000, 64), torch.bfloat16),
+             *weights_of(40 + k, 64, torch.bfloat16)) for k in range(6)]
+    part, grec = [tbl.new_partials(1, 1, 8) for _ in sets], tbl.new_grad_partials(1, 1, 64)
+    ws = tbl.gn_workspace_cl(1, 8)
+    for p, (x, *_) in zip(part, sets):
+        tbl.tb_patch_gn_stats_cl([x], 8, p)
+
+    def backward(k):
+        x, dy, gamma, beta = sets[k]
+        return tbl.patch_group_norm_backward_cl([dy], [x], 8, part[k], gamma, beta, 1e-6, grad_partials=grec, workspace=ws)
+    alone = []
+    for k in range(len(sets)):
+        ws.fill_(255)
+        alone.append(backward(k))
+        torch.cuda.synchronize()
+    for _ in range(5):
+        got = [backward(k) for k in range(len(sets))]
+        for ((dx,), dg, db), ((wx,), wg, wb) in zip(got, alone):
+            assert torch.equal(dx, wx) and torch.equal(dg, wg) and torch.equal(db, wb)

@@ -180,7 +180,10 @@ __global__ void __launch_bounds__(DROP_BLOCK) dropout_kernel(const __grid_consta
         for (int e = 0; e < RB; ++e) {
             if (e < rest) {
                 const int64_t i = per_row * RB + e;
-                if (!in_bounds(x + i * ES, ES, x, p.cols * ES, p.status)) continue;
+                if (!in_bounds(x + i * ES, ES, x, p.cols * ES, p.status) ||
+                    (RES && !in_bounds(res + i * ES, ES, res, p.cols * ES, p.status)) ||
+                    !in_bounds(y + i * ES, ES, y, p.cols * ES, p.status))
+                    continue;
                 float f[1], r[1] = {0.f};
                 unpack<DT, 1>(reinterpret_cast<const W*>(x)[i], f);
                 if (RES) unpack<DT, 1>(reinterpret_cast<const W*>(res)[i], r);
@@ -307,20 +310,23 @@ struct Words {
 
 // The words that hold a unit's elements, the first at `at`, `off` bytes past a 16-byte
 // boundary.  WHOLE: 16 bytes from that boundary on, and 16 more if off > 0, lie in the
-// tensor; else elements [lo, hi) one by one, from the first word's start.
+// tensor; else elements [lo, hi) one by one, from the first word's start.  The tensor:
+// `size` bytes at `base` (bounds-checked build).
 template <bool WHOLE>
-__device__ __forceinline__ void load_unit(const char* at, int off, int lo, int hi, uint4 (&w)[2]) {
-    w[1] = make_uint4(0u, 0u, 0u, 0u);
+__device__ __forceinline__ void load_unit(const char* at, int off, int lo, int hi, uint4 (&w)[2], const char* base,
+                                          int64_t size, uint32_t* status) {
+    w[0] = w[1] = make_uint4(0u, 0u, 0u, 0u);
     if constexpr (WHOLE) {
         const uint4* const from = reinterpret_cast<const uint4*>(at - off);
-        w[0] = from[0];
-        if (off > 0) w[1] = from[1];
+        if (in_bounds(from, 16, base, size, status)) w[0] = from[0];
+        if (off > 0 && in_bounds(from + 1, 16, base, size, status)) w[1] = from[1];
     } else {
+        const unsigned short* const from = reinterpret_cast<const unsigned short*>(at);
         uint32_t u[4] = {};
 #pragma unroll
         for (int e = 0; e < RB; ++e)
-            if (e >= lo && e < hi)
-                u[e / 2] |= (uint32_t)*(reinterpret_cast<const unsigned short*>(at) + e) << (e % 2 * 16);
+            if (e >= lo && e < hi && in_bounds(from + e, 2, base, size, status))
+                u[e / 2] |= (uint32_t)from[e] << (e % 2 * 16);
         w[0] = make_uint4(u[0], u[1], u[2], u[3]);
     }
 }
@@ -412,9 +418,10 @@ __global__ void __launch_bounds__(WORD_BLOCK) dropout_word_kernel(const __grid_c
     const int off_x = (int)(reinterpret_cast<uintptr_t>(from_x) & 15u);
     const int off_r = RES ? (int)(reinterpret_cast<uintptr_t>(from_r) & 15u) : 0;
     const int first = col < 0 ? before : 0, end = (int)min(left, (int64_t)SPAN), units = (end + RB - 1) / RB;
+    auto bytes = [&](int64_t ld) { return ((p.rows - 1) * ld + p.cols) * 2; };
     // all units' words lie in the tensor
     auto inside = [&](const char* from, int off, const char* base, int64_t ld) {
-        return from - off >= base && from - off + (units + (off > 0)) * 16 <= base + ((p.rows - 1) * ld + p.cols) * 2;
+        return from - off >= base && from - off + (units + (off > 0)) * 16 <= base + bytes(ld);
     };
     const bool whole = inside(from_x, off_x, x, p.x_ld) && (!RES || inside(from_r, off_r, res, p.r_ld));
     uint4 vx[T][2], vr[T][2];
@@ -427,22 +434,22 @@ __global__ void __launch_bounds__(WORD_BLOCK) dropout_word_kernel(const __grid_c
         for (int t = 0; t < T; ++t) {
             const int u = t * 32 + lane;
             if (u < units) {
-                load_unit<true>(from_x + u * 16, off_x, 0, RB, vx[t]);
-                if (RES) load_unit<true>(from_r + u * 16, off_r, 0, RB, vr[t]);
+                load_unit<true>(from_x + u * 16, off_x, 0, RB, vx[t], x, bytes(p.x_ld), p.status);
+                if (RES) load_unit<true>(from_r + u * 16, off_r, 0, RB, vr[t], res, bytes(p.r_ld), p.status);
             }
         }
     } else {
 #pragma unroll
         for (int t = 0; t < T; ++t) {
             const int u = t * 32 + lane, lo = max(first - u * RB, 0), hi = end - u * RB;
-            load_unit<false>(from_x + u * 16, 0, lo, hi, vx[t]);
-            if (RES) load_unit<false>(from_r + u * 16, 0, lo, hi, vr[t]);
+            load_unit<false>(from_x + u * 16, 0, lo, hi, vx[t], x, bytes(p.x_ld), p.status);
+            if (RES) load_unit<false>(from_r + u * 16, 0, lo, hi, vr[t], res, bytes(p.r_ld), p.status);
         }
     }
     const int by_x = whole ? off_x : 0, by_r = whole ? off_r : 0;
     [[maybe_unused]] const int into = (int)(at & 7);
     auto bits = [&](int u) { return mask_bits<RANDOM>((uint64_t)((at >> 3) + u), offset, keys, p.threshold); };
-    const int64_t size = ((p.rows - 1) * p.y_ld + p.cols) * 2;
+    const int64_t size = bytes(p.y_ld);
     uint32_t mask = bits(lane);
 #pragma unroll
     for (int t = 0; t < T; ++t) {

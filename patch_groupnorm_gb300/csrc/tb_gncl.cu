@@ -63,8 +63,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_stats_kernel(const __grid_co
         const int h = piece == 0 && u.slab == 0 ? run.head : 0, t = piece == last && u.slab == 0 ? run.tail : 0;
         if (lane < h + t) {
             const int64_t e = lane < h ? lane : run.elems - run.tail + (lane - h);
-            if (in_bounds(patch + (run.first + e) * ES, ES, patch, bytes, p.status))
-                edge = cl_elem<DT>(patch, run.first + e);
+            edge = cl_elem<DT>(patch, run.first + e, bytes, p.status);
             edge_group = (int)(e % C) / K;
         }
     }
@@ -211,11 +210,9 @@ __global__ void __launch_bounds__(CL_BLOCK, 3) gncl_apply_kernel(const __grid_co
             const int64_t e = (int)threadIdx.x < h ? threadIdx.x : run.elems - run.tail + (threadIdx.x - h);
             const int c = (int)(e % C);
             const float2 s = stats[c / K];
-            if (in_bounds(patch + (run.first + e) * ES, ES, patch, bytes, p.status)) {
-                const float d = cl_elem<DT>(patch, run.first + e) - s.x;
-                const float z = fmaf(d, s.y * weight_at(p.gamma, DT, c, 1.f), weight_at(p.beta, DT, c, 0.f));
-                cl_store_elem<DT>(out, run.first + e, act<SILU>(z));
-            }
+            const float d = cl_elem<DT>(patch, run.first + e, bytes, p.status) - s.x;
+            const float z = fmaf(d, s.y * cl_weight<DT>(p, p.gamma, c, 1.f), cl_weight<DT>(p, p.beta, c, 0.f));
+            cl_store_elem<DT>(out, run.first + e, act<SILU>(z), bytes, p.status);
         }
     }
 }

@@ -596,6 +596,17 @@ struct ClChannel {
     }
 };
 
+// gamma's or beta's value for channel c, and a weight's gradient; w is null where the call
+// has none.
+template <int DT>
+__device__ __forceinline__ float cl_weight(const GnClParams& p, const void* w, int64_t c, float dflt) {
+    return index_ok(c >= 0 && c < p.C, p.status) ? weight_at(w, DT, c, dflt) : dflt;
+}
+template <int DT>
+__device__ __forceinline__ void cl_store_weight(const GnClParams& p, void* w, int64_t c, float v) {
+    if (w != nullptr && index_ok(c >= 0 && c < p.C, p.status)) store_weight(w, DT, c, v);
+}
+
 // gamma and beta of a thread's VEC channels: one load each where they lie together.
 template <int DT, int VEC>
 __device__ __forceinline__ void cl_weights(const GnClParams& p, int head, int phase, float (&ga)[VEC], float (&be)[VEC]) {
@@ -609,8 +620,8 @@ __device__ __forceinline__ void cl_weights(const GnClParams& p, int head, int ph
         ClChannel ch(head, phase, (int)p.C, 1);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            ga[i] = weight_at(p.gamma, DT, ch.c, 1.f);
-            be[i] = weight_at(p.beta, DT, ch.c, 0.f);
+            ga[i] = cl_weight<DT>(p, p.gamma, ch.c, 1.f);
+            be[i] = cl_weight<DT>(p, p.beta, ch.c, 0.f);
             ch.next();
         }
     }
@@ -662,16 +673,18 @@ __device__ __forceinline__ float dz_of(float dy, float z) {
     }
 }
 
-// One element, as the elements of head and tail are read and written.
+// One element, as the elements of head and tail are read and written; `bytes` of a
+// tensor (bounds-checked build).
 template <int DT>
-__device__ __forceinline__ float cl_elem(const void* base, int64_t i) {
-    if constexpr (DT == F32) return reinterpret_cast<const float*>(base)[i];
-    else return elem_to_f<DT>(reinterpret_cast<const unsigned short*>(base)[i]);
+__device__ __forceinline__ float cl_elem(const void* base, int64_t i, int64_t bytes, uint32_t* status) {
+    const ClWord<DT, 1>* const at = reinterpret_cast<const ClWord<DT, 1>*>(base) + i;
+    return in_bounds(at, sizeof(*at), base, bytes, status) ? elem_to_f<DT>(*at) : 0.f;
 }
 template <int DT>
-__device__ __forceinline__ void cl_store_elem(void* base, int64_t i, float v) {
+__device__ __forceinline__ void cl_store_elem(void* base, int64_t i, float v, int64_t bytes, uint32_t* status) {
+    ClWord<DT, 1>* const at = reinterpret_cast<ClWord<DT, 1>*>(base) + i;
     float f[1] = {v};
-    reinterpret_cast<ClWord<DT, 1>*>(base)[i] = pack<DT, 1>(f);
+    if (in_bounds(at, sizeof(*at), base, bytes, status)) *at = pack<DT, 1>(f);
 }
 
 // Launches `fn` with programmatic stream serialisation in clusters of `cluster` CTAs.

@@ -144,16 +144,14 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_stats_kernel(const __gr
         int c = -1;
         if (lane < h + t) {
             const int64_t e = lane < h ? lane : run.elems - run.tail + (lane - h);
-            if (in_bounds(patch + (run.first + e) * ES, ES, patch, bytes, p.status)) {
-                c = (int)(e % C);
-                if (c >= c0 && c < c0 + cs) {
-                    const float2 s = stats[c / K - g0];
-                    xhat = (cl_elem<DT>(patch, run.first + e) - s.x) * s.y;
-                    dz = dz_of<SILU>(cl_elem<DT>(grad, run.first + e),
-                                     fmaf(xhat, weight_at(p.gamma, DT, c, 1.f), weight_at(p.beta, DT, c, 0.f)));
-                } else {
-                    c = -1;
-                }
+            c = (int)(e % C);
+            if (c >= c0 && c < c0 + cs) {
+                const float2 s = stats[c / K - g0];
+                xhat = (cl_elem<DT>(patch, run.first + e, bytes, p.status) - s.x) * s.y;
+                dz = dz_of<SILU>(cl_elem<DT>(grad, run.first + e, bytes, p.status),
+                                 fmaf(xhat, cl_weight<DT>(p, p.gamma, c, 1.f), cl_weight<DT>(p, p.beta, c, 0.f)));
+            } else {
+                c = -1;
             }
         }
         for (unsigned left = __ballot_sync(0xffffffffu, c >= 0); left; left &= left - 1) {
@@ -232,7 +230,7 @@ __global__ void __launch_bounds__(CL_BLOCK) gncl_coefs_kernel(const __grid_const
             for (int i = threadIdx.x; i < per_set; i += CL_BLOCK) {
                 if (!in_bounds(first + i, sizeof(float2), p.grad_partials, size, p.status)) continue;
                 const float2 v = first[i];
-                const float w = weight_at(p.gamma, DT, g * K + i / TB_GN_PARTS, 1.f);
+                const float w = cl_weight<DT>(p, p.gamma, g * K + i / TB_GN_PARTS, 1.f);
                 B = fmaf(w, v.x, B);
                 A = fmaf(w, v.y, A);
             }
@@ -243,8 +241,13 @@ __global__ void __launch_bounds__(CL_BLOCK) gncl_coefs_kernel(const __grid_const
         // the count: of the forward pass's records
         long long count = 0;
         if (warp == 0) {
-            for (int q = lane; q < p.R * TB_GN_PARTS; q += 32)
-                count += p.partials[(((int64_t)(q / TB_GN_PARTS) * p.N + n) * p.G + g) * TB_GN_PARTS + q % TB_GN_PARTS].n;
+            for (int q = lane; q < p.R * TB_GN_PARTS; q += 32) {
+                const GnPartial* const at =
+                    p.partials + (((int64_t)(q / TB_GN_PARTS) * p.N + n) * p.G + g) * TB_GN_PARTS + q % TB_GN_PARTS;
+                if (in_bounds(at, sizeof(GnPartial), p.partials,
+                              p.R * p.N * p.G * TB_GN_PARTS * (int64_t)sizeof(GnPartial), p.status))
+                    count += at->n;
+            }
 #pragma unroll
             for (int d = 16; d >= 1; d >>= 1) count += __shfl_xor_sync(0xffffffffu, count, d);
         }
@@ -257,7 +260,8 @@ __global__ void __launch_bounds__(CL_BLOCK) gncl_coefs_kernel(const __grid_const
                 A += sums[k].y;
             }
             const float inv = count > 0 ? 1.f / (float)count : 0.f, rstd = stats[0].y;
-            p.coefs[blockIdx.x] = make_float4(stats[0].x, rstd, -(rstd * rstd) * (A * inv), -rstd * (B * inv));
+            if (index_ok(blockIdx.x < p.N * p.G, p.status))
+                p.coefs[blockIdx.x] = make_float4(stats[0].x, rstd, -(rstd * rstd) * (A * inv), -rstd * (B * inv));
         }
         return;
     }
@@ -279,8 +283,8 @@ __global__ void __launch_bounds__(CL_BLOCK) gncl_coefs_kernel(const __grid_const
         A += __shfl_xor_sync(0xffffffffu, A, d);
     }
     if (c < C && threadIdx.x % TB_GN_PARTS == 0) {
-        if (p.dgamma != nullptr) store_weight(p.dgamma, DT, c, A);
-        if (p.dbeta != nullptr) store_weight(p.dbeta, DT, c, B);
+        cl_store_weight<DT>(p, p.dgamma, c, A);
+        cl_store_weight<DT>(p, p.dbeta, c, B);
     }
 }
 
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_apply_kernel(const __gr
         ClChannel ch(run.head, q.col * VEC, C, K);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            const float4 k = coefs[ch.g];
+            const float4 k = index_ok(ch.g >= 0 && ch.g < p.G, p.status) ? coefs[ch.g] : make_float4(0.f, 0.f, 0.f, 0.f);
             f0[i] = k.x;
             f1[i] *= k.y;
             f3[i] = k.z;
@@ -362,14 +366,12 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_apply_kernel(const __gr
         if ((int)threadIdx.x < h + t) {
             const int64_t e = (int)threadIdx.x < h ? threadIdx.x : run.elems - run.tail + (threadIdx.x - h);
             const int c = (int)(e % C);
-            const float4 k = coefs[c / K];
-            const float gam = k.y * weight_at(p.gamma, DT, c, 1.f);
-            if (in_bounds(patch + (run.first + e) * ES, ES, patch, bytes, p.status)) {
-                const float d = cl_elem<DT>(patch, run.first + e) - k.x;
-                const float dz = dz_of<SILU>(cl_elem<DT>(grad, run.first + e),
-                                             fmaf(d, gam, weight_at(p.beta, DT, c, 0.f)));
-                cl_store_elem<DT>(out, run.first + e, fmaf(dz, gam, fmaf(d, k.z, k.w)));
-            }
+            const float4 k = index_ok(c / K < p.G, p.status) ? coefs[c / K] : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float gam = k.y * cl_weight<DT>(p, p.gamma, c, 1.f);
+            const float d = cl_elem<DT>(patch, run.first + e, bytes, p.status) - k.x;
+            const float dz = dz_of<SILU>(cl_elem<DT>(grad, run.first + e, bytes, p.status),
+                                         fmaf(d, gam, cl_weight<DT>(p, p.beta, c, 0.f)));
+            cl_store_elem<DT>(out, run.first + e, fmaf(dz, gam, fmaf(d, k.z, k.w)), bytes, p.status);
         }
     }
 }

@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) gncl_fused_grad_kernel(con
         float B = 0.f, A = 0.f;
         if (i < seat.gs) {
             for (int j = threadIdx.x & 7; j < K; j += 8) {
-                const float w = weight_at(p.gamma, DT, c0 + i * K + j, 1.f);
+                const float w = cl_weight<DT>(p, p.gamma, c0 + i * K + j, 1.f);
                 const float2 t = whole[i * K + j];
                 B = fmaf(w, t.x, B);
                 A = fmaf(w, t.y, A);
@@ -392,8 +392,8 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) gncl_fused_grad_kernel(con
         for (int i = threadIdx.x; i < cs; i += BLOCK) {
             const float2 t = whole[i];
             if (p.N == 1) {
-                if (p.dgamma != nullptr) store_weight(p.dgamma, DT, c0 + i, t.y);
-                if (p.dbeta != nullptr) store_weight(p.dbeta, DT, c0 + i, t.x);
+                cl_store_weight<DT>(p, p.dgamma, c0 + i, t.y);
+                cl_store_weight<DT>(p, p.dbeta, c0 + i, t.x);
                 continue;
             }
             // one record a sample, for the launch that adds the samples up

@@ -144,3 +144,23 @@ def test_kernels_launched_early_read_coherently(name):
     # already, so none is read through the read-only path
     source = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
     assert not re.findall(r"__ldg\s*\(|\.nc\b|__restrict__", source)
+
+
+@pytest.mark.parametrize("name", ["tb_gncl.cuh", "tb_gncl.cu", "tb_gncl_bwd.cu", "tb_gncl_fused.cu", "tb_dropout.cu"])
+def test_accesses_of_global_memory_are_behind_checks(name):
+    # in the bounds-checked build: whatever function reads or writes a tensor, a weight or a
+    # record by address checks it, or calls one that does
+    source = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
+    access = (r"__ldcs\(|__stcs\(|cp\.async\.cg|from\[\d\]|\*at = |\*reinterpret_cast<(?:const )?(?:W|longlong2|uint4)\*>"
+              r"|at->n|weight_at\(w")
+    for f in re.split(r"\n(?=(?:template|__device__|__global__|static|inline|struct)\b)", source):
+        if re.search(access, f):
+            assert re.search(r"in_bounds\(|index_ok\(", f), f[:200]
+    # single elements and weights go through the checked helpers
+    assert not re.search(r"(?<!cl_)(?:\bweight_at|\bstore_weight)\((?!w, DT)", source)
+    for call in re.findall(r"(?:cl_elem<DT>|cl_store_elem<DT>|load_unit<(?:true|false)>)\(.*?[;?]", source, re.S):
+        assert "status" in call, call
+    # what is left of the last block: all three tensors
+    if name == "tb_dropout.cu":
+        rest = source[source.index("if (e < rest)"):source.index("pack<DT, 1>(f);")]
+        assert [t for t in ("x", "res", "y") if "in_bounds(%s + i * ES" % t in rest] == ["x", "res", "y"]

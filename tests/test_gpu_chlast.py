@@ -475,3 +475,86 @@ def test_calls_in_turn_share_a_workspace(tbl):
         got = [backward(k) for k in range(len(sets))]
         for ((dx,), dg, db), ((wx,), wg, wb) in zip(got, alone):
             assert torch.equal(dx, wx) and torch.equal(dg, wg) and torch.equal(db, wb)
+
+
+# [N, *spatial, C] of two patches, split axis 1: calls that fit into shared memory in every
+# type.  Chunks of 8 halves (4 floats) that two groups share leave two sums where a group has
+# a chunk's channels, so these have odd and small multiples of channels a group
+ONE_LAUNCH = [
+    (1, 515, 5, (24, 16)),      # a chunk over the end of a position; several slabs of columns
+    (1, 67, 67, (40, 24)),      # a channel a group
+    (2, 184, 8, (600, 18)),     # 23 channels a group, whole chunks a position
+    (1, 400, 8, (300, 300)),    # 50 channels a group, the groups split among clusters
+    (2, 400, 8, (200, 50)),
+    (2, 1200, 8, (90, 31)),     # 150
+    (1, 37, 1, (1312, 8)),      # both sums of a chunk over a position's end are one group's
+    (2, 36, 4, (50, 30)),       # 9
+    (4, 88, 8, (40, 41)),       # 11
+    (2, 9, 1, (8, 72)),         # a position of a chunk and an element
+    (3, 1029, 7, (8, 16)),      # 147 channels, a period of more than a thousand chunks in halves
+    (1, 24, 2, (40, 41)),       # 12: a sum for every four
+]
+
+
+@pytest.mark.parametrize("silu", [True, False])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("N,C,G,sizes", ONE_LAUNCH, ids=lambda v: str(v))
+def test_one_launch_of_every_kind_of_group(tbl, N, C, G, sizes, dtype, silu):
+    dt = DT[dtype]
+    x = rows_of(C, (N, sum(sizes), C), torch.float64, 1.5)
+    xs = [(p + m).to(dt).contiguous() for p, m in zip(x.split(sizes, 1), (-2.0, 1.0))]
+    dys = [p.contiguous() for p in rows_of(7, x.shape, dt, 0.5).split(sizes, 1)]
+    gamma, beta = weights_of(8, C, dt)
+    part = tbl.new_partials(2, N, G).fill_(-1)
+    outs = tbl.patch_group_norm_cl(xs, G, gamma, beta, 1e-6, silu, partials=part)
+    check_forward(xs, G, gamma, beta, 1e-6, silu, outs)
+    # one launch leaves one record of the patches together
+    assert (part[0, ..., 0, 0] == sum(sizes) * (C // G)).all() and (part[1] == 0).all() and (part[0, ..., 1:, :] == 0).all()
+    grec = tbl.new_grad_partials(2, N, C).fill_(float("nan"))
+    dxs, dg, db = tbl.patch_group_norm_backward_cl(dys, xs, G, part, gamma, beta, 1e-6, silu, grad_partials=grec)
+    check_backward(dys, xs, G, gamma, beta, 1e-6, silu, dxs, dg, db)
+    # and uses no records of the gradients, or one a sample
+    assert grec.isnan().all() if N == 1 else (grec[1] == 0).all() and (grec[0, ..., 1:, :] == 0).all()
+
+
+def _general(tbl, x, dy, G, gamma, beta):
+    N, C = x.shape[0], x.shape[-1]
+    rec = tbl.tb_patch_gn_stats_cl([x], G, tbl.new_partials(1, N, G))
+    y, = tbl.tb_patch_gn_apply_cl([x], [torch.empty_like(x)], G, rec, 1, gamma, beta, 1e-6)
+    grec = tbl.tb_patch_gn_grad_stats_cl([dy], [x], G, rec, 1, gamma, beta, 1e-6, tbl.new_grad_partials(1, N, C))
+    dg, db, dx = torch.empty_like(gamma), torch.empty_like(gamma), torch.empty_like(x)
+    tbl.tb_patch_gn_grad_apply_cl([dy], [x], [dx], G, rec, grec, 1, gamma, beta, 1e-6, tbl.gn_workspace_cl(N, G), dg, db)
+    return rec, y, dx, dg, db
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("shape,G", [((1, 4000, 400), 8), ((2, 1500, 1200), 8), ((1, 900, 880), 16)])
+def test_split_channels_with_chunks_of_two_groups(tbl, shape, G, dtype):
+    # the launches of the general path, their statistics split by channels
+    dt = DT[dtype]
+    x, dy = rows_of(1, shape, dt, 1.5, 0.5), rows_of(2, shape, dt, 0.5)
+    gamma, beta = weights_of(3, shape[-1], dt)
+    rec, y, dx, dg, db = _general(tbl, x, dy, G, gamma, beta)
+    assert (rec[..., 0].sum(-1) == shape[1] * (shape[2] // G)).all()
+    check_forward([x], G, gamma, beta, 1e-6, True, [y])
+    check_backward([dy], [x], G, gamma, beta, 1e-6, True, [dx], dg, db)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("shape,G", [((1, 704, 37), 1), ((1, 1312, 37), 1), ((2, 600, 184), 8), ((1, 600, 400), 8)])
+def test_one_launch_and_several_agree(tbl, shape, G, dtype):
+    dt = DT[dtype]
+    x, dy = rows_of(1, shape, dt, 1.0, 3.0), rows_of(2, shape, dt)
+    gamma, beta = weights_of(3, shape[-1], dt)
+    part = tbl.new_partials(1, shape[0], G)
+    y, = tbl.patch_group_norm_cl([x], G, gamma, beta, 1e-6, partials=part)
+    grec = tbl.new_grad_partials(1, shape[0], shape[-1]).fill_(float("nan"))
+    (dx,), dg, db = tbl.patch_group_norm_backward_cl([dy], [x], G, part, gamma, beta, 1e-6, grad_partials=grec)
+    rec, *several = _general(tbl, x, dy, G, gamma, beta)
+    # two ways: one record, and one from each of several clusters
+    assert (part[..., 1:, 0] == 0).all() and (rec[..., 1, 0] > 0).all()
+    assert grec.isnan().all() if shape[0] == 1 else (grec[..., 1:, :] == 0).all()
+    # both round once what differs by fp32 arithmetic: a step apart at most, or 64 u of the values' size
+    for a, b in zip((y, dx, dg, db), several):
+        a, b = a.double(), b.double()
+        assert ((a - b).abs() <= 2 * HALF[dt] * b.abs() + 64 * U * b.abs().max()).all()

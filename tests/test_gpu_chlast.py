@@ -558,3 +558,51 @@ def test_one_launch_and_several_agree(tbl, shape, G, dtype):
     for a, b in zip((y, dx, dg, db), several):
         a, b = a.double(), b.double()
         assert ((a - b).abs() <= 2 * HALF[dt] * b.abs() + 64 * U * b.abs().max()).all()
+
+
+def _ranks(tbl, xs, dys, gamma, beta, G=4):
+    """The four separate calls of a rank with the first two patches and of one with the
+    others, and the records of both gathered: R > P."""
+    N, C = xs[0].shape[0], xs[0].shape[-1]
+    ranks = [(xs[:2], dys[:2]), (xs[2:], dys[2:])]
+    R = len(xs)
+    rec = torch.cat([tbl.tb_patch_gn_stats_cl(x, G, tbl.new_partials(len(x), N, G)) for x, _ in ranks])
+    ys = [y for x, _ in ranks
+          for y in tbl.tb_patch_gn_apply_cl(x, [torch.empty_like(t) for t in x], G, rec, R, gamma, beta, 1e-6)]
+    grec = torch.cat([tbl.tb_patch_gn_grad_stats_cl(d, x, G, rec, R, gamma, beta, 1e-6, tbl.new_grad_partials(len(x), N, C))
+                      for x, d in ranks])
+    ws, dxs, weights = tbl.gn_workspace_cl(N, G), [], []
+    for x, d in ranks:
+        dg, db = torch.empty_like(gamma), torch.empty_like(beta)
+        dxs += tbl.tb_patch_gn_grad_apply_cl(d, x, [torch.empty_like(t) for t in x], G, rec, grec, R, gamma, beta, 1e-6,
+                                             ws, dg, db)
+        weights += [dg, db]
+    return ys, dxs, weights
+
+
+def _rank_inputs(seed, C=24):
+    x, dy = rows_of(seed, (2, 400, C), torch.bfloat16, 1.5, 0.5), rows_of(seed + 1, (2, 400, C), torch.bfloat16)
+    cut = [101, 99, 150, 50]
+    return ([p.contiguous() for p in x.split(cut, 1)], [p.contiguous() for p in dy.split(cut, 1)],
+            *weights_of(seed + 2, C, torch.bfloat16))
+
+
+def test_separate_calls_replay_from_a_graph(tbl):
+    ins = _rank_inputs(1)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        _ranks(tbl, *ins)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        ys, dxs, weights = _ranks(tbl, *ins)
+    for seed in (100, 200, 300):
+        xs, dys, gamma, beta = ins
+        for t, u in zip([*xs, *dys, gamma, beta], (lambda a, b, c, d: [*a, *b, c, d])(*_rank_inputs(seed))):
+            t.copy_(u)
+        g.replay()
+        torch.cuda.synchronize()
+        check_forward(xs, 4, gamma, beta, 1e-6, True, ys)
+        check_backward(dys, xs, 4, gamma, beta, 1e-6, True, dxs, *weights[:2])
+        want = _ranks(tbl, *ins)
+        assert all(torch.equal(a, b) for a, b in zip([*ys, *dxs, *weights], [t for ts in want for t in ts]))

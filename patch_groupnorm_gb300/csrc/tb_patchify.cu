@@ -71,7 +71,8 @@ __global__ void __launch_bounds__(PF_BLOCK) patch_copy_kernel(const __grid_const
     T* const wb = static_cast<T*>(p.whole);
     const int64_t pbytes = p.outer * ppitch * V, wbytes = p.outer * wpitch * V;  // bounds-checked build
     // The previous kernel on the stream (launched with programmatic
-    // serialisation) may still be writing what this one reads.
+    // serialisation) may still be writing what this one reads: coherent loads,
+    // not the read-only path, behind the wait.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     while (c < c1) {
         T v[PF_INFLIGHT];
@@ -85,10 +86,10 @@ __global__ void __launch_bounds__(PF_BLOCK) patch_copy_kernel(const __grid_const
                 if (!in_bounds(at_patch, V, pb, pbytes, p.status) || !in_bounds(at_whole, V, wb, wbytes, p.status)) {
                     // skipped (bounds-checked build only)
                 } else if (TO_PATCHES) {
-                    v[u] = __ldg(at_whole);
+                    v[u] = *at_whole;
                     dst[u] = at_patch;
                 } else {
-                    v[u] = __ldg(at_patch);
+                    v[u] = *at_patch;
                     dst[u] = at_whole;
                 }
             }

@@ -167,3 +167,25 @@ def test_gather_writes_nothing_outside_its_output(tbl):
     torch.cuda.synchronize()
     assert (buf[:guard] == 9.0).all() and (buf[guard + x.numel():] == 9.0).all()
     assert np.array_equal(_bits(out), _bits(x))
+
+
+def test_split_right_behind_the_stitch_that_writes_its_input(tbl):
+    # the split's grid is resident while the stitch still writes: it sees this stitch's output
+    axis = tbl.Axis(96, 32, 0.25, 8)
+    lay = tbl.tb_axis_layout(axis)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    sets = [[[torch.randn(1, 3, h, w, generator=g, device="cuda").bfloat16() for w in lay.extents] for h in lay.extents]
+            for _ in range(4)]
+    out = torch.empty(1, 3, lay.out_extent, lay.out_extent, dtype=torch.bfloat16, device="cuda")
+    want = []
+    for tiles in sets:
+        tbl.tb_stitch2d(tiles, axis, axis, out)
+        torch.cuda.synchronize()
+        want.append(out.clone())
+    for _ in range(20):
+        got = []
+        for tiles in sets:
+            tbl.tb_stitch2d(tiles, axis, axis, out)
+            got.append(tbl.tb_patchify(out, 3, 1, 4))
+        for parts, w in zip(got, want):
+            assert torch.equal(torch.cat(parts, 3), w)

@@ -430,3 +430,9 @@ def test_ramp_spread_rejects_bad_layouts(tbl):
     assert f(100, 32, 4, 8, 4, 8, None, ctypes.byref(a)) == tbl.TB_ERR_NULL
     assert f(100, 32, 4, 8, 4, 8, org, ctypes.byref(a)) == tbl.TB_OK
     assert list(org[:4]) == [0, 22 * 8, 45 * 8, 68 * 8] and a.n_tiles == 4
+
+
+def test_patch_copies_read_coherently():
+    # a split may be resident while the stitch before it writes its input: no read-only loads
+    source = open(os.path.join(ROOT, "patch_groupnorm_gb300", "csrc", "tb_patchify.cu")).read()
+    assert not re.findall(r"__ldg\s*\(|\.nc\b", re.sub(r"//[^\n]*", "", source))

@@ -291,8 +291,10 @@ __global__ void __launch_bounds__(CL_BLOCK) gncl_coefs_kernel(const __grid_const
 // --- dx -----------------------------------------------------------------------------
 
 // As DEPTH, pairs of chunks (two CTAs per SM: 114 us alone for 13 x 120 x 208 x 384 bf16,
-// 122 with 5).
-constexpr int APPLY_DEPTH = 4;
+// 122 with 5).  Single elements: with 4, 6, 8, 10 and 12 the whole call takes 138, 120, 122,
+// 118 and 113 us for 65536 x 512 bf16, 318, 288, 275, 281 and 273 for 3 x 24568 x 515 f32.
+template <int VEC>
+constexpr int APPLY_DEPTH = VEC > 1 ? 4 : 12;
 
 template <int DT, int VEC, bool SILU>
 __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_apply_kernel(const __grid_constant__ GnClParams p) {
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(CL_BLOCK, 2) gncl_grad_apply_kernel(const __gr
     // from the end: the records' pass left that in L2
     const int64_t last = from + (w.at + (w.count - 1) * w.stride) * (int64_t)sizeof(W);
     extern __shared__ uint4 shared4[];
-    ClStream<DT, VEC, 2, APPLY_DEPTH> in;
+    ClStream<DT, VEC, 2, APPLY_DEPTH<VEC>> in;
     in.base[0] = patch;
     in.base[1] = grad;
     in.at[0] = patch + last;
@@ -393,7 +395,7 @@ cudaError_t apply_launch(const GnClParams& p, bool vector, int64_t ctas, cudaStr
         vector ? (p.silu ? gncl_grad_apply_kernel<DT, V, true> : gncl_grad_apply_kernel<DT, V, false>)
                : (p.silu ? gncl_grad_apply_kernel<DT, 1, true> : gncl_grad_apply_kernel<DT, 1, false>);
     const unsigned slabs = (unsigned)((p.period + p.columns - 1) / p.columns);
-    return launch_cluster(fn, p, dim3((unsigned)ctas, slabs, 1), 1, vector ? ClStream<DT, V, 2, APPLY_DEPTH>::SMEM : 0, s);
+    return launch_cluster(fn, p, dim3((unsigned)ctas, slabs, 1), 1, vector ? ClStream<DT, V, 2, APPLY_DEPTH<V>>::SMEM : 0, s);
 }
 
 }  // namespace

@@ -1344,8 +1344,8 @@ def patch_group_norm_cl(patches: Sequence[torch.Tensor], G: int, gamma: Optional
     SiLU) of the whole tensor over its patches.  ``partials`` receives records
     that describe the patches together.  Outputs that are not given are made."""
     if outs is None or partials is None:
-        if len(patches) == 0:
-            raise ValueError("at least one patch")
+        if len(patches) == 0 or patches[0].dim() < 2:
+            raise ValueError("at least one patch, [N, *spatial, C]")
         outs, partials = _on_stream(lambda: (
             [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in patches] if outs is None else outs,
             new_partials(len(patches), patches[0].shape[0], G, patches[0].device) if partials is None else partials),

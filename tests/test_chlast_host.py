@@ -164,3 +164,11 @@ def test_accesses_of_global_memory_are_behind_checks(name):
     if name == "tb_dropout.cu":
         rest = source[source.index("if (e < rest)"):source.index("pack<DT, 1>(f);")]
         assert [t for t in ("x", "res", "y") if "in_bounds(%s + i * ES" % t in rest] == ["x", "res", "y"]
+
+
+def test_bindings_refuse_patches_without_channels(tbl):
+    for x in (torch.zeros(()), torch.zeros(8)):
+        for call in (lambda: tbl.patch_group_norm_cl([x], 2, None, None, 1e-6), lambda: tbl.patch_group_norm_cl([], 2, None, None, 1e-6),
+                     lambda: tbl.patch_group_norm_backward_cl([x], [x], 2, None, None, None, 1e-6)):
+            with pytest.raises(ValueError):
+                call()

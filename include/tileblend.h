@@ -849,7 +849,9 @@ tb_status tb_patch_gn_apply_cl(const void* const* patches, void* const* outs, in
  *             for the backward pass, or for ranks that gather them).  Which of
  *             them holds what is not specified; tb_patch_gn_stats_cl writes
  *             each patch's own
- * Where the patches fit into shared memory this is one launch. */
+ * One launch where every patch and output starts on 16 bytes, every patch's
+ * samples are whole 16-byte chunks and all of them fit into shared memory, if
+ * that is the faster way; otherwise two. */
 tb_status tb_patch_group_norm_cl(const void* const* patches, void* const* outs, int32_t P, tb_dtype dtype, int64_t N,
                                  int64_t C, const int64_t* spatial, int32_t G, tb_gn_partial* partials,
                                  const void* gamma, const void* beta, float eps, int32_t silu, void* stream);
@@ -885,7 +887,8 @@ tb_status tb_patch_gn_grad_apply_cl(const void* const* patches, const void* cons
  * call, from R = P record sets of these patches.
  *   grad_partials  device [P][N][C][TB_GN_PARTS], 16-byte aligned: a workspace
  *                  here; its contents afterwards are not specified
- * Where patches and gradients fit into shared memory this is one launch. */
+ * One launch as above, patches and gradients together (and another for the
+ * weight gradients where N > 1); otherwise three. */
 tb_status tb_patch_group_norm_backward_cl(const void* const* patches, const void* const* grads, void* const* outs,
                                           int32_t P, tb_dtype dtype, int64_t N, int64_t C, const int64_t* spatial,
                                           int32_t G, const tb_gn_partial* partials,

@@ -13,7 +13,8 @@
 // 16 bits an element, not 32: the generator's products and sums are what bounds
 // the kernel otherwise (a trial of 16384 x 4096 bf16: 53.4 us with a word an element,
 // 43.1 with half a word, 42.4 for a copy).  That size takes 40.2 us, 6680 GB/s; 65536 x 512
-// onto a residual 29.2, 6900 GB/s.
+// onto a residual 29.1 in a graph, 6910 GB/s (two reads to a write; a copy, with one, gives
+// 6790), and 30.2 from call to call.
 #include "tb_elem.cuh"
 
 namespace tb {

@@ -8,10 +8,11 @@
 // Statistics need all of a group before the first output, so x is read twice, by
 // two launches (where it fits into shared memory, once: tb_gncl_fused.cu).  1 x 256 x
 // 256 x 512 bf16 in four patches takes 37.7 us, 16.3 of them the statistics; 67 MB
-// read twice and written once are 31 us at the copy rate.  What is left is the start
+// read twice and written once are 29.7 us at the copy rate.  What is left is the start
 // and the end of each launch: sums joined over rows, groups and clusters, a latency
 // after the other (3 us), and the groups' pooled statistics before the first output
-// (2 us).  13 x 120 x 208 x 384: 126 us, of 115 at that rate.
+// (2 us).  13 x 120 x 208 x 384: 126 us, of 110 at that rate; the channels-first kernels
+// take 114 for the same bytes, so a tenth is these kernels' own.
 //
 // Statistics grids: 288 CTAs in clusters of 3 for four patches on 152 SMs; 256 in
 // clusters of 8 took 18.8 us for the first and 50.8 for the second (16.3, 43), 304

@@ -14,7 +14,7 @@
 // second triggers the third, which fetches its first chunks meanwhile.
 //
 // x and dy are read twice.  1 x 256 x 256 x 512 bf16 in four patches takes 60.5 us
-// (the records 26.4, the constants and dx 34.7), where 335 MB are 51 us at the copy
+// (the records 26.4, the constants and dx 34.7), where 335 MB are 49 us at the copy
 // rate; 13 x 120 x 208 x 384: 199 us, of 184.  The records are bound by memory and by
 // issue slots (43 % busy over the launch, 55 % while CTAs are resident): per pair of
 // chunks an exponential and a reciprocal an element, and 128 registers, so two CTAs

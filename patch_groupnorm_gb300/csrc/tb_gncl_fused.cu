@@ -9,8 +9,8 @@
 // path spend on starting and on waiting for each other is spent once.  Chunks are a
 // thread's own from its copy to its result, so the copies need no barrier.
 //
-// What bounds it is latency: 2 patches of 15 x 16 x 64 bf16 take 5.4 us (backward, f32,
-// 6.5; in several launches 7.7 and 10.4), 64 x 64 x 512 8.8 (11.3): starting, the
+// What bounds it is latency: 2 patches of 15 x 16 x 64 bf16 take 5.5 us (backward 6.5; in
+// several launches 7.7 and 10.3), 64 x 64 x 512 8.9 (11.4): starting, the
 // first chunks' way, and the joining of sums, some 2000 instructions a warp of which
 // few overlap.
 //
